@@ -88,6 +88,7 @@ typedef enum moe_status {
 #define MOE_DEV_NAN_LOGIT 0x2     /* NaN among a token's logits (ranked as -inf) */
 #define MOE_DEV_BAD_PACK 0x4      /* packed weight blob header mismatch      */
 #define MOE_DEV_TIMEOUT 0x8       /* a kernel gave up waiting on itself      */
+#define MOE_DEV_BAD_OFFSETS 0x10  /* a product's group offsets descend or leave [0, R] */
 
 enum { MOE_ACT_SWIGLU = 0, MOE_ACT_SWIGLU_CLAMP = 1, MOE_ACT_GEGLU = 2, MOE_ACT_SRELU = 3 };
 enum { MOE_WFMT_NVFP4 = 0, MOE_WFMT_MXFP8 = 1, MOE_WFMT_MXFP4 = 2 };
@@ -402,6 +403,122 @@ moe_status_t moe_layer_backward(const moe_config_t* cfg, const uint16_t* dout, c
                                 const moe_train_save_t* save, const void* packed_w_dgrad, uint16_t* dx,
                                 uint16_t* dW1, uint16_t* dW2, float* dlogits, float* db1, void* ws,
                                 void* stream);
+
+/* ---- training-side operators ----------------------------------------------
+ *
+ * Operators of the block around the routed layer, for experts and
+ * projections kept in 16 bits or in FP8 with 128-blocks: they take the
+ * dispatch results (offsets, w_row, perm_src) of the calls above. The pages
+ * have no counterpart for them; the formulas stand at each call.
+ *
+ * Conventions beyond the shared ones: matrices have an explicit row stride
+ * ("ld", in elements, at least the row's length) and, where grouped, a stride
+ * between groups; element types are MOE_DT_*. Unless stated otherwise a
+ * pointer is aligned to its elements (16-byte rows take the wide-access
+ * path). Sums and statistics are fp32; each result is rounded once. None of
+ * these calls uses an atomic for a result: the same inputs give the same bits.
+ * Sizes are any positive number; zero rows are legal and launch nothing that
+ * reads. Overlapping inputs and outputs are not. */
+enum { MOE_DT_BF16 = 0, MOE_DT_F16 = 1, MOE_DT_F32 = 2 };
+
+/* Layer norm of T rows of H: mu and v the mean and (biased) variance of a
+ * row, r = 1 / sqrt(v + eps), y = (x - mu) r gamma + beta. x, y: dtype
+ * (bf16, f16, f32); gamma, beta [H]: wdtype (fp32 or dtype), NULL for ones /
+ * zeros. mean, rstd [T] fp32: nullable, what the backward needs of mu and r. */
+moe_status_t moe_layer_norm_forward(const void* x, int64_t ldx, const void* gamma, const void* beta, float eps,
+                                    int64_t T, int H, int dtype, int wdtype, void* y, int64_t ldy, float* mean,
+                                    float* rstd, void* stream);
+
+/* Its backward: with xh = (x - mean) rstd and t = dy gamma,
+ * dx = rstd (t - avg(t) - xh avg(t xh)), dgamma = sum over rows of dy xh,
+ * dbeta = sum over rows of dy (wdtype, each nullable). ws (16-byte aligned,
+ * moe_layer_norm_workspace_size bytes; not needed when both are NULL) holds
+ * the fp32 partial sums, added in a fixed order. T = 0 writes zero sums. */
+moe_status_t moe_layer_norm_backward(const void* dy, int64_t lddy, const void* x, int64_t ldx, const void* gamma,
+                                     const float* mean, const float* rstd, int64_t T, int H, int dtype, int wdtype,
+                                     void* dx, int64_t lddx, void* dgamma, void* dbeta, void* ws, size_t ws_bytes,
+                                     void* stream);
+
+/* Host only. Workspace of moe_layer_norm_backward: min(T, 1024) rows of 2 H
+ * fp32. */
+moe_status_t moe_layer_norm_workspace_size(int64_t T, int H, size_t* bytes);
+
+/* The experts' activation with an 8-bit checkpoint. h [R, 2I] (gate, up;
+ * MOE_ACT_SRELU: [R, I]) and y [R, I] of dtype bf16 or f16:
+ * y = w_row act(h) (w_row [R] fp32, NULL for ones; act as in moe_config_t),
+ * and of h the E4M3 codes q (as h, row stride ldq) with scales s [R, halves *
+ * ceil(I/128)] fp32 (gate's blocks, then up's): of each block of 128 columns
+ * of a half, s = max(amax * fl(1/448), 2^-126), q = E4M3(h * fl(1/s)). amax is
+ * over finite values; an infinity or NaN becomes a NaN code. */
+moe_status_t moe_act_ckpt_forward(const void* h, int64_t ldh, const float* w_row, int64_t R, int I, int dtype,
+                                  int act, float alpha, float limit, void* y, int64_t ldy, uint8_t* q, int64_t ldq,
+                                  float* s, void* stream);
+
+/* Its backward from the checkpoint alone, h~ = q s: dh [R, 2I] (or [R, I])
+ * = w_row dy act'(h~); dw_row [R] fp32 (nullable) = sum over columns of
+ * dy act(h~); y [R, I] (nullable) = w_row act(h~), recomputed for the weight
+ * gradient of the product that followed. The clamp's gradient is inclusive. */
+moe_status_t moe_act_ckpt_backward(const void* dy, int64_t lddy, const uint8_t* q, int64_t ldq, const float* s,
+                                   const float* w_row, int64_t R, int I, int dtype, int act, float alpha, float limit,
+                                   void* dh, int64_t lddh, float* dw_row, void* y, int64_t ldy, void* stream);
+
+/* Products. kind, for the workspace of one call:
+ * MOE_MM_ROWS moe_grouped_mm, MOE_MM_WGRAD moe_grouped_mm_wgrad,
+ * MOE_MM_FP8 moe_fp8_mm. The workspace starts with a sticky status word
+ * (zero it once; read with moe_mm_read_status) and holds the partial sums of
+ * a product that is split along its reduction: at most 64 MiB + 256 bytes. */
+enum { MOE_MM_ROWS = 0, MOE_MM_WGRAD = 1, MOE_MM_FP8 = 2 };
+moe_status_t moe_mm_workspace_size(int kind, int R, int N, int K, int G, size_t* bytes);
+
+/* Products grouped by expert with ragged sizes: for every row r of group e
+ * (offsets[e] <= r < offsets[e+1]; offsets [G + 1] int32 on the device, as
+ * moe_dispatch writes them; G <= 2048)
+ *   trans_w = 0: out[r, n] = sum_k x[r, k] w[e, n, k], w [G, N, K]
+ *   trans_w = 1: out[r, n] = sum_k x[r, k] w[e, k, n], w [G, K, N]: with the
+ *                forward's w, the gradient of its rows
+ * x and w bf16 or f16 (dtype); out dtype or fp32. Rows in no group become
+ * zero; offsets that descend or leave [0, R] are clamped and set
+ * MOE_DEV_BAD_OFFSETS. x, w and ws start on 16 bytes, ldx, ldw and w_group
+ * are multiples of 8 elements (MOE_ERR_INVALID_ARG otherwise); N, K and the
+ * group sizes are any. */
+moe_status_t moe_grouped_mm(const void* x, int64_t ldx, const void* w, int64_t w_group, int64_t ldw, int trans_w,
+                            const int32_t* offsets, int R, int N, int K, int G, int dtype, void* out, int64_t ldo,
+                            int out_dtype, void* ws, size_t ws_bytes, void* stream);
+
+/* The gradient of the weights of moe_grouped_mm (trans_w = 0):
+ * dw[e, n, k] = sum over group e's rows of dy[r, n] x[r, k]; dw [G, N, K] of
+ * dtype or fp32; groups without rows get zeros. dy and x start on 16 bytes,
+ * lddy and ldx are multiples of 8 elements. */
+moe_status_t moe_grouped_mm_wgrad(const void* dy, int64_t lddy, const void* x, int64_t ldx, const int32_t* offsets,
+                                  int R, int N, int K, int G, int dtype, void* dw, int64_t dw_group, int64_t lddw,
+                                  int out_dtype, void* ws, size_t ws_bytes, void* stream);
+
+/* FP8 operands with a scale for each block of 128. Rows (activations,
+ * gradients): x [R, C] of dtype -> E4M3 q [R, C] and s [R, ceil(C/128)] fp32
+ * (row stride lds), one scale for 128 columns. */
+moe_status_t moe_fp8_quant_rows(const void* x, int64_t ldx, int64_t R, int C, int dtype, uint8_t* q, int64_t ldq,
+                                float* s, int64_t lds, void* stream);
+
+/* Weights: w [G, N, K] -> q [G, N, K] and s [G, ceil(N/128), ceil(K/128)],
+ * one scale for 128 x 128; qt, st (both or neither): the same codes and
+ * scales transposed, [G, K, N] and [G, ceil(K/128), ceil(N/128)], for the
+ * gradient of the rows. Scale and codes as in moe_act_ckpt_forward. */
+moe_status_t moe_fp8_quant_weights(const void* w, int64_t w_group, int64_t ldw, int G, int N, int K, int dtype,
+                                   uint8_t* q, int64_t q_group, int64_t ldq, float* s, uint8_t* qt, int64_t qt_group,
+                                   int64_t ldqt, float* st, void* stream);
+
+/* The FP8 product: out[r, n] = sum over K blocks b of xs[r, b]
+ * wscale[e, n/128, b] sum_{k in b} xq[r, k] wq[e, n, k], fp32 sums, out bf16,
+ * f16 or fp32. offsets as in moe_grouped_mm, or NULL with G = 1: one product
+ * of all rows. xq, wq and ws start on 16 bytes; ldx, ldw and w_group are
+ * multiples of 16. */
+moe_status_t moe_fp8_mm(const uint8_t* xq, int64_t ldx, const float* xs, int64_t ldxs, const uint8_t* wq,
+                        int64_t w_group, int64_t ldw, const float* wscale, const int32_t* offsets, int R, int N, int K,
+                        int G, void* out, int64_t ldo, int out_dtype, void* ws, size_t ws_bytes, void* stream);
+
+/* Synchronises `stream`, copies the status word of a products' workspace to
+ * *out (host) and clears it, as moe_read_status does for the layer's. */
+moe_status_t moe_mm_read_status(void* ws, int32_t* out, void* stream);
 
 /* ---- status --------------------------------------------------------------- */
 

@@ -23,12 +23,17 @@ MOE_DEV_BAD_EXPERT_ID = 0x1
 MOE_DEV_NAN_LOGIT = 0x2
 MOE_DEV_BAD_PACK = 0x4
 MOE_DEV_TIMEOUT = 0x8
+MOE_DEV_BAD_OFFSETS = 0x10
 MOE_ACT_SWIGLU, MOE_ACT_SWIGLU_CLAMP, MOE_ACT_GEGLU, MOE_ACT_SRELU = 0, 1, 2, 3
 ACTS = {"swiglu": MOE_ACT_SWIGLU, "swiglu_clamp": MOE_ACT_SWIGLU_CLAMP, "geglu": MOE_ACT_GEGLU,
         "srelu": MOE_ACT_SRELU}
 MOE_WFMT_NVFP4, MOE_WFMT_MXFP8, MOE_WFMT_MXFP4 = 0, 1, 2
 WFMTS = {"nvfp4": MOE_WFMT_NVFP4, "mxfp8": MOE_WFMT_MXFP8, "mxfp4": MOE_WFMT_MXFP4}
 MOE_PACK_FORWARD, MOE_PACK_DGRAD = 0, 1
+MOE_DT_BF16, MOE_DT_F16, MOE_DT_F32 = 0, 1, 2
+DTYPES = {torch.bfloat16: MOE_DT_BF16, torch.float16: MOE_DT_F16, torch.float32: MOE_DT_F32}
+MOE_MM_ROWS, MOE_MM_WGRAD, MOE_MM_FP8 = 0, 1, 2
+FP8_BLOCK = 128     # elements that share a scale in the FP8 products and the activation checkpoints
 
 # every exported symbol the header declares
 EXPORTS = (
@@ -38,6 +43,9 @@ EXPORTS = (
     "moe_layer_forward", "moe_layer_backward", "moe_read_status", "moe_clear_status", "moe_status_string",
     "moe_last_launch_count", "moe_set_phase_events", "moe_router_logits_noalloc", "moe_debug_unpack_weights",
     "moe_layer_fused", "moe_debug_flag_wait",
+    "moe_layer_norm_forward", "moe_layer_norm_backward", "moe_layer_norm_workspace_size",
+    "moe_act_ckpt_forward", "moe_act_ckpt_backward", "moe_mm_workspace_size", "moe_grouped_mm",
+    "moe_grouped_mm_wgrad", "moe_fp8_quant_rows", "moe_fp8_quant_weights", "moe_fp8_mm", "moe_mm_read_status",
 )
 MOE_N_PHASE_EVENTS = 6
 
@@ -92,6 +100,7 @@ def load(path: str | None = None) -> ctypes.CDLL:
         raise RuntimeError(f"libmoe.so not built at {p}; run quantized_grouped_gemm_topk_gb300.build.build()")
     lib = ctypes.CDLL(p)
     P = ctypes.c_void_p
+    L, N, F, Z = ctypes.c_int64, ctypes.c_int, ctypes.c_float, ctypes.c_size_t
     cfgp = ctypes.POINTER(moe_config_t)
     sig = {
         "moe_config_validate": [cfgp],
@@ -119,6 +128,18 @@ def load(path: str | None = None) -> ctypes.CDLL:
         "moe_debug_flag_wait": [cfgp, P, ctypes.c_int64, P, P],
         "moe_router_logits_noalloc": [cfgp, P, P, ctypes.c_int, P, P],
         "moe_debug_unpack_weights": [cfgp, P, ctypes.c_int, ctypes.c_int, P, P, P],
+        "moe_layer_norm_forward": [P, L, P, P, F, L, N, N, N, P, L, P, P, P],
+        "moe_layer_norm_backward": [P, L, P, L, P, P, P, L, N, N, N, P, L, P, P, P, Z, P],
+        "moe_layer_norm_workspace_size": [L, N, ctypes.POINTER(Z)],
+        "moe_act_ckpt_forward": [P, L, P, L, N, N, N, F, F, P, L, P, L, P, P],
+        "moe_act_ckpt_backward": [P, L, P, L, P, P, L, N, N, N, F, F, P, L, P, P, L, P],
+        "moe_mm_workspace_size": [N, N, N, N, N, ctypes.POINTER(Z)],
+        "moe_grouped_mm": [P, L, P, L, L, N, P, N, N, N, N, N, P, L, N, P, Z, P],
+        "moe_grouped_mm_wgrad": [P, L, P, L, P, N, N, N, N, N, P, L, L, N, P, Z, P],
+        "moe_fp8_quant_rows": [P, L, L, N, N, P, L, P, L, P],
+        "moe_fp8_quant_weights": [P, L, L, N, N, N, N, P, L, L, P, P, L, L, P, P],
+        "moe_fp8_mm": [P, L, P, L, P, L, L, P, P, N, N, N, N, P, L, N, P, Z, P],
+        "moe_mm_read_status": [P, ctypes.POINTER(ctypes.c_int32), P],
     }
     for name, args in sig.items():
         f = getattr(lib, name)
@@ -384,3 +405,214 @@ def alloc_train_save(cfg, T, device="cuda", amax=False):
     }
     st = moe_train_save_t(*(_ptr(bufs[k]) for k in ("h", "y1t_q", "y1t_s", "at_q", "at_s", "poff", "amax")))
     return st, bufs
+
+
+# ---- training-side operators --------------------------------------------------------
+# These take tensors with any row stride (the last axis contiguous) and read
+# the sizes from them, so shapes, types and devices are checked here: a tensor
+# that does not fit raises ValueError and nothing is enqueued. The library's
+# own refusals (alignment, workspace size) raise MoEError.
+_U8 = (torch.uint8, torch.float8_e4m3fn)
+_F32 = (torch.float32,)
+_I32 = (torch.int32,)
+_16BIT = (torch.bfloat16, torch.float16)
+_FLOATS = (torch.bfloat16, torch.float16, torch.float32)
+
+
+def _arg(t, name, dtypes, shape):
+    """Checks a tensor argument: on the current CUDA device, one of dtypes, of this shape, last axis contiguous."""
+    if not t.is_cuda or t.device.index != torch.cuda.current_device():
+        raise ValueError(f"{name} must be on the current CUDA device, is on {t.device}")
+    if t.dtype not in dtypes:
+        raise ValueError(f"{name} has type {t.dtype}, wants {' or '.join(map(str, dtypes))}")
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, wants {shape}")
+    if t.shape[-1] > 1 and t.stride(-1) != 1:
+        raise ValueError(f"the last axis of {name} must be contiguous")
+    return t.data_ptr()
+
+
+def _flat(t, name, dtypes, shape):
+    """As _arg, for an array without strides of its own; None stays None."""
+    if t is None:
+        return None
+    p = _arg(t, name, dtypes, shape)
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return p
+
+
+def _ld(t, name, whole=1):
+    """Stride between the rows of t (axis -2), in elements. A single row has none: its length, rounded up to `whole`."""
+    if t.shape[-2] <= 1:
+        n = max(t.shape[-1], t.stride(-2))
+        return -(-n // whole) * whole
+    if t.stride(-2) < t.shape[-1]:
+        raise ValueError(f"the rows of {name} overlap (stride {t.stride(-2)}, length {t.shape[-1]})")
+    return t.stride(-2)
+
+
+def _group(t):
+    """Stride between the matrices of t [G, rows, cols]; ignored by the library for one group."""
+    return t.stride(0) if t.shape[0] > 1 else 0
+
+
+def _dims(t, name, n):
+    if t.dim() != n:
+        raise ValueError(f"{name} has {t.dim()} axes, wants {n}")
+    return t.shape
+
+
+def _ws(ws, name="ws"):
+    if ws is None:
+        return None, 0
+    if not ws.is_cuda or not ws.is_contiguous() or ws.device.index != torch.cuda.current_device():
+        raise ValueError(f"{name} must be a contiguous buffer on the current CUDA device")
+    return ws.data_ptr(), ws.numel() * ws.element_size()
+
+
+def moe_layer_norm_workspace_size(T, H) -> int:
+    n = ctypes.c_size_t()
+    _check("moe_layer_norm_workspace_size", load().moe_layer_norm_workspace_size(int(T), int(H), ctypes.byref(n)))
+    return n.value
+
+
+def moe_layer_norm_forward(x, gamma, beta, eps, y, mean=None, rstd=None, stream=None):
+    """y = (x - mu) / sqrt(var + eps) * gamma + beta by rows of x [T, H] (bf16, f16, f32); gamma, beta [H] in x's type
+    or fp32, or None; mean, rstd [T] fp32 for the backward, or None."""
+    _require_cuda()
+    T, H = _dims(x, "x", 2)
+    wt = next((w.dtype for w in (gamma, beta) if w is not None), torch.float32)
+    wts = (wt,) if wt in (torch.float32, x.dtype) else _F32
+    _check("moe_layer_norm_forward", load().moe_layer_norm_forward(
+        _arg(x, "x", _FLOATS, (T, H)), _ld(x, "x"), _flat(gamma, "gamma", wts, (H,)), _flat(beta, "beta", wts, (H,)),
+        eps, T, H, DTYPES[x.dtype], DTYPES[wt], _arg(y, "y", (x.dtype,), (T, H)), _ld(y, "y"),
+        _flat(mean, "mean", _F32, (T,)), _flat(rstd, "rstd", _F32, (T,)), _stream(stream)))
+
+
+def moe_layer_norm_backward(dy, x, gamma, mean, rstd, dx, dgamma=None, dbeta=None, ws=None, stream=None):
+    """Gradients of moe_layer_norm_forward: dx [T, H]; dgamma, dbeta [H] (gamma's type, None to skip), whose partial
+    sums take the workspace ws (moe_layer_norm_workspace_size bytes)."""
+    _require_cuda()
+    T, H = _dims(x, "x", 2)
+    wt = next((w.dtype for w in (gamma, dgamma, dbeta) if w is not None), torch.float32)
+    wts = (wt,) if wt in (torch.float32, x.dtype) else _F32
+    own = (x.dtype,)
+    wp, wn = _ws(ws)
+    _check("moe_layer_norm_backward", load().moe_layer_norm_backward(
+        _arg(dy, "dy", own, (T, H)), _ld(dy, "dy"), _arg(x, "x", _FLOATS, (T, H)), _ld(x, "x"),
+        _flat(gamma, "gamma", wts, (H,)), _flat(mean, "mean", _F32, (T,)), _flat(rstd, "rstd", _F32, (T,)), T, H,
+        DTYPES[x.dtype], DTYPES[wt], _arg(dx, "dx", own, (T, H)), _ld(dx, "dx"), _flat(dgamma, "dgamma", wts, (H,)),
+        _flat(dbeta, "dbeta", wts, (H,)), wp, wn, _stream(stream)))
+
+
+def moe_act_ckpt_forward(h, w_row, y, q, s, act="swiglu", alpha=1.0, limit=0.0, stream=None):
+    """y [R, I] = w_row * act(h), and h's 8-bit checkpoint q (E4M3, h's shape), s [R, halves * ceil(I / 128)] fp32;
+    h [R, 2 I] (gate, up; sReLU [R, I]) bf16 or f16, w_row [R] fp32 or None."""
+    _require_cuda()
+    R, I = _dims(y, "y", 2)
+    halves = 1 if act == "srelu" else 2
+    nb = halves * -(-I // FP8_BLOCK)
+    _check("moe_act_ckpt_forward", load().moe_act_ckpt_forward(
+        _arg(h, "h", _16BIT, (R, halves * I)), _ld(h, "h"), _flat(w_row, "w_row", _F32, (R,)), R, I, DTYPES[h.dtype],
+        ACTS[act], alpha, limit, _arg(y, "y", (h.dtype,), (R, I)), _ld(y, "y"), _arg(q, "q", _U8, (R, halves * I)),
+        _ld(q, "q"), _flat(s, "s", _F32, (R, nb)), _stream(stream)))
+
+
+def moe_act_ckpt_backward(dy, q, s, w_row, dh, dw_row=None, y=None, act="swiglu", alpha=1.0, limit=0.0, stream=None):
+    """From the checkpoint of moe_act_ckpt_forward: dh (q's shape, dy's type), dw_row [R] fp32 (the gradient of w_row)
+    and the recomputed y [R, I], the last two each None to skip."""
+    _require_cuda()
+    R, I = _dims(dy, "dy", 2)
+    halves = 1 if act == "srelu" else 2
+    nb = halves * -(-I // FP8_BLOCK)
+    own = (dy.dtype,)
+    _check("moe_act_ckpt_backward", load().moe_act_ckpt_backward(
+        _arg(dy, "dy", _16BIT, (R, I)), _ld(dy, "dy"), _arg(q, "q", _U8, (R, halves * I)), _ld(q, "q"),
+        _flat(s, "s", _F32, (R, nb)), _flat(w_row, "w_row", _F32, (R,)), R, I, DTYPES[dy.dtype], ACTS[act], alpha, limit,
+        _arg(dh, "dh", own, (R, halves * I)), _ld(dh, "dh"), _flat(dw_row, "dw_row", _F32, (R,)),
+        None if y is None else _arg(y, "y", own, (R, I)), 0 if y is None else _ld(y, "y"), _stream(stream)))
+
+
+def moe_mm_workspace_size(kind, R, N, K, G=1) -> int:
+    n = ctypes.c_size_t()
+    _check("moe_mm_workspace_size", load().moe_mm_workspace_size(kind, R, N, K, G, ctypes.byref(n)))
+    return n.value
+
+
+def moe_grouped_mm(x, w, offsets, out, ws, trans_w=False, stream=None):
+    """out[r] = w[e] x[r] for the rows r of each group e (offsets [G + 1] int32): x [R, K], w [G, N, K], out [R, N];
+    trans_w: w [G, K, N], out[r] = w[e]^T x[r], the gradient of the forward's rows. bf16 or f16; out in x's type or
+    fp32. ws: moe_mm_workspace_size(MOE_MM_ROWS, R, N, K, G) bytes, zeroed once."""
+    _require_cuda()
+    R, K = _dims(x, "x", 2)
+    G = _dims(w, "w", 3)[0]
+    N = w.shape[2] if trans_w else w.shape[1]
+    wp, wn = _ws(ws)
+    _check("moe_grouped_mm", load().moe_grouped_mm(
+        _arg(x, "x", _16BIT, (R, K)), _ld(x, "x", 8), _arg(w, "w", (x.dtype,), (G, K, N) if trans_w else (G, N, K)),
+        _group(w), _ld(w, "w", 8), int(trans_w), _flat(offsets, "offsets", _I32, (G + 1,)), R, N, K, G, DTYPES[x.dtype],
+        _arg(out, "out", (x.dtype, torch.float32), (R, N)), _ld(out, "out"), DTYPES[out.dtype], wp, wn,
+        _stream(stream)))
+
+
+def moe_grouped_mm_wgrad(dy, x, offsets, dw, ws, stream=None):
+    """dw[e] [N, K] = sum over group e's rows of dy[r]^T x[r]; dy [R, N], x [R, K] bf16 or f16, dw [G, N, K] in their
+    type or fp32. ws: moe_mm_workspace_size(MOE_MM_WGRAD, R, N, K, G) bytes, zeroed once."""
+    _require_cuda()
+    G, N, K = _dims(dw, "dw", 3)
+    R = _dims(x, "x", 2)[0]
+    wp, wn = _ws(ws)
+    _check("moe_grouped_mm_wgrad", load().moe_grouped_mm_wgrad(
+        _arg(dy, "dy", (x.dtype,), (R, N)), _ld(dy, "dy", 8), _arg(x, "x", _16BIT, (R, K)), _ld(x, "x", 8),
+        _flat(offsets, "offsets", _I32, (G + 1,)), R, N, K, G, DTYPES[x.dtype],
+        _arg(dw, "dw", (x.dtype, torch.float32), (G, N, K)), _group(dw), _ld(dw, "dw"), DTYPES[dw.dtype], wp, wn,
+        _stream(stream)))
+
+
+def moe_fp8_quant_rows(x, q, s, stream=None):
+    """E4M3 codes q [R, C] and fp32 scales s [R, ceil(C / 128)] of x [R, C], one scale for 128 columns of a row."""
+    _require_cuda()
+    R, C = _dims(x, "x", 2)
+    _check("moe_fp8_quant_rows", load().moe_fp8_quant_rows(
+        _arg(x, "x", _FLOATS, (R, C)), _ld(x, "x"), R, C, DTYPES[x.dtype], _arg(q, "q", _U8, (R, C)), _ld(q, "q"),
+        _arg(s, "s", _F32, (R, -(-C // FP8_BLOCK))), _ld(s, "s"), _stream(stream)))
+
+
+def moe_fp8_quant_weights(w, q, s, qt=None, st=None, stream=None):
+    """E4M3 codes q [G, N, K] and fp32 scales s [G, ceil(N / 128), ceil(K / 128)] of w [G, N, K], one scale for
+    128 x 128; qt [G, K, N], st [G, ceil(K / 128), ceil(N / 128)]: the same, transposed."""
+    _require_cuda()
+    G, N, K = _dims(w, "w", 3)
+    nb, kb = -(-N // FP8_BLOCK), -(-K // FP8_BLOCK)
+    t = qt is not None
+    _check("moe_fp8_quant_weights", load().moe_fp8_quant_weights(
+        _arg(w, "w", _FLOATS, (G, N, K)), _group(w), _ld(w, "w"), G, N, K, DTYPES[w.dtype],
+        _arg(q, "q", _U8, (G, N, K)), _group(q), _ld(q, "q"), _flat(s, "s", _F32, (G, nb, kb)),
+        _arg(qt, "qt", _U8, (G, K, N)) if t else None, _group(qt) if t else 0, _ld(qt, "qt") if t else 0,
+        _flat(st, "st", _F32, (G, kb, nb)), _stream(stream)))
+
+
+def moe_fp8_mm(xq, xs, wq, wscale, out, ws, offsets=None, stream=None):
+    """out [R, N] (bf16, f16 or fp32) = the product of E4M3 rows xq [R, K] with scales xs [R, ceil(K / 128)] and E4M3
+    weights wq [G, N, K] with scales wscale [G, ceil(N / 128), ceil(K / 128)]; offsets as in moe_grouped_mm, or None
+    with one group. ws: moe_mm_workspace_size(MOE_MM_FP8, R, N, K, G) bytes, zeroed once."""
+    _require_cuda()
+    R, K = _dims(xq, "xq", 2)
+    G, N = _dims(wq, "wq", 3)[:2]
+    nb, kb = -(-N // FP8_BLOCK), -(-K // FP8_BLOCK)
+    wp, wn = _ws(ws)
+    _check("moe_fp8_mm", load().moe_fp8_mm(
+        _arg(xq, "xq", _U8, (R, K)), _ld(xq, "xq", 16), _arg(xs, "xs", _F32, (R, kb)), _ld(xs, "xs"),
+        _arg(wq, "wq", _U8, (G, N, K)), _group(wq), _ld(wq, "wq", 16), _flat(wscale, "wscale", _F32, (G, nb, kb)),
+        _flat(offsets, "offsets", _I32, (G + 1,)), R, N, K, G, _arg(out, "out", _FLOATS, (R, N)), _ld(out, "out"),
+        DTYPES[out.dtype], wp, wn, _stream(stream)))
+
+
+def moe_mm_read_status(ws, stream=None) -> int:
+    """Status bits (MOE_DEV_*) of a products' workspace since the last call; synchronises the stream and clears them."""
+    v = ctypes.c_int32()
+    code = load().moe_mm_read_status(_ptr(ws), ctypes.byref(v), _stream(stream))
+    if code not in (MOE_OK, 5):
+        raise MoEError("moe_mm_read_status", code)
+    return v.value

@@ -1,0 +1,453 @@
+// Layer norm of rows, forward and backward, for the block the routed layer
+// sits in (the norm in front of the router).
+//
+//   mu = mean(x), v = mean((x - mu)^2), r = 1 / sqrt(v + eps)
+//   y  = (x - mu) r gamma + beta
+//   xh = (x - mu) r, t = dy gamma
+//   dx = r (t - mean(t) - xh mean(t xh))
+//   dgamma = sum over rows of dy xh,  dbeta = sum over rows of dy
+//
+// Bound: HBM. A row is read once and kept in registers (packed as it came),
+// so the variance is taken about the finished mean, in fp32, without a second
+// read. A row belongs to TPR threads of one CTA (a warp for short rows), each
+// with NV packs of 16 bytes; a persistent grid walks the rows. The backward's
+// threads own the same columns in every row, so the sums over rows of the
+// weight's gradient stay in registers and reach memory once per CTA, as fp32
+// partial rows that a second kernel adds in a fixed order: no atomics, the
+// same bits every run.
+#include "ops.cuh"
+
+namespace moe {
+
+constexpr int kNormMaxThreads = 1024;
+constexpr int kNormBwdThreads = 512;    // the backward holds four fp32 or packed values a column
+
+// Sums of a and b over the TPR threads of a row: shuffles, then the warps'
+// sums through shared memory (red: two floats a warp), added in warp order by
+// everyone. One barrier; consecutive calls alternate between two buffers.
+template <bool BLOCK>
+__device__ __forceinline__ float2 row_sum2(float a, float b, float2* red, int nw) {
+  a = warp_sum(a);
+  b = warp_sum(b);
+  if constexpr (!BLOCK) return make_float2(a, b);
+  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = make_float2(a, b);
+  __syncthreads();
+  float2 s = red[0];
+  for (int i = 1; i < nw; ++i) {
+    const float2 o = red[i];
+    s.x += o.x;
+    s.y += o.y;
+  }
+  return s;
+}
+
+// Element i of a weight vector held in E's type or fp32; `def` when absent.
+template <typename E, bool WF32>
+__device__ __forceinline__ float weight_at(const void* w, int i, float def) {
+  if (!w) return def;
+  if constexpr (WF32) return reinterpret_cast<const float*>(w)[i];
+  else return E::to(reinterpret_cast<const typename E::raw*>(w)[i]);
+}
+
+// V consecutive weights from column c (16-byte accesses where V > 1).
+template <typename E, bool WF32, int V>
+__device__ __forceinline__ void weights_at(float (&o)[V], const void* w, int c, float def) {
+  if (!w) {
+#pragma unroll
+    for (int j = 0; j < V; ++j) o[j] = def;
+    return;
+  }
+  if constexpr (V == 1) {
+    o[0] = weight_at<E, WF32>(w, c, def);
+  } else if constexpr (WF32) {
+    const float4* p = reinterpret_cast<const float4*>(reinterpret_cast<const float*>(w) + c);
+#pragma unroll
+    for (int j = 0; j < V / 4; ++j) {
+      const float4 f = p[j];
+      o[4 * j] = f.x; o[4 * j + 1] = f.y; o[4 * j + 2] = f.z; o[4 * j + 3] = f.w;
+    }
+  } else {
+    Pack<E, V> p;
+    load_pack(p, reinterpret_cast<const typename E::raw*>(w) + c);
+#pragma unroll
+    for (int j = 0; j < V; ++j) o[j] = E::to(p.v[j]);
+  }
+}
+
+// Rows per CTA: 1 with BLOCK, else one per warp.
+template <typename E, bool WF32, int V, int NV, bool BLOCK>
+__global__ void __launch_bounds__(BLOCK ? kNormMaxThreads : 128) k_norm_fwd(NormArgs a) {
+  using raw = typename E::raw;
+  pdl_enter();
+  __shared__ float2 red[2][kNormMaxThreads / 32];
+  const int tpr = BLOCK ? blockDim.x : 32, t = BLOCK ? threadIdx.x : threadIdx.x & 31;
+  const int nw = tpr / 32, rpb = BLOCK ? 1 : blockDim.x / 32;
+  const float inv_h = 1.0f / (float)a.H;
+  for (int64_t row = (int64_t)blockIdx.x * rpb + (BLOCK ? 0 : threadIdx.x / 32); row < a.T;
+       row += (int64_t)gridDim.x * rpb) {
+    const raw* x = reinterpret_cast<const raw*>(a.x) + row * a.ldx;
+    Pack<E, V> p[NV];
+    float s = 0.f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int c = (i * tpr + t) * V;
+      if (c < a.H) load_pack(p[i], x + c);
+    }
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+      if ((i * tpr + t) * V < a.H) {
+#pragma unroll
+        for (int j = 0; j < V; ++j) s += E::to(p[i].v[j]);
+      }
+    const float mu = row_sum2<BLOCK>(s, 0.f, red[0], nw).x * inv_h;
+    float m2 = 0.f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+      if ((i * tpr + t) * V < a.H) {
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+          const float d = E::to(p[i].v[j]) - mu;
+          m2 = fmaf(d, d, m2);
+        }
+      }
+    const float r = rsqrtf(row_sum2<BLOCK>(m2, 0.f, red[1], nw).x * inv_h + a.eps);
+    if (t == 0) {
+      if (a.mean) a.mean[row] = mu;
+      if (a.rstd) a.rstd[row] = r;
+    }
+    raw* y = reinterpret_cast<raw*>(a.out) + row * a.ldo;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int c = (i * tpr + t) * V;
+      if (c < a.H) {
+        float g[V], b[V];
+        weights_at<E, WF32, V>(g, a.gamma, c, 1.f);
+        weights_at<E, WF32, V>(b, a.beta, c, 0.f);
+        Pack<E, V> o;
+#pragma unroll
+        for (int j = 0; j < V; ++j) o.v[j] = E::from(fmaf((E::to(p[i].v[j]) - mu) * r, g[j], b[j]));
+        store_pack<E, V>(y + c, o);
+      }
+    }
+  }
+}
+
+// Rows too long for the registers of one CTA: the row is read three times
+// (the later reads come from L2).
+template <typename E, bool WF32>
+__global__ void __launch_bounds__(kNormMaxThreads) k_norm_fwd_long(NormArgs a) {
+  using raw = typename E::raw;
+  pdl_enter();
+  __shared__ float2 red[2][kNormMaxThreads / 32];
+  const int nw = blockDim.x / 32;
+  const float inv_h = 1.0f / (float)a.H;
+  for (int64_t row = blockIdx.x; row < a.T; row += gridDim.x) {
+    const raw* x = reinterpret_cast<const raw*>(a.x) + row * a.ldx;
+    float s = 0.f;
+    for (int c = threadIdx.x; c < a.H; c += blockDim.x) s += E::to(x[c]);
+    const float mu = row_sum2<true>(s, 0.f, red[0], nw).x * inv_h;
+    float m2 = 0.f;
+    for (int c = threadIdx.x; c < a.H; c += blockDim.x) {
+      const float d = E::to(x[c]) - mu;
+      m2 = fmaf(d, d, m2);
+    }
+    const float r = rsqrtf(row_sum2<true>(m2, 0.f, red[1], nw).x * inv_h + a.eps);
+    if (threadIdx.x == 0) {
+      if (a.mean) a.mean[row] = mu;
+      if (a.rstd) a.rstd[row] = r;
+    }
+    raw* y = reinterpret_cast<raw*>(a.out) + row * a.ldo;
+    for (int c = threadIdx.x; c < a.H; c += blockDim.x)
+      y[c] = E::from(fmaf((E::to(x[c]) - mu) * r, weight_at<E, WF32>(a.gamma, c, 1.f),
+                          weight_at<E, WF32>(a.beta, c, 0.f)));
+  }
+}
+
+// PART: the weight's gradient is wanted. Partial row p = the CTA (BLOCK) or
+// the warp: part[p][0][c] = dgamma, part[p][1][c] = dbeta over its rows.
+template <typename E, bool WF32, int V, int NV, bool BLOCK, bool PART>
+__global__ void __launch_bounds__(BLOCK ? kNormBwdThreads : 128) k_norm_bwd(NormArgs a) {
+  using raw = typename E::raw;
+  pdl_enter();
+  __shared__ float2 red[2][kNormMaxThreads / 32];
+  const int tpr = BLOCK ? blockDim.x : 32, t = BLOCK ? threadIdx.x : threadIdx.x & 31;
+  const int nw = tpr / 32, rpb = BLOCK ? 1 : blockDim.x / 32;
+  const int64_t slot = (int64_t)blockIdx.x * rpb + (BLOCK ? 0 : threadIdx.x / 32);
+  const float inv_h = 1.0f / (float)a.H;
+  float dg[PART ? NV * V : 1], db[PART ? NV * V : 1];
+  if constexpr (PART) {
+#pragma unroll
+    for (int i = 0; i < NV * V; ++i) dg[i] = db[i] = 0.f;
+  }
+  int flip = 0;
+  for (int64_t row = slot; row < a.T; row += (int64_t)gridDim.x * rpb, flip ^= 1) {
+    const raw* x = reinterpret_cast<const raw*>(a.x) + row * a.ldx;
+    const raw* dy = reinterpret_cast<const raw*>(a.dy) + row * a.lddy;
+    Pack<E, V> px[NV], pd[NV];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int c = (i * tpr + t) * V;
+      if (c < a.H) {
+        load_pack(px[i], x + c);
+        load_pack(pd[i], dy + c);
+      }
+    }
+    const float mu = a.mean[row], r = a.rstd[row];
+    float s1 = 0.f, s2 = 0.f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int c = (i * tpr + t) * V;
+      if (c < a.H) {
+        float g[V];
+        weights_at<E, WF32, V>(g, a.gamma, c, 1.f);
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+          const float d = E::to(pd[i].v[j]), xh = (E::to(px[i].v[j]) - mu) * r, tg = d * g[j];
+          s1 += tg;
+          s2 = fmaf(tg, xh, s2);
+          if constexpr (PART) {
+            dg[i * V + j] = fmaf(d, xh, dg[i * V + j]);
+            db[i * V + j] += d;
+          }
+        }
+      }
+    }
+    const float2 m = row_sum2<BLOCK>(s1, s2, red[flip], nw);
+    const float m1 = m.x * inv_h, m2 = m.y * inv_h;
+    raw* dx = reinterpret_cast<raw*>(a.out) + row * a.ldo;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int c = (i * tpr + t) * V;
+      if (c < a.H) {
+        float g[V];
+        weights_at<E, WF32, V>(g, a.gamma, c, 1.f);
+        Pack<E, V> o;
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+          const float xh = (E::to(px[i].v[j]) - mu) * r;
+          o.v[j] = E::from(r * (E::to(pd[i].v[j]) * g[j] - m1 - xh * m2));
+        }
+        store_pack<E, V>(dx + c, o);
+      }
+    }
+  }
+  if constexpr (PART) {
+    if (slot >= a.T) return;      // a warp without rows owns no partial row
+    float* pg = a.part + slot * 2 * a.H;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int c = (i * tpr + t) * V;
+      if (c < a.H) {
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+          pg[c + j] = dg[i * V + j];
+          pg[a.H + c + j] = db[i * V + j];
+        }
+      }
+    }
+  }
+}
+
+// dx of rows too long for registers (three reads), without the weight's
+// gradient.
+template <typename E, bool WF32>
+__global__ void __launch_bounds__(kNormMaxThreads) k_norm_bwd_long(NormArgs a) {
+  using raw = typename E::raw;
+  pdl_enter();
+  __shared__ float2 red[2][kNormMaxThreads / 32];
+  const int nw = blockDim.x / 32;
+  const float inv_h = 1.0f / (float)a.H;
+  int flip = 0;
+  for (int64_t row = blockIdx.x; row < a.T; row += gridDim.x, flip ^= 1) {
+    const raw* x = reinterpret_cast<const raw*>(a.x) + row * a.ldx;
+    const raw* dy = reinterpret_cast<const raw*>(a.dy) + row * a.lddy;
+    const float mu = a.mean[row], r = a.rstd[row];
+    float s1 = 0.f, s2 = 0.f;
+    for (int c = threadIdx.x; c < a.H; c += blockDim.x) {
+      const float tg = E::to(dy[c]) * weight_at<E, WF32>(a.gamma, c, 1.f);
+      s1 += tg;
+      s2 = fmaf(tg, (E::to(x[c]) - mu) * r, s2);
+    }
+    const float2 m = row_sum2<true>(s1, s2, red[flip], nw);
+    const float m1 = m.x * inv_h, m2 = m.y * inv_h;
+    raw* dx = reinterpret_cast<raw*>(a.out) + row * a.ldo;
+    for (int c = threadIdx.x; c < a.H; c += blockDim.x) {
+      const float tg = E::to(dy[c]) * weight_at<E, WF32>(a.gamma, c, 1.f);
+      dx[c] = E::from(r * (tg - m1 - (E::to(x[c]) - mu) * r * m2));
+    }
+  }
+}
+
+// Partial rows of the weight's gradient of long rows: thread = column, block
+// row p takes rows p, p + P, ...
+template <typename E>
+__global__ void __launch_bounds__(256) k_norm_dw_long(NormArgs a) {
+  using raw = typename E::raw;
+  pdl_enter();
+  const int c = blockIdx.x * 256 + threadIdx.x;
+  if (c >= a.H) return;
+  float dg = 0.f, db = 0.f;
+  for (int64_t row = blockIdx.y; row < a.T; row += gridDim.y) {
+    const float d = E::to(reinterpret_cast<const raw*>(a.dy)[row * a.lddy + c]);
+    dg = fmaf(d, (E::to(reinterpret_cast<const raw*>(a.x)[row * a.ldx + c]) - a.mean[row]) * a.rstd[row], dg);
+    db += d;
+  }
+  float* p = a.part + (int64_t)blockIdx.y * 2 * a.H;
+  p[c] = dg;
+  p[a.H + c] = db;
+}
+
+// dgamma / dbeta = the P partial rows added in a fixed order: 32 columns a
+// block, row lane l adds partial rows l, l + 32, ..., then the lanes in order.
+template <typename E, bool WF32>
+__global__ void __launch_bounds__(1024) k_norm_dw_sum(const float* __restrict__ part, int P, int H, void* dgamma,
+                                                      void* dbeta) {
+  pdl_enter();
+  __shared__ float s[32][33];
+  const int c = blockIdx.x * 32 + (threadIdx.x & 31), l = threadIdx.x >> 5;
+  const int64_t at = (int64_t)blockIdx.y * H + c;
+  float v = 0.f;
+  if (c < H)
+    for (int p = l; p < P; p += 32) v += part[(int64_t)p * 2 * H + at];
+  s[l][threadIdx.x & 31] = v;
+  __syncthreads();
+  if (l == 0 && c < H) {
+    float sum = 0.f;
+#pragma unroll
+    for (int i = 0; i < 32; ++i) sum += s[i][threadIdx.x];
+    void* d = blockIdx.y == 0 ? dgamma : dbeta;
+    if (d) {
+      if constexpr (WF32) reinterpret_cast<float*>(d)[c] = sum;
+      else reinterpret_cast<typename E::raw*>(d)[c] = E::from(sum);
+    }
+  }
+}
+
+// ---- host ---------------------------------------------------------------------
+static bool aligned(const void* p, size_t n) { return ((uintptr_t)p & (n - 1)) == 0; }
+
+// 16-byte accesses: every row of x, dy and out, and the weights, start on 16
+// bytes and H is a whole number of packs.
+static bool vec_ok(const NormArgs& a, int esize) {
+  const int V = 16 / esize;
+  const bool rows = a.H % V == 0 && a.ldx % V == 0 && a.ldo % V == 0 && aligned(a.x, 16) && aligned(a.out, 16) &&
+                    (!a.dy || (a.lddy % V == 0 && aligned(a.dy, 16)));
+  return rows && aligned(a.gamma, 16) && aligned(a.beta, 16);
+}
+
+struct NormPlan {
+  bool longrow, block;
+  int nv, threads;
+  int64_t grid;
+};
+// Threads and packs a thread for rows of n packs; per_cta: rows a CTA holds.
+static NormPlan norm_plan(int64_t n, int64_t T, int max_nv, int max_threads_per_sm, int max_parts, int max_threads) {
+  NormPlan p = {};
+  if (n <= 32) {                       // a warp a row
+    p.nv = 1;
+    p.threads = 128;
+  } else {
+    p.block = true;
+    // fewest packs a thread that leave at most 256 threads a row: short
+    // barriers, several rows in flight on an SM; longer rows take max_nv
+    p.nv = 1;
+    while (p.nv < max_nv && (n + p.nv - 1) / p.nv > 256) p.nv *= 2;
+    p.threads = (int)(((n + p.nv - 1) / p.nv + 31) / 32 * 32);
+    if (p.threads > max_threads) p.longrow = true;
+  }
+  if (p.longrow) p.threads = kNormMaxThreads;
+  const int rpb = p.block ? 1 : p.threads / 32;
+  int64_t g = (int64_t)device_sms() * std::max(1, max_threads_per_sm / p.threads);
+  if (max_parts) g = std::min<int64_t>(g, max_parts / rpb);
+  p.grid = std::max<int64_t>(1, std::min<int64_t>(g, (T + rpb - 1) / rpb));
+  return p;
+}
+
+template <typename E, bool WF32, int V>
+static cudaError_t fwd_v(const NormArgs& a, cudaStream_t st) {
+  constexpr int kMaxNv = V == 1 ? 16 : 4;
+  const NormPlan p = norm_plan(((int64_t)a.H + V - 1) / V, a.T, kMaxNv, 2048, 0, kNormMaxThreads);
+  const dim3 g((unsigned)p.grid), b(p.threads);
+  note_launch();
+  if (p.longrow) return launch_pdl(k_norm_fwd_long<E, WF32>, g, b, 0, st, a);
+  if (!p.block) return launch_pdl(k_norm_fwd<E, WF32, V, 1, false>, g, b, 0, st, a);
+  switch (p.nv) {
+    case 1: return launch_pdl(k_norm_fwd<E, WF32, V, 1, true>, g, b, 0, st, a);
+    case 2: return launch_pdl(k_norm_fwd<E, WF32, V, 2, true>, g, b, 0, st, a);
+    case 4: return launch_pdl(k_norm_fwd<E, WF32, V, 4, true>, g, b, 0, st, a);
+    default: break;
+  }
+  if constexpr (V == 1) {
+    if (p.nv == 8) return launch_pdl(k_norm_fwd<E, WF32, V, 8, true>, g, b, 0, st, a);
+    return launch_pdl(k_norm_fwd<E, WF32, V, 16, true>, g, b, 0, st, a);
+  }
+  return cudaErrorInvalidValue;
+}
+
+template <typename E, bool WF32, int V, int NV, bool BLOCK>
+static cudaError_t bwd_launch(const NormArgs& a, const NormPlan& p, cudaStream_t st) {
+  const dim3 g((unsigned)p.grid), b(p.threads);
+  note_launch();
+  if (a.dgamma || a.dbeta) return launch_pdl(k_norm_bwd<E, WF32, V, NV, BLOCK, true>, g, b, 0, st, a);
+  return launch_pdl(k_norm_bwd<E, WF32, V, NV, BLOCK, false>, g, b, 0, st, a);
+}
+
+template <typename E, bool WF32, int V>
+static cudaError_t bwd_v(const NormArgs& a, cudaStream_t st) {
+  const bool want = a.dgamma || a.dbeta;
+  constexpr int kMaxNv = V == 1 ? 16 : 4;
+  const NormPlan p = norm_plan(((int64_t)a.H + V - 1) / V, a.T, kMaxNv, 1024, want ? kNormMaxParts : 0,
+                               kNormBwdThreads);
+  cudaError_t e = cudaErrorInvalidValue;
+  int64_t parts = std::min<int64_t>(a.T, p.grid * (p.block ? 1 : p.threads / 32));
+  if (p.longrow) {
+    note_launch();
+    e = launch_pdl(k_norm_bwd_long<E, WF32>, dim3((unsigned)p.grid), dim3(p.threads), 0, st, a);
+    if (e != cudaSuccess) return e;
+    if (want) {
+      const int cb = (a.H + 255) / 256;
+      parts = std::min<int64_t>(std::min<int64_t>(a.T, kNormMaxParts), std::max(1, device_sms() * 8 / cb));
+      note_launch();
+      e = launch_pdl(k_norm_dw_long<E>, dim3(cb, (unsigned)parts), dim3(256), 0, st, a);
+    }
+  } else if (!p.block) {
+    e = bwd_launch<E, WF32, V, 1, false>(a, p, st);
+  } else if (p.nv == 1) {
+    e = bwd_launch<E, WF32, V, 1, true>(a, p, st);
+  } else if (p.nv == 2) {
+    e = bwd_launch<E, WF32, V, 2, true>(a, p, st);
+  } else if (p.nv == 4) {
+    e = bwd_launch<E, WF32, V, 4, true>(a, p, st);
+  } else if constexpr (V == 1) {
+    if (p.nv == 8) e = bwd_launch<E, WF32, V, 8, true>(a, p, st);
+    else e = bwd_launch<E, WF32, V, 16, true>(a, p, st);
+  }
+  if (e != cudaSuccess || !want) return e;
+  note_launch();
+  return launch_pdl(k_norm_dw_sum<E, WF32>, dim3((a.H + 31) / 32, 2), dim3(1024), 0, st, (const float*)a.part,
+                    (int)parts, a.H, a.dgamma, a.dbeta);
+}
+
+template <typename E, bool WF32, bool FWD>
+static cudaError_t by_vec(const NormArgs& a, cudaStream_t st) {
+  constexpr int V = 16 / (int)sizeof(typename E::raw);
+  if (vec_ok(a, sizeof(typename E::raw))) {
+    if constexpr (FWD) return fwd_v<E, WF32, V>(a, st);
+    else return bwd_v<E, WF32, V>(a, st);
+  }
+  if constexpr (FWD) return fwd_v<E, WF32, 1>(a, st);
+  else return bwd_v<E, WF32, 1>(a, st);
+}
+
+template <bool FWD>
+static cudaError_t by_type(const NormArgs& a, cudaStream_t st) {
+  if (a.dtype == MOE_DT_F32) return by_vec<F32, true, FWD>(a, st);
+  if (a.dtype == MOE_DT_F16)
+    return a.wdtype == MOE_DT_F32 ? by_vec<F16, true, FWD>(a, st) : by_vec<F16, false, FWD>(a, st);
+  return a.wdtype == MOE_DT_F32 ? by_vec<Bf16, true, FWD>(a, st) : by_vec<Bf16, false, FWD>(a, st);
+}
+
+cudaError_t launch_norm_fwd(const NormArgs& a, cudaStream_t st) { return by_type<true>(a, st); }
+cudaError_t launch_norm_bwd(const NormArgs& a, cudaStream_t st) { return by_type<false>(a, st); }
+
+}  // namespace moe
