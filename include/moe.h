@@ -480,7 +480,7 @@ moe_status_t moe_mm_workspace_size(int kind, int R, int N, int K, int G, size_t*
  * zero; offsets that descend or leave [0, R] are clamped and set
  * MOE_DEV_BAD_OFFSETS. x, w and ws start on 16 bytes, ldx, ldw and w_group
  * are multiples of 8 elements (MOE_ERR_INVALID_ARG otherwise); N, K and the
- * group sizes are any. */
+ * group sizes are any (R, N, K at most 2^30). */
 moe_status_t moe_grouped_mm(const void* x, int64_t ldx, const void* w, int64_t w_group, int64_t ldw, int trans_w,
                             const int32_t* offsets, int R, int N, int K, int G, int dtype, void* out, int64_t ldo,
                             int out_dtype, void* ws, size_t ws_bytes, void* stream);

@@ -23,9 +23,15 @@ bool act_ok(int act, float limit) {
 }
 int64_t blocks_of(int64_t n) { return (n + kQBlock - 1) / kQBlock; }
 
+// Sizes up to 2^30 leave room to round up to whole tiles in 32 bits.
+bool mm_sizes_ok(int R, int N, int K, int G) {
+  constexpr int kMost = 1 << 30;
+  return R >= 0 && R <= kMost && N >= 1 && N <= kMost && K >= 1 && K <= kMost && G >= 1 && G <= 2048;
+}
+
 // Common checks of a product's sizes and workspace.
 moe_status_t mm_check(int kind, int R, int N, int K, int G, const int32_t* offsets, void* ws, size_t ws_bytes) {
-  if (R < 0 || N < 1 || K < 1 || G < 1 || G > 2048) return MOE_ERR_INVALID_ARG;
+  if (!mm_sizes_ok(R, N, K, G)) return MOE_ERR_INVALID_ARG;
   if (!maybe(offsets, 4) || (!offsets && (G != 1 || kind != MOE_MM_FP8))) return MOE_ERR_INVALID_ARG;
   if (!have(ws, 16)) return MOE_ERR_INVALID_ARG;
   size_t need = 0;
@@ -152,7 +158,7 @@ moe_status_t moe_fp8_quant_weights(const void* w, int64_t w_group, int64_t ldw, 
 }
 
 moe_status_t moe_mm_workspace_size(int kind, int R, int N, int K, int G, size_t* bytes) {
-  if (!bytes || R < 0 || N < 1 || K < 1 || G < 1 || G > 2048) return MOE_ERR_INVALID_ARG;
+  if (!bytes || !mm_sizes_ok(R, N, K, G)) return MOE_ERR_INVALID_ARG;
   if (kind != MOE_MM_ROWS && kind != MOE_MM_WGRAD && kind != MOE_MM_FP8) return MOE_ERR_INVALID_ARG;
   const int S = mm_splits(kind, R, N, K, G);
   const size_t outs = kind == MOE_MM_WGRAD ? (size_t)G * N * K : (size_t)R * N;

@@ -129,8 +129,18 @@ struct MmArgs {
   int S;                        // pieces of the reduction (1: no partial sums)
 };
 enum { kMmRows = 0, kMmWgrad = 1, kMmFp8 = 2 };
-// Pieces the reduction of a product is split into, from its sizes alone.
+// Column tile and pieces of the reduction, from the sizes alone.
+struct MmPlan {
+  int bn, S;
+};
+MmPlan mm_plan(int kind, int R, int N, int K, int G);
 int mm_splits(int kind, int R, int N, int K, int G);
+// Adds the partial sums of a split product into out.
+cudaError_t launch_mm_join(const MmArgs& a, bool wgrad, cudaStream_t st);
+// Tensor map of rank dimensions (innermost first; strides in elements, from
+// the second axis on), 128-byte swizzle, zeros past every edge.
+bool make_tmap(CUtensorMap* map, const void* base, int esize, int rank, const int64_t* dims, const int64_t* strides,
+               const int* box);
 cudaError_t launch_mm16(const MmArgs& a, bool wgrad, cudaStream_t st);
 cudaError_t launch_mm_fp8(const MmArgs& a, cudaStream_t st);
 
