@@ -33,7 +33,6 @@ namespace moe {
 
 enum { kRowsNT = 0, kRowsNN = 1, kWgradMN = 2 };
 
-constexpr int kGM = 128;              // tile rows (MMA M)
 constexpr int kGK = 64;               // reduction a stage: one 128-byte swizzle row
 constexpr int kGThreads = 384;
 constexpr int kGChunk = 64 * kGK * 2; // bytes of 64 M / N elements of an MN-contiguous stage
@@ -60,41 +59,6 @@ struct GArgs {
   int a_chunks, b_chunks;   // MN-contiguous operands: 64-wide chunks a copy takes (1: one copy a chunk)
 };
 
-struct GUnit {
-  int e, row0, rows;    // first A row of the tile (wgrad: first feature) and its real rows
-  int n0;               // first column
-  int k0, k1;           // 64-wide reduction blocks [k0, k1) of this piece
-  int red;              // the whole reduction's length
-  int piece;
-};
-
-template <int MODE, int BN>
-__device__ __forceinline__ void g_unit(const GArgs& g, const int32_t* off, const int32_t* uoff, int64_t u, GUnit& w) {
-  const int S = g.m.S;
-  const int64_t t = u / S;
-  w.piece = (int)(u - t * S);
-  const int ui = (int)(t / g.n_tiles);
-  w.n0 = (int)(t - (int64_t)ui * g.n_tiles) * BN;
-  w.e = group_of_unit(uoff, g.m.G, ui);
-  const int mi = ui - uoff[w.e], cnt = off[w.e + 1] - off[w.e];
-  if (MODE == kWgradMN) {
-    w.row0 = mi * kGM;
-    w.rows = min(kGM, g.m.N - w.row0);
-    w.red = cnt;
-  } else {
-    w.row0 = off[w.e] + mi * kGM;
-    w.rows = min(kGM, cnt - mi * kGM);
-    w.red = g.m.K;
-  }
-  const int nk = (w.red + kGK - 1) / kGK;
-  w.k0 = (int)((int64_t)nk * w.piece / S);
-  w.k1 = (int)((int64_t)nk * (w.piece + 1) / S);
-}
-
-// A copy of a K-major tile covers 16 << i rows, the fewest that hold its real
-// ones; the MMA's other rows are an earlier stage's bytes and are not stored.
-__device__ __forceinline__ int g_a_box(int rows) { return rows <= 16 ? 0 : rows <= 32 ? 1 : rows <= 64 ? 2 : 3; }
-
 // Copies of one MN-contiguous operand stage: `chunks` chunks of 64 columns
 // from column c0, rows row0 .. row0 + 63 of matrix z.
 __device__ __forceinline__ void g_load_mn(uint8_t* dst, const CUtensorMap* map, int c0, int row0, int z, int chunks,
@@ -103,44 +67,6 @@ __device__ __forceinline__ void g_load_mn(uint8_t* dst, const CUtensorMap* map, 
     tc::tma_load_4d_plain(dst, map, 0, row0, c0 / 64, z, bar);
   } else {
     for (int c = 0; c < chunks; ++c) tc::tma_load_4d_plain(dst + c * kGChunk, map, c0 + 64 * c, row0, 0, z, bar);
-  }
-}
-
-// 32 columns of a row from fp32 bits: n valid ones at p (esize 4: fp32, else
-// bf16 / f16); vec: 16-byte stores are aligned.
-__device__ __forceinline__ void store32(void* p, const uint32_t (&v)[32], int n, int out_dtype, bool vec) {
-  if (out_dtype == MOE_DT_F32) {
-    uint32_t* d = reinterpret_cast<uint32_t*>(p);
-    if (vec && n >= 32) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-        reinterpret_cast<uint4*>(d)[i] = make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
-    } else {
-#pragma unroll
-      for (int i = 0; i < 32; ++i)
-        if (i < n) d[i] = v[i];
-    }
-    return;
-  }
-  uint32_t pk[16];
-  if (out_dtype == MOE_DT_F16) {
-#pragma unroll
-    for (int i = 0; i < 16; ++i)
-      pk[i] = (uint32_t)F16::from(__uint_as_float(v[2 * i])) | ((uint32_t)F16::from(__uint_as_float(v[2 * i + 1])) << 16);
-  } else {
-#pragma unroll
-    for (int i = 0; i < 16; ++i)
-      pk[i] = (uint32_t)Bf16::from(__uint_as_float(v[2 * i])) | ((uint32_t)Bf16::from(__uint_as_float(v[2 * i + 1])) << 16);
-  }
-  if (vec && n >= 32) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      reinterpret_cast<uint4*>(p)[i] = make_uint4(pk[4 * i], pk[4 * i + 1], pk[4 * i + 2], pk[4 * i + 3]);
-  } else {
-    uint16_t* d = reinterpret_cast<uint16_t*>(p);
-#pragma unroll
-    for (int i = 0; i < 32; ++i)
-      if (i < n) d[i] = (uint16_t)(pk[i >> 1] >> (16 * (i & 1)));
   }
 }
 
@@ -199,7 +125,7 @@ __global__ void __launch_bounds__(kGThreads, 1) k_gemm16(const GArgs g, const __
       bool ok = true;
       for (int64_t u = blockIdx.x; ok && u < U; u += gridDim.x) {
         GUnit w;
-        g_unit<MODE, BN>(g, off, uoff, u, w);
+        g_unit<kWg, BN, kGK>(m, g.n_tiles, off, uoff, u, w);
         const int ai = g_a_box(w.rows);
         for (int kb = w.k0; kb < w.k1; ++kb, ++it) {
           const int slot = it % C::kStages;
@@ -242,7 +168,7 @@ __global__ void __launch_bounds__(kGThreads, 1) k_gemm16(const GArgs g, const __
     bool ok = true;
     for (int64_t u = blockIdx.x; ok && u < U; u += gridDim.x, ++tcount) {
       GUnit w;
-      g_unit<MODE, BN>(g, off, uoff, u, w);
+      g_unit<kWg, BN, kGK>(m, g.n_tiles, off, uoff, u, w);
       const int d = tcount & 1;
       ok = __all_sync(kFull, tc::mbar_wait(&accempty[d], ((tcount >> 1) & 1) ^ 1, abort));
       if (!ok) break;
@@ -327,7 +253,7 @@ __global__ void __launch_bounds__(kGThreads, 1) k_gemm16(const GArgs g, const __
     for (int64_t u = blockIdx.x; u < U; u += gridDim.x, ++tcount) {
       if ((int)(tcount & 1) != wg) continue;
       GUnit w;
-      g_unit<MODE, BN>(g, off, uoff, u, w);
+      g_unit<kWg, BN, kGK>(m, g.n_tiles, off, uoff, u, w);
       const bool got = tc::mbar_wait(&accfull[wg], mine & 1, abort);
       if (!__all_sync(kFull, got)) break;
       tc::fence_after_sync();

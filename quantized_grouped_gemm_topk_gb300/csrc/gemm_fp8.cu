@@ -1,91 +1,311 @@
-// FP8 products with a scale for each block of 128: the plain CUDA-core form (64 x 64 output tiles, 16 of the reduction at a time
-// in shared memory, fp32 sums).
+// FP8 products with a scale for each block of 128, dense or grouped by expert:
+//
+//   out[r, n] = sum_b xs[r, b] ws[n / 128, b] sum_{k in block b} xq[r, k] wq[n, k]
+//
+// on the 5th-generation tensor cores (tcgen05.mma kind::f8f6f4, E4M3 operands
+// in shared memory). The scales are arbitrary fp32 numbers, so the tensor
+// core only sums inside a block: every 128 of K its accumulator starts anew,
+// in one of 512 / BN tensor-memory slots, and the epilogue threads add it,
+// times the block's scale, to the fp32 sums of the tile that they hold in
+// registers. A thread's columns share one weight scale, so a block costs one
+// multiply per row and one fused multiply-add (two to an instruction) per
+// element, while the next blocks' MMAs run.
+//
+// Bound: the tensor pipe at training sizes (a 128 x 256 x 128 block is 512
+// cycles of MMA, its additions 256 issue slots a scheduler at most), the
+// weights' bytes at decode sizes.
+// Tiles, copies and edges as in gemm16.cu. Roles: warp 0 copies W, warp 2
+// copies x, warp 1 issues MMAs, warp 3 clears rows outside every group, warps
+// 4-11 add: warp quarter q of tensor memory, half h of the columns. They
+// take registers from the first four warps (setmaxnreg).
+// Every wait is bounded, as in gemm16.cu.
 #include "groups.cuh"
+#include "tc.cuh"
 
 namespace moe {
 
-constexpr int kTile = 64, kDepth = 16, kThr = 256;
+constexpr int kFK = kQBlock;              // reduction a stage: one scale block, one 128-byte swizzle row
+constexpr int kFThreads = 384;
+constexpr int kFABytes = kGM * kFK;
+constexpr int kFTables = 2 * 4 * (kMmMaxGroups + 1);
+// Registers a thread: at launch, then of warps 0-3 and of warps 4-11. The
+// shares sum to at most the launch's (checked against the built kernel
+// before its first launch).
+constexpr int kFRegs = 168, kFRegsLow = 88, kFRegsHigh = 208;
+static_assert(128 * kFRegsLow + 256 * kFRegsHigh <= kFThreads * kFRegs, "register shares");
 
-template <int KIND>
-__device__ __forceinline__ float mm_a(const MmArgs& a, int64_t r, int64_t i) {
-  if constexpr (KIND == kMmFp8)
-    return e4m3_to_f32(reinterpret_cast<const uint8_t*>(a.a)[r * a.lda + i]) * a.sa[r * a.ldsa + i / kQBlock];
-  const uint16_t v = reinterpret_cast<const uint16_t*>(a.a)[r * a.lda + i];
-  return a.dtype == MOE_DT_F16 ? F16::to(v) : Bf16::to(v);
+template <int BN>
+struct FCfg {
+  static constexpr int kBBytes = BN * kFK;
+  static constexpr int kStages = BN == 256 ? 4 : BN == 128 ? 6 : 8;
+  static constexpr int kSlots = 512 / BN;
+  static constexpr int kSmem = 1024 + kStages * (kFABytes + kBBytes) + 1024 + kFTables;
+  static_assert(kSmem <= 227 * 1024, "shared memory budget");
+};
+struct FMaps {
+  CUtensorMap a[4];     // boxes of 16 << i rows
+  CUtensorMap b;
+};
+struct FArgs {
+  MmArgs m;
+  int n_tiles;
+};
+
+// acc (two fp32) += {lo, hi} * s (two equal fp32)
+__device__ __forceinline__ void fma2(uint64_t& acc, uint32_t lo, uint32_t hi, uint64_t s) {
+  asm("{\n .reg .b64 t;\n mov.b64 t, {%1, %2};\n fma.rn.f32x2 %0, t, %3, %0;\n}"
+      : "+l"(acc)
+      : "r"(lo), "r"(hi), "l"(s));
 }
 
-template <int KIND>
-__global__ void __launch_bounds__(kThr) k_mm_simple(MmArgs a) {
+template <int BN>
+__global__ void __launch_bounds__(kFThreads, 1) k_gemm_fp8(const FArgs g, const __grid_constant__ FMaps maps) {
+  using C = FCfg<BN>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* base = reinterpret_cast<uint8_t*>(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+  uint8_t* sa = base;
+  uint8_t* sb = sa + C::kStages * kFABytes;
+  uint64_t* full = reinterpret_cast<uint64_t*>(sb + C::kStages * C::kBBytes);
+  uint64_t* empty = full + C::kStages;
+  uint64_t* tfull = empty + C::kStages;
+  uint64_t* tempty = tfull + C::kSlots;
+  uint64_t* drain = tempty + C::kSlots;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+  volatile int* abort = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  int* tmp = reinterpret_cast<int*>(tmem_slot + 2);
+  int32_t* off = reinterpret_cast<int32_t*>(reinterpret_cast<uint8_t*>(full) + 1024);
+  int32_t* uoff = off + kMmMaxGroups + 1;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const MmArgs& m = g.m;
+
   pdl_enter();
-  __shared__ int32_t off[kMmMaxGroups + 1], uoff[kMmMaxGroups + 1];
-  __shared__ int tmp[2 * kThr / 32];
-  __shared__ float As[kDepth][kTile + 1], Bs[kDepth][kTile + 1];
-  const bool wg = KIND == kMmWgrad;
-  // rows mode: M = rows of the group, N columns, reduction K; wgrad: M = N features, columns K, reduction rows
-  const int cols = wg ? a.K : a.N;
-  const int nt = (cols + kTile - 1) / kTile;
-  build_groups<kThr>(a.offsets, a.G, a.R, off, uoff, tmp, a.status,
-                     [&](int c) { return wg ? (a.N + kTile - 1) / kTile : (c + kTile - 1) / kTile; });
-  const int64_t units = (int64_t)uoff[a.G] * nt;
-  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-  for (int64_t u = blockIdx.x; u < units; u += gridDim.x) {
-    const int ui = (int)(u / nt), n0 = (int)(u - (int64_t)ui * nt) * kTile;
-    const int e = group_of_unit(uoff, a.G, ui);
-    const int m0 = (ui - uoff[e]) * kTile, r0 = off[e], cnt = off[e + 1] - r0;
-    const int M = wg ? a.N : cnt, red = wg ? cnt : a.K;
-    const uint16_t* b16 = reinterpret_cast<const uint16_t*>(a.b);
-    float acc[4][4] = {};
-    for (int k0 = 0; k0 < red; k0 += kDepth) {
-      for (int i = threadIdx.x; i < kTile * kDepth; i += kThr) {
-        const int m = i / kDepth, k = i % kDepth, mm = m0 + m, nn = n0 + m, kk = k0 + k;
-        float va = 0.f, vb = 0.f;
-        if (mm < M && kk < red) va = wg ? mm_a<KIND>(a, r0 + kk, mm) : mm_a<KIND>(a, r0 + mm, kk);
-        if (nn < cols && kk < red) {
-          if constexpr (KIND == kMmFp8) {
-            const int nb = (a.N + kQBlock - 1) / kQBlock, kb = (a.K + kQBlock - 1) / kQBlock;
-            vb = e4m3_to_f32(reinterpret_cast<const uint8_t*>(a.b)[e * a.bg + nn * a.ldb + kk]) *
-                 a.sb[((int64_t)e * nb + nn / kQBlock) * kb + kk / kQBlock];
-          } else {
-            const uint16_t v = wg ? b16[(int64_t)(r0 + kk) * a.ldb + nn]
-                                  : a.trans_b ? b16[e * a.bg + (int64_t)kk * a.ldb + nn]
-                                              : b16[e * a.bg + (int64_t)nn * a.ldb + kk];
-            vb = a.dtype == MOE_DT_F16 ? F16::to(v) : Bf16::to(v);
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < C::kStages; ++i) {
+      tc::mbar_init(&full[i], 2);
+      tc::mbar_init(&empty[i], 1);
+    }
+    for (int i = 0; i < C::kSlots; ++i) {
+      tc::mbar_init(&tfull[i], 1);
+      tc::mbar_init(&tempty[i], 8);     // one per adding warp
+    }
+    tc::mbar_init(drain, 1);
+    *abort = 0;
+    tc::fence_mbar_init();
+  }
+  if (warp == 1) tc::tmem_alloc(tmem_slot, 512);
+  build_groups<kFThreads>(m.offsets, m.G, m.R, off, uoff, tmp, m.status, [](int c) { return (c + kGM - 1) / kGM; });
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  const uint32_t tmem = *tmem_slot;
+  const int64_t U = (int64_t)uoff[m.G] * g.n_tiles * m.S;
+
+  if (warp < 4) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kFRegsLow));
+    if (warp == 0 || warp == 2) {
+      // ---------------- copies: warp 0 W, warp 2 x ----------------
+      if (lane == 0) {
+        const bool isb = warp == 0;
+        if (isb) tc::prefetch_tmap(&maps.b);
+        else
+          for (int i = 0; i < 4; ++i) tc::prefetch_tmap(&maps.a[i]);
+        uint32_t it = 0;
+        bool ok = true;
+        for (int64_t u = blockIdx.x; ok && u < U; u += gridDim.x) {
+          GUnit w;
+          g_unit<false, BN, kFK>(m, g.n_tiles, off, uoff, u, w);
+          const int ai = g_a_box(w.rows);
+          for (int kb = w.k0; kb < w.k1; ++kb, ++it) {
+            const int slot = it % C::kStages;
+            if (!tc::mbar_wait(&empty[slot], ((it / C::kStages) & 1) ^ 1, abort)) { ok = false; break; }
+            if (isb) {
+              tc::mbar_arrive_expect_tx(&full[slot], C::kBBytes);
+              tc::tma_load_3d_plain(sb + slot * C::kBBytes, &maps.b, kb * kFK, w.n0, w.e, &full[slot]);
+            } else {
+              tc::mbar_arrive_expect_tx(&full[slot], (uint32_t)(kFK * (16 << ai)));
+              tc::tma_load_2d_plain(sa + slot * kFABytes, &maps.a[ai], kb * kFK, w.row0, &full[slot]);
+            }
           }
         }
-        As[k][m] = va;
-        Bs[k][m] = vb;
+        if (!ok || *abort) {        // wind-down: bounded waits for the copies in flight
+          volatile int never = 0;
+          const uint32_t n = it < (uint32_t)C::kStages ? it : (uint32_t)C::kStages;
+          for (uint32_t k = 0; k < n; ++k) {
+            const uint32_t i2 = it - 1 - k;
+            tc::mbar_wait(&full[i2 % C::kStages], (i2 / C::kStages) & 1, &never, 100000000ll);
+          }
+        }
       }
-      __syncthreads();
-      for (int k = 0; k < kDepth; ++k)
-        for (int i = 0; i < 4; ++i)
-          for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(As[k][ty + 16 * i], Bs[k][tx + 16 * j], acc[i][j]);
-      __syncthreads();
-    }
-    for (int i = 0; i < 4; ++i)
-      for (int j = 0; j < 4; ++j) {
-        const int m = m0 + ty + 16 * i, n = n0 + tx + 16 * j;
-        if (m >= M || n >= cols) continue;
-        const int64_t at = wg ? e * a.og + (int64_t)m * a.ldo + n : (int64_t)(r0 + m) * a.ldo + n;
-        if (a.out_dtype == MOE_DT_F32) reinterpret_cast<float*>(a.out)[at] = acc[i][j];
-        else reinterpret_cast<uint16_t*>(a.out)[at] =
-            a.out_dtype == MOE_DT_F16 ? F16::from(acc[i][j]) : Bf16::from(acc[i][j]);
+    } else if (warp == 1) {
+      // ---------------- MMAs ----------------
+      if (lane == 0) {
+        // kind::f8f6f4: E4M3 is format 0 of both operands; fp32 accumulator
+        constexpr uint32_t idesc = tc::idesc_f16_f32(kGM, BN);
+        uint32_t it = 0;
+        bool ok = true;
+        for (int64_t u = blockIdx.x; ok && u < U; u += gridDim.x) {
+          GUnit w;
+          g_unit<false, BN, kFK>(m, g.n_tiles, off, uoff, u, w);
+          for (int kb = w.k0; kb < w.k1; ++kb, ++it) {
+            const int slot = it % C::kStages, ts = it % C::kSlots;
+            if (!tc::mbar_wait(&tempty[ts], ((it / C::kSlots) & 1) ^ 1, abort)) { ok = false; break; }
+            if (!tc::mbar_wait(&full[slot], (it / C::kStages) & 1, abort)) { ok = false; break; }
+            tc::fence_after_sync();
+            const uint64_t ad = tc::smem_desc_sw128(tc::smem_u32(sa + slot * kFABytes));
+            const uint64_t bd = tc::smem_desc_sw128(tc::smem_u32(sb + slot * C::kBBytes));
+#pragma unroll
+            for (int j = 0; j < 4; ++j)     // K = 32: 32 bytes along the rows; past K both read as zero
+              tc::mma_f8_ss(tmem + ts * BN, ad + 2 * j, bd + 2 * j, idesc, j > 0 ? 1u : 0u);
+            tc::mma_commit(&empty[slot]);
+            tc::mma_commit(&tfull[ts]);
+          }
+        }
+        tc::mma_commit(drain);
+        volatile int never = 0;
+        tc::mbar_wait(drain, 0, &never, 400000000ll);
       }
-  }
-  if (wg) return;
-  // rows outside every group
-  const int esize = a.out_dtype == MOE_DT_F32 ? 4 : 2;
-  for (int64_t r = blockIdx.x; r < a.R; r += gridDim.x) {
-    if (r >= off[0] && r < off[a.G]) continue;
-    for (int64_t i = threadIdx.x; i < (int64_t)a.N; i += kThr) {
-      if (esize == 4) reinterpret_cast<float*>(a.out)[r * a.ldo + i] = 0.f;
-      else reinterpret_cast<uint16_t*>(a.out)[r * a.ldo + i] = 0;
+      __syncwarp();
+    } else {
+      // ---------------- rows outside every group ----------------
+      const int lo = off[0], hi = off[m.G];
+      for (int64_t r = blockIdx.x; r < m.R - (int64_t)(hi - lo); r += gridDim.x) {
+        const int64_t row = r < lo ? r : r - lo + hi;
+        if (m.S > 1) {
+          for (int s = 0; s < m.S; ++s)
+            for (int64_t i = lane; i < m.N; i += 32) m.part[((int64_t)s * m.R + row) * m.N + i] = 0.f;
+        } else {
+          for (int64_t i = lane; i < m.N; i += 32) {
+            if (m.out_dtype == MOE_DT_F32) reinterpret_cast<float*>(m.out)[row * m.ldo + i] = 0.f;
+            else reinterpret_cast<uint16_t*>(m.out)[row * m.ldo + i] = 0;
+          }
+        }
+      }
+    }
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kFRegsHigh));
+    // ---------------- sums of the blocks ----------------
+    constexpr int kCols = BN / 2, kChunks = kCols / 32;
+    const int h = (warp - 4) >> 2, q = warp & 3;
+    const uint32_t lanes = tmem + ((uint32_t)(q * 32) << 16) + h * kCols;
+    const int KB = (m.K + kFK - 1) / kFK, NB = (m.N + kQBlock - 1) / kQBlock;
+    const int dt = m.S > 1 ? MOE_DT_F32 : m.out_dtype;
+    const int esize = dt == MOE_DT_F32 ? 4 : 2;
+    const int64_t ld = m.S > 1 ? m.N : m.ldo, os = (int64_t)m.R * m.N;
+    uint8_t* obase = reinterpret_cast<uint8_t*>(m.S > 1 ? (void*)m.part : m.out);
+    const bool vec = ((uintptr_t)obase & 15) == 0 && (ld * esize) % 16 == 0 && (m.S == 1 || (os * 4) % 16 == 0);
+    uint32_t it = 0;
+    bool ok = true;
+    for (int64_t u = blockIdx.x; ok && u < U; u += gridDim.x) {
+      GUnit w;
+      g_unit<false, BN, kFK>(m, g.n_tiles, off, uoff, u, w);
+      const int r = q * 32 + lane;
+      const bool live = r < w.rows;
+      const float* xs = m.sa + (int64_t)(w.row0 + (live ? r : 0)) * m.ldsa;
+      const int nb = min((w.n0 + h * kCols) / kQBlock, NB - 1);     // past N: nothing is stored
+      const float* ws = m.sb + ((int64_t)w.e * NB + nb) * KB;
+      uint64_t acc[kCols / 2];
+#pragma unroll
+      for (int i = 0; i < kCols / 2; ++i) acc[i] = 0;
+      // the scales of two blocks ahead are on their way
+      float s0 = 0.f, s1 = 0.f, t0 = 0.f, t1 = 0.f;
+      if (w.k0 < w.k1) { s0 = xs[w.k0]; t0 = ws[w.k0]; }
+      if (w.k0 + 1 < w.k1) { s1 = xs[w.k0 + 1]; t1 = ws[w.k0 + 1]; }
+      for (int kb = w.k0; kb < w.k1; ++kb, ++it) {
+        const int ts = it % C::kSlots;
+        float s2 = 0.f, t2 = 0.f;
+        if (kb + 2 < w.k1) { s2 = xs[kb + 2]; t2 = ws[kb + 2]; }
+        const float sc = s0 * t0;
+        uint64_t sc2;
+        asm("mov.b64 %0, {%1, %1};" : "=l"(sc2) : "f"(sc));
+        ok = __all_sync(kFull, tc::mbar_wait(&tfull[ts], (it / C::kSlots) & 1, abort));
+        if (!ok) break;
+        tc::fence_after_sync();
+        const uint32_t at = lanes + ts * BN;
+        // chunk c + 1 is read while chunk c is added
+        uint32_t v[2][32];
+        tc::tmem_ld32(at, v[0]);
+#pragma unroll
+        for (int c = 0; c < kChunks; ++c) {
+          tc::tmem_wait_ld();
+          if (c + 1 < kChunks) {
+            tc::tmem_ld32(at + 32 * (c + 1), v[(c + 1) & 1]);
+          } else {
+            tc::fence_before_sync();
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive(&tempty[ts]);
+          }
+#pragma unroll
+          for (int i = 0; i < 16; ++i) fma2(acc[c * 16 + i], v[c & 1][2 * i], v[c & 1][2 * i + 1], sc2);
+        }
+        s0 = s1; t0 = t1; s1 = s2; t1 = t2;
+      }
+      if (!ok) break;
+      if (live) {
+        const int64_t row = (int64_t)(w.row0 + r) * ld + w.piece * (m.S > 1 ? os : 0);
+#pragma unroll
+        for (int c = 0; c < kChunks; ++c) {
+          const int col = w.n0 + h * kCols + 32 * c;
+          if (col < m.N) {
+            uint32_t v[32];
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+              asm("mov.b64 {%0, %1}, %2;" : "=r"(v[2 * i]), "=r"(v[2 * i + 1]) : "l"(acc[c * 16 + i]));
+            store32(obase + (row + col) * esize, v, m.N - col, dt, vec);
+          }
+        }
+      }
+      __syncwarp();
     }
   }
+
+  tc::fence_before_sync();
+  __syncthreads();
+  if (threadIdx.x == 0 && *abort) set_status(m.status, MOE_DEV_TIMEOUT);
+  if (warp == 1) {
+    tc::fence_after_sync();
+    tc::tmem_dealloc(tmem, 512);
+  }
+}
+
+// ---- host -------------------------------------------------------------------------
+template <int BN>
+static cudaError_t launch_f(FArgs g, cudaStream_t st) {
+  using C = FCfg<BN>;
+  const MmArgs& m = g.m;
+  FMaps maps;
+  for (int i = 0; i < 4; ++i) {
+    const int64_t dims[2] = {m.K, m.R}, strides[1] = {m.lda};
+    const int box[2] = {kFK, 16 << i};
+    if (!make_tmap(&maps.a[i], m.a, 1, 2, dims, strides, box)) return cudaErrorInvalidValue;
+  }
+  const int64_t dims[3] = {m.K, m.N, m.G}, strides[2] = {m.ldb, m.G > 1 ? m.bg : m.ldb};
+  const int box[3] = {kFK, BN, 1};
+  if (!make_tmap(&maps.b, m.b, 1, 3, dims, strides, box)) return cudaErrorInvalidValue;
+  g.n_tiles = (m.N + BN - 1) / BN;
+  // a kernel launched with fewer registers than its warps then share out
+  // would wait for them forever
+  static std::atomic<int> regs{0};
+  if (regs.load(std::memory_order_acquire) == 0) {
+    cudaFuncAttributes at;
+    const cudaError_t e = cudaFuncGetAttributes(&at, k_gemm_fp8<BN>);
+    if (e != cudaSuccess) return e;
+    regs.store(at.numRegs, std::memory_order_release);
+  }
+  if (128 * kFRegsLow + 256 * kFRegsHigh > kFThreads * regs.load()) return cudaErrorInvalidConfiguration;
+  static std::atomic<bool> done[kMaxDevices] = {};
+  cudaError_t e = set_smem_once((const void*)k_gemm_fp8<BN>, C::kSmem, done);
+  if (e != cudaSuccess) return e;
+  note_launch();
+  e = launch_pdl(k_gemm_fp8<BN>, dim3(device_sms()), dim3(kFThreads), C::kSmem, st, g, maps);
+  if (e != cudaSuccess || m.S == 1) return e;
+  return launch_mm_join(m, false, st);
 }
 
 cudaError_t launch_mm_fp8(const MmArgs& a, cudaStream_t st) {
-  note_launch();
-  return launch_pdl(k_mm_simple<kMmFp8>, dim3(device_sms() * 4), dim3(kThr), 0, st, a);
+  FArgs g = {};
+  g.m = a;
+  const int bn = mm_plan(kMmFp8, a.R, a.N, a.K, a.G).bn;
+  return bn == 256 ? launch_f<256>(g, st) : bn == 128 ? launch_f<128>(g, st) : launch_f<64>(g, st);
 }
 
 }  // namespace moe

@@ -97,4 +97,83 @@ __device__ __forceinline__ int group_of_unit(const int32_t* uoff, int G, int u) 
   return lo;
 }
 
+constexpr int kGM = 128;              // tile rows (MMA M)
+
+struct GUnit {
+  int e, row0, rows;    // first A row of the tile (wgrad: first feature) and its real rows
+  int n0;               // first column
+  int k0, k1;           // reduction blocks of a stage each: [k0, k1) of this piece
+  int red;              // the whole reduction's length
+  int piece;
+};
+
+// Unit u of a product: (row tile of a group, column tile, piece of the
+// reduction), pieces innermost, then column tiles. WG: weight gradient (M =
+// N features, the reduction is the group's rows); BK: the stage's depth.
+template <bool WG, int BN, int BK>
+__device__ __forceinline__ void g_unit(const MmArgs& m, int n_tiles, const int32_t* off, const int32_t* uoff, int64_t u,
+                                       GUnit& w) {
+  const int S = m.S;
+  const int64_t t = u / S;
+  w.piece = (int)(u - t * S);
+  const int ui = (int)(t / n_tiles);
+  w.n0 = (int)(t - (int64_t)ui * n_tiles) * BN;
+  w.e = group_of_unit(uoff, m.G, ui);
+  const int mi = ui - uoff[w.e], cnt = off[w.e + 1] - off[w.e];
+  if (WG) {
+    w.row0 = mi * kGM;
+    w.rows = min(kGM, m.N - w.row0);
+    w.red = cnt;
+  } else {
+    w.row0 = off[w.e] + mi * kGM;
+    w.rows = min(kGM, cnt - mi * kGM);
+    w.red = m.K;
+  }
+  const int nk = (w.red + BK - 1) / BK;
+  w.k0 = (int)((int64_t)nk * w.piece / S);
+  w.k1 = (int)((int64_t)nk * (w.piece + 1) / S);
+}
+
+// A copy of a K-major tile covers 16 << i rows, the fewest that hold its real
+// ones; the MMA's other rows are an earlier stage's bytes and are not stored.
+__device__ __forceinline__ int g_a_box(int rows) { return rows <= 16 ? 0 : rows <= 32 ? 1 : rows <= 64 ? 2 : 3; }
+
+// 32 columns of a row from fp32 bits: n valid ones at p (esize 4: fp32, else
+// bf16 / f16); vec: 16-byte stores are aligned.
+__device__ __forceinline__ void store32(void* p, const uint32_t (&v)[32], int n, int out_dtype, bool vec) {
+  if (out_dtype == MOE_DT_F32) {
+    uint32_t* d = reinterpret_cast<uint32_t*>(p);
+    if (vec && n >= 32) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        reinterpret_cast<uint4*>(d)[i] = make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 32; ++i)
+        if (i < n) d[i] = v[i];
+    }
+    return;
+  }
+  uint32_t pk[16];
+  if (out_dtype == MOE_DT_F16) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+      pk[i] = (uint32_t)F16::from(__uint_as_float(v[2 * i])) | ((uint32_t)F16::from(__uint_as_float(v[2 * i + 1])) << 16);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+      pk[i] = (uint32_t)Bf16::from(__uint_as_float(v[2 * i])) | ((uint32_t)Bf16::from(__uint_as_float(v[2 * i + 1])) << 16);
+  }
+  if (vec && n >= 32) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      reinterpret_cast<uint4*>(p)[i] = make_uint4(pk[4 * i], pk[4 * i + 1], pk[4 * i + 2], pk[4 * i + 3]);
+  } else {
+    uint16_t* d = reinterpret_cast<uint16_t*>(p);
+#pragma unroll
+    for (int i = 0; i < 32; ++i)
+      if (i < n) d[i] = (uint16_t)(pk[i >> 1] >> (16 * (i & 1)));
+  }
+}
+
 }  // namespace moe
