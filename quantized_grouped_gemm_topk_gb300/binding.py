@@ -158,8 +158,8 @@ def _ptr(t):
 
 
 def _stream(stream=None):
-    if stream is None:
-        return torch.cuda.current_stream().cuda_stream
+    if stream is None:      # the raw handle, without a Stream object around it
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else stream
 
 
@@ -168,9 +168,15 @@ def _check(name, code):
         raise MoEError(name, code)
 
 
+_cuda_seen = False
+
+
 def _require_cuda():
-    if not torch.cuda.is_available():
-        raise RuntimeError("no CUDA device: the routed-MoE library runs only on the GPU")
+    global _cuda_seen
+    if not _cuda_seen:
+        if not torch.cuda.is_available():
+            raise RuntimeError("no CUDA device: the routed-MoE library runs only on the GPU")
+        _cuda_seen = True
 
 
 def make_config(H, I, E, k, n_shared=0, T_max=0, act="swiglu", alpha=1.0, limit=0.0, routed_scale=1.0,
@@ -419,37 +425,42 @@ _16BIT = (torch.bfloat16, torch.float16)
 _FLOATS = (torch.bfloat16, torch.float16, torch.float32)
 
 
-def _arg(t, name, dtypes, shape):
-    """Checks a tensor argument: on the current CUDA device, one of dtypes, of this shape, last axis contiguous."""
-    if not t.is_cuda or t.device.index != torch.cuda.current_device():
+def _device() -> int:
+    _require_cuda()
+    return torch.cuda.current_device()
+
+
+def _arg(t, name, dtypes, shape, dev):
+    """Checks a tensor argument: on device dev (the current one), one of dtypes, of this shape, last axis contiguous."""
+    if t.get_device() != dev:
         raise ValueError(f"{name} must be on the current CUDA device, is on {t.device}")
     if t.dtype not in dtypes:
         raise ValueError(f"{name} has type {t.dtype}, wants {' or '.join(map(str, dtypes))}")
-    if tuple(t.shape) != shape:
+    if t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, wants {shape}")
-    if t.shape[-1] > 1 and t.stride(-1) != 1:
+    if shape[-1] > 1 and t.stride(-1) != 1:
         raise ValueError(f"the last axis of {name} must be contiguous")
     return t.data_ptr()
 
 
-def _flat(t, name, dtypes, shape):
+def _flat(t, name, dtypes, shape, dev):
     """As _arg, for an array without strides of its own; None stays None."""
     if t is None:
         return None
-    p = _arg(t, name, dtypes, shape)
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
-    return p
+    return _arg(t, name, dtypes, shape, dev)
 
 
 def _ld(t, name, whole=1):
     """Stride between the rows of t (axis -2), in elements. A single row has none: its length, rounded up to `whole`."""
-    if t.shape[-2] <= 1:
-        n = max(t.shape[-1], t.stride(-2))
-        return -(-n // whole) * whole
-    if t.stride(-2) < t.shape[-1]:
-        raise ValueError(f"the rows of {name} overlap (stride {t.stride(-2)}, length {t.shape[-1]})")
-    return t.stride(-2)
+    rows, cols = t.shape[-2:]
+    ld = t.stride(-2)
+    if rows <= 1:
+        return -(-max(cols, ld) // whole) * whole
+    if ld < cols:
+        raise ValueError(f"the rows of {name} overlap (stride {ld}, length {cols})")
+    return ld
 
 
 def _group(t):
@@ -463,11 +474,11 @@ def _dims(t, name, n):
     return t.shape
 
 
-def _ws(ws, name="ws"):
+def _ws(ws, dev):
     if ws is None:
         return None, 0
-    if not ws.is_cuda or not ws.is_contiguous() or ws.device.index != torch.cuda.current_device():
-        raise ValueError(f"{name} must be a contiguous buffer on the current CUDA device")
+    if ws.get_device() != dev or not ws.is_contiguous():
+        raise ValueError("ws must be a contiguous buffer on the current CUDA device")
     return ws.data_ptr(), ws.numel() * ws.element_size()
 
 
@@ -480,58 +491,58 @@ def moe_layer_norm_workspace_size(T, H) -> int:
 def moe_layer_norm_forward(x, gamma, beta, eps, y, mean=None, rstd=None, stream=None):
     """y = (x - mu) / sqrt(var + eps) * gamma + beta by rows of x [T, H] (bf16, f16, f32); gamma, beta [H] in x's type
     or fp32, or None; mean, rstd [T] fp32 for the backward, or None."""
-    _require_cuda()
+    dev = _device()
     T, H = _dims(x, "x", 2)
     wt = next((w.dtype for w in (gamma, beta) if w is not None), torch.float32)
     wts = (wt,) if wt in (torch.float32, x.dtype) else _F32
     _check("moe_layer_norm_forward", load().moe_layer_norm_forward(
-        _arg(x, "x", _FLOATS, (T, H)), _ld(x, "x"), _flat(gamma, "gamma", wts, (H,)), _flat(beta, "beta", wts, (H,)),
-        eps, T, H, DTYPES[x.dtype], DTYPES[wt], _arg(y, "y", (x.dtype,), (T, H)), _ld(y, "y"),
-        _flat(mean, "mean", _F32, (T,)), _flat(rstd, "rstd", _F32, (T,)), _stream(stream)))
+        _arg(x, "x", _FLOATS, (T, H), dev), _ld(x, "x"), _flat(gamma, "gamma", wts, (H,), dev), _flat(beta, "beta", wts, (H,), dev),
+        eps, T, H, DTYPES[x.dtype], DTYPES[wt], _arg(y, "y", (x.dtype,), (T, H), dev), _ld(y, "y"),
+        _flat(mean, "mean", _F32, (T,), dev), _flat(rstd, "rstd", _F32, (T,), dev), _stream(stream)))
 
 
 def moe_layer_norm_backward(dy, x, gamma, mean, rstd, dx, dgamma=None, dbeta=None, ws=None, stream=None):
     """Gradients of moe_layer_norm_forward: dx [T, H]; dgamma, dbeta [H] (gamma's type, None to skip), whose partial
     sums take the workspace ws (moe_layer_norm_workspace_size bytes)."""
-    _require_cuda()
+    dev = _device()
     T, H = _dims(x, "x", 2)
     wt = next((w.dtype for w in (gamma, dgamma, dbeta) if w is not None), torch.float32)
     wts = (wt,) if wt in (torch.float32, x.dtype) else _F32
     own = (x.dtype,)
-    wp, wn = _ws(ws)
+    wp, wn = _ws(ws, dev)
     _check("moe_layer_norm_backward", load().moe_layer_norm_backward(
-        _arg(dy, "dy", own, (T, H)), _ld(dy, "dy"), _arg(x, "x", _FLOATS, (T, H)), _ld(x, "x"),
-        _flat(gamma, "gamma", wts, (H,)), _flat(mean, "mean", _F32, (T,)), _flat(rstd, "rstd", _F32, (T,)), T, H,
-        DTYPES[x.dtype], DTYPES[wt], _arg(dx, "dx", own, (T, H)), _ld(dx, "dx"), _flat(dgamma, "dgamma", wts, (H,)),
-        _flat(dbeta, "dbeta", wts, (H,)), wp, wn, _stream(stream)))
+        _arg(dy, "dy", own, (T, H), dev), _ld(dy, "dy"), _arg(x, "x", _FLOATS, (T, H), dev), _ld(x, "x"),
+        _flat(gamma, "gamma", wts, (H,), dev), _flat(mean, "mean", _F32, (T,), dev), _flat(rstd, "rstd", _F32, (T,), dev), T, H,
+        DTYPES[x.dtype], DTYPES[wt], _arg(dx, "dx", own, (T, H), dev), _ld(dx, "dx"), _flat(dgamma, "dgamma", wts, (H,), dev),
+        _flat(dbeta, "dbeta", wts, (H,), dev), wp, wn, _stream(stream)))
 
 
 def moe_act_ckpt_forward(h, w_row, y, q, s, act="swiglu", alpha=1.0, limit=0.0, stream=None):
     """y [R, I] = w_row * act(h), and h's 8-bit checkpoint q (E4M3, h's shape), s [R, halves * ceil(I / 128)] fp32;
     h [R, 2 I] (gate, up; sReLU [R, I]) bf16 or f16, w_row [R] fp32 or None."""
-    _require_cuda()
+    dev = _device()
     R, I = _dims(y, "y", 2)
     halves = 1 if act == "srelu" else 2
     nb = halves * -(-I // FP8_BLOCK)
     _check("moe_act_ckpt_forward", load().moe_act_ckpt_forward(
-        _arg(h, "h", _16BIT, (R, halves * I)), _ld(h, "h"), _flat(w_row, "w_row", _F32, (R,)), R, I, DTYPES[h.dtype],
-        ACTS[act], alpha, limit, _arg(y, "y", (h.dtype,), (R, I)), _ld(y, "y"), _arg(q, "q", _U8, (R, halves * I)),
-        _ld(q, "q"), _flat(s, "s", _F32, (R, nb)), _stream(stream)))
+        _arg(h, "h", _16BIT, (R, halves * I), dev), _ld(h, "h"), _flat(w_row, "w_row", _F32, (R,), dev), R, I, DTYPES[h.dtype],
+        ACTS[act], alpha, limit, _arg(y, "y", (h.dtype,), (R, I), dev), _ld(y, "y"), _arg(q, "q", _U8, (R, halves * I), dev),
+        _ld(q, "q"), _flat(s, "s", _F32, (R, nb), dev), _stream(stream)))
 
 
 def moe_act_ckpt_backward(dy, q, s, w_row, dh, dw_row=None, y=None, act="swiglu", alpha=1.0, limit=0.0, stream=None):
     """From the checkpoint of moe_act_ckpt_forward: dh (q's shape, dy's type), dw_row [R] fp32 (the gradient of w_row)
     and the recomputed y [R, I], the last two each None to skip."""
-    _require_cuda()
+    dev = _device()
     R, I = _dims(dy, "dy", 2)
     halves = 1 if act == "srelu" else 2
     nb = halves * -(-I // FP8_BLOCK)
     own = (dy.dtype,)
     _check("moe_act_ckpt_backward", load().moe_act_ckpt_backward(
-        _arg(dy, "dy", _16BIT, (R, I)), _ld(dy, "dy"), _arg(q, "q", _U8, (R, halves * I)), _ld(q, "q"),
-        _flat(s, "s", _F32, (R, nb)), _flat(w_row, "w_row", _F32, (R,)), R, I, DTYPES[dy.dtype], ACTS[act], alpha, limit,
-        _arg(dh, "dh", own, (R, halves * I)), _ld(dh, "dh"), _flat(dw_row, "dw_row", _F32, (R,)),
-        None if y is None else _arg(y, "y", own, (R, I)), 0 if y is None else _ld(y, "y"), _stream(stream)))
+        _arg(dy, "dy", _16BIT, (R, I), dev), _ld(dy, "dy"), _arg(q, "q", _U8, (R, halves * I), dev), _ld(q, "q"),
+        _flat(s, "s", _F32, (R, nb), dev), _flat(w_row, "w_row", _F32, (R,), dev), R, I, DTYPES[dy.dtype], ACTS[act], alpha, limit,
+        _arg(dh, "dh", own, (R, halves * I), dev), _ld(dh, "dh"), _flat(dw_row, "dw_row", _F32, (R,), dev),
+        None if y is None else _arg(y, "y", own, (R, I), dev), 0 if y is None else _ld(y, "y"), _stream(stream)))
 
 
 def moe_mm_workspace_size(kind, R, N, K, G=1) -> int:
@@ -544,68 +555,68 @@ def moe_grouped_mm(x, w, offsets, out, ws, trans_w=False, stream=None):
     """out[r] = w[e] x[r] for the rows r of each group e (offsets [G + 1] int32): x [R, K], w [G, N, K], out [R, N];
     trans_w: w [G, K, N], out[r] = w[e]^T x[r], the gradient of the forward's rows. bf16 or f16; out in x's type or
     fp32. ws: moe_mm_workspace_size(MOE_MM_ROWS, R, N, K, G) bytes, zeroed once."""
-    _require_cuda()
+    dev = _device()
     R, K = _dims(x, "x", 2)
     G = _dims(w, "w", 3)[0]
     N = w.shape[2] if trans_w else w.shape[1]
-    wp, wn = _ws(ws)
+    wp, wn = _ws(ws, dev)
     _check("moe_grouped_mm", load().moe_grouped_mm(
-        _arg(x, "x", _16BIT, (R, K)), _ld(x, "x", 8), _arg(w, "w", (x.dtype,), (G, K, N) if trans_w else (G, N, K)),
-        _group(w), _ld(w, "w", 8), int(trans_w), _flat(offsets, "offsets", _I32, (G + 1,)), R, N, K, G, DTYPES[x.dtype],
-        _arg(out, "out", (x.dtype, torch.float32), (R, N)), _ld(out, "out"), DTYPES[out.dtype], wp, wn,
+        _arg(x, "x", _16BIT, (R, K), dev), _ld(x, "x", 8), _arg(w, "w", (x.dtype,), (G, K, N) if trans_w else (G, N, K), dev),
+        _group(w), _ld(w, "w", 8), int(trans_w), _flat(offsets, "offsets", _I32, (G + 1,), dev), R, N, K, G, DTYPES[x.dtype],
+        _arg(out, "out", (x.dtype, torch.float32), (R, N), dev), _ld(out, "out"), DTYPES[out.dtype], wp, wn,
         _stream(stream)))
 
 
 def moe_grouped_mm_wgrad(dy, x, offsets, dw, ws, stream=None):
     """dw[e] [N, K] = sum over group e's rows of dy[r]^T x[r]; dy [R, N], x [R, K] bf16 or f16, dw [G, N, K] in their
     type or fp32. ws: moe_mm_workspace_size(MOE_MM_WGRAD, R, N, K, G) bytes, zeroed once."""
-    _require_cuda()
+    dev = _device()
     G, N, K = _dims(dw, "dw", 3)
     R = _dims(x, "x", 2)[0]
-    wp, wn = _ws(ws)
+    wp, wn = _ws(ws, dev)
     _check("moe_grouped_mm_wgrad", load().moe_grouped_mm_wgrad(
-        _arg(dy, "dy", (x.dtype,), (R, N)), _ld(dy, "dy", 8), _arg(x, "x", _16BIT, (R, K)), _ld(x, "x", 8),
-        _flat(offsets, "offsets", _I32, (G + 1,)), R, N, K, G, DTYPES[x.dtype],
-        _arg(dw, "dw", (x.dtype, torch.float32), (G, N, K)), _group(dw), _ld(dw, "dw"), DTYPES[dw.dtype], wp, wn,
+        _arg(dy, "dy", (x.dtype,), (R, N), dev), _ld(dy, "dy", 8), _arg(x, "x", _16BIT, (R, K), dev), _ld(x, "x", 8),
+        _flat(offsets, "offsets", _I32, (G + 1,), dev), R, N, K, G, DTYPES[x.dtype],
+        _arg(dw, "dw", (x.dtype, torch.float32), (G, N, K), dev), _group(dw), _ld(dw, "dw"), DTYPES[dw.dtype], wp, wn,
         _stream(stream)))
 
 
 def moe_fp8_quant_rows(x, q, s, stream=None):
     """E4M3 codes q [R, C] and fp32 scales s [R, ceil(C / 128)] of x [R, C], one scale for 128 columns of a row."""
-    _require_cuda()
+    dev = _device()
     R, C = _dims(x, "x", 2)
     _check("moe_fp8_quant_rows", load().moe_fp8_quant_rows(
-        _arg(x, "x", _FLOATS, (R, C)), _ld(x, "x"), R, C, DTYPES[x.dtype], _arg(q, "q", _U8, (R, C)), _ld(q, "q"),
-        _arg(s, "s", _F32, (R, -(-C // FP8_BLOCK))), _ld(s, "s"), _stream(stream)))
+        _arg(x, "x", _FLOATS, (R, C), dev), _ld(x, "x"), R, C, DTYPES[x.dtype], _arg(q, "q", _U8, (R, C), dev), _ld(q, "q"),
+        _arg(s, "s", _F32, (R, -(-C // FP8_BLOCK)), dev), _ld(s, "s"), _stream(stream)))
 
 
 def moe_fp8_quant_weights(w, q, s, qt=None, st=None, stream=None):
     """E4M3 codes q [G, N, K] and fp32 scales s [G, ceil(N / 128), ceil(K / 128)] of w [G, N, K], one scale for
     128 x 128; qt [G, K, N], st [G, ceil(K / 128), ceil(N / 128)]: the same, transposed."""
-    _require_cuda()
+    dev = _device()
     G, N, K = _dims(w, "w", 3)
     nb, kb = -(-N // FP8_BLOCK), -(-K // FP8_BLOCK)
     t = qt is not None
     _check("moe_fp8_quant_weights", load().moe_fp8_quant_weights(
-        _arg(w, "w", _FLOATS, (G, N, K)), _group(w), _ld(w, "w"), G, N, K, DTYPES[w.dtype],
-        _arg(q, "q", _U8, (G, N, K)), _group(q), _ld(q, "q"), _flat(s, "s", _F32, (G, nb, kb)),
-        _arg(qt, "qt", _U8, (G, K, N)) if t else None, _group(qt) if t else 0, _ld(qt, "qt") if t else 0,
-        _flat(st, "st", _F32, (G, kb, nb)), _stream(stream)))
+        _arg(w, "w", _FLOATS, (G, N, K), dev), _group(w), _ld(w, "w"), G, N, K, DTYPES[w.dtype],
+        _arg(q, "q", _U8, (G, N, K), dev), _group(q), _ld(q, "q"), _flat(s, "s", _F32, (G, nb, kb), dev),
+        _arg(qt, "qt", _U8, (G, K, N), dev) if t else None, _group(qt) if t else 0, _ld(qt, "qt") if t else 0,
+        _flat(st, "st", _F32, (G, kb, nb), dev), _stream(stream)))
 
 
 def moe_fp8_mm(xq, xs, wq, wscale, out, ws, offsets=None, stream=None):
     """out [R, N] (bf16, f16 or fp32) = the product of E4M3 rows xq [R, K] with scales xs [R, ceil(K / 128)] and E4M3
     weights wq [G, N, K] with scales wscale [G, ceil(N / 128), ceil(K / 128)]; offsets as in moe_grouped_mm, or None
     with one group. ws: moe_mm_workspace_size(MOE_MM_FP8, R, N, K, G) bytes, zeroed once."""
-    _require_cuda()
+    dev = _device()
     R, K = _dims(xq, "xq", 2)
     G, N = _dims(wq, "wq", 3)[:2]
     nb, kb = -(-N // FP8_BLOCK), -(-K // FP8_BLOCK)
-    wp, wn = _ws(ws)
+    wp, wn = _ws(ws, dev)
     _check("moe_fp8_mm", load().moe_fp8_mm(
-        _arg(xq, "xq", _U8, (R, K)), _ld(xq, "xq", 16), _arg(xs, "xs", _F32, (R, kb)), _ld(xs, "xs"),
-        _arg(wq, "wq", _U8, (G, N, K)), _group(wq), _ld(wq, "wq", 16), _flat(wscale, "wscale", _F32, (G, nb, kb)),
-        _flat(offsets, "offsets", _I32, (G + 1,)), R, N, K, G, _arg(out, "out", _FLOATS, (R, N)), _ld(out, "out"),
+        _arg(xq, "xq", _U8, (R, K), dev), _ld(xq, "xq", 16), _arg(xs, "xs", _F32, (R, kb), dev), _ld(xs, "xs"),
+        _arg(wq, "wq", _U8, (G, N, K), dev), _group(wq), _ld(wq, "wq", 16), _flat(wscale, "wscale", _F32, (G, nb, kb), dev),
+        _flat(offsets, "offsets", _I32, (G + 1,), dev), R, N, K, G, _arg(out, "out", _FLOATS, (R, N), dev), _ld(out, "out"),
         DTYPES[out.dtype], wp, wn, _stream(stream)))
 
 

@@ -10,11 +10,13 @@ namespace moe {
 // Elements of a runtime-chosen type, held as template tags.
 struct Bf16 {
   using raw = uint16_t;
+  static constexpr uint32_t kInf = 0x7f80u;
   static __device__ __forceinline__ float to(raw v) { return bf16_bits_to_f32(v); }
   static __device__ __forceinline__ raw from(float f) { return f32_to_bf16_bits(f); }
 };
 struct F16 {
   using raw = uint16_t;
+  static constexpr uint32_t kInf = 0x7c00u;
   static __device__ __forceinline__ float to(raw v) { return __half2float(__ushort_as_half(v)); }
   static __device__ __forceinline__ raw from(float f) { return __half_as_ushort(__float2half_rn(f)); }
 };

@@ -134,8 +134,8 @@ def test_tensors_that_do_not_fit_are_refused(lib, monkeypatch):
         def __getattr__(self, k):
             return getattr(self.t, k)
 
-        is_cuda = True
-        device = torch.device("cuda", 0)
+        def get_device(self):
+            return 0
 
     monkeypatch.setattr(m, "_require_cuda", lambda: None)
     monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
