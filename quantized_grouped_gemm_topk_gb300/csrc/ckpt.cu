@@ -9,17 +9,16 @@
 //   gradient, so neither h nor y is kept in 16 bits between the passes.
 //
 // Bound: HBM (per gated element 8 bytes forward, 10 backward). One pass, no
-// shared memory: a half-warp owns a 128-column block, eight columns a lane
-// (one 16-byte access for each half), so the block's largest magnitude takes
-// four shuffles. The backward adds a row's dw over its half-warps in a fixed
-// order. NaN passes through every activation; an infinity or NaN becomes a
+// staging: a quarter-warp owns a 128-column block, sixteen columns a lane, so
+// the block's largest magnitude takes three shuffles. The backward adds a
+// row's dw over its quarter-warps in a fixed order. NaN passes through every activation; an infinity or NaN becomes a
 // NaN code and leaves the block's scale to the others.
 #include "ops.cuh"
 
 namespace moe {
 
 constexpr int kCkptThreads = 256;
-constexpr int kCkptHalfWarps = kCkptThreads / 16;
+constexpr int kCkptQuarters = kCkptThreads / 8;
 
 // 1 / (1 + 2^(-v log2 e)): the exponential and the reciprocal on the
 // special-function unit (relative error about 2^-22 each, far below the 16
@@ -85,212 +84,216 @@ __device__ __forceinline__ float3 ckpt_act_grad(float g, float u, const ActParam
   }
 }
 
-// A lane's eight columns of a 128-column block as four words of two 16-bit
-// elements: columns 8 l .. 8 l + 7 (VEC: one 16-byte access, I a multiple of
-// 8), or l + 16 j. Columns past the block's n are zeros and not written.
+// A block's 128 columns belong to eight lanes, sixteen to a lane: columns
+// 8 l .. 8 l + 7 and 64 + 8 l .. (VEC: two 16-byte accesses, I a multiple of
+// 8), or l + 8 j. Sixteen, so that a block's fixed work (the scales' divisions,
+// shuffles, addresses) is spread over more elements. Held as words of two
+// 16-bit elements. Columns past the block's n are zeros and not written.
 template <bool VEC>
-__device__ __forceinline__ void load8(uint32_t (&w)[4], const uint16_t* p, int l, int n) {
+__device__ __forceinline__ void load16(uint32_t (&w)[8], const uint16_t* p, int l, int n) {
   if constexpr (VEC) {
-    uint4 v = make_uint4(0u, 0u, 0u, 0u);
-    if (l * 8 < n) v = *reinterpret_cast<const uint4*>(p + l * 8);
-    w[0] = v.x; w[1] = v.y; w[2] = v.z; w[3] = v.w;
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const int c = 64 * k + 8 * l;
+      uint4 v = make_uint4(0u, 0u, 0u, 0u);
+      if (c < n) v = *reinterpret_cast<const uint4*>(p + c);
+      w[4 * k] = v.x; w[4 * k + 1] = v.y; w[4 * k + 2] = v.z; w[4 * k + 3] = v.w;
+    }
   } else {
-    uint16_t e[8];
+    uint16_t e[16];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) e[j] = l + 16 * j < n ? p[l + 16 * j] : (uint16_t)0;
+    for (int j = 0; j < 16; ++j) e[j] = l + 8 * j < n ? p[l + 8 * j] : (uint16_t)0;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) w[j] = (uint32_t)e[2 * j] | ((uint32_t)e[2 * j + 1] << 16);
+    for (int j = 0; j < 8; ++j) w[j] = (uint32_t)e[2 * j] | ((uint32_t)e[2 * j + 1] << 16);
   }
 }
 template <typename E>
-__device__ __forceinline__ void unpack8(float (&v)[8], const uint32_t (&w)[4]) {
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    v[2 * j] = E::to((uint16_t)(w[j] & 0xffffu));
-    v[2 * j + 1] = E::to((uint16_t)(w[j] >> 16));
-  }
+__device__ __forceinline__ float2 pair_of(uint32_t w) {
+  return make_float2(E::to((uint16_t)(w & 0xffffu)), E::to((uint16_t)(w >> 16)));
 }
-template <typename E, bool VEC>
-__device__ __forceinline__ void store8(uint16_t* p, const float (&v)[8], int l, int n) {
+template <bool VEC>
+__device__ __forceinline__ void store16(uint16_t* p, const uint32_t (&w)[8], int l, int n) {
   if constexpr (VEC) {
-    Pack<E, 8> k;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) k.v[j] = E::from(v[j]);
-    if (l * 8 < n) store_pack<E, 8>(p + l * 8, k);
+    for (int k = 0; k < 2; ++k) {
+      const int c = 64 * k + 8 * l;
+      if (c < n) *reinterpret_cast<uint4*>(p + c) = make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
+    }
   } else {
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
-      if (l + 16 * j < n) p[l + 16 * j] = E::from(v[j]);
+    for (int j = 0; j < 16; ++j)
+      if (l + 8 * j < n) p[l + 8 * j] = (uint16_t)(w[j >> 1] >> (16 * (j & 1)));
+  }
+}
+// Sixteen codes as four words.
+template <bool VEC>
+__device__ __forceinline__ void load_codes(uint32_t (&w)[4], const uint8_t* q, int l, int n) {
+  if constexpr (VEC) {
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const int c = 64 * k + 8 * l;
+      uint2 v = make_uint2(0u, 0u);
+      if (c < n) v = *reinterpret_cast<const uint2*>(q + c);
+      w[2 * k] = v.x; w[2 * k + 1] = v.y;
+    }
+  } else {
+    uint8_t e[16];
+#pragma unroll
+    for (int j = 0; j < 16; ++j) e[j] = l + 8 * j < n ? q[l + 8 * j] : (uint8_t)0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      w[j] = (uint32_t)e[4 * j] | ((uint32_t)e[4 * j + 1] << 8) | ((uint32_t)e[4 * j + 2] << 16) |
+             ((uint32_t)e[4 * j + 3] << 24);
   }
 }
 template <bool VEC>
-__device__ __forceinline__ void store_codes(uint8_t* q, const uint16_t (&c)[4], int l, int n) {
+__device__ __forceinline__ void store_codes(uint8_t* q, const uint32_t (&w)[4], int l, int n) {
   if constexpr (VEC) {
-    if (l * 8 < n)
-      *reinterpret_cast<uint2*>(q + l * 8) = make_uint2((uint32_t)c[0] | ((uint32_t)c[1] << 16),
-                                                        (uint32_t)c[2] | ((uint32_t)c[3] << 16));
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const int c = 64 * k + 8 * l;
+      if (c < n) *reinterpret_cast<uint2*>(q + c) = make_uint2(w[2 * k], w[2 * k + 1]);
+    }
   } else {
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
-      if (l + 16 * j < n) q[l + 16 * j] = (uint8_t)(c[j >> 1] >> (8 * (j & 1)));
+    for (int j = 0; j < 16; ++j)
+      if (l + 8 * j < n) q[l + 8 * j] = (uint8_t)(w[j >> 2] >> (8 * (j & 3)));
   }
 }
 
 // Magnitude bits (16-bit elements without their sign order as integers:
-// finite < infinity < NaN) of the largest of the lane's eight.
-__device__ __forceinline__ uint32_t mag_bits(const uint32_t (&w)[4]) {
+// finite < infinity < NaN) of the largest of the lane's sixteen.
+__device__ __forceinline__ uint32_t mag_bits(const uint32_t (&w)[8]) {
   constexpr uint32_t k = 0x7fff7fffu;
-  const uint32_t m = __vmaxu2(__vmaxu2(w[0] & k, w[1] & k), __vmaxu2(w[2] & k, w[3] & k));
+  uint32_t m = w[0] & k;
+#pragma unroll
+  for (int j = 1; j < 8; ++j) m = __vmaxu2(m, w[j] & k);
   return max(m & 0xffffu, m >> 16);
 }
-
-// E4M3 codes of v at 1 / inv; FIN: without the test for infinities.
-template <bool FIN>
-__device__ __forceinline__ void codes8(uint16_t (&c)[4], const float (&v)[8], float inv) {
+// Codes of sixteen values at 1 / inv; FIN: without the test for infinities.
+template <typename E, bool FIN>
+__device__ __forceinline__ void codes16(uint32_t (&c)[4], const uint32_t (&w)[8], float inv) {
 #pragma unroll
-  for (int j = 0; j < 4; ++j)
-    c[j] = FIN ? f32x2_to_e4m3x2(v[2 * j] * inv, v[2 * j + 1] * inv)
-               : f32x2_to_e4m3x2(code_arg(v[2 * j], inv), code_arg(v[2 * j + 1], inv));
+  for (int j = 0; j < 4; ++j) {
+    const float2 a = pair_of<E>(w[2 * j]), b = pair_of<E>(w[2 * j + 1]);
+    const uint32_t lo = FIN ? f32x2_to_e4m3x2(a.x * inv, a.y * inv)
+                            : f32x2_to_e4m3x2(code_arg(a.x, inv), code_arg(a.y, inv));
+    const uint32_t hi = FIN ? f32x2_to_e4m3x2(b.x * inv, b.y * inv)
+                            : f32x2_to_e4m3x2(code_arg(b.x, inv), code_arg(b.y, inv));
+    c[j] = lo | (hi << 16);
+  }
 }
-
 // The block's scale where some element is an infinity or NaN: the largest of
-// the finite ones, over the half-warp.
-__device__ __forceinline__ float finite_scale(const float (&v)[8], unsigned half) {
+// the finite ones, over the eight lanes.
+template <typename E>
+__device__ __forceinline__ float finite_scale(const uint32_t (&w)[8], unsigned lanes) {
   float am = 0.f;
 #pragma unroll
-  for (int j = 0; j < 8; ++j) am = fmaxf(am, finite_mag(v[j]));
+  for (int j = 0; j < 8; ++j) {
+    const float2 a = pair_of<E>(w[j]);
+    am = fmaxf(am, fmaxf(finite_mag(a.x), finite_mag(a.y)));
+  }
 #pragma unroll
-  for (int o = 8; o > 0; o >>= 1) am = fmaxf(am, __shfl_xor_sync(half, am, o));
+  for (int o = 4; o > 0; o >>= 1) am = fmaxf(am, __shfl_xor_sync(lanes, am, o));
   return block_scale(am);
 }
 
+// Half a row's block forward: y's words, codes and scales.
+template <typename E, int ACT, bool FIN>
+__device__ __forceinline__ void fwd16(uint32_t (&y)[8], uint32_t (&cg)[4], uint32_t (&cu)[4], const uint32_t (&gw)[8],
+                                      const uint32_t (&uw)[8], float sg, float su, float w, const ActParams& p) {
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const float2 g = pair_of<E>(gw[j]), u = pair_of<E>(uw[j]);
+    y[j] = E::from2(w * ckpt_act<ACT, FIN>(g.x, u.x, p), w * ckpt_act<ACT, FIN>(g.y, u.y, p));
+  }
+  codes16<E, FIN>(cg, gw, 1.0f / sg);
+  if constexpr (ACT != MOE_ACT_SRELU) codes16<E, FIN>(cu, uw, 1.0f / su);
+}
+
+// qpr quarter-warps of a CTA (a power of two) share a row; the others take
+// other rows.
 template <typename E, bool VEC, int ACT>
-__global__ void __launch_bounds__(kCkptThreads) k_ckpt_fwd(CkptArgs a) {
+__global__ void __launch_bounds__(kCkptThreads) k_ckpt_fwd(CkptArgs a, int qpr) {
   constexpr bool GATED = ACT != MOE_ACT_SRELU;
   pdl_enter();
-  const int l = threadIdx.x & 15, hw = threadIdx.x >> 4;
-  const unsigned half = 0xffffu << (threadIdx.x & 16);
+  const int l = threadIdx.x & 7, qw = threadIdx.x >> 3;
+  const unsigned lanes = 0xffu << (threadIdx.x & 24);
   const int nb = (a.I + kQBlock - 1) / kQBlock;
-  const int64_t items = a.R * nb;
-  // both half-warps of a warp go round together (the shuffles need them); the
-  // item's row and block are carried along instead of divided out
-  const int64_t step = (int64_t)gridDim.x * kCkptHalfWarps;
-  const int64_t step_row = step / nb;
-  const int step_b = (int)(step - step_row * nb);
-  const int64_t it1 = (int64_t)blockIdx.x * kCkptHalfWarps + hw;
-  int64_t row_at = it1 / nb;
-  int b_at = (int)(it1 - row_at * nb);
-  for (int64_t it0 = it1 - (hw & 1); it0 < items; it0 += step) {
-    const bool live = it0 + (hw & 1) < items;
-    const int64_t row = live ? row_at : 0;
-    const int b = live ? b_at : 0, c0 = b * kQBlock, n = live ? min(kQBlock, a.I - c0) : 0;
-    row_at += step_row;
-    b_at += step_b;
-    if (b_at >= nb) {
-      b_at -= nb;
-      ++row_at;
-    }
-    const uint16_t* h = reinterpret_cast<const uint16_t*>(a.h) + row * a.ldh + c0;
-    uint8_t* q = a.q + row * a.ldq + c0;
-    float* s = a.s + row * nb * (GATED ? 2 : 1) + b;
-    uint32_t gw[4], uw[4] = {0u, 0u, 0u, 0u};
-    load8<VEC>(gw, h, l, n);
-    if constexpr (GATED) load8<VEC>(uw, h + a.I, l, n);
-    const float w = a.w && live ? a.w[row] : 1.f;
-    // both halves' largest magnitudes in one word: four shuffles
-    uint32_t mm = mag_bits(gw) | (GATED ? mag_bits(uw) << 16 : 0u);
+  const int rpc = kCkptQuarters / qpr, rl = qw / qpr, part = qw % qpr;
+  for (int64_t row = (int64_t)blockIdx.x * rpc + rl; row < a.R; row += (int64_t)gridDim.x * rpc) {
+    const uint16_t* h = reinterpret_cast<const uint16_t*>(a.h) + row * a.ldh;
+    uint16_t* y = reinterpret_cast<uint16_t*>(a.y) + row * a.ldy;
+    uint8_t* q = a.q + row * a.ldq;
+    float* s = a.s + row * nb * (GATED ? 2 : 1);
+    const float w = a.w ? a.w[row] : 1.f;
+    for (int b = part; b < nb; b += qpr) {
+      const int c0 = b * kQBlock, n = min(kQBlock, a.I - c0);
+      uint32_t gw[8], uw[8] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u};
+      load16<VEC>(gw, h + c0, l, n);
+      if constexpr (GATED) load16<VEC>(uw, h + a.I + c0, l, n);
+      // both halves' largest magnitudes in one word: three shuffles
+      uint32_t mm = mag_bits(gw) | (GATED ? mag_bits(uw) << 16 : 0u);
 #pragma unroll
-    for (int o = 8; o > 0; o >>= 1) mm = __vmaxu2(mm, __shfl_xor_sync(kFull, mm, o));
-    float g[8], u[8], y[8];
-    unpack8<E>(g, gw);
-    unpack8<E>(u, uw);
-    uint16_t cg[4], cu[4];
-    float sg, su;
-    if ((mm & 0xffffu) < E::kInf && (mm >> 16) < E::kInf) {
-      sg = block_scale(E::to((uint16_t)(mm & 0xffffu)));
-      su = block_scale(E::to((uint16_t)(mm >> 16)));
-#pragma unroll
-      for (int j = 0; j < 8; ++j) y[j] = w * ckpt_act<ACT, true>(g[j], u[j], a.act);
-      codes8<true>(cg, g, 1.0f / sg);
-      if constexpr (GATED) codes8<true>(cu, u, 1.0f / su);
-    } else {
-      sg = finite_scale(g, half);
-      su = GATED ? finite_scale(u, half) : 0.f;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) y[j] = w * ckpt_act<ACT, false>(g[j], u[j], a.act);
-      codes8<false>(cg, g, 1.0f / sg);
-      if constexpr (GATED) codes8<false>(cu, u, 1.0f / su);
+      for (int o = 4; o > 0; o >>= 1) mm = __vmaxu2(mm, __shfl_xor_sync(lanes, mm, o));
+      uint32_t yw[8], cg[4], cu[4];
+      float sg, su;
+      if ((mm & 0xffffu) < E::kInf && (mm >> 16) < E::kInf) {
+        sg = block_scale(E::to((uint16_t)(mm & 0xffffu)));
+        su = block_scale(E::to((uint16_t)(mm >> 16)));
+        fwd16<E, ACT, true>(yw, cg, cu, gw, uw, sg, su, w, a.act);
+      } else {
+        sg = finite_scale<E>(gw, lanes);
+        su = GATED ? finite_scale<E>(uw, lanes) : 1.f;
+        fwd16<E, ACT, false>(yw, cg, cu, gw, uw, sg, su, w, a.act);
+      }
+      store_codes<VEC>(q + c0, cg, l, n);
+      if constexpr (GATED) store_codes<VEC>(q + a.I + c0, cu, l, n);
+      if (l == 0) {
+        s[b] = sg;
+        if constexpr (GATED) s[nb + b] = su;
+      }
+      store16<VEC>(y + c0, yw, l, n);
     }
-    __syncwarp();
-    store_codes<VEC>(q, cg, l, n);
-    if constexpr (GATED) store_codes<VEC>(q + a.I, cu, l, n);
-    if (live && l == 0) {
-      s[0] = sg;
-      if constexpr (GATED) s[nb] = su;
-    }
-    store8<E, VEC>(reinterpret_cast<uint16_t*>(a.y) + row * a.ldy + c0, y, l, n);
   }
 }
 
-// The lane's eight codes of a block, as two words; whether one is NaN.
-template <bool VEC>
-__device__ __forceinline__ uint2 load_codes(const uint8_t* q, int l, int n) {
-  uint2 w = make_uint2(0u, 0u);
-  if constexpr (VEC) {
-    if (l * 8 < n) w = *reinterpret_cast<const uint2*>(q + l * 8);
-  } else {
-    uint8_t e[8];
-#pragma unroll
-    for (int j = 0; j < 8; ++j) e[j] = l + 16 * j < n ? q[l + 16 * j] : (uint8_t)0;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      w.x |= (uint32_t)e[j] << (8 * j);
-      w.y |= (uint32_t)e[4 + j] << (8 * j);
-    }
-  }
-  return w;
-}
-__device__ __forceinline__ bool nan_code(uint2 w) {      // a byte whose low seven bits are all set
-  constexpr uint32_t k = 0x7f7f7f7fu;
-  return ((((w.x & k) + 0x01010101u) | ((w.y & k) + 0x01010101u)) & 0x80808080u) != 0u;
-}
-__device__ __forceinline__ void dequant8(float (&v)[8], uint2 w, float s) {
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const float2 f = e4m3x2_to_f32x2((uint16_t)((j < 2 ? w.x : w.y) >> (16 * (j & 1))));
-    v[2 * j] = f.x * s;
-    v[2 * j + 1] = f.y * s;
-  }
+__device__ __forceinline__ bool nan_code(uint32_t w) {      // a byte whose low seven bits are all set
+  return (((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u) != 0u;
 }
 
-// g, u -> dh's halves in place, y; returns the lane's part of dw. Columns past
-// the row's end are zeros and add nothing.
-template <int ACT, bool FIN>
-__device__ __forceinline__ float grad8(float (&g)[8], float (&u)[8], float (&y)[8], const float (&d)[8], float w,
+// Sixteen columns backward: the words of dh's halves and of y; returns the
+// lane's part of dw. Columns past the row's end are zeros and add nothing.
+template <typename E, int ACT, bool FIN>
+__device__ __forceinline__ float bwd16(uint32_t (&dg)[8], uint32_t (&du)[8], uint32_t (&y)[8], const uint32_t (&qg)[4],
+                                       const uint32_t (&qu)[4], const uint32_t (&dw_)[8], float sg, float su, float w,
                                        const ActParams& p) {
   float dw = 0.f;
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
-    const float3 f = ckpt_act_grad<ACT, FIN>(g[j], u[j], p);
-    const float wd = w * d[j];
-    dw = fmaf(d[j], f.x, dw);
-    y[j] = w * f.x;
-    g[j] = wd * f.y;
-    u[j] = wd * f.z;
+    const float2 g = e4m3x2_to_f32x2((uint16_t)(qg[j >> 1] >> (16 * (j & 1))));
+    const float2 u = e4m3x2_to_f32x2((uint16_t)(qu[j >> 1] >> (16 * (j & 1))));
+    const float2 d = pair_of<E>(dw_[j]);
+    const float3 fx = ckpt_act_grad<ACT, FIN>(g.x * sg, u.x * su, p);
+    const float3 fy = ckpt_act_grad<ACT, FIN>(g.y * sg, u.y * su, p);
+    dw = fmaf(d.x, fx.x, dw);
+    dw = fmaf(d.y, fy.x, dw);
+    const float wx = w * d.x, wy = w * d.y;
+    y[j] = E::from2(w * fx.x, w * fy.x);
+    dg[j] = E::from2(wx * fx.y, wy * fy.y);
+    if constexpr (ACT != MOE_ACT_SRELU) du[j] = E::from2(wx * fx.z, wy * fy.z);
   }
   return dw;
 }
 
-// hpr half-warps of a CTA (a power of two) share a row; the others take other
-// rows.
 template <typename E, bool VEC, int ACT>
-__global__ void __launch_bounds__(kCkptThreads) k_ckpt_bwd(CkptArgs a, int hpr) {
+__global__ void __launch_bounds__(kCkptThreads) k_ckpt_bwd(CkptArgs a, int qpr) {
   constexpr bool GATED = ACT != MOE_ACT_SRELU;
   pdl_enter();
-  __shared__ float sdw[2][kCkptHalfWarps];
-  const int l = threadIdx.x & 15, hw = threadIdx.x >> 4;
+  __shared__ float sdw[2][kCkptQuarters];
+  const int l = threadIdx.x & 7, qw = threadIdx.x >> 3;
   const int nb = (a.I + kQBlock - 1) / kQBlock;
-  const int rpc = kCkptHalfWarps / hpr, rl = hw / hpr, part = hw % hpr;
+  const int rpc = kCkptQuarters / qpr, rl = qw / qpr, part = qw % qpr;
   int flip = 0;
   for (int64_t r0 = (int64_t)blockIdx.x * rpc; r0 < a.R; r0 += (int64_t)gridDim.x * rpc, flip ^= 1) {
     const int64_t row = r0 + rl;
@@ -302,35 +305,35 @@ __global__ void __launch_bounds__(kCkptThreads) k_ckpt_bwd(CkptArgs a, int hpr) 
       const float* s = a.s + row * nb * (GATED ? 2 : 1);
       const uint16_t* dy = reinterpret_cast<const uint16_t*>(a.dy) + row * a.lddy;
       uint16_t* dh = reinterpret_cast<uint16_t*>(a.dh) + row * a.lddh;
-      for (int b = part; b < nb; b += hpr) {
+      uint16_t* y = reinterpret_cast<uint16_t*>(a.y) + row * a.ldy;
+      for (int b = part; b < nb; b += qpr) {
         const int c0 = b * kQBlock, n = min(kQBlock, a.I - c0);
-        const uint2 qg = load_codes<VEC>(q + c0, l, n);
-        uint2 qu = make_uint2(0u, 0u);
-        if constexpr (GATED) qu = load_codes<VEC>(q + a.I + c0, l, n);
-        uint32_t dword[4];
-        load8<VEC>(dword, dy + c0, l, n);
+        uint32_t qg[4], qu[4] = {0u, 0u, 0u, 0u}, d[8], dg[8], du[8], yw[8];
+        load_codes<VEC>(qg, q + c0, l, n);
+        if constexpr (GATED) load_codes<VEC>(qu, q + a.I + c0, l, n);
+        load16<VEC>(d, dy + c0, l, n);
         const float sg = s[b], su = GATED ? s[nb + b] : 0.f;
-        float g[8], u[8], d[8], y[8];
-        dequant8(g, qg, sg);
-        dequant8(u, qu, su);
-        unpack8<E>(d, dword);
+        bool nan = false;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) nan |= nan_code(qg[j]) | nan_code(qu[j]);
         // 448 s overflows for the largest scales; a caller's scale may be anything
-        const bool fin = !nan_code(qg) && !nan_code(qu) && fabsf(sg) < 1e35f && fabsf(su) < 1e35f;
-        dw += fin ? grad8<ACT, true>(g, u, y, d, w, a.act) : grad8<ACT, false>(g, u, y, d, w, a.act);
-        store8<E, VEC>(dh + c0, g, l, n);
-        if constexpr (GATED) store8<E, VEC>(dh + a.I + c0, u, l, n);
-        if (a.y) store8<E, VEC>(reinterpret_cast<uint16_t*>(a.y) + row * a.ldy + c0, y, l, n);
+        const bool fin = !nan && fabsf(sg) < 1e35f && fabsf(su) < 1e35f;
+        dw += fin ? bwd16<E, ACT, true>(dg, du, yw, qg, qu, d, sg, su, w, a.act)
+                  : bwd16<E, ACT, false>(dg, du, yw, qg, qu, d, sg, su, w, a.act);
+        store16<VEC>(dh + c0, dg, l, n);
+        if constexpr (GATED) store16<VEC>(dh + a.I + c0, du, l, n);
+        if (a.y) store16<VEC>(y + c0, yw, l, n);
       }
     }
     if (a.dw) {
       __syncwarp();
 #pragma unroll
-      for (int o = 8; o > 0; o >>= 1) dw += __shfl_xor_sync(kFull, dw, o);
-      if (l == 0) sdw[flip][hw] = dw;
+      for (int o = 4; o > 0; o >>= 1) dw += __shfl_xor_sync(kFull, dw, o);
+      if (l == 0) sdw[flip][qw] = dw;
       __syncthreads();
       if (live && part == 0 && l == 0) {
         float t = 0.f;
-        for (int i = 0; i < hpr; ++i) t += sdw[flip][hw + i];
+        for (int i = 0; i < qpr; ++i) t += sdw[flip][qw + i];
         a.dw[row] = t;
       }
     }
@@ -340,31 +343,35 @@ __global__ void __launch_bounds__(kCkptThreads) k_ckpt_bwd(CkptArgs a, int hpr) 
 // ---- host ----------------------------------------------------------------------
 static bool al(const void* p, unsigned n) { return ((uintptr_t)p & (n - 1)) == 0; }
 
+// Quarter-warps a row: the most that leave at most a tenth of them idle in the
+// row's last round.
+static int quarters_a_row(int I) {
+  const int nb = (I + kQBlock - 1) / kQBlock;
+  int q = kCkptQuarters;
+  while (q > 1 && 10 * ((nb + q - 1) / q * q) > 11 * nb) q /= 2;
+  return q;
+}
+
 template <typename E, int ACT>
 static cudaError_t fwd_t(const CkptArgs& a, cudaStream_t st) {
   const bool vec = a.I % 8 == 0 && a.ldh % 8 == 0 && a.ldy % 8 == 0 && a.ldq % 8 == 0 && al(a.h, 16) && al(a.y, 16) &&
                    al(a.q, 8);
-  const int64_t items = a.R * ((a.I + kQBlock - 1) / kQBlock);
-  const int64_t g = std::min<int64_t>((items + kCkptHalfWarps - 1) / kCkptHalfWarps, (int64_t)device_sms() * 32);
+  const int qpr = quarters_a_row(a.I), rpc = kCkptQuarters / qpr;
+  const int64_t g = std::min<int64_t>((a.R + rpc - 1) / rpc, (int64_t)device_sms() * 32);
   note_launch();
-  if (vec) return launch_pdl(k_ckpt_fwd<E, true, ACT>, dim3((unsigned)g), dim3(kCkptThreads), 0, st, a);
-  return launch_pdl(k_ckpt_fwd<E, false, ACT>, dim3((unsigned)g), dim3(kCkptThreads), 0, st, a);
+  if (vec) return launch_pdl(k_ckpt_fwd<E, true, ACT>, dim3((unsigned)g), dim3(kCkptThreads), 0, st, a, qpr);
+  return launch_pdl(k_ckpt_fwd<E, false, ACT>, dim3((unsigned)g), dim3(kCkptThreads), 0, st, a, qpr);
 }
 
 template <typename E, int ACT>
 static cudaError_t bwd_t(const CkptArgs& a, cudaStream_t st) {
   const bool vec = a.I % 8 == 0 && a.lddy % 8 == 0 && a.lddh % 8 == 0 && a.ldq % 8 == 0 && al(a.dy, 16) &&
                    al(a.dh, 16) && al(a.q, 8) && (!a.y || (a.ldy % 8 == 0 && al(a.y, 16)));
-  const int nb = (a.I + kQBlock - 1) / kQBlock;
-  // half-warps a row: the most that leave at most a tenth of them idle in the
-  // row's last round
-  int hpr = kCkptHalfWarps;
-  while (hpr > 1 && 10 * ((nb + hpr - 1) / hpr * hpr) > 11 * nb) hpr /= 2;
-  const int rpc = kCkptHalfWarps / hpr;
+  const int qpr = quarters_a_row(a.I), rpc = kCkptQuarters / qpr;
   const int64_t g = std::min<int64_t>((a.R + rpc - 1) / rpc, (int64_t)device_sms() * 32);
   note_launch();
-  if (vec) return launch_pdl(k_ckpt_bwd<E, true, ACT>, dim3((unsigned)g), dim3(kCkptThreads), 0, st, a, hpr);
-  return launch_pdl(k_ckpt_bwd<E, false, ACT>, dim3((unsigned)g), dim3(kCkptThreads), 0, st, a, hpr);
+  if (vec) return launch_pdl(k_ckpt_bwd<E, true, ACT>, dim3((unsigned)g), dim3(kCkptThreads), 0, st, a, qpr);
+  return launch_pdl(k_ckpt_bwd<E, false, ACT>, dim3((unsigned)g), dim3(kCkptThreads), 0, st, a, qpr);
 }
 
 template <typename E, bool FWD>

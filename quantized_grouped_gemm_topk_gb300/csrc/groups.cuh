@@ -158,11 +158,11 @@ __device__ __forceinline__ void store32(void* p, const uint32_t (&v)[32], int n,
   if (out_dtype == MOE_DT_F16) {
 #pragma unroll
     for (int i = 0; i < 16; ++i)
-      pk[i] = (uint32_t)F16::from(__uint_as_float(v[2 * i])) | ((uint32_t)F16::from(__uint_as_float(v[2 * i + 1])) << 16);
+      pk[i] = F16::from2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]));
   } else {
 #pragma unroll
     for (int i = 0; i < 16; ++i)
-      pk[i] = (uint32_t)Bf16::from(__uint_as_float(v[2 * i])) | ((uint32_t)Bf16::from(__uint_as_float(v[2 * i + 1])) << 16);
+      pk[i] = Bf16::from2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]));
   }
   if (vec && n >= 32) {
 #pragma unroll

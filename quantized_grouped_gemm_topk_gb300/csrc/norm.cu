@@ -16,29 +16,50 @@
 // partial rows that a second kernel adds in a fixed order: no atomics, the
 // same bits every run.
 #include "ops.cuh"
+#include "tc.cuh"
 
 namespace moe {
 
 constexpr int kNormMaxThreads = 1024;
 constexpr int kNormBwdThreads = 512;    // the backward holds four fp32 or packed values a column
 
-// Sums of a and b over the TPR threads of a row: shuffles, then the warps'
-// sums through shared memory (red: two floats a warp), added in warp order by
-// everyone. One barrier; consecutive calls alternate between two buffers.
+// Sums of a and b over the threads of a row (BLOCK: the nw warps of the CTA,
+// else the warp), in a fixed order, known to all of them. The first step of
+// each round sends one sum to the lower and one to the upper half-warp, so
+// two sums take five shuffles, not ten; the warps' sums cross shared memory
+// (red: one float2 a warp) behind one barrier. Consecutive calls alternate
+// between two buffers.
 template <bool BLOCK>
 __device__ __forceinline__ float2 row_sum2(float a, float b, float2* red, int nw) {
-  a = warp_sum(a);
-  b = warp_sum(b);
-  if constexpr (!BLOCK) return make_float2(a, b);
-  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = make_float2(a, b);
-  __syncthreads();
-  float2 s = red[0];
-  for (int i = 1; i < nw; ++i) {
-    const float2 o = red[i];
-    s.x += o.x;
-    s.y += o.y;
+  const int lane = threadIdx.x & 31;
+  const bool up = lane & 16;
+  float v = (up ? b : a) + __shfl_xor_sync(kFull, up ? a : b, 16);
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1) v += __shfl_xor_sync(kFull, v, o);
+  if constexpr (BLOCK) {
+    float* mine = reinterpret_cast<float*>(red + (threadIdx.x >> 5)) + (up ? 1 : 0);
+    if ((lane & 15) == 0) *mine = v;
+    __syncthreads();
+    const float* r = reinterpret_cast<const float*>(red) + (up ? 1 : 0);
+    const int i = lane & 15;
+    v = i < nw ? r[2 * i] : 0.f;
+    if (nw > 16) v += i + 16 < nw ? r[2 * (i + 16)] : 0.f;
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) v += __shfl_xor_sync(kFull, v, o);
   }
-  return s;
+  return make_float2(__shfl_sync(kFull, v, 0), __shfl_sync(kFull, v, 16));
+}
+// One sum.
+template <bool BLOCK>
+__device__ __forceinline__ float row_sum(float a, float2* red, int nw) {
+  a = warp_sum(a);
+  if constexpr (BLOCK) {
+    const int lane = threadIdx.x & 31;
+    if (lane == 0) red[threadIdx.x >> 5].x = a;
+    __syncthreads();
+    a = warp_sum(lane < nw ? red[lane].x : 0.f);
+  }
+  return a;
 }
 
 // Element i of a weight vector held in E's type or fp32; `def` when absent.
@@ -99,7 +120,7 @@ __global__ void __launch_bounds__(BLOCK ? kNormMaxThreads : 128) k_norm_fwd(Norm
 #pragma unroll
         for (int j = 0; j < V; ++j) s += E::to(p[i].v[j]);
       }
-    const float mu = row_sum2<BLOCK>(s, 0.f, red[0], nw).x * inv_h;
+    const float mu = row_sum<BLOCK>(s, red[0], nw) * inv_h;
     float m2 = 0.f;
 #pragma unroll
     for (int i = 0; i < NV; ++i)
@@ -110,7 +131,7 @@ __global__ void __launch_bounds__(BLOCK ? kNormMaxThreads : 128) k_norm_fwd(Norm
           m2 = fmaf(d, d, m2);
         }
       }
-    const float r = rsqrtf(row_sum2<BLOCK>(m2, 0.f, red[1], nw).x * inv_h + a.eps);
+    const float r = rsqrtf(row_sum<BLOCK>(m2, red[1], nw) * inv_h + a.eps);
     if (t == 0) {
       if (a.mean) a.mean[row] = mu;
       if (a.rstd) a.rstd[row] = r;
@@ -145,13 +166,13 @@ __global__ void __launch_bounds__(kNormMaxThreads) k_norm_fwd_long(NormArgs a) {
     const raw* x = reinterpret_cast<const raw*>(a.x) + row * a.ldx;
     float s = 0.f;
     for (int c = threadIdx.x; c < a.H; c += blockDim.x) s += E::to(x[c]);
-    const float mu = row_sum2<true>(s, 0.f, red[0], nw).x * inv_h;
+    const float mu = row_sum<true>(s, red[0], nw) * inv_h;
     float m2 = 0.f;
     for (int c = threadIdx.x; c < a.H; c += blockDim.x) {
       const float d = E::to(x[c]) - mu;
       m2 = fmaf(d, d, m2);
     }
-    const float r = rsqrtf(row_sum2<true>(m2, 0.f, red[1], nw).x * inv_h + a.eps);
+    const float r = rsqrtf(row_sum<true>(m2, red[1], nw) * inv_h + a.eps);
     if (threadIdx.x == 0) {
       if (a.mean) a.mean[row] = mu;
       if (a.rstd) a.rstd[row] = r;
@@ -248,6 +269,193 @@ __global__ void __launch_bounds__(BLOCK ? kNormBwdThreads : 128) k_norm_bwd(Norm
   }
 }
 
+// ---- many rows: a ring of rows in shared memory ---------------------------------
+// Registers alone keep too few bytes in flight (a row's barriers come between
+// its loads and the next row's): thread 0 keeps kRing bulk copies of rows
+// ahead in shared memory. A stage is refilled behind the row's first barrier,
+// when every thread has its packs in registers. Rows start on 16 bytes and are
+// a whole number of packs.
+constexpr int kRingMax = 8;
+constexpr int kRingBytes = 200 * 1024;    // of an SM's shared memory, for all its CTAs
+constexpr int kRingHead = 128;            // barriers, in front of the stages
+
+// The bounded wait for a row. A copy from this GPU's memory always lands;
+// should the wait run out all the same, the row's results become NaN.
+__device__ __forceinline__ bool ring_wait(uint64_t* bar, uint32_t parity) {
+  volatile int give_up = 0;
+  return tc::mbar_wait(bar, parity, &give_up);
+}
+
+template <typename E, bool WF32, int NV, bool PART, bool BWD>
+__global__ void __launch_bounds__(kNormBwdThreads, NV == 1 ? 2 : 1) k_norm_ring(NormArgs a, int stages) {
+  using raw = typename E::raw;
+  constexpr int V = 16 / (int)sizeof(raw);
+  pdl_enter();
+  __shared__ float2 red[2][kNormBwdThreads / 32];
+  extern __shared__ __align__(128) uint8_t ring[];
+  uint64_t* full = reinterpret_cast<uint64_t*>(ring);
+  const uint32_t row_bytes = (uint32_t)a.H * sizeof(raw);
+  const uint32_t stage_bytes = row_bytes * (BWD ? 2 : 1);
+  const int tpr = blockDim.x, t = threadIdx.x, nw = tpr / 32;
+  const float inv_h = 1.0f / (float)a.H;
+  const raw* X = reinterpret_cast<const raw*>(a.x);
+  const raw* DY = reinterpret_cast<const raw*>(a.dy);
+  auto fetch = [&](int s, int64_t row) {
+    if (row >= a.T) return;
+    uint8_t* d = ring + kRingHead + s * stage_bytes;
+    tc::mbar_arrive_expect_tx(&full[s], stage_bytes);
+    tc::bulk_g2s_plain(d, X + row * a.ldx, row_bytes, &full[s]);
+    if (BWD) tc::bulk_g2s_plain(d + row_bytes, DY + row * a.lddy, row_bytes, &full[s]);
+  };
+  if (t == 0) {
+    for (int s = 0; s < stages; ++s) tc::mbar_init(&full[s], 1);
+    tc::fence_mbar_init();
+    for (int s = 0; s < stages; ++s) fetch(s, blockIdx.x + (int64_t)s * gridDim.x);
+  }
+  __syncthreads();
+  // the thread's columns are the same in every row: weights stay in registers
+  float g[NV * V], b[BWD ? 1 : NV * V];
+  float dg[PART ? NV * V : 1], db[PART ? NV * V : 1];
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int c = (i * tpr + t) * V;
+    float w[V];
+#pragma unroll
+    for (int j = 0; j < V; ++j) w[j] = 0.f;
+    if (c < a.H) weights_at<E, WF32, V>(w, a.gamma, c, 1.f);
+#pragma unroll
+    for (int j = 0; j < V; ++j) g[i * V + j] = w[j];
+    if constexpr (!BWD) {
+      if (c < a.H) weights_at<E, WF32, V>(w, a.beta, c, 0.f);
+#pragma unroll
+      for (int j = 0; j < V; ++j) b[i * V + j] = w[j];
+    }
+    if constexpr (PART) {
+#pragma unroll
+      for (int j = 0; j < V; ++j) dg[i * V + j] = db[i * V + j] = 0.f;
+    }
+  }
+  float mu = 0.f, r = 0.f, mu_next = 0.f, r_next = 0.f;
+  if (BWD) {
+    mu_next = a.mean[blockIdx.x];
+    r_next = a.rstd[blockIdx.x];
+  }
+  int s = 0;
+  uint32_t parity = 0;
+  int flip = 0;
+  for (int64_t row = blockIdx.x; row < a.T; row += gridDim.x) {
+    if (BWD) {
+      mu = mu_next;
+      r = r_next;
+      if (row + gridDim.x < a.T) {
+        mu_next = a.mean[row + gridDim.x];
+        r_next = a.rstd[row + gridDim.x];
+      }
+    }
+    const bool got = ring_wait(&full[s], parity);
+    const uint8_t* sx = ring + kRingHead + s * stage_bytes;
+    Pack<E, V> px[NV], pd[BWD ? NV : 1];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int c = i * tpr + t;
+      if (c * V < a.H) {
+        load_pack(px[i], reinterpret_cast<const raw*>(sx) + c * V);
+        if constexpr (BWD) load_pack(pd[i], reinterpret_cast<const raw*>(sx + row_bytes) + c * V);
+      }
+    }
+    raw* out = reinterpret_cast<raw*>(a.out) + row * a.ldo;
+    const float bad = got ? 0.f : __int_as_float(0x7fffffff);
+    if constexpr (BWD) {
+      float s1 = bad, s2 = 0.f;
+#pragma unroll
+      for (int i = 0; i < NV; ++i)
+        if ((i * tpr + t) * V < a.H) {
+#pragma unroll
+          for (int j = 0; j < V; ++j) {
+            const float d = E::to(pd[i].v[j]), xh = (E::to(px[i].v[j]) - mu) * r, tg = d * g[i * V + j];
+            s1 += tg;
+            s2 = fmaf(tg, xh, s2);
+            if constexpr (PART) {
+              dg[i * V + j] = fmaf(d, xh, dg[i * V + j]);
+              db[i * V + j] += d;
+            }
+          }
+        }
+      const float2 m = row_sum2<true>(s1, s2, red[flip], nw);
+      flip ^= 1;
+      if (t == 0) fetch(s, row + (int64_t)stages * gridDim.x);
+      const float m1 = m.x * inv_h, m2 = m.y * inv_h;
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const int c = (i * tpr + t) * V;
+        if (c < a.H) {
+          Pack<E, V> o;
+#pragma unroll
+          for (int j = 0; j < V; ++j) {
+            const float xh = (E::to(px[i].v[j]) - mu) * r;
+            o.v[j] = E::from(r * (E::to(pd[i].v[j]) * g[i * V + j] - m1 - xh * m2));
+          }
+          store_pack<E, V>(out + c, o);
+        }
+      }
+    } else {
+      float sum = bad;
+#pragma unroll
+      for (int i = 0; i < NV; ++i)
+        if ((i * tpr + t) * V < a.H) {
+#pragma unroll
+          for (int j = 0; j < V; ++j) sum += E::to(px[i].v[j]);
+        }
+      mu = row_sum<true>(sum, red[0], nw) * inv_h;
+      if (t == 0) fetch(s, row + (int64_t)stages * gridDim.x);
+      float m2 = 0.f;
+#pragma unroll
+      for (int i = 0; i < NV; ++i)
+        if ((i * tpr + t) * V < a.H) {
+#pragma unroll
+          for (int j = 0; j < V; ++j) {
+            const float d = E::to(px[i].v[j]) - mu;
+            m2 = fmaf(d, d, m2);
+          }
+        }
+      r = rsqrtf(row_sum<true>(m2, red[1], nw) * inv_h + a.eps);
+      if (t == 0) {
+        if (a.mean) a.mean[row] = mu;
+        if (a.rstd) a.rstd[row] = r;
+      }
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const int c = (i * tpr + t) * V;
+        if (c < a.H) {
+          Pack<E, V> o;
+#pragma unroll
+          for (int j = 0; j < V; ++j)
+            o.v[j] = E::from(fmaf((E::to(px[i].v[j]) - mu) * r, g[i * V + j], b[i * V + j]));
+          store_pack<E, V>(out + c, o);
+        }
+      }
+    }
+    if (++s == stages) {
+      s = 0;
+      parity ^= 1;
+    }
+  }
+  if constexpr (PART) {
+    float* pg = a.part + (int64_t)blockIdx.x * 2 * a.H;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int c = (i * tpr + t) * V;
+      if (c < a.H) {
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+          pg[c + j] = dg[i * V + j];
+          pg[a.H + c + j] = db[i * V + j];
+        }
+      }
+    }
+  }
+}
+
 // dx of rows too long for registers (three reads), without the weight's
 // gradient.
 template <typename E, bool WF32>
@@ -307,8 +515,17 @@ __global__ void __launch_bounds__(1024) k_norm_dw_sum(const float* __restrict__ 
   const int c = blockIdx.x * 32 + (threadIdx.x & 31), l = threadIdx.x >> 5;
   const int64_t at = (int64_t)blockIdx.y * H + c;
   float v = 0.f;
-  if (c < H)
-    for (int p = l; p < P; p += 32) v += part[(int64_t)p * 2 * H + at];
+  if (c < H) {
+    int p = l;
+    for (; p + 7 * 32 < P; p += 8 * 32) {       // eight loads in flight
+      float t[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) t[j] = part[(int64_t)(p + 32 * j) * 2 * H + at];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v += t[j];
+    }
+    for (; p < P; p += 32) v += part[(int64_t)p * 2 * H + at];
+  }
   s[l][threadIdx.x & 31] = v;
   __syncthreads();
   if (l == 0 && c < H) {
@@ -340,8 +557,11 @@ struct NormPlan {
   int nv, threads;
   int64_t grid;
 };
-// Threads and packs a thread for rows of n packs; per_cta: rows a CTA holds.
-static NormPlan norm_plan(int64_t n, int64_t T, int max_nv, int max_threads_per_sm, int max_parts, int max_threads) {
+// Threads and packs a thread for rows of n packs. resident: threads an SM
+// holds, for a grid that is resident at once and whose CTAs sum over rows (at
+// most max_parts of them where that is not 0); 0: a CTA a row, handed out as
+// SMs come free.
+static NormPlan norm_plan(int64_t n, int64_t T, int max_nv, int resident, int max_parts, int max_threads) {
   NormPlan p = {};
   if (n <= 32) {                       // a warp a row
     p.nv = 1;
@@ -357,16 +577,65 @@ static NormPlan norm_plan(int64_t n, int64_t T, int max_nv, int max_threads_per_
   }
   if (p.longrow) p.threads = kNormMaxThreads;
   const int rpb = p.block ? 1 : p.threads / 32;
-  int64_t g = (int64_t)device_sms() * std::max(1, max_threads_per_sm / p.threads);
+  int64_t g = p.block && !resident ? INT32_MAX
+                                   : (int64_t)device_sms() * std::max(1, (resident ? resident : 2048) / p.threads);
   if (max_parts) g = std::min<int64_t>(g, max_parts / rpb);
   p.grid = std::max<int64_t>(1, std::min<int64_t>(g, (T + rpb - 1) / rpb));
   return p;
 }
 
+// Launch of the ring, or cudaErrorNotSupported where it does not apply: few
+// rows (their latency is shorter without it), rows of at most a warp's packs
+// (many rows in flight already) or of more than the registers hold.
+template <typename E, bool WF32, int NV, bool PART, bool BWD>
+static cudaError_t ring_nv(const NormArgs& a, int threads, int64_t* parts, cudaStream_t st) {
+  const auto kern = k_norm_ring<E, WF32, NV, PART, BWD>;
+  static std::atomic<int> regs{0};
+  if (regs.load(std::memory_order_acquire) == 0) {
+    cudaFuncAttributes at;
+    const cudaError_t e = cudaFuncGetAttributes(&at, kern);
+    if (e != cudaSuccess) return e;
+    regs.store((at.numRegs + 7) / 8 * 8, std::memory_order_release);
+  }
+  static std::atomic<bool> done[kMaxDevices] = {};
+  cudaError_t e = set_smem_once((const void*)kern, kRingBytes + 1024, done);
+  if (e != cudaSuccess) return e;
+  const int stage = a.H * (int)sizeof(typename E::raw) * (BWD ? 2 : 1);
+  // CTAs an SM holds (registers are handed out to four warps at a time), each
+  // with at least two stages; then all the stages that fit
+  int ctas = std::max(1, std::min({6, 65536 / (regs.load() * ((threads + 127) / 128 * 128)), 2048 / threads}));
+  while (ctas > 1 && 2 * stage * ctas > kRingBytes) --ctas;
+  const int stages = std::min(kRingMax, kRingBytes / (ctas * stage));
+  if (stages < 2) return cudaErrorNotSupported;
+  const int64_t grid = std::min<int64_t>({a.T, (int64_t)device_sms() * ctas, kNormMaxParts});
+  *parts = grid;
+  note_launch();
+  return launch_pdl(kern, dim3((unsigned)grid), dim3(threads), (size_t)kRingHead + (size_t)stages * stage, st, a, stages);
+}
+template <typename E, bool WF32, bool PART, bool BWD>
+static cudaError_t ring_launch(const NormArgs& a, int64_t* parts, cudaStream_t st) {
+  constexpr int V = 16 / (int)sizeof(typename E::raw);
+  const int n = a.H / V;
+  if (n <= 32 || n > 4 * kNormBwdThreads || a.T < 4LL * device_sms()) return cudaErrorNotSupported;
+  // one pack a thread while that is at most 512 threads, then two, four: the
+  // sums over rows of a thread's columns stay in registers, and the fewer of
+  // them the more warps hide the row's barriers
+  const int nv = n <= kNormBwdThreads ? 1 : n <= 2 * kNormBwdThreads ? 2 : 4;
+  const int threads = ((n + nv - 1) / nv + 31) / 32 * 32;
+  if (nv == 1) return ring_nv<E, WF32, 1, PART, BWD>(a, threads, parts, st);
+  return nv == 2 ? ring_nv<E, WF32, 2, PART, BWD>(a, threads, parts, st)
+                 : ring_nv<E, WF32, 4, PART, BWD>(a, threads, parts, st);
+}
+
 template <typename E, bool WF32, int V>
 static cudaError_t fwd_v(const NormArgs& a, cudaStream_t st) {
+  if constexpr (V > 1) {
+    int64_t parts;
+    const cudaError_t e = ring_launch<E, WF32, false, false>(a, &parts, st);
+    if (e != cudaErrorNotSupported) return e;
+  }
   constexpr int kMaxNv = V == 1 ? 16 : 4;
-  const NormPlan p = norm_plan(((int64_t)a.H + V - 1) / V, a.T, kMaxNv, 2048, 0, kNormMaxThreads);
+  const NormPlan p = norm_plan(((int64_t)a.H + V - 1) / V, a.T, kMaxNv, 0, 0, kNormMaxThreads);
   const dim3 g((unsigned)p.grid), b(p.threads);
   note_launch();
   if (p.longrow) return launch_pdl(k_norm_fwd_long<E, WF32>, g, b, 0, st, a);
@@ -396,11 +665,14 @@ template <typename E, bool WF32, int V>
 static cudaError_t bwd_v(const NormArgs& a, cudaStream_t st) {
   const bool want = a.dgamma || a.dbeta;
   constexpr int kMaxNv = V == 1 ? 16 : 4;
-  const NormPlan p = norm_plan(((int64_t)a.H + V - 1) / V, a.T, kMaxNv, 1024, want ? kNormMaxParts : 0,
+  const NormPlan p = norm_plan(((int64_t)a.H + V - 1) / V, a.T, kMaxNv, 512, want ? kNormMaxParts : 0,
                                kNormBwdThreads);
-  cudaError_t e = cudaErrorInvalidValue;
+  cudaError_t e = cudaErrorNotSupported;
   int64_t parts = std::min<int64_t>(a.T, p.grid * (p.block ? 1 : p.threads / 32));
-  if (p.longrow) {
+  if constexpr (V > 1)
+    e = want ? ring_launch<E, WF32, true, true>(a, &parts, st) : ring_launch<E, WF32, false, true>(a, &parts, st);
+  if (e != cudaErrorNotSupported) {
+  } else if (p.longrow) {
     note_launch();
     e = launch_pdl(k_norm_bwd_long<E, WF32>, dim3((unsigned)p.grid), dim3(p.threads), 0, st, a);
     if (e != cudaSuccess) return e;

@@ -13,12 +13,21 @@ struct Bf16 {
   static constexpr uint32_t kInf = 0x7f80u;
   static __device__ __forceinline__ float to(raw v) { return bf16_bits_to_f32(v); }
   static __device__ __forceinline__ raw from(float f) { return f32_to_bf16_bits(f); }
+  // two at once, a in the low half
+  static __device__ __forceinline__ uint32_t from2(float a, float b) {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&v);
+  }
 };
 struct F16 {
   using raw = uint16_t;
   static constexpr uint32_t kInf = 0x7c00u;
   static __device__ __forceinline__ float to(raw v) { return __half2float(__ushort_as_half(v)); }
   static __device__ __forceinline__ raw from(float f) { return __half_as_ushort(__float2half_rn(f)); }
+  static __device__ __forceinline__ uint32_t from2(float a, float b) {
+    const __half2 v = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&v);
+  }
 };
 struct F32 {
   using raw = float;

@@ -82,6 +82,12 @@ def test_layer_norm(T, H, dtype, wdtype, pad):
         assert torch.equal(dx2, dx)
 
 
+@pytest.mark.parametrize("T,H", [(700, 264), (1300, 2880), (900, 4096), (640, 7168), (620, 8200), (615, 16384), (1500, 520)])
+@pytest.mark.parametrize("dtype,wdtype", [(BF16, F32), (F16, F16), (F32, F32)])
+def test_layer_norm_many_rows(T, H, dtype, wdtype):
+    test_layer_norm(T, H, dtype, wdtype, 0)
+
+
 def test_layer_norm_without_weights_and_repeatable():
     cuda_device()
     g = _gen(5)
