@@ -85,26 +85,28 @@ __device__ __forceinline__ float3 ckpt_act_grad(float g, float u, const ActParam
 }
 
 // A block's 128 columns belong to eight lanes, sixteen to a lane: columns
-// 8 l .. 8 l + 7 and 64 + 8 l .. (VEC: two 16-byte accesses, I a multiple of
-// 8), or l + 8 j. Sixteen, so that a block's fixed work (the scales' divisions,
-// shuffles, addresses) is spread over more elements. Held as words of two
-// 16-bit elements. Columns past the block's n are zeros and not written.
+// 8 l .. 8 l + 7 and 64 + 8 l .. . Sixteen, so that a block's fixed work (the
+// scales' divisions, shuffles, addresses) is spread over more elements. Held
+// as words of two 16-bit elements (four codes). VEC: every eight start on a
+// 16-byte (codes: 8-byte) boundary, I being a multiple of 8; otherwise rows at
+// any alignment. Columns past the n of the half (counted from the block's
+// first) read as zeros and are not written.
 template <bool VEC>
-__device__ __forceinline__ void load16(uint32_t (&w)[8], const uint16_t* p, int l, int n) {
-  if constexpr (VEC) {
+__device__ __forceinline__ void load16(uint32_t (&w)[8], const uint16_t* p, int l, int n, const uint16_t* half, int I) {
 #pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      const int c = 64 * k + 8 * l;
-      uint4 v = make_uint4(0u, 0u, 0u, 0u);
-      if (c < n) v = *reinterpret_cast<const uint4*>(p + c);
-      w[4 * k] = v.x; w[4 * k + 1] = v.y; w[4 * k + 2] = v.z; w[4 * k + 3] = v.w;
+  for (int k = 0; k < 2; ++k) {
+    const int c = 64 * k + 8 * l;
+    uint32_t v[4] = {0u, 0u, 0u, 0u};
+    if constexpr (VEC) {
+      if (c < n) {
+        const uint4 u = *reinterpret_cast<const uint4*>(p + c);
+        v[0] = u.x; v[1] = u.y; v[2] = u.z; v[3] = u.w;
+      }
+    } else {
+      load_any<2, 16>(v, p + c, half, half + I);
     }
-  } else {
-    uint16_t e[16];
 #pragma unroll
-    for (int j = 0; j < 16; ++j) e[j] = l + 8 * j < n ? p[l + 8 * j] : (uint16_t)0;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) w[j] = (uint32_t)e[2 * j] | ((uint32_t)e[2 * j + 1] << 16);
+    for (int i = 0; i < 4; ++i) w[4 * k + i] = v[i];
   }
 }
 template <typename E>
@@ -113,51 +115,44 @@ __device__ __forceinline__ float2 pair_of(uint32_t w) {
 }
 template <bool VEC>
 __device__ __forceinline__ void store16(uint16_t* p, const uint32_t (&w)[8], int l, int n) {
-  if constexpr (VEC) {
 #pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      const int c = 64 * k + 8 * l;
-      if (c < n) *reinterpret_cast<uint4*>(p + c) = make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
+  for (int k = 0; k < 2; ++k) {
+    const int c = 64 * k + 8 * l;
+    const uint32_t v[4] = {w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]};
+    if (c < n) {
+      if constexpr (VEC) *reinterpret_cast<uint4*>(p + c) = make_uint4(v[0], v[1], v[2], v[3]);
+      else store_any<2>(p + c, v, n - c);
     }
-  } else {
-#pragma unroll
-    for (int j = 0; j < 16; ++j)
-      if (l + 8 * j < n) p[l + 8 * j] = (uint16_t)(w[j >> 1] >> (16 * (j & 1)));
   }
 }
-// Sixteen codes as four words.
 template <bool VEC>
-__device__ __forceinline__ void load_codes(uint32_t (&w)[4], const uint8_t* q, int l, int n) {
-  if constexpr (VEC) {
+__device__ __forceinline__ void load_codes(uint32_t (&w)[4], const uint8_t* q, int l, int n, const uint8_t* half, int I) {
 #pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      const int c = 64 * k + 8 * l;
-      uint2 v = make_uint2(0u, 0u);
-      if (c < n) v = *reinterpret_cast<const uint2*>(q + c);
-      w[2 * k] = v.x; w[2 * k + 1] = v.y;
+  for (int k = 0; k < 2; ++k) {
+    const int c = 64 * k + 8 * l;
+    uint32_t v[2] = {0u, 0u};
+    if constexpr (VEC) {
+      if (c < n) {
+        const uint2 u = *reinterpret_cast<const uint2*>(q + c);
+        v[0] = u.x; v[1] = u.y;
+      }
+    } else {
+      load_any<1, 8>(v, q + c, half, half + I);
     }
-  } else {
-    uint8_t e[16];
-#pragma unroll
-    for (int j = 0; j < 16; ++j) e[j] = l + 8 * j < n ? q[l + 8 * j] : (uint8_t)0;
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-      w[j] = (uint32_t)e[4 * j] | ((uint32_t)e[4 * j + 1] << 8) | ((uint32_t)e[4 * j + 2] << 16) |
-             ((uint32_t)e[4 * j + 3] << 24);
+    w[2 * k] = v[0];
+    w[2 * k + 1] = v[1];
   }
 }
 template <bool VEC>
 __device__ __forceinline__ void store_codes(uint8_t* q, const uint32_t (&w)[4], int l, int n) {
-  if constexpr (VEC) {
 #pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      const int c = 64 * k + 8 * l;
-      if (c < n) *reinterpret_cast<uint2*>(q + c) = make_uint2(w[2 * k], w[2 * k + 1]);
+  for (int k = 0; k < 2; ++k) {
+    const int c = 64 * k + 8 * l;
+    const uint2 v = make_uint2(w[2 * k], w[2 * k + 1]);
+    if (c < n) {
+      if constexpr (VEC) *reinterpret_cast<uint2*>(q + c) = v;
+      else store_bytes8(q + c, v, n - c);
     }
-  } else {
-#pragma unroll
-    for (int j = 0; j < 16; ++j)
-      if (l + 8 * j < n) q[l + 8 * j] = (uint8_t)(w[j >> 2] >> (8 * (j & 3)));
   }
 }
 
@@ -230,8 +225,8 @@ __global__ void __launch_bounds__(kCkptThreads) k_ckpt_fwd(CkptArgs a, int qpr) 
     for (int b = part; b < nb; b += qpr) {
       const int c0 = b * kQBlock, n = min(kQBlock, a.I - c0);
       uint32_t gw[8], uw[8] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u};
-      load16<VEC>(gw, h + c0, l, n);
-      if constexpr (GATED) load16<VEC>(uw, h + a.I + c0, l, n);
+      load16<VEC>(gw, h + c0, l, n, h, a.I);
+      if constexpr (GATED) load16<VEC>(uw, h + a.I + c0, l, n, h + a.I, a.I);
       // both halves' largest magnitudes in one word: three shuffles
       uint32_t mm = mag_bits(gw) | (GATED ? mag_bits(uw) << 16 : 0u);
 #pragma unroll
@@ -309,9 +304,9 @@ __global__ void __launch_bounds__(kCkptThreads) k_ckpt_bwd(CkptArgs a, int qpr) 
       for (int b = part; b < nb; b += qpr) {
         const int c0 = b * kQBlock, n = min(kQBlock, a.I - c0);
         uint32_t qg[4], qu[4] = {0u, 0u, 0u, 0u}, d[8], dg[8], du[8], yw[8];
-        load_codes<VEC>(qg, q + c0, l, n);
-        if constexpr (GATED) load_codes<VEC>(qu, q + a.I + c0, l, n);
-        load16<VEC>(d, dy + c0, l, n);
+        load_codes<VEC>(qg, q + c0, l, n, q, a.I);
+        if constexpr (GATED) load_codes<VEC>(qu, q + a.I + c0, l, n, q + a.I, a.I);
+        load16<VEC>(d, dy + c0, l, n, dy, a.I);
         const float sg = s[b], su = GATED ? s[nb + b] : 0.f;
         bool nan = false;
 #pragma unroll

@@ -95,10 +95,45 @@ __device__ __forceinline__ void weights_at(float (&o)[V], const void* w, int c, 
   }
 }
 
+// A pack of a row (VEC: on 16 bytes and whole; else at any alignment, with
+// zeros from the row's end on), and its store.
+template <typename E, int V, bool VEC>
+__device__ __forceinline__ void load_row_pack(Pack<E, V>& p, const typename E::raw* row, int c, int H) {
+  if constexpr (VEC) {
+    load_pack(p, row + c);
+  } else {
+    uint32_t w[4];
+    load_any<(int)sizeof(typename E::raw), 16>(w, row + c, row, row + H);
+    *reinterpret_cast<uint4*>(&p) = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+}
+template <typename E, int V, bool VEC>
+__device__ __forceinline__ void store_row_pack(typename E::raw* row, const Pack<E, V>& p, int c, int H) {
+  if constexpr (VEC) {
+    store_pack<E, V>(row + c, p);
+  } else {
+    const uint4 u = *reinterpret_cast<const uint4*>(&p);
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+    store_any<(int)sizeof(typename E::raw)>(row + c, w, H - c);
+  }
+}
+// The pack's weights; single loads where they are not aligned or the row ends
+// inside the pack.
+template <typename E, bool WF32, int V, bool VEC>
+__device__ __forceinline__ void row_weights(float (&o)[V], const void* w, int c, int H, float def) {
+  if (VEC || (((uintptr_t)w & 15) == 0 && c + V <= H)) {
+    weights_at<E, WF32, V>(o, w, c, def);
+  } else {
+#pragma unroll
+    for (int j = 0; j < V; ++j) o[j] = c + j < H ? weight_at<E, WF32>(w, c + j, def) : 0.f;
+  }
+}
+
 // Rows per CTA: 1 with BLOCK, else one per warp.
-template <typename E, bool WF32, int V, int NV, bool BLOCK>
+template <typename E, bool WF32, int NV, bool BLOCK, bool VEC>
 __global__ void __launch_bounds__(BLOCK ? kNormMaxThreads : 128) k_norm_fwd(NormArgs a) {
   using raw = typename E::raw;
+  constexpr int V = 16 / (int)sizeof(raw);
   pdl_enter();
   __shared__ float2 red[2][kNormMaxThreads / 32];
   const int tpr = BLOCK ? blockDim.x : 32, t = BLOCK ? threadIdx.x : threadIdx.x & 31;
@@ -112,7 +147,7 @@ __global__ void __launch_bounds__(BLOCK ? kNormMaxThreads : 128) k_norm_fwd(Norm
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int c = (i * tpr + t) * V;
-      if (c < a.H) load_pack(p[i], x + c);
+      if (c < a.H) load_row_pack<E, V, VEC>(p[i], x, c, a.H);
     }
 #pragma unroll
     for (int i = 0; i < NV; ++i)
@@ -127,6 +162,7 @@ __global__ void __launch_bounds__(BLOCK ? kNormMaxThreads : 128) k_norm_fwd(Norm
       if ((i * tpr + t) * V < a.H) {
 #pragma unroll
         for (int j = 0; j < V; ++j) {
+          if (!VEC && (i * tpr + t) * V + j >= a.H) continue;
           const float d = E::to(p[i].v[j]) - mu;
           m2 = fmaf(d, d, m2);
         }
@@ -142,12 +178,12 @@ __global__ void __launch_bounds__(BLOCK ? kNormMaxThreads : 128) k_norm_fwd(Norm
       const int c = (i * tpr + t) * V;
       if (c < a.H) {
         float g[V], b[V];
-        weights_at<E, WF32, V>(g, a.gamma, c, 1.f);
-        weights_at<E, WF32, V>(b, a.beta, c, 0.f);
+        row_weights<E, WF32, V, VEC>(g, a.gamma, c, a.H, 1.f);
+        row_weights<E, WF32, V, VEC>(b, a.beta, c, a.H, 0.f);
         Pack<E, V> o;
 #pragma unroll
         for (int j = 0; j < V; ++j) o.v[j] = E::from(fmaf((E::to(p[i].v[j]) - mu) * r, g[j], b[j]));
-        store_pack<E, V>(y + c, o);
+        store_row_pack<E, V, VEC>(y, o, c, a.H);
       }
     }
   }
@@ -186,9 +222,10 @@ __global__ void __launch_bounds__(kNormMaxThreads) k_norm_fwd_long(NormArgs a) {
 
 // PART: the weight's gradient is wanted. Partial row p = the CTA (BLOCK) or
 // the warp: part[p][0][c] = dgamma, part[p][1][c] = dbeta over its rows.
-template <typename E, bool WF32, int V, int NV, bool BLOCK, bool PART>
+template <typename E, bool WF32, int NV, bool BLOCK, bool PART, bool VEC>
 __global__ void __launch_bounds__(BLOCK ? kNormBwdThreads : 128) k_norm_bwd(NormArgs a) {
   using raw = typename E::raw;
+  constexpr int V = 16 / (int)sizeof(raw);
   pdl_enter();
   __shared__ float2 red[2][kNormMaxThreads / 32];
   const int tpr = BLOCK ? blockDim.x : 32, t = BLOCK ? threadIdx.x : threadIdx.x & 31;
@@ -209,8 +246,8 @@ __global__ void __launch_bounds__(BLOCK ? kNormBwdThreads : 128) k_norm_bwd(Norm
     for (int i = 0; i < NV; ++i) {
       const int c = (i * tpr + t) * V;
       if (c < a.H) {
-        load_pack(px[i], x + c);
-        load_pack(pd[i], dy + c);
+        load_row_pack<E, V, VEC>(px[i], x, c, a.H);
+        load_row_pack<E, V, VEC>(pd[i], dy, c, a.H);      // zeros past the row's end: they add nothing
       }
     }
     const float mu = a.mean[row], r = a.rstd[row];
@@ -220,7 +257,7 @@ __global__ void __launch_bounds__(BLOCK ? kNormBwdThreads : 128) k_norm_bwd(Norm
       const int c = (i * tpr + t) * V;
       if (c < a.H) {
         float g[V];
-        weights_at<E, WF32, V>(g, a.gamma, c, 1.f);
+        row_weights<E, WF32, V, VEC>(g, a.gamma, c, a.H, 1.f);
 #pragma unroll
         for (int j = 0; j < V; ++j) {
           const float d = E::to(pd[i].v[j]), xh = (E::to(px[i].v[j]) - mu) * r, tg = d * g[j];
@@ -241,14 +278,14 @@ __global__ void __launch_bounds__(BLOCK ? kNormBwdThreads : 128) k_norm_bwd(Norm
       const int c = (i * tpr + t) * V;
       if (c < a.H) {
         float g[V];
-        weights_at<E, WF32, V>(g, a.gamma, c, 1.f);
+        row_weights<E, WF32, V, VEC>(g, a.gamma, c, a.H, 1.f);
         Pack<E, V> o;
 #pragma unroll
         for (int j = 0; j < V; ++j) {
           const float xh = (E::to(px[i].v[j]) - mu) * r;
           o.v[j] = E::from(r * (E::to(pd[i].v[j]) * g[j] - m1 - xh * m2));
         }
-        store_pack<E, V>(dx + c, o);
+        store_row_pack<E, V, VEC>(dx, o, c, a.H);
       }
     }
   }
@@ -261,6 +298,7 @@ __global__ void __launch_bounds__(BLOCK ? kNormBwdThreads : 128) k_norm_bwd(Norm
       if (c < a.H) {
 #pragma unroll
         for (int j = 0; j < V; ++j) {
+          if (!VEC && c + j >= a.H) continue;
           pg[c + j] = dg[i * V + j];
           pg[a.H + c + j] = db[i * V + j];
         }
@@ -541,15 +579,15 @@ __global__ void __launch_bounds__(1024) k_norm_dw_sum(const float* __restrict__ 
 }
 
 // ---- host ---------------------------------------------------------------------
-static bool aligned(const void* p, size_t n) { return ((uintptr_t)p & (n - 1)) == 0; }
+static bool on(const void* p, size_t n) { return ((uintptr_t)p & (n - 1)) == 0; }
 
 // 16-byte accesses: every row of x, dy and out, and the weights, start on 16
 // bytes and H is a whole number of packs.
 static bool vec_ok(const NormArgs& a, int esize) {
   const int V = 16 / esize;
-  const bool rows = a.H % V == 0 && a.ldx % V == 0 && a.ldo % V == 0 && aligned(a.x, 16) && aligned(a.out, 16) &&
-                    (!a.dy || (a.lddy % V == 0 && aligned(a.dy, 16)));
-  return rows && aligned(a.gamma, 16) && aligned(a.beta, 16);
+  const bool rows = a.H % V == 0 && a.ldx % V == 0 && a.ldo % V == 0 && on(a.x, 16) && on(a.out, 16) &&
+                    (!a.dy || (a.lddy % V == 0 && on(a.dy, 16)));
+  return rows && on(a.gamma, 16) && on(a.beta, 16);
 }
 
 struct NormPlan {
@@ -561,17 +599,17 @@ struct NormPlan {
 // holds, for a grid that is resident at once and whose CTAs sum over rows (at
 // most max_parts of them where that is not 0); 0: a CTA a row, handed out as
 // SMs come free.
-static NormPlan norm_plan(int64_t n, int64_t T, int max_nv, int resident, int max_parts, int max_threads) {
+static NormPlan norm_plan(int64_t n, int64_t T, int resident, int max_parts, int max_threads) {
   NormPlan p = {};
   if (n <= 32) {                       // a warp a row
     p.nv = 1;
     p.threads = 128;
   } else {
     p.block = true;
-    // fewest packs a thread that leave at most 256 threads a row: short
-    // barriers, several rows in flight on an SM; longer rows take max_nv
+    // fewest packs a thread (one, two, four) that leave at most 256 threads a
+    // row: short barriers, several rows in flight on an SM
     p.nv = 1;
-    while (p.nv < max_nv && (n + p.nv - 1) / p.nv > 256) p.nv *= 2;
+    while (p.nv < 4 && (n + p.nv - 1) / p.nv > 256) p.nv *= 2;
     p.threads = (int)(((n + p.nv - 1) / p.nv + 31) / 32 * 32);
     if (p.threads > max_threads) p.longrow = true;
   }
@@ -627,49 +665,40 @@ static cudaError_t ring_launch(const NormArgs& a, int64_t* parts, cudaStream_t s
                  : ring_nv<E, WF32, 4, PART, BWD>(a, threads, parts, st);
 }
 
-template <typename E, bool WF32, int V>
+template <typename E, bool WF32, bool VEC>
 static cudaError_t fwd_v(const NormArgs& a, cudaStream_t st) {
-  if constexpr (V > 1) {
+  constexpr int V = 16 / (int)sizeof(typename E::raw);
+  if constexpr (VEC) {
     int64_t parts;
     const cudaError_t e = ring_launch<E, WF32, false, false>(a, &parts, st);
     if (e != cudaErrorNotSupported) return e;
   }
-  constexpr int kMaxNv = V == 1 ? 16 : 4;
-  const NormPlan p = norm_plan(((int64_t)a.H + V - 1) / V, a.T, kMaxNv, 0, 0, kNormMaxThreads);
+  const NormPlan p = norm_plan(((int64_t)a.H + V - 1) / V, a.T, 0, 0, kNormMaxThreads);
   const dim3 g((unsigned)p.grid), b(p.threads);
   note_launch();
   if (p.longrow) return launch_pdl(k_norm_fwd_long<E, WF32>, g, b, 0, st, a);
-  if (!p.block) return launch_pdl(k_norm_fwd<E, WF32, V, 1, false>, g, b, 0, st, a);
-  switch (p.nv) {
-    case 1: return launch_pdl(k_norm_fwd<E, WF32, V, 1, true>, g, b, 0, st, a);
-    case 2: return launch_pdl(k_norm_fwd<E, WF32, V, 2, true>, g, b, 0, st, a);
-    case 4: return launch_pdl(k_norm_fwd<E, WF32, V, 4, true>, g, b, 0, st, a);
-    default: break;
-  }
-  if constexpr (V == 1) {
-    if (p.nv == 8) return launch_pdl(k_norm_fwd<E, WF32, V, 8, true>, g, b, 0, st, a);
-    return launch_pdl(k_norm_fwd<E, WF32, V, 16, true>, g, b, 0, st, a);
-  }
-  return cudaErrorInvalidValue;
+  if (!p.block) return launch_pdl(k_norm_fwd<E, WF32, 1, false, VEC>, g, b, 0, st, a);
+  if (p.nv == 1) return launch_pdl(k_norm_fwd<E, WF32, 1, true, VEC>, g, b, 0, st, a);
+  if (p.nv == 2) return launch_pdl(k_norm_fwd<E, WF32, 2, true, VEC>, g, b, 0, st, a);
+  return launch_pdl(k_norm_fwd<E, WF32, 4, true, VEC>, g, b, 0, st, a);
 }
 
-template <typename E, bool WF32, int V, int NV, bool BLOCK>
+template <typename E, bool WF32, int NV, bool BLOCK, bool VEC>
 static cudaError_t bwd_launch(const NormArgs& a, const NormPlan& p, cudaStream_t st) {
   const dim3 g((unsigned)p.grid), b(p.threads);
   note_launch();
-  if (a.dgamma || a.dbeta) return launch_pdl(k_norm_bwd<E, WF32, V, NV, BLOCK, true>, g, b, 0, st, a);
-  return launch_pdl(k_norm_bwd<E, WF32, V, NV, BLOCK, false>, g, b, 0, st, a);
+  if (a.dgamma || a.dbeta) return launch_pdl(k_norm_bwd<E, WF32, NV, BLOCK, true, VEC>, g, b, 0, st, a);
+  return launch_pdl(k_norm_bwd<E, WF32, NV, BLOCK, false, VEC>, g, b, 0, st, a);
 }
 
-template <typename E, bool WF32, int V>
+template <typename E, bool WF32, bool VEC>
 static cudaError_t bwd_v(const NormArgs& a, cudaStream_t st) {
+  constexpr int V = 16 / (int)sizeof(typename E::raw);
   const bool want = a.dgamma || a.dbeta;
-  constexpr int kMaxNv = V == 1 ? 16 : 4;
-  const NormPlan p = norm_plan(((int64_t)a.H + V - 1) / V, a.T, kMaxNv, 512, want ? kNormMaxParts : 0,
-                               kNormBwdThreads);
+  const NormPlan p = norm_plan(((int64_t)a.H + V - 1) / V, a.T, 512, want ? kNormMaxParts : 0, kNormBwdThreads);
   cudaError_t e = cudaErrorNotSupported;
   int64_t parts = std::min<int64_t>(a.T, p.grid * (p.block ? 1 : p.threads / 32));
-  if constexpr (V > 1)
+  if constexpr (VEC)
     e = want ? ring_launch<E, WF32, true, true>(a, &parts, st) : ring_launch<E, WF32, false, true>(a, &parts, st);
   if (e != cudaErrorNotSupported) {
   } else if (p.longrow) {
@@ -683,16 +712,13 @@ static cudaError_t bwd_v(const NormArgs& a, cudaStream_t st) {
       e = launch_pdl(k_norm_dw_long<E>, dim3(cb, (unsigned)parts), dim3(256), 0, st, a);
     }
   } else if (!p.block) {
-    e = bwd_launch<E, WF32, V, 1, false>(a, p, st);
+    e = bwd_launch<E, WF32, 1, false, VEC>(a, p, st);
   } else if (p.nv == 1) {
-    e = bwd_launch<E, WF32, V, 1, true>(a, p, st);
+    e = bwd_launch<E, WF32, 1, true, VEC>(a, p, st);
   } else if (p.nv == 2) {
-    e = bwd_launch<E, WF32, V, 2, true>(a, p, st);
-  } else if (p.nv == 4) {
-    e = bwd_launch<E, WF32, V, 4, true>(a, p, st);
-  } else if constexpr (V == 1) {
-    if (p.nv == 8) e = bwd_launch<E, WF32, V, 8, true>(a, p, st);
-    else e = bwd_launch<E, WF32, V, 16, true>(a, p, st);
+    e = bwd_launch<E, WF32, 2, true, VEC>(a, p, st);
+  } else {
+    e = bwd_launch<E, WF32, 4, true, VEC>(a, p, st);
   }
   if (e != cudaSuccess || !want) return e;
   note_launch();
@@ -702,13 +728,9 @@ static cudaError_t bwd_v(const NormArgs& a, cudaStream_t st) {
 
 template <typename E, bool WF32, bool FWD>
 static cudaError_t by_vec(const NormArgs& a, cudaStream_t st) {
-  constexpr int V = 16 / (int)sizeof(typename E::raw);
-  if (vec_ok(a, sizeof(typename E::raw))) {
-    if constexpr (FWD) return fwd_v<E, WF32, V>(a, st);
-    else return bwd_v<E, WF32, V>(a, st);
-  }
-  if constexpr (FWD) return fwd_v<E, WF32, 1>(a, st);
-  else return bwd_v<E, WF32, 1>(a, st);
+  const bool vec = vec_ok(a, sizeof(typename E::raw));
+  if constexpr (FWD) return vec ? fwd_v<E, WF32, true>(a, st) : fwd_v<E, WF32, false>(a, st);
+  else return vec ? bwd_v<E, WF32, true>(a, st) : bwd_v<E, WF32, false>(a, st);
 }
 
 template <bool FWD>

@@ -55,6 +55,126 @@ __device__ __forceinline__ void store_pack(typename E::raw* dst, const Pack<E, V
   else *reinterpret_cast<uint4*>(dst) = *reinterpret_cast<const uint4*>(&p);
 }
 
+// ---- rows at any alignment ------------------------------------------------------
+// Sixteen (eight) bytes of a row that starts anywhere: the aligned units that
+// hold them, shifted together. A unit is read whole only where all of it lies
+// in the row's bytes [lo, hi); in the row's first and last one the elements
+// (ES bytes each) are read one by one, so nothing outside the row is touched.
+// Bytes outside the row are zeros.
+template <int ES, int N>
+__device__ __forceinline__ void load_unit(uint32_t (&w)[N / 4], const uint8_t* q, const uint8_t* lo, const uint8_t* hi) {
+  if (q >= lo && q + N <= hi) {
+    if constexpr (N == 16) {
+      const uint4 v = *reinterpret_cast<const uint4*>(q);
+      w[0] = v.x; w[1] = v.y; w[2] = v.z; w[3] = v.w;
+    } else {
+      const uint2 v = *reinterpret_cast<const uint2*>(q);
+      w[0] = v.x; w[1] = v.y;
+    }
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < N / 4; ++i) w[i] = 0u;
+#pragma unroll
+  for (int i = 0; i < N; i += ES) {
+    const uint8_t* p = q + i;
+    if (p >= lo && p < hi) {
+      if constexpr (ES == 4) w[i / 4] = *reinterpret_cast<const uint32_t*>(p);
+      else if constexpr (ES == 2) w[i / 4] |= (uint32_t)*reinterpret_cast<const uint16_t*>(p) << (8 * (i & 3));
+      else w[i / 4] |= (uint32_t)*p << (8 * (i & 3));
+    }
+  }
+}
+template <int ES, int N>
+__device__ __forceinline__ void load_any(uint32_t (&r)[N / 4], const void* at, const void* lo_, const void* hi_) {
+  const uint8_t *p = reinterpret_cast<const uint8_t*>(at), *lo = reinterpret_cast<const uint8_t*>(lo_),
+                *hi = reinterpret_cast<const uint8_t*>(hi_);
+  constexpr int W = N / 4;
+  const int off = (int)((uintptr_t)p & (N - 1));
+  uint32_t a[W], b[W];
+#pragma unroll
+  for (int i = 0; i < W; ++i) a[i] = b[i] = 0u;
+  if (p < hi) load_unit<ES, N>(a, p - off, lo, hi);
+  if (off && p - off + N < hi) load_unit<ES, N>(b, p - off + N, lo, hi);
+  uint32_t w[2 * W];
+#pragma unroll
+  for (int i = 0; i < W; ++i) {
+    w[i] = a[i];
+    w[W + i] = b[i];
+  }
+  if constexpr (W == 4) {
+    const bool two = off & 8;
+#pragma unroll
+    for (int i = 0; i < 6; ++i) w[i] = two ? w[i + 2] : w[i];
+  }
+  const bool one = off & 4;
+#pragma unroll
+  for (int i = 0; i <= W; ++i) w[i] = one && i + 1 < 2 * W ? w[i + 1] : w[i];
+  if constexpr (ES < 4) {
+    const uint32_t sh = (uint32_t)(off & 3) * 8;
+#pragma unroll
+    for (int i = 0; i < W; ++i) r[i] = __funnelshift_r(w[i], w[i + 1], sh);
+  } else {
+#pragma unroll
+    for (int i = 0; i < W; ++i) r[i] = w[i];
+  }
+}
+
+// Stores the first n of 16 / ES (ES 2, 4) elements at any element alignment.
+template <int ES>
+__device__ __forceinline__ void store_any(void* at, const uint32_t (&w)[4], int n) {
+  uint8_t* p = reinterpret_cast<uint8_t*>(at);
+  const int bytes = n * ES;
+  if (((uintptr_t)p & 15) == 0 && bytes >= 16) {
+    *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+  } else if (ES == 4 || ((uintptr_t)p & 3) == 0) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (bytes >= 4 * i + 4) *reinterpret_cast<uint32_t*>(p + 4 * i) = w[i];
+      else if (bytes >= 4 * i + 2) *reinterpret_cast<uint16_t*>(p + 4 * i) = (uint16_t)w[i];
+    }
+  } else {
+    if (bytes >= 2) *reinterpret_cast<uint16_t*>(p) = (uint16_t)w[0];
+#pragma unroll
+    for (int i = 0; i < 3; ++i) {
+      const uint32_t v = __funnelshift_r(w[i], w[i + 1], 16);
+      if (bytes >= 4 * i + 6) *reinterpret_cast<uint32_t*>(p + 4 * i + 2) = v;
+      else if (bytes >= 4 * i + 4) *reinterpret_cast<uint16_t*>(p + 4 * i + 2) = (uint16_t)v;
+    }
+    if (bytes >= 16) *reinterpret_cast<uint16_t*>(p + 14) = (uint16_t)(w[3] >> 16);
+  }
+}
+// Stores the first n of eight bytes at any address.
+__device__ __forceinline__ void store_bytes8(uint8_t* p, uint2 w, int n) {
+  if (n >= 8 && ((uintptr_t)p & 3) == 0) {
+    reinterpret_cast<uint32_t*>(p)[0] = w.x;
+    reinterpret_cast<uint32_t*>(p)[1] = w.y;
+  } else if (n >= 8) {
+    // an odd address: a byte, words or halves of the rest, and the last bytes
+    const int lead = 4 - (int)((uintptr_t)p & 3);      // 1, 2 or 3 bytes to the next word
+    uint32_t head = w.x;
+    if (lead & 1) {
+      *p = (uint8_t)head;
+      if (lead == 3) *reinterpret_cast<uint16_t*>(p + 1) = (uint16_t)(head >> 8);
+    } else {
+      *reinterpret_cast<uint16_t*>(p) = (uint16_t)head;
+    }
+    *reinterpret_cast<uint32_t*>(p + lead) = __funnelshift_r(w.x, w.y, 8 * lead);
+    const uint32_t rest = w.y >> (8 * lead);           // 4 - lead bytes, at a word's start
+    uint8_t* e = p + lead + 4;
+    if (lead == 3) {
+      *e = (uint8_t)rest;
+    } else {
+      *reinterpret_cast<uint16_t*>(e) = (uint16_t)rest;
+      if (lead == 1) e[2] = (uint8_t)(rest >> 16);
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (j < n) p[j] = (uint8_t)((j < 4 ? w.x : w.y) >> (8 * (j & 3)));
+  }
+}
+
 // Largest magnitude E4M3 holds, and the smallest scale of a 128-block: with
 // it an all-zero block, or one of fp32 subnormals, divides by a normal number.
 constexpr int kQBlock = 128;

@@ -17,30 +17,27 @@ namespace moe {
 
 constexpr int kQThreads = 256;
 
-// Eight consecutive elements c .. c + 7 of a row (zeros from n on).
+// Eight consecutive elements c .. c + 7 of a row of n (zeros from n on). VEC:
+// 16-byte aligned; otherwise rows at any alignment.
 template <typename E, bool VEC>
 __device__ __forceinline__ void load_run8(float (&v)[8], const typename E::raw* p, int c, int n) {
-  if constexpr (VEC) {
-    if (c < n) {
-      if constexpr (sizeof(typename E::raw) == 2) {
-        Pack<E, 8> k;
-        load_pack(k, p + c);
+  constexpr int kES = (int)sizeof(typename E::raw), kPer = 16 / kES;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = E::to(k.v[j]);
-      } else {
-        Pack<E, 4> k[2];
-        load_pack(k[0], p + c);
-        load_pack(k[1], p + c + 4);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = E::to(k[j >> 2].v[j & 3]);
+  for (int k = 0; k < 8 / kPer; ++k) {
+    uint32_t w[4] = {0u, 0u, 0u, 0u};
+    if constexpr (VEC) {
+      if (c + k * kPer < n) {
+        const uint4 u = *reinterpret_cast<const uint4*>(p + c + k * kPer);
+        w[0] = u.x; w[1] = u.y; w[2] = u.z; w[3] = u.w;
       }
     } else {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = 0.f;
+      load_any<kES, 16>(w, p + c + k * kPer, p, p + n);
     }
-  } else {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = c + j < n ? E::to(p[c + j]) : 0.f;
+    for (int j = 0; j < kPer; ++j) {
+      if constexpr (kES == 2) v[k * kPer + j] = E::to((uint16_t)(w[j >> 1] >> (16 * (j & 1))));
+      else v[k * kPer + j] = __uint_as_float(w[j]);
+    }
   }
 }
 
@@ -58,13 +55,9 @@ __device__ __forceinline__ float mag8(const float (&v)[8]) {
 }
 template <bool VEC>
 __device__ __forceinline__ void store_codes8(uint8_t* p, uint2 w, int c, int n) {
-  if constexpr (VEC) {
-    if (c < n) *reinterpret_cast<uint2*>(p + c) = w;
-  } else {
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-      if (c + j < n) p[c + j] = (uint8_t)((j < 4 ? w.x : w.y) >> (8 * (j & 3)));
-  }
+  if (c >= n) return;
+  if constexpr (VEC) *reinterpret_cast<uint2*>(p + c) = w;
+  else store_bytes8(p + c, w, n - c);
 }
 
 template <typename E, bool VEC>
@@ -77,14 +70,15 @@ __global__ void __launch_bounds__(kQThreads) k_quant128_rows(QuantRowsArgs a) {
     const int64_t it = it0 + (hw & 1);
     const bool live = it < items;
     const int64_t row = live ? it / nb : 0;
-    const int b = live ? (int)(it - row * nb) : 0, n = live ? min(kQBlock, a.C - b * kQBlock) : 0;
+    const int b = live ? (int)(it - row * nb) : 0;
     float v[8];
-    load_run8<E, VEC>(v, reinterpret_cast<const typename E::raw*>(a.x) + row * a.ldx + b * kQBlock, l * 8, n);
+    const int c = b * kQBlock + l * 8;
+    load_run8<E, VEC>(v, reinterpret_cast<const typename E::raw*>(a.x) + row * a.ldx, c, live ? a.C : 0);
     float am = mag8(v);
 #pragma unroll
     for (int o = 8; o > 0; o >>= 1) am = fmaxf(am, __shfl_xor_sync(kFull, am, o));
     const float s = block_scale(am);
-    store_codes8<VEC>(a.q + row * a.ldq + b * kQBlock, codes8(v, 1.0f / s), l * 8, n);
+    if (live) store_codes8<VEC>(a.q + row * a.ldq, codes8(v, 1.0f / s), c, a.C);
     if (live && l == 0) a.s[row * a.lds + b] = s;
   }
 }
@@ -105,13 +99,13 @@ __global__ void __launch_bounds__(kQThreads) k_quant128_weights(QuantWeightsArgs
     const int64_t g = blk / ((int64_t)nb * kb);
     const int bi = (int)(blk - g * nb * kb), n0 = bi / kb * kQBlock, k0 = bi % kb * kQBlock;
     const int nn = min(kQBlock, a.N - n0), kn = min(kQBlock, a.K - k0);
-    const typename E::raw* w = reinterpret_cast<const typename E::raw*>(a.w) + g * a.wg + (int64_t)n0 * a.ldw + k0;
+    const typename E::raw* w = reinterpret_cast<const typename E::raw*>(a.w) + g * a.wg + (int64_t)n0 * a.ldw;
     float v[8][8];
     float am = 0.f;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const int r = y + 16 * i;
-      load_run8<E, VEC>(v[i], w + (int64_t)min(r, nn - 1) * a.ldw, x * 8, r < nn ? kn : 0);
+      load_run8<E, VEC>(v[i], w + (int64_t)min(r, nn - 1) * a.ldw, k0 + x * 8, r < nn ? a.K : 0);
     }
 #pragma unroll
     for (int i = 0; i < 8; ++i) am = fmaxf(am, mag8(v[i]));
