@@ -112,7 +112,7 @@ __global__ void __launch_bounds__(kGThreads, 1) k_gemm16(const GArgs g, const __
   __syncthreads();
   tc::fence_after_sync();
   const uint32_t tmem = *tmem_slot;
-  const int64_t U = (int64_t)uoff[m.G] * g.n_tiles * m.S;
+  const int U = uoff[m.G] * g.n_tiles * m.S;
 
   if (warp == 0 || warp == 2) {
     // ---------------- copies: warp 0 B, warp 2 A ----------------
@@ -123,7 +123,7 @@ __global__ void __launch_bounds__(kGThreads, 1) k_gemm16(const GArgs g, const __
         for (int i = 0; i < (kWg ? 1 : 4); ++i) tc::prefetch_tmap(&maps.a[i]);
       uint32_t it = 0;
       bool ok = true;
-      for (int64_t u = blockIdx.x; ok && u < U; u += gridDim.x) {
+      for (int u = blockIdx.x; ok && u < U; u += gridDim.x) {
         GUnit w;
         g_unit<kWg, BN, kGK>(m, g.n_tiles, off, uoff, u, w);
         const int ai = g_a_box(w.rows);
@@ -166,7 +166,7 @@ __global__ void __launch_bounds__(kGThreads, 1) k_gemm16(const GArgs g, const __
     const uint32_t idesc = tc::idesc_16bit(kGM, BN, m.dtype == MOE_DT_BF16, kWg, MODE != kRowsNT);
     uint32_t it = 0, tcount = 0;
     bool ok = true;
-    for (int64_t u = blockIdx.x; ok && u < U; u += gridDim.x, ++tcount) {
+    for (int u = blockIdx.x; ok && u < U; u += gridDim.x, ++tcount) {
       GUnit w;
       g_unit<kWg, BN, kGK>(m, g.n_tiles, off, uoff, u, w);
       const int d = tcount & 1;
@@ -220,22 +220,7 @@ __global__ void __launch_bounds__(kGThreads, 1) k_gemm16(const GArgs g, const __
     __syncwarp();
   } else if (warp == 3) {
     // ---------------- rows outside every group ----------------
-    if (!kWg) {
-      const int esize = m.out_dtype == MOE_DT_F32 ? 4 : 2;
-      const int lo = off[0], hi = off[m.G];
-      for (int64_t r = blockIdx.x; r < m.R - (int64_t)(hi - lo); r += gridDim.x) {
-        const int64_t row = r < lo ? r : r - lo + hi;
-        if (m.S > 1) {
-          for (int s = 0; s < m.S; ++s)
-            for (int64_t i = lane; i < m.N; i += 32) m.part[((int64_t)s * m.R + row) * m.N + i] = 0.f;
-        } else {
-          for (int64_t i = lane; i < m.N; i += 32) {
-            if (esize == 4) reinterpret_cast<float*>(m.out)[row * m.ldo + i] = 0.f;
-            else reinterpret_cast<uint16_t*>(m.out)[row * m.ldo + i] = 0;
-          }
-        }
-      }
-    }
+    if (!kWg) clear_rows_outside(m, off, lane);
   } else {
     // ---------------- epilogue ----------------
     const int wg = (warp - 4) >> 2, q = warp & 3;
@@ -250,7 +235,7 @@ __global__ void __launch_bounds__(kGThreads, 1) k_gemm16(const GArgs g, const __
     const bool vec = ((uintptr_t)obase & 15) == 0 && (ld * esize) % 16 == 0 && (og * esize) % 16 == 0 &&
                      (m.S == 1 || (os * 4) % 16 == 0);
     uint32_t tcount = 0, mine = 0;
-    for (int64_t u = blockIdx.x; u < U; u += gridDim.x, ++tcount) {
+    for (int u = blockIdx.x; u < U; u += gridDim.x, ++tcount) {
       if ((int)(tcount & 1) != wg) continue;
       GUnit w;
       g_unit<kWg, BN, kGK>(m, g.n_tiles, off, uoff, u, w);
@@ -269,7 +254,7 @@ __global__ void __launch_bounds__(kGThreads, 1) k_gemm16(const GArgs g, const __
 #pragma unroll
           for (int i = 0; i < 32; ++i) v[i] = 0u;       // no rows to sum over
         }
-        if (r < w.rows) store32(obase + (at + w.n0 + c0) * esize, v, cols - w.n0 - c0, dt, vec);
+        if (r < w.rows) store_cols(obase + (at + w.n0 + c0) * esize, v, cols - w.n0 - c0, dt, vec);
         __syncwarp();
       }
       tc::fence_before_sync();
@@ -420,6 +405,7 @@ static cudaError_t launch_g(GArgs g, cudaStream_t st) {
     }
     g.n_tiles = (m.N + BN - 1) / BN;
   }
+  if (!units_fit(m, kWg ? (int64_t)m.G * g.m_tiles : m.R / kGM, g.n_tiles)) return cudaErrorInvalidValue;
   static std::atomic<bool> done[kMaxDevices] = {};
   cudaError_t e = set_smem_once((const void*)k_gemm16<MODE, BN>, C::kSmem, done);
   if (e != cudaSuccess) return e;

@@ -8,16 +8,16 @@
 // in one of 512 / BN tensor-memory slots, and the epilogue threads add it,
 // times the block's scale, to the fp32 sums of the tile that they hold in
 // registers. A thread's columns share one weight scale, so a block costs one
-// multiply per row and one fused multiply-add (two to an instruction) per
-// element, while the next blocks' MMAs run.
+// multiply per row and one fused multiply-add per element, while the next
+// blocks' MMAs run.
 //
 // Bound: the tensor pipe at training sizes (a 128 x 256 x 128 block is 512
 // cycles of MMA, its additions 256 issue slots a scheduler at most), the
 // weights' bytes at decode sizes.
 // Tiles, copies and edges as in gemm16.cu. Roles: warp 0 copies W, warp 2
 // copies x, warp 1 issues MMAs, warp 3 clears rows outside every group, warps
-// 4-11 add: warp quarter q of tensor memory, half h of the columns. They
-// take registers from the first four warps (setmaxnreg).
+// 4-19 add: warp quarter q of tensor memory, quarter h of the columns (four
+// warps a scheduler: with two, the reads' latency showed). They take registers from the first four warps (setmaxnreg).
 // Every wait is bounded, as in gemm16.cu.
 #include "groups.cuh"
 #include "tc.cuh"
@@ -25,20 +25,26 @@
 namespace moe {
 
 constexpr int kFK = kQBlock;              // reduction a stage: one scale block, one 128-byte swizzle row
-constexpr int kFThreads = 384;
+constexpr int kFThreads = 640;
 constexpr int kFABytes = kGM * kFK;
 constexpr int kFTables = 2 * 4 * (kMmMaxGroups + 1);
-// Registers a thread: at launch, then of warps 0-3 and of warps 4-11. The
+// Registers a thread: at launch, then of warps 0-3 and of warps 4-19. The
 // shares sum to at most the launch's (checked against the built kernel
 // before its first launch).
-constexpr int kFRegs = 168, kFRegsLow = 88, kFRegsHigh = 208;
-static_assert(128 * kFRegsLow + 256 * kFRegsHigh <= kFThreads * kFRegs, "register shares");
+constexpr int kFRegs = 96, kFRegsLow = 64, kFRegsHigh = 104;
+static_assert(128 * kFRegsLow + 512 * kFRegsHigh <= kFThreads * kFRegs, "register shares");
 
 template <int BN>
 struct FCfg {
   static constexpr int kBBytes = BN * kFK;
   static constexpr int kStages = BN == 256 ? 4 : BN == 128 ? 6 : 8;
-  static constexpr int kSlots = 512 / BN;
+  // Tensor memory holds 512 / BN blocks' accumulators. A 256-wide tile runs as
+  // two halves with an MMA issuer and slots of their own: the round trip of a
+  // slot (MMA, commit, additions, release) is longer than the MMAs that two
+  // slots queue, and half the columns halve its share of it.
+  static constexpr int kHalves = BN == 256 ? 2 : 1;
+  static constexpr int kHN = BN / kHalves;
+  static constexpr int kSlots = 512 / BN;       // of each half
   static constexpr int kSmem = 1024 + kStages * (kFABytes + kBBytes) + 1024 + kFTables;
   static_assert(kSmem <= 227 * 1024, "shared memory budget");
 };
@@ -51,13 +57,6 @@ struct FArgs {
   int n_tiles;
 };
 
-// acc (two fp32) += {lo, hi} * s (two equal fp32)
-__device__ __forceinline__ void fma2(uint64_t& acc, uint32_t lo, uint32_t hi, uint64_t s) {
-  asm("{\n .reg .b64 t;\n mov.b64 t, {%1, %2};\n fma.rn.f32x2 %0, t, %3, %0;\n}"
-      : "+l"(acc)
-      : "r"(lo), "r"(hi), "l"(s));
-}
-
 template <int BN>
 __global__ void __launch_bounds__(kFThreads, 1) k_gemm_fp8(const FArgs g, const __grid_constant__ FMaps maps) {
   using C = FCfg<BN>;
@@ -68,9 +67,9 @@ __global__ void __launch_bounds__(kFThreads, 1) k_gemm_fp8(const FArgs g, const 
   uint64_t* full = reinterpret_cast<uint64_t*>(sb + C::kStages * C::kBBytes);
   uint64_t* empty = full + C::kStages;
   uint64_t* tfull = empty + C::kStages;
-  uint64_t* tempty = tfull + C::kSlots;
-  uint64_t* drain = tempty + C::kSlots;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+  uint64_t* tempty = tfull + C::kHalves * C::kSlots;      // of half h: [h * kSlots, ...)
+  uint64_t* drain = tempty + C::kHalves * C::kSlots;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + C::kHalves);
   volatile int* abort = reinterpret_cast<volatile int*>(tmem_slot + 1);
   int* tmp = reinterpret_cast<int*>(tmem_slot + 2);
   int32_t* off = reinterpret_cast<int32_t*>(reinterpret_cast<uint8_t*>(full) + 1024);
@@ -82,13 +81,13 @@ __global__ void __launch_bounds__(kFThreads, 1) k_gemm_fp8(const FArgs g, const 
   if (threadIdx.x == 0) {
     for (int i = 0; i < C::kStages; ++i) {
       tc::mbar_init(&full[i], 2);
-      tc::mbar_init(&empty[i], 1);
+      tc::mbar_init(&empty[i], C::kHalves);
     }
-    for (int i = 0; i < C::kSlots; ++i) {
+    for (int i = 0; i < C::kHalves * C::kSlots; ++i) {
       tc::mbar_init(&tfull[i], 1);
-      tc::mbar_init(&tempty[i], 8);     // one per adding warp
+      tc::mbar_init(&tempty[i], 16 / C::kHalves);     // one per adding warp
     }
-    tc::mbar_init(drain, 1);
+    for (int i = 0; i < C::kHalves; ++i) tc::mbar_init(&drain[i], 1);
     *abort = 0;
     tc::fence_mbar_init();
   }
@@ -98,7 +97,7 @@ __global__ void __launch_bounds__(kFThreads, 1) k_gemm_fp8(const FArgs g, const 
   __syncthreads();
   tc::fence_after_sync();
   const uint32_t tmem = *tmem_slot;
-  const int64_t U = (int64_t)uoff[m.G] * g.n_tiles * m.S;
+  const int U = uoff[m.G] * g.n_tiles * m.S;
 
   if (warp < 4) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kFRegsLow));
@@ -111,7 +110,7 @@ __global__ void __launch_bounds__(kFThreads, 1) k_gemm_fp8(const FArgs g, const 
           for (int i = 0; i < 4; ++i) tc::prefetch_tmap(&maps.a[i]);
         uint32_t it = 0;
         bool ok = true;
-        for (int64_t u = blockIdx.x; ok && u < U; u += gridDim.x) {
+        for (int u = blockIdx.x; ok && u < U; u += gridDim.x) {
           GUnit w;
           g_unit<false, BN, kFK>(m, g.n_tiles, off, uoff, u, w);
           const int ai = g_a_box(w.rows);
@@ -136,57 +135,48 @@ __global__ void __launch_bounds__(kFThreads, 1) k_gemm_fp8(const FArgs g, const 
           }
         }
       }
-    } else if (warp == 1) {
-      // ---------------- MMAs ----------------
-      if (lane == 0) {
+    } else {
+      if (warp == 3) clear_rows_outside(m, off, lane);
+      // ---------------- MMAs: warp 1 the first half, warp 3 the second ----------------
+      const int h = warp >> 1;
+      if (lane == 0 && h < C::kHalves) {
         // kind::f8f6f4: E4M3 is format 0 of both operands; fp32 accumulator
-        constexpr uint32_t idesc = tc::idesc_f16_f32(kGM, BN);
+        constexpr uint32_t idesc = tc::idesc_f16_f32(kGM, C::kHN);
+        uint64_t* hfull = tfull + h * C::kSlots;
+        uint64_t* hempty = tempty + h * C::kSlots;
         uint32_t it = 0;
         bool ok = true;
-        for (int64_t u = blockIdx.x; ok && u < U; u += gridDim.x) {
+        for (int u = blockIdx.x; ok && u < U; u += gridDim.x) {
           GUnit w;
           g_unit<false, BN, kFK>(m, g.n_tiles, off, uoff, u, w);
           for (int kb = w.k0; kb < w.k1; ++kb, ++it) {
             const int slot = it % C::kStages, ts = it % C::kSlots;
-            if (!tc::mbar_wait(&tempty[ts], ((it / C::kSlots) & 1) ^ 1, abort)) { ok = false; break; }
+            if (!tc::mbar_wait(&hempty[ts], ((it / C::kSlots) & 1) ^ 1, abort)) { ok = false; break; }
             if (!tc::mbar_wait(&full[slot], (it / C::kStages) & 1, abort)) { ok = false; break; }
             tc::fence_after_sync();
             const uint64_t ad = tc::smem_desc_sw128(tc::smem_u32(sa + slot * kFABytes));
-            const uint64_t bd = tc::smem_desc_sw128(tc::smem_u32(sb + slot * C::kBBytes));
+            const uint64_t bd = tc::smem_desc_sw128(tc::smem_u32(sb + slot * C::kBBytes + h * C::kHN * kFK));
 #pragma unroll
             for (int j = 0; j < 4; ++j)     // K = 32: 32 bytes along the rows; past K both read as zero
-              tc::mma_f8_ss(tmem + ts * BN, ad + 2 * j, bd + 2 * j, idesc, j > 0 ? 1u : 0u);
+              tc::mma_f8_ss(tmem + ts * BN + h * C::kHN, ad + 2 * j, bd + 2 * j, idesc, j > 0 ? 1u : 0u);
             tc::mma_commit(&empty[slot]);
-            tc::mma_commit(&tfull[ts]);
+            tc::mma_commit(&hfull[ts]);
           }
         }
-        tc::mma_commit(drain);
+        tc::mma_commit(&drain[h]);
         volatile int never = 0;
-        tc::mbar_wait(drain, 0, &never, 400000000ll);
+        tc::mbar_wait(&drain[h], 0, &never, 400000000ll);
       }
       __syncwarp();
-    } else {
-      // ---------------- rows outside every group ----------------
-      const int lo = off[0], hi = off[m.G];
-      for (int64_t r = blockIdx.x; r < m.R - (int64_t)(hi - lo); r += gridDim.x) {
-        const int64_t row = r < lo ? r : r - lo + hi;
-        if (m.S > 1) {
-          for (int s = 0; s < m.S; ++s)
-            for (int64_t i = lane; i < m.N; i += 32) m.part[((int64_t)s * m.R + row) * m.N + i] = 0.f;
-        } else {
-          for (int64_t i = lane; i < m.N; i += 32) {
-            if (m.out_dtype == MOE_DT_F32) reinterpret_cast<float*>(m.out)[row * m.ldo + i] = 0.f;
-            else reinterpret_cast<uint16_t*>(m.out)[row * m.ldo + i] = 0;
-          }
-        }
-      }
     }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kFRegsHigh));
     // ---------------- sums of the blocks ----------------
-    constexpr int kCols = BN / 2, kChunks = kCols / 32;
+    constexpr int kCols = BN / 4, kChunks = kCols / 16;
     const int h = (warp - 4) >> 2, q = warp & 3;
     const uint32_t lanes = tmem + ((uint32_t)(q * 32) << 16) + h * kCols;
+    uint64_t* hfull = tfull + h * C::kHalves / 4 * C::kSlots;
+    uint64_t* hempty = tempty + h * C::kHalves / 4 * C::kSlots;
     const int KB = (m.K + kFK - 1) / kFK, NB = (m.N + kQBlock - 1) / kQBlock;
     const int dt = m.S > 1 ? MOE_DT_F32 : m.out_dtype;
     const int esize = dt == MOE_DT_F32 ? 4 : 2;
@@ -195,7 +185,7 @@ __global__ void __launch_bounds__(kFThreads, 1) k_gemm_fp8(const FArgs g, const 
     const bool vec = ((uintptr_t)obase & 15) == 0 && (ld * esize) % 16 == 0 && (m.S == 1 || (os * 4) % 16 == 0);
     uint32_t it = 0;
     bool ok = true;
-    for (int64_t u = blockIdx.x; ok && u < U; u += gridDim.x) {
+    for (int u = blockIdx.x; ok && u < U; u += gridDim.x) {
       GUnit w;
       g_unit<false, BN, kFK>(m, g.n_tiles, off, uoff, u, w);
       const int r = q * 32 + lane;
@@ -203,54 +193,66 @@ __global__ void __launch_bounds__(kFThreads, 1) k_gemm_fp8(const FArgs g, const 
       const float* xs = m.sa + (int64_t)(w.row0 + (live ? r : 0)) * m.ldsa;
       const int nb = min((w.n0 + h * kCols) / kQBlock, NB - 1);     // past N: nothing is stored
       const float* ws = m.sb + ((int64_t)w.e * NB + nb) * KB;
-      uint64_t acc[kCols / 2];
+      float acc[kCols];
 #pragma unroll
-      for (int i = 0; i < kCols / 2; ++i) acc[i] = 0;
-      // the scales of two blocks ahead are on their way
-      float s0 = 0.f, s1 = 0.f, t0 = 0.f, t1 = 0.f;
-      if (w.k0 < w.k1) { s0 = xs[w.k0]; t0 = ws[w.k0]; }
-      if (w.k0 + 1 < w.k1) { s1 = xs[w.k0 + 1]; t1 = ws[w.k0 + 1]; }
-      for (int kb = w.k0; kb < w.k1; ++kb, ++it) {
-        const int ts = it % C::kSlots;
-        float s2 = 0.f, t2 = 0.f;
-        if (kb + 2 < w.k1) { s2 = xs[kb + 2]; t2 = ws[kb + 2]; }
-        const float sc = s0 * t0;
-        uint64_t sc2;
-        asm("mov.b64 %0, {%1, %1};" : "=l"(sc2) : "f"(sc));
-        ok = __all_sync(kFull, tc::mbar_wait(&tfull[ts], (it / C::kSlots) & 1, abort));
-        if (!ok) break;
-        tc::fence_after_sync();
-        const uint32_t at = lanes + ts * BN;
-        // chunk c + 1 is read while chunk c is added
-        uint32_t v[2][32];
-        tc::tmem_ld32(at, v[0]);
+      for (int i = 0; i < kCols; ++i) acc[i] = 0.f;
+      // The scales of the next four blocks are on their way, each in registers
+      // of its own: a copy from register to register would wait for the load.
+      float s[4], t[4];
 #pragma unroll
-        for (int c = 0; c < kChunks; ++c) {
-          tc::tmem_wait_ld();
-          if (c + 1 < kChunks) {
-            tc::tmem_ld32(at + 32 * (c + 1), v[(c + 1) & 1]);
-          } else {
-            tc::fence_before_sync();
-            __syncwarp();
-            if (lane == 0) tc::mbar_arrive(&tempty[ts]);
+      for (int j = 0; j < 4; ++j) {
+        const bool in = w.k0 + j < w.k1;
+        s[j] = in ? xs[w.k0 + j] : 0.f;
+        t[j] = in ? ws[w.k0 + j] : 0.f;
+      }
+      for (int kb0 = w.k0; kb0 < w.k1; kb0 += 4) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int kb = kb0 + j;
+          if (kb < w.k1 && ok) {
+            const int ts = it % C::kSlots;
+            const float sc = s[j] * t[j];
+            if (kb + 4 < w.k1) {
+              s[j] = xs[kb + 4];
+              t[j] = ws[kb + 4];
+            }
+            ok = __all_sync(kFull, tc::mbar_wait(&hfull[ts], (it / C::kSlots) & 1, abort));
+            if (ok) {
+              tc::fence_after_sync();
+              const uint32_t at = lanes + ts * BN;
+              // chunk c + 1 is read while chunk c is added
+              uint32_t v[2][16];
+              tc::tmem_ld16(at, v[0]);
+#pragma unroll
+              for (int c = 0; c < kChunks; ++c) {
+                tc::tmem_wait_ld();
+                if (c + 1 < kChunks) {
+                  tc::tmem_ld16(at + 16 * (c + 1), v[(c + 1) & 1]);
+                } else {
+                  tc::fence_before_sync();
+                  __syncwarp();
+                  if (lane == 0) tc::mbar_arrive(&hempty[ts]);
+                }
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                  acc[c * 16 + i] = fmaf(__uint_as_float(v[c & 1][i]), sc, acc[c * 16 + i]);
+              }
+              ++it;
+            }
           }
-#pragma unroll
-          for (int i = 0; i < 16; ++i) fma2(acc[c * 16 + i], v[c & 1][2 * i], v[c & 1][2 * i + 1], sc2);
         }
-        s0 = s1; t0 = t1; s1 = s2; t1 = t2;
       }
       if (!ok) break;
       if (live) {
         const int64_t row = (int64_t)(w.row0 + r) * ld + w.piece * (m.S > 1 ? os : 0);
 #pragma unroll
         for (int c = 0; c < kChunks; ++c) {
-          const int col = w.n0 + h * kCols + 32 * c;
+          const int col = w.n0 + h * kCols + 16 * c;
           if (col < m.N) {
-            uint32_t v[32];
+            uint32_t v[16];
 #pragma unroll
-            for (int i = 0; i < 16; ++i)
-              asm("mov.b64 {%0, %1}, %2;" : "=r"(v[2 * i]), "=r"(v[2 * i + 1]) : "l"(acc[c * 16 + i]));
-            store32(obase + (row + col) * esize, v, m.N - col, dt, vec);
+            for (int i = 0; i < 16; ++i) v[i] = __float_as_uint(acc[c * 16 + i]);
+            store_cols(obase + (row + col) * esize, v, m.N - col, dt, vec);
           }
         }
       }
@@ -291,7 +293,8 @@ static cudaError_t launch_f(FArgs g, cudaStream_t st) {
     if (e != cudaSuccess) return e;
     regs.store(at.numRegs, std::memory_order_release);
   }
-  if (128 * kFRegsLow + 256 * kFRegsHigh > kFThreads * regs.load()) return cudaErrorInvalidConfiguration;
+  if (128 * kFRegsLow + 512 * kFRegsHigh > kFThreads * regs.load()) return cudaErrorInvalidConfiguration;
+  if (!units_fit(m, m.R / kGM, g.n_tiles)) return cudaErrorInvalidValue;
   static std::atomic<bool> done[kMaxDevices] = {};
   cudaError_t e = set_smem_once((const void*)k_gemm_fp8<BN>, C::kSmem, done);
   if (e != cudaSuccess) return e;

@@ -111,13 +111,13 @@ struct GUnit {
 // reduction), pieces innermost, then column tiles. WG: weight gradient (M =
 // N features, the reduction is the group's rows); BK: the stage's depth.
 template <bool WG, int BN, int BK>
-__device__ __forceinline__ void g_unit(const MmArgs& m, int n_tiles, const int32_t* off, const int32_t* uoff, int64_t u,
+__device__ __forceinline__ void g_unit(const MmArgs& m, int n_tiles, const int32_t* off, const int32_t* uoff, int u,
                                        GUnit& w) {
   const int S = m.S;
-  const int64_t t = u / S;
-  w.piece = (int)(u - t * S);
-  const int ui = (int)(t / n_tiles);
-  w.n0 = (int)(t - (int64_t)ui * n_tiles) * BN;
+  const int t = u / S;
+  w.piece = u - t * S;
+  const int ui = t / n_tiles;
+  w.n0 = (t - ui * n_tiles) * BN;
   w.e = group_of_unit(uoff, m.G, ui);
   const int mi = ui - uoff[w.e], cnt = off[w.e + 1] - off[w.e];
   if (WG) {
@@ -131,48 +131,68 @@ __device__ __forceinline__ void g_unit(const MmArgs& m, int n_tiles, const int32
   }
   const int nk = (w.red + BK - 1) / BK;
   w.k0 = (int)((int64_t)nk * w.piece / S);
-  w.k1 = (int)((int64_t)nk * (w.piece + 1) / S);
+  w.k1 = S == 1 ? nk : (int)((int64_t)nk * (w.piece + 1) / S);
+}
+// The kernels count units in 32 bits; more than that many would write more
+// than any GPU's memory.
+inline bool units_fit(const MmArgs& m, int64_t row_tiles, int64_t n_tiles) {
+  return (row_tiles + m.G) * n_tiles * m.S < (1ll << 31) - 4096;
 }
 
 // A copy of a K-major tile covers 16 << i rows, the fewest that hold its real
 // ones; the MMA's other rows are an earlier stage's bytes and are not stored.
 __device__ __forceinline__ int g_a_box(int rows) { return rows <= 16 ? 0 : rows <= 32 ? 1 : rows <= 64 ? 2 : 3; }
 
-// 32 columns of a row from fp32 bits: n valid ones at p (esize 4: fp32, else
-// bf16 / f16); vec: 16-byte stores are aligned.
-__device__ __forceinline__ void store32(void* p, const uint32_t (&v)[32], int n, int out_dtype, bool vec) {
+// C columns (a multiple of 8) of a row from fp32 bits: n valid ones at p, as
+// out_dtype; vec: 16-byte stores are aligned.
+template <int C>
+__device__ __forceinline__ void store_cols(void* p, const uint32_t (&v)[C], int n, int out_dtype, bool vec) {
   if (out_dtype == MOE_DT_F32) {
     uint32_t* d = reinterpret_cast<uint32_t*>(p);
-    if (vec && n >= 32) {
+    if (vec && n >= C) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
+      for (int i = 0; i < C / 4; ++i)
         reinterpret_cast<uint4*>(d)[i] = make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
     } else {
 #pragma unroll
-      for (int i = 0; i < 32; ++i)
+      for (int i = 0; i < C; ++i)
         if (i < n) d[i] = v[i];
     }
     return;
   }
-  uint32_t pk[16];
-  if (out_dtype == MOE_DT_F16) {
+  uint32_t pk[C / 2];
 #pragma unroll
-    for (int i = 0; i < 16; ++i)
-      pk[i] = F16::from2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]));
-  } else {
-#pragma unroll
-    for (int i = 0; i < 16; ++i)
-      pk[i] = Bf16::from2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]));
+  for (int i = 0; i < C / 2; ++i) {
+    const float a = __uint_as_float(v[2 * i]), b = __uint_as_float(v[2 * i + 1]);
+    pk[i] = out_dtype == MOE_DT_F16 ? F16::from2(a, b) : Bf16::from2(a, b);
   }
-  if (vec && n >= 32) {
+  if (vec && n >= C) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < C / 8; ++i)
       reinterpret_cast<uint4*>(p)[i] = make_uint4(pk[4 * i], pk[4 * i + 1], pk[4 * i + 2], pk[4 * i + 3]);
   } else {
     uint16_t* d = reinterpret_cast<uint16_t*>(p);
 #pragma unroll
-    for (int i = 0; i < 32; ++i)
+    for (int i = 0; i < C; ++i)
       if (i < n) d[i] = (uint16_t)(pk[i >> 1] >> (16 * (i & 1)));
+  }
+}
+
+// Rows outside every group become zeros (their partial sums, where the product
+// is split). One warp of each CTA.
+__device__ __forceinline__ void clear_rows_outside(const MmArgs& m, const int32_t* off, int lane) {
+  const int lo = off[0], hi = off[m.G];
+  for (int64_t r = blockIdx.x; r < m.R - (int64_t)(hi - lo); r += gridDim.x) {
+    const int64_t row = r < lo ? r : r - lo + hi;
+    if (m.S > 1) {
+      for (int s = 0; s < m.S; ++s)
+        for (int64_t i = lane; i < m.N; i += 32) m.part[((int64_t)s * m.R + row) * m.N + i] = 0.f;
+    } else {
+      for (int64_t i = lane; i < m.N; i += 32) {
+        if (m.out_dtype == MOE_DT_F32) reinterpret_cast<float*>(m.out)[row * m.ldo + i] = 0.f;
+        else reinterpret_cast<uint16_t*>(m.out)[row * m.ldo + i] = 0;
+      }
+    }
   }
 }
 
