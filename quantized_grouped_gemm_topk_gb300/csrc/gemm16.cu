@@ -1,29 +1,38 @@
 // Products grouped by expert with ragged sizes, bf16 or f16, on the
 // 5th-generation tensor cores (tcgen05.mma kind::f16, operands in shared
-// memory, fp32 accumulators in tensor memory).
+// memory, fp32 accumulators in tensor memory). D[M][N] of a tile is
 //
-//   kRowsNT   out[r] = W_e x[r]      A = x rows, B = W rows; both K-major
-//   kRowsNN   out[r] = W_e^T x[r]    B has its N axis contiguous (the
+//   kRowsNT   out^T = W_e x^T    M features of W (K-major), N token rows of x
+//   kRowsNN   out^T = W_e^T x^T  the same with W's feature axis contiguous (the
 //             gradient of the rows with the forward's weights, no transpose)
-//   kWgrad    dW_e = sum over group rows dy[r]^T x[r]; both operands have
-//             their M / N axis contiguous and the reduction runs over rows
+//   kWgradMN  dW_e = dy^T x      M features of dy, N features of x, both
+//             contiguous; the reduction runs over the group's rows
 //
-// Bound: the tensor pipe at training sizes (2 R N K FLOPs), the weights'
-// bytes at decode sizes. Tiles: 128 rows x BN columns (256; 128 or 64 where
-// larger tiles would leave SMs without work) x 64 of the reduction a stage,
-// in a ring that fills the shared memory, filled by tensor copies with the
-// 128-byte swizzle and drained by four MMAs of K = 16. Ragged edges cost no
-// branch in the main loop: rows of a tile that belong to the next group only
-// reach accumulator rows that are not stored; columns and the K tail read as
-// zeros (the tensor maps end at N and K); the weight gradient's last rows are
-// cleared in shared memory, both operands (a NaN of the next group times zero
-// would be NaN).
+// The weights are the MMA's M side, so the ragged side is N: an instruction's
+// N is the tile's real rows rounded up to 32, and a group of 300 rows costs
+// 300, not the next multiple of 128 or 256; a decode step of a few rows costs
+// little next to its weights' bytes.
 //
-// Roles (one CTA per SM, persistent over the units): warp 0 copies B, warp 2
+// Bound: the tensor pipe at training sizes, the weights' bytes at decode
+// sizes. What an SM can take in from L2 (64 bytes a cycle, measured: 48 KB a
+// stage took 745 cycles whatever else was changed) is less than a 128 x 256
+// tile on one SM wants (48 KB per 512 cycles of MMA). So where there is work
+// for it a pair of SMs (cta_group::2) multiplies a 256 x 256 tile together:
+// 32 KB a stage for each. Tiles of one SM (128 x up to 256) serve few tiles
+// and few rows. Stages of 64 of the reduction in a ring that fills the shared
+// memory, filled by tensor copies with the 128-byte swizzle. Ragged edges cost
+// no branch in the main loop: rows of a tile that belong to the next group
+// only reach accumulator columns that are not stored; columns and the K tail
+// read as zeros (the tensor maps end at N and K); the weight gradient's last
+// rows are cleared in shared memory, both operands (a NaN of the next group
+// times zero would be NaN).
+//
+// Roles (a CTA an SM, persistent over the units): warp 0 copies B, warp 2
 // copies A (two issuers: a copy costs its thread some hundred cycles), warp 1
-// issues the MMAs, warps 4-7 and 8-11 are epilogues that alternate between
-// tiles and the two accumulators, so a tile's stores overlap the next one's
-// MMAs; warp 3 clears rows outside every group.
+// issues the MMAs (in a pair the first CTA's, whose barriers all copies of the
+// pair report to), warps 4-7 and 8-11 are epilogues
+// that alternate between tiles and the two accumulators, so a tile's stores
+// overlap the next one's MMAs; warp 3 clears rows outside every group.
 // Every wait is bounded; a CTA whose wait runs out sets MOE_DEV_TIMEOUT, waits
 // for its copies and MMAs in flight, frees tensor memory and returns.
 #include "groups.cuh"
@@ -34,52 +43,149 @@ namespace moe {
 enum { kRowsNT = 0, kRowsNN = 1, kWgradMN = 2 };
 
 constexpr int kGK = 64;               // reduction a stage: one 128-byte swizzle row
+constexpr int kGN = 256;              // widest tile
 constexpr int kGThreads = 384;
 constexpr int kGChunk = 64 * kGK * 2; // bytes of 64 M / N elements of an MN-contiguous stage
 constexpr int kGABytes = kGM * kGK * 2;
 constexpr int kGTables = 2 * 4 * (kMmMaxGroups + 1);
 
-template <int BN>
+template <int CG>
 struct GCfg {
-  static constexpr int kBBytes = BN * kGK * 2;
-  static constexpr int kStages = BN == 256 ? 4 : BN == 128 ? 6 : 8;
-  static constexpr int kTmemCols = 2 * BN < 32 ? 32 : 2 * BN;
+  static constexpr int kBBytes = kGN / CG * kGK * 2;
+  static constexpr int kStages = CG == 2 ? 6 : 4;
   static constexpr int kSmem = 1024 + kStages * (kGABytes + kBBytes) + 1024 + kGTables;
   static_assert(kSmem <= 227 * 1024, "shared memory budget");
 };
 
+constexpr int kGBoxes = 5;            // K-major B: boxes of 16 << i rows
 struct GMaps {
-  CUtensorMap a[4];     // K-major A: boxes of 16 << i rows; MN: a[0]
-  CUtensorMap b;
+  CUtensorMap a;
+  CUtensorMap b[kGBoxes];             // MN-contiguous B: b[0]
 };
 struct GArgs {
   MmArgs m;
-  int n_tiles;          // BN-wide column tiles
-  int m_tiles;          // wgrad: 128-row tiles of N
+  int bn;               // widest N of a tile
+  int m_tiles;          // tiles of 128 CG features
+  int n_tiles;          // weight gradient: bn-wide column tiles
   int a_chunks, b_chunks;   // MN-contiguous operands: 64-wide chunks a copy takes (1: one copy a chunk)
 };
 
-// Copies of one MN-contiguous operand stage: `chunks` chunks of 64 columns
-// from column c0, rows row0 .. row0 + 63 of matrix z.
-__device__ __forceinline__ void g_load_mn(uint8_t* dst, const CUtensorMap* map, int c0, int row0, int z, int chunks,
-                                          int per_copy, uint64_t* bar) {
-  if (per_copy > 1) {
-    tc::tma_load_4d_plain(dst, map, 0, row0, c0 / 64, z, bar);
+struct GTile {
+  int e;
+  int m0;               // first feature (row of D)
+  int c0, nc, N;        // first token row (weight gradient: column), real ones, the MMA's N
+  int k0, k1, red;      // stages [k0, k1) of the reduction's `red`
+  int piece;
+};
+
+template <int MODE, int CG>
+__device__ __forceinline__ void g_tile(const GArgs& g, const int32_t* off, const int32_t* uoff, int u, GTile& w) {
+  const MmArgs& m = g.m;
+  const int t = m.S == 1 ? u : u / m.S;
+  w.piece = u - t * m.S;
+  if (MODE == kWgradMN) {
+    // units of a group: row tiles, then column tiles innermost
+    const int ui = t / g.n_tiles;
+    w.c0 = (t - ui * g.n_tiles) * g.bn;
+    w.nc = min(g.bn, m.K - w.c0);
+    w.N = g.bn;
+    w.e = ui / g.m_tiles;
+    w.m0 = (ui - w.e * g.m_tiles) * (kGM * CG);
+    w.red = off[w.e + 1] - off[w.e];
   } else {
-    for (int c = 0; c < chunks; ++c) tc::tma_load_4d_plain(dst + c * kGChunk, map, c0 + 64 * c, row0, 0, z, bar);
+    // token tiles of a group, feature tiles innermost
+    const int ui = t / g.m_tiles;
+    w.m0 = (t - ui * g.m_tiles) * (kGM * CG);
+    w.e = group_of_unit(uoff, m.G, ui);
+    const int cnt = off[w.e + 1] - off[w.e], nt = uoff[w.e + 1] - uoff[w.e];
+    // the group's rows in equal tiles, of a multiple of 32 each
+    const int wide = (((cnt + nt - 1) / nt) + 31) & ~31;
+    const int r = (ui - uoff[w.e]) * wide;
+    w.c0 = off[w.e] + r;
+    w.nc = min(wide, cnt - r);
+    w.N = (w.nc + 31) & ~31;
+    w.red = m.K;
+  }
+  const int nk = (w.red + kGK - 1) / kGK;
+  w.k0 = m.S == 1 ? 0 : (int)((int64_t)nk * w.piece / m.S);
+  w.k1 = m.S == 1 ? nk : (int)((int64_t)nk * (w.piece + 1) / m.S);
+}
+
+// A copy of K-major token rows covers 16 << i of them, the fewest that hold
+// the tile's; what lies behind them in the stage only reaches columns that
+// are not stored.
+__device__ __forceinline__ int g_box(int rows) {
+  return rows <= 16 ? 0 : rows <= 32 ? 1 : rows <= 64 ? 2 : rows <= 128 ? 3 : 4;
+}
+
+// The copies of a stage: into this CTA's memory, reported to `bar` (one SM: its
+// own barrier; a pair: a barrier of either CTA).
+template <int CG>
+struct GCopy {
+  uint32_t bar;
+  __device__ __forceinline__ void d2(void* dst, const CUtensorMap* map, int x, int y) const {
+    if (CG == 2) tc::tma_load_2d_pair(dst, map, x, y, bar);
+    else tc::tma_load_2d_plain(dst, map, x, y, reinterpret_cast<uint64_t*>(__cvta_shared_to_generic(bar)));
+  }
+  __device__ __forceinline__ void d3(void* dst, const CUtensorMap* map, int x, int y, int z) const {
+    if (CG == 2) tc::tma_load_3d_pair(dst, map, x, y, z, bar);
+    else tc::tma_load_3d_plain(dst, map, x, y, z, reinterpret_cast<uint64_t*>(__cvta_shared_to_generic(bar)));
+  }
+  __device__ __forceinline__ void d4(void* dst, const CUtensorMap* map, int x, int y, int z, int w) const {
+    if (CG == 2) tc::tma_load_4d_pair(dst, map, x, y, z, w, bar);
+    else tc::tma_load_4d_plain(dst, map, x, y, z, w, reinterpret_cast<uint64_t*>(__cvta_shared_to_generic(bar)));
+  }
+  // An MN-contiguous operand: `chunks` chunks of 64 columns from column c0,
+  // rows row0 .. row0 + 63 of matrix z.
+  __device__ __forceinline__ void mn(uint8_t* dst, const CUtensorMap* map, int c0, int row0, int z, int chunks,
+                                     int per_copy) const {
+    if (per_copy > 1) {
+      d4(dst, map, 0, row0, c0 / 64, z);
+    } else {
+      for (int c = 0; c < chunks; ++c) d4(dst + c * kGChunk, map, c0 + 64 * c, row0, 0, z);
+    }
+  }
+};
+
+// Whether a stage of the weight gradient ends inside an MMA's K of 16: the
+// group's last rows, `left` of them; the rows behind are cleared in shared
+// memory by each CTA before the MMAs read them.
+__device__ __forceinline__ bool g_tail(int left) { return left < kGK && (left & 15); }
+
+// 32 token rows (n of them real) of the lane's feature: out[row][f], f =
+// f0 + lane < F. 16-bit outputs: two lanes exchange so that each stores two
+// neighbouring features of one row (`pairs`: 4-byte stores are aligned).
+template <typename E>
+__device__ __forceinline__ void store_tokens16(uint16_t* out, int64_t ld, const uint32_t (&v)[32], int n, int lane,
+                                               int f0, int F, bool pairs) {
+  if (pairs && f0 + 32 <= F) {
+    const bool odd = lane & 1;
+    uint16_t* p = out + f0 + (lane & ~1) + (odd ? ld : 0);
+#pragma unroll
+    for (int i = 0; i < 32; i += 2) {
+      const uint32_t other = __shfl_xor_sync(kFull, odd ? v[i] : v[i + 1], 1);
+      const uint32_t w = odd ? E::from2(__uint_as_float(other), __uint_as_float(v[i + 1]))
+                             : E::from2(__uint_as_float(v[i]), __uint_as_float(other));
+      if (i + (odd ? 1 : 0) < n) *reinterpret_cast<uint32_t*>(p + i * ld) = w;
+    }
+  } else if (f0 + lane < F) {
+#pragma unroll
+    for (int i = 0; i < 32; ++i)
+      if (i < n) out[i * ld + f0 + lane] = E::from(__uint_as_float(v[i]));
   }
 }
 
-template <int MODE, int BN>
+template <int MODE, int CG>
 __global__ void __launch_bounds__(kGThreads, 1) k_gemm16(const GArgs g, const __grid_constant__ GMaps maps) {
-  using C = GCfg<BN>;
+  using C = GCfg<CG>;
   constexpr bool kWg = MODE == kWgradMN;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* base = reinterpret_cast<uint8_t*>(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
   uint8_t* sa = base;
   uint8_t* sb = sa + C::kStages * kGABytes;
   uint64_t* full = reinterpret_cast<uint64_t*>(sb + C::kStages * C::kBBytes);
-  uint64_t* empty = full + C::kStages;
+  uint64_t* pfull = full + C::kStages;          // pair: the second CTA has cleared its rows of a tail stage
+  uint64_t* empty = pfull + C::kStages;
   uint64_t* accfull = empty + C::kStages;
   uint64_t* accempty = accfull + 2;
   uint64_t* drain = accempty + 2;
@@ -90,61 +196,73 @@ __global__ void __launch_bounds__(kGThreads, 1) k_gemm16(const GArgs g, const __
   int32_t* uoff = off + kMmMaxGroups + 1;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const MmArgs& m = g.m;
+  const int rank = CG == 2 ? (int)tc::cluster_rank() : 0;
+  const int first = blockIdx.x / CG, stride = gridDim.x / CG;
 
-  pdl_enter();
   if (threadIdx.x == 0) {
     for (int i = 0; i < C::kStages; ++i) {
       tc::mbar_init(&full[i], 2);       // one arrival (with its bytes) from each copying warp
+      tc::mbar_init(&pfull[i], 1);
       tc::mbar_init(&empty[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
       tc::mbar_init(&accfull[i], 1);
-      tc::mbar_init(&accempty[i], 4);   // one per epilogue warp
+      tc::mbar_init(&accempty[i], 4 * CG);   // one per epilogue warp of the tile, of both CTAs
     }
     tc::mbar_init(drain, 1);
     *abort = 0;
     tc::fence_mbar_init();
   }
-  if (warp == 1) tc::tmem_alloc(tmem_slot, C::kTmemCols);
+  if (warp == 1) {
+    if (CG == 2) tc::tmem_alloc_pair(tmem_slot, 512);
+    else tc::tmem_alloc(tmem_slot, 512);
+  }
+  if (warp == 0 && lane == 0) {
+    tc::prefetch_tmap(&maps.a);
+    for (int i = 0; i < (kWg ? 1 : kGBoxes); ++i) tc::prefetch_tmap(&maps.b[i]);
+  }
+  pdl_enter();
   build_groups<kGThreads>(m.offsets, m.G, m.R, off, uoff, tmp, m.status,
-                          [&](int c) { return kWg ? g.m_tiles : (c + kGM - 1) / kGM; });
+                          [&](int c) { return kWg ? g.m_tiles : (c + g.bn - 1) / g.bn; });
   tc::fence_before_sync();
   __syncthreads();
+  // the peer's barriers are initialised before anything reaches them
+  if constexpr (CG == 2) tc::cluster_sync();
   tc::fence_after_sync();
   const uint32_t tmem = *tmem_slot;
-  const int U = uoff[m.G] * g.n_tiles * m.S;
+  const int U = uoff[m.G] * (kWg ? g.n_tiles : g.m_tiles) * m.S;
 
   if (warp == 0 || warp == 2) {
     // ---------------- copies: warp 0 B, warp 2 A ----------------
     if (lane == 0) {
       const bool isb = warp == 0;
-      if (isb) tc::prefetch_tmap(&maps.b);
-      else
-        for (int i = 0; i < (kWg ? 1 : 4); ++i) tc::prefetch_tmap(&maps.a[i]);
       uint32_t it = 0;
       bool ok = true;
-      for (int u = blockIdx.x; ok && u < U; u += gridDim.x) {
-        GUnit w;
-        g_unit<kWg, BN, kGK>(m, g.n_tiles, off, uoff, u, w);
-        const int ai = g_a_box(w.rows);
+      for (int u = first; ok && u < U; u += stride) {
+        GTile w;
+        g_tile<MODE, CG>(g, off, uoff, u, w);
+        const int half = w.N / CG;                    // B rows of this CTA
+        const int c0 = w.c0 + rank * half, m0 = w.m0 + rank * kGM;
+        const int bi = g_box(half);
+        const uint32_t bytes = !isb ? kGABytes : kWg ? (uint32_t)(half / 64 * kGChunk) : (uint32_t)(kGK * 2 * (16 << bi));
         for (int kb = w.k0; kb < w.k1; ++kb, ++it) {
           const int slot = it % C::kStages;
           if (!tc::mbar_wait(&empty[slot], ((it / C::kStages) & 1) ^ 1, abort)) { ok = false; break; }
+          // both CTAs' copies report to the first one's barrier, which expects
+          // them all; those of a tail stage, where the second CTA has rows to
+          // clear first, to their own CTA's
+          const bool own = CG == 1 || (kWg && g_tail(w.red - kb * kGK));
+          if (own || rank == 0) tc::mbar_arrive_expect_tx(&full[slot], own ? bytes : CG * bytes);
+          const GCopy<CG> copy = {own ? tc::smem_u32(&full[slot]) : tc::peer_smem(&full[slot], 0)};
           if (isb) {
             uint8_t* d = sb + slot * C::kBBytes;
-            tc::mbar_arrive_expect_tx(&full[slot], C::kBBytes);
-            if (MODE == kRowsNT) tc::tma_load_3d_plain(d, &maps.b, kb * kGK, w.n0, w.e, &full[slot]);
-            else if (MODE == kRowsNN) g_load_mn(d, &maps.b, w.n0, kb * kGK, w.e, BN / 64, g.b_chunks, &full[slot]);
-            else g_load_mn(d, &maps.b, w.n0, off[w.e] + kb * kGK, 0, BN / 64, g.b_chunks, &full[slot]);
+            if (kWg) copy.mn(d, &maps.b[0], c0, off[w.e] + kb * kGK, 0, half / 64, g.b_chunks);
+            else copy.d2(d, &maps.b[bi], kb * kGK, c0);
           } else {
             uint8_t* d = sa + slot * kGABytes;
-            if (kWg) {
-              tc::mbar_arrive_expect_tx(&full[slot], kGABytes);
-              g_load_mn(d, &maps.a[0], w.row0, off[w.e] + kb * kGK, 0, kGM / 64, g.a_chunks, &full[slot]);
-            } else {
-              tc::mbar_arrive_expect_tx(&full[slot], (uint32_t)(kGK * 2 * (16 << ai)));
-              tc::tma_load_2d_plain(d, &maps.a[ai], kb * kGK, w.row0, &full[slot]);
-            }
+            if (MODE == kRowsNT) copy.d3(d, &maps.a, kb * kGK, m0, w.e);
+            else if (MODE == kRowsNN) copy.mn(d, &maps.a, m0, kb * kGK, w.e, kGM / 64, g.a_chunks);
+            else copy.mn(d, &maps.a, m0, off[w.e] + kb * kGK, 0, kGM / 64, g.a_chunks);
           }
         }
       }
@@ -152,7 +270,8 @@ __global__ void __launch_bounds__(kGThreads, 1) k_gemm16(const GArgs g, const __
         // wind-down: wait (bounded, ignoring the abort flag) for the copies
         // this thread still has in flight. A slot's barrier completes only
         // when the other copying warp arrived too; it may have stopped
-        // earlier, so the wait's limit is what ends this then.
+        // earlier (and the second CTA of a pair reports elsewhere), so the
+        // wait's limit is what ends this then.
         volatile int never = 0;
         const uint32_t n = it < (uint32_t)C::kStages ? it : (uint32_t)C::kStages;
         for (uint32_t k = 0; k < n; ++k) {
@@ -162,70 +281,96 @@ __global__ void __launch_bounds__(kGThreads, 1) k_gemm16(const GArgs g, const __
       }
     }
   } else if (warp == 1) {
-    // ---------------- MMAs ----------------
-    const uint32_t idesc = tc::idesc_16bit(kGM, BN, m.dtype == MOE_DT_BF16, kWg, MODE != kRowsNT);
+    // ---------------- MMAs (second CTA of a pair: its tail stages) ----------------
     uint32_t it = 0, tcount = 0;
+    uint32_t tails = 0;         // pair: parity, by slot, of the barriers that only tail stages use
     bool ok = true;
-    for (int u = blockIdx.x; ok && u < U; u += gridDim.x, ++tcount) {
-      GUnit w;
-      g_unit<kWg, BN, kGK>(m, g.n_tiles, off, uoff, u, w);
+    for (int u = first; ok && u < U; u += stride, ++tcount) {
+      GTile w;
+      g_tile<MODE, CG>(g, off, uoff, u, w);
       const int d = tcount & 1;
-      ok = __all_sync(kFull, tc::mbar_wait(&accempty[d], ((tcount >> 1) & 1) ^ 1, abort));
-      if (!ok) break;
-      tc::fence_after_sync();
-      const uint32_t dt = tmem + d * BN;
+      if (rank == 0) {
+        ok = __all_sync(kFull, tc::mbar_wait(&accempty[d], ((tcount >> 1) & 1) ^ 1, abort));
+        if (!ok) break;
+        tc::fence_after_sync();
+      }
+      const uint32_t dt = tmem + d * kGN;
+      const uint32_t idesc = tc::idesc_16bit(kGM * CG, w.N, m.dtype == MOE_DT_BF16, MODE != kRowsNT, kWg);
       for (int kb = w.k0; kb < w.k1; ++kb, ++it) {
         const int slot = it % C::kStages;
-        ok = __all_sync(kFull, tc::mbar_wait(&full[slot], (it / C::kStages) & 1, abort));
-        if (!ok) break;
-        uint8_t* pa = sa + slot * kGABytes;
-        uint8_t* pb = sb + slot * C::kBBytes;
         const int left = w.red - kb * kGK;          // of the reduction in this stage
         const int steps = left >= kGK ? 4 : (left + 15) / 16;
-        if (kWg && left < kGK && (left & 15)) {
+        const bool tail = kWg && g_tail(left);
+        if (rank != 0 && !tail) continue;
+        uint8_t* pa = sa + slot * kGABytes;
+        uint8_t* pb = sb + slot * C::kBBytes;
+        const uint32_t parity = rank != 0 ? (tails >> slot) & 1 : (it / C::kStages) & 1;
+        ok = __all_sync(kFull, tc::mbar_wait(&full[slot], parity, abort));
+        if (!ok) break;
+        if (tail) {
           // rows of the next group behind the last ones: cleared up to the
           // MMA's K, a 128-byte line per row and chunk (the swizzle permutes
           // within a line)
-          const int bad = 16 - (left & 15);
-          for (int i = lane; i < bad * 8 * (kGM / 64 + BN / 64); i += 32) {
+          const int bad = 16 - (left & 15), chunks = kGM / 64 + w.N / CG / 64;
+          for (int i = lane; i < bad * 8 * chunks; i += 32) {
             const int q = i & 7, r = left + (i >> 3) % bad, c = (i >> 3) / bad;
             uint8_t* line = (c < kGM / 64 ? pa + c * kGChunk : pb + (c - kGM / 64) * kGChunk) + r * 128;
             reinterpret_cast<uint4*>(line)[q] = make_uint4(0u, 0u, 0u, 0u);
           }
           asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
           __syncwarp();
+          if constexpr (CG == 2) {
+            const uint32_t pp = (tails >> slot) & 1;
+            tails ^= 1u << slot;
+            if (rank != 0) {
+              if (lane == 0) tc::mbar_arrive_peer(tc::peer_smem(&pfull[slot], 0));
+              __syncwarp();
+              continue;
+            }
+            ok = __all_sync(kFull, tc::mbar_wait(&pfull[slot], pp, abort));
+            if (!ok) break;
+          }
         }
         if (lane == 0) {
           tc::fence_after_sync();
-          const uint64_t ad = kWg ? tc::smem_desc_mn_sw128(tc::smem_u32(pa), kGChunk) : tc::smem_desc_sw128(tc::smem_u32(pa));
-          const uint64_t bd = MODE != kRowsNT ? tc::smem_desc_mn_sw128(tc::smem_u32(pb), kGChunk)
-                                              : tc::smem_desc_sw128(tc::smem_u32(pb));
+          const uint64_t ad = MODE != kRowsNT ? tc::smem_desc_mn_sw128(tc::smem_u32(pa), kGChunk)
+                                              : tc::smem_desc_sw128(tc::smem_u32(pa));
+          const uint64_t bd = kWg ? tc::smem_desc_mn_sw128(tc::smem_u32(pb), kGChunk)
+                                  : tc::smem_desc_sw128(tc::smem_u32(pb));
           // a step of K = 16: 32 bytes along a K-major row, two 8-row atoms otherwise
-          constexpr uint32_t sta = kWg ? 2048 / 16 : 32 / 16, stb = MODE != kRowsNT ? 2048 / 16 : 32 / 16;
-          for (int j = 0; j < steps; ++j)
-            tc::mma_f16_ss(dt, ad + sta * j, bd + stb * j, idesc, (kb > w.k0 || j > 0) ? 1u : 0u);
-          tc::mma_commit(&empty[slot]);
+          constexpr uint32_t sta = MODE != kRowsNT ? 2048 / 16 : 32 / 16, stb = kWg ? 2048 / 16 : 32 / 16;
+          for (int j = 0; j < steps; ++j) {
+            const uint32_t acc = (kb > w.k0 || j > 0) ? 1u : 0u;
+            if constexpr (CG == 2) tc::mma_f16_ss_pair(dt, ad + sta * j, bd + stb * j, idesc, acc);
+            else tc::mma_f16_ss(dt, ad + sta * j, bd + stb * j, idesc, acc);
+          }
+          if constexpr (CG == 2) tc::mma_commit_pair(&empty[slot]);
+          else tc::mma_commit(&empty[slot]);
         }
         __syncwarp();
       }
       if (!ok) break;
-      if (lane == 0) tc::mma_commit(&accfull[d]);
+      if (lane == 0 && rank == 0) {
+        if constexpr (CG == 2) tc::mma_commit_pair(&accfull[d]);
+        else tc::mma_commit(&accfull[d]);
+      }
       __syncwarp();
     }
-    if (lane == 0) {
-      tc::mma_commit(drain);              // every MMA of this thread has completed once it fires
+    if (lane == 0 && rank == 0) {
+      // every MMA of this thread has completed once `drain` fires
+      if constexpr (CG == 2) tc::mma_commit_pair(drain);
+      else tc::mma_commit(drain);
       volatile int never = 0;
       tc::mbar_wait(drain, 0, &never, 400000000ll);
     }
     __syncwarp();
   } else if (warp == 3) {
-    // ---------------- rows outside every group ----------------
     if (!kWg) clear_rows_outside(m, off, lane);
   } else {
     // ---------------- epilogue ----------------
     const int wg = (warp - 4) >> 2, q = warp & 3;
-    const uint32_t acc = tmem + ((uint32_t)(q * 32) << 16) + wg * BN;
-    const int cols = kWg ? m.K : m.N;
+    const uint32_t acc = tmem + ((uint32_t)(q * 32) << 16) + wg * kGN;
+    const int cols = kWg ? m.K : m.N;               // of a row of out
     const int dt = m.S > 1 ? MOE_DT_F32 : m.out_dtype;
     const int esize = dt == MOE_DT_F32 ? 4 : 2;
     const int64_t ld = m.S > 1 ? cols : m.ldo;
@@ -234,42 +379,68 @@ __global__ void __launch_bounds__(kGThreads, 1) k_gemm16(const GArgs g, const __
     const int64_t os = kWg ? (int64_t)m.G * m.N * m.K : (int64_t)m.R * m.N;      // a piece's partial sums
     const bool vec = ((uintptr_t)obase & 15) == 0 && (ld * esize) % 16 == 0 && (og * esize) % 16 == 0 &&
                      (m.S == 1 || (os * 4) % 16 == 0);
+    const bool pairs = ((uintptr_t)obase & 3) == 0 && ld % 2 == 0;
     uint32_t tcount = 0, mine = 0;
-    for (int u = blockIdx.x; u < U; u += gridDim.x, ++tcount) {
+    for (int u = first; u < U; u += stride, ++tcount) {
       if ((int)(tcount & 1) != wg) continue;
-      GUnit w;
-      g_unit<kWg, BN, kGK>(m, g.n_tiles, off, uoff, u, w);
+      GTile w;
+      g_tile<MODE, CG>(g, off, uoff, u, w);
       const bool got = tc::mbar_wait(&accfull[wg], mine & 1, abort);
       if (!__all_sync(kFull, got)) break;
       tc::fence_after_sync();
-      const int r = q * 32 + lane;
-      int64_t at = kWg ? w.e * og + (int64_t)(w.row0 + r) * ld : (int64_t)(w.row0 + r) * ld;
-      if (m.S > 1) at += w.piece * os;
-      for (int c0 = 0; c0 < BN && w.n0 + c0 < cols; c0 += 32) {
+      const int f0 = w.m0 + rank * kGM + q * 32;    // the warp's first feature
+      for (int c = 0; c < w.nc; c += 32) {
         uint32_t v[32];
         if (w.k1 > w.k0) {
-          tc::tmem_ld32(acc + c0, v);
+          tc::tmem_ld32(acc + c, v);
           tc::tmem_wait_ld();
         } else {
 #pragma unroll
           for (int i = 0; i < 32; ++i) v[i] = 0u;       // no rows to sum over
         }
-        if (r < w.rows) store_cols(obase + (at + w.n0 + c0) * esize, v, cols - w.n0 - c0, dt, vec);
+        if (kWg) {
+          if (f0 + lane < m.N) {
+            const int64_t at = w.e * og + (int64_t)(f0 + lane) * ld + w.c0 + c + (m.S > 1 ? w.piece * os : 0);
+            store_cols(obase + at * esize, v, w.nc - c, dt, vec);
+          }
+        } else {
+          const int64_t at = (int64_t)(w.c0 + c) * ld + (m.S > 1 ? w.piece * os : 0);
+          const int n = w.nc - c;
+          if (dt == MOE_DT_F32) {
+            float* p = reinterpret_cast<float*>(obase) + at + f0 + lane;
+            if (f0 + lane < m.N) {
+#pragma unroll
+              for (int i = 0; i < 32; ++i)
+                if (i < n) p[i * ld] = __uint_as_float(v[i]);
+            }
+          } else if (dt == MOE_DT_F16) {
+            store_tokens16<F16>(reinterpret_cast<uint16_t*>(obase) + at, ld, v, n, lane, f0, m.N, pairs);
+          } else {
+            store_tokens16<Bf16>(reinterpret_cast<uint16_t*>(obase) + at, ld, v, n, lane, f0, m.N, pairs);
+          }
+        }
         __syncwarp();
       }
       tc::fence_before_sync();
       __syncwarp();
-      if (lane == 0) tc::mbar_arrive(&accempty[wg]);
+      if (lane == 0) {
+        if (CG == 2 && rank != 0) tc::mbar_arrive_peer(tc::peer_smem(&accempty[wg], 0));
+        else tc::mbar_arrive(&accempty[wg]);
+      }
       ++mine;
     }
   }
 
   tc::fence_before_sync();
   __syncthreads();
+  // neither CTA of a pair leaves while the other's MMAs read its memory or its
+  // arrivals are on their way
+  if constexpr (CG == 2) tc::cluster_sync();
   if (threadIdx.x == 0 && *abort) set_status(m.status, MOE_DEV_TIMEOUT);
   if (warp == 1) {
     tc::fence_after_sync();
-    tc::tmem_dealloc(tmem, C::kTmemCols);
+    if (CG == 2) tc::tmem_dealloc_pair(tmem, 512);
+    else tc::tmem_dealloc(tmem, 512);
   }
 }
 
@@ -304,25 +475,36 @@ cudaError_t launch_mm_join(const MmArgs& a, bool wgrad, cudaStream_t st) {
 constexpr int kPlanSms = 152;
 constexpr int64_t kPartBytes = 64ll << 20;
 
+static int64_t tiles(int64_t n, int64_t t) { return (n + t - 1) / t; }
+
 MmPlan mm_plan(int kind, int R, int N, int K, int G) {
   const bool wg = kind == kMmWgrad;
-  // row tiles: at least one for every group that can have rows
-  const int64_t mt = wg ? (int64_t)G * ((N + kGM - 1) / kGM)
-                        : std::max<int64_t>((R + kGM - 1) / kGM, std::min(G, R));
-  const int cols = wg ? K : N;
-  const int64_t red = wg ? (R + G - 1) / G : K;
-  MmPlan p;
-  p.bn = 256;
-  auto units = [&] { return mt * ((cols + p.bn - 1) / p.bn); };
-  while (p.bn > 64 && units() < kPlanSms) p.bn /= 2;
-  p.S = 1;
-  const int64_t u = std::max<int64_t>(1, units());
+  MmPlan p = {1, 256, 1};
+  // tiles of `b` rows: at least one for every group that can have rows
+  auto row_tiles = [&](int b) { return std::max<int64_t>(tiles(R, b), std::min(G, R)); };
+  int64_t units;
+  if (kind == kMmFp8) {
+    while (true) {
+      units = row_tiles(kGM) * tiles(N, p.bn);
+      if (p.bn == 64 || units >= kPlanSms) break;
+      p.bn /= 2;
+    }
+  } else {
+    auto count = [&](int cg, int bn) {
+      return wg ? G * tiles(N, kGM * cg) * tiles(K, bn) : row_tiles(bn) * tiles(N, kGM * cg);
+    };
+    // pairs of SMs where there is a tile for each of them, except at a few
+    // rows a group, which stream weights
+    p.cg = count(2, 256) >= kPlanSms / 2 && (wg || R >= 64ll * std::min(G, R)) ? 2 : 1;
+    while (p.cg == 1 && p.bn > 64 && count(1, p.bn) < kPlanSms) p.bn /= 2;
+    units = count(p.cg, p.bn);
+  }
   // pieces of at least 512 (FP8: 1024) of the reduction, partial sums within
   // the workspace's bound
-  const int64_t step = kind == kMmFp8 ? 1024 : 512;
-  const int64_t outs = (wg ? (int64_t)G * N : (int64_t)R) * cols;
-  if (u < kPlanSms && outs > 0)
-    p.S = (int)std::max<int64_t>(1, std::min({kPlanSms / u, red / step, kPartBytes / (outs * 4), (int64_t)32}));
+  const int64_t red = wg ? tiles(R, G) : K, step = kind == kMmFp8 ? 1024 : 512;
+  const int64_t outs = wg ? (int64_t)G * N * K : (int64_t)R * N;
+  if (p.cg == 1 && units > 0 && units < kPlanSms && outs > 0)
+    p.S = (int)std::max<int64_t>(1, std::min({kPlanSms / units, red / step, kPartBytes / (outs * 4), (int64_t)32}));
   return p;
 }
 int mm_splits(int kind, int R, int N, int K, int G) { return mm_plan(kind, R, N, K, G).S; }
@@ -359,7 +541,8 @@ bool make_tmap(CUtensorMap* map, const void* base, int esize, int rank, const in
 // boxes. Where cols is a whole number of 64-wide chunks, the map has a chunk
 // axis and one copy brings `chunks` of them, one after the other (a copy
 // costs its issuer more than its bytes); else a copy a chunk (a chunk axis
-// would read past the last row's end). Returns the chunks a copy takes.
+// would read past the last row's end). Returns the chunks a copy takes, 0 if
+// the map cannot be made.
 static int make_mn(CUtensorMap* map, const void* base, int64_t rows, int64_t cols, int64_t ld, int64_t G, int64_t gs,
                    int chunks) {
   if (G == 1) gs = ld;      // never stepped over
@@ -373,59 +556,91 @@ static int make_mn(CUtensorMap* map, const void* base, int64_t rows, int64_t col
   return make_tmap(map, base, 2, 4, dims, strides, box) ? 1 : 0;
 }
 
-template <int MODE, int BN>
+template <int MODE, int CG>
 static cudaError_t launch_g(GArgs g, cudaStream_t st) {
-  using C = GCfg<BN>;
+  using C = GCfg<CG>;
   const MmArgs& m = g.m;
   constexpr bool kWg = MODE == kWgradMN;
   GMaps maps;
   const int64_t rows = std::max(m.R, 1);
+  g.m_tiles = (int)tiles(m.N, kGM * CG);
+  g.n_tiles = kWg ? (int)tiles(m.K, g.bn) : 1;
   if (kWg) {
     // without rows nothing is copied, and the maps only need an aligned address
     const void* a = m.R > 0 ? m.a : m.status;
     const void* b = m.R > 0 ? m.b : m.status;
-    g.a_chunks = make_mn(&maps.a[0], a, rows, m.N, m.lda, 1, 0, kGM / 64);
-    g.b_chunks = make_mn(&maps.b, b, rows, m.K, m.ldb, 1, 0, BN / 64);
+    g.a_chunks = make_mn(&maps.a, a, rows, m.N, m.lda, 1, 0, kGM / 64);
+    g.b_chunks = make_mn(&maps.b[0], b, rows, m.K, m.ldb, 1, 0, g.bn / CG / 64);
     if (!g.a_chunks || !g.b_chunks) return cudaErrorInvalidValue;
-    g.m_tiles = (m.N + kGM - 1) / kGM;
-    g.n_tiles = (m.K + BN - 1) / BN;
   } else {
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < kGBoxes; ++i) {
       const int64_t dims[2] = {m.K, rows}, strides[1] = {m.lda};
       const int box[2] = {kGK, 16 << i};
-      if (!make_tmap(&maps.a[i], m.a, 2, 2, dims, strides, box)) return cudaErrorInvalidValue;
+      if (!make_tmap(&maps.b[i], m.a, 2, 2, dims, strides, box)) return cudaErrorInvalidValue;
     }
     if (MODE == kRowsNT) {
       const int64_t dims[3] = {m.K, m.N, m.G}, strides[2] = {m.ldb, m.G > 1 ? m.bg : m.ldb};
-      const int box[3] = {kGK, BN, 1};
-      if (!make_tmap(&maps.b, m.b, 2, 3, dims, strides, box)) return cudaErrorInvalidValue;
+      const int box[3] = {kGK, kGM, 1};
+      if (!make_tmap(&maps.a, m.b, 2, 3, dims, strides, box)) return cudaErrorInvalidValue;
     } else {
-      g.b_chunks = make_mn(&maps.b, m.b, m.K, m.N, m.ldb, m.G, m.bg, BN / 64);
-      if (!g.b_chunks) return cudaErrorInvalidValue;
+      g.a_chunks = make_mn(&maps.a, m.b, m.K, m.N, m.ldb, m.G, m.bg, kGM / 64);
+      if (!g.a_chunks) return cudaErrorInvalidValue;
     }
-    g.n_tiles = (m.N + BN - 1) / BN;
   }
-  if (!units_fit(m, kWg ? (int64_t)m.G * g.m_tiles : m.R / kGM, g.n_tiles)) return cudaErrorInvalidValue;
+  if (!units_fit(m, kWg ? (int64_t)m.G * g.m_tiles : m.R / g.bn, kWg ? g.n_tiles : g.m_tiles))
+    return cudaErrorInvalidValue;
   static std::atomic<bool> done[kMaxDevices] = {};
-  cudaError_t e = set_smem_once((const void*)k_gemm16<MODE, BN>, C::kSmem, done);
+  cudaError_t e = set_smem_once((const void*)k_gemm16<MODE, CG>, C::kSmem, done);
   if (e != cudaSuccess) return e;
   note_launch();
-  e = launch_pdl(k_gemm16<MODE, BN>, dim3(device_sms()), dim3(kGThreads), C::kSmem, st, g, maps);
+  if constexpr (CG == 1) {
+    e = launch_pdl(k_gemm16<MODE, CG>, dim3(device_sms()), dim3(kGThreads), C::kSmem, st, g, maps);
+  } else {
+    cudaLaunchConfig_t cfg = {};
+    cfg.blockDim = dim3(kGThreads);
+    cfg.dynamicSmemBytes = C::kSmem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = CG;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    // pairs that are resident at once, asked once per device
+    static std::atomic<int> pairs[kMaxDevices] = {};
+    int dev = 0;
+    if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
+    const bool slot = dev >= 0 && dev < kMaxDevices;
+    int np = slot ? pairs[dev].load(std::memory_order_acquire) : 0;
+    if (np <= 0) {
+      cfg.gridDim = dim3(CG * (device_sms() / CG));
+      cfg.numAttrs = 1;
+      if (cudaOccupancyMaxActiveClusters(&np, k_gemm16<MODE, CG>, &cfg) != cudaSuccess || np <= 0)
+        np = std::max(1, device_sms() / CG);
+      if (slot) pairs[dev].store(np, std::memory_order_release);
+    }
+    cfg.gridDim = dim3(CG * np);
+    cfg.numAttrs = 2;
+    e = cudaLaunchKernelEx(&cfg, k_gemm16<MODE, CG>, g, maps);
+  }
   if (e != cudaSuccess || m.S == 1) return e;
   return launch_mm_join(m, kWg, st);
 }
 
 template <int MODE>
-static cudaError_t launch_bn(const GArgs& g, int bn, cudaStream_t st) {
-  return bn == 256 ? launch_g<MODE, 256>(g, st) : bn == 128 ? launch_g<MODE, 128>(g, st) : launch_g<MODE, 64>(g, st);
+static cudaError_t launch_cg(const GArgs& g, int cg, cudaStream_t st) {
+  return cg == 2 ? launch_g<MODE, 2>(g, st) : launch_g<MODE, 1>(g, st);
 }
 
 cudaError_t launch_mm16(const MmArgs& a, bool wgrad, cudaStream_t st) {
   GArgs g = {};
   g.m = a;
-  const int bn = mm_plan(wgrad ? kMmWgrad : kMmRows, a.R, a.N, a.K, a.G).bn;
-  if (wgrad) return launch_bn<kWgradMN>(g, bn, st);
-  return a.trans_b ? launch_bn<kRowsNN>(g, bn, st) : launch_bn<kRowsNT>(g, bn, st);
+  const MmPlan p = mm_plan(wgrad ? kMmWgrad : kMmRows, a.R, a.N, a.K, a.G);
+  g.bn = p.bn;
+  if (wgrad) return launch_cg<kWgradMN>(g, p.cg, st);
+  return a.trans_b ? launch_cg<kRowsNN>(g, p.cg, st) : launch_cg<kRowsNT>(g, p.cg, st);
 }
 
 }  // namespace moe

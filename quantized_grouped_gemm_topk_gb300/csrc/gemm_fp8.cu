@@ -57,6 +57,36 @@ struct FArgs {
   int n_tiles;
 };
 
+struct GUnit {
+  int e, row0, rows;    // first x row of the tile and its real rows
+  int n0;               // first column
+  int k0, k1;           // reduction blocks of a stage each: [k0, k1) of this piece
+  int piece;
+};
+
+// Unit u: (row tile of a group, column tile, piece of the reduction), pieces
+// innermost, then column tiles.
+template <int BN>
+__device__ __forceinline__ void f_unit(const MmArgs& m, int n_tiles, const int32_t* off, const int32_t* uoff, int u,
+                                       GUnit& w) {
+  const int S = m.S;
+  const int t = u / S;
+  w.piece = u - t * S;
+  const int ui = t / n_tiles;
+  w.n0 = (t - ui * n_tiles) * BN;
+  w.e = group_of_unit(uoff, m.G, ui);
+  const int mi = ui - uoff[w.e], cnt = off[w.e + 1] - off[w.e];
+  w.row0 = off[w.e] + mi * kGM;
+  w.rows = min(kGM, cnt - mi * kGM);
+  const int nk = (m.K + kFK - 1) / kFK;
+  w.k0 = (int)((int64_t)nk * w.piece / S);
+  w.k1 = S == 1 ? nk : (int)((int64_t)nk * (w.piece + 1) / S);
+}
+
+// A copy of a tile's rows covers 16 << i of them, the fewest that hold its real
+// ones; the MMA's other rows are an earlier stage's bytes and are not stored.
+__device__ __forceinline__ int f_a_box(int rows) { return rows <= 16 ? 0 : rows <= 32 ? 1 : rows <= 64 ? 2 : 3; }
+
 template <int BN>
 __global__ void __launch_bounds__(kFThreads, 1) k_gemm_fp8(const FArgs g, const __grid_constant__ FMaps maps) {
   using C = FCfg<BN>;
@@ -112,8 +142,8 @@ __global__ void __launch_bounds__(kFThreads, 1) k_gemm_fp8(const FArgs g, const 
         bool ok = true;
         for (int u = blockIdx.x; ok && u < U; u += gridDim.x) {
           GUnit w;
-          g_unit<false, BN, kFK>(m, g.n_tiles, off, uoff, u, w);
-          const int ai = g_a_box(w.rows);
+          f_unit<BN>(m, g.n_tiles, off, uoff, u, w);
+          const int ai = f_a_box(w.rows);
           for (int kb = w.k0; kb < w.k1; ++kb, ++it) {
             const int slot = it % C::kStages;
             if (!tc::mbar_wait(&empty[slot], ((it / C::kStages) & 1) ^ 1, abort)) { ok = false; break; }
@@ -148,7 +178,7 @@ __global__ void __launch_bounds__(kFThreads, 1) k_gemm_fp8(const FArgs g, const 
         bool ok = true;
         for (int u = blockIdx.x; ok && u < U; u += gridDim.x) {
           GUnit w;
-          g_unit<false, BN, kFK>(m, g.n_tiles, off, uoff, u, w);
+          f_unit<BN>(m, g.n_tiles, off, uoff, u, w);
           for (int kb = w.k0; kb < w.k1; ++kb, ++it) {
             const int slot = it % C::kStages, ts = it % C::kSlots;
             if (!tc::mbar_wait(&hempty[ts], ((it / C::kSlots) & 1) ^ 1, abort)) { ok = false; break; }
@@ -187,7 +217,7 @@ __global__ void __launch_bounds__(kFThreads, 1) k_gemm_fp8(const FArgs g, const 
     bool ok = true;
     for (int u = blockIdx.x; ok && u < U; u += gridDim.x) {
       GUnit w;
-      g_unit<false, BN, kFK>(m, g.n_tiles, off, uoff, u, w);
+      f_unit<BN>(m, g.n_tiles, off, uoff, u, w);
       const int r = q * 32 + lane;
       const bool live = r < w.rows;
       const float* xs = m.sa + (int64_t)(w.row0 + (live ? r : 0)) * m.ldsa;

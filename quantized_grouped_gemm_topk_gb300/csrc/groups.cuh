@@ -99,40 +99,6 @@ __device__ __forceinline__ int group_of_unit(const int32_t* uoff, int G, int u) 
 
 constexpr int kGM = 128;              // tile rows (MMA M)
 
-struct GUnit {
-  int e, row0, rows;    // first A row of the tile (wgrad: first feature) and its real rows
-  int n0;               // first column
-  int k0, k1;           // reduction blocks of a stage each: [k0, k1) of this piece
-  int red;              // the whole reduction's length
-  int piece;
-};
-
-// Unit u of a product: (row tile of a group, column tile, piece of the
-// reduction), pieces innermost, then column tiles. WG: weight gradient (M =
-// N features, the reduction is the group's rows); BK: the stage's depth.
-template <bool WG, int BN, int BK>
-__device__ __forceinline__ void g_unit(const MmArgs& m, int n_tiles, const int32_t* off, const int32_t* uoff, int u,
-                                       GUnit& w) {
-  const int S = m.S;
-  const int t = u / S;
-  w.piece = u - t * S;
-  const int ui = t / n_tiles;
-  w.n0 = (t - ui * n_tiles) * BN;
-  w.e = group_of_unit(uoff, m.G, ui);
-  const int mi = ui - uoff[w.e], cnt = off[w.e + 1] - off[w.e];
-  if (WG) {
-    w.row0 = mi * kGM;
-    w.rows = min(kGM, m.N - w.row0);
-    w.red = cnt;
-  } else {
-    w.row0 = off[w.e] + mi * kGM;
-    w.rows = min(kGM, cnt - mi * kGM);
-    w.red = m.K;
-  }
-  const int nk = (w.red + BK - 1) / BK;
-  w.k0 = (int)((int64_t)nk * w.piece / S);
-  w.k1 = S == 1 ? nk : (int)((int64_t)nk * (w.piece + 1) / S);
-}
 // The kernels count units in 32 bits; more than that many would write more
 // than any GPU's memory.
 inline bool units_fit(const MmArgs& m, int64_t row_tiles, int64_t n_tiles) {

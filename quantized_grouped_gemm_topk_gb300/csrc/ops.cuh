@@ -260,9 +260,10 @@ struct MmArgs {
   int S;                        // pieces of the reduction (1: no partial sums)
 };
 enum { kMmRows = 0, kMmWgrad = 1, kMmFp8 = 2 };
-// Column tile and pieces of the reduction, from the sizes alone.
+// SMs a tile (a pair or one), widest tile and pieces of the reduction, from the
+// sizes alone.
 struct MmPlan {
-  int bn, S;
+  int cg, bn, S;
 };
 MmPlan mm_plan(int kind, int R, int N, int K, int G);
 int mm_splits(int kind, int R, int N, int K, int G);

@@ -389,6 +389,18 @@ def test_grouped_mm_wgrad(sizes, N, K, dtype, out):
     assert m.moe_mm_read_status(ws) == 0
 
 
+@pytest.mark.parametrize("N,K", [(1536, 64), (1500, 200), (2001, 1003), (1600, 1024)])
+@pytest.mark.parametrize("dtype,out", [(BF16, BF16), (F16, F32)])
+@pytest.mark.parametrize("what", ["forward", "dgrad", "wgrad"])
+def test_products_of_many_tiles(N, K, dtype, out, what):
+    """Enough tiles for every pair of SMs, ragged groups of one row to thousands."""
+    sizes = [300, 0, 17, 1, 1000, 256, 31, 2100, 0]
+    if what == "wgrad":
+        test_grouped_mm_wgrad(sizes, N, K, dtype, out)
+    else:
+        test_grouped_mm(sizes, N, K, dtype, out, what == "dgrad")
+
+
 def test_grouped_mm_wgrad_nan_stays_in_its_group():
     cuda_device()
     g = _gen(1)
