@@ -32,7 +32,8 @@
 // issues the MMAs (in a pair the first CTA's, whose barriers all copies of the
 // pair report to), warps 4-7 and 8-11 are epilogues
 // that alternate between tiles and the two accumulators, so a tile's stores
-// overlap the next one's MMAs; warp 3 clears rows outside every group.
+// overlap the next one's MMAs; warp 3 clears rows outside every group (weight
+// gradient: those behind a group's last rows, in shared memory).
 // Every wait is bounded; a CTA whose wait runs out sets MOE_DEV_TIMEOUT, waits
 // for its copies and MMAs in flight, frees tensor memory and returns.
 #include "groups.cuh"
@@ -118,34 +119,30 @@ __device__ __forceinline__ int g_box(int rows) {
   return rows <= 16 ? 0 : rows <= 32 ? 1 : rows <= 64 ? 2 : rows <= 128 ? 3 : 4;
 }
 
-// The copies of a stage: into this CTA's memory, reported to `bar` (one SM: its
-// own barrier; a pair: a barrier of either CTA).
+// The copies of a stage, by shared-memory addresses: into this CTA's memory,
+// reported to `bar` (one SM: its own barrier; a pair: one of either CTA).
 template <int CG>
-struct GCopy {
-  uint32_t bar;
-  __device__ __forceinline__ void d2(void* dst, const CUtensorMap* map, int x, int y) const {
-    if (CG == 2) tc::tma_load_2d_pair(dst, map, x, y, bar);
-    else tc::tma_load_2d_plain(dst, map, x, y, reinterpret_cast<uint64_t*>(__cvta_shared_to_generic(bar)));
+__device__ __forceinline__ void g_copy2(uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t bar) {
+  if (CG == 2) tc::tma_load_2d_pair(dst, map, x, y, bar);
+  else tc::tma_load_2d_at(dst, map, x, y, bar);
+}
+template <int CG>
+__device__ __forceinline__ void g_copy3(uint32_t dst, const CUtensorMap* map, int x, int y, int z, uint32_t bar) {
+  if (CG == 2) tc::tma_load_3d_pair(dst, map, x, y, z, bar);
+  else tc::tma_load_3d_at(dst, map, x, y, z, bar);
+}
+// An MN-contiguous operand: `chunks` chunks of 64 columns from column c0, rows
+// row0 .. row0 + 63 of matrix z; one copy where the map has a chunk axis.
+template <int CG>
+__device__ __forceinline__ void g_copy_mn(uint32_t dst, const CUtensorMap* map, int c0, int row0, int z, int chunks,
+                                          bool one, uint32_t bar) {
+  const int n = one ? 1 : chunks;
+  for (int c = 0; c < n; ++c) {
+    const int x = one ? 0 : c0 + 64 * c, ch = one ? c0 / 64 : 0;
+    if (CG == 2) tc::tma_load_4d_pair(dst + c * kGChunk, map, x, row0, ch, z, bar);
+    else tc::tma_load_4d_at(dst + c * kGChunk, map, x, row0, ch, z, bar);
   }
-  __device__ __forceinline__ void d3(void* dst, const CUtensorMap* map, int x, int y, int z) const {
-    if (CG == 2) tc::tma_load_3d_pair(dst, map, x, y, z, bar);
-    else tc::tma_load_3d_plain(dst, map, x, y, z, reinterpret_cast<uint64_t*>(__cvta_shared_to_generic(bar)));
-  }
-  __device__ __forceinline__ void d4(void* dst, const CUtensorMap* map, int x, int y, int z, int w) const {
-    if (CG == 2) tc::tma_load_4d_pair(dst, map, x, y, z, w, bar);
-    else tc::tma_load_4d_plain(dst, map, x, y, z, w, reinterpret_cast<uint64_t*>(__cvta_shared_to_generic(bar)));
-  }
-  // An MN-contiguous operand: `chunks` chunks of 64 columns from column c0,
-  // rows row0 .. row0 + 63 of matrix z.
-  __device__ __forceinline__ void mn(uint8_t* dst, const CUtensorMap* map, int c0, int row0, int z, int chunks,
-                                     int per_copy) const {
-    if (per_copy > 1) {
-      d4(dst, map, 0, row0, c0 / 64, z);
-    } else {
-      for (int c = 0; c < chunks; ++c) d4(dst + c * kGChunk, map, c0 + 64 * c, row0, 0, z);
-    }
-  }
-};
+}
 
 // Whether a stage of the weight gradient ends inside an MMA's K of 16: the
 // group's last rows, `left` of them; the rows behind are cleared in shared
@@ -184,12 +181,13 @@ __global__ void __launch_bounds__(kGThreads, 1) k_gemm16(const GArgs g, const __
   uint8_t* sa = base;
   uint8_t* sb = sa + C::kStages * kGABytes;
   uint64_t* full = reinterpret_cast<uint64_t*>(sb + C::kStages * C::kBBytes);
-  uint64_t* pfull = full + C::kStages;          // pair: the second CTA has cleared its rows of a tail stage
+  uint64_t* pfull = full + C::kStages;          // weight gradient: the rows of a tail stage are cleared
   uint64_t* empty = pfull + C::kStages;
   uint64_t* accfull = empty + C::kStages;
   uint64_t* accempty = accfull + 2;
   uint64_t* drain = accempty + 2;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+  uint64_t* tgo = drain + 1;                    // weight gradient: a tail stage has landed
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(tgo + 1);
   volatile int* abort = reinterpret_cast<volatile int*>(tmem_slot + 1);
   int* tmp = reinterpret_cast<int*>(tmem_slot + 2);
   int32_t* off = reinterpret_cast<int32_t*>(reinterpret_cast<uint8_t*>(full) + 1024);
@@ -202,7 +200,7 @@ __global__ void __launch_bounds__(kGThreads, 1) k_gemm16(const GArgs g, const __
   if (threadIdx.x == 0) {
     for (int i = 0; i < C::kStages; ++i) {
       tc::mbar_init(&full[i], 2);       // one arrival (with its bytes) from each copying warp
-      tc::mbar_init(&pfull[i], 1);
+      tc::mbar_init(&pfull[i], CG);
       tc::mbar_init(&empty[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
@@ -210,6 +208,7 @@ __global__ void __launch_bounds__(kGThreads, 1) k_gemm16(const GArgs g, const __
       tc::mbar_init(&accempty[i], 4 * CG);   // one per epilogue warp of the tile, of both CTAs
     }
     tc::mbar_init(drain, 1);
+    tc::mbar_init(tgo, 1);
     *abort = 0;
     tc::fence_mbar_init();
   }
@@ -232,11 +231,20 @@ __global__ void __launch_bounds__(kGThreads, 1) k_gemm16(const GArgs g, const __
   const uint32_t tmem = *tmem_slot;
   const int U = uoff[m.G] * (kWg ? g.n_tiles : g.m_tiles) * m.S;
 
+  const uint32_t full_u = tc::smem_u32(full), pfull_u = tc::smem_u32(pfull), empty_u = tc::smem_u32(empty);
+  const uint32_t sa_u = tc::smem_u32(sa), sb_u = tc::smem_u32(sb);
   if (warp == 0 || warp == 2) {
     // ---------------- copies: warp 0 B, warp 2 A ----------------
     if (lane == 0) {
       const bool isb = warp == 0;
-      uint32_t it = 0;
+      const uint32_t dst0 = isb ? sb_u : sa_u, step = isb ? C::kBBytes : kGABytes;
+      // both CTAs' copies report to the first one's barriers, which expect them
+      // all; those of a tail stage, where each CTA has rows to clear first, to
+      // their own CTA's
+      const uint32_t lead_u = CG == 2 ? tc::peer_smem(full, 0) : full_u;
+      int slot = 0;
+      uint32_t phase = 1;          // of empty: the ring starts free
+      uint32_t issued = 0;
       bool ok = true;
       for (int u = first; ok && u < U; u += stride) {
         GTile w;
@@ -245,24 +253,25 @@ __global__ void __launch_bounds__(kGThreads, 1) k_gemm16(const GArgs g, const __
         const int c0 = w.c0 + rank * half, m0 = w.m0 + rank * kGM;
         const int bi = g_box(half);
         const uint32_t bytes = !isb ? kGABytes : kWg ? (uint32_t)(half / 64 * kGChunk) : (uint32_t)(kGK * 2 * (16 << bi));
-        for (int kb = w.k0; kb < w.k1; ++kb, ++it) {
-          const int slot = it % C::kStages;
-          if (!tc::mbar_wait(&empty[slot], ((it / C::kStages) & 1) ^ 1, abort)) { ok = false; break; }
-          // both CTAs' copies report to the first one's barrier, which expects
-          // them all; those of a tail stage, where the second CTA has rows to
-          // clear first, to their own CTA's
-          const bool own = CG == 1 || (kWg && g_tail(w.red - kb * kGK));
-          if (own || rank == 0) tc::mbar_arrive_expect_tx(&full[slot], own ? bytes : CG * bytes);
-          const GCopy<CG> copy = {own ? tc::smem_u32(&full[slot]) : tc::peer_smem(&full[slot], 0)};
+        const CUtensorMap* map = isb ? (kWg ? &maps.b[0] : &maps.b[bi]) : &maps.a;
+        const int r0 = kWg ? off[w.e] : 0;
+        for (int kb = w.k0; kb < w.k1; ++kb) {
+          const int k = kb * kGK;
+          if (!tc::bar_wait(empty_u + 8 * slot, phase, abort)) { ok = false; break; }
+          const bool own = CG == 1 || (kWg && g_tail(w.red - k));
+          const uint32_t bar = (own ? full_u : lead_u) + 8 * slot, dst = dst0 + slot * step;
+          if (own || rank == 0) tc::bar_arrive_expect_tx(full_u + 8 * slot, own ? bytes : CG * bytes);
           if (isb) {
-            uint8_t* d = sb + slot * C::kBBytes;
-            if (kWg) copy.mn(d, &maps.b[0], c0, off[w.e] + kb * kGK, 0, half / 64, g.b_chunks);
-            else copy.d2(d, &maps.b[bi], kb * kGK, c0);
+            if (kWg) g_copy_mn<CG>(dst, map, c0, r0 + k, 0, half / 64, g.b_chunks > 1, bar);
+            else g_copy2<CG>(dst, map, k, c0, bar);
           } else {
-            uint8_t* d = sa + slot * kGABytes;
-            if (MODE == kRowsNT) copy.d3(d, &maps.a, kb * kGK, m0, w.e);
-            else if (MODE == kRowsNN) copy.mn(d, &maps.a, m0, kb * kGK, w.e, kGM / 64, g.a_chunks);
-            else copy.mn(d, &maps.a, m0, off[w.e] + kb * kGK, 0, kGM / 64, g.a_chunks);
+            if (MODE == kRowsNT) g_copy3<CG>(dst, map, k, m0, w.e, bar);
+            else g_copy_mn<CG>(dst, map, m0, kWg ? r0 + k : k, kWg ? 0 : w.e, kGM / 64, g.a_chunks > 1, bar);
+          }
+          ++issued;
+          if (++slot == C::kStages) {
+            slot = 0;
+            phase ^= 1;
           }
         }
       }
@@ -273,90 +282,75 @@ __global__ void __launch_bounds__(kGThreads, 1) k_gemm16(const GArgs g, const __
         // earlier (and the second CTA of a pair reports elsewhere), so the
         // wait's limit is what ends this then.
         volatile int never = 0;
-        const uint32_t n = it < (uint32_t)C::kStages ? it : (uint32_t)C::kStages;
+        const uint32_t n = issued < (uint32_t)C::kStages ? issued : (uint32_t)C::kStages;
         for (uint32_t k = 0; k < n; ++k) {
-          const uint32_t i2 = it - 1 - k;
+          const uint32_t i2 = issued - 1 - k;
           tc::mbar_wait(&full[i2 % C::kStages], (i2 / C::kStages) & 1, &never, 100000000ll);
         }
       }
     }
   } else if (warp == 1) {
-    // ---------------- MMAs (second CTA of a pair: its tail stages) ----------------
-    uint32_t it = 0, tcount = 0;
-    uint32_t tails = 0;         // pair: parity, by slot, of the barriers that only tail stages use
-    bool ok = true;
-    for (int u = first; ok && u < U; u += stride, ++tcount) {
-      GTile w;
-      g_tile<MODE, CG>(g, off, uoff, u, w);
-      const int d = tcount & 1;
-      if (rank == 0) {
-        ok = __all_sync(kFull, tc::mbar_wait(&accempty[d], ((tcount >> 1) & 1) ^ 1, abort));
-        if (!ok) break;
+    // ---------------- MMAs ----------------
+    // One thread, whose loop bounds the whole when it is longer than the MMAs:
+    // addresses, descriptors and parities are carried along, not computed.
+    if (lane == 0 && rank == 0) {
+      constexpr uint32_t sta = MODE != kRowsNT ? 2048 / 16 : 32 / 16, stb = kWg ? 2048 / 16 : 32 / 16;
+      const uint64_t ad0 = MODE != kRowsNT ? tc::smem_desc_mn_sw128(sa_u, kGChunk) : tc::smem_desc_sw128(sa_u);
+      const uint64_t bd0 = kWg ? tc::smem_desc_mn_sw128(sb_u, kGChunk) : tc::smem_desc_sw128(sb_u);
+      uint64_t ad = ad0, bd = bd0;
+      int slot = 0;
+      uint32_t phase = 0, tails = 0;     // tails: parity, by slot, of pfull
+      uint32_t tcount = 0;
+      bool ok = true;
+      for (int u = first; ok && u < U; u += stride, ++tcount) {
+        GTile w;
+        g_tile<MODE, CG>(g, off, uoff, u, w);
+        const int d = tcount & 1;
+        if (!tc::mbar_wait(&accempty[d], ((tcount >> 1) & 1) ^ 1, abort)) { ok = false; break; }
         tc::fence_after_sync();
-      }
-      const uint32_t dt = tmem + d * kGN;
-      const uint32_t idesc = tc::idesc_16bit(kGM * CG, w.N, m.dtype == MOE_DT_BF16, MODE != kRowsNT, kWg);
-      for (int kb = w.k0; kb < w.k1; ++kb, ++it) {
-        const int slot = it % C::kStages;
-        const int left = w.red - kb * kGK;          // of the reduction in this stage
-        const int steps = left >= kGK ? 4 : (left + 15) / 16;
-        const bool tail = kWg && g_tail(left);
-        if (rank != 0 && !tail) continue;
-        uint8_t* pa = sa + slot * kGABytes;
-        uint8_t* pb = sb + slot * C::kBBytes;
-        const uint32_t parity = rank != 0 ? (tails >> slot) & 1 : (it / C::kStages) & 1;
-        ok = __all_sync(kFull, tc::mbar_wait(&full[slot], parity, abort));
-        if (!ok) break;
-        if (tail) {
-          // rows of the next group behind the last ones: cleared up to the
-          // MMA's K, a 128-byte line per row and chunk (the swizzle permutes
-          // within a line)
-          const int bad = 16 - (left & 15), chunks = kGM / 64 + w.N / CG / 64;
-          for (int i = lane; i < bad * 8 * chunks; i += 32) {
-            const int q = i & 7, r = left + (i >> 3) % bad, c = (i >> 3) / bad;
-            uint8_t* line = (c < kGM / 64 ? pa + c * kGChunk : pb + (c - kGM / 64) * kGChunk) + r * 128;
-            reinterpret_cast<uint4*>(line)[q] = make_uint4(0u, 0u, 0u, 0u);
-          }
-          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-          __syncwarp();
-          if constexpr (CG == 2) {
-            const uint32_t pp = (tails >> slot) & 1;
+        const uint32_t dt = tmem + d * kGN;
+        const uint32_t idesc = tc::idesc_16bit(kGM * CG, w.N, m.dtype == MOE_DT_BF16, MODE != kRowsNT, kWg);
+        uint32_t acc = 0;
+        int left = w.red - w.k0 * kGK;
+        for (int n = w.k1 - w.k0; n > 0; --n, left -= kGK) {
+          if (!tc::bar_wait(full_u + 8 * slot, phase, abort)) { ok = false; break; }
+          if (kWg && g_tail(left)) {
+            // warp 3 (of both CTAs) clears the rows of the next group
+            tc::mbar_arrive(tgo);
+            if (!tc::bar_wait(pfull_u + 8 * slot, (tails >> slot) & 1, abort)) { ok = false; break; }
             tails ^= 1u << slot;
-            if (rank != 0) {
-              if (lane == 0) tc::mbar_arrive_peer(tc::peer_smem(&pfull[slot], 0));
-              __syncwarp();
-              continue;
-            }
-            ok = __all_sync(kFull, tc::mbar_wait(&pfull[slot], pp, abort));
-            if (!ok) break;
           }
-        }
-        if (lane == 0) {
           tc::fence_after_sync();
-          const uint64_t ad = MODE != kRowsNT ? tc::smem_desc_mn_sw128(tc::smem_u32(pa), kGChunk)
-                                              : tc::smem_desc_sw128(tc::smem_u32(pa));
-          const uint64_t bd = kWg ? tc::smem_desc_mn_sw128(tc::smem_u32(pb), kGChunk)
-                                  : tc::smem_desc_sw128(tc::smem_u32(pb));
           // a step of K = 16: 32 bytes along a K-major row, two 8-row atoms otherwise
-          constexpr uint32_t sta = MODE != kRowsNT ? 2048 / 16 : 32 / 16, stb = kWg ? 2048 / 16 : 32 / 16;
-          for (int j = 0; j < steps; ++j) {
-            const uint32_t acc = (kb > w.k0 || j > 0) ? 1u : 0u;
-            if constexpr (CG == 2) tc::mma_f16_ss_pair(dt, ad + sta * j, bd + stb * j, idesc, acc);
-            else tc::mma_f16_ss(dt, ad + sta * j, bd + stb * j, idesc, acc);
+          const int steps = left >= kGK ? 4 : (left + 15) / 16;
+          if (steps == 4) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              if constexpr (CG == 2) tc::mma_f16_ss_pair(dt, ad + sta * j, bd + stb * j, idesc, j ? 1u : acc);
+              else tc::mma_f16_ss(dt, ad + sta * j, bd + stb * j, idesc, j ? 1u : acc);
+            }
+          } else {
+            for (int j = 0; j < steps; ++j) {
+              if constexpr (CG == 2) tc::mma_f16_ss_pair(dt, ad + sta * j, bd + stb * j, idesc, j ? 1u : acc);
+              else tc::mma_f16_ss(dt, ad + sta * j, bd + stb * j, idesc, j ? 1u : acc);
+            }
           }
-          if constexpr (CG == 2) tc::mma_commit_pair(&empty[slot]);
-          else tc::mma_commit(&empty[slot]);
+          acc = 1;
+          if constexpr (CG == 2) tc::bar_commit_pair(empty_u + 8 * slot);
+          else tc::bar_commit(empty_u + 8 * slot);
+          ad += kGABytes / 16;
+          bd += C::kBBytes / 16;
+          if (++slot == C::kStages) {
+            slot = 0;
+            phase ^= 1;
+            ad = ad0;
+            bd = bd0;
+          }
         }
-        __syncwarp();
-      }
-      if (!ok) break;
-      if (lane == 0 && rank == 0) {
+        if (!ok) break;
         if constexpr (CG == 2) tc::mma_commit_pair(&accfull[d]);
         else tc::mma_commit(&accfull[d]);
       }
-      __syncwarp();
-    }
-    if (lane == 0 && rank == 0) {
       // every MMA of this thread has completed once `drain` fires
       if constexpr (CG == 2) tc::mma_commit_pair(drain);
       else tc::mma_commit(drain);
@@ -365,7 +359,46 @@ __global__ void __launch_bounds__(kGThreads, 1) k_gemm16(const GArgs g, const __
     }
     __syncwarp();
   } else if (warp == 3) {
-    if (!kWg) clear_rows_outside(m, off, lane);
+    if (!kWg) {
+      clear_rows_outside(m, off, lane);
+    } else {
+      // ---------------- tail stages ----------------
+      // Rows behind a group's last ones: cleared up to the MMA's K, a 128-byte
+      // line per row and chunk (the swizzle permutes within a line). This warp
+      // is told of a landed tail stage (`tgo`, by the MMA thread; in the second
+      // CTA of a pair, whose barriers only tail stages use, by the copies): it
+      // would miss phases of a barrier that does not wait for it.
+      int slot = 0;
+      uint32_t told = 0, tails = 0;
+      for (int u = first; u < U; u += stride) {
+        GTile w;
+        g_tile<MODE, CG>(g, off, uoff, u, w);
+        const int n = w.k1 - w.k0, left = w.red - (w.k1 - 1) * kGK;
+        const int at = (slot + n + C::kStages - 1) % C::kStages;     // the piece's last stage
+        slot = (slot + n) % C::kStages;
+        if (n <= 0 || !g_tail(left)) continue;
+        const bool got = rank == 0 ? tc::mbar_wait(tgo, told, abort)
+                                   : tc::mbar_wait(&full[at], (tails >> at) & 1, abort);
+        if (!__all_sync(kFull, got)) break;
+        told ^= 1;
+        tails ^= 1u << at;
+        const int bad = 16 - (left & 15), chunks = kGM / 64 + w.N / CG / 64;
+        uint8_t* pa = sa + at * kGABytes;
+        uint8_t* pb = sb + at * C::kBBytes;
+        for (int i = lane; i < bad * 8 * chunks; i += 32) {
+          const int q = i & 7, r = left + (i >> 3) % bad, c = (i >> 3) / bad;
+          uint8_t* line = (c < kGM / 64 ? pa + c * kGChunk : pb + (c - kGM / 64) * kGChunk) + r * 128;
+          reinterpret_cast<uint4*>(line)[q] = make_uint4(0u, 0u, 0u, 0u);
+        }
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncwarp();
+        if (lane == 0) {
+          if (CG == 2 && rank != 0) tc::mbar_arrive_peer(tc::peer_smem(&pfull[at], 0));
+          else tc::mbar_arrive(&pfull[at]);
+        }
+        __syncwarp();
+      }
+    }
   } else {
     // ---------------- epilogue ----------------
     const int wg = (warp - 4) >> 2, q = warp & 3;

@@ -149,7 +149,7 @@ __global__ void __launch_bounds__(kFThreads, 1) k_gemm_fp8(const FArgs g, const 
             if (!tc::mbar_wait(&empty[slot], ((it / C::kStages) & 1) ^ 1, abort)) { ok = false; break; }
             if (isb) {
               tc::mbar_arrive_expect_tx(&full[slot], C::kBBytes);
-              tc::tma_load_3d_plain(sb + slot * C::kBBytes, &maps.b, kb * kFK, w.n0, w.e, &full[slot]);
+              tc::tma_load_3d_at(tc::smem_u32(sb + slot * C::kBBytes), &maps.b, kb * kFK, w.n0, w.e, tc::smem_u32(&full[slot]));
             } else {
               tc::mbar_arrive_expect_tx(&full[slot], (uint32_t)(kFK * (16 << ai)));
               tc::tma_load_2d_plain(sa + slot * kFABytes, &maps.a[ai], kb * kFK, w.row0, &full[slot]);
