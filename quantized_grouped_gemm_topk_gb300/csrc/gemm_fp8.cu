@@ -131,36 +131,41 @@ __global__ void __launch_bounds__(kFThreads, 1) k_gemm_fp8(const FArgs g, const 
 
   if (warp < 4) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kFRegsLow));
+    // the single-thread loops below bound the whole where they are longer than
+    // the MMAs: addresses and parities are carried along, not computed
+    const uint32_t full_u = tc::smem_u32(full), empty_u = tc::smem_u32(empty);
+    const uint32_t sa_u = tc::smem_u32(sa), sb_u = tc::smem_u32(sb);
     if (warp == 0 || warp == 2) {
       // ---------------- copies: warp 0 W, warp 2 x ----------------
       if (lane == 0) {
         const bool isb = warp == 0;
-        if (isb) tc::prefetch_tmap(&maps.b);
-        else
-          for (int i = 0; i < 4; ++i) tc::prefetch_tmap(&maps.a[i]);
-        uint32_t it = 0;
+        const uint32_t dst0 = isb ? sb_u : sa_u, step = isb ? C::kBBytes : kFABytes;
+        int slot = 0;
+        uint32_t phase = 1, issued = 0;          // of empty: the ring starts free
         bool ok = true;
         for (int u = blockIdx.x; ok && u < U; u += gridDim.x) {
           GUnit w;
           f_unit<BN>(m, g.n_tiles, off, uoff, u, w);
           const int ai = f_a_box(w.rows);
-          for (int kb = w.k0; kb < w.k1; ++kb, ++it) {
-            const int slot = it % C::kStages;
-            if (!tc::mbar_wait(&empty[slot], ((it / C::kStages) & 1) ^ 1, abort)) { ok = false; break; }
-            if (isb) {
-              tc::mbar_arrive_expect_tx(&full[slot], C::kBBytes);
-              tc::tma_load_3d_at(tc::smem_u32(sb + slot * C::kBBytes), &maps.b, kb * kFK, w.n0, w.e, tc::smem_u32(&full[slot]));
-            } else {
-              tc::mbar_arrive_expect_tx(&full[slot], (uint32_t)(kFK * (16 << ai)));
-              tc::tma_load_2d_plain(sa + slot * kFABytes, &maps.a[ai], kb * kFK, w.row0, &full[slot]);
+          const uint32_t bytes = isb ? C::kBBytes : (uint32_t)(kFK * (16 << ai));
+          for (int kb = w.k0; kb < w.k1; ++kb) {
+            if (!tc::bar_wait(empty_u + 8 * slot, phase, abort)) { ok = false; break; }
+            const uint32_t bar = full_u + 8 * slot;
+            tc::bar_arrive_expect_tx(bar, bytes);
+            if (isb) tc::tma_load_3d_at(dst0 + slot * step, &maps.b, kb * kFK, w.n0, w.e, bar);
+            else tc::tma_load_2d_at(dst0 + slot * step, &maps.a[ai], kb * kFK, w.row0, bar);
+            ++issued;
+            if (++slot == C::kStages) {
+              slot = 0;
+              phase ^= 1;
             }
           }
         }
         if (!ok || *abort) {        // wind-down: bounded waits for the copies in flight
           volatile int never = 0;
-          const uint32_t n = it < (uint32_t)C::kStages ? it : (uint32_t)C::kStages;
+          const uint32_t n = issued < (uint32_t)C::kStages ? issued : (uint32_t)C::kStages;
           for (uint32_t k = 0; k < n; ++k) {
-            const uint32_t i2 = it - 1 - k;
+            const uint32_t i2 = issued - 1 - k;
             tc::mbar_wait(&full[i2 % C::kStages], (i2 / C::kStages) & 1, &never, 100000000ll);
           }
         }
@@ -172,25 +177,42 @@ __global__ void __launch_bounds__(kFThreads, 1) k_gemm_fp8(const FArgs g, const 
       if (lane == 0 && h < C::kHalves) {
         // kind::f8f6f4: E4M3 is format 0 of both operands; fp32 accumulator
         constexpr uint32_t idesc = tc::idesc_f16_f32(kGM, C::kHN);
-        uint64_t* hfull = tfull + h * C::kSlots;
-        uint64_t* hempty = tempty + h * C::kSlots;
-        uint32_t it = 0;
+        const uint32_t tfull_u = tc::smem_u32(tfull + h * C::kSlots), tempty_u = tc::smem_u32(tempty + h * C::kSlots);
+        const uint64_t ad0 = tc::smem_desc_sw128(sa_u), bd0 = tc::smem_desc_sw128(sb_u + h * C::kHN * kFK);
+        uint64_t ad = ad0, bd = bd0;
+        uint32_t slot_b = 0, phase = 0;          // the stage's barriers' offset, its parity
+        uint32_t ts_b = 0, tphase = 1;           // the same of the accumulator's
+        const uint32_t t0 = tmem + h * C::kHN;
+        uint32_t dt = t0;
         bool ok = true;
         for (int u = blockIdx.x; ok && u < U; u += gridDim.x) {
           GUnit w;
           f_unit<BN>(m, g.n_tiles, off, uoff, u, w);
-          for (int kb = w.k0; kb < w.k1; ++kb, ++it) {
-            const int slot = it % C::kStages, ts = it % C::kSlots;
-            if (!tc::mbar_wait(&hempty[ts], ((it / C::kSlots) & 1) ^ 1, abort)) { ok = false; break; }
-            if (!tc::mbar_wait(&full[slot], (it / C::kStages) & 1, abort)) { ok = false; break; }
+          for (int n = w.k1 - w.k0; n > 0; --n) {
+            if (!tc::bar_wait(full_u + slot_b, phase, abort)) { ok = false; break; }
+            if (!tc::bar_wait(tempty_u + ts_b, tphase, abort)) { ok = false; break; }
             tc::fence_after_sync();
-            const uint64_t ad = tc::smem_desc_sw128(tc::smem_u32(sa + slot * kFABytes));
-            const uint64_t bd = tc::smem_desc_sw128(tc::smem_u32(sb + slot * C::kBBytes + h * C::kHN * kFK));
 #pragma unroll
             for (int j = 0; j < 4; ++j)     // K = 32: 32 bytes along the rows; past K both read as zero
-              tc::mma_f8_ss(tmem + ts * BN + h * C::kHN, ad + 2 * j, bd + 2 * j, idesc, j > 0 ? 1u : 0u);
-            tc::mma_commit(&empty[slot]);
-            tc::mma_commit(&hfull[ts]);
+              tc::mma_f8_ss(dt, ad + 2 * j, bd + 2 * j, idesc, j > 0 ? 1u : 0u);
+            tc::bar_commit(tfull_u + ts_b);
+            tc::bar_commit(empty_u + slot_b);
+            ad += kFABytes / 16;
+            bd += C::kBBytes / 16;
+            slot_b += 8;
+            if (slot_b == 8 * C::kStages) {
+              slot_b = 0;
+              phase ^= 1;
+              ad = ad0;
+              bd = bd0;
+            }
+            ts_b += 8;
+            dt += BN;
+            if (ts_b == 8 * C::kSlots) {
+              ts_b = 0;
+              tphase ^= 1;
+              dt = t0;
+            }
           }
         }
         tc::mma_commit(&drain[h]);
@@ -205,48 +227,51 @@ __global__ void __launch_bounds__(kFThreads, 1) k_gemm_fp8(const FArgs g, const 
     constexpr int kCols = BN / 4, kChunks = kCols / 16;
     const int h = (warp - 4) >> 2, q = warp & 3;
     const uint32_t lanes = tmem + ((uint32_t)(q * 32) << 16) + h * kCols;
-    uint64_t* hfull = tfull + h * C::kHalves / 4 * C::kSlots;
-    uint64_t* hempty = tempty + h * C::kHalves / 4 * C::kSlots;
+    const uint32_t hfull = tc::smem_u32(tfull + h * C::kHalves / 4 * C::kSlots);
+    const uint32_t hempty = tc::smem_u32(tempty + h * C::kHalves / 4 * C::kSlots);
+    uint32_t ts = 0, tphase = 0;       // the accumulator's slot and parity
     const int KB = (m.K + kFK - 1) / kFK, NB = (m.N + kQBlock - 1) / kQBlock;
     const int dt = m.S > 1 ? MOE_DT_F32 : m.out_dtype;
     const int esize = dt == MOE_DT_F32 ? 4 : 2;
     const int64_t ld = m.S > 1 ? m.N : m.ldo, os = (int64_t)m.R * m.N;
     uint8_t* obase = reinterpret_cast<uint8_t*>(m.S > 1 ? (void*)m.part : m.out);
     const bool vec = ((uintptr_t)obase & 15) == 0 && (ld * esize) % 16 == 0 && (m.S == 1 || (os * 4) % 16 == 0);
-    uint32_t it = 0;
+    const int r = q * 32 + lane;
     bool ok = true;
-    for (int u = blockIdx.x; ok && u < U; u += gridDim.x) {
-      GUnit w;
+    GUnit w;
+    const float *xs = nullptr, *ws = nullptr;
+    // The scales of the next four blocks are on their way, each in registers
+    // of its own: a copy from register to register would wait for the load. A
+    // tile's first ones are loaded before the last tile is stored.
+    float s[4], t[4];
+    auto begin = [&](int u) {
       f_unit<BN>(m, g.n_tiles, off, uoff, u, w);
-      const int r = q * 32 + lane;
-      const bool live = r < w.rows;
-      const float* xs = m.sa + (int64_t)(w.row0 + (live ? r : 0)) * m.ldsa;
+      xs = m.sa + (int64_t)(w.row0 + (r < w.rows ? r : 0)) * m.ldsa;
       const int nb = min((w.n0 + h * kCols) / kQBlock, NB - 1);     // past N: nothing is stored
-      const float* ws = m.sb + ((int64_t)w.e * NB + nb) * KB;
-      float acc[kCols];
-#pragma unroll
-      for (int i = 0; i < kCols; ++i) acc[i] = 0.f;
-      // The scales of the next four blocks are on their way, each in registers
-      // of its own: a copy from register to register would wait for the load.
-      float s[4], t[4];
+      ws = m.sb + ((int64_t)w.e * NB + nb) * KB;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const bool in = w.k0 + j < w.k1;
         s[j] = in ? xs[w.k0 + j] : 0.f;
         t[j] = in ? ws[w.k0 + j] : 0.f;
       }
+    };
+    if ((int)blockIdx.x < U) begin(blockIdx.x);
+    for (int u = blockIdx.x; u < U; u += gridDim.x) {
+      float acc[kCols];
+#pragma unroll
+      for (int i = 0; i < kCols; ++i) acc[i] = 0.f;
       for (int kb0 = w.k0; kb0 < w.k1; kb0 += 4) {
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           const int kb = kb0 + j;
           if (kb < w.k1 && ok) {
-            const int ts = it % C::kSlots;
             const float sc = s[j] * t[j];
             if (kb + 4 < w.k1) {
               s[j] = xs[kb + 4];
               t[j] = ws[kb + 4];
             }
-            ok = __all_sync(kFull, tc::mbar_wait(&hfull[ts], (it / C::kSlots) & 1, abort));
+            ok = __all_sync(kFull, tc::bar_wait_inline(hfull + 8 * ts, tphase, abort));
             if (ok) {
               tc::fence_after_sync();
               const uint32_t at = lanes + ts * BN;
@@ -261,28 +286,34 @@ __global__ void __launch_bounds__(kFThreads, 1) k_gemm_fp8(const FArgs g, const 
                 } else {
                   tc::fence_before_sync();
                   __syncwarp();
-                  if (lane == 0) tc::mbar_arrive(&hempty[ts]);
+                  if (lane == 0) tc::bar_arrive(hempty + 8 * ts);
                 }
 #pragma unroll
                 for (int i = 0; i < 16; ++i)
                   acc[c * 16 + i] = fmaf(__uint_as_float(v[c & 1][i]), sc, acc[c * 16 + i]);
               }
-              ++it;
+              if (++ts == C::kSlots) {
+                ts = 0;
+                tphase ^= 1;
+              }
             }
           }
         }
       }
       if (!ok) break;
-      if (live) {
-        const int64_t row = (int64_t)(w.row0 + r) * ld + w.piece * (m.S > 1 ? os : 0);
+      const int col = w.n0 + h * kCols, rows = w.rows - q * 32;
+      const int64_t row = (int64_t)(w.row0 + q * 32) * ld + (m.S > 1 ? w.piece * os : 0);
+      if (u + (int)gridDim.x < U) begin(u + gridDim.x);
+      if (vec && col + kCols <= m.N) {
+        store_block<kCols>(obase + (row + col) * esize, ld * esize, acc, rows, lane, dt);
+      } else if (lane < rows) {
 #pragma unroll
         for (int c = 0; c < kChunks; ++c) {
-          const int col = w.n0 + h * kCols + 16 * c;
-          if (col < m.N) {
+          if (col + 16 * c < m.N) {
             uint32_t v[16];
 #pragma unroll
             for (int i = 0; i < 16; ++i) v[i] = __float_as_uint(acc[c * 16 + i]);
-            store_cols(obase + (row + col) * esize, v, m.N - col, dt, vec);
+            store_cols(obase + (row + lane * ld + col + 16 * c) * esize, v, m.N - col - 16 * c, dt, vec);
           }
         }
       }

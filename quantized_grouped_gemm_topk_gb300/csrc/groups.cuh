@@ -144,6 +144,58 @@ __device__ __forceinline__ void store_cols(void* p, const uint32_t (&v)[C], int 
   }
 }
 
+// A warp's 32 rows x C columns (lane = row, v the row's fp32 bits) to row-major
+// out, 16-byte accesses. A lane's own row would make every store touch 32
+// lines; instead NU = units of 16 bytes in a row's C columns are exchanged
+// among NU lanes (a transpose in log2 NU steps), so that a store covers whole
+// segments of 16 NU bytes of 32 / NU rows. p: the first row's first column;
+// rows < n_rows are written.
+template <int C, typename Conv>
+__device__ __forceinline__ void store_block16(uint8_t* p, int64_t row_bytes, const float (&v)[C], int n_rows, int lane,
+                                              Conv conv) {
+  constexpr int NU = C / 8;
+  uint32_t w[NU][4];
+#pragma unroll
+  for (int i = 0; i < NU; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) w[i][j] = conv(v[8 * i + 2 * j], v[8 * i + 2 * j + 1]);
+#pragma unroll
+  for (int s = 1; s < NU; s <<= 1) {
+    const bool up = lane & s;
+#pragma unroll
+    for (int i = 0; i < NU; ++i) {
+      if (i & s) continue;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const uint32_t got = __shfl_xor_sync(kFull, up ? w[i][j] : w[i | s][j], s);
+        w[i][j] = up ? got : w[i][j];
+        w[i | s][j] = up ? w[i | s][j] : got;
+      }
+    }
+  }
+  const int r0 = lane & ~(NU - 1);
+  uint8_t* d = p + r0 * row_bytes + (lane & (NU - 1)) * 16;
+#pragma unroll
+  for (int i = 0; i < NU; ++i)
+    if (r0 + i < n_rows) *reinterpret_cast<uint4*>(d + i * row_bytes) = make_uint4(w[i][0], w[i][1], w[i][2], w[i][3]);
+}
+template <int C>
+__device__ __forceinline__ void store_block(uint8_t* p, int64_t row_bytes, const float (&v)[C], int n_rows, int lane,
+                                            int out_dtype) {
+  if (out_dtype == MOE_DT_BF16) {
+    store_block16<C>(p, row_bytes, v, n_rows, lane, [](float a, float b) { return Bf16::from2(a, b); });
+  } else if (out_dtype == MOE_DT_F16) {
+    store_block16<C>(p, row_bytes, v, n_rows, lane, [](float a, float b) { return F16::from2(a, b); });
+  } else {
+    // fp32 results are partial sums and small products: a lane stores its row
+#pragma unroll
+    for (int i = 0; i < C / 4; ++i)
+      if (lane < n_rows)
+        *reinterpret_cast<float4*>(p + lane * row_bytes + 16 * i) =
+            make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+  }
+}
+
 // Rows outside every group become zeros (their partial sums, where the product
 // is split). One warp of each CTA.
 __device__ __forceinline__ void clear_rows_outside(const MmArgs& m, const int32_t* off, int lane) {

@@ -101,10 +101,26 @@ static __device__ __noinline__ bool bar_wait_slow(uint32_t bar, uint32_t parity,
     }
   }
 }
+// Without a call, for warps whose registers are all taken.
+__device__ __forceinline__ bool bar_wait_inline(uint32_t bar, uint32_t parity, volatile int* abort) {
+  if (bar_try_wait(bar, parity)) return true;
+  const long long t0 = clock64();
+  while (!bar_try_wait(bar, parity)) {
+    if (*abort) return false;
+    if (clock64() - t0 > 4000000000ll) {
+      *abort = 1;
+      return false;
+    }
+  }
+  return true;
+}
 __device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, volatile int* abort) {
   if (bar_try_wait(bar, parity)) return true;
   if (bar_try_wait(bar, parity)) return true;
   return bar_wait_slow(bar, parity, abort);
+}
+__device__ __forceinline__ void bar_arrive(uint32_t bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 __device__ __forceinline__ void bar_arrive_expect_tx(uint32_t bar, uint32_t bytes) {
   asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
