@@ -14,10 +14,15 @@
 // Bound: the tensor pipe at training sizes (a 128 x 256 x 128 block is 512
 // cycles of MMA, its additions 256 issue slots a scheduler at most), the
 // weights' bytes at decode sizes.
-// Tiles, copies and edges as in gemm16.cu. Roles: warp 0 copies W, warp 2
-// copies x, warp 1 issues MMAs, warp 3 clears rows outside every group, warps
-// 4-19 add: warp quarter q of tensor memory, quarter h of the columns (four
-// warps a scheduler: with two, the reads' latency showed). They take registers from the first four warps (setmaxnreg).
+// Measured at 8192^3: 511 us (2.15 PFLOP/s), 1000 cycles a block; without the
+// additions 816, without them and three of the four MMAs 670 (the copies:
+// 48 KB at what an SM takes in). The slots' round trip is what shows.
+// Tiles are 128 rows x BN columns on one SM; copies and edges as in gemm16.cu.
+// Roles: warp 0 copies W, warp 2 copies x, warps 1 and 3 issue the MMAs of the
+// tile's halves (warp 3 first clears rows outside every group), warps 4-11
+// add: warp quarter q of tensor memory, half h of the columns (eight warps of
+// 128 columns took 511 us there, sixteen of 64 columns 549). They take
+// registers from the first four warps (setmaxnreg).
 // Every wait is bounded, as in gemm16.cu.
 #include "groups.cuh"
 #include "tc.cuh"
@@ -25,14 +30,14 @@
 namespace moe {
 
 constexpr int kFK = kQBlock;              // reduction a stage: one scale block, one 128-byte swizzle row
-constexpr int kFThreads = 640;
+constexpr int kFThreads = 384;
 constexpr int kFABytes = kGM * kFK;
 constexpr int kFTables = 2 * 4 * (kMmMaxGroups + 1);
-// Registers a thread: at launch, then of warps 0-3 and of warps 4-19. The
+// Registers a thread: at launch, then of warps 0-3 and of warps 4-11. The
 // shares sum to at most the launch's (checked against the built kernel
 // before its first launch).
-constexpr int kFRegs = 96, kFRegsLow = 64, kFRegsHigh = 104;
-static_assert(128 * kFRegsLow + 512 * kFRegsHigh <= kFThreads * kFRegs, "register shares");
+constexpr int kFRegs = 168, kFRegsLow = 80, kFRegsHigh = 208;
+static_assert(128 * kFRegsLow + 256 * kFRegsHigh <= kFThreads * kFRegs, "register shares");
 
 template <int BN>
 struct FCfg {
@@ -115,7 +120,7 @@ __global__ void __launch_bounds__(kFThreads, 1) k_gemm_fp8(const FArgs g, const 
     }
     for (int i = 0; i < C::kHalves * C::kSlots; ++i) {
       tc::mbar_init(&tfull[i], 1);
-      tc::mbar_init(&tempty[i], 16 / C::kHalves);     // one per adding warp
+      tc::mbar_init(&tempty[i], 8 / C::kHalves);     // one per adding warp
     }
     for (int i = 0; i < C::kHalves; ++i) tc::mbar_init(&drain[i], 1);
     *abort = 0;
@@ -224,11 +229,11 @@ __global__ void __launch_bounds__(kFThreads, 1) k_gemm_fp8(const FArgs g, const 
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kFRegsHigh));
     // ---------------- sums of the blocks ----------------
-    constexpr int kCols = BN / 4, kChunks = kCols / 16;
+    constexpr int kCols = BN / 2, kChunks = kCols / 16;
     const int h = (warp - 4) >> 2, q = warp & 3;
     const uint32_t lanes = tmem + ((uint32_t)(q * 32) << 16) + h * kCols;
-    const uint32_t hfull = tc::smem_u32(tfull + h * C::kHalves / 4 * C::kSlots);
-    const uint32_t hempty = tc::smem_u32(tempty + h * C::kHalves / 4 * C::kSlots);
+    const uint32_t hfull = tc::smem_u32(tfull + h * C::kHalves / 2 * C::kSlots);
+    const uint32_t hempty = tc::smem_u32(tempty + h * C::kHalves / 2 * C::kSlots);
     uint32_t ts = 0, tphase = 0;       // the accumulator's slot and parity
     const int KB = (m.K + kFK - 1) / kFK, NB = (m.N + kQBlock - 1) / kQBlock;
     const int dt = m.S > 1 ? MOE_DT_F32 : m.out_dtype;
@@ -354,7 +359,7 @@ static cudaError_t launch_f(FArgs g, cudaStream_t st) {
     if (e != cudaSuccess) return e;
     regs.store(at.numRegs, std::memory_order_release);
   }
-  if (128 * kFRegsLow + 512 * kFRegsHigh > kFThreads * regs.load()) return cudaErrorInvalidConfiguration;
+  if (128 * kFRegsLow + 256 * kFRegsHigh > kFThreads * regs.load()) return cudaErrorInvalidConfiguration;
   if (!units_fit(m, m.R / kGM, g.n_tiles)) return cudaErrorInvalidValue;
   static std::atomic<bool> done[kMaxDevices] = {};
   cudaError_t e = set_smem_once((const void*)k_gemm_fp8<BN>, C::kSmem, done);
