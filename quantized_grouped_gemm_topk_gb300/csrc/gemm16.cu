@@ -48,15 +48,9 @@ constexpr int kGN = 256;              // widest tile
 constexpr int kGThreads = 384;
 constexpr int kGChunk = 64 * kGK * 2; // bytes of 64 M / N elements of an MN-contiguous stage
 constexpr int kGABytes = kGM * kGK * 2;
-constexpr int kGTables = 2 * 4 * (kMmMaxGroups + 1);
-
-template <int CG>
-struct GCfg {
-  static constexpr int kBBytes = kGN / CG * kGK * 2;
-  static constexpr int kStages = CG == 2 ? 6 : 4;
-  static constexpr int kSmem = 1024 + kStages * (kGABytes + kBBytes) + 1024 + kGTables;
-  static_assert(kSmem <= 227 * 1024, "shared memory budget");
-};
+constexpr int kGHeadBars = 512;       // barriers and scratch, in front of the group tables
+constexpr int kGMaxStages = 12;
+constexpr int kGSmem = 227 * 1024;
 
 constexpr int kGBoxes = 5;            // K-major B: boxes of 16 << i rows
 struct GMaps {
@@ -66,6 +60,9 @@ struct GMaps {
 struct GArgs {
   MmArgs m;
   int bn;               // widest N of a tile
+  int stages;           // of the ring, each kGABytes + b_bytes
+  int b_bytes;
+  int head;             // bytes in front of the ring
   int m_tiles;          // tiles of 128 CG features
   int n_tiles;          // weight gradient: bn-wide column tiles
   int a_chunks, b_chunks;   // MN-contiguous operands: 64-wide chunks a copy takes (1: one copy a chunk)
@@ -174,31 +171,31 @@ __device__ __forceinline__ void store_tokens16(uint16_t* out, int64_t ld, const 
 
 template <int MODE, int CG>
 __global__ void __launch_bounds__(kGThreads, 1) k_gemm16(const GArgs g, const __grid_constant__ GMaps maps) {
-  using C = GCfg<CG>;
   constexpr bool kWg = MODE == kWgradMN;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* base = reinterpret_cast<uint8_t*>(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
-  uint8_t* sa = base;
-  uint8_t* sb = sa + C::kStages * kGABytes;
-  uint64_t* full = reinterpret_cast<uint64_t*>(sb + C::kStages * C::kBBytes);
-  uint64_t* pfull = full + C::kStages;          // weight gradient: the rows of a tail stage are cleared
-  uint64_t* empty = pfull + C::kStages;
-  uint64_t* accfull = empty + C::kStages;
+  const int stages = g.stages, b_bytes = g.b_bytes;
+  uint8_t* sa = base + g.head;
+  uint8_t* sb = sa + stages * kGABytes;
+  uint64_t* full = reinterpret_cast<uint64_t*>(base);
+  uint64_t* pfull = full + kGMaxStages;         // weight gradient: the rows of a tail stage are cleared
+  uint64_t* empty = pfull + kGMaxStages;
+  uint64_t* accfull = empty + kGMaxStages;
   uint64_t* accempty = accfull + 2;
   uint64_t* drain = accempty + 2;
   uint64_t* tgo = drain + 1;                    // weight gradient: a tail stage has landed
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(tgo + 1);
   volatile int* abort = reinterpret_cast<volatile int*>(tmem_slot + 1);
   int* tmp = reinterpret_cast<int*>(tmem_slot + 2);
-  int32_t* off = reinterpret_cast<int32_t*>(reinterpret_cast<uint8_t*>(full) + 1024);
-  int32_t* uoff = off + kMmMaxGroups + 1;
+  int32_t* off = reinterpret_cast<int32_t*>(base + kGHeadBars);
+  int32_t* uoff = off + g.m.G + 1;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const MmArgs& m = g.m;
   const int rank = CG == 2 ? (int)tc::cluster_rank() : 0;
   const int first = blockIdx.x / CG, stride = gridDim.x / CG;
 
   if (threadIdx.x == 0) {
-    for (int i = 0; i < C::kStages; ++i) {
+    for (int i = 0; i < stages; ++i) {
       tc::mbar_init(&full[i], 2);       // one arrival (with its bytes) from each copying warp
       tc::mbar_init(&pfull[i], CG);
       tc::mbar_init(&empty[i], 1);
@@ -237,7 +234,7 @@ __global__ void __launch_bounds__(kGThreads, 1) k_gemm16(const GArgs g, const __
     // ---------------- copies: warp 0 B, warp 2 A ----------------
     if (lane == 0) {
       const bool isb = warp == 0;
-      const uint32_t dst0 = isb ? sb_u : sa_u, step = isb ? C::kBBytes : kGABytes;
+      const uint32_t dst0 = isb ? sb_u : sa_u, step = isb ? b_bytes : kGABytes;
       // both CTAs' copies report to the first one's barriers, which expect them
       // all; those of a tail stage, where each CTA has rows to clear first, to
       // their own CTA's
@@ -269,7 +266,7 @@ __global__ void __launch_bounds__(kGThreads, 1) k_gemm16(const GArgs g, const __
             else g_copy_mn<CG>(dst, map, m0, kWg ? r0 + k : k, kWg ? 0 : w.e, kGM / 64, g.a_chunks > 1, bar);
           }
           ++issued;
-          if (++slot == C::kStages) {
+          if (++slot == stages) {
             slot = 0;
             phase ^= 1;
           }
@@ -282,10 +279,10 @@ __global__ void __launch_bounds__(kGThreads, 1) k_gemm16(const GArgs g, const __
         // earlier (and the second CTA of a pair reports elsewhere), so the
         // wait's limit is what ends this then.
         volatile int never = 0;
-        const uint32_t n = issued < (uint32_t)C::kStages ? issued : (uint32_t)C::kStages;
+        const uint32_t n = issued < (uint32_t)stages ? issued : (uint32_t)stages;
         for (uint32_t k = 0; k < n; ++k) {
           const uint32_t i2 = issued - 1 - k;
-          tc::mbar_wait(&full[i2 % C::kStages], (i2 / C::kStages) & 1, &never, 100000000ll);
+          tc::mbar_wait(&full[i2 % stages], (i2 / stages) & 1, &never, 100000000ll);
         }
       }
     }
@@ -297,6 +294,7 @@ __global__ void __launch_bounds__(kGThreads, 1) k_gemm16(const GArgs g, const __
       constexpr uint32_t sta = MODE != kRowsNT ? 2048 / 16 : 32 / 16, stb = kWg ? 2048 / 16 : 32 / 16;
       const uint64_t ad0 = MODE != kRowsNT ? tc::smem_desc_mn_sw128(sa_u, kGChunk) : tc::smem_desc_sw128(sa_u);
       const uint64_t bd0 = kWg ? tc::smem_desc_mn_sw128(sb_u, kGChunk) : tc::smem_desc_sw128(sb_u);
+      const uint64_t b_step = b_bytes / 16;
       uint64_t ad = ad0, bd = bd0;
       int slot = 0;
       uint32_t phase = 0, tails = 0;     // tails: parity, by slot, of pfull
@@ -339,8 +337,8 @@ __global__ void __launch_bounds__(kGThreads, 1) k_gemm16(const GArgs g, const __
           if constexpr (CG == 2) tc::bar_commit_pair(empty_u + 8 * slot);
           else tc::bar_commit(empty_u + 8 * slot);
           ad += kGABytes / 16;
-          bd += C::kBBytes / 16;
-          if (++slot == C::kStages) {
+          bd += b_step;
+          if (++slot == stages) {
             slot = 0;
             phase ^= 1;
             ad = ad0;
@@ -374,8 +372,8 @@ __global__ void __launch_bounds__(kGThreads, 1) k_gemm16(const GArgs g, const __
         GTile w;
         g_tile<MODE, CG>(g, off, uoff, u, w);
         const int n = w.k1 - w.k0, left = w.red - (w.k1 - 1) * kGK;
-        const int at = (slot + n + C::kStages - 1) % C::kStages;     // the piece's last stage
-        slot = (slot + n) % C::kStages;
+        const int at = (slot + n + stages - 1) % stages;     // the piece's last stage
+        slot = (slot + n) % stages;
         if (n <= 0 || !g_tail(left)) continue;
         const bool got = rank == 0 ? tc::mbar_wait(tgo, told, abort)
                                    : tc::mbar_wait(&full[at], (tails >> at) & 1, abort);
@@ -384,7 +382,7 @@ __global__ void __launch_bounds__(kGThreads, 1) k_gemm16(const GArgs g, const __
         tails ^= 1u << at;
         const int bad = 16 - (left & 15), chunks = kGM / 64 + w.N / CG / 64;
         uint8_t* pa = sa + at * kGABytes;
-        uint8_t* pb = sb + at * C::kBBytes;
+        uint8_t* pb = sb + at * b_bytes;
         for (int i = lane; i < bad * 8 * chunks; i += 32) {
           const int q = i & 7, r = left + (i >> 3) % bad, c = (i >> 3) / bad;
           uint8_t* line = (c < kGM / 64 ? pa + c * kGChunk : pb + (c - kGM / 64) * kGChunk) + r * 128;
@@ -529,6 +527,8 @@ MmPlan mm_plan(int kind, int R, int N, int K, int G) {
     // pairs of SMs where there is a tile for each of them, except at a few
     // rows a group, which stream weights
     p.cg = count(2, 256) >= kPlanSms / 2 && (wg || R >= 64ll * std::min(G, R)) ? 2 : 1;
+    // (and whose stages are small then: more of them in flight)
+    if (!wg && R <= 32ll * std::min(G, R)) p.bn = 64;
     while (p.cg == 1 && p.bn > 64 && count(1, p.bn) < kPlanSms) p.bn /= 2;
     units = count(p.cg, p.bn);
   }
@@ -591,9 +591,15 @@ static int make_mn(CUtensorMap* map, const void* base, int64_t rows, int64_t col
 
 template <int MODE, int CG>
 static cudaError_t launch_g(GArgs g, cudaStream_t st) {
-  using C = GCfg<CG>;
   const MmArgs& m = g.m;
   constexpr bool kWg = MODE == kWgradMN;
+  // As many stages as fit: the ring's round trip (copy, MMAs, release) is
+  // longer than a few stages' MMAs. With six stages of 32 KB a stage took 595
+  // cycles on a pair of SMs, not the MMAs' 512.
+  g.b_bytes = g.bn / CG * kGK * 2;
+  g.head = (kGHeadBars + 2 * 4 * (m.G + 1) + 1023) / 1024 * 1024;
+  g.stages = std::min(kGMaxStages, (kGSmem - 1024 - g.head) / (kGABytes + g.b_bytes));
+  const int smem = 1024 + g.head + g.stages * (kGABytes + g.b_bytes);
   GMaps maps;
   const int64_t rows = std::max(m.R, 1);
   g.m_tiles = (int)tiles(m.N, kGM * CG);
@@ -623,15 +629,15 @@ static cudaError_t launch_g(GArgs g, cudaStream_t st) {
   if (!units_fit(m, kWg ? (int64_t)m.G * g.m_tiles : m.R / g.bn, kWg ? g.n_tiles : g.m_tiles))
     return cudaErrorInvalidValue;
   static std::atomic<bool> done[kMaxDevices] = {};
-  cudaError_t e = set_smem_once((const void*)k_gemm16<MODE, CG>, C::kSmem, done);
+  cudaError_t e = set_smem_once((const void*)k_gemm16<MODE, CG>, kGSmem, done);
   if (e != cudaSuccess) return e;
   note_launch();
   if constexpr (CG == 1) {
-    e = launch_pdl(k_gemm16<MODE, CG>, dim3(device_sms()), dim3(kGThreads), C::kSmem, st, g, maps);
+    e = launch_pdl(k_gemm16<MODE, CG>, dim3(device_sms()), dim3(kGThreads), smem, st, g, maps);
   } else {
     cudaLaunchConfig_t cfg = {};
     cfg.blockDim = dim3(kGThreads);
-    cfg.dynamicSmemBytes = C::kSmem;
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;
