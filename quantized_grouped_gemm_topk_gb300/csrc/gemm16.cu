@@ -294,12 +294,12 @@ __global__ void __launch_bounds__(kGThreads, 1) k_gemm16(const GArgs g, const __
       constexpr uint32_t sta = MODE != kRowsNT ? 2048 / 16 : 32 / 16, stb = kWg ? 2048 / 16 : 32 / 16;
       const uint64_t ad0 = MODE != kRowsNT ? tc::smem_desc_mn_sw128(sa_u, kGChunk) : tc::smem_desc_sw128(sa_u);
       const uint64_t bd0 = kWg ? tc::smem_desc_mn_sw128(sb_u, kGChunk) : tc::smem_desc_sw128(sb_u);
-      const uint64_t b_step = b_bytes / 16;
-      uint64_t ad = ad0, bd = bd0;
+      const uint32_t a_hi = (uint32_t)(ad0 >> 32), b_hi = (uint32_t)(bd0 >> 32), a_step = kGABytes / 16, b_step = b_bytes / 16;
+      uint32_t ad = (uint32_t)ad0, bd = (uint32_t)bd0;
       int slot = 0;
       uint32_t phase = 0, tails = 0;     // tails: parity, by slot, of pfull
       uint32_t tcount = 0;
-      bool ok = true;
+      bool ok = true, ready = false;     // ready: the next stage is known to have landed
       for (int u = first; ok && u < U; u += stride, ++tcount) {
         GTile w;
         g_tile<MODE, CG>(g, off, uoff, u, w);
@@ -311,39 +311,41 @@ __global__ void __launch_bounds__(kGThreads, 1) k_gemm16(const GArgs g, const __
         uint32_t acc = 0;
         int left = w.red - w.k0 * kGK;
         for (int n = w.k1 - w.k0; n > 0; --n, left -= kGK) {
-          if (!tc::bar_wait(full_u + 8 * slot, phase, abort)) { ok = false; break; }
-          if (kWg && g_tail(left)) {
-            // warp 3 (of both CTAs) clears the rows of the next group
-            tc::mbar_arrive(tgo);
-            if (!tc::bar_wait(pfull_u + 8 * slot, (tails >> slot) & 1, abort)) { ok = false; break; }
-            tails ^= 1u << slot;
-          }
-          tc::fence_after_sync();
-          // a step of K = 16: 32 bytes along a K-major row, two 8-row atoms otherwise
-          const int steps = left >= kGK ? 4 : (left + 15) / 16;
-          if (steps == 4) {
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              if constexpr (CG == 2) tc::mma_f16_ss_pair(dt, ad + sta * j, bd + stb * j, idesc, j ? 1u : acc);
-              else tc::mma_f16_ss(dt, ad + sta * j, bd + stb * j, idesc, j ? 1u : acc);
-            }
-          } else {
-            for (int j = 0; j < steps; ++j) {
-              if constexpr (CG == 2) tc::mma_f16_ss_pair(dt, ad + sta * j, bd + stb * j, idesc, j ? 1u : acc);
-              else tc::mma_f16_ss(dt, ad + sta * j, bd + stb * j, idesc, j ? 1u : acc);
-            }
-          }
-          acc = 1;
-          if constexpr (CG == 2) tc::bar_commit_pair(empty_u + 8 * slot);
-          else tc::bar_commit(empty_u + 8 * slot);
-          ad += kGABytes / 16;
+          if (!ready && !tc::bar_wait(full_u + 8 * slot, phase, abort)) { ok = false; break; }
+          const uint32_t done = empty_u + 8 * slot, a_now = ad, b_now = bd;
+          const int slot_now = slot;
+          ad += a_step;
           bd += b_step;
           if (++slot == stages) {
             slot = 0;
             phase ^= 1;
-            ad = ad0;
-            bd = bd0;
+            ad = (uint32_t)ad0;
+            bd = (uint32_t)bd0;
           }
+          // asked now, so that the answer's latency passes behind the MMAs' issue
+          ready = tc::bar_test(full_u + 8 * slot, phase);
+          // a step of K = 16: 32 bytes along a K-major row, two 8-row atoms otherwise
+          if (left >= kGK || (!kWg && left > 48)) {
+            tc::fence_after_sync();
+            tc::mma_f16_x4<CG>(dt, a_now, a_hi, sta, b_now, b_hi, stb, idesc, acc);
+          } else {
+            if (kWg && g_tail(left)) {
+              // warp 3 (of both CTAs) clears the rows of the next group
+              tc::mbar_arrive(tgo);
+              if (!tc::bar_wait(pfull_u + 8 * slot_now, (tails >> slot_now) & 1, abort)) { ok = false; break; }
+              tails ^= 1u << slot_now;
+            }
+            tc::fence_after_sync();
+            const int steps = (left + 15) / 16;
+            for (int j = 0; j < steps; ++j) {
+              const uint64_t da = ((uint64_t)a_hi << 32) | (a_now + sta * j), db = ((uint64_t)b_hi << 32) | (b_now + stb * j);
+              if constexpr (CG == 2) tc::mma_f16_ss_pair(dt, da, db, idesc, j ? 1u : acc);
+              else tc::mma_f16_ss(dt, da, db, idesc, j ? 1u : acc);
+            }
+          }
+          acc = 1;
+          if constexpr (CG == 2) tc::bar_commit_pair(done);
+          else tc::bar_commit(done);
         }
         if (!ok) break;
         if constexpr (CG == 2) tc::mma_commit_pair(&accfull[d]);

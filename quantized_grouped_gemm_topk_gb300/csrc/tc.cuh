@@ -88,6 +88,16 @@ __device__ __forceinline__ bool bar_try_wait(uint32_t bar, uint32_t parity) {
       : "memory");
   return ok != 0;
 }
+// Whether the phase is complete, without waiting.
+__device__ __forceinline__ bool bar_test(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
 static __device__ __noinline__ bool bar_wait_slow(uint32_t bar, uint32_t parity, volatile int* abort) {
   const long long t0 = clock64();
   for (uint32_t it = 1;; ++it) {
@@ -428,6 +438,45 @@ __device__ __forceinline__ void tma_load_4d_at(uint32_t dst, const CUtensorMap* 
       " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
       "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar)
       : "memory");
+}
+// Four MMAs of K = 16 each, kind::f16, on consecutive steps of a stage (sa, sb:
+// step in 16 bytes), the first one accumulating if `acc`: one predicate and
+// 32-bit descriptor arithmetic for all of them (the descriptors' upper words
+// are constant), because a stage's issue must not take longer than its MMAs.
+template <int CG>
+__device__ __forceinline__ void mma_f16_x4(uint32_t d, uint32_t a_lo, uint32_t a_hi, uint32_t sa, uint32_t b_lo,
+                                           uint32_t b_hi, uint32_t sb, uint32_t idesc, uint32_t acc) {
+  if constexpr (CG == 2) {
+    asm volatile(
+        "{\n .reg .pred p, t;\n .reg .b64 a0, a1, a2, a3, b0, b1, b2, b3;\n"
+        " setp.ne.b32 p, %8, 0;\n setp.eq.u32 t, 0, 0;\n"
+        " mov.b64 a0, {%1, %9};\n mov.b64 b0, {%4, %10};\n"
+        " tcgen05.mma.cta_group::2.kind::f16 [%0], a0, b0, %7, p;\n"
+        " mov.b64 a1, {%2, %9};\n mov.b64 b1, {%5, %10};\n"
+        " tcgen05.mma.cta_group::2.kind::f16 [%0], a1, b1, %7, t;\n"
+        " mov.b64 a2, {%3, %9};\n mov.b64 b2, {%6, %10};\n"
+        " tcgen05.mma.cta_group::2.kind::f16 [%0], a2, b2, %7, t;\n"
+        " mov.b64 a3, {%11, %9};\n mov.b64 b3, {%12, %10};\n"
+        " tcgen05.mma.cta_group::2.kind::f16 [%0], a3, b3, %7, t;\n}" ::"r"(d),
+        "r"(a_lo), "r"(a_lo + sa), "r"(a_lo + 2 * sa), "r"(b_lo), "r"(b_lo + sb), "r"(b_lo + 2 * sb), "r"(idesc),
+        "r"(acc), "r"(a_hi), "r"(b_hi), "r"(a_lo + 3 * sa), "r"(b_lo + 3 * sb)
+        : "memory");
+  } else {
+    asm volatile(
+        "{\n .reg .pred p, t;\n .reg .b64 a0, a1, a2, a3, b0, b1, b2, b3;\n"
+        " setp.ne.b32 p, %8, 0;\n setp.eq.u32 t, 0, 0;\n"
+        " mov.b64 a0, {%1, %9};\n mov.b64 b0, {%4, %10};\n"
+        " tcgen05.mma.cta_group::1.kind::f16 [%0], a0, b0, %7, p;\n"
+        " mov.b64 a1, {%2, %9};\n mov.b64 b1, {%5, %10};\n"
+        " tcgen05.mma.cta_group::1.kind::f16 [%0], a1, b1, %7, t;\n"
+        " mov.b64 a2, {%3, %9};\n mov.b64 b2, {%6, %10};\n"
+        " tcgen05.mma.cta_group::1.kind::f16 [%0], a2, b2, %7, t;\n"
+        " mov.b64 a3, {%11, %9};\n mov.b64 b3, {%12, %10};\n"
+        " tcgen05.mma.cta_group::1.kind::f16 [%0], a3, b3, %7, t;\n}" ::"r"(d),
+        "r"(a_lo), "r"(a_lo + sa), "r"(a_lo + 2 * sa), "r"(b_lo), "r"(b_lo + sb), "r"(b_lo + 2 * sb), "r"(idesc),
+        "r"(acc), "r"(a_hi), "r"(b_hi), "r"(a_lo + 3 * sa), "r"(b_lo + 3 * sb)
+        : "memory");
+  }
 }
 // Commits by barrier address (see mma_commit, mma_commit_pair).
 __device__ __forceinline__ void bar_commit(uint32_t bar) {
