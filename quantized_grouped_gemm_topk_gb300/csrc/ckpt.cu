@@ -13,7 +13,7 @@
 // the block's largest magnitude takes three shuffles. The backward adds a
 // row's dw over its quarter-warps in a fixed order. NaN passes through every activation; an infinity or NaN becomes a
 // NaN code and leaves the block's scale to the others.
-#include "ops.cuh"
+#include "blocks.cuh"
 
 namespace moe {
 
@@ -82,115 +82,6 @@ __device__ __forceinline__ float3 ckpt_act_grad(float g, float u, const ActParam
     const float du = (uc == u || !FIN && u != u) ? gs : 0.f;
     return make_float3(gs * uc, dg, du);
   }
-}
-
-// A block's 128 columns belong to eight lanes, sixteen to a lane: columns
-// 8 l .. 8 l + 7 and 64 + 8 l .. . Sixteen, so that a block's fixed work (the
-// scales' divisions, shuffles, addresses) is spread over more elements. Held
-// as words of two 16-bit elements (four codes). VEC: every eight start on a
-// 16-byte (codes: 8-byte) boundary, I being a multiple of 8; otherwise rows at
-// any alignment. Columns past the n of the half (counted from the block's
-// first) read as zeros and are not written.
-template <bool VEC>
-__device__ __forceinline__ void load16(uint32_t (&w)[8], const uint16_t* p, int l, int n, const uint16_t* half, int I) {
-#pragma unroll
-  for (int k = 0; k < 2; ++k) {
-    const int c = 64 * k + 8 * l;
-    uint32_t v[4] = {0u, 0u, 0u, 0u};
-    if constexpr (VEC) {
-      if (c < n) {
-        const uint4 u = *reinterpret_cast<const uint4*>(p + c);
-        v[0] = u.x; v[1] = u.y; v[2] = u.z; v[3] = u.w;
-      }
-    } else {
-      load_any<2, 16>(v, p + c, half, half + I);
-    }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) w[4 * k + i] = v[i];
-  }
-}
-template <typename E>
-__device__ __forceinline__ float2 pair_of(uint32_t w) {
-  return make_float2(E::to((uint16_t)(w & 0xffffu)), E::to((uint16_t)(w >> 16)));
-}
-template <bool VEC>
-__device__ __forceinline__ void store16(uint16_t* p, const uint32_t (&w)[8], int l, int n) {
-#pragma unroll
-  for (int k = 0; k < 2; ++k) {
-    const int c = 64 * k + 8 * l;
-    const uint32_t v[4] = {w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]};
-    if (c < n) {
-      if constexpr (VEC) *reinterpret_cast<uint4*>(p + c) = make_uint4(v[0], v[1], v[2], v[3]);
-      else store_any<2>(p + c, v, n - c);
-    }
-  }
-}
-template <bool VEC>
-__device__ __forceinline__ void load_codes(uint32_t (&w)[4], const uint8_t* q, int l, int n, const uint8_t* half, int I) {
-#pragma unroll
-  for (int k = 0; k < 2; ++k) {
-    const int c = 64 * k + 8 * l;
-    uint32_t v[2] = {0u, 0u};
-    if constexpr (VEC) {
-      if (c < n) {
-        const uint2 u = *reinterpret_cast<const uint2*>(q + c);
-        v[0] = u.x; v[1] = u.y;
-      }
-    } else {
-      load_any<1, 8>(v, q + c, half, half + I);
-    }
-    w[2 * k] = v[0];
-    w[2 * k + 1] = v[1];
-  }
-}
-template <bool VEC>
-__device__ __forceinline__ void store_codes(uint8_t* q, const uint32_t (&w)[4], int l, int n) {
-#pragma unroll
-  for (int k = 0; k < 2; ++k) {
-    const int c = 64 * k + 8 * l;
-    const uint2 v = make_uint2(w[2 * k], w[2 * k + 1]);
-    if (c < n) {
-      if constexpr (VEC) *reinterpret_cast<uint2*>(q + c) = v;
-      else store_bytes8(q + c, v, n - c);
-    }
-  }
-}
-
-// Magnitude bits (16-bit elements without their sign order as integers:
-// finite < infinity < NaN) of the largest of the lane's sixteen.
-__device__ __forceinline__ uint32_t mag_bits(const uint32_t (&w)[8]) {
-  constexpr uint32_t k = 0x7fff7fffu;
-  uint32_t m = w[0] & k;
-#pragma unroll
-  for (int j = 1; j < 8; ++j) m = __vmaxu2(m, w[j] & k);
-  return max(m & 0xffffu, m >> 16);
-}
-// Codes of sixteen values at 1 / inv; FIN: without the test for infinities.
-template <typename E, bool FIN>
-__device__ __forceinline__ void codes16(uint32_t (&c)[4], const uint32_t (&w)[8], float inv) {
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const float2 a = pair_of<E>(w[2 * j]), b = pair_of<E>(w[2 * j + 1]);
-    const uint32_t lo = FIN ? f32x2_to_e4m3x2(a.x * inv, a.y * inv)
-                            : f32x2_to_e4m3x2(code_arg(a.x, inv), code_arg(a.y, inv));
-    const uint32_t hi = FIN ? f32x2_to_e4m3x2(b.x * inv, b.y * inv)
-                            : f32x2_to_e4m3x2(code_arg(b.x, inv), code_arg(b.y, inv));
-    c[j] = lo | (hi << 16);
-  }
-}
-// The block's scale where some element is an infinity or NaN: the largest of
-// the finite ones, over the eight lanes.
-template <typename E>
-__device__ __forceinline__ float finite_scale(const uint32_t (&w)[8], unsigned lanes) {
-  float am = 0.f;
-#pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    const float2 a = pair_of<E>(w[j]);
-    am = fmaxf(am, fmaxf(finite_mag(a.x), finite_mag(a.y)));
-  }
-#pragma unroll
-  for (int o = 4; o > 0; o >>= 1) am = fmaxf(am, __shfl_xor_sync(lanes, am, o));
-  return block_scale(am);
 }
 
 // Half a row's block forward: y's words, codes and scales.
@@ -338,20 +229,11 @@ __global__ void __launch_bounds__(kCkptThreads) k_ckpt_bwd(CkptArgs a, int qpr) 
 // ---- host ----------------------------------------------------------------------
 static bool al(const void* p, unsigned n) { return ((uintptr_t)p & (n - 1)) == 0; }
 
-// Quarter-warps a row: the most that leave at most a tenth of them idle in the
-// row's last round.
-static int quarters_a_row(int I) {
-  const int nb = (I + kQBlock - 1) / kQBlock;
-  int q = kCkptQuarters;
-  while (q > 1 && 10 * ((nb + q - 1) / q * q) > 11 * nb) q /= 2;
-  return q;
-}
-
 template <typename E, int ACT>
 static cudaError_t fwd_t(const CkptArgs& a, cudaStream_t st) {
   const bool vec = a.I % 8 == 0 && a.ldh % 8 == 0 && a.ldy % 8 == 0 && a.ldq % 8 == 0 && al(a.h, 16) && al(a.y, 16) &&
                    al(a.q, 8);
-  const int qpr = quarters_a_row(a.I), rpc = kCkptQuarters / qpr;
+  const int qpr = quarters_a_row(a.I, kCkptQuarters), rpc = kCkptQuarters / qpr;
   const int64_t g = std::min<int64_t>((a.R + rpc - 1) / rpc, (int64_t)device_sms() * 32);
   note_launch();
   if (vec) return launch_pdl(k_ckpt_fwd<E, true, ACT>, dim3((unsigned)g), dim3(kCkptThreads), 0, st, a, qpr);
@@ -362,7 +244,7 @@ template <typename E, int ACT>
 static cudaError_t bwd_t(const CkptArgs& a, cudaStream_t st) {
   const bool vec = a.I % 8 == 0 && a.lddy % 8 == 0 && a.lddh % 8 == 0 && a.ldq % 8 == 0 && al(a.dy, 16) &&
                    al(a.dh, 16) && al(a.q, 8) && (!a.y || (a.ldy % 8 == 0 && al(a.y, 16)));
-  const int qpr = quarters_a_row(a.I), rpc = kCkptQuarters / qpr;
+  const int qpr = quarters_a_row(a.I, kCkptQuarters), rpc = kCkptQuarters / qpr;
   const int64_t g = std::min<int64_t>((a.R + rpc - 1) / rpc, (int64_t)device_sms() * 32);
   note_launch();
   if (vec) return launch_pdl(k_ckpt_bwd<E, true, ACT>, dim3((unsigned)g), dim3(kCkptThreads), 0, st, a, qpr);

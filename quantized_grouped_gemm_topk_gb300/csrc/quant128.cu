@@ -9,9 +9,10 @@
 // code and leaves the others as they are. Columns and rows past the matrix
 // count as zeros and are not written.
 // Bound: HBM (3 bytes an element, 4 with the transposed copy), one pass: a
-// half-warp holds a row's block in registers; a CTA a 128 x 128 block, whose
-// codes cross shared memory once for the transposed copy.
-#include "ops.cuh"
+// quarter-warp (fp32: a half-warp) holds a row's block in registers; a CTA a
+// 128 x 128 block, whose codes cross shared memory once for the transposed
+// copy.
+#include "blocks.cuh"
 
 namespace moe {
 
@@ -60,8 +61,9 @@ __device__ __forceinline__ void store_codes8(uint8_t* p, uint2 w, int c, int n) 
   else store_bytes8(p + c, w, n - c);
 }
 
-template <typename E, bool VEC>
-__global__ void __launch_bounds__(kQThreads) k_quant128_rows(QuantRowsArgs a) {
+// fp32 rows: a half-warp a block, eight columns a lane.
+template <bool VEC>
+__global__ void __launch_bounds__(kQThreads) k_quant128_rows32(QuantRowsArgs a) {
   pdl_enter();
   const int l = threadIdx.x & 15, hw = threadIdx.x >> 4;
   const int nb = (a.C + kQBlock - 1) / kQBlock;
@@ -73,7 +75,7 @@ __global__ void __launch_bounds__(kQThreads) k_quant128_rows(QuantRowsArgs a) {
     const int b = live ? (int)(it - row * nb) : 0;
     float v[8];
     const int c = b * kQBlock + l * 8;
-    load_run8<E, VEC>(v, reinterpret_cast<const typename E::raw*>(a.x) + row * a.ldx, c, live ? a.C : 0);
+    load_run8<F32, VEC>(v, reinterpret_cast<const float*>(a.x) + row * a.ldx, c, live ? a.C : 0);
     float am = mag8(v);
 #pragma unroll
     for (int o = 8; o > 0; o >>= 1) am = fmaxf(am, __shfl_xor_sync(kFull, am, o));
@@ -83,15 +85,68 @@ __global__ void __launch_bounds__(kQThreads) k_quant128_rows(QuantRowsArgs a) {
   }
 }
 
+// 16-bit rows: a quarter-warp a block, sixteen columns a lane (blocks.cuh);
+// qpr quarter-warps of a CTA share a row.
+template <typename E, bool VEC>
+__global__ void __launch_bounds__(kQThreads) k_quant128_rows(QuantRowsArgs a, int qpr) {
+  pdl_enter();
+  const int l = threadIdx.x & 7, qw = threadIdx.x >> 3;
+  const unsigned lanes = 0xffu << (threadIdx.x & 24);
+  const int nb = (a.C + kQBlock - 1) / kQBlock;
+  const int rpc = kQThreads / 8 / qpr, rl = qw / qpr, part = qw % qpr;
+  for (int64_t row = (int64_t)blockIdx.x * rpc + rl; row < a.R; row += (int64_t)gridDim.x * rpc) {
+    const uint16_t* x = reinterpret_cast<const uint16_t*>(a.x) + row * a.ldx;
+    uint8_t* q = a.q + row * a.ldq;
+    for (int b = part; b < nb; b += qpr) {
+      const int c0 = b * kQBlock, n = min(kQBlock, a.C - c0);
+      uint32_t w[8], codes[4];
+      load16<VEC>(w, x + c0, l, n, x, a.C);
+      uint32_t mm = mag_bits(w);
+#pragma unroll
+      for (int o = 4; o > 0; o >>= 1) mm = max(mm, __shfl_xor_sync(lanes, mm, o));
+      float s;
+      if (mm < E::kInf) {
+        s = block_scale(E::to((uint16_t)mm));
+        codes16<E, true>(codes, w, 1.0f / s);
+      } else {
+        s = finite_scale<E>(w, lanes);
+        codes16<E, false>(codes, w, 1.0f / s);
+      }
+      store_codes<VEC>(q + c0, codes, l, n);
+      if (l == 0) a.s[row * a.lds + b] = s;
+    }
+  }
+}
+
+// Bytes (i, j) of eight rows of eight -> the same transposed: row words r[i][2]
+// become column words c[j][2]. Four 4 x 4 blocks by byte permutes.
+__device__ __forceinline__ void transpose8x8(uint32_t (&c)[8][2], const uint2 (&r)[8]) {
+#pragma unroll
+  for (int h = 0; h < 2; ++h)       // rows 4 h .. 4 h + 3 -> word h of the columns
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {   // columns 4 k .. 4 k + 3
+      const uint32_t a = k ? r[4 * h].y : r[4 * h].x, b = k ? r[4 * h + 1].y : r[4 * h + 1].x;
+      const uint32_t d = k ? r[4 * h + 2].y : r[4 * h + 2].x, e = k ? r[4 * h + 3].y : r[4 * h + 3].x;
+      const uint32_t ab0 = __byte_perm(a, b, 0x5140), ab1 = __byte_perm(a, b, 0x7362);
+      const uint32_t de0 = __byte_perm(d, e, 0x5140), de1 = __byte_perm(d, e, 0x7362);
+      c[4 * k][h] = __byte_perm(ab0, de0, 0x5410);
+      c[4 * k + 1][h] = __byte_perm(ab0, de0, 0x7632);
+      c[4 * k + 2][h] = __byte_perm(ab1, de1, 0x5410);
+      c[4 * k + 3][h] = __byte_perm(ab1, de1, 0x7632);
+    }
+}
+
 // One CTA per 128 x 128 block of a group: thread (y, x) = (id / 16, id % 16)
-// holds columns 8x .. 8x + 7 of rows y, y + 16, ...
+// holds columns 8x .. 8x + 7 of rows 8y .. 8y + 7. For the transposed copy
+// each thread transposes its 8 x 8 codes in registers; they cross shared
+// memory as 8-byte words (column, y), at y ^ x so that neither side meets a
+// bank twice.
 template <typename E, bool VEC>
 __global__ void __launch_bounds__(kQThreads) k_quant128_weights(QuantWeightsArgs a) {
+  constexpr bool k16 = sizeof(typename E::raw) == 2;
   pdl_enter();
   __shared__ float red[kQThreads / 32];
-  // codes of the block, column-major, 4-byte words of four rows; the row of
-  // words is padded by one so a column's writes spread over the banks
-  __shared__ uint8_t tile[kQBlock][kQBlock + 4];
+  __shared__ uint2 tile[kQBlock][16];
   const int x = threadIdx.x & 15, y = threadIdx.x >> 4;
   const int nb = (a.N + kQBlock - 1) / kQBlock, kb = (a.K + kQBlock - 1) / kQBlock;
   const int64_t blocks = (int64_t)a.G * nb * kb;
@@ -100,15 +155,52 @@ __global__ void __launch_bounds__(kQThreads) k_quant128_weights(QuantWeightsArgs
     const int bi = (int)(blk - g * nb * kb), n0 = bi / kb * kQBlock, k0 = bi % kb * kQBlock;
     const int nn = min(kQBlock, a.N - n0), kn = min(kQBlock, a.K - k0);
     const typename E::raw* w = reinterpret_cast<const typename E::raw*>(a.w) + g * a.wg + (int64_t)n0 * a.ldw;
-    float v[8][8];
+    uint32_t h[k16 ? 8 : 1][4];         // 16-bit elements as they came
+    float v[k16 ? 1 : 8][8];
     float am = 0.f;
+    if constexpr (k16) {
+      uint32_t mm = 0;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int r = y + 16 * i;
-      load_run8<E, VEC>(v[i], w + (int64_t)min(r, nn - 1) * a.ldw, k0 + x * 8, r < nn ? a.K : 0);
+      for (int i = 0; i < 8; ++i) {
+        const int r = 8 * y + i;
+        const uint16_t* p = reinterpret_cast<const uint16_t*>(w) + (int64_t)min(r, nn - 1) * a.ldw;
+        const int c = k0 + x * 8, end = r < nn ? a.K : 0;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) h[i][j] = 0u;
+        if constexpr (VEC) {
+          if (c < end) {
+            const uint4 u = *reinterpret_cast<const uint4*>(p + c);
+            h[i][0] = u.x; h[i][1] = u.y; h[i][2] = u.z; h[i][3] = u.w;
+          }
+        } else {
+          load_any<2, 16>(h[i], p + c, p, p + end);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) mm = __vmaxu2(mm, h[i][j] & 0x7fff7fffu);
+      mm = max(mm & 0xffffu, mm >> 16);
+      am = E::to((uint16_t)mm);
+      if (mm >= E::kInf) {              // an infinity or NaN: the largest of the finite ones
+        am = 0.f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const float2 f = pair_of<E>(h[i][j]);
+            am = fmaxf(am, fmaxf(finite_mag(f.x), finite_mag(f.y)));
+          }
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int r = 8 * y + i;
+        load_run8<E, VEC>(v[i], w + (int64_t)min(r, nn - 1) * a.ldw, k0 + x * 8, r < nn ? a.K : 0);
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) am = fmaxf(am, mag8(v[i]));
     }
-#pragma unroll
-    for (int i = 0; i < 8; ++i) am = fmaxf(am, mag8(v[i]));
     am = warp_max(am);
     __syncthreads();               // the last block's reads of red and tile are done
     if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = am;
@@ -117,34 +209,37 @@ __global__ void __launch_bounds__(kQThreads) k_quant128_weights(QuantWeightsArgs
     for (int i = 0; i < kQThreads / 32; ++i) am = fmaxf(am, red[i]);
     const float s = block_scale(am), inv = 1.0f / s;
     uint8_t* q = a.q + g * a.qg + (int64_t)n0 * a.ldq + k0;
+    uint2 c[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const int r = y + 16 * i;
-      const uint2 c = codes8(v[i], inv);
-      if (r < nn) store_codes8<VEC>(q + (int64_t)r * a.ldq, c, x * 8, kn);
-      if (a.qt) {
+      if constexpr (k16) {
+        float f[8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) tile[x * 8 + j][r] = (uint8_t)((j < 4 ? c.x : c.y) >> (8 * (j & 3)));
+        for (int j = 0; j < 4; ++j) {
+          const float2 p = pair_of<E>(h[i][j]);
+          f[2 * j] = p.x;
+          f[2 * j + 1] = p.y;
+        }
+        c[i] = codes8(f, inv);
+      } else {
+        c[i] = codes8(v[i], inv);
       }
+      const int r = 8 * y + i;
+      if (r < nn) store_codes8<VEC>(q + (int64_t)r * a.ldq, c[i], x * 8, kn);
     }
     if (threadIdx.x == 0) {
       a.s[(g * nb + n0 / kQBlock) * kb + k0 / kQBlock] = s;
       if (a.qt) a.st[(g * kb + k0 / kQBlock) * nb + n0 / kQBlock] = s;
     }
     if (a.qt) {
+      uint32_t t[8][2];
+      transpose8x8(t, c);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) tile[8 * x + j][y ^ x] = make_uint2(t[j][0], t[j][1]);
       __syncthreads();
-      // transposed rows (one per column k of the block), four codes a lane
+      // transposed rows (one per column k of the block), eight codes a lane
       uint8_t* qt = a.qt + g * a.qtg + (int64_t)k0 * a.ldqt + n0;
-      const int c4 = (threadIdx.x & 31) * 4;
-      for (int r = threadIdx.x >> 5; r < kn; r += kQThreads / 32) {
-        const uint32_t wd = *reinterpret_cast<const uint32_t*>(&tile[r][c4]);
-        uint8_t* d = qt + (int64_t)r * a.ldqt + c4;
-        if (VEC && c4 + 4 <= nn) {
-          *reinterpret_cast<uint32_t*>(d) = wd;
-        } else {
-          for (int j = 0; j < 4 && c4 + j < nn; ++j) d[j] = (uint8_t)(wd >> (8 * j));
-        }
-      }
+      for (int r = y; r < kn; r += 16) store_codes8<VEC>(qt + (int64_t)r * a.ldqt, tile[r][x ^ (r >> 3)], x * 8, nn);
     }
   }
 }
@@ -152,21 +247,29 @@ __global__ void __launch_bounds__(kQThreads) k_quant128_weights(QuantWeightsArgs
 // ---- host ----------------------------------------------------------------------
 static bool al(const void* p, unsigned n) { return ((uintptr_t)p & (n - 1)) == 0; }
 
+static bool rows_vec(const QuantRowsArgs& a, int esize) {
+  return a.C % 8 == 0 && a.ldx % (16 / esize) == 0 && a.ldq % 8 == 0 && al(a.x, 16) && al(a.q, 8);
+}
 template <typename E>
 static cudaError_t rows_t(const QuantRowsArgs& a, cudaStream_t st) {
-  const int per = 16 / (int)sizeof(typename E::raw);
-  const bool vec = a.C % 8 == 0 && a.ldx % per == 0 && a.ldq % 8 == 0 && al(a.x, 16) && al(a.q, 8);
+  const int qpr = quarters_a_row(a.C, kQThreads / 8), rpc = kQThreads / 8 / qpr;
+  const int64_t g = std::min<int64_t>((a.R + rpc - 1) / rpc, (int64_t)device_sms() * 32);
+  note_launch();
+  if (rows_vec(a, 2)) return launch_pdl(k_quant128_rows<E, true>, dim3((unsigned)g), dim3(kQThreads), 0, st, a, qpr);
+  return launch_pdl(k_quant128_rows<E, false>, dim3((unsigned)g), dim3(kQThreads), 0, st, a, qpr);
+}
+static cudaError_t rows_32(const QuantRowsArgs& a, cudaStream_t st) {
   const int64_t items = a.R * ((a.C + kQBlock - 1) / kQBlock);
   const int64_t g = std::min<int64_t>((items + kQThreads / 16 - 1) / (kQThreads / 16), (int64_t)device_sms() * 32);
   note_launch();
-  if (vec) return launch_pdl(k_quant128_rows<E, true>, dim3((unsigned)g), dim3(kQThreads), 0, st, a);
-  return launch_pdl(k_quant128_rows<E, false>, dim3((unsigned)g), dim3(kQThreads), 0, st, a);
+  if (rows_vec(a, 4)) return launch_pdl(k_quant128_rows32<true>, dim3((unsigned)g), dim3(kQThreads), 0, st, a);
+  return launch_pdl(k_quant128_rows32<false>, dim3((unsigned)g), dim3(kQThreads), 0, st, a);
 }
 template <typename E>
 static cudaError_t weights_t(const QuantWeightsArgs& a, cudaStream_t st) {
   const int per = 16 / (int)sizeof(typename E::raw);
   const bool vec = a.K % 8 == 0 && a.ldw % per == 0 && a.wg % per == 0 && a.ldq % 8 == 0 && a.qg % 8 == 0 &&
-                   al(a.w, 16) && al(a.q, 8) && (!a.qt || (a.ldqt % 4 == 0 && a.qtg % 4 == 0 && al(a.qt, 4)));
+                   al(a.w, 16) && al(a.q, 8) && (!a.qt || (a.N % 8 == 0 && a.ldqt % 8 == 0 && a.qtg % 8 == 0 && al(a.qt, 8)));
   const int64_t blocks = (int64_t)a.G * ((a.N + kQBlock - 1) / kQBlock) * ((a.K + kQBlock - 1) / kQBlock);
   const int64_t g = std::min<int64_t>(blocks, (int64_t)device_sms() * 16);
   note_launch();
@@ -175,7 +278,7 @@ static cudaError_t weights_t(const QuantWeightsArgs& a, cudaStream_t st) {
 }
 
 cudaError_t launch_quant128_rows(const QuantRowsArgs& a, cudaStream_t st) {
-  if (a.dtype == MOE_DT_F32) return rows_t<F32>(a, st);
+  if (a.dtype == MOE_DT_F32) return rows_32(a, st);
   return a.dtype == MOE_DT_F16 ? rows_t<F16>(a, st) : rows_t<Bf16>(a, st);
 }
 cudaError_t launch_quant128_weights(const QuantWeightsArgs& a, cudaStream_t st) {
