@@ -14,12 +14,12 @@
 // little next to its weights' bytes.
 //
 // Bound: the tensor pipe at training sizes, the weights' bytes at decode
-// sizes. What an SM can take in from L2 (64 bytes a cycle, measured: 48 KB a
-// stage took 745 cycles whatever else was changed) is less than a 128 x 256
+// sizes. What an SM can take in from L2 (64 bytes a cycle, measured: 48 KB
+// took 745 cycles whatever else was changed) is less than a 128 x 256
 // tile on one SM wants (48 KB per 512 cycles of MMA). So where there is work
 // for it a pair of SMs (cta_group::2) multiplies a 256 x 256 tile together:
-// 32 KB a stage for each. Tiles of one SM (128 x up to 256) serve few tiles
-// and few rows. Stages of 64 of the reduction in a ring that fills the shared
+// 32 KB for each. Tiles of one SM (128 x up to 256) serve few tiles
+// and few rows. Stages of 128 of the reduction in a ring that fills the shared
 // memory, filled by tensor copies with the 128-byte swizzle. Ragged edges cost
 // no branch in the main loop: rows of a tile that belong to the next group
 // only reach accumulator columns that are not stored; columns and the K tail
@@ -43,11 +43,16 @@ namespace moe {
 
 enum { kRowsNT = 0, kRowsNN = 1, kWgradMN = 2 };
 
-constexpr int kGK = 64;               // reduction a stage: one 128-byte swizzle row
+// Reduction a stage: two halves of one 128-byte swizzle row each, behind one
+// barrier. The thread that issues the MMAs spends some 270 cycles a stage
+// besides the MMAs themselves; with one half a stage that was the bound of
+// tiles narrower than 256 (about 570 cycles a stage whatever their width).
+constexpr int kGH = 64;
+constexpr int kGK = 2 * kGH;
 constexpr int kGN = 256;              // widest tile
 constexpr int kGThreads = 384;
-constexpr int kGChunk = 64 * kGK * 2; // bytes of 64 M / N elements of an MN-contiguous stage
-constexpr int kGABytes = kGM * kGK * 2;
+constexpr int kGChunk = 64 * kGH * 2; // bytes of 64 M / N elements of an MN-contiguous half
+constexpr int kGABytes = kGM * kGH * 2;   // of a half
 constexpr int kGHeadBars = 512;       // barriers and scratch, in front of the group tables
 constexpr int kGMaxStages = 12;
 constexpr int kGSmem = 227 * 1024;
@@ -60,8 +65,8 @@ struct GMaps {
 struct GArgs {
   MmArgs m;
   int bn;               // widest N of a tile
-  int stages;           // of the ring, each kGABytes + b_bytes
-  int b_bytes;
+  int stages;           // of the ring, each 2 (kGABytes + b_bytes)
+  int b_bytes;          // of B's half
   int head;             // bytes in front of the ring
   int m_tiles;          // tiles of 128 CG features
   int n_tiles;          // weight gradient: bn-wide column tiles
@@ -176,7 +181,7 @@ __global__ void __launch_bounds__(kGThreads, 1) k_gemm16(const GArgs g, const __
   uint8_t* base = reinterpret_cast<uint8_t*>(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
   const int stages = g.stages, b_bytes = g.b_bytes;
   uint8_t* sa = base + g.head;
-  uint8_t* sb = sa + stages * kGABytes;
+  uint8_t* sb = sa + stages * 2 * kGABytes;
   uint64_t* full = reinterpret_cast<uint64_t*>(base);
   uint64_t* pfull = full + kGMaxStages;         // weight gradient: the rows of a tail stage are cleared
   uint64_t* empty = pfull + kGMaxStages;
@@ -234,7 +239,7 @@ __global__ void __launch_bounds__(kGThreads, 1) k_gemm16(const GArgs g, const __
     // ---------------- copies: warp 0 B, warp 2 A ----------------
     if (lane == 0) {
       const bool isb = warp == 0;
-      const uint32_t dst0 = isb ? sb_u : sa_u, step = isb ? b_bytes : kGABytes;
+      const uint32_t dst0 = isb ? sb_u : sa_u, half_bytes = isb ? b_bytes : kGABytes;
       // both CTAs' copies report to the first one's barriers, which expect them
       // all; those of a tail stage, where each CTA has rows to clear first, to
       // their own CTA's
@@ -249,21 +254,26 @@ __global__ void __launch_bounds__(kGThreads, 1) k_gemm16(const GArgs g, const __
         const int half = w.N / CG;                    // B rows of this CTA
         const int c0 = w.c0 + rank * half, m0 = w.m0 + rank * kGM;
         const int bi = g_box(half);
-        const uint32_t bytes = !isb ? kGABytes : kWg ? (uint32_t)(half / 64 * kGChunk) : (uint32_t)(kGK * 2 * (16 << bi));
+        const uint32_t bytes = !isb ? kGABytes : kWg ? (uint32_t)(half / 64 * kGChunk) : (uint32_t)(kGH * 2 * (16 << bi));
         const CUtensorMap* map = isb ? (kWg ? &maps.b[0] : &maps.b[bi]) : &maps.a;
         const int r0 = kWg ? off[w.e] : 0;
         for (int kb = w.k0; kb < w.k1; ++kb) {
           const int k = kb * kGK;
           if (!tc::bar_wait(empty_u + 8 * slot, phase, abort)) { ok = false; break; }
           const bool own = CG == 1 || (kWg && g_tail(w.red - k));
-          const uint32_t bar = (own ? full_u : lead_u) + 8 * slot, dst = dst0 + slot * step;
-          if (own || rank == 0) tc::bar_arrive_expect_tx(full_u + 8 * slot, own ? bytes : CG * bytes);
-          if (isb) {
-            if (kWg) g_copy_mn<CG>(dst, map, c0, r0 + k, 0, half / 64, g.b_chunks > 1, bar);
-            else g_copy2<CG>(dst, map, k, c0, bar);
-          } else {
-            if (MODE == kRowsNT) g_copy3<CG>(dst, map, k, m0, w.e, bar);
-            else g_copy_mn<CG>(dst, map, m0, kWg ? r0 + k : k, kWg ? 0 : w.e, kGM / 64, g.a_chunks > 1, bar);
+          const uint32_t bar = (own ? full_u : lead_u) + 8 * slot;
+          uint32_t dst = dst0 + slot * 2 * half_bytes;
+          const int halves = w.red - k > kGH ? 2 : 1;
+          if (own || rank == 0) tc::bar_arrive_expect_tx(full_u + 8 * slot, (own ? bytes : CG * bytes) * halves);
+          for (int s = 0; s < halves; ++s, dst += half_bytes) {
+            const int ks = k + s * kGH;
+            if (isb) {
+              if (kWg) g_copy_mn<CG>(dst, map, c0, r0 + ks, 0, half / 64, g.b_chunks > 1, bar);
+              else g_copy2<CG>(dst, map, ks, c0, bar);
+            } else {
+              if (MODE == kRowsNT) g_copy3<CG>(dst, map, ks, m0, w.e, bar);
+              else g_copy_mn<CG>(dst, map, m0, kWg ? r0 + ks : ks, kWg ? 0 : w.e, kGM / 64, g.a_chunks > 1, bar);
+            }
           }
           ++issued;
           if (++slot == stages) {
@@ -294,7 +304,7 @@ __global__ void __launch_bounds__(kGThreads, 1) k_gemm16(const GArgs g, const __
       constexpr uint32_t sta = MODE != kRowsNT ? 2048 / 16 : 32 / 16, stb = kWg ? 2048 / 16 : 32 / 16;
       const uint64_t ad0 = MODE != kRowsNT ? tc::smem_desc_mn_sw128(sa_u, kGChunk) : tc::smem_desc_sw128(sa_u);
       const uint64_t bd0 = kWg ? tc::smem_desc_mn_sw128(sb_u, kGChunk) : tc::smem_desc_sw128(sb_u);
-      const uint32_t a_hi = (uint32_t)(ad0 >> 32), b_hi = (uint32_t)(bd0 >> 32), a_step = kGABytes / 16, b_step = b_bytes / 16;
+      const uint32_t a_hi = (uint32_t)(ad0 >> 32), b_hi = (uint32_t)(bd0 >> 32), a_half = kGABytes / 16, b_half = b_bytes / 16;
       uint32_t ad = (uint32_t)ad0, bd = (uint32_t)bd0;
       int slot = 0;
       uint32_t phase = 0, tails = 0;     // tails: parity, by slot, of pfull
@@ -314,8 +324,8 @@ __global__ void __launch_bounds__(kGThreads, 1) k_gemm16(const GArgs g, const __
           if (!ready && !tc::bar_wait(full_u + 8 * slot, phase, abort)) { ok = false; break; }
           const uint32_t done = empty_u + 8 * slot, a_now = ad, b_now = bd;
           const int slot_now = slot;
-          ad += a_step;
-          bd += b_step;
+          ad += 2 * a_half;
+          bd += 2 * b_half;
           if (++slot == stages) {
             slot = 0;
             phase ^= 1;
@@ -324,21 +334,23 @@ __global__ void __launch_bounds__(kGThreads, 1) k_gemm16(const GArgs g, const __
           }
           // asked now, so that the answer's latency passes behind the MMAs' issue
           ready = tc::bar_test(full_u + 8 * slot, phase);
+          if (kWg && g_tail(left)) {
+            // warp 3 (of both CTAs) clears the rows of the next group
+            tc::mbar_arrive(tgo);
+            if (!tc::bar_wait(pfull_u + 8 * slot_now, (tails >> slot_now) & 1, abort)) { ok = false; break; }
+            tails ^= 1u << slot_now;
+          }
+          tc::fence_after_sync();
           // a step of K = 16: 32 bytes along a K-major row, two 8-row atoms otherwise
-          if (left >= kGK || (!kWg && left > 48)) {
-            tc::fence_after_sync();
+          if (left > kGK - 16) {
             tc::mma_f16_x4<CG>(dt, a_now, a_hi, sta, b_now, b_hi, stb, idesc, acc);
+            tc::mma_f16_x4<CG>(dt, a_now + a_half, a_hi, sta, b_now + b_half, b_hi, stb, idesc, 1u);
           } else {
-            if (kWg && g_tail(left)) {
-              // warp 3 (of both CTAs) clears the rows of the next group
-              tc::mbar_arrive(tgo);
-              if (!tc::bar_wait(pfull_u + 8 * slot_now, (tails >> slot_now) & 1, abort)) { ok = false; break; }
-              tails ^= 1u << slot_now;
-            }
-            tc::fence_after_sync();
             const int steps = (left + 15) / 16;
             for (int j = 0; j < steps; ++j) {
-              const uint64_t da = ((uint64_t)a_hi << 32) | (a_now + sta * j), db = ((uint64_t)b_hi << 32) | (b_now + stb * j);
+              const uint32_t al = a_now + (j >= 4 ? a_half : 0u) + sta * (j & 3);
+              const uint32_t bl = b_now + (j >= 4 ? b_half : 0u) + stb * (j & 3);
+              const uint64_t da = ((uint64_t)a_hi << 32) | al, db = ((uint64_t)b_hi << 32) | bl;
               if constexpr (CG == 2) tc::mma_f16_ss_pair(dt, da, db, idesc, j ? 1u : acc);
               else tc::mma_f16_ss(dt, da, db, idesc, j ? 1u : acc);
             }
@@ -383,10 +395,10 @@ __global__ void __launch_bounds__(kGThreads, 1) k_gemm16(const GArgs g, const __
         told ^= 1;
         tails ^= 1u << at;
         const int bad = 16 - (left & 15), chunks = kGM / 64 + w.N / CG / 64;
-        uint8_t* pa = sa + at * kGABytes;
-        uint8_t* pb = sb + at * b_bytes;
+        uint8_t* pa = sa + (2 * at + left / kGH) * kGABytes;         // the half that `left` ends in
+        uint8_t* pb = sb + (2 * at + left / kGH) * b_bytes;
         for (int i = lane; i < bad * 8 * chunks; i += 32) {
-          const int q = i & 7, r = left + (i >> 3) % bad, c = (i >> 3) / bad;
+          const int q = i & 7, r = left % kGH + (i >> 3) % bad, c = (i >> 3) / bad;
           uint8_t* line = (c < kGM / 64 ? pa + c * kGChunk : pb + (c - kGM / 64) * kGChunk) + r * 128;
           reinterpret_cast<uint4*>(line)[q] = make_uint4(0u, 0u, 0u, 0u);
         }
@@ -422,21 +434,41 @@ __global__ void __launch_bounds__(kGThreads, 1) k_gemm16(const GArgs g, const __
       if (!__all_sync(kFull, got)) break;
       tc::fence_after_sync();
       const int f0 = w.m0 + rank * kGM + q * 32;    // the warp's first feature
-      for (int c = 0; c < w.nc; c += 32) {
-        uint32_t v[32];
-        if (w.k1 > w.k0) {
-          tc::tmem_ld32(acc + c, v);
-          tc::tmem_wait_ld();
-        } else {
+      if constexpr (kWg) {
+        // 64 columns at a time: a row's 128 bytes (16-bit), exchanged between
+        // the lanes before they are stored
+        const int rows = m.N - f0;
+        const int64_t at0 = w.e * og + (int64_t)f0 * ld + w.c0 + (m.S > 1 ? w.piece * os : 0);
+        for (int c = 0; c < w.nc; c += 64) {
+          uint32_t v[64];
+          if (w.k1 > w.k0) {
+            tc::tmem_ld32(acc + c, reinterpret_cast<uint32_t(&)[32]>(v[0]));
+            tc::tmem_ld32(acc + c + 32, reinterpret_cast<uint32_t(&)[32]>(v[32]));
+            tc::tmem_wait_ld();
+          } else {
 #pragma unroll
-          for (int i = 0; i < 32; ++i) v[i] = 0u;       // no rows to sum over
-        }
-        if (kWg) {
-          if (f0 + lane < m.N) {
-            const int64_t at = w.e * og + (int64_t)(f0 + lane) * ld + w.c0 + c + (m.S > 1 ? w.piece * os : 0);
-            store_cols(obase + at * esize, v, w.nc - c, dt, vec);
+            for (int i = 0; i < 64; ++i) v[i] = 0u;       // no rows to sum over
           }
-        } else {
+          if (vec && c + 64 <= w.nc) {
+            float f[64];
+#pragma unroll
+            for (int i = 0; i < 64; ++i) f[i] = __uint_as_float(v[i]);
+            store_block<64>(obase + (at0 + c) * esize, ld * esize, f, rows, lane, dt);
+          } else if (lane < rows) {
+            store_cols<64>(obase + (at0 + lane * ld + c) * esize, v, w.nc - c, dt, vec);
+          }
+          __syncwarp();
+        }
+      } else {
+        for (int c = 0; c < w.nc; c += 32) {
+          uint32_t v[32];
+          if (w.k1 > w.k0) {
+            tc::tmem_ld32(acc + c, v);
+            tc::tmem_wait_ld();
+          } else {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[i] = 0u;
+          }
           const int64_t at = (int64_t)(w.c0 + c) * ld + (m.S > 1 ? w.piece * os : 0);
           const int n = w.nc - c;
           if (dt == MOE_DT_F32) {
@@ -451,8 +483,8 @@ __global__ void __launch_bounds__(kGThreads, 1) k_gemm16(const GArgs g, const __
           } else {
             store_tokens16<Bf16>(reinterpret_cast<uint16_t*>(obase) + at, ld, v, n, lane, f0, m.N, pairs);
           }
+          __syncwarp();
         }
-        __syncwarp();
       }
       tc::fence_before_sync();
       __syncwarp();
@@ -530,7 +562,7 @@ MmPlan mm_plan(int kind, int R, int N, int K, int G) {
     // rows a group, which stream weights
     p.cg = count(2, 256) >= kPlanSms / 2 && (wg || R >= 64ll * std::min(G, R)) ? 2 : 1;
     // (and whose stages are small then: more of them in flight)
-    if (!wg && R <= 32ll * std::min(G, R)) p.bn = 64;
+    if (!wg && R <= 32ll * std::min(G, R)) p.bn = R <= 8ll * std::min(G, R) ? 32 : 64;
     while (p.cg == 1 && p.bn > 64 && count(1, p.bn) < kPlanSms) p.bn /= 2;
     units = count(p.cg, p.bn);
   }
@@ -583,11 +615,11 @@ static int make_mn(CUtensorMap* map, const void* base, int64_t rows, int64_t col
   if (G == 1) gs = ld;      // never stepped over
   if (cols % 64 == 0 && chunks > 1) {
     const int64_t dims[4] = {64, rows, cols / 64, G}, strides[3] = {ld, 64, gs};
-    const int box[4] = {64, kGK, chunks, 1};
+    const int box[4] = {64, kGH, chunks, 1};
     return make_tmap(map, base, 2, 4, dims, strides, box) ? chunks : 0;
   }
   const int64_t dims[4] = {cols, rows, 1, G}, strides[3] = {ld, ld, gs};
-  const int box[4] = {64, kGK, 1, 1};
+  const int box[4] = {64, kGH, 1, 1};
   return make_tmap(map, base, 2, 4, dims, strides, box) ? 1 : 0;
 }
 
@@ -595,13 +627,12 @@ template <int MODE, int CG>
 static cudaError_t launch_g(GArgs g, cudaStream_t st) {
   const MmArgs& m = g.m;
   constexpr bool kWg = MODE == kWgradMN;
-  // As many stages as fit: the ring's round trip (copy, MMAs, release) is
-  // longer than a few stages' MMAs. With six stages of 32 KB a stage took 595
-  // cycles on a pair of SMs, not the MMAs' 512.
-  g.b_bytes = g.bn / CG * kGK * 2;
+  // as many stages as fit: the ring's round trip (copy, MMAs, release) is long
+  g.b_bytes = g.bn / CG * kGH * 2;
   g.head = (kGHeadBars + 2 * 4 * (m.G + 1) + 1023) / 1024 * 1024;
-  g.stages = std::min(kGMaxStages, (kGSmem - 1024 - g.head) / (kGABytes + g.b_bytes));
-  const int smem = 1024 + g.head + g.stages * (kGABytes + g.b_bytes);
+  const int stage = 2 * (kGABytes + g.b_bytes);
+  g.stages = std::min(kGMaxStages, (kGSmem - 1024 - g.head) / stage);
+  const int smem = 1024 + g.head + g.stages * stage;
   GMaps maps;
   const int64_t rows = std::max(m.R, 1);
   g.m_tiles = (int)tiles(m.N, kGM * CG);
@@ -616,12 +647,12 @@ static cudaError_t launch_g(GArgs g, cudaStream_t st) {
   } else {
     for (int i = 0; i < kGBoxes; ++i) {
       const int64_t dims[2] = {m.K, rows}, strides[1] = {m.lda};
-      const int box[2] = {kGK, 16 << i};
+      const int box[2] = {kGH, 16 << i};
       if (!make_tmap(&maps.b[i], m.a, 2, 2, dims, strides, box)) return cudaErrorInvalidValue;
     }
     if (MODE == kRowsNT) {
       const int64_t dims[3] = {m.K, m.N, m.G}, strides[2] = {m.ldb, m.G > 1 ? m.bg : m.ldb};
-      const int box[3] = {kGK, kGM, 1};
+      const int box[3] = {kGH, kGM, 1};
       if (!make_tmap(&maps.a, m.b, 2, 3, dims, strides, box)) return cudaErrorInvalidValue;
     } else {
       g.a_chunks = make_mn(&maps.a, m.b, m.K, m.N, m.ldb, m.G, m.bg, kGM / 64);

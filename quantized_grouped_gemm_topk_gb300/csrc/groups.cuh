@@ -144,21 +144,13 @@ __device__ __forceinline__ void store_cols(void* p, const uint32_t (&v)[C], int 
   }
 }
 
-// A warp's 32 rows x C columns (lane = row, v the row's fp32 bits) to row-major
-// out, 16-byte accesses. A lane's own row would make every store touch 32
-// lines; instead NU = units of 16 bytes in a row's C columns are exchanged
-// among NU lanes (a transpose in log2 NU steps), so that a store covers whole
-// segments of 16 NU bytes of 32 / NU rows. p: the first row's first column;
-// rows < n_rows are written.
-template <int C, typename Conv>
-__device__ __forceinline__ void store_block16(uint8_t* p, int64_t row_bytes, const float (&v)[C], int n_rows, int lane,
-                                              Conv conv) {
-  constexpr int NU = C / 8;
-  uint32_t w[NU][4];
-#pragma unroll
-  for (int i = 0; i < NU; ++i)
-#pragma unroll
-    for (int j = 0; j < 4; ++j) w[i][j] = conv(v[8 * i + 2 * j], v[8 * i + 2 * j + 1]);
+// A warp's 32 rows (lane = row), NU units of 16 bytes each, to row-major out. A
+// lane's own row would make every store touch 32 lines; instead the units are
+// exchanged among NU lanes (a transpose in log2 NU steps), so that a store
+// covers whole segments of 16 NU bytes of 32 / NU rows. p: the first row's
+// first unit (16-byte aligned, as row_bytes is); rows < n_rows are written.
+template <int NU>
+__device__ __forceinline__ void store_units(uint8_t* p, int64_t row_bytes, uint32_t (&w)[NU][4], int n_rows, int lane) {
 #pragma unroll
   for (int s = 1; s < NU; s <<= 1) {
     const bool up = lane & s;
@@ -179,20 +171,25 @@ __device__ __forceinline__ void store_block16(uint8_t* p, int64_t row_bytes, con
   for (int i = 0; i < NU; ++i)
     if (r0 + i < n_rows) *reinterpret_cast<uint4*>(d + i * row_bytes) = make_uint4(w[i][0], w[i][1], w[i][2], w[i][3]);
 }
+// C columns of those rows from fp32, as out_dtype.
 template <int C>
 __device__ __forceinline__ void store_block(uint8_t* p, int64_t row_bytes, const float (&v)[C], int n_rows, int lane,
                                             int out_dtype) {
-  if (out_dtype == MOE_DT_BF16) {
-    store_block16<C>(p, row_bytes, v, n_rows, lane, [](float a, float b) { return Bf16::from2(a, b); });
-  } else if (out_dtype == MOE_DT_F16) {
-    store_block16<C>(p, row_bytes, v, n_rows, lane, [](float a, float b) { return F16::from2(a, b); });
-  } else {
-    // fp32 results are partial sums and small products: a lane stores its row
+  if (out_dtype == MOE_DT_F32) {
+    constexpr int CF = C < 32 ? C : 32;       // 128 bytes a row at a time
 #pragma unroll
-    for (int i = 0; i < C / 4; ++i)
-      if (lane < n_rows)
-        *reinterpret_cast<float4*>(p + lane * row_bytes + 16 * i) =
-            make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+    for (int k = 0; k < C; k += CF) {
+      uint32_t w[CF / 4][4];
+#pragma unroll
+      for (int i = 0; i < CF; ++i) w[i / 4][i & 3] = __float_as_uint(v[k + i]);
+      store_units<CF / 4>(p + 4 * k, row_bytes, w, n_rows, lane);
+    }
+  } else {
+    uint32_t w[C / 8][4];
+#pragma unroll
+    for (int i = 0; i < C / 2; ++i)
+      w[i / 4][i & 3] = out_dtype == MOE_DT_F16 ? F16::from2(v[2 * i], v[2 * i + 1]) : Bf16::from2(v[2 * i], v[2 * i + 1]);
+    store_units<C / 8>(p, row_bytes, w, n_rows, lane);
   }
 }
 
