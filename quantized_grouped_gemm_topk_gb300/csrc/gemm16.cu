@@ -43,8 +43,8 @@ namespace moe {
 
 enum { kRowsNT = 0, kRowsNN = 1, kWgradMN = 2 };
 
-// Reduction a stage: two halves of one 128-byte swizzle row each, behind one
-// barrier. The thread that issues the MMAs spends some 270 cycles a stage
+// Reduction a stage: two halves of one 128-byte swizzle row each, which land
+// behind one barrier and are freed one by one. The thread that issues the MMAs spends some 270 cycles a stage
 // besides the MMAs themselves; with one half a stage that was the bound of
 // tiles narrower than 256 (about 570 cycles a stage whatever their width).
 constexpr int kGH = 64;
@@ -54,7 +54,7 @@ constexpr int kGThreads = 384;
 constexpr int kGChunk = 64 * kGH * 2; // bytes of 64 M / N elements of an MN-contiguous half
 constexpr int kGABytes = kGM * kGH * 2;   // of a half
 constexpr int kGHeadBars = 512;       // barriers and scratch, in front of the group tables
-constexpr int kGMaxStages = 12;
+constexpr int kGMaxStages = 6;
 constexpr int kGSmem = 227 * 1024;
 
 constexpr int kGBoxes = 5;            // K-major B: boxes of 16 << i rows
@@ -146,6 +146,12 @@ __device__ __forceinline__ void g_copy_mn(uint32_t dst, const CUtensorMap* map, 
   }
 }
 
+template <int CG>
+__device__ __forceinline__ void g_commit(uint32_t bar) {
+  if (CG == 2) tc::bar_commit_pair(bar);
+  else tc::bar_commit(bar);
+}
+
 // Whether a stage of the weight gradient ends inside an MMA's K of 16: the
 // group's last rows, `left` of them; the rows behind are cleared in shared
 // memory by each CTA before the MMAs read them.
@@ -185,7 +191,7 @@ __global__ void __launch_bounds__(kGThreads, 1) k_gemm16(const GArgs g, const __
   uint64_t* full = reinterpret_cast<uint64_t*>(base);
   uint64_t* pfull = full + kGMaxStages;         // weight gradient: the rows of a tail stage are cleared
   uint64_t* empty = pfull + kGMaxStages;
-  uint64_t* accfull = empty + kGMaxStages;
+  uint64_t* accfull = empty + 2 * kGMaxStages;    // empty: of each half
   uint64_t* accempty = accfull + 2;
   uint64_t* drain = accempty + 2;
   uint64_t* tgo = drain + 1;                    // weight gradient: a tail stage has landed
@@ -203,7 +209,8 @@ __global__ void __launch_bounds__(kGThreads, 1) k_gemm16(const GArgs g, const __
     for (int i = 0; i < stages; ++i) {
       tc::mbar_init(&full[i], 2);       // one arrival (with its bytes) from each copying warp
       tc::mbar_init(&pfull[i], CG);
-      tc::mbar_init(&empty[i], 1);
+      tc::mbar_init(&empty[2 * i], 1);
+      tc::mbar_init(&empty[2 * i + 1], 1);
     }
     for (int i = 0; i < 2; ++i) {
       tc::mbar_init(&accfull[i], 1);
@@ -259,13 +266,16 @@ __global__ void __launch_bounds__(kGThreads, 1) k_gemm16(const GArgs g, const __
         const int r0 = kWg ? off[w.e] : 0;
         for (int kb = w.k0; kb < w.k1; ++kb) {
           const int k = kb * kGK;
-          if (!tc::bar_wait(empty_u + 8 * slot, phase, abort)) { ok = false; break; }
           const bool own = CG == 1 || (kWg && g_tail(w.red - k));
           const uint32_t bar = (own ? full_u : lead_u) + 8 * slot;
           uint32_t dst = dst0 + slot * 2 * half_bytes;
           const int halves = w.red - k > kGH ? 2 : 1;
-          if (own || rank == 0) tc::bar_arrive_expect_tx(full_u + 8 * slot, (own ? bytes : CG * bytes) * halves);
-          for (int s = 0; s < halves; ++s, dst += half_bytes) {
+          // each half is refilled as soon as its own MMAs are done
+          for (int s = 0; s < 2; ++s, dst += half_bytes) {
+            if (!tc::bar_wait(empty_u + 16 * slot + 8 * s, phase, abort)) { ok = false; break; }
+            if (s == 0 && (own || rank == 0))
+              tc::bar_arrive_expect_tx(full_u + 8 * slot, (own ? bytes : CG * bytes) * halves);
+            if (s == halves) break;
             const int ks = k + s * kGH;
             if (isb) {
               if (kWg) g_copy_mn<CG>(dst, map, c0, r0 + ks, 0, half / 64, g.b_chunks > 1, bar);
@@ -274,8 +284,9 @@ __global__ void __launch_bounds__(kGThreads, 1) k_gemm16(const GArgs g, const __
               if (MODE == kRowsNT) g_copy3<CG>(dst, map, ks, m0, w.e, bar);
               else g_copy_mn<CG>(dst, map, m0, kWg ? r0 + ks : ks, kWg ? 0 : w.e, kGM / 64, g.a_chunks > 1, bar);
             }
+            if (s == 0) ++issued;        // counted as soon as a copy of the stage is in flight
           }
-          ++issued;
+          if (!ok) break;
           if (++slot == stages) {
             slot = 0;
             phase ^= 1;
@@ -322,7 +333,7 @@ __global__ void __launch_bounds__(kGThreads, 1) k_gemm16(const GArgs g, const __
         int left = w.red - w.k0 * kGK;
         for (int n = w.k1 - w.k0; n > 0; --n, left -= kGK) {
           if (!ready && !tc::bar_wait(full_u + 8 * slot, phase, abort)) { ok = false; break; }
-          const uint32_t done = empty_u + 8 * slot, a_now = ad, b_now = bd;
+          const uint32_t done = empty_u + 16 * slot, a_now = ad, b_now = bd;
           const int slot_now = slot;
           ad += 2 * a_half;
           bd += 2 * b_half;
@@ -344,6 +355,7 @@ __global__ void __launch_bounds__(kGThreads, 1) k_gemm16(const GArgs g, const __
           // a step of K = 16: 32 bytes along a K-major row, two 8-row atoms otherwise
           if (left > kGK - 16) {
             tc::mma_f16_x4<CG>(dt, a_now, a_hi, sta, b_now, b_hi, stb, idesc, acc);
+            g_commit<CG>(done);
             tc::mma_f16_x4<CG>(dt, a_now + a_half, a_hi, sta, b_now + b_half, b_hi, stb, idesc, 1u);
           } else {
             const int steps = (left + 15) / 16;
@@ -354,10 +366,10 @@ __global__ void __launch_bounds__(kGThreads, 1) k_gemm16(const GArgs g, const __
               if constexpr (CG == 2) tc::mma_f16_ss_pair(dt, da, db, idesc, j ? 1u : acc);
               else tc::mma_f16_ss(dt, da, db, idesc, j ? 1u : acc);
             }
+            g_commit<CG>(done);
           }
+          g_commit<CG>(done + 8);
           acc = 1;
-          if constexpr (CG == 2) tc::bar_commit_pair(done);
-          else tc::bar_commit(done);
         }
         if (!ok) break;
         if constexpr (CG == 2) tc::mma_commit_pair(&accfull[d]);

@@ -325,9 +325,9 @@ __device__ __forceinline__ bool ring_wait(uint64_t* bar, uint32_t parity) {
 }
 
 template <typename E, bool WF32, int NV, bool PART, bool BWD>
-__global__ void __launch_bounds__(kNormBwdThreads, NV == 1 ? 2 : 1) k_norm_ring(NormArgs a, int stages) {
+__global__ void __launch_bounds__(kNormBwdThreads) k_norm_ring(NormArgs a, int stages) {
   using raw = typename E::raw;
-  constexpr int V = 16 / (int)sizeof(raw);
+  constexpr int V = 16 / (int)sizeof(raw), NP = V / 2;      // pairs of a pack
   pdl_enter();
   __shared__ float2 red[2][kNormBwdThreads / 32];
   extern __shared__ __align__(128) uint8_t ring[];
@@ -352,8 +352,8 @@ __global__ void __launch_bounds__(kNormBwdThreads, NV == 1 ? 2 : 1) k_norm_ring(
   }
   __syncthreads();
   // the thread's columns are the same in every row: weights stay in registers
-  float g[NV * V], b[BWD ? 1 : NV * V];
-  float dg[PART ? NV * V : 1], db[PART ? NV * V : 1];
+  f32x2 g[NV][NP], b[BWD ? 1 : NV][NP];
+  f32x2 dg[PART ? NV : 1][NP], db[PART ? NV : 1][NP];
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
     const int c = (i * tpr + t) * V;
@@ -362,15 +362,15 @@ __global__ void __launch_bounds__(kNormBwdThreads, NV == 1 ? 2 : 1) k_norm_ring(
     for (int j = 0; j < V; ++j) w[j] = 0.f;
     if (c < a.H) weights_at<E, WF32, V>(w, a.gamma, c, 1.f);
 #pragma unroll
-    for (int j = 0; j < V; ++j) g[i * V + j] = w[j];
+    for (int j = 0; j < NP; ++j) g[i][j] = pack2(w[2 * j], w[2 * j + 1]);
     if constexpr (!BWD) {
       if (c < a.H) weights_at<E, WF32, V>(w, a.beta, c, 0.f);
 #pragma unroll
-      for (int j = 0; j < V; ++j) b[i * V + j] = w[j];
+      for (int j = 0; j < NP; ++j) b[i][j] = pack2(w[2 * j], w[2 * j + 1]);
     }
     if constexpr (PART) {
 #pragma unroll
-      for (int j = 0; j < V; ++j) dg[i * V + j] = db[i * V + j] = 0.f;
+      for (int j = 0; j < NP; ++j) dg[i][j] = db[i][j] = 0;
     }
   }
   float mu = 0.f, r = 0.f, mu_next = 0.f, r_next = 0.f;
@@ -404,71 +404,77 @@ __global__ void __launch_bounds__(kNormBwdThreads, NV == 1 ? 2 : 1) k_norm_ring(
     raw* out = reinterpret_cast<raw*>(a.out) + row * a.ldo;
     const float bad = got ? 0.f : __int_as_float(0x7fffffff);
     if constexpr (BWD) {
-      float s1 = bad, s2 = 0.f;
+      const f32x2 nmu = pack2(-mu, -mu), rr = pack2(r, r);
+      f32x2 s1 = pack2(bad, 0.f), s2 = 0;
 #pragma unroll
       for (int i = 0; i < NV; ++i)
         if ((i * tpr + t) * V < a.H) {
 #pragma unroll
-          for (int j = 0; j < V; ++j) {
-            const float d = E::to(pd[i].v[j]), xh = (E::to(px[i].v[j]) - mu) * r, tg = d * g[i * V + j];
-            s1 += tg;
-            s2 = fmaf(tg, xh, s2);
+          for (int j = 0; j < NP; ++j) {
+            const f32x2 d = pd[i].pair(j), xh = mul2(add2(px[i].pair(j), nmu), rr), tg = mul2(d, g[i][j]);
+            s1 = add2(s1, tg);
+            s2 = fma2(tg, xh, s2);
             if constexpr (PART) {
-              dg[i * V + j] = fmaf(d, xh, dg[i * V + j]);
-              db[i * V + j] += d;
+              dg[i][j] = fma2(d, xh, dg[i][j]);
+              db[i][j] = add2(db[i][j], d);
             }
           }
         }
-      const float2 m = row_sum2<true>(s1, s2, red[flip], nw);
+      const float2 u1 = unpack2(s1), u2 = unpack2(s2);
+      const float2 m = row_sum2<true>(u1.x + u1.y, u2.x + u2.y, red[flip], nw);
       flip ^= 1;
       if (t == 0) fetch(s, row + (int64_t)stages * gridDim.x);
       const float m1 = m.x * inv_h, m2 = m.y * inv_h;
+      const f32x2 nm1 = pack2(-m1, -m1), nm2 = pack2(-m2, -m2);
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
         const int c = (i * tpr + t) * V;
         if (c < a.H) {
           Pack<E, V> o;
 #pragma unroll
-          for (int j = 0; j < V; ++j) {
-            const float xh = (E::to(px[i].v[j]) - mu) * r;
-            o.v[j] = E::from(r * (E::to(pd[i].v[j]) * g[i * V + j] - m1 - xh * m2));
+          for (int j = 0; j < NP; ++j) {
+            const f32x2 xh = mul2(add2(px[i].pair(j), nmu), rr);
+            o.set_pair(j, mul2(rr, fma2(xh, nm2, fma2(pd[i].pair(j), g[i][j], nm1))));
           }
           store_pack<E, V>(out + c, o);
         }
       }
     } else {
-      float sum = bad;
+      f32x2 sum = pack2(bad, 0.f);
 #pragma unroll
       for (int i = 0; i < NV; ++i)
         if ((i * tpr + t) * V < a.H) {
 #pragma unroll
-          for (int j = 0; j < V; ++j) sum += E::to(px[i].v[j]);
+          for (int j = 0; j < NP; ++j) sum = add2(sum, px[i].pair(j));
         }
-      mu = row_sum<true>(sum, red[0], nw) * inv_h;
+      const float2 us = unpack2(sum);
+      mu = row_sum<true>(us.x + us.y, red[0], nw) * inv_h;
       if (t == 0) fetch(s, row + (int64_t)stages * gridDim.x);
-      float m2 = 0.f;
+      const f32x2 nmu = pack2(-mu, -mu);
+      f32x2 m2 = 0;
 #pragma unroll
       for (int i = 0; i < NV; ++i)
         if ((i * tpr + t) * V < a.H) {
 #pragma unroll
-          for (int j = 0; j < V; ++j) {
-            const float d = E::to(px[i].v[j]) - mu;
-            m2 = fmaf(d, d, m2);
+          for (int j = 0; j < NP; ++j) {
+            const f32x2 d = add2(px[i].pair(j), nmu);
+            m2 = fma2(d, d, m2);
           }
         }
-      r = rsqrtf(row_sum<true>(m2, red[1], nw) * inv_h + a.eps);
+      const float2 um = unpack2(m2);
+      r = rsqrtf(row_sum<true>(um.x + um.y, red[1], nw) * inv_h + a.eps);
       if (t == 0) {
         if (a.mean) a.mean[row] = mu;
         if (a.rstd) a.rstd[row] = r;
       }
+      const f32x2 rr = pack2(r, r);
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
         const int c = (i * tpr + t) * V;
         if (c < a.H) {
           Pack<E, V> o;
 #pragma unroll
-          for (int j = 0; j < V; ++j)
-            o.v[j] = E::from(fmaf((E::to(px[i].v[j]) - mu) * r, g[i * V + j], b[i * V + j]));
+          for (int j = 0; j < NP; ++j) o.set_pair(j, fma2(mul2(add2(px[i].pair(j), nmu), rr), g[i][j], b[i][j]));
           store_pack<E, V>(out + c, o);
         }
       }
@@ -485,9 +491,9 @@ __global__ void __launch_bounds__(kNormBwdThreads, NV == 1 ? 2 : 1) k_norm_ring(
       const int c = (i * tpr + t) * V;
       if (c < a.H) {
 #pragma unroll
-        for (int j = 0; j < V; ++j) {
-          pg[c + j] = dg[i * V + j];
-          pg[a.H + c + j] = db[i * V + j];
+        for (int j = 0; j < NP; ++j) {
+          *reinterpret_cast<f32x2*>(pg + c + 2 * j) = dg[i][j];
+          *reinterpret_cast<f32x2*>(pg + a.H + c + 2 * j) = db[i][j];
         }
       }
     }

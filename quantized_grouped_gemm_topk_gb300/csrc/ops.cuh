@@ -35,10 +35,45 @@ struct F32 {
   static __device__ __forceinline__ raw from(float f) { return f; }
 };
 
+// Two fp32 values to an instruction (add / mul / fma .f32x2).
+typedef unsigned long long f32x2;
+__device__ __forceinline__ f32x2 pack2(float a, float b) {
+  f32x2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float2 unpack2(f32x2 v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b) {
+  f32x2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) {
+  f32x2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
+  f32x2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+
 // V consecutive elements as one access (V * sizeof(raw) is 16, or V is 1).
 template <typename E, int V>
 struct Pack {
   typename E::raw v[V];
+  // elements 2 i and 2 i + 1
+  __device__ __forceinline__ f32x2 pair(int i) const { return pack2(E::to(v[2 * i]), E::to(v[2 * i + 1])); }
+  __device__ __forceinline__ void set_pair(int i, f32x2 p) {
+    const float2 f = unpack2(p);
+    if constexpr (sizeof(typename E::raw) == 2) reinterpret_cast<uint32_t*>(v)[i] = E::from2(f.x, f.y);
+    else { v[2 * i] = f.x; v[2 * i + 1] = f.y; }
+  }
 };
 template <typename E, int V>
 __device__ __forceinline__ void load_pack(Pack<E, V>& p, const typename E::raw* src) {
