@@ -406,6 +406,9 @@ __global__ void __launch_bounds__(kNormBwdThreads) k_norm_ring(NormArgs a, int s
     if constexpr (BWD) {
       const f32x2 nmu = pack2(-mu, -mu), rr = pack2(r, r);
       f32x2 s1 = pack2(bad, 0.f), s2 = 0;
+      // one pack a thread: xh and dy gamma are kept for the second pass
+      constexpr bool kKeep = NV == 1;
+      f32x2 xk[kKeep ? NP : 1], tk[kKeep ? NP : 1];
 #pragma unroll
       for (int i = 0; i < NV; ++i)
         if ((i * tpr + t) * V < a.H) {
@@ -414,6 +417,10 @@ __global__ void __launch_bounds__(kNormBwdThreads) k_norm_ring(NormArgs a, int s
             const f32x2 d = pd[i].pair(j), xh = mul2(add2(px[i].pair(j), nmu), rr), tg = mul2(d, g[i][j]);
             s1 = add2(s1, tg);
             s2 = fma2(tg, xh, s2);
+            if constexpr (kKeep) {
+              xk[j] = xh;
+              tk[j] = tg;
+            }
             if constexpr (PART) {
               dg[i][j] = fma2(d, xh, dg[i][j]);
               db[i][j] = add2(db[i][j], d);
@@ -424,8 +431,9 @@ __global__ void __launch_bounds__(kNormBwdThreads) k_norm_ring(NormArgs a, int s
       const float2 m = row_sum2<true>(u1.x + u1.y, u2.x + u2.y, red[flip], nw);
       flip ^= 1;
       if (t == 0) fetch(s, row + (int64_t)stages * gridDim.x);
-      const float m1 = m.x * inv_h, m2 = m.y * inv_h;
-      const f32x2 nm1 = pack2(-m1, -m1), nm2 = pack2(-m2, -m2);
+      // r (t - m1 - xh m2)
+      const float m1 = -r * (m.x * inv_h), m2 = -r * (m.y * inv_h);
+      const f32x2 nm1 = pack2(m1, m1), nm2 = pack2(m2, m2);
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
         const int c = (i * tpr + t) * V;
@@ -433,8 +441,12 @@ __global__ void __launch_bounds__(kNormBwdThreads) k_norm_ring(NormArgs a, int s
           Pack<E, V> o;
 #pragma unroll
           for (int j = 0; j < NP; ++j) {
-            const f32x2 xh = mul2(add2(px[i].pair(j), nmu), rr);
-            o.set_pair(j, mul2(rr, fma2(xh, nm2, fma2(pd[i].pair(j), g[i][j], nm1))));
+            if constexpr (kKeep) {
+              o.set_pair(j, fma2(tk[j], rr, fma2(xk[j], nm2, nm1)));
+            } else {
+              const f32x2 xh = mul2(add2(px[i].pair(j), nmu), rr);
+              o.set_pair(j, fma2(mul2(pd[i].pair(j), g[i][j]), rr, fma2(xh, nm2, nm1)));
+            }
           }
           store_pack<E, V>(out + c, o);
         }
@@ -560,15 +572,13 @@ __global__ void __launch_bounds__(1024) k_norm_dw_sum(const float* __restrict__ 
   const int64_t at = (int64_t)blockIdx.y * H + c;
   float v = 0.f;
   if (c < H) {
-    int p = l;
-    for (; p + 7 * 32 < P; p += 8 * 32) {       // eight loads in flight
-      float t[8];
+    for (int p = l; p < P; p += 10 * 32) {      // ten loads in flight
+      float t[10];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) t[j] = part[(int64_t)(p + 32 * j) * 2 * H + at];
+      for (int j = 0; j < 10; ++j) t[j] = p + 32 * j < P ? part[(int64_t)(p + 32 * j) * 2 * H + at] : 0.f;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v += t[j];
+      for (int j = 0; j < 10; ++j) v += t[j];
     }
-    for (; p < P; p += 32) v += part[(int64_t)p * 2 * H + at];
   }
   s[l][threadIdx.x & 31] = v;
   __syncthreads();
