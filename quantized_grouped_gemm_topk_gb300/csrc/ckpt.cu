@@ -172,16 +172,21 @@ __device__ __forceinline__ float bwd16(uint32_t (&dg)[8], uint32_t (&du)[8], uin
   return dw;
 }
 
-template <typename E, bool VEC, int ACT>
+// qpr quarter-warps share a row. WARP: at most four, of one warp: the row's dw
+// needs shuffles only, and warps go on at their own pace. Otherwise all of a
+// CTA's may share one (few rows), and dw crosses shared memory.
+template <typename E, bool VEC, int ACT, bool WARP>
 __global__ void __launch_bounds__(kCkptThreads) k_ckpt_bwd(CkptArgs a, int qpr) {
   constexpr bool GATED = ACT != MOE_ACT_SRELU;
   pdl_enter();
-  __shared__ float sdw[2][kCkptQuarters];
-  const int l = threadIdx.x & 7, qw = threadIdx.x >> 3;
+  __shared__ float sdw[2][WARP ? 1 : kCkptQuarters];
+  const int l = threadIdx.x & 7, qw = WARP ? (threadIdx.x & 31) >> 3 : threadIdx.x >> 3;
   const int nb = (a.I + kQBlock - 1) / kQBlock;
-  const int rpc = kCkptQuarters / qpr, rl = qw / qpr, part = qw % qpr;
+  const int rpg = (WARP ? 4 : kCkptQuarters) / qpr, rl = qw / qpr, part = qw % qpr;   // rows a warp (CTA) takes
+  const int64_t group = WARP ? (int64_t)blockIdx.x * (kCkptThreads / 32) + (threadIdx.x >> 5) : blockIdx.x;
+  const int64_t groups = WARP ? (int64_t)gridDim.x * (kCkptThreads / 32) : gridDim.x;
   int flip = 0;
-  for (int64_t r0 = (int64_t)blockIdx.x * rpc; r0 < a.R; r0 += (int64_t)gridDim.x * rpc, flip ^= 1) {
+  for (int64_t r0 = group * rpg; r0 < a.R; r0 += groups * rpg, flip ^= 1) {
     const int64_t row = r0 + rl;
     const bool live = row < a.R;
     const float w = live && a.w ? a.w[row] : 1.f;
@@ -215,12 +220,18 @@ __global__ void __launch_bounds__(kCkptThreads) k_ckpt_bwd(CkptArgs a, int qpr) 
       __syncwarp();
 #pragma unroll
       for (int o = 4; o > 0; o >>= 1) dw += __shfl_xor_sync(kFull, dw, o);
-      if (l == 0) sdw[flip][qw] = dw;
-      __syncthreads();
-      if (live && part == 0 && l == 0) {
-        float t = 0.f;
-        for (int i = 0; i < qpr; ++i) t += sdw[flip][qw + i];
-        a.dw[row] = t;
+      if constexpr (WARP) {
+        if (qpr > 1) dw += __shfl_xor_sync(kFull, dw, 8);
+        if (qpr > 2) dw += __shfl_xor_sync(kFull, dw, 16);
+        if (live && part == 0 && l == 0) a.dw[row] = dw;
+      } else {
+        if (l == 0) sdw[flip][qw] = dw;
+        __syncthreads();
+        if (live && part == 0 && l == 0) {
+          float t = 0.f;
+          for (int i = 0; i < qpr; ++i) t += sdw[flip][qw + i];
+          a.dw[row] = t;
+        }
       }
     }
   }
@@ -240,15 +251,21 @@ static cudaError_t fwd_t(const CkptArgs& a, cudaStream_t st) {
   return launch_pdl(k_ckpt_fwd<E, false, ACT>, dim3((unsigned)g), dim3(kCkptThreads), 0, st, a, qpr);
 }
 
+template <typename E, int ACT, bool WARP>
+static cudaError_t bwd_w(const CkptArgs& a, bool vec, int qpr, cudaStream_t st) {
+  const int64_t rows = WARP ? kCkptThreads / 32 * (4 / qpr) : kCkptQuarters / qpr;     // a CTA's
+  const int64_t g = std::min<int64_t>((a.R + rows - 1) / rows, (int64_t)device_sms() * 32);
+  note_launch();
+  if (vec) return launch_pdl(k_ckpt_bwd<E, true, ACT, WARP>, dim3((unsigned)g), dim3(kCkptThreads), 0, st, a, qpr);
+  return launch_pdl(k_ckpt_bwd<E, false, ACT, WARP>, dim3((unsigned)g), dim3(kCkptThreads), 0, st, a, qpr);
+}
 template <typename E, int ACT>
 static cudaError_t bwd_t(const CkptArgs& a, cudaStream_t st) {
   const bool vec = a.I % 8 == 0 && a.lddy % 8 == 0 && a.lddh % 8 == 0 && a.ldq % 8 == 0 && al(a.dy, 16) &&
                    al(a.dh, 16) && al(a.q, 8) && (!a.y || (a.ldy % 8 == 0 && al(a.y, 16)));
-  const int qpr = quarters_a_row(a.I, kCkptQuarters), rpc = kCkptQuarters / qpr;
-  const int64_t g = std::min<int64_t>((a.R + rpc - 1) / rpc, (int64_t)device_sms() * 32);
-  note_launch();
-  if (vec) return launch_pdl(k_ckpt_bwd<E, true, ACT>, dim3((unsigned)g), dim3(kCkptThreads), 0, st, a, qpr);
-  return launch_pdl(k_ckpt_bwd<E, false, ACT>, dim3((unsigned)g), dim3(kCkptThreads), 0, st, a, qpr);
+  // a warp a row (or more rows) where that leaves every SM a full set of warps
+  if (a.R >= 32LL * device_sms()) return bwd_w<E, ACT, true>(a, vec, quarters_a_row(a.I, 4), st);
+  return bwd_w<E, ACT, false>(a, vec, quarters_a_row(a.I, kCkptQuarters), st);
 }
 
 template <typename E, bool FWD>
