@@ -114,7 +114,8 @@ __device__ __forceinline__ void store_row_pack(typename E::raw* row, const Pack<
   } else {
     const uint4 u = *reinterpret_cast<const uint4*>(&p);
     const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-    store_any<(int)sizeof(typename E::raw)>(row + c, w, H - c);
+    if (c + V <= H) store_inner<(int)sizeof(typename E::raw)>(row + c, w);
+    else store_any<(int)sizeof(typename E::raw)>(row + c, w, H - c);
   }
 }
 // The pack's weights; single loads where they are not aligned or the row ends
@@ -311,8 +312,7 @@ __global__ void __launch_bounds__(BLOCK ? kNormBwdThreads : 128) k_norm_bwd(Norm
 // Registers alone keep too few bytes in flight (a row's barriers come between
 // its loads and the next row's): thread 0 keeps kRing bulk copies of rows
 // ahead in shared memory. A stage is refilled behind the row's first barrier,
-// when every thread has its packs in registers. Rows start on 16 bytes and are
-// a whole number of packs.
+// when every thread has its packs in registers.
 constexpr int kRingMax = 8;
 constexpr int kRingBytes = 200 * 1024;    // of an SM's shared memory, for all its CTAs
 constexpr int kRingHead = 128;            // barriers, in front of the stages
@@ -324,7 +324,43 @@ __device__ __forceinline__ bool ring_wait(uint64_t* bar, uint32_t parity) {
   return tc::mbar_wait(bar, parity, &give_up);
 }
 
-template <typename E, bool WF32, int NV, bool PART, bool BWD>
+// Bytes of a row of `bytes` from p as a stage holds them: from the 16-byte
+// boundary at or before p, with a unit to spare behind.
+__host__ __device__ inline uint32_t ring_row_bytes(uint32_t bytes, bool any) {
+  return any ? (bytes + 15) / 16 * 16 + 32 : bytes;
+}
+// ANY: a row at any alignment, copied with the rest of the 16-byte units that
+// it starts and ends in. Those belong to the rows before and after it; the
+// first row's head and the last row's tail, where there may be nothing, go
+// element by element.
+template <typename raw, bool ANY>
+__device__ __forceinline__ void ring_copy(uint8_t* d, const raw* p, uint32_t bytes, bool head, bool tail, uint64_t* bar) {
+  if constexpr (!ANY) {
+    tc::mbar_arrive_expect_tx(bar, bytes);
+    tc::bulk_g2s_plain(d, p, bytes, bar);
+  } else {
+    const uint8_t* lo = reinterpret_cast<const uint8_t*>(p);
+    const uint8_t* hi = lo + bytes;
+    const uint8_t* a = reinterpret_cast<const uint8_t*>((uintptr_t)lo & ~(uintptr_t)15);
+    const uint8_t* b = reinterpret_cast<const uint8_t*>(((uintptr_t)hi + 15) & ~(uintptr_t)15);
+    const uint8_t* base = a;
+    if (head && a != lo) {
+      a += 16;
+      for (const uint8_t* e = lo; e < a && e < hi; e += sizeof(raw))
+        *reinterpret_cast<raw*>(d + (e - base)) = *reinterpret_cast<const raw*>(e);
+    }
+    if (tail && b != hi) {
+      b -= 16;
+      for (const uint8_t* e = b < lo ? lo : b; e < hi; e += sizeof(raw))
+        *reinterpret_cast<raw*>(d + (e - base)) = *reinterpret_cast<const raw*>(e);
+    }
+    const uint32_t n = b > a ? (uint32_t)(b - a) : 0u;
+    tc::mbar_arrive_expect_tx(bar, n);
+    if (n) tc::bulk_g2s_plain(d + (a - base), a, n, bar);
+  }
+}
+
+template <typename E, bool WF32, int NV, bool PART, bool BWD, bool ANY>
 __global__ void __launch_bounds__(kNormBwdThreads) k_norm_ring(NormArgs a, int stages) {
   using raw = typename E::raw;
   constexpr int V = 16 / (int)sizeof(raw), NP = V / 2;      // pairs of a pack
@@ -332,7 +368,7 @@ __global__ void __launch_bounds__(kNormBwdThreads) k_norm_ring(NormArgs a, int s
   __shared__ float2 red[2][kNormBwdThreads / 32];
   extern __shared__ __align__(128) uint8_t ring[];
   uint64_t* full = reinterpret_cast<uint64_t*>(ring);
-  const uint32_t row_bytes = (uint32_t)a.H * sizeof(raw);
+  const uint32_t bytes = (uint32_t)a.H * sizeof(raw), row_bytes = ring_row_bytes(bytes, ANY);
   const uint32_t stage_bytes = row_bytes * (BWD ? 2 : 1);
   const int tpr = blockDim.x, t = threadIdx.x, nw = tpr / 32;
   const float inv_h = 1.0f / (float)a.H;
@@ -341,12 +377,28 @@ __global__ void __launch_bounds__(kNormBwdThreads) k_norm_ring(NormArgs a, int s
   auto fetch = [&](int s, int64_t row) {
     if (row >= a.T) return;
     uint8_t* d = ring + kRingHead + s * stage_bytes;
-    tc::mbar_arrive_expect_tx(&full[s], stage_bytes);
-    tc::bulk_g2s_plain(d, X + row * a.ldx, row_bytes, &full[s]);
-    if (BWD) tc::bulk_g2s_plain(d + row_bytes, DY + row * a.lddy, row_bytes, &full[s]);
+    ring_copy<raw, ANY>(d, X + row * a.ldx, bytes, row == 0, row == a.T - 1, &full[s]);
+    if (BWD) ring_copy<raw, ANY>(d + row_bytes, DY + row * a.lddy, bytes, row == 0, row == a.T - 1, &full[s]);
+  };
+  // pack c of the row in a stage; ANY: elements past the row's end are zeros
+  auto pack_of = [&](Pack<E, V>& p, const uint8_t* src, const raw* row, int c) {
+    if constexpr (!ANY) {
+      load_pack(p, reinterpret_cast<const raw*>(src) + c * V);
+    } else {
+      const int off = (int)((uintptr_t)row & 15);
+      const uint4 u0 = reinterpret_cast<const uint4*>(src)[c], u1 = reinterpret_cast<const uint4*>(src)[c + 1];
+      uint32_t w[8] = {u0.x, u0.y, u0.z, u0.w, u1.x, u1.y, u1.z, u1.w}, r4[4];
+      shift_units<(int)sizeof(raw), 16>(r4, w, off);
+      *reinterpret_cast<uint4*>(&p) = make_uint4(r4[0], r4[1], r4[2], r4[3]);
+      if (c * V + V > a.H) {
+#pragma unroll
+        for (int j = 0; j < V; ++j)
+          if (c * V + j >= a.H) p.v[j] = 0;
+      }
+    }
   };
   if (t == 0) {
-    for (int s = 0; s < stages; ++s) tc::mbar_init(&full[s], 1);
+    for (int s = 0; s < stages; ++s) tc::mbar_init(&full[s], BWD ? 2 : 1);
     tc::fence_mbar_init();
     for (int s = 0; s < stages; ++s) fetch(s, blockIdx.x + (int64_t)s * gridDim.x);
   }
@@ -360,11 +412,11 @@ __global__ void __launch_bounds__(kNormBwdThreads) k_norm_ring(NormArgs a, int s
     float w[V];
 #pragma unroll
     for (int j = 0; j < V; ++j) w[j] = 0.f;
-    if (c < a.H) weights_at<E, WF32, V>(w, a.gamma, c, 1.f);
+    if (c < a.H) row_weights<E, WF32, V, !ANY>(w, a.gamma, c, a.H, 1.f);
 #pragma unroll
     for (int j = 0; j < NP; ++j) g[i][j] = pack2(w[2 * j], w[2 * j + 1]);
     if constexpr (!BWD) {
-      if (c < a.H) weights_at<E, WF32, V>(w, a.beta, c, 0.f);
+      if (c < a.H) row_weights<E, WF32, V, !ANY>(w, a.beta, c, a.H, 0.f);
 #pragma unroll
       for (int j = 0; j < NP; ++j) b[i][j] = pack2(w[2 * j], w[2 * j + 1]);
     }
@@ -397,8 +449,8 @@ __global__ void __launch_bounds__(kNormBwdThreads) k_norm_ring(NormArgs a, int s
     for (int i = 0; i < NV; ++i) {
       const int c = i * tpr + t;
       if (c * V < a.H) {
-        load_pack(px[i], reinterpret_cast<const raw*>(sx) + c * V);
-        if constexpr (BWD) load_pack(pd[i], reinterpret_cast<const raw*>(sx + row_bytes) + c * V);
+        pack_of(px[i], sx, X + row * a.ldx, c);
+        if constexpr (BWD) pack_of(pd[i], sx + row_bytes, DY + row * a.lddy, c);
       }
     }
     raw* out = reinterpret_cast<raw*>(a.out) + row * a.ldo;
@@ -448,7 +500,7 @@ __global__ void __launch_bounds__(kNormBwdThreads) k_norm_ring(NormArgs a, int s
               o.set_pair(j, fma2(mul2(pd[i].pair(j), g[i][j]), rr, fma2(xh, nm2, nm1)));
             }
           }
-          store_pack<E, V>(out + c, o);
+          store_row_pack<E, V, !ANY>(out, o, c, a.H);
         }
       }
     } else {
@@ -469,7 +521,11 @@ __global__ void __launch_bounds__(kNormBwdThreads) k_norm_ring(NormArgs a, int s
         if ((i * tpr + t) * V < a.H) {
 #pragma unroll
           for (int j = 0; j < NP; ++j) {
-            const f32x2 d = add2(px[i].pair(j), nmu);
+            f32x2 d = add2(px[i].pair(j), nmu);
+            if (ANY) {                                  // past the row's end
+              const int c = (i * tpr + t) * V + 2 * j;
+              if (c + 1 >= a.H) d = c >= a.H ? 0 : pack2(unpack2(d).x, 0.f);
+            }
             m2 = fma2(d, d, m2);
           }
         }
@@ -487,7 +543,7 @@ __global__ void __launch_bounds__(kNormBwdThreads) k_norm_ring(NormArgs a, int s
           Pack<E, V> o;
 #pragma unroll
           for (int j = 0; j < NP; ++j) o.set_pair(j, fma2(mul2(add2(px[i].pair(j), nmu), rr), g[i][j], b[i][j]));
-          store_pack<E, V>(out + c, o);
+          store_row_pack<E, V, !ANY>(out, o, c, a.H);
         }
       }
     }
@@ -504,8 +560,15 @@ __global__ void __launch_bounds__(kNormBwdThreads) k_norm_ring(NormArgs a, int s
       if (c < a.H) {
 #pragma unroll
         for (int j = 0; j < NP; ++j) {
-          *reinterpret_cast<f32x2*>(pg + c + 2 * j) = dg[i][j];
-          *reinterpret_cast<f32x2*>(pg + a.H + c + 2 * j) = db[i][j];
+          const float2 u = unpack2(dg[i][j]), v = unpack2(db[i][j]);
+          if (!ANY || c + 2 * j < a.H) {
+            pg[c + 2 * j] = u.x;
+            pg[a.H + c + 2 * j] = v.x;
+          }
+          if (!ANY || c + 2 * j + 1 < a.H) {
+            pg[c + 2 * j + 1] = u.y;
+            pg[a.H + c + 2 * j + 1] = v.y;
+          }
         }
       }
     }
@@ -641,9 +704,9 @@ static NormPlan norm_plan(int64_t n, int64_t T, int resident, int max_parts, int
 // Launch of the ring, or cudaErrorNotSupported where it does not apply: few
 // rows (their latency is shorter without it), rows of at most a warp's packs
 // (many rows in flight already) or of more than the registers hold.
-template <typename E, bool WF32, int NV, bool PART, bool BWD>
+template <typename E, bool WF32, int NV, bool PART, bool BWD, bool ANY>
 static cudaError_t ring_nv(const NormArgs& a, int threads, int64_t* parts, cudaStream_t st) {
-  const auto kern = k_norm_ring<E, WF32, NV, PART, BWD>;
+  const auto kern = k_norm_ring<E, WF32, NV, PART, BWD, ANY>;
   static std::atomic<int> regs{0};
   if (regs.load(std::memory_order_acquire) == 0) {
     cudaFuncAttributes at;
@@ -654,7 +717,7 @@ static cudaError_t ring_nv(const NormArgs& a, int threads, int64_t* parts, cudaS
   static std::atomic<bool> done[kMaxDevices] = {};
   cudaError_t e = set_smem_once((const void*)kern, kRingBytes + 1024, done);
   if (e != cudaSuccess) return e;
-  const int stage = a.H * (int)sizeof(typename E::raw) * (BWD ? 2 : 1);
+  const int stage = (int)ring_row_bytes((uint32_t)a.H * sizeof(typename E::raw), ANY) * (BWD ? 2 : 1);
   // CTAs an SM holds (registers are handed out to four warps at a time), each
   // with at least two stages; then all the stages that fit
   int ctas = std::max(1, std::min({6, 65536 / (regs.load() * ((threads + 127) / 128 * 128)), 2048 / threads}));
@@ -666,29 +729,27 @@ static cudaError_t ring_nv(const NormArgs& a, int threads, int64_t* parts, cudaS
   note_launch();
   return launch_pdl(kern, dim3((unsigned)grid), dim3(threads), (size_t)kRingHead + (size_t)stages * stage, st, a, stages);
 }
-template <typename E, bool WF32, bool PART, bool BWD>
+template <typename E, bool WF32, bool PART, bool BWD, bool ANY>
 static cudaError_t ring_launch(const NormArgs& a, int64_t* parts, cudaStream_t st) {
   constexpr int V = 16 / (int)sizeof(typename E::raw);
-  const int n = a.H / V;
+  const int n = (a.H + V - 1) / V;
   if (n <= 32 || n > 4 * kNormBwdThreads || a.T < 4LL * device_sms()) return cudaErrorNotSupported;
   // one pack a thread while that is at most 512 threads, then two, four: the
   // sums over rows of a thread's columns stay in registers, and the fewer of
   // them the more warps hide the row's barriers
   const int nv = n <= kNormBwdThreads ? 1 : n <= 2 * kNormBwdThreads ? 2 : 4;
   const int threads = ((n + nv - 1) / nv + 31) / 32 * 32;
-  if (nv == 1) return ring_nv<E, WF32, 1, PART, BWD>(a, threads, parts, st);
-  return nv == 2 ? ring_nv<E, WF32, 2, PART, BWD>(a, threads, parts, st)
-                 : ring_nv<E, WF32, 4, PART, BWD>(a, threads, parts, st);
+  if (nv == 1) return ring_nv<E, WF32, 1, PART, BWD, ANY>(a, threads, parts, st);
+  return nv == 2 ? ring_nv<E, WF32, 2, PART, BWD, ANY>(a, threads, parts, st)
+                 : ring_nv<E, WF32, 4, PART, BWD, ANY>(a, threads, parts, st);
 }
 
 template <typename E, bool WF32, bool VEC>
 static cudaError_t fwd_v(const NormArgs& a, cudaStream_t st) {
   constexpr int V = 16 / (int)sizeof(typename E::raw);
-  if constexpr (VEC) {
-    int64_t parts;
-    const cudaError_t e = ring_launch<E, WF32, false, false>(a, &parts, st);
-    if (e != cudaErrorNotSupported) return e;
-  }
+  int64_t ring_parts;
+  const cudaError_t re = ring_launch<E, WF32, false, false, !VEC>(a, &ring_parts, st);
+  if (re != cudaErrorNotSupported) return re;
   const NormPlan p = norm_plan(((int64_t)a.H + V - 1) / V, a.T, 0, 0, kNormMaxThreads);
   const dim3 g((unsigned)p.grid), b(p.threads);
   note_launch();
@@ -714,8 +775,7 @@ static cudaError_t bwd_v(const NormArgs& a, cudaStream_t st) {
   const NormPlan p = norm_plan(((int64_t)a.H + V - 1) / V, a.T, 512, want ? kNormMaxParts : 0, kNormBwdThreads);
   cudaError_t e = cudaErrorNotSupported;
   int64_t parts = std::min<int64_t>(a.T, p.grid * (p.block ? 1 : p.threads / 32));
-  if constexpr (VEC)
-    e = want ? ring_launch<E, WF32, true, true>(a, &parts, st) : ring_launch<E, WF32, false, true>(a, &parts, st);
+  e = want ? ring_launch<E, WF32, true, true, !VEC>(a, &parts, st) : ring_launch<E, WF32, false, true, !VEC>(a, &parts, st);
   if (e != cudaErrorNotSupported) {
   } else if (p.longrow) {
     note_launch();

@@ -120,23 +120,10 @@ __device__ __forceinline__ void load_unit(uint32_t (&w)[N / 4], const uint8_t* q
     }
   }
 }
+// The N bytes from byte `off` of 2 N.
 template <int ES, int N>
-__device__ __forceinline__ void load_any(uint32_t (&r)[N / 4], const void* at, const void* lo_, const void* hi_) {
-  const uint8_t *p = reinterpret_cast<const uint8_t*>(at), *lo = reinterpret_cast<const uint8_t*>(lo_),
-                *hi = reinterpret_cast<const uint8_t*>(hi_);
+__device__ __forceinline__ void shift_units(uint32_t (&r)[N / 4], uint32_t (&w)[N / 2], int off) {
   constexpr int W = N / 4;
-  const int off = (int)((uintptr_t)p & (N - 1));
-  uint32_t a[W], b[W];
-#pragma unroll
-  for (int i = 0; i < W; ++i) a[i] = b[i] = 0u;
-  if (p < hi) load_unit<ES, N>(a, p - off, lo, hi);
-  if (off && p - off + N < hi) load_unit<ES, N>(b, p - off + N, lo, hi);
-  uint32_t w[2 * W];
-#pragma unroll
-  for (int i = 0; i < W; ++i) {
-    w[i] = a[i];
-    w[W + i] = b[i];
-  }
   if constexpr (W == 4) {
     const bool two = off & 8;
 #pragma unroll
@@ -153,6 +140,24 @@ __device__ __forceinline__ void load_any(uint32_t (&r)[N / 4], const void* at, c
 #pragma unroll
     for (int i = 0; i < W; ++i) r[i] = w[i];
   }
+}
+template <int ES, int N>
+__device__ __forceinline__ void load_any(uint32_t (&r)[N / 4], const void* at, const void* lo_, const void* hi_) {
+  const uint8_t *p = reinterpret_cast<const uint8_t*>(at), *lo = reinterpret_cast<const uint8_t*>(lo_),
+                *hi = reinterpret_cast<const uint8_t*>(hi_);
+  constexpr int W = N / 4;
+  const int off = (int)((uintptr_t)p & (N - 1));
+  uint32_t a[W], b[W], w[2 * W];
+#pragma unroll
+  for (int i = 0; i < W; ++i) a[i] = b[i] = 0u;
+  if (p < hi) load_unit<ES, N>(a, p - off, lo, hi);
+  if (off && p - off + N < hi) load_unit<ES, N>(b, p - off + N, lo, hi);
+#pragma unroll
+  for (int i = 0; i < W; ++i) {
+    w[i] = a[i];
+    w[W + i] = b[i];
+  }
+  shift_units<ES, N>(r, w, off);
 }
 
 // Stores the first n of 16 / ES (ES 2, 4) elements at any element alignment.
@@ -177,6 +182,22 @@ __device__ __forceinline__ void store_any(void* at, const uint32_t (&w)[4], int 
       else if (bytes >= 4 * i + 4) *reinterpret_cast<uint16_t*>(p + 4 * i + 2) = (uint16_t)v;
     }
     if (bytes >= 16) *reinterpret_cast<uint16_t*>(p + 14) = (uint16_t)(w[3] >> 16);
+  }
+}
+// All 16 bytes at any element alignment.
+template <int ES>
+__device__ __forceinline__ void store_inner(void* at, const uint32_t (&w)[4]) {
+  uint8_t* p = reinterpret_cast<uint8_t*>(at);
+  if (((uintptr_t)p & 15) == 0) {
+    *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+  } else if (ES == 4 || ((uintptr_t)p & 3) == 0) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) reinterpret_cast<uint32_t*>(p)[i] = w[i];
+  } else {
+    *reinterpret_cast<uint16_t*>(p) = (uint16_t)w[0];
+#pragma unroll
+    for (int i = 0; i < 3; ++i) *reinterpret_cast<uint32_t*>(p + 4 * i + 2) = __funnelshift_r(w[i], w[i + 1], 16);
+    *reinterpret_cast<uint16_t*>(p + 14) = (uint16_t)(w[3] >> 16);
   }
 }
 // Stores the first n of eight bytes at any address.

@@ -88,6 +88,28 @@ def test_layer_norm_many_rows(T, H, dtype, wdtype):
     test_layer_norm(T, H, dtype, wdtype, 0)
 
 
+@pytest.mark.parametrize("T,H,pad", [(700, 259, 0), (1300, 1031, 0), (610, 2881, 7), (900, 4099, 3), (650, 8195, 1), (640, 264, 3)])
+@pytest.mark.parametrize("dtype,wdtype", [(BF16, F32), (F16, F16), (F32, F32)])
+def test_layer_norm_many_rows_at_any_alignment(T, H, pad, dtype, wdtype):
+    test_layer_norm(T, H, dtype, wdtype, pad)
+
+
+def test_layer_norm_rows_that_start_and_end_off_a_boundary():
+    """A tensor that begins and ends inside 16-byte units: its neighbours in memory are NaN and stay unread."""
+    cuda_device()
+    g = _gen(21)
+    for H, lead in ((301, 1), (1031, 3), (520, 5)):
+        T = 700
+        buf = torch.full((T * H + 16,), NAN, dtype=BF16, device="cuda")
+        x = buf[lead:lead + T * H].view(T, H)
+        x.copy_(_randn(g, T, H))
+        y, mean, rstd = torch.empty(T, H, dtype=BF16, device="cuda"), torch.empty(T, device="cuda"), torch.empty(T, device="cuda")
+        m.moe_layer_norm_forward(x, None, None, 1e-5, y, mean, rstd)
+        z, mean2, rstd2 = torch.empty_like(y), torch.empty_like(mean), torch.empty_like(rstd)
+        m.moe_layer_norm_forward(x.clone(), None, None, 1e-5, z, mean2, rstd2)
+        assert torch.equal(y, z) and torch.equal(mean, mean2) and torch.equal(rstd, rstd2)
+
+
 def test_layer_norm_without_weights_and_repeatable():
     cuda_device()
     g = _gen(5)
