@@ -21,6 +21,7 @@
 namespace moe {
 
 constexpr int kNormMaxThreads = 1024;
+constexpr int kWarpRowThreads = 256;    // a CTA of warps that hold a row each
 constexpr int kNormBwdThreads = 512;    // the backward holds four fp32 or packed values a column
 
 // Sums of a and b over the threads of a row (BLOCK: the nw warps of the CTA,
@@ -153,7 +154,7 @@ __device__ __forceinline__ void row_weights(float (&o)[V], const void* w, int c,
 
 // Rows per CTA: 1 with BLOCK, else one per warp.
 template <typename E, bool WF32, int NV, bool BLOCK, bool VEC>
-__global__ void __launch_bounds__(BLOCK ? kNormMaxThreads : 128) k_norm_fwd(NormArgs a) {
+__global__ void __launch_bounds__(BLOCK ? kNormMaxThreads : kWarpRowThreads) k_norm_fwd(NormArgs a) {
   using raw = typename E::raw;
   constexpr int V = 16 / (int)sizeof(raw);
   pdl_enter();
@@ -242,10 +243,11 @@ __global__ void __launch_bounds__(kNormMaxThreads) k_norm_fwd_long(NormArgs a) {
   }
 }
 
-// PART: the weight's gradient is wanted. Partial row p = the CTA (BLOCK) or
-// the warp: part[p][0][c] = dgamma, part[p][1][c] = dbeta over its rows.
+// PART: the weight's gradient is wanted. Partial row p = the CTA:
+// part[p][0][c] = dgamma, part[p][1][c] = dbeta over its rows (of its warps,
+// where they hold a row each, added in warp order).
 template <typename E, bool WF32, int NV, bool BLOCK, bool PART, bool VEC>
-__global__ void __launch_bounds__(BLOCK ? kNormBwdThreads : 128) k_norm_bwd(NormArgs a) {
+__global__ void __launch_bounds__(BLOCK ? kNormBwdThreads : kWarpRowThreads) k_norm_bwd(NormArgs a) {
   using raw = typename E::raw;
   constexpr int V = 16 / (int)sizeof(raw);
   pdl_enter();
@@ -312,18 +314,35 @@ __global__ void __launch_bounds__(BLOCK ? kNormBwdThreads : 128) k_norm_bwd(Norm
     }
   }
   if constexpr (PART) {
-    if (slot >= a.T) return;      // a warp without rows owns no partial row
-    float* pg = a.part + slot * 2 * a.H;
+    float* pg = a.part + (int64_t)blockIdx.x * 2 * a.H;
+    if constexpr (BLOCK) {
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int c = (i * tpr + t) * V;
-      if (c < a.H) {
+      for (int i = 0; i < NV; ++i) {
+        const int c = (i * tpr + t) * V;
+        if (c < a.H) {
 #pragma unroll
-        for (int j = 0; j < V; ++j) {
-          if (!VEC && c + j >= a.H) continue;
-          pg[c + j] = dg[i * V + j];
-          pg[a.H + c + j] = db[i * V + j];
+          for (int j = 0; j < V; ++j) {
+            if (!VEC && c + j >= a.H) continue;
+            pg[c + j] = dg[i * V + j];
+            pg[a.H + c + j] = db[i * V + j];
+          }
         }
+      }
+    } else {
+      __shared__ float sums[kWarpRowThreads / 32][2][32 * V];
+      const int w = threadIdx.x >> 5;
+#pragma unroll
+      for (int j = 0; j < V; ++j) {
+        sums[w][0][t * V + j] = dg[j];
+        sums[w][1][t * V + j] = db[j];
+      }
+      __syncthreads();
+      for (int c = threadIdx.x; c < 2 * a.H; c += kWarpRowThreads) {
+        const int k = c >= a.H;
+        float v = 0.f;
+#pragma unroll
+        for (int i = 0; i < kWarpRowThreads / 32; ++i) v += sums[i][k][c - k * a.H];
+        pg[c] = v;
       }
     }
   }
@@ -776,7 +795,7 @@ static NormPlan norm_plan(int64_t n, int64_t T, int resident, int max_parts, int
   NormPlan p = {};
   if (n <= 32) {                       // a warp a row
     p.nv = 1;
-    p.threads = 128;
+    p.threads = kWarpRowThreads;
   } else {
     p.block = true;
     // fewest packs a thread (one, two, four) that leave at most 256 threads a
@@ -790,7 +809,7 @@ static NormPlan norm_plan(int64_t n, int64_t T, int resident, int max_parts, int
   const int rpb = p.block ? 1 : p.threads / 32;
   int64_t g = p.block && !resident ? INT32_MAX
                                    : (int64_t)device_sms() * std::max(1, (resident ? resident : 2048) / p.threads);
-  if (max_parts) g = std::min<int64_t>(g, max_parts / rpb);
+  if (max_parts) g = std::min<int64_t>(g, max_parts);
   p.grid = std::max<int64_t>(1, std::min<int64_t>(g, (T + rpb - 1) / rpb));
   return p;
 }
@@ -866,9 +885,9 @@ template <typename E, bool WF32, bool VEC>
 static cudaError_t bwd_v(const NormArgs& a, cudaStream_t st) {
   constexpr int V = 16 / (int)sizeof(typename E::raw);
   const bool want = a.dgamma || a.dbeta;
-  const NormPlan p = norm_plan(((int64_t)a.H + V - 1) / V, a.T, 512, want ? kNormMaxParts : 0, kNormBwdThreads);
+  const NormPlan p = norm_plan(((int64_t)a.H + V - 1) / V, a.T, (int64_t)a.H <= 32 * V ? 2048 : 512, want ? kNormMaxParts : 0, kNormBwdThreads);
   cudaError_t e = cudaErrorNotSupported;
-  int64_t parts = std::min<int64_t>(a.T, p.grid * (p.block ? 1 : p.threads / 32));
+  int64_t parts = p.grid;
   e = want ? ring_launch<E, WF32, true, true, !VEC>(a, &parts, st) : ring_launch<E, WF32, false, true, !VEC>(a, &parts, st);
   if (e != cudaErrorNotSupported) {
   } else if (p.longrow) {
