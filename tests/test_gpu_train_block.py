@@ -1,0 +1,55 @@
+"""The training example's block: its gradients against autograd in 64 bits on
+the same routing, and a falling loss."""
+import importlib.util
+import os
+
+import pytest
+import torch
+
+from util import cuda_device, rel_l2
+
+pytestmark = pytest.mark.gpu
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+
+
+def _example():
+    spec = importlib.util.spec_from_file_location("train_block", os.path.join(ROOT, "examples", "train_block.py"))
+    mod = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(mod)
+    return mod
+
+
+def test_block_gradients():
+    """Two 8-bit roundings (relative 2^-4 each at most) stand between the block and the 64-bit one."""
+    cuda_device()
+    ex = _example()
+    T, H, I, E, k = 300, 256, 192, 8, 3
+    b = ex.Block(T, H, I, E, k, seed=3)
+    g = torch.Generator(device="cuda").manual_seed(9)
+    x = torch.randn(T, H, generator=g, device="cuda").bfloat16()
+    dout = torch.randn(T, H, generator=g, device="cuda").bfloat16()
+    out = b.forward(x)
+    v = b.saved[4]
+    ids, tw = v["topk_ids"].long().clone(), v["topk_w"].double().clone()
+    grads = b.backward(dout)
+
+    p = {n: getattr(b, n).double().requires_grad_() for n in ("gamma", "beta", "w1", "w2", "wp")}
+    x64 = x.double().requires_grad_()
+    mu = x64.mean(1, keepdim=True)
+    xn = (x64 - mu) / torch.sqrt((x64 - mu).pow(2).mean(1, keepdim=True) + ex.EPS) * p["gamma"] + p["beta"]
+    ref = xn @ p["wp"][0].t()
+    for j in range(k):
+        h = torch.einsum("th,tnh->tn", xn, p["w1"][ids[:, j]])
+        a = torch.nn.functional.silu(h[:, :I]) * h[:, I:]
+        ref = ref + tw[:, j:j + 1] * torch.einsum("ti,thi->th", a, p["w2"][ids[:, j]])
+    (ref * dout.double()).sum().backward()
+    assert rel_l2(out.double().cpu().numpy(), ref.detach().cpu().numpy()) < 2 * 2.0 ** -4
+    for n, want in (("x", x64.grad), *((n, t.grad) for n, t in p.items())):
+        assert rel_l2(grads[n].double().cpu().numpy(), want.cpu().numpy()) < 2 * 2.0 ** -4, n
+
+
+def test_training_lowers_the_loss():
+    cuda_device()
+    losses = _example().train(steps=12, tokens=512, hidden=256, inner=128, experts=8, k=2)
+    assert losses[-1] < 0.8 * losses[0] and all(l == l for l in losses), losses
