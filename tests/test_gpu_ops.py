@@ -520,6 +520,28 @@ def test_fp8_mm_dense(R, N, K, out):
     assert m.moe_mm_read_status(ws) == 0
 
 
+# enough rows and columns that pairs of SMs share the tiles: the last rows of a group in either CTA's half of a tile,
+# columns that end in either's, an empty group
+@pytest.mark.parametrize("sizes", [(2500,), (1290, 0, 2310), (4097,), (1025, 3001)], ids=lambda s: "-".join(map(str, s)))
+@pytest.mark.parametrize("N,K", [(2100, 700), (2432, 384), (4160, 1000)])
+@pytest.mark.parametrize("out", [F32, BF16])
+def test_fp8_mm_many_rows(sizes, N, K, out):
+    cuda_device()
+    off, offsets = _offsets(sizes)
+    R, G = off[-1] + 3, len(sizes)
+    xq, xs, wq, wsc, x64, w64 = _fp8(_gen(R + N), R, N, K, G)
+    xq[off[-1]:].view(torch.uint8).fill_(0x7F)
+    xs[off[-1]:] = NAN
+    y, buf = P.strided(torch.full((R, N), NAN, dtype=out, device="cuda"), 8)
+    ws = _workspace(m.MOE_MM_FP8, R, N, K, G)
+    m.moe_fp8_mm(xq, xs, wq, wsc, y, ws, offsets=offsets)
+    ref, mag = P.grouped(x64, w64, off)
+    P.assert_within(y, ref, (K + 8) * P.EPS32 * mag, "out")
+    assert bool((y[off[-1]:] == 0).all())
+    _canary(buf, N, "out")
+    assert m.moe_mm_read_status(ws) == 0
+
+
 def test_fp8_mm_blocks_of_zeros_and_wide_scales():
     """Blocks of zeros next to blocks near fp32's ends: the scales multiply outside the sum over a block."""
     cuda_device()
