@@ -46,6 +46,33 @@ __device__ __forceinline__ void store16(uint16_t* p, const uint32_t (&w)[8], int
     }
   }
 }
+// A block at any alignment by way of shared memory: each lane's columns go to
+// `buf` (the quarter-warp's own, kStageBytes) at the block's place in its
+// 16-byte units, and after a __syncwarp the lanes store whole units from there.
+// Their own columns would leave in words and halves of a 32-byte sector each.
+constexpr int kStageBytes = 256 + 16;
+__device__ __forceinline__ void stage16(uint8_t* buf, const uint16_t* p, const uint32_t (&w)[8], int l) {
+  const int off = (int)((uintptr_t)p & 15);
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    const uint32_t v[4] = {w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]};
+    store_inner<2>(buf + off + 128 * k + 16 * l, v);
+  }
+}
+__device__ __forceinline__ void store_staged(uint16_t* p, const uint8_t* buf, int l, int n) {
+  const int off = (int)((uintptr_t)p & 15), end = off + 2 * n;
+  uint8_t* base = reinterpret_cast<uint8_t*>(p) - off;
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    const int at = 16 * (8 * k + l);
+    if (at >= off && at + 16 <= end) *reinterpret_cast<uint4*>(base + at) = *reinterpret_cast<const uint4*>(buf + at);
+  }
+  // what lies in the first and the last unit besides: an element a lane
+  const int e = 2 * l, first = min(16, end), last = end & ~15;
+  if (off && e >= off && e < first) *reinterpret_cast<uint16_t*>(base + e) = *reinterpret_cast<const uint16_t*>(buf + e);
+  if ((!off || last) && last + e < end)
+    *reinterpret_cast<uint16_t*>(base + last + e) = *reinterpret_cast<const uint16_t*>(buf + last + e);
+}
 template <bool VEC>
 __device__ __forceinline__ void load_codes(uint32_t (&w)[4], const uint8_t* q, int l, int n, const uint8_t* half, int I) {
 #pragma unroll

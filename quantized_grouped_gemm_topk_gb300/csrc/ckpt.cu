@@ -185,6 +185,9 @@ __global__ void __launch_bounds__(kCkptThreads) k_ckpt_bwd(CkptArgs a, int qpr) 
   const int rpg = (WARP ? 4 : kCkptQuarters) / qpr, rl = qw / qpr, part = qw % qpr;   // rows a warp (CTA) takes
   const int64_t group = WARP ? (int64_t)blockIdx.x * (kCkptThreads / 32) + (threadIdx.x >> 5) : blockIdx.x;
   const int64_t groups = WARP ? (int64_t)gridDim.x * (kCkptThreads / 32) : gridDim.x;
+  __shared__ __align__(16) uint8_t staged[VEC ? 1 : kCkptQuarters][VEC ? 16 : 3 * kStageBytes];
+  uint8_t* buf = staged[VEC ? 0 : threadIdx.x >> 3];
+  const unsigned lanes = 0xffu << (threadIdx.x & 24);
   int flip = 0;
   for (int64_t r0 = group * rpg; r0 < a.R; r0 += groups * rpg, flip ^= 1) {
     const int64_t row = r0 + rl;
@@ -211,9 +214,20 @@ __global__ void __launch_bounds__(kCkptThreads) k_ckpt_bwd(CkptArgs a, int qpr) 
         const bool fin = !nan && fabsf(sg) < 1e35f && fabsf(su) < 1e35f;
         dw += fin ? bwd16<E, ACT, true>(dg, du, yw, qg, qu, d, sg, su, w, a.act)
                   : bwd16<E, ACT, false>(dg, du, yw, qg, qu, d, sg, su, w, a.act);
-        store16<VEC>(dh + c0, dg, l, n);
-        if constexpr (GATED) store16<VEC>(dh + a.I + c0, du, l, n);
-        if (a.y) store16<VEC>(y + c0, yw, l, n);
+        if constexpr (VEC) {
+          store16<VEC>(dh + c0, dg, l, n);
+          if constexpr (GATED) store16<VEC>(dh + a.I + c0, du, l, n);
+          if (a.y) store16<VEC>(y + c0, yw, l, n);
+        } else {
+          __syncwarp(lanes);          // the last block's units have been read
+          stage16(buf, dh + c0, dg, l);
+          if constexpr (GATED) stage16(buf + kStageBytes, dh + a.I + c0, du, l);
+          if (a.y) stage16(buf + 2 * kStageBytes, y + c0, yw, l);
+          __syncwarp(lanes);
+          store_staged(dh + c0, buf, l, n);
+          if constexpr (GATED) store_staged(dh + a.I + c0, buf + kStageBytes, l, n);
+          if (a.y) store_staged(y + c0, buf + 2 * kStageBytes, l, n);
+        }
       }
     }
     if (a.dw) {
