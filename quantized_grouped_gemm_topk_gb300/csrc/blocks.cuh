@@ -73,22 +73,13 @@ __device__ __forceinline__ void store_staged(uint16_t* p, const uint8_t* buf, in
   if ((!off || last) && last + e < end)
     *reinterpret_cast<uint16_t*>(base + last + e) = *reinterpret_cast<const uint16_t*>(buf + last + e);
 }
-template <bool VEC>
-__device__ __forceinline__ void load_codes(uint32_t (&w)[4], const uint8_t* q, int l, int n, const uint8_t* half, int I) {
+__device__ __forceinline__ void load_codes(uint32_t (&w)[4], const uint8_t* q, int l, int n) {
 #pragma unroll
   for (int k = 0; k < 2; ++k) {
     const int c = 64 * k + 8 * l;
-    uint32_t v[2] = {0u, 0u};
-    if constexpr (VEC) {
-      if (c < n) {
-        const uint2 u = *reinterpret_cast<const uint2*>(q + c);
-        v[0] = u.x; v[1] = u.y;
-      }
-    } else {
-      load_any<1, 8>(v, q + c, half, half + I);
-    }
-    w[2 * k] = v[0];
-    w[2 * k + 1] = v[1];
+    const uint2 v = c < n ? *reinterpret_cast<const uint2*>(q + c) : make_uint2(0u, 0u);
+    w[2 * k] = v.x;
+    w[2 * k + 1] = v.y;
   }
 }
 template <bool VEC>
@@ -101,6 +92,55 @@ __device__ __forceinline__ void store_codes(uint8_t* q, const uint32_t (&w)[4], 
       if constexpr (VEC) *reinterpret_cast<uint2*>(q + c) = v;
       else store_bytes8(q + c, v, n - c);
     }
+  }
+}
+
+// Columns [c, c + 128) of a row of `n` elements of ES bytes, at any alignment,
+// on their way to shared memory (asynchronous copies, to be committed and
+// waited for): the 16-byte units that hold them, U = 8 ES + 1 of them at `buf`.
+// Bytes past the block or the row become zeros and are not read; a first unit that
+// begins before `base`, the tensor's first byte, is read byte by byte.
+template <int ES>
+__device__ __forceinline__ void fetch_block(uint8_t* buf, const uint8_t* row, int c, int n, const uint8_t* base, int l) {
+  const uint8_t* p = row + (int64_t)c * ES;
+  const int off = (int)((uintptr_t)p & 15);
+  const uint8_t* at = p - off + 16 * l;
+  const int left = min(n - c, kQBlock) * ES + off - 16 * l;     // bytes of the block from `at`
+  auto unit = [&](int u) {
+    const int bytes = min(16, max(0, left - 16 * u));
+    cp_async16(buf + 16 * (l + u), bytes ? at + 16 * u : base - ((uintptr_t)base & 15), bytes);
+  };
+  if (at >= base) {
+    unit(0);
+  } else {
+#pragma unroll 1
+    for (int i = 0; i < 16; ++i) buf[16 * l + i] = at + i >= base && i < left ? at[i] : 0;
+  }
+  if (ES == 2) unit(8);
+  if (l == 0) unit(8 * ES);
+}
+// The lane's sixteen elements of a block in shared memory; off: the place of
+// its first byte in the first unit.
+__device__ __forceinline__ void read16(uint32_t (&w)[8], const uint8_t* buf, int off, int l) {
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    const uint4 a = *reinterpret_cast<const uint4*>(buf + 128 * k + 16 * l);
+    const uint4 b = *reinterpret_cast<const uint4*>(buf + 128 * k + 16 * l + 16);
+    uint32_t u[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w}, r[4];
+    shift_units<2, 16>(r, u, off);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[4 * k + i] = r[i];
+  }
+}
+__device__ __forceinline__ void read_codes(uint32_t (&w)[4], const uint8_t* buf, int off, int l) {
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    const uint8_t* p = buf + (off & 8) + 64 * k + 8 * l;
+    const uint2 a = *reinterpret_cast<const uint2*>(p), b = *reinterpret_cast<const uint2*>(p + 8);
+    uint32_t u[4] = {a.x, a.y, b.x, b.y}, r[2];
+    shift_units<1, 8>(r, u, off & 7);
+    w[2 * k] = r[0];
+    w[2 * k + 1] = r[1];
   }
 }
 

@@ -172,10 +172,45 @@ __device__ __forceinline__ float bwd16(uint32_t (&dg)[8], uint32_t (&du)[8], uin
   return dw;
 }
 
+// The row's dw from its quarter-warps' parts, in a fixed order. WARP: the row's
+// quarters are of one warp; otherwise of the CTA (sdw: two rounds' parts).
+template <bool WARP>
+__device__ __forceinline__ void join_dw(float* out, float dw, bool live, int part, int qpr, float* sdw, int qw, int l) {
+  __syncwarp();
+#pragma unroll
+  for (int o = 4; o > 0; o >>= 1) dw += __shfl_xor_sync(kFull, dw, o);
+  if constexpr (WARP) {
+    if (qpr > 1) dw += __shfl_xor_sync(kFull, dw, 8);
+    if (qpr > 2) dw += __shfl_xor_sync(kFull, dw, 16);
+    if (live && part == 0 && l == 0) *out = dw;
+  } else {
+    if (l == 0) sdw[qw] = dw;
+    __syncthreads();
+    if (live && part == 0 && l == 0) {
+      float t = 0.f;
+      for (int i = 0; i < qpr; ++i) t += sdw[qw + i];
+      *out = t;
+    }
+  }
+}
+
+template <typename E, int ACT>
+__device__ __forceinline__ float bwd_block(uint32_t (&dg)[8], uint32_t (&du)[8], uint32_t (&y)[8], const uint32_t (&qg)[4],
+                                           const uint32_t (&qu)[4], const uint32_t (&d)[8], float sg, float su, float w,
+                                           const ActParams& p) {
+  bool nan = false;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) nan |= nan_code(qg[j]) | nan_code(qu[j]);
+  // 448 s overflows for the largest scales; a caller's scale may be anything
+  const bool fin = !nan && fabsf(sg) < 1e35f && fabsf(su) < 1e35f;
+  return fin ? bwd16<E, ACT, true>(dg, du, y, qg, qu, d, sg, su, w, p)
+             : bwd16<E, ACT, false>(dg, du, y, qg, qu, d, sg, su, w, p);
+}
+
 // qpr quarter-warps share a row. WARP: at most four, of one warp: the row's dw
 // needs shuffles only, and warps go on at their own pace. Otherwise all of a
 // CTA's may share one (few rows), and dw crosses shared memory.
-template <typename E, bool VEC, int ACT, bool WARP>
+template <typename E, int ACT, bool WARP>
 __global__ void __launch_bounds__(kCkptThreads) k_ckpt_bwd(CkptArgs a, int qpr) {
   constexpr bool GATED = ACT != MOE_ACT_SRELU;
   pdl_enter();
@@ -185,9 +220,6 @@ __global__ void __launch_bounds__(kCkptThreads) k_ckpt_bwd(CkptArgs a, int qpr) 
   const int rpg = (WARP ? 4 : kCkptQuarters) / qpr, rl = qw / qpr, part = qw % qpr;   // rows a warp (CTA) takes
   const int64_t group = WARP ? (int64_t)blockIdx.x * (kCkptThreads / 32) + (threadIdx.x >> 5) : blockIdx.x;
   const int64_t groups = WARP ? (int64_t)gridDim.x * (kCkptThreads / 32) : gridDim.x;
-  __shared__ __align__(16) uint8_t staged[VEC ? 1 : kCkptQuarters][VEC ? 16 : 3 * kStageBytes];
-  uint8_t* buf = staged[VEC ? 0 : threadIdx.x >> 3];
-  const unsigned lanes = 0xffu << (threadIdx.x & 24);
   int flip = 0;
   for (int64_t r0 = group * rpg; r0 < a.R; r0 += groups * rpg, flip ^= 1) {
     const int64_t row = r0 + rl;
@@ -203,52 +235,92 @@ __global__ void __launch_bounds__(kCkptThreads) k_ckpt_bwd(CkptArgs a, int qpr) 
       for (int b = part; b < nb; b += qpr) {
         const int c0 = b * kQBlock, n = min(kQBlock, a.I - c0);
         uint32_t qg[4], qu[4] = {0u, 0u, 0u, 0u}, d[8], dg[8], du[8], yw[8];
-        load_codes<VEC>(qg, q + c0, l, n, q, a.I);
-        if constexpr (GATED) load_codes<VEC>(qu, q + a.I + c0, l, n, q + a.I, a.I);
-        load16<VEC>(d, dy + c0, l, n, dy, a.I);
-        const float sg = s[b], su = GATED ? s[nb + b] : 0.f;
-        bool nan = false;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) nan |= nan_code(qg[j]) | nan_code(qu[j]);
-        // 448 s overflows for the largest scales; a caller's scale may be anything
-        const bool fin = !nan && fabsf(sg) < 1e35f && fabsf(su) < 1e35f;
-        dw += fin ? bwd16<E, ACT, true>(dg, du, yw, qg, qu, d, sg, su, w, a.act)
-                  : bwd16<E, ACT, false>(dg, du, yw, qg, qu, d, sg, su, w, a.act);
-        if constexpr (VEC) {
-          store16<VEC>(dh + c0, dg, l, n);
-          if constexpr (GATED) store16<VEC>(dh + a.I + c0, du, l, n);
-          if (a.y) store16<VEC>(y + c0, yw, l, n);
-        } else {
-          __syncwarp(lanes);          // the last block's units have been read
-          stage16(buf, dh + c0, dg, l);
-          if constexpr (GATED) stage16(buf + kStageBytes, dh + a.I + c0, du, l);
-          if (a.y) stage16(buf + 2 * kStageBytes, y + c0, yw, l);
-          __syncwarp(lanes);
-          store_staged(dh + c0, buf, l, n);
-          if constexpr (GATED) store_staged(dh + a.I + c0, buf + kStageBytes, l, n);
-          if (a.y) store_staged(y + c0, buf + 2 * kStageBytes, l, n);
-        }
+        load_codes(qg, q + c0, l, n);
+        if constexpr (GATED) load_codes(qu, q + a.I + c0, l, n);
+        load16<true>(d, dy + c0, l, n, dy, a.I);
+        dw += bwd_block<E, ACT>(dg, du, yw, qg, qu, d, s[b], GATED ? s[nb + b] : 0.f, w, a.act);
+        store16<true>(dh + c0, dg, l, n);
+        if constexpr (GATED) store16<true>(dh + a.I + c0, du, l, n);
+        if (a.y) store16<true>(y + c0, yw, l, n);
       }
     }
-    if (a.dw) {
-      __syncwarp();
-#pragma unroll
-      for (int o = 4; o > 0; o >>= 1) dw += __shfl_xor_sync(kFull, dw, o);
-      if constexpr (WARP) {
-        if (qpr > 1) dw += __shfl_xor_sync(kFull, dw, 8);
-        if (qpr > 2) dw += __shfl_xor_sync(kFull, dw, 16);
-        if (live && part == 0 && l == 0) a.dw[row] = dw;
-      } else {
-        if (l == 0) sdw[flip][qw] = dw;
-        __syncthreads();
-        if (live && part == 0 && l == 0) {
-          float t = 0.f;
-          for (int i = 0; i < qpr; ++i) t += sdw[flip][qw + i];
-          a.dw[row] = t;
-        }
-      }
-    }
+    if (a.dw) join_dw<WARP>(a.dw + row, dw, live, part, qpr, sdw[flip], qw, l);
   }
+}
+
+// The same for rows at any alignment. A quarter-warp fetches its next block's
+// units into shared memory while it works on one (loads of its own columns
+// waited for half the time, at 8 of 13 cycles an instruction), and its outputs
+// leave through shared memory too (store_staged).
+template <typename E, int ACT, bool WARP>
+__global__ void __launch_bounds__(kCkptThreads) k_ckpt_bwd_any(CkptArgs a, int qpr) {
+  constexpr bool GATED = ACT != MOE_ACT_SRELU;
+  constexpr int kCodes = 128 + 16, kIn = kStageBytes + (GATED ? 2 : 1) * kCodes;
+  __shared__ __align__(16) uint8_t in_smem[kCkptQuarters][2][kIn];
+  __shared__ __align__(16) uint8_t out_smem[kCkptQuarters][kStageBytes];
+  __shared__ float sdw[2][WARP ? 1 : kCkptQuarters];
+  pdl_enter();
+  const int l = threadIdx.x & 7, qc = threadIdx.x >> 3, qw = WARP ? qc & 3 : qc;
+  const unsigned lanes = 0xffu << (threadIdx.x & 24);
+  const int nb = (a.I + kQBlock - 1) / kQBlock;
+  const int rpg = (WARP ? 4 : kCkptQuarters) / qpr, rl = qw / qpr, part = qw % qpr;   // rows a warp (CTA) takes
+  const int64_t group = WARP ? (int64_t)blockIdx.x * (kCkptThreads / 32) + (threadIdx.x >> 5) : blockIdx.x;
+  const int64_t step = (WARP ? (int64_t)gridDim.x * (kCkptThreads / 32) : gridDim.x) * rpg;
+  const uint8_t* dy0 = reinterpret_cast<const uint8_t*>(a.dy);
+  uint8_t* out = out_smem[qc];
+  float sg_next = 0.f, su_next = 0.f;
+  auto fetch = [&](int64_t row, int b, int stage) {
+    if (row < a.R && b < nb) {
+      uint8_t* in = in_smem[qc][stage];
+      const uint8_t* q = a.q + row * a.ldq;
+      const float* s = a.s + row * nb * (GATED ? 2 : 1);
+      fetch_block<2>(in, dy0 + row * a.lddy * 2, b * kQBlock, a.I, dy0, l);
+      fetch_block<1>(in + kStageBytes, q, b * kQBlock, a.I, a.q, l);
+      if constexpr (GATED) fetch_block<1>(in + kStageBytes + kCodes, q + a.I, b * kQBlock, a.I, a.q, l);
+      sg_next = s[b];
+      if constexpr (GATED) su_next = s[nb + b];
+    }
+    cp_async_commit();
+  };
+  int flip = 0, stage = 0;
+  fetch(group * rpg + rl, part, 0);
+  for (int64_t r0 = group * rpg; r0 < a.R; r0 += step, flip ^= 1) {
+    const int64_t row = r0 + rl;
+    const bool live = row < a.R;
+    const float w = live && a.w ? a.w[row] : 1.f;
+    float dw = 0.f;
+    if (live) {
+      const uint8_t* q = a.q + row * a.ldq;
+      const uint16_t* dy = reinterpret_cast<const uint16_t*>(a.dy) + row * a.lddy;
+      uint16_t* dh = reinterpret_cast<uint16_t*>(a.dh) + row * a.lddh;
+      uint16_t* y = reinterpret_cast<uint16_t*>(a.y) + row * a.ldy;
+      for (int b = part; b < nb; b += qpr, stage ^= 1) {
+        const int c0 = b * kQBlock, n = min(kQBlock, a.I - c0);
+        const float sg = sg_next, su = su_next;
+        const bool more = b + qpr < nb;
+        fetch(more ? row : row + step, more ? b + qpr : part, stage ^ 1);
+        cp_async_wait<1>();
+        __syncwarp(lanes);
+        uint32_t qg[4], qu[4] = {0u, 0u, 0u, 0u}, d[8], dg[8], du[8], yw[8];
+        const uint8_t* in = in_smem[qc][stage];
+        read16(d, in, (int)((uintptr_t)(dy + c0) & 15), l);
+        read_codes(qg, in + kStageBytes, (int)((uintptr_t)(q + c0) & 15), l);
+        if constexpr (GATED) read_codes(qu, in + kStageBytes + kCodes, (int)((uintptr_t)(q + a.I + c0) & 15), l);
+        dw += bwd_block<E, ACT>(dg, du, yw, qg, qu, d, sg, su, w, a.act);
+        auto put = [&](uint16_t* p, const uint32_t(&v)[8]) {
+          stage16(out, p, v, l);
+          __syncwarp(lanes);
+          store_staged(p, out, l, n);
+          __syncwarp(lanes);
+        };
+        put(dh + c0, dg);
+        if constexpr (GATED) put(dh + a.I + c0, du);
+        if (a.y) put(y + c0, yw);
+      }
+    }
+    if (a.dw) join_dw<WARP>(a.dw + row, dw, live, part, qpr, sdw[flip], qw, l);
+  }
+  cp_async_wait<0>();
 }
 
 // ---- host ----------------------------------------------------------------------
@@ -270,8 +342,8 @@ static cudaError_t bwd_w(const CkptArgs& a, bool vec, int qpr, cudaStream_t st) 
   const int64_t rows = WARP ? kCkptThreads / 32 * (4 / qpr) : kCkptQuarters / qpr;     // a CTA's
   const int64_t g = std::min<int64_t>((a.R + rows - 1) / rows, (int64_t)device_sms() * 32);
   note_launch();
-  if (vec) return launch_pdl(k_ckpt_bwd<E, true, ACT, WARP>, dim3((unsigned)g), dim3(kCkptThreads), 0, st, a, qpr);
-  return launch_pdl(k_ckpt_bwd<E, false, ACT, WARP>, dim3((unsigned)g), dim3(kCkptThreads), 0, st, a, qpr);
+  if (vec) return launch_pdl(k_ckpt_bwd<E, ACT, WARP>, dim3((unsigned)g), dim3(kCkptThreads), 0, st, a, qpr);
+  return launch_pdl(k_ckpt_bwd_any<E, ACT, WARP>, dim3((unsigned)g), dim3(kCkptThreads), 0, st, a, qpr);
 }
 template <typename E, int ACT>
 static cudaError_t bwd_t(const CkptArgs& a, cudaStream_t st) {
