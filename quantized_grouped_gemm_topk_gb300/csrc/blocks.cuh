@@ -34,16 +34,11 @@ template <typename E>
 __device__ __forceinline__ float2 pair_of(uint32_t w) {
   return make_float2(E::to((uint16_t)(w & 0xffffu)), E::to((uint16_t)(w >> 16)));
 }
-template <bool VEC>
 __device__ __forceinline__ void store16(uint16_t* p, const uint32_t (&w)[8], int l, int n) {
 #pragma unroll
   for (int k = 0; k < 2; ++k) {
     const int c = 64 * k + 8 * l;
-    const uint32_t v[4] = {w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]};
-    if (c < n) {
-      if constexpr (VEC) *reinterpret_cast<uint4*>(p + c) = make_uint4(v[0], v[1], v[2], v[3]);
-      else store_any<2>(p + c, v, n - c);
-    }
+    if (c < n) *reinterpret_cast<uint4*>(p + c) = make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
   }
 }
 // A block at any alignment by way of shared memory: each lane's columns go to
@@ -92,6 +87,31 @@ __device__ __forceinline__ void store_codes(uint8_t* q, const uint32_t (&w)[4], 
       if constexpr (VEC) *reinterpret_cast<uint2*>(q + c) = v;
       else store_bytes8(q + c, v, n - c);
     }
+  }
+}
+
+// The codes of a block at any address by way of shared memory: eight at a time
+// to their columns' place in `buf` (kCodeBytes), after a __syncwarp whole units
+// of the row from there, what is left at the block's ends byte by byte.
+constexpr int kCodeBytes = 128 + 16;
+__device__ __forceinline__ void stage_codes(uint8_t* buf, const uint32_t (&w)[4], int l) {
+#pragma unroll
+  for (int k = 0; k < 2; ++k) *reinterpret_cast<uint2*>(buf + 64 * k + 8 * l) = make_uint2(w[2 * k], w[2 * k + 1]);
+}
+__device__ __forceinline__ void store_staged_codes(uint8_t* q, const uint8_t* buf, int l, int n) {
+  const int off = (int)((uintptr_t)q & 15), at = 16 * l - off;
+  if (at >= 0 && at + 16 <= n) {
+    const uint8_t* p = buf + (at & ~15);
+    const uint4 a = *reinterpret_cast<const uint4*>(p), b = *reinterpret_cast<const uint4*>(p + 16);
+    uint32_t u[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w}, r[4];
+    shift_units<1, 16>(r, u, at & 15);
+    *reinterpret_cast<uint4*>(q + at) = make_uint4(r[0], r[1], r[2], r[3]);
+  }
+  const int last = ((off + n) & ~15) - off;
+#pragma unroll
+  for (int e = l; e < 16; e += 8) {
+    if (off && e < min(n, 16 - off)) q[e] = buf[e];
+    if (last >= 0 && last + e < n) q[last + e] = buf[last + e];
   }
 }
 

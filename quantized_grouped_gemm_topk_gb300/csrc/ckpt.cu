@@ -97,9 +97,31 @@ __device__ __forceinline__ void fwd16(uint32_t (&y)[8], uint32_t (&cg)[4], uint3
   if constexpr (ACT != MOE_ACT_SRELU) codes16<E, FIN>(cu, uw, 1.0f / su);
 }
 
+// A block's scales and their codes, and y: the words of both halves to the
+// words of y and the codes.
+template <typename E, int ACT>
+__device__ __forceinline__ void fwd_block(uint32_t (&y)[8], uint32_t (&cg)[4], uint32_t (&cu)[4], float& sg, float& su,
+                                          const uint32_t (&gw)[8], const uint32_t (&uw)[8], float w, const ActParams& p,
+                                          unsigned lanes) {
+  constexpr bool GATED = ACT != MOE_ACT_SRELU;
+  // both halves' largest magnitudes in one word: three shuffles
+  uint32_t mm = mag_bits(gw) | (GATED ? mag_bits(uw) << 16 : 0u);
+#pragma unroll
+  for (int o = 4; o > 0; o >>= 1) mm = __vmaxu2(mm, __shfl_xor_sync(lanes, mm, o));
+  if ((mm & 0xffffu) < E::kInf && (mm >> 16) < E::kInf) {
+    sg = block_scale(E::to((uint16_t)(mm & 0xffffu)));
+    su = block_scale(E::to((uint16_t)(mm >> 16)));
+    fwd16<E, ACT, true>(y, cg, cu, gw, uw, sg, su, w, p);
+  } else {
+    sg = finite_scale<E>(gw, lanes);
+    su = GATED ? finite_scale<E>(uw, lanes) : 1.f;
+    fwd16<E, ACT, false>(y, cg, cu, gw, uw, sg, su, w, p);
+  }
+}
+
 // qpr quarter-warps of a CTA (a power of two) share a row; the others take
 // other rows.
-template <typename E, bool VEC, int ACT>
+template <typename E, int ACT>
 __global__ void __launch_bounds__(kCkptThreads) k_ckpt_fwd(CkptArgs a, int qpr) {
   constexpr bool GATED = ACT != MOE_ACT_SRELU;
   pdl_enter();
@@ -115,33 +137,87 @@ __global__ void __launch_bounds__(kCkptThreads) k_ckpt_fwd(CkptArgs a, int qpr) 
     const float w = a.w ? a.w[row] : 1.f;
     for (int b = part; b < nb; b += qpr) {
       const int c0 = b * kQBlock, n = min(kQBlock, a.I - c0);
-      uint32_t gw[8], uw[8] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u};
-      load16<VEC>(gw, h + c0, l, n, h, a.I);
-      if constexpr (GATED) load16<VEC>(uw, h + a.I + c0, l, n, h + a.I, a.I);
-      // both halves' largest magnitudes in one word: three shuffles
-      uint32_t mm = mag_bits(gw) | (GATED ? mag_bits(uw) << 16 : 0u);
-#pragma unroll
-      for (int o = 4; o > 0; o >>= 1) mm = __vmaxu2(mm, __shfl_xor_sync(lanes, mm, o));
-      uint32_t yw[8], cg[4], cu[4];
+      uint32_t gw[8], uw[8] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u}, yw[8], cg[4], cu[4];
+      load16<true>(gw, h + c0, l, n, h, a.I);
+      if constexpr (GATED) load16<true>(uw, h + a.I + c0, l, n, h + a.I, a.I);
       float sg, su;
-      if ((mm & 0xffffu) < E::kInf && (mm >> 16) < E::kInf) {
-        sg = block_scale(E::to((uint16_t)(mm & 0xffffu)));
-        su = block_scale(E::to((uint16_t)(mm >> 16)));
-        fwd16<E, ACT, true>(yw, cg, cu, gw, uw, sg, su, w, a.act);
-      } else {
-        sg = finite_scale<E>(gw, lanes);
-        su = GATED ? finite_scale<E>(uw, lanes) : 1.f;
-        fwd16<E, ACT, false>(yw, cg, cu, gw, uw, sg, su, w, a.act);
-      }
-      store_codes<VEC>(q + c0, cg, l, n);
-      if constexpr (GATED) store_codes<VEC>(q + a.I + c0, cu, l, n);
+      fwd_block<E, ACT>(yw, cg, cu, sg, su, gw, uw, w, a.act, lanes);
+      store_codes<true>(q + c0, cg, l, n);
+      if constexpr (GATED) store_codes<true>(q + a.I + c0, cu, l, n);
       if (l == 0) {
         s[b] = sg;
         if constexpr (GATED) s[nb + b] = su;
       }
-      store16<VEC>(y + c0, yw, l, n);
+      store16(y + c0, yw, l, n);
     }
   }
+}
+
+// The same for rows at any alignment. A quarter-warp fetches its next block's
+// units into shared memory while it works on one, and its outputs leave
+// through shared memory, in whole units.
+template <typename E, int ACT>
+__global__ void __launch_bounds__(kCkptThreads) k_ckpt_fwd_any(CkptArgs a, int qpr) {
+  constexpr bool GATED = ACT != MOE_ACT_SRELU;
+  __shared__ __align__(16) uint8_t in_smem[kCkptQuarters][2][(GATED ? 2 : 1) * kStageBytes];
+  __shared__ __align__(16) uint8_t out_smem[kCkptQuarters][kStageBytes];
+  static_assert(kCodeBytes <= kStageBytes, "either fits");
+  pdl_enter();
+  const int l = threadIdx.x & 7, qw = threadIdx.x >> 3;
+  const unsigned lanes = 0xffu << (threadIdx.x & 24);
+  const int nb = (a.I + kQBlock - 1) / kQBlock;
+  const int rpc = kCkptQuarters / qpr, rl = qw / qpr, part = qw % qpr;
+  const int64_t step = (int64_t)gridDim.x * rpc;
+  const uint8_t* h0 = reinterpret_cast<const uint8_t*>(a.h);
+  uint8_t* out = out_smem[qw];
+  auto fetch = [&](int64_t row, int b, int stage) {
+    if (row < a.R && b < nb) {
+      const uint8_t* h = h0 + row * a.ldh * 2;
+      fetch_block<2>(in_smem[qw][stage], h, b * kQBlock, a.I, h0, l);
+      if constexpr (GATED) fetch_block<2>(in_smem[qw][stage] + kStageBytes, h + 2 * (int64_t)a.I, b * kQBlock, a.I, h0, l);
+    }
+    cp_async_commit();
+  };
+  int stage = 0;
+  int64_t row = (int64_t)blockIdx.x * rpc + rl;
+  fetch(row, part, 0);
+  for (; row < a.R; row += step) {
+    const uint16_t* h = reinterpret_cast<const uint16_t*>(a.h) + row * a.ldh;
+    uint16_t* y = reinterpret_cast<uint16_t*>(a.y) + row * a.ldy;
+    uint8_t* q = a.q + row * a.ldq;
+    float* s = a.s + row * nb * (GATED ? 2 : 1);
+    const float w = a.w ? a.w[row] : 1.f;
+    for (int b = part; b < nb; b += qpr, stage ^= 1) {
+      const int c0 = b * kQBlock, n = min(kQBlock, a.I - c0);
+      const bool more = b + qpr < nb;
+      fetch(more ? row : row + step, more ? b + qpr : part, stage ^ 1);
+      cp_async_wait<1>();
+      __syncwarp(lanes);
+      uint32_t gw[8], uw[8] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u}, yw[8], cg[4], cu[4];
+      const uint8_t* in = in_smem[qw][stage];
+      read16(gw, in, (int)((uintptr_t)(h + c0) & 15), l);
+      if constexpr (GATED) read16(uw, in + kStageBytes, (int)((uintptr_t)(h + a.I + c0) & 15), l);
+      float sg, su;
+      fwd_block<E, ACT>(yw, cg, cu, sg, su, gw, uw, w, a.act, lanes);
+      auto put_codes = [&](uint8_t* p, const uint32_t(&v)[4]) {
+        stage_codes(out, v, l);
+        __syncwarp(lanes);
+        store_staged_codes(p, out, l, n);
+        __syncwarp(lanes);
+      };
+      put_codes(q + c0, cg);
+      if constexpr (GATED) put_codes(q + a.I + c0, cu);
+      if (l == 0) {
+        s[b] = sg;
+        if constexpr (GATED) s[nb + b] = su;
+      }
+      stage16(out, y + c0, yw, l);
+      __syncwarp(lanes);
+      store_staged(y + c0, out, l, n);
+      __syncwarp(lanes);
+    }
+  }
+  cp_async_wait<0>();
 }
 
 __device__ __forceinline__ bool nan_code(uint32_t w) {      // a byte whose low seven bits are all set
@@ -239,9 +315,9 @@ __global__ void __launch_bounds__(kCkptThreads) k_ckpt_bwd(CkptArgs a, int qpr) 
         if constexpr (GATED) load_codes(qu, q + a.I + c0, l, n);
         load16<true>(d, dy + c0, l, n, dy, a.I);
         dw += bwd_block<E, ACT>(dg, du, yw, qg, qu, d, s[b], GATED ? s[nb + b] : 0.f, w, a.act);
-        store16<true>(dh + c0, dg, l, n);
-        if constexpr (GATED) store16<true>(dh + a.I + c0, du, l, n);
-        if (a.y) store16<true>(y + c0, yw, l, n);
+        store16(dh + c0, dg, l, n);
+        if constexpr (GATED) store16(dh + a.I + c0, du, l, n);
+        if (a.y) store16(y + c0, yw, l, n);
       }
     }
     if (a.dw) join_dw<WARP>(a.dw + row, dw, live, part, qpr, sdw[flip], qw, l);
@@ -255,7 +331,7 @@ __global__ void __launch_bounds__(kCkptThreads) k_ckpt_bwd(CkptArgs a, int qpr) 
 template <typename E, int ACT, bool WARP>
 __global__ void __launch_bounds__(kCkptThreads) k_ckpt_bwd_any(CkptArgs a, int qpr) {
   constexpr bool GATED = ACT != MOE_ACT_SRELU;
-  constexpr int kCodes = 128 + 16, kIn = kStageBytes + (GATED ? 2 : 1) * kCodes;
+  constexpr int kIn = kStageBytes + (GATED ? 2 : 1) * kCodeBytes;
   __shared__ __align__(16) uint8_t in_smem[kCkptQuarters][2][kIn];
   __shared__ __align__(16) uint8_t out_smem[kCkptQuarters][kStageBytes];
   __shared__ float sdw[2][WARP ? 1 : kCkptQuarters];
@@ -276,7 +352,7 @@ __global__ void __launch_bounds__(kCkptThreads) k_ckpt_bwd_any(CkptArgs a, int q
       const float* s = a.s + row * nb * (GATED ? 2 : 1);
       fetch_block<2>(in, dy0 + row * a.lddy * 2, b * kQBlock, a.I, dy0, l);
       fetch_block<1>(in + kStageBytes, q, b * kQBlock, a.I, a.q, l);
-      if constexpr (GATED) fetch_block<1>(in + kStageBytes + kCodes, q + a.I, b * kQBlock, a.I, a.q, l);
+      if constexpr (GATED) fetch_block<1>(in + kStageBytes + kCodeBytes, q + a.I, b * kQBlock, a.I, a.q, l);
       sg_next = s[b];
       if constexpr (GATED) su_next = s[nb + b];
     }
@@ -305,7 +381,7 @@ __global__ void __launch_bounds__(kCkptThreads) k_ckpt_bwd_any(CkptArgs a, int q
         const uint8_t* in = in_smem[qc][stage];
         read16(d, in, (int)((uintptr_t)(dy + c0) & 15), l);
         read_codes(qg, in + kStageBytes, (int)((uintptr_t)(q + c0) & 15), l);
-        if constexpr (GATED) read_codes(qu, in + kStageBytes + kCodes, (int)((uintptr_t)(q + a.I + c0) & 15), l);
+        if constexpr (GATED) read_codes(qu, in + kStageBytes + kCodeBytes, (int)((uintptr_t)(q + a.I + c0) & 15), l);
         dw += bwd_block<E, ACT>(dg, du, yw, qg, qu, d, sg, su, w, a.act);
         auto put = [&](uint16_t* p, const uint32_t(&v)[8]) {
           stage16(out, p, v, l);
@@ -333,8 +409,8 @@ static cudaError_t fwd_t(const CkptArgs& a, cudaStream_t st) {
   const int qpr = quarters_a_row(a.I, kCkptQuarters), rpc = kCkptQuarters / qpr;
   const int64_t g = std::min<int64_t>((a.R + rpc - 1) / rpc, (int64_t)device_sms() * 32);
   note_launch();
-  if (vec) return launch_pdl(k_ckpt_fwd<E, true, ACT>, dim3((unsigned)g), dim3(kCkptThreads), 0, st, a, qpr);
-  return launch_pdl(k_ckpt_fwd<E, false, ACT>, dim3((unsigned)g), dim3(kCkptThreads), 0, st, a, qpr);
+  if (vec) return launch_pdl(k_ckpt_fwd<E, ACT>, dim3((unsigned)g), dim3(kCkptThreads), 0, st, a, qpr);
+  return launch_pdl(k_ckpt_fwd_any<E, ACT>, dim3((unsigned)g), dim3(kCkptThreads), 0, st, a, qpr);
 }
 
 template <typename E, int ACT, bool WARP>

@@ -237,6 +237,51 @@ def test_activation_checkpoint(R, I, act, dtype, pad):
         assert torch.equal(dh2, dh)
 
 
+# more rows than there are warps, at odd widths and strides too: rows of less than a block, of one quarter's and of four quarters' blocks
+@pytest.mark.parametrize("act", ["swiglu", "srelu"])
+@pytest.mark.parametrize("R,I", [(5001, 100), (4999, 129), (6000, 383), (5003, 512), (20001, 41)])
+@pytest.mark.parametrize("dtype,pad", [(BF16, 0), (F16, 8), (BF16, 3)])
+def test_activation_checkpoint_many_rows(R, I, act, dtype, pad):
+    test_activation_checkpoint(R, I, act, dtype, pad)
+
+
+@pytest.mark.parametrize("R,I", [(1, 5), (3, 7), (40, 301), (5000, 131)])
+@pytest.mark.parametrize("lead", [1, 6])
+def test_activation_checkpoint_of_tensors_off_a_boundary(R, I, lead):
+    """Tensors that begin and end inside 16-byte units: their neighbours in memory stay unread and unwritten."""
+    cuda_device()
+    g = _gen(R + I)
+
+    def inside(cols, dtype):
+        raw = torch.full(((R * cols + 32) * dtype.itemsize,), 0x7F, dtype=torch.uint8, device="cuda")
+        if dtype == BF16:
+            raw.view(BF16).fill_(NAN)
+        before = raw.clone()
+        a, n = lead * dtype.itemsize, R * cols * dtype.itemsize
+
+        def untouched():
+            return torch.equal(raw[:a], before[:a]) and torch.equal(raw[a + n:], before[a + n:])
+        return raw[a:a + n].view(dtype).view(R, cols), untouched
+
+    nb = -(-I // 128)
+    h, _ = inside(2 * I, BF16)
+    h.copy_(_randn(g, R, 2 * I, std=2.0))
+    dy, _ = inside(I, BF16)
+    dy.copy_(_randn(g, R, I))
+    w = torch.rand(R, generator=g, device="cuda")
+    (y, fy), (q, fq), (dh, fh) = inside(I, BF16), inside(2 * I, E4M3), inside(2 * I, BF16)
+    s, dw = torch.empty(R, 2 * nb, device="cuda"), torch.empty(R, device="cuda")
+    m.moe_act_ckpt_forward(h, w, y, q, s)
+    m.moe_act_ckpt_backward(dy, q, s, w, dh, dw)
+    assert fy() and fq() and fh()
+    y2, q2, s2 = torch.empty(R, I, dtype=BF16, device="cuda"), torch.empty(R, 2 * I, dtype=E4M3, device="cuda"), torch.empty_like(s)
+    dh2, dw2 = torch.empty(R, 2 * I, dtype=BF16, device="cuda"), torch.empty_like(dw)
+    m.moe_act_ckpt_forward(h.clone(), w, y2, q2, s2)
+    m.moe_act_ckpt_backward(dy.clone(), q2, s2, w, dh2, dw2)
+    assert torch.equal(y, y2) and torch.equal(q.view(torch.uint8), q2.view(torch.uint8)) and torch.equal(s, s2)
+    assert torch.equal(dh, dh2) and torch.equal(dw, dw2) and bool(torch.isfinite(dw).all())
+
+
 def test_activation_checkpoint_special_values():
     """Zeros, the smallest and largest values, infinities and NaN; no weight; no rows."""
     cuda_device()
