@@ -8,26 +8,16 @@ namespace moe {
 // A block's 128 columns belong to eight lanes, sixteen to a lane: columns
 // 8 l .. 8 l + 7 and 64 + 8 l .. . Sixteen, so that a block's fixed work (the
 // scales' divisions, shuffles, addresses) is spread over more elements. Held
-// as words of two 16-bit elements (four codes). VEC: every eight start on a
-// 16-byte (codes: 8-byte) boundary, I being a multiple of 8; otherwise rows at
-// any alignment. Columns past the n of the half (counted from the block's
-// first) read as zeros and are not written.
-template <bool VEC>
-__device__ __forceinline__ void load16(uint32_t (&w)[8], const uint16_t* p, int l, int n, const uint16_t* half, int I) {
+// as words of two 16-bit elements (four codes). These four where every eight
+// start on a 16-byte (codes: 8-byte) boundary and rows are of a multiple of
+// eight; the ones by way of shared memory below at any alignment. Columns past
+// the block's n read as zeros and are not written.
+__device__ __forceinline__ void load16(uint32_t (&w)[8], const uint16_t* p, int l, int n) {
 #pragma unroll
   for (int k = 0; k < 2; ++k) {
     const int c = 64 * k + 8 * l;
-    uint32_t v[4] = {0u, 0u, 0u, 0u};
-    if constexpr (VEC) {
-      if (c < n) {
-        const uint4 u = *reinterpret_cast<const uint4*>(p + c);
-        v[0] = u.x; v[1] = u.y; v[2] = u.z; v[3] = u.w;
-      }
-    } else {
-      load_any<2, 16>(v, p + c, half, half + I);
-    }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) w[4 * k + i] = v[i];
+    const uint4 u = c < n ? *reinterpret_cast<const uint4*>(p + c) : make_uint4(0u, 0u, 0u, 0u);
+    w[4 * k] = u.x; w[4 * k + 1] = u.y; w[4 * k + 2] = u.z; w[4 * k + 3] = u.w;
   }
 }
 template <typename E>
@@ -77,19 +67,13 @@ __device__ __forceinline__ void load_codes(uint32_t (&w)[4], const uint8_t* q, i
     w[2 * k + 1] = v.y;
   }
 }
-template <bool VEC>
 __device__ __forceinline__ void store_codes(uint8_t* q, const uint32_t (&w)[4], int l, int n) {
 #pragma unroll
   for (int k = 0; k < 2; ++k) {
     const int c = 64 * k + 8 * l;
-    const uint2 v = make_uint2(w[2 * k], w[2 * k + 1]);
-    if (c < n) {
-      if constexpr (VEC) *reinterpret_cast<uint2*>(q + c) = v;
-      else store_bytes8(q + c, v, n - c);
-    }
+    if (c < n) *reinterpret_cast<uint2*>(q + c) = make_uint2(w[2 * k], w[2 * k + 1]);
   }
 }
-
 // The codes of a block at any address by way of shared memory: eight at a time
 // to their columns' place in `buf` (kCodeBytes), after a __syncwarp whole units
 // of the row from there, what is left at the block's ends byte by byte.

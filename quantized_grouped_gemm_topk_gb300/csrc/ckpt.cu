@@ -138,12 +138,12 @@ __global__ void __launch_bounds__(kCkptThreads) k_ckpt_fwd(CkptArgs a, int qpr) 
     for (int b = part; b < nb; b += qpr) {
       const int c0 = b * kQBlock, n = min(kQBlock, a.I - c0);
       uint32_t gw[8], uw[8] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u}, yw[8], cg[4], cu[4];
-      load16<true>(gw, h + c0, l, n, h, a.I);
-      if constexpr (GATED) load16<true>(uw, h + a.I + c0, l, n, h + a.I, a.I);
+      load16(gw, h + c0, l, n);
+      if constexpr (GATED) load16(uw, h + a.I + c0, l, n);
       float sg, su;
       fwd_block<E, ACT>(yw, cg, cu, sg, su, gw, uw, w, a.act, lanes);
-      store_codes<true>(q + c0, cg, l, n);
-      if constexpr (GATED) store_codes<true>(q + a.I + c0, cu, l, n);
+      store_codes(q + c0, cg, l, n);
+      if constexpr (GATED) store_codes(q + a.I + c0, cu, l, n);
       if (l == 0) {
         s[b] = sg;
         if constexpr (GATED) s[nb + b] = su;
@@ -313,7 +313,7 @@ __global__ void __launch_bounds__(kCkptThreads) k_ckpt_bwd(CkptArgs a, int qpr) 
         uint32_t qg[4], qu[4] = {0u, 0u, 0u, 0u}, d[8], dg[8], du[8], yw[8];
         load_codes(qg, q + c0, l, n);
         if constexpr (GATED) load_codes(qu, q + a.I + c0, l, n);
-        load16<true>(d, dy + c0, l, n, dy, a.I);
+        load16(d, dy + c0, l, n);
         dw += bwd_block<E, ACT>(dg, du, yw, qg, qu, d, s[b], GATED ? s[nb + b] : 0.f, w, a.act);
         store16(dh + c0, dg, l, n);
         if constexpr (GATED) store16(dh + a.I + c0, du, l, n);

@@ -85,9 +85,26 @@ __global__ void __launch_bounds__(kQThreads) k_quant128_rows32(QuantRowsArgs a) 
   }
 }
 
+// A block's scale and codes.
+template <typename E>
+__device__ __forceinline__ float quant_block(uint32_t (&codes)[4], const uint32_t (&w)[8], unsigned lanes) {
+  uint32_t mm = mag_bits(w);
+#pragma unroll
+  for (int o = 4; o > 0; o >>= 1) mm = max(mm, __shfl_xor_sync(lanes, mm, o));
+  float s;
+  if (mm < E::kInf) {
+    s = block_scale(E::to((uint16_t)mm));
+    codes16<E, true>(codes, w, 1.0f / s);
+  } else {
+    s = finite_scale<E>(w, lanes);
+    codes16<E, false>(codes, w, 1.0f / s);
+  }
+  return s;
+}
+
 // 16-bit rows: a quarter-warp a block, sixteen columns a lane (blocks.cuh);
 // qpr quarter-warps of a CTA share a row.
-template <typename E, bool VEC>
+template <typename E>
 __global__ void __launch_bounds__(kQThreads) k_quant128_rows(QuantRowsArgs a, int qpr) {
   pdl_enter();
   const int l = threadIdx.x & 7, qw = threadIdx.x >> 3;
@@ -100,22 +117,54 @@ __global__ void __launch_bounds__(kQThreads) k_quant128_rows(QuantRowsArgs a, in
     for (int b = part; b < nb; b += qpr) {
       const int c0 = b * kQBlock, n = min(kQBlock, a.C - c0);
       uint32_t w[8], codes[4];
-      load16<VEC>(w, x + c0, l, n, x, a.C);
-      uint32_t mm = mag_bits(w);
-#pragma unroll
-      for (int o = 4; o > 0; o >>= 1) mm = max(mm, __shfl_xor_sync(lanes, mm, o));
-      float s;
-      if (mm < E::kInf) {
-        s = block_scale(E::to((uint16_t)mm));
-        codes16<E, true>(codes, w, 1.0f / s);
-      } else {
-        s = finite_scale<E>(w, lanes);
-        codes16<E, false>(codes, w, 1.0f / s);
-      }
-      store_codes<VEC>(q + c0, codes, l, n);
+      load16(w, x + c0, l, n);
+      const float s = quant_block<E>(codes, w, lanes);
+      store_codes(q + c0, codes, l, n);
       if (l == 0) a.s[row * a.lds + b] = s;
     }
   }
+}
+
+// The same for rows at any alignment: the next block's units on their way to
+// shared memory during a block, the codes stored from there.
+template <typename E>
+__global__ void __launch_bounds__(kQThreads) k_quant128_rows_any(QuantRowsArgs a, int qpr) {
+  __shared__ __align__(16) uint8_t in_smem[kQThreads / 8][2][kStageBytes];
+  __shared__ __align__(16) uint8_t out_smem[kQThreads / 8][kCodeBytes];
+  pdl_enter();
+  const int l = threadIdx.x & 7, qw = threadIdx.x >> 3;
+  const unsigned lanes = 0xffu << (threadIdx.x & 24);
+  const int nb = (a.C + kQBlock - 1) / kQBlock;
+  const int rpc = kQThreads / 8 / qpr, rl = qw / qpr, part = qw % qpr;
+  const int64_t step = (int64_t)gridDim.x * rpc;
+  const uint8_t* x0 = reinterpret_cast<const uint8_t*>(a.x);
+  auto fetch = [&](int64_t row, int b, int stage) {
+    if (row < a.R && b < nb) fetch_block<2>(in_smem[qw][stage], x0 + row * a.ldx * 2, b * kQBlock, a.C, x0, l);
+    cp_async_commit();
+  };
+  int stage = 0;
+  int64_t row = (int64_t)blockIdx.x * rpc + rl;
+  fetch(row, part, 0);
+  for (; row < a.R; row += step) {
+    const uint16_t* x = reinterpret_cast<const uint16_t*>(a.x) + row * a.ldx;
+    uint8_t* q = a.q + row * a.ldq;
+    for (int b = part; b < nb; b += qpr, stage ^= 1) {
+      const int c0 = b * kQBlock, n = min(kQBlock, a.C - c0);
+      const bool more = b + qpr < nb;
+      fetch(more ? row : row + step, more ? b + qpr : part, stage ^ 1);
+      cp_async_wait<1>();
+      __syncwarp(lanes);
+      uint32_t w[8], codes[4];
+      read16(w, in_smem[qw][stage], (int)((uintptr_t)(x + c0) & 15), l);
+      const float s = quant_block<E>(codes, w, lanes);
+      stage_codes(out_smem[qw], codes, l);
+      __syncwarp(lanes);
+      store_staged_codes(q + c0, out_smem[qw], l, n);
+      __syncwarp(lanes);
+      if (l == 0) a.s[row * a.lds + b] = s;
+    }
+  }
+  cp_async_wait<0>();
 }
 
 // Bytes (i, j) of eight rows of eight -> the same transposed: row words r[i][2]
@@ -255,8 +304,8 @@ static cudaError_t rows_t(const QuantRowsArgs& a, cudaStream_t st) {
   const int qpr = quarters_a_row(a.C, kQThreads / 8), rpc = kQThreads / 8 / qpr;
   const int64_t g = std::min<int64_t>((a.R + rpc - 1) / rpc, (int64_t)device_sms() * 32);
   note_launch();
-  if (rows_vec(a, 2)) return launch_pdl(k_quant128_rows<E, true>, dim3((unsigned)g), dim3(kQThreads), 0, st, a, qpr);
-  return launch_pdl(k_quant128_rows<E, false>, dim3((unsigned)g), dim3(kQThreads), 0, st, a, qpr);
+  if (rows_vec(a, 2)) return launch_pdl(k_quant128_rows<E>, dim3((unsigned)g), dim3(kQThreads), 0, st, a, qpr);
+  return launch_pdl(k_quant128_rows_any<E>, dim3((unsigned)g), dim3(kQThreads), 0, st, a, qpr);
 }
 static cudaError_t rows_32(const QuantRowsArgs& a, cudaStream_t st) {
   const int64_t items = a.R * ((a.C + kQBlock - 1) / kQBlock);

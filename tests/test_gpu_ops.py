@@ -365,6 +365,24 @@ def test_fp8_quant_rows(R, C, dtype, pad):
     assert bool((qbuf[:, C:].view(torch.uint8) == 0x7F).all())
 
 
+@pytest.mark.parametrize("R,C,lead", [(1, 3, 1), (3, 300, 7), (700, 131, 5)])
+def test_fp8_quant_rows_of_tensors_off_a_boundary(R, C, lead):
+    """Rows that begin and end inside 16-byte units, codes at odd addresses: the neighbours stay unread and unwritten."""
+    cuda_device()
+    buf = torch.full((R * C + 32,), NAN, dtype=BF16, device="cuda")
+    x = buf[lead:lead + R * C].view(R, C)
+    x.copy_(_randn(_gen(C), R, C))
+    raw = torch.full((R * C + 32,), 0x7F, dtype=torch.uint8, device="cuda")
+    q = raw[lead:lead + R * C].view(E4M3).view(R, C)
+    s, s2 = torch.empty(R, -(-C // 128), device="cuda"), torch.empty(R, -(-C // 128), device="cuda")
+    m.moe_fp8_quant_rows(x, q, s)
+    assert bool((raw[:lead] == 0x7F).all()) and bool((raw[lead + R * C:] == 0x7F).all())
+    q2 = torch.empty(R, C, dtype=E4M3, device="cuda")
+    m.moe_fp8_quant_rows(x.clone(), q2, s2)
+    assert torch.equal(s, s2) and torch.equal(q.contiguous().view(torch.uint8), q2.view(torch.uint8))
+    assert torch.equal(s, P.row_scales(x))
+
+
 @pytest.mark.parametrize("G,N,K", [(1, 1, 1), (2, 128, 128), (3, 130, 257), (1, 2048, 200), (2, 96, 1031), (1, 16, 4096)])
 @pytest.mark.parametrize("dtype,pad", [(BF16, 0), (F32, 3)])
 @pytest.mark.parametrize("transposed", [True, False])
