@@ -559,27 +559,41 @@ MmPlan mm_plan(int kind, int R, int N, int K, int G) {
   MmPlan p = {1, 256, 1};
   // tiles of `b` rows: at least one for every group that can have rows
   auto row_tiles = [&](int b) { return std::max<int64_t>(tiles(R, b), std::min(G, R)); };
-  int64_t units;
-  if (kind == kMmFp8) {
-    while (true) {
-      units = row_tiles(kGM) * tiles(N, p.bn);
-      if (p.bn == 64 || units >= kPlanSms) break;
-      p.bn /= 2;
-    }
-  } else {
-    auto count = [&](int cg, int bn) {
-      return wg ? G * tiles(N, kGM * cg) * tiles(K, bn) : row_tiles(bn) * tiles(N, kGM * cg);
-    };
-    // pairs of SMs where there is a tile for each of them, except at a few
-    // rows a group, which stream weights
+  auto count = [&](int cg, int bn) {
+    if (kind == kMmFp8) return row_tiles(kGM) * tiles(N, bn);
+    return wg ? G * tiles(N, kGM * cg) * tiles(K, bn) : row_tiles(bn) * tiles(N, kGM * cg);
+  };
+  if (kind != kMmFp8) {
+    // Pairs of SMs where there is a tile for each of them, except at a few
+    // rows a group, which stream weights. 4096 x 7168 weights, 32 groups: 256
+    // rows 276 us with single SMs, 281 with pairs; 1024 rows 283 and 280; 2048
+    // rows 324 and 301. One group, 8192^3: 755 and 615.
     p.cg = count(2, 256) >= kPlanSms / 2 && (wg || R >= 64ll * std::min(G, R)) ? 2 : 1;
-    // (and whose stages are small then: more of them in flight)
+    // Few rows a group: narrow tiles, whose stages are small, so that more of
+    // them are in flight (the same weights: 8 rows 76 us, 91 with wide tiles;
+    // 1024 rows 283 and 319).
     if (!wg && R <= 32ll * std::min(G, R)) p.bn = R <= 8ll * std::min(G, R) ? 32 : 64;
-    while (p.cg == 1 && p.bn > 64 && count(1, p.bn) < kPlanSms) p.bn /= 2;
-    units = count(p.cg, p.bn);
   }
-  // pieces of at least 512 (FP8: 1024) of the reduction, partial sums within
-  // the workspace's bound
+  if (p.cg == 1 && p.bn > 64) {
+    // The width that takes the least time: rounds of tiles over the SMs times
+    // a stage's bytes, 128 + bn rows of an operand, which bound it. Against
+    // the widest with a tile for every SM: FP8 1024 x 2048 x 4096 18.4 us (28.7),
+    // 512 x 7168 x 4096 24 (32), 1500 x 4096 x 2048 27 (26); bf16 1024 x 2880 x
+    // 2880 24 (28), 1500 x 2048 x 7168 48 (58). Against the widest of all: FP8
+    // 3 x 7168 x 2048 10.6 us (13.3).
+    int64_t least = INT64_MAX;
+    for (int bn = p.bn; bn >= 64; bn /= 2) {
+      const int64_t cost = tiles(count(1, bn), kPlanSms) * (kGM + bn);
+      if (cost <= least) {
+        least = cost;
+        p.bn = bn;
+      }
+    }
+  }
+  const int64_t units = count(p.cg, p.bn);
+  // Too few tiles: pieces of at least 512 (FP8: 1024) of the reduction, partial
+  // sums within the workspace's bound (bf16 64 x 2880 x 2880 14.8 us, 20.7 in
+  // one piece).
   const int64_t red = wg ? tiles(R, G) : K, step = kind == kMmFp8 ? 1024 : 512;
   const int64_t outs = wg ? (int64_t)G * N * K : (int64_t)R * N;
   if (p.cg == 1 && units > 0 && units < kPlanSms && outs > 0)
