@@ -283,21 +283,17 @@ __device__ __forceinline__ float bwd_block(uint32_t (&dg)[8], uint32_t (&du)[8],
              : bwd16<E, ACT, false>(dg, du, y, qg, qu, d, sg, su, w, p);
 }
 
-// qpr quarter-warps share a row. WARP: at most four, of one warp: the row's dw
-// needs shuffles only, and warps go on at their own pace. Otherwise all of a
-// CTA's may share one (few rows), and dw crosses shared memory.
-template <typename E, int ACT, bool WARP>
+// qpr quarter-warps of a CTA share a row, whose dw crosses shared memory.
+template <typename E, int ACT>
 __global__ void __launch_bounds__(kCkptThreads) k_ckpt_bwd(CkptArgs a, int qpr) {
   constexpr bool GATED = ACT != MOE_ACT_SRELU;
   pdl_enter();
-  __shared__ float sdw[2][WARP ? 1 : kCkptQuarters];
-  const int l = threadIdx.x & 7, qw = WARP ? (threadIdx.x & 31) >> 3 : threadIdx.x >> 3;
+  __shared__ float sdw[2][kCkptQuarters];
+  const int l = threadIdx.x & 7, qw = threadIdx.x >> 3;
   const int nb = (a.I + kQBlock - 1) / kQBlock;
-  const int rpg = (WARP ? 4 : kCkptQuarters) / qpr, rl = qw / qpr, part = qw % qpr;   // rows a warp (CTA) takes
-  const int64_t group = WARP ? (int64_t)blockIdx.x * (kCkptThreads / 32) + (threadIdx.x >> 5) : blockIdx.x;
-  const int64_t groups = WARP ? (int64_t)gridDim.x * (kCkptThreads / 32) : gridDim.x;
+  const int rpc = kCkptQuarters / qpr, rl = qw / qpr, part = qw % qpr;     // rows a CTA takes
   int flip = 0;
-  for (int64_t r0 = group * rpg; r0 < a.R; r0 += groups * rpg, flip ^= 1) {
+  for (int64_t r0 = (int64_t)blockIdx.x * rpc; r0 < a.R; r0 += (int64_t)gridDim.x * rpc, flip ^= 1) {
     const int64_t row = r0 + rl;
     const bool live = row < a.R;
     const float w = live && a.w ? a.w[row] : 1.f;
@@ -320,12 +316,14 @@ __global__ void __launch_bounds__(kCkptThreads) k_ckpt_bwd(CkptArgs a, int qpr) 
         if (a.y) store16(y + c0, yw, l, n);
       }
     }
-    if (a.dw) join_dw<WARP>(a.dw + row, dw, live, part, qpr, sdw[flip], qw, l);
+    if (a.dw) join_dw<false>(a.dw + row, dw, live, part, qpr, sdw[flip], qw, l);
   }
 }
 
-// The same for rows at any alignment. A quarter-warp fetches its next block's
-// units into shared memory while it works on one (loads of its own columns
+// The same for rows at any alignment. WARP: at most four quarter-warps, of one
+// warp, share a row: its dw needs shuffles only, and warps go on at their own
+// pace. A quarter-warp fetches its next block's units into shared memory while
+// it works on one (loads of its own columns
 // waited for half the time, at 8 of 13 cycles an instruction), and its outputs
 // leave through shared memory too (store_staged).
 template <typename E, int ACT, bool WARP>
@@ -413,21 +411,22 @@ static cudaError_t fwd_t(const CkptArgs& a, cudaStream_t st) {
   return launch_pdl(k_ckpt_fwd_any<E, ACT>, dim3((unsigned)g), dim3(kCkptThreads), 0, st, a, qpr);
 }
 
-template <typename E, int ACT, bool WARP>
-static cudaError_t bwd_w(const CkptArgs& a, bool vec, int qpr, cudaStream_t st) {
-  const int64_t rows = WARP ? kCkptThreads / 32 * (4 / qpr) : kCkptQuarters / qpr;     // a CTA's
-  const int64_t g = std::min<int64_t>((a.R + rows - 1) / rows, (int64_t)device_sms() * 32);
-  note_launch();
-  if (vec) return launch_pdl(k_ckpt_bwd<E, ACT, WARP>, dim3((unsigned)g), dim3(kCkptThreads), 0, st, a, qpr);
-  return launch_pdl(k_ckpt_bwd_any<E, ACT, WARP>, dim3((unsigned)g), dim3(kCkptThreads), 0, st, a, qpr);
-}
 template <typename E, int ACT>
 static cudaError_t bwd_t(const CkptArgs& a, cudaStream_t st) {
   const bool vec = a.I % 8 == 0 && a.lddy % 8 == 0 && a.lddh % 8 == 0 && a.ldq % 8 == 0 && al(a.dy, 16) &&
                    al(a.dh, 16) && al(a.q, 8) && (!a.y || (a.ldy % 8 == 0 && al(a.y, 16)));
-  // a warp a row (or more rows) where that leaves every SM a full set of warps
-  if (a.R >= 32LL * device_sms()) return bwd_w<E, ACT, true>(a, vec, quarters_a_row(a.I, 4), st);
-  return bwd_w<E, ACT, false>(a, vec, quarters_a_row(a.I, kCkptQuarters), st);
+  // A warp a row (or more rows) at odd alignments, where that leaves a warp
+  // several rows: 16385 x 2047 79.6 us (87.2 by CTAs), 65536 x 2881 414 (445);
+  // with fewer rows the last ones leave SMs idle (5000 x 2047 31.1 and 27.2).
+  // Aligned rows gain nothing (16384 x 2048 53.1 and 52.7, x 2880 76.6 and 72.6).
+  const bool warp = !vec && a.R >= 96LL * device_sms();
+  const int qpr = quarters_a_row(a.I, warp ? 4 : kCkptQuarters);
+  const int64_t rows = kCkptQuarters / qpr;     // a CTA's
+  const dim3 g((unsigned)std::min<int64_t>((a.R + rows - 1) / rows, (int64_t)device_sms() * 32)), b(kCkptThreads);
+  note_launch();
+  if (vec) return launch_pdl(k_ckpt_bwd<E, ACT>, g, b, 0, st, a, qpr);
+  if (warp) return launch_pdl(k_ckpt_bwd_any<E, ACT, true>, g, b, 0, st, a, qpr);
+  return launch_pdl(k_ckpt_bwd_any<E, ACT, false>, g, b, 0, st, a, qpr);
 }
 
 template <typename E, bool FWD>

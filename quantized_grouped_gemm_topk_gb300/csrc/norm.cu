@@ -814,9 +814,8 @@ static NormPlan norm_plan(int64_t n, int64_t T, int resident, int max_parts, int
   return p;
 }
 
-// Launch of the ring, or cudaErrorNotSupported where it does not apply: few
-// rows (their latency is shorter without it), rows of at most a warp's packs
-// (many rows in flight already) or of more than the registers hold.
+// Launch of the ring, or cudaErrorNotSupported: few rows, rows of at most a
+// warp's packs (many rows in flight already) or of more than the registers hold.
 template <typename E, bool WF32, int NV, bool PART, bool BWD, bool ANY>
 static cudaError_t ring_nv(const NormArgs& a, int threads, int64_t* parts, cudaStream_t st) {
   const auto kern = k_norm_ring<E, WF32, NV, PART, BWD, ANY>;
@@ -846,7 +845,10 @@ template <typename E, bool WF32, bool PART, bool BWD, bool ANY>
 static cudaError_t ring_launch(const NormArgs& a, int64_t* parts, cudaStream_t st) {
   constexpr int V = 16 / (int)sizeof(typename E::raw);
   const int n = (a.H + V - 1) / V;
-  if (n <= 32 || n > 4 * kNormBwdThreads || a.T < 4LL * device_sms()) return cudaErrorNotSupported;
+  // The backward's two inputs, in a CTA's registers, leave few bytes in flight:
+  // 16384 x 2880 65.6 us against 97.8 with rows in registers, 300 x 2880 10.1
+  // against 13.8, 32 x 2880 8.4 and 8.3.
+  if (n <= 32 || n > 4 * kNormBwdThreads || 2 * a.T < (BWD ? device_sms() : 0)) return cudaErrorNotSupported;
   // one pack a thread while that is at most 512 threads, then two, four: the
   // sums over rows of a thread's columns stay in registers, and the fewer of
   // them the more warps hide the row's barriers
@@ -860,9 +862,19 @@ static cudaError_t ring_launch(const NormArgs& a, int64_t* parts, cudaStream_t s
 template <typename E, bool WF32, bool VEC>
 static cudaError_t fwd_v(const NormArgs& a, cudaStream_t st) {
   constexpr int V = 16 / (int)sizeof(typename E::raw);
-  int64_t ring_parts;
-  const cudaError_t re = ring_launch<E, WF32, false, false, !VEC>(a, &ring_parts, st);
-  if (re != cudaErrorNotSupported) return re;
+  // The ring gains only in many long rows of 16 bits (16384 x 2880 47.2 us, 49.9
+  // with rows in registers; 9000 x 2880 27.6 and 28.6; but 4096 x 2880 13.8 and
+  // 12.9, 16384 x 1000 23.6 and 20.8), which at odd alignments it slows down
+  // (16384 x 2881 84 and 77), and in fp32 at odd alignments (8192 x 2881 44.9 and
+  // 59.1, 1000 x 2881 8.2 and 9.7; aligned, 16384 x 2880, 69 and 59).
+  constexpr bool k32 = sizeof(typename E::raw) == 4;
+  if constexpr (k32 != VEC) {
+    int64_t parts;
+    if (a.T >= (k32 ? 4LL : 48LL) * device_sms() && (k32 || a.H > 256 * V)) {
+      const cudaError_t re = ring_launch<E, WF32, false, false, !VEC>(a, &parts, st);
+      if (re != cudaErrorNotSupported) return re;
+    }
+  }
   const NormPlan p = norm_plan(((int64_t)a.H + V - 1) / V, a.T, 0, 0, kNormMaxThreads);
   const dim3 g((unsigned)p.grid), b(p.threads);
   note_launch();
@@ -885,7 +897,8 @@ template <typename E, bool WF32, bool VEC>
 static cudaError_t bwd_v(const NormArgs& a, cudaStream_t st) {
   constexpr int V = 16 / (int)sizeof(typename E::raw);
   const bool want = a.dgamma || a.dbeta;
-  const NormPlan p = norm_plan(((int64_t)a.H + V - 1) / V, a.T, (int64_t)a.H <= 32 * V ? 2048 : 512, want ? kNormMaxParts : 0, kNormBwdThreads);
+  const NormPlan p = norm_plan(((int64_t)a.H + V - 1) / V, a.T, (int64_t)a.H <= 32 * V ? 2048 : 512,
+                               want ? kNormMaxParts : 0, kNormBwdThreads);
   cudaError_t e = cudaErrorNotSupported;
   int64_t parts = p.grid;
   e = want ? ring_launch<E, WF32, true, true, !VEC>(a, &parts, st) : ring_launch<E, WF32, false, true, !VEC>(a, &parts, st);
