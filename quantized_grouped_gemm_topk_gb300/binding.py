@@ -496,7 +496,8 @@ def moe_layer_norm_forward(x, gamma, beta, eps, y, mean=None, rstd=None, stream=
     wt = next((w.dtype for w in (gamma, beta) if w is not None), torch.float32)
     wts = (wt,) if wt in (torch.float32, x.dtype) else _F32
     _check("moe_layer_norm_forward", load().moe_layer_norm_forward(
-        _arg(x, "x", _FLOATS, (T, H), dev), _ld(x, "x"), _flat(gamma, "gamma", wts, (H,), dev), _flat(beta, "beta", wts, (H,), dev),
+        _arg(x, "x", _FLOATS, (T, H), dev), _ld(x, "x"), _flat(gamma, "gamma", wts, (H,), dev),
+        _flat(beta, "beta", wts, (H,), dev),
         eps, T, H, DTYPES[x.dtype], DTYPES[wt], _arg(y, "y", (x.dtype,), (T, H), dev), _ld(y, "y"),
         _flat(mean, "mean", _F32, (T,), dev), _flat(rstd, "rstd", _F32, (T,), dev), _stream(stream)))
 
@@ -512,7 +513,8 @@ def moe_layer_norm_backward(dy, x, gamma, mean, rstd, dx, dgamma=None, dbeta=Non
     wp, wn = _ws(ws, dev)
     _check("moe_layer_norm_backward", load().moe_layer_norm_backward(
         _arg(dy, "dy", own, (T, H), dev), _ld(dy, "dy"), _arg(x, "x", _FLOATS, (T, H), dev), _ld(x, "x"),
-        _flat(gamma, "gamma", wts, (H,), dev), _flat(mean, "mean", _F32, (T,), dev), _flat(rstd, "rstd", _F32, (T,), dev), T, H,
+        _flat(gamma, "gamma", wts, (H,), dev), _flat(mean, "mean", _F32, (T,), dev),
+        _flat(rstd, "rstd", _F32, (T,), dev), T, H,
         DTYPES[x.dtype], DTYPES[wt], _arg(dx, "dx", own, (T, H), dev), _ld(dx, "dx"), _flat(dgamma, "dgamma", wts, (H,), dev),
         _flat(dbeta, "dbeta", wts, (H,), dev), wp, wn, _stream(stream)))
 
@@ -525,7 +527,8 @@ def moe_act_ckpt_forward(h, w_row, y, q, s, act="swiglu", alpha=1.0, limit=0.0, 
     halves = 1 if act == "srelu" else 2
     nb = halves * -(-I // FP8_BLOCK)
     _check("moe_act_ckpt_forward", load().moe_act_ckpt_forward(
-        _arg(h, "h", _16BIT, (R, halves * I), dev), _ld(h, "h"), _flat(w_row, "w_row", _F32, (R,), dev), R, I, DTYPES[h.dtype],
+        _arg(h, "h", _16BIT, (R, halves * I), dev), _ld(h, "h"), _flat(w_row, "w_row", _F32, (R,), dev), R,
+        I, DTYPES[h.dtype],
         ACTS[act], alpha, limit, _arg(y, "y", (h.dtype,), (R, I), dev), _ld(y, "y"), _arg(q, "q", _U8, (R, halves * I), dev),
         _ld(q, "q"), _flat(s, "s", _F32, (R, nb), dev), _stream(stream)))
 
@@ -540,7 +543,8 @@ def moe_act_ckpt_backward(dy, q, s, w_row, dh, dw_row=None, y=None, act="swiglu"
     own = (dy.dtype,)
     _check("moe_act_ckpt_backward", load().moe_act_ckpt_backward(
         _arg(dy, "dy", _16BIT, (R, I), dev), _ld(dy, "dy"), _arg(q, "q", _U8, (R, halves * I), dev), _ld(q, "q"),
-        _flat(s, "s", _F32, (R, nb), dev), _flat(w_row, "w_row", _F32, (R,), dev), R, I, DTYPES[dy.dtype], ACTS[act], alpha, limit,
+        _flat(s, "s", _F32, (R, nb), dev), _flat(w_row, "w_row", _F32, (R,), dev), R, I, DTYPES[dy.dtype],
+        ACTS[act], alpha, limit,
         _arg(dh, "dh", own, (R, halves * I), dev), _ld(dh, "dh"), _flat(dw_row, "dw_row", _F32, (R,), dev),
         None if y is None else _arg(y, "y", own, (R, I), dev), 0 if y is None else _ld(y, "y"), _stream(stream)))
 
@@ -561,8 +565,10 @@ def moe_grouped_mm(x, w, offsets, out, ws, trans_w=False, stream=None):
     N = w.shape[2] if trans_w else w.shape[1]
     wp, wn = _ws(ws, dev)
     _check("moe_grouped_mm", load().moe_grouped_mm(
-        _arg(x, "x", _16BIT, (R, K), dev), _ld(x, "x", 8), _arg(w, "w", (x.dtype,), (G, K, N) if trans_w else (G, N, K), dev),
-        _group(w), _ld(w, "w", 8), int(trans_w), _flat(offsets, "offsets", _I32, (G + 1,), dev), R, N, K, G, DTYPES[x.dtype],
+        _arg(x, "x", _16BIT, (R, K), dev), _ld(x, "x", 8),
+        _arg(w, "w", (x.dtype,), (G, K, N) if trans_w else (G, N, K), dev),
+        _group(w), _ld(w, "w", 8), int(trans_w), _flat(offsets, "offsets", _I32, (G + 1,), dev), R, N, K, G,
+        DTYPES[x.dtype],
         _arg(out, "out", (x.dtype, torch.float32), (R, N), dev), _ld(out, "out"), DTYPES[out.dtype], wp, wn,
         _stream(stream)))
 
@@ -586,7 +592,8 @@ def moe_fp8_quant_rows(x, q, s, stream=None):
     dev = _device()
     R, C = _dims(x, "x", 2)
     _check("moe_fp8_quant_rows", load().moe_fp8_quant_rows(
-        _arg(x, "x", _FLOATS, (R, C), dev), _ld(x, "x"), R, C, DTYPES[x.dtype], _arg(q, "q", _U8, (R, C), dev), _ld(q, "q"),
+        _arg(x, "x", _FLOATS, (R, C), dev), _ld(x, "x"), R, C, DTYPES[x.dtype],
+        _arg(q, "q", _U8, (R, C), dev), _ld(q, "q"),
         _arg(s, "s", _F32, (R, -(-C // FP8_BLOCK)), dev), _ld(s, "s"), _stream(stream)))
 
 
@@ -615,8 +622,10 @@ def moe_fp8_mm(xq, xs, wq, wscale, out, ws, offsets=None, stream=None):
     wp, wn = _ws(ws, dev)
     _check("moe_fp8_mm", load().moe_fp8_mm(
         _arg(xq, "xq", _U8, (R, K), dev), _ld(xq, "xq", 16), _arg(xs, "xs", _F32, (R, kb), dev), _ld(xs, "xs"),
-        _arg(wq, "wq", _U8, (G, N, K), dev), _group(wq), _ld(wq, "wq", 16), _flat(wscale, "wscale", _F32, (G, nb, kb), dev),
-        _flat(offsets, "offsets", _I32, (G + 1,), dev), R, N, K, G, _arg(out, "out", _FLOATS, (R, N), dev), _ld(out, "out"),
+        _arg(wq, "wq", _U8, (G, N, K), dev), _group(wq), _ld(wq, "wq", 16),
+        _flat(wscale, "wscale", _F32, (G, nb, kb), dev),
+        _flat(offsets, "offsets", _I32, (G + 1,), dev), R, N, K, G, _arg(out, "out", _FLOATS, (R, N), dev),
+        _ld(out, "out"),
         DTYPES[out.dtype], wp, wn, _stream(stream)))
 
 

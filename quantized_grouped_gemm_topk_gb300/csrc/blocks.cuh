@@ -54,7 +54,8 @@ __device__ __forceinline__ void store_staged(uint16_t* p, const uint8_t* buf, in
   }
   // what lies in the first and the last unit besides: an element a lane
   const int e = 2 * l, first = min(16, end), last = end & ~15;
-  if (off && e >= off && e < first) *reinterpret_cast<uint16_t*>(base + e) = *reinterpret_cast<const uint16_t*>(buf + e);
+  if (off && e >= off && e < first)
+    *reinterpret_cast<uint16_t*>(base + e) = *reinterpret_cast<const uint16_t*>(buf + e);
   if ((!off || last) && last + e < end)
     *reinterpret_cast<uint16_t*>(base + last + e) = *reinterpret_cast<const uint16_t*>(buf + last + e);
 }
@@ -105,7 +106,8 @@ __device__ __forceinline__ void store_staged_codes(uint8_t* q, const uint8_t* bu
 // Bytes past the block or the row become zeros and are not read; a first unit that
 // begins before `base`, the tensor's first byte, is read byte by byte.
 template <int ES>
-__device__ __forceinline__ void fetch_block(uint8_t* buf, const uint8_t* row, int c, int n, const uint8_t* base, int l) {
+__device__ __forceinline__ void fetch_block(uint8_t* buf, const uint8_t* row, int c, int n, const uint8_t* base,
+                                            int l) {
   const uint8_t* p = row + (int64_t)c * ES;
   const int off = (int)((uintptr_t)p & 15);
   const uint8_t* at = p - off + 16 * l;

@@ -18,9 +18,9 @@
 // took 745 cycles whatever else was changed) is less than a 128 x 256
 // tile on one SM wants (48 KB per 512 cycles of MMA). So where there is work
 // for it a pair of SMs (cta_group::2) multiplies a 256 x 256 tile together:
-// 32 KB for each. Tiles of one SM (128 x up to 256) serve few tiles
-// and few rows. Stages of 128 of the reduction in a ring that fills the shared
-// memory, filled by tensor copies with the 128-byte swizzle. Ragged edges cost
+// 32 KB for each. Tiles of one SM (128 x up to 256) serve few tiles and few
+// rows. Stages of 128 of the reduction in a ring that fills the shared memory,
+// filled by tensor copies with the 128-byte swizzle. Ragged edges cost
 // no branch in the main loop: rows of a tile that belong to the next group
 // only reach accumulator columns that are not stored; columns and the K tail
 // read as zeros (the tensor maps end at N and K); the weight gradient's last
@@ -36,6 +36,10 @@
 // gradient: those behind a group's last rows, in shared memory).
 // Every wait is bounded; a CTA whose wait runs out sets MOE_DEV_TIMEOUT, waits
 // for its copies and MMAs in flight, frees tensor memory and returns.
+// Measured, bf16: 8192^3 NT 615 us (1.79 PFLOP/s), NN 634, weight gradient 646;
+// 65536 rows in 128 groups x 5760 x 2880 1.45 to 1.53 ms (1.42 to 1.50 PFLOP/s;
+// tensor pipe 68 % busy); 30011 rows in 64 groups, 2880 x 2880 weight gradients
+// 0.47 to 0.58 ms; 8 rows of 8 experts x 4096 x 7168 76 us (6.2 TB/s of weights).
 #include "groups.cuh"
 #include "tc.cuh"
 
@@ -44,9 +48,10 @@ namespace moe {
 enum { kRowsNT = 0, kRowsNN = 1, kWgradMN = 2 };
 
 // Reduction a stage: two halves of one 128-byte swizzle row each, which land
-// behind one barrier and are freed one by one. The thread that issues the MMAs spends some 270 cycles a stage
-// besides the MMAs themselves; with one half a stage that was the bound of
-// tiles narrower than 256 (about 570 cycles a stage whatever their width).
+// behind one barrier and are freed one by one. The thread that issues the MMAs
+// spends some 270 cycles a stage besides the MMAs themselves; with one half a
+// stage that was the bound of tiles narrower than 256 (about 570 cycles a stage
+// whatever their width).
 constexpr int kGH = 64;
 constexpr int kGK = 2 * kGH;
 constexpr int kGN = 256;              // widest tile

@@ -14,9 +14,14 @@
 // Bound: the tensor pipe at training sizes (a 128 x 256 x 128 block is 512
 // cycles of MMA, its additions 256 issue slots a scheduler at most), the
 // weights' bytes at decode sizes.
-// Measured at 8192^3: 511 us (2.15 PFLOP/s), 1000 cycles a block; without the
-// additions 816, without them and three of the four MMAs 670 (the copies:
-// 48 KB at what an SM takes in). The slots' round trip is what shows.
+// Measured: 8192^3 511 us (2.15 PFLOP/s), 8192 x 7168 x 4096 236 us, 12289 rows in
+// 32 groups x 4096 x 7168 395 us, 3 x 7168 x 2048 10.6 us.
+// At 8192^3 a block takes 1000 cycles; without the additions 816, without them
+// and three of the four MMAs 670 (the copies: 48 KB at what an SM takes in).
+// Of a block's way the issue of its MMAs is 600 cycles, the last commit's until
+// the adding warps see it 680, the reads of tensor memory and the sums 460: the
+// round trip of its slot is what shows, not the copies (a pair of SMs, with 32
+// KB a block, took 512 us) nor power (all-zero operands 507).
 // Tiles are 128 rows x BN columns on one SM; copies and edges as in gemm16.cu.
 // Roles: warp 0 copies W, warp 2 copies x, warps 1 and 3 issue the MMAs of the
 // tile's halves (warp 3 first clears rows outside every group), warps 4-11
