@@ -515,7 +515,8 @@ def moe_layer_norm_backward(dy, x, gamma, mean, rstd, dx, dgamma=None, dbeta=Non
         _arg(dy, "dy", own, (T, H), dev), _ld(dy, "dy"), _arg(x, "x", _FLOATS, (T, H), dev), _ld(x, "x"),
         _flat(gamma, "gamma", wts, (H,), dev), _flat(mean, "mean", _F32, (T,), dev),
         _flat(rstd, "rstd", _F32, (T,), dev), T, H,
-        DTYPES[x.dtype], DTYPES[wt], _arg(dx, "dx", own, (T, H), dev), _ld(dx, "dx"), _flat(dgamma, "dgamma", wts, (H,), dev),
+        DTYPES[x.dtype], DTYPES[wt], _arg(dx, "dx", own, (T, H), dev), _ld(dx, "dx"),
+        _flat(dgamma, "dgamma", wts, (H,), dev),
         _flat(dbeta, "dbeta", wts, (H,), dev), wp, wn, _stream(stream)))
 
 
@@ -529,7 +530,8 @@ def moe_act_ckpt_forward(h, w_row, y, q, s, act="swiglu", alpha=1.0, limit=0.0, 
     _check("moe_act_ckpt_forward", load().moe_act_ckpt_forward(
         _arg(h, "h", _16BIT, (R, halves * I), dev), _ld(h, "h"), _flat(w_row, "w_row", _F32, (R,), dev), R,
         I, DTYPES[h.dtype],
-        ACTS[act], alpha, limit, _arg(y, "y", (h.dtype,), (R, I), dev), _ld(y, "y"), _arg(q, "q", _U8, (R, halves * I), dev),
+        ACTS[act], alpha, limit, _arg(y, "y", (h.dtype,), (R, I), dev), _ld(y, "y"),
+        _arg(q, "q", _U8, (R, halves * I), dev),
         _ld(q, "q"), _flat(s, "s", _F32, (R, nb), dev), _stream(stream)))
 
 

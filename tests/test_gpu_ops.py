@@ -708,3 +708,49 @@ def test_operators_on_another_stream_and_in_a_graph():
     graph.replay()
     torch.cuda.synchronize()
     assert all(torch.equal(p, r) for p, r in zip((y, h, a, q.view(torch.uint8), s), ref))
+
+
+def test_elements_past_32_bits():
+    """More than 2^31 elements: the last rows come out as they do alone."""
+    cuda_device()
+    if torch.cuda.mem_get_info()[0] < 40 << 30:
+        pytest.skip("needs 40 GB")
+    g, L = _gen(31), 70
+
+    def last(t):
+        return t[-L:].clone()
+
+    R, I = 380001, 2881
+    nb = -(-I // 128)
+    h = torch.empty(R, 2 * I, dtype=BF16, device="cuda").normal_(generator=g)
+    w = torch.rand(R, generator=g, device="cuda")
+
+    def forward(h, w):
+        n = h.shape[0]
+        y, q = torch.empty(n, I, dtype=BF16, device="cuda"), torch.empty(n, 2 * I, dtype=E4M3, device="cuda")
+        s = torch.empty(n, 2 * nb, device="cuda")
+        m.moe_act_ckpt_forward(h, w, y, q, s)
+        return y, q, s
+    y, q, s = forward(h, w)
+    y2, q2, s2 = forward(last(h), last(w))
+    assert torch.equal(y[-L:], y2) and torch.equal(q[-L:].view(torch.uint8), q2.view(torch.uint8)) and torch.equal(s[-L:], s2)
+    dh2 = torch.empty(L, 2 * I, dtype=BF16, device="cuda")
+    m.moe_act_ckpt_backward(last(y), q2, s2, last(w), dh2)
+    m.moe_act_ckpt_backward(y, q, s, w, h)
+    assert torch.equal(h[-L:], dh2)
+
+    K, N, G = 2 * I + 6, 64, 3           # rows of h's buffer, as a product's: a stride that is a multiple of 8
+    x = h.view(-1)[:R * 2 * I // K * K].view(-1, K)
+    x.normal_(generator=g)
+    T = x.shape[0]
+    off = torch.tensor([0, 100000, 100000, T], dtype=torch.int32, device="cuda")
+    wt = _randn(g, G, N, K, dtype=BF16, std=0.05)
+    o = torch.empty(T, N, device="cuda")
+    m.moe_grouped_mm(x, wt, off, o, _workspace(m.MOE_MM_ROWS, T, N, K, G))
+    ref, mag = P.grouped(last(x), wt[2:], [0, L])
+    P.assert_within(o[-L:], ref, (K + 4) * P.EPS32 * mag, "product")
+    xq, xs = torch.empty(T, K, dtype=E4M3, device="cuda"), torch.empty(T, -(-K // 128), device="cuda")
+    xq2, xs2 = torch.empty(L, K, dtype=E4M3, device="cuda"), torch.empty(L, -(-K // 128), device="cuda")
+    m.moe_fp8_quant_rows(x, xq, xs)
+    m.moe_fp8_quant_rows(last(x), xq2, xs2)
+    assert torch.equal(xq[-L:].view(torch.uint8), xq2.view(torch.uint8)) and torch.equal(xs[-L:], xs2)
