@@ -39,7 +39,7 @@
 // Measured, bf16: 8192^3 NT 615 us (1.79 PFLOP/s), NN 634, weight gradient 646;
 // 65536 rows in 128 groups x 5760 x 2880 1.45 to 1.53 ms (1.42 to 1.50 PFLOP/s;
 // tensor pipe 68 % busy); 30011 rows in 64 groups, 2880 x 2880 weight gradients
-// 0.47 to 0.58 ms; 8 rows of 8 experts x 4096 x 7168 76 us (6.2 TB/s of weights).
+// 0.43 ms; 8 rows of 8 experts x 4096 x 7168 76 us (6.2 TB/s of weights).
 #include "groups.cuh"
 #include "tc.cuh"
 
@@ -351,7 +351,9 @@ __global__ void __launch_bounds__(kGThreads, 1) k_gemm16(const GArgs g, const __
           // asked now, so that the answer's latency passes behind the MMAs' issue
           ready = tc::bar_test(full_u + 8 * slot, phase);
           if (kWg && g_tail(left)) {
-            // warp 3 (of both CTAs) clears the rows of the next group
+            // warp 3 (of both CTAs) clears the rows of the next group. No step
+            // of the stage is issued before: that the second CTA's copies have
+            // landed is only known from its arrival
             tc::mbar_arrive(tgo);
             if (!tc::bar_wait(pfull_u + 8 * slot_now, (tails >> slot_now) & 1, abort)) { ok = false; break; }
             tails ^= 1u << slot_now;
