@@ -754,3 +754,206 @@ def test_elements_past_32_bits():
     m.moe_fp8_quant_rows(x, xq, xs)
     m.moe_fp8_quant_rows(last(x), xq2, xs2)
     assert torch.equal(xq[-L:].view(torch.uint8), xq2.view(torch.uint8)) and torch.equal(xs[-L:], xs2)
+
+
+# ---- both sides of the rules that pick a kernel ------------------------------------------
+# Sizes in rows an SM, as the rules count them, so that they follow the machine.
+def _rows(per_sm, more):
+    return per_sm * torch.cuda.get_device_properties(0).multi_processor_count + more
+
+
+def _check_norm_forward(x, gamma, beta, eps, y, mean, rstd):
+    """The bounds of test_layer_norm."""
+    H = x.shape[1]
+    ry, rm, rr = P.norm_fwd(x, gamma, beta, eps)
+    dmean = (H + 4) * P.EPS32 * x.double().abs().mean(1)
+    P.assert_within(mean, rm, dmean, "mean")
+    rel = (H + 8) * P.EPS32 + (dmean * rr) ** 2
+    P.assert_within(rstd, rr, rr * rel, "rstd")
+    c = (x.double() - rm[:, None]).abs() * rr[:, None]
+    gm = 1.0 if gamma is None else gamma.double().abs()
+    b = 0.0 if beta is None else beta.double().abs()
+    P.assert_within(y, ry, (c * (rel[:, None] + 4 * P.EPS32) + (dmean * rr)[:, None]) * gm + 2 * P.EPS32 * b, "y")
+
+
+def _check_norm_dx(dy, x, gamma, mean, rstd, dx):
+    """The bounds of test_layer_norm."""
+    H = x.shape[1]
+    xh = (x.double() - mean.double()[:, None]).abs() * rstd.double()[:, None]
+    t = dy.double().abs() * (1.0 if gamma is None else gamma.double().abs())
+    b = rstd.double()[:, None] * (4 * P.EPS32 * t + (H + 4) * P.EPS32 * t.mean(1, keepdim=True) +
+                                  (H + 8) * P.EPS32 * xh * (t * xh).mean(1, keepdim=True))
+    P.assert_within(dx, P.norm_bwd(dy, x, gamma, mean, rstd)[0], b, "dx")
+
+
+# aligned 16-bit forward: rows run ahead in shared memory from 48 rows an SM and H > 2048 on; one, two and four packs a
+# thread, the last CTA's rows even and odd in number
+@pytest.mark.parametrize("more", [-1, 0, 1, 333])
+@pytest.mark.parametrize("H", [2048, 2056, 2880, 4096, 4104, 8192, 8200, 16384])
+@pytest.mark.parametrize("dtype,wdtype", [(BF16, F32), (F16, F16)])
+def test_layer_norm_forward_of_a_training_batch(more, H, dtype, wdtype):
+    cuda_device()
+    T, g = _rows(48, more), _gen(H + more)
+    x = _randn(g, T, H, dtype=dtype, std=2.0) + 0.5
+    gamma, beta = (_randn(g, H) * 0.3 + 1).to(wdtype), _randn(g, H).to(wdtype)
+    y, ybuf = P.strided(torch.zeros(T, H, dtype=dtype, device="cuda"), 8)
+    mean, rstd = torch.empty(T, device="cuda"), torch.empty(T, device="cuda")
+    m.moe_layer_norm_forward(x, gamma, beta, 1e-5, y, mean, rstd)
+    _check_norm_forward(x, gamma, beta, 1e-5, y, mean, rstd)
+    _canary(ybuf, H, "y")
+    y2 = torch.empty(T, H, dtype=dtype, device="cuda")
+    m.moe_layer_norm_forward(x, gamma, beta, 1e-5, y2)
+    assert torch.equal(y2, y)
+
+
+# off a boundary: fp32 forward runs rows ahead from 4 rows an SM on, any backward from half a row an SM on
+@pytest.mark.parametrize("per_sm,more", [(0, 40), (1, 1), (4, -1), (4, 1), (9, 5)])
+@pytest.mark.parametrize("H,lead", [(301, 1), (1031, 3), (520, 1), (4099, 2), (2881, 3)])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_layer_norm_of_tensors_off_a_boundary(per_sm, more, H, lead, dtype):
+    """Tensors that begin and end inside 16-byte units: their neighbours in memory are NaN, stay unread and unwritten."""
+    cuda_device()
+    T, g = _rows(per_sm, more), _gen(H + more)
+
+    def inside(std):
+        buf = torch.full((T * H + 16,), NAN, dtype=dtype, device="cuda")
+        t = buf[lead:lead + T * H].view(T, H)
+        t.copy_(_randn(g, T, H, std=std))
+        return t, buf
+
+    def untouched(buf, what):
+        assert bool(torch.isnan(buf[:lead]).all()) and bool(torch.isnan(buf[lead + T * H:]).all()), what
+
+    (x, _), (dy, _), (y, ybuf), (dx, dxbuf) = inside(2.0), inside(1.0), inside(0.0), inside(0.0)
+    gamma, beta = _randn(g, H) * 0.3 + 1, _randn(g, H)
+    mean, rstd = torch.empty(T, device="cuda"), torch.empty(T, device="cuda")
+    m.moe_layer_norm_forward(x, gamma, beta, 1e-5, y, mean, rstd)
+    _check_norm_forward(x, gamma, beta, 1e-5, y, mean, rstd)
+    dgamma, dbeta = torch.full_like(gamma, NAN), torch.full_like(beta, NAN)
+    ws = torch.empty(m.moe_layer_norm_workspace_size(T, H), dtype=torch.uint8, device="cuda")
+    m.moe_layer_norm_backward(dy, x, gamma, mean, rstd, dx, dgamma, dbeta, ws)
+    _check_norm_dx(dy, x, gamma, mean, rstd, dx)
+    _, rdg, rdb = P.norm_bwd(dy, x, gamma, mean, rstd)
+    xh = (x.double() - mean.double()[:, None]).abs() * rstd.double()[:, None]
+    P.assert_within(dgamma, rdg, (T + 4) * P.EPS32 * (dy.double().abs() * xh).sum(0), "dgamma")
+    P.assert_within(dbeta, rdb, (T + 4) * P.EPS32 * dy.double().abs().sum(0), "dbeta")
+    untouched(ybuf, "y")
+    untouched(dxbuf, "dx")
+
+
+# odd alignments, a warp a row from 96 rows an SM on: rows of two blocks (two quarter-warps a row), of three (one, three
+# rounds), of four and of sixteen (four quarter-warps a row)
+@pytest.mark.parametrize("more", [-1, 1])
+@pytest.mark.parametrize("I,act,dtype,pad", [(129, "swiglu", BF16, 0), (255, "srelu", F16, 8), (200, "geglu", BF16, 3),
+                                             (383, "swiglu", F16, 0), (511, "swiglu_clamp", BF16, 0),
+                                             (512, "swiglu", F16, 3), (2047, "swiglu", BF16, 0)])
+def test_activation_checkpoint_a_warp_a_row(more, I, act, dtype, pad):
+    test_activation_checkpoint(_rows(96, more), I, act, dtype, pad)
+
+
+def _needs_gb(n):
+    cuda_device()
+    torch.cuda.empty_cache()
+    if torch.cuda.mem_get_info()[0] < n << 30:
+        pytest.skip(f"needs {n} GB")
+
+
+@pytest.mark.parametrize("H", [2880, 2881])
+def test_layer_norm_elements_past_32_bits(H):
+    """More than 2^31 elements: the last rows, and the sums over all rows."""
+    _needs_gb(40)
+    g, T, L = _gen(H), 2 ** 31 // H + 3001, 70
+    x = torch.empty(T, H, dtype=BF16, device="cuda").normal_(generator=g)
+    gamma, beta = _randn(g, H), _randn(g, H)
+    y, mean, rstd = torch.empty_like(x), torch.empty(T, device="cuda"), torch.empty(T, device="cuda")
+    m.moe_layer_norm_forward(x, gamma, beta, 1e-5, y, mean, rstd)
+    _check_norm_forward(x[-L:], gamma, beta, 1e-5, y[-L:], mean[-L:], rstd[-L:])
+    dx, dgamma, dbeta = torch.empty_like(x), torch.empty_like(gamma), torch.empty_like(beta)
+    ws = torch.empty(m.moe_layer_norm_workspace_size(T, H), dtype=torch.uint8, device="cuda")
+    m.moe_layer_norm_backward(y, x, gamma, mean, rstd, dx, dgamma, dbeta, ws)
+    _check_norm_dx(y[-L:], x[-L:], gamma, mean[-L:], rstd[-L:], dx[-L:])
+    ref = [torch.zeros(H, dtype=torch.float64, device="cuda") for _ in range(4)]
+    for a in range(0, T, 50000):
+        d = y[a:a + 50000].double()
+        xh = (x[a:a + 50000].double() - mean[a:a + 50000, None]) * rstd[a:a + 50000, None]
+        for r, v in zip(ref, (d * xh, d, (d * xh).abs(), d.abs())):
+            r += v.sum(0)
+    P.assert_within(dgamma, ref[0], (T + 4) * P.EPS32 * ref[2], "dgamma")
+    P.assert_within(dbeta, ref[1], (T + 4) * P.EPS32 * ref[3], "dbeta")
+
+
+def test_weight_gradient_elements_past_32_bits():
+    """More than 2^31 elements of rows, and of gradients."""
+    _needs_gb(30)
+    g = _gen(41)
+    N, K = 64, 5776
+    R = 2 ** 31 // K + 1001
+    off, offsets = _offsets([R - 3000, 0, 3000])
+    dy, x = _randn(g, R, N, dtype=BF16), torch.empty(R, K, dtype=BF16, device="cuda").normal_(generator=g)
+    dw = torch.full((3, N, K), NAN, device="cuda")
+    m.moe_grouped_mm_wgrad(dy, x, offsets, dw, _workspace(m.MOE_MM_WGRAD, R, N, K, 3))
+    ref, mag = P.grouped_wgrad(dy[-3000:], x[-3000:], [0, 3000])
+    P.assert_within(dw[2], ref[0], (3000 + 4) * P.EPS32 * mag[0], "last group")
+    assert bool((dw[1] == 0).all())
+    ref, mag = torch.zeros(N, K, dtype=torch.float64, device="cuda"), torch.zeros(N, K, dtype=torch.float64, device="cuda")
+    for a in range(0, R - 3000, 50000):
+        s = slice(a, min(a + 50000, R - 3000))
+        r, v = P.grouped_wgrad(dy[s], x[s], [0, s.stop - s.start])
+        ref += r[0]
+        mag += v[0]
+    P.assert_within(dw[0], ref, (R + 4) * P.EPS32 * mag, "first group")
+    del x, dw
+    N = K = 5632
+    G = 2 ** 31 // (N * K) + 2
+    off, offsets = _offsets([5] * G)
+    dy, x = _randn(g, 5 * G, N, dtype=BF16), _randn(g, 5 * G, K, dtype=BF16)
+    dw = torch.empty(G, N, K, dtype=BF16, device="cuda")
+    m.moe_grouped_mm_wgrad(dy, x, offsets, dw, _workspace(m.MOE_MM_WGRAD, 5 * G, N, K, G))
+    ref, mag = P.grouped_wgrad(dy[-5:], x[-5:], [0, 5])
+    P.assert_within(dw[-1], ref[0], 9 * P.EPS32 * mag[0], "last gradient")
+
+
+def test_fp8_elements_past_32_bits():
+    """More than 2^31 elements of weights, with their transposed copy, and of rows: the quantisers and the products."""
+    _needs_gb(30)
+    g = _gen(42)
+    N, K = 5640, 5632
+    G = 2 ** 31 // (N * K) + 2
+    w = torch.empty(G, N, K, dtype=BF16, device="cuda").normal_(0.0, 0.05, generator=g)
+    nb, kb = -(-N // 128), -(-K // 128)
+    q, s = torch.empty(G, N, K, dtype=E4M3, device="cuda"), torch.empty(G, nb, kb, device="cuda")
+    ld = -(-N // 16) * 16
+    qt = torch.zeros(G, K, ld, dtype=E4M3, device="cuda")[:, :, :N]
+    st = torch.empty(G, kb, nb, device="cuda")
+    m.moe_fp8_quant_weights(w, q, s, qt, st)
+    q1, s1 = torch.empty(1, N, K, dtype=E4M3, device="cuda"), torch.empty(1, nb, kb, device="cuda")
+    m.moe_fp8_quant_weights(w[-1:].clone(), q1, s1)
+    assert torch.equal(q[-1:].view(torch.uint8), q1.view(torch.uint8)) and torch.equal(s[-1:], s1)
+    assert torch.equal(qt[-1].view(torch.uint8), q1[0].view(torch.uint8).t()) and torch.equal(st[-1], s1[0].t())
+    del w
+    R = 300
+    off, offsets = _offsets([0] * (G - 1) + [R])
+    x = _randn(g, R, K, dtype=BF16)
+    xq, xs = torch.empty(R, K, dtype=E4M3, device="cuda"), torch.empty(R, kb, device="cuda")
+    m.moe_fp8_quant_rows(x, xq, xs)
+
+    def value(q, s):
+        return P.decode(q) * s.double().repeat_interleave(128, 1)[:, :q.shape[1]]
+
+    def weight(q, s):
+        return P.decode(q) * s.double().repeat_interleave(128, 0)[:q.shape[0]].repeat_interleave(128, 1)[:, :q.shape[1]]
+
+    out = torch.empty(R, N, device="cuda")
+    m.moe_fp8_mm(xq, xs, q, s, out, _workspace(m.MOE_MM_FP8, R, N, K, G), offsets=offsets)
+    ref, mag = P.grouped(value(xq, xs), weight(q[-1], s[-1])[None], [0, R])
+    P.assert_within(out, ref, (K + 8) * P.EPS32 * mag, "the last group's weights")
+    del q, qt
+    N, L = 64, 70
+    R = 2 ** 31 // K + 301
+    xq = torch.randint(0, 0x7F, (R, K), dtype=torch.uint8, device="cuda", generator=g).view(E4M3)
+    xs = torch.rand(R, kb, device="cuda", generator=g)
+    wq, ws = q1[:, :N].contiguous(), s1[:, :1].contiguous()
+    out = torch.empty(R, N, device="cuda")
+    m.moe_fp8_mm(xq, xs, wq, ws, out, _workspace(m.MOE_MM_FP8, R, N, K, 1))
+    ref, mag = P.grouped(value(xq[-L:], xs[-L:]), weight(wq[0], ws[0])[None], [0, L])
+    P.assert_within(out[-L:], ref, (K + 8) * P.EPS32 * mag, "the last rows")
