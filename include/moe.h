@@ -417,8 +417,9 @@ moe_status_t moe_layer_backward(const moe_config_t* cfg, const uint16_t* dout, c
  * pointer is aligned to its elements (16-byte rows take the wide-access
  * path). Sums and statistics are fp32; each result is rounded once. None of
  * these calls uses an atomic for a result: the same inputs give the same bits.
- * Sizes are any positive number; zero rows are legal and launch nothing that
- * reads. Overlapping inputs and outputs are not. */
+ * Sizes are any positive number, row lengths (and the weights' N and K) up to
+ * 2^30; zero rows are legal and launch nothing that reads. Overlapping inputs
+ * and outputs are not. */
 enum { MOE_DT_BF16 = 0, MOE_DT_F16 = 1, MOE_DT_F32 = 2 };
 
 /* Layer norm of T rows of H: mu and v the mean and (biased) variance of a

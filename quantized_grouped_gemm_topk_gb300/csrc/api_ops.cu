@@ -23,10 +23,12 @@ bool act_ok(int act, float limit) {
 }
 int64_t blocks_of(int64_t n) { return (n + kQBlock - 1) / kQBlock; }
 
-// Sizes up to 2^30 leave room to round up to whole tiles in 32 bits.
+// Sizes up to 2^30 leave room to round up to whole tiles and blocks, and to
+// step past the end, in 32 bits.
+constexpr int kMost = 1 << 30;
+bool width_ok(int n) { return n >= 1 && n <= kMost; }
 bool mm_sizes_ok(int R, int N, int K, int G) {
-  constexpr int kMost = 1 << 30;
-  return R >= 0 && R <= kMost && N >= 1 && N <= kMost && K >= 1 && K <= kMost && G >= 1 && G <= 2048;
+  return R >= 0 && R <= kMost && width_ok(N) && width_ok(K) && G >= 1 && G <= 2048;
 }
 
 // Common checks of a product's sizes and workspace.
@@ -50,7 +52,7 @@ void mm_workspace(MmArgs& a, int kind, void* ws) {
 extern "C" {
 
 moe_status_t moe_layer_norm_workspace_size(int64_t T, int H, size_t* bytes) {
-  if (T < 0 || H < 1 || !bytes) return MOE_ERR_INVALID_ARG;
+  if (T < 0 || !width_ok(H) || !bytes) return MOE_ERR_INVALID_ARG;
   *bytes = (size_t)std::min<int64_t>(T, kNormMaxParts) * 2 * (size_t)H * 4;
   return MOE_OK;
 }
@@ -58,7 +60,7 @@ moe_status_t moe_layer_norm_workspace_size(int64_t T, int H, size_t* bytes) {
 moe_status_t moe_layer_norm_forward(const void* x, int64_t ldx, const void* gamma, const void* beta, float eps,
                                     int64_t T, int H, int dtype, int wdtype, void* y, int64_t ldy, float* mean,
                                     float* rstd, void* stream) {
-  if (T < 0 || H < 1 || !is_float(dtype) || (wdtype != MOE_DT_F32 && wdtype != dtype)) return MOE_ERR_INVALID_ARG;
+  if (T < 0 || !width_ok(H) || !is_float(dtype) || (wdtype != MOE_DT_F32 && wdtype != dtype)) return MOE_ERR_INVALID_ARG;
   if (ldx < H || ldy < H || !(eps >= 0.f)) return MOE_ERR_INVALID_ARG;
   const size_t e = size_of(dtype), we = size_of(wdtype);
   if (!maybe(gamma, we) || !maybe(beta, we) || !maybe(mean, 4) || !maybe(rstd, 4)) return MOE_ERR_INVALID_ARG;
@@ -75,7 +77,7 @@ moe_status_t moe_layer_norm_backward(const void* dy, int64_t lddy, const void* x
                                      const float* mean, const float* rstd, int64_t T, int H, int dtype, int wdtype,
                                      void* dx, int64_t lddx, void* dgamma, void* dbeta, void* ws, size_t ws_bytes,
                                      void* stream) {
-  if (T < 0 || H < 1 || !is_float(dtype) || (wdtype != MOE_DT_F32 && wdtype != dtype)) return MOE_ERR_INVALID_ARG;
+  if (T < 0 || !width_ok(H) || !is_float(dtype) || (wdtype != MOE_DT_F32 && wdtype != dtype)) return MOE_ERR_INVALID_ARG;
   if (lddy < H || ldx < H || lddx < H) return MOE_ERR_INVALID_ARG;
   const size_t e = size_of(dtype), we = size_of(wdtype);
   if (!maybe(gamma, we) || !maybe(dgamma, we) || !maybe(dbeta, we)) return MOE_ERR_INVALID_ARG;
@@ -105,7 +107,7 @@ moe_status_t moe_layer_norm_backward(const void* dy, int64_t lddy, const void* x
 moe_status_t moe_act_ckpt_forward(const void* h, int64_t ldh, const float* w_row, int64_t R, int I, int dtype,
                                   int act, float alpha, float limit, void* y, int64_t ldy, uint8_t* q, int64_t ldq,
                                   float* s, void* stream) {
-  if (R < 0 || I < 1 || !is16(dtype) || !act_ok(act, limit)) return MOE_ERR_INVALID_ARG;
+  if (R < 0 || !width_ok(I) || !is16(dtype) || !act_ok(act, limit)) return MOE_ERR_INVALID_ARG;
   const int64_t width = (int64_t)I * (act == MOE_ACT_SRELU ? 1 : 2);
   if (width > INT32_MAX || ldh < width || ldq < width || ldy < I || !maybe(w_row, 4)) return MOE_ERR_INVALID_ARG;
   reset_launch_count();
@@ -120,7 +122,7 @@ moe_status_t moe_act_ckpt_forward(const void* h, int64_t ldh, const float* w_row
 moe_status_t moe_act_ckpt_backward(const void* dy, int64_t lddy, const uint8_t* q, int64_t ldq, const float* s,
                                    const float* w_row, int64_t R, int I, int dtype, int act, float alpha, float limit,
                                    void* dh, int64_t lddh, float* dw_row, void* y, int64_t ldy, void* stream) {
-  if (R < 0 || I < 1 || !is16(dtype) || !act_ok(act, limit)) return MOE_ERR_INVALID_ARG;
+  if (R < 0 || !width_ok(I) || !is16(dtype) || !act_ok(act, limit)) return MOE_ERR_INVALID_ARG;
   const int64_t width = (int64_t)I * (act == MOE_ACT_SRELU ? 1 : 2);
   if (width > INT32_MAX || lddh < width || ldq < width || lddy < I || (y && ldy < I)) return MOE_ERR_INVALID_ARG;
   if (!maybe(w_row, 4) || !maybe(dw_row, 4) || !maybe(y, 2)) return MOE_ERR_INVALID_ARG;
@@ -136,7 +138,7 @@ moe_status_t moe_act_ckpt_backward(const void* dy, int64_t lddy, const uint8_t* 
 
 moe_status_t moe_fp8_quant_rows(const void* x, int64_t ldx, int64_t R, int C, int dtype, uint8_t* q, int64_t ldq,
                                 float* s, int64_t lds, void* stream) {
-  if (R < 0 || C < 1 || !is_float(dtype) || ldx < C || ldq < C || lds < blocks_of(C)) return MOE_ERR_INVALID_ARG;
+  if (R < 0 || !width_ok(C) || !is_float(dtype) || ldx < C || ldq < C || lds < blocks_of(C)) return MOE_ERR_INVALID_ARG;
   reset_launch_count();
   if (R == 0) return MOE_OK;
   if (!have(x, size_of(dtype)) || !q || !have(s, 4)) return MOE_ERR_INVALID_ARG;
@@ -147,7 +149,7 @@ moe_status_t moe_fp8_quant_rows(const void* x, int64_t ldx, int64_t R, int C, in
 moe_status_t moe_fp8_quant_weights(const void* w, int64_t w_group, int64_t ldw, int G, int N, int K, int dtype,
                                    uint8_t* q, int64_t q_group, int64_t ldq, float* s, uint8_t* qt, int64_t qt_group,
                                    int64_t ldqt, float* st, void* stream) {
-  if (G < 1 || N < 1 || K < 1 || !is_float(dtype) || ldw < K || ldq < K) return MOE_ERR_INVALID_ARG;
+  if (G < 1 || !width_ok(N) || !width_ok(K) || !is_float(dtype) || ldw < K || ldq < K) return MOE_ERR_INVALID_ARG;
   if (G > 1 && (w_group < (int64_t)N * ldw || q_group < (int64_t)N * ldq)) return MOE_ERR_INVALID_ARG;
   if (!have(w, size_of(dtype)) || !q || !have(s, 4)) return MOE_ERR_INVALID_ARG;
   if ((qt != nullptr) != (st != nullptr) || !maybe(st, 4)) return MOE_ERR_INVALID_ARG;

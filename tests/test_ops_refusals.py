@@ -176,3 +176,21 @@ def test_tensors_that_do_not_fit_are_refused(lib, monkeypatch):
     cpu = torch.zeros(4, 64, dtype=bf)
     with pytest.raises(ValueError, match="device"):
         m.moe_layer_norm_forward(cpu, None, None, 1e-5, cpu)
+
+
+BIG = 2 ** 30 + 1       # one past the longest row; 2^31 - 100: rounding up to a block of 128 leaves 32 bits
+
+
+@pytest.mark.parametrize("n", [BIG, 2 ** 31 - 100])
+def test_rows_too_long(lib, n):
+    """Refused like the products' sizes: the kernels round up to blocks and step past the end in 32 bits."""
+    wide = dict(ldx=n, ldy=n)
+    assert _call(lib.moe_layer_norm_forward, NORM_F, H=n, **wide) == INVALID
+    assert _call(lib.moe_layer_norm_backward, NORM_B, H=n, lddy=n, ldx=n, lddx=n, ws_bytes=1 << 40) == INVALID
+    need = ctypes.c_size_t()
+    assert lib.moe_layer_norm_workspace_size(4, n, ctypes.byref(need)) == INVALID
+    assert _call(lib.moe_act_ckpt_forward, CKPT_F, act=3, I=n, ldh=n, ldy=n, ldq=n) == INVALID
+    assert _call(lib.moe_act_ckpt_backward, CKPT_B, act=3, I=n, lddy=n, ldq=n, lddh=n) == INVALID
+    assert _call(lib.moe_fp8_quant_rows, QR, C=n, ldx=n, ldq=n, lds=n) == INVALID
+    assert _call(lib.moe_fp8_quant_weights, QW, K=n, ldw=n, ldq=n, wg=64 * n, qg=64 * n, qtg=64 * n) == INVALID
+    assert _call(lib.moe_fp8_quant_weights, QW, N=n, ldqt=n, wg=64 * n, qg=64 * n, qtg=64 * n) == INVALID
