@@ -4,9 +4,11 @@ The block is  out = experts(norm(x)) + norm(x) . Wp^T : a layer norm, top-k
 routing and dispatch, the experts' two grouped products with SwiGLU between
 them, the combine, and next to the experts an always-on FP8 projection with a
 scale for each block of 128. The backward pass recomputes the experts'
-activation from its 8-bit checkpoint. Every step runs in the library's
-kernels; PyTorch holds the memory, gathers rows by index and applies the
-update.
+activation from its 8-bit checkpoint, and the router is trained through the
+routing weights. The products, the norm, the activation and the routing run in
+the library's kernels; PyTorch holds the memory, gathers rows by index, takes
+the routing weights back to the router (as the layer's backward, which leaves
+the router's two dense products to its caller) and applies the update.
 
     python examples/train_block.py [--steps 30] [--tokens 2048] [--hidden 1024]
 """
@@ -87,8 +89,10 @@ class Block:
         self.saved = (x, xn, mean, rstd, v, src, xg, q, s, wtq, wtsc)
         return out + p
 
-    def backward(self, dout):
-        """Gradients of sum(dout * forward(x)) by name; the routing weights' gradient is dw_row (by dispatched row)."""
+    def backward(self, dout, router=False):
+        """Gradients of L = sum(dout * forward(x)) by name. The routing weights count as constants, and dw_row is L's
+        gradient by them (by dispatched row); with router=True they are functions of x and of the router (the choice of
+        experts stays fixed): "router" is returned too, and x, gamma and beta include that path."""
         x, xn, mean, rstd, v, src, xg, q, s, wtq, wtsc = self.saved
         T, H, I, R, off = self.T, self.H, self.I, self.R, v["offsets"]
         dz = dout.index_select(0, src)
@@ -108,12 +112,25 @@ class Block:
         m.moe_grouped_mm_wgrad(dout, xn, self.all_rows, dwp, self.mm_ws)
 
         dx, dgamma, dbeta = torch.empty_like(x), torch.empty_like(self.gamma), torch.empty_like(self.beta)
-        m.moe_layer_norm_backward(dxn + dp, x, self.gamma, mean, rstd, dx, dgamma, dbeta, self.norm_ws)
-        return {"x": dx, "gamma": dgamma, "beta": dbeta, "w1": dw1, "w2": dw2, "wp": dwp, "dw_row": dw_row}
+        grads = {"x": dx, "gamma": dgamma, "beta": dbeta, "w1": dw1, "w2": dw2, "wp": dwp, "dw_row": dw_row}
+        dxn = dxn + dp
+        if router:
+            dlogits = self._dlogits(v, dw_row)
+            grads["router"] = xn.float().t() @ dlogits
+            dxn = (dxn.float() + dlogits @ self.router.t()).bfloat16()
+        m.moe_layer_norm_backward(dxn, x, self.gamma, mean, rstd, dx, dgamma, dbeta, self.norm_ws)
+        return grads
+
+    def _dlogits(self, v, dw_row):
+        """The routing weights are the softmax p of a token's chosen logits: d logit_j = p_j (d p_j - sum_i p_i d p_i)."""
+        p, dp = v["topk_w"], dw_row[v["inv"].long()].view(self.T, self.k)
+        d = p * (dp - (p * dp).sum(1, keepdim=True))
+        return torch.zeros(self.T, self.E, device=d.device).scatter_(1, v["topk_ids"].long(), d)
 
     def step(self, grads, lr):
-        for name in ("gamma", "beta", "w1", "w2", "wp"):
-            getattr(self, name).add_(grads[name], alpha=-lr)
+        for name in ("gamma", "beta", "router", "w1", "w2", "wp"):
+            if name in grads:
+                getattr(self, name).add_(grads[name], alpha=-lr)
 
 
 def train(steps=30, tokens=2048, hidden=1024, inner=512, experts=16, k=4, lr=0.1, seed=0):
@@ -127,7 +144,7 @@ def train(steps=30, tokens=2048, hidden=1024, inner=512, experts=16, k=4, lr=0.1
     for _ in range(steps):
         err = block.forward(x).float() - target
         losses.append(float(err.square().mean()))
-        block.step(block.backward((err * (2.0 / tokens)).bfloat16()), lr)
+        block.step(block.backward((err * (2.0 / tokens)).bfloat16(), router=True), lr)
     status = m.moe_mm_read_status(block.mm_ws) | m.moe_read_status(block.cfg, block.ws)
     if status:
         raise RuntimeError(f"device status {status:#x}")
