@@ -97,6 +97,11 @@ __device__ __forceinline__ void f_unit(const MmArgs& m, int n_tiles, const int32
 // ones; the MMA's other rows are an earlier stage's bytes and are not stored.
 __device__ __forceinline__ int f_a_box(int rows) { return rows <= 16 ? 0 : rows <= 32 ? 1 : rows <= 64 ? 2 : 3; }
 
+// Neither zero nor subnormal, infinite or NaN.
+__device__ __forceinline__ bool normal(float v) {
+  return (__float_as_uint(v) & 0x7fffffffu) - 0x00800000u < 0x7f000000u;
+}
+
 template <int BN>
 __global__ void __launch_bounds__(kFThreads, 1) k_gemm_fp8(const FArgs g, const __grid_constant__ FMaps maps) {
   using C = FCfg<BN>;
@@ -271,12 +276,46 @@ __global__ void __launch_bounds__(kFThreads, 1) k_gemm_fp8(const FArgs g, const 
       float acc[kCols];
 #pragma unroll
       for (int i = 0; i < kCols; ++i) acc[i] = 0.f;
+      // acc += f1 x (TWICE: f0 x) the block's sums, and the slot is released
+      auto add_block = [&](auto twice, float f0, float f1) {
+        const uint32_t at = lanes + ts * BN;
+        // chunk c + 1 is read while chunk c is added
+        uint32_t v[2][16];
+        tc::tmem_ld16(at, v[0]);
+#pragma unroll
+        for (int c = 0; c < kChunks; ++c) {
+          tc::tmem_wait_ld();
+          if (c + 1 < kChunks) {
+            tc::tmem_ld16(at + 16 * (c + 1), v[(c + 1) & 1]);
+          } else {
+            tc::fence_before_sync();
+            __syncwarp();
+            if (lane == 0) tc::bar_arrive(hempty + 8 * ts);
+          }
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const float x = __uint_as_float(v[c & 1][i]);
+            acc[c * 16 + i] = fmaf(decltype(twice)::value ? x * f0 : x, f1, acc[c * 16 + i]);
+          }
+        }
+      };
+      // Scales whose product leaves fp32's normal range though its product with
+      // the sum need not (0 x inf would be NaN, a subnormal would cut digits):
+      // one after the other, the intermediate in range, by the smaller first
+      // where the product is large and by the larger where it is small. Other
+      // rows of the warp keep their bits.
+      auto add_odd_block = [&](float a, float b) {
+        const float sc = a * b;
+        const bool a_first = (fabsf(a) > fabsf(b)) != (fabsf(sc) > 1.f), one = normal(sc);
+        add_block(std::true_type(), one ? 1.f : a_first ? a : b, one ? sc : a_first ? b : a);
+      };
       for (int kb0 = w.k0; kb0 < w.k1; kb0 += 4) {
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           const int kb = kb0 + j;
           if (kb < w.k1 && ok) {
             const float sc = s[j] * t[j];
+            const bool odd = __any_sync(kFull, !normal(sc));
             if (kb + 4 < w.k1) {
               s[j] = xs[kb + 4];
               t[j] = ws[kb + 4];
@@ -284,24 +323,8 @@ __global__ void __launch_bounds__(kFThreads, 1) k_gemm_fp8(const FArgs g, const 
             ok = __all_sync(kFull, tc::bar_wait_inline(hfull + 8 * ts, tphase, abort));
             if (ok) {
               tc::fence_after_sync();
-              const uint32_t at = lanes + ts * BN;
-              // chunk c + 1 is read while chunk c is added
-              uint32_t v[2][16];
-              tc::tmem_ld16(at, v[0]);
-#pragma unroll
-              for (int c = 0; c < kChunks; ++c) {
-                tc::tmem_wait_ld();
-                if (c + 1 < kChunks) {
-                  tc::tmem_ld16(at + 16 * (c + 1), v[(c + 1) & 1]);
-                } else {
-                  tc::fence_before_sync();
-                  __syncwarp();
-                  if (lane == 0) tc::bar_arrive(hempty + 8 * ts);
-                }
-#pragma unroll
-                for (int i = 0; i < 16; ++i)
-                  acc[c * 16 + i] = fmaf(__uint_as_float(v[c & 1][i]), sc, acc[c * 16 + i]);
-              }
+              if (!odd) add_block(std::false_type(), 1.f, sc);
+              else add_odd_block(xs[kb], ws[kb]);
               if (++ts == C::kSlots) {
                 ts = 0;
                 tphase ^= 1;

@@ -756,6 +756,36 @@ def test_elements_past_32_bits():
     assert torch.equal(xq[-L:].view(torch.uint8), xq2.view(torch.uint8)) and torch.equal(xs[-L:], xs2)
 
 
+@pytest.mark.parametrize("R,N,K", [(70, 200, 700), (600, 1100, 640), (2500, 2100, 700)])
+@pytest.mark.parametrize("swap", [False, True])
+def test_fp8_mm_scales_whose_product_leaves_fp32(R, N, K, swap):
+    """Two scales whose product overflows, over a block of zeros, and two whose product is subnormal, over a block whose
+    sum times them is not. The other rows keep their bits."""
+    cuda_device()
+    g = _gen(R)
+    kb, nb = -(-K // 128), -(-N // 128)
+    big, less, small, tiny = (1e4, 1e35, 1e-16, 1e-27) if swap else (1e35, 1e4, 1e-27, 1e-16)
+    xq, _ = P.strided(_randn(g, R, K, std=100.0).abs().clamp(max=448.0).to(E4M3), 0, whole=16)
+    wq, _ = P.strided(_randn(g, 1, N, K, std=100.0).abs().clamp(max=448.0).to(E4M3), 0, whole=16)
+    xs, wsc = torch.rand(R, kb, generator=g, device="cuda") + 0.5, torch.rand(1, nb, kb, generator=g, device="cuda") + 0.5
+    wq[:, :, 128:256] = 0
+    wsc[:, :, 1] = less
+    wsc[:, -1] = tiny
+    wsc[:, -1, 1] = less
+    plain = xs.clone()
+    xs[::3, 1] = big                  # next to ordinary blocks
+    xs[1::3] *= small                 # every block of the row
+    out, out2 = torch.empty(R, N, device="cuda"), torch.empty(R, N, device="cuda")
+    ws = _workspace(m.MOE_MM_FP8, R, N, K, 1)
+    m.moe_fp8_mm(xq, xs, wq, wsc, out, ws)
+    m.moe_fp8_mm(xq, plain, wq, wsc, out2, ws)
+    x64 = P.decode(xq) * xs.double().repeat_interleave(128, 1)[:, :K]
+    w64 = P.decode(wq) * wsc.double().repeat_interleave(128, 1)[:, :N].repeat_interleave(128, 2)[:, :, :K]
+    ref, mag = P.grouped(x64, w64, [0, R])
+    P.assert_within(out, ref, (K + 8) * P.EPS32 * mag, "out")
+    assert torch.equal(out[2::3], out2[2::3])
+    assert torch.equal(out[::3, :(nb - 1) * 128], out2[::3, :(nb - 1) * 128])
+
 # ---- both sides of the rules that pick a kernel ------------------------------------------
 # Sizes in rows an SM, as the rules count them, so that they follow the machine.
 def _rows(per_sm, more):
