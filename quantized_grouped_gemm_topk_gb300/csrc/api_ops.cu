@@ -31,6 +31,10 @@ bool mm_sizes_ok(int R, int N, int K, int G) {
   return R >= 0 && R <= kMost && width_ok(N) && width_ok(K) && G >= 1 && G <= 2048;
 }
 
+// Elements from the first to the last of a rows x cols matrix with row stride
+// ld: the least a group's stride may be.
+int64_t span(int rows, int cols, int64_t ld) { return (int64_t)(rows - 1) * ld + cols; }
+
 // Common checks of a product's sizes and workspace.
 moe_status_t mm_check(int kind, int R, int N, int K, int G, const int32_t* offsets, void* ws, size_t ws_bytes) {
   if (!mm_sizes_ok(R, N, K, G)) return MOE_ERR_INVALID_ARG;
@@ -150,10 +154,10 @@ moe_status_t moe_fp8_quant_weights(const void* w, int64_t w_group, int64_t ldw, 
                                    uint8_t* q, int64_t q_group, int64_t ldq, float* s, uint8_t* qt, int64_t qt_group,
                                    int64_t ldqt, float* st, void* stream) {
   if (G < 1 || !width_ok(N) || !width_ok(K) || !is_float(dtype) || ldw < K || ldq < K) return MOE_ERR_INVALID_ARG;
-  if (G > 1 && (w_group < (int64_t)N * ldw || q_group < (int64_t)N * ldq)) return MOE_ERR_INVALID_ARG;
+  if (G > 1 && (w_group < span(N, K, ldw) || q_group < span(N, K, ldq))) return MOE_ERR_INVALID_ARG;
   if (!have(w, size_of(dtype)) || !q || !have(s, 4)) return MOE_ERR_INVALID_ARG;
   if ((qt != nullptr) != (st != nullptr) || !maybe(st, 4)) return MOE_ERR_INVALID_ARG;
-  if (qt && (ldqt < N || (G > 1 && qt_group < (int64_t)K * ldqt))) return MOE_ERR_INVALID_ARG;
+  if (qt && (ldqt < N || (G > 1 && qt_group < span(K, N, ldqt)))) return MOE_ERR_INVALID_ARG;
   reset_launch_count();
   const QuantWeightsArgs a = {w, w_group, ldw, G, N, K, dtype, q, q_group, ldq, s, qt, qt_group, ldqt, st};
   return done(launch_quant128_weights(a, (cudaStream_t)stream));
@@ -176,7 +180,7 @@ moe_status_t moe_grouped_mm(const void* x, int64_t ldx, const void* w, int64_t w
   const int wr = trans_w ? K : N, wc = trans_w ? N : K;      // rows and row length of a group's matrix
   if (!is16(dtype) || (out_dtype != dtype && out_dtype != MOE_DT_F32)) return MOE_ERR_INVALID_ARG;
   if ((trans_w != 0 && trans_w != 1) || ldx < K || ldw < wc || ldo < N) return MOE_ERR_INVALID_ARG;
-  if (G > 1 && w_group < (int64_t)(wr - 1) * ldw + wc) return MOE_ERR_INVALID_ARG;
+  if (G > 1 && w_group < span(wr, wc, ldw)) return MOE_ERR_INVALID_ARG;
   // rows and groups start on 16 bytes: the tensor copies' rule
   if (!have(w, 16) || ldw % 8 || ldx % 8 || (G > 1 && w_group % 8)) return MOE_ERR_INVALID_ARG;
   reset_launch_count();
@@ -196,7 +200,7 @@ moe_status_t moe_grouped_mm_wgrad(const void* dy, int64_t lddy, const void* x, i
   moe_status_t s = mm_check(MOE_MM_WGRAD, R, N, K, G, offsets, ws, ws_bytes);
   if (s != MOE_OK) return s;
   if (!is16(dtype) || (out_dtype != dtype && out_dtype != MOE_DT_F32)) return MOE_ERR_INVALID_ARG;
-  if (lddy < N || ldx < K || lddw < K || (G > 1 && dw_group < (int64_t)(N - 1) * lddw + K)) return MOE_ERR_INVALID_ARG;
+  if (lddy < N || ldx < K || lddw < K || (G > 1 && dw_group < span(N, K, lddw))) return MOE_ERR_INVALID_ARG;
   if (lddy % 8 || ldx % 8 || !have(dw, size_of(out_dtype))) return MOE_ERR_INVALID_ARG;
   // no rows: the kernel writes zeros and reads neither
   if (R > 0 ? !have(dy, 16) || !have(x, 16) : !maybe(dy, 16) || !maybe(x, 16)) return MOE_ERR_INVALID_ARG;
@@ -215,7 +219,7 @@ moe_status_t moe_fp8_mm(const uint8_t* xq, int64_t ldx, const float* xs, int64_t
   moe_status_t s = mm_check(MOE_MM_FP8, R, N, K, G, offsets, ws, ws_bytes);
   if (s != MOE_OK) return s;
   if (!is_float(out_dtype) || ldx < K || ldw < K || ldo < N || ldxs < blocks_of(K)) return MOE_ERR_INVALID_ARG;
-  if (G > 1 && w_group < (int64_t)(N - 1) * ldw + K) return MOE_ERR_INVALID_ARG;
+  if (G > 1 && w_group < span(N, K, ldw)) return MOE_ERR_INVALID_ARG;
   if (!have(wq, 16) || ldw % 16 || ldx % 16 || (G > 1 && w_group % 16) || !have(wscale, 4)) return MOE_ERR_INVALID_ARG;
   reset_launch_count();
   if (R == 0) return MOE_OK;

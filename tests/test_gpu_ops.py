@@ -786,6 +786,31 @@ def test_fp8_mm_scales_whose_product_leaves_fp32(R, N, K, swap):
     assert torch.equal(out[2::3], out2[2::3])
     assert torch.equal(out[::3, :(nb - 1) * 128], out2[::3, :(nb - 1) * 128])
 
+def test_fp8_quant_weights_groups_behind_the_last_row():
+    """Groups that begin right behind the last row's elements, as the products take them: w, q and qt."""
+    cuda_device()
+    g = _gen(12)
+    G, N, K, ld = 3, 40, 144, 160
+    gs = (N - 1) * ld + K                      # N ld would be 16 more
+    w = torch.as_strided(_randn(g, G * gs, dtype=BF16), (G, N, K), (gs, ld, 1))
+    q = torch.as_strided(torch.zeros(G * gs, dtype=torch.uint8, device="cuda"), (G, N, K), (gs, ld, 1))
+    ldt = 64
+    gt = (K - 1) * ldt + N
+    qt = torch.as_strided(torch.zeros(G * gt, dtype=torch.uint8, device="cuda"), (G, K, N), (gt, ldt, 1))
+    s, st = torch.empty(G, 1, 2, device="cuda"), torch.empty(G, 2, 1, device="cuda")
+    m.moe_fp8_quant_weights(w, q, s, qt, st)
+    q2, s2 = torch.empty(G, N, K, dtype=torch.uint8, device="cuda"), torch.empty_like(s)
+    m.moe_fp8_quant_weights(w.contiguous(), q2, s2)
+    assert torch.equal(q, q2) and torch.equal(s, s2) and torch.equal(qt, q2.transpose(1, 2)) and torch.equal(st, s.transpose(1, 2))
+    R = 50
+    xq, xs = torch.empty(R, K, dtype=torch.uint8, device="cuda"), torch.empty(R, 2, device="cuda")
+    m.moe_fp8_quant_rows(_randn(g, R, K, dtype=BF16), xq, xs)
+    off, offsets = _offsets([20, 0, 30])
+    y, y2 = torch.empty(R, N, device="cuda"), torch.empty(R, N, device="cuda")
+    m.moe_fp8_mm(xq, xs, q, s, y, _workspace(m.MOE_MM_FP8, R, N, K, G), offsets=offsets)
+    m.moe_fp8_mm(xq, xs, q2, s2, y2, _workspace(m.MOE_MM_FP8, R, N, K, G), offsets=offsets)
+    assert torch.equal(y, y2)
+
 # ---- both sides of the rules that pick a kernel ------------------------------------------
 # Sizes in rows an SM, as the rules count them, so that they follow the machine.
 def _rows(per_sm, more):
