@@ -467,7 +467,9 @@ moe_status_t moe_act_ckpt_backward(const void* dy, int64_t lddy, const uint8_t* 
  * MOE_MM_ROWS moe_grouped_mm, MOE_MM_WGRAD moe_grouped_mm_wgrad,
  * MOE_MM_FP8 moe_fp8_mm. The workspace starts with a sticky status word
  * (zero it once; read with moe_mm_read_status) and holds the partial sums of
- * a product that is split along its reduction: at most 64 MiB + 256 bytes. */
+ * a product that is split along its reduction: at most 64 MiB + 256 bytes. A
+ * size from this call suffices for R rows and for any fewer (N, K and G as
+ * given): one for the largest batch serves every batch. */
 enum { MOE_MM_ROWS = 0, MOE_MM_WGRAD = 1, MOE_MM_FP8 = 2 };
 moe_status_t moe_mm_workspace_size(int kind, int R, int N, int K, int G, size_t* bytes);
 

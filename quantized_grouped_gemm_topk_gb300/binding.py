@@ -552,6 +552,7 @@ def moe_act_ckpt_backward(dy, q, s, w_row, dh, dw_row=None, y=None, act="swiglu"
 
 
 def moe_mm_workspace_size(kind, R, N, K, G=1) -> int:
+    """Bytes of workspace for a product (MOE_MM_*) of R rows or fewer."""
     n = ctypes.c_size_t()
     _check("moe_mm_workspace_size", load().moe_mm_workspace_size(kind, R, N, K, G, ctypes.byref(n)))
     return n.value

@@ -40,10 +40,9 @@ moe_status_t mm_check(int kind, int R, int N, int K, int G, const int32_t* offse
   if (!mm_sizes_ok(R, N, K, G)) return MOE_ERR_INVALID_ARG;
   if (!maybe(offsets, 4) || (!offsets && (G != 1 || kind != MOE_MM_FP8))) return MOE_ERR_INVALID_ARG;
   if (!have(ws, 16)) return MOE_ERR_INVALID_ARG;
-  size_t need = 0;
-  const moe_status_t s = moe_mm_workspace_size(kind, R, N, K, G, &need);
-  if (s != MOE_OK) return s;
-  return ws_bytes < need ? MOE_ERR_WORKSPACE : MOE_OK;
+  const int S = mm_splits(kind, R, N, K, G);
+  const size_t outs = kind == MOE_MM_WGRAD ? (size_t)G * N * K : (size_t)R * N;
+  return ws_bytes < kStatusBytes + (S > 1 ? outs * 4 * S : 0) ? MOE_ERR_WORKSPACE : MOE_OK;
 }
 void mm_workspace(MmArgs& a, int kind, void* ws) {
   a.status = reinterpret_cast<int32_t*>(ws);
@@ -166,9 +165,7 @@ moe_status_t moe_fp8_quant_weights(const void* w, int64_t w_group, int64_t ldw, 
 moe_status_t moe_mm_workspace_size(int kind, int R, int N, int K, int G, size_t* bytes) {
   if (!bytes || !mm_sizes_ok(R, N, K, G)) return MOE_ERR_INVALID_ARG;
   if (kind != MOE_MM_ROWS && kind != MOE_MM_WGRAD && kind != MOE_MM_FP8) return MOE_ERR_INVALID_ARG;
-  const int S = mm_splits(kind, R, N, K, G);
-  const size_t outs = kind == MOE_MM_WGRAD ? (size_t)G * N * K : (size_t)R * N;
-  *bytes = kStatusBytes + (S > 1 ? outs * 4 * S : 0);
+  *bytes = kStatusBytes + (size_t)mm_part_bytes(kind, R, N, K, G);
   return MOE_OK;
 }
 

@@ -563,6 +563,7 @@ cudaError_t launch_mm_join(const MmArgs& a, bool wgrad, cudaStream_t st) {
 // The split rule must not depend on the device a size query runs on.
 constexpr int kPlanSms = 152;
 constexpr int64_t kPartBytes = 64ll << 20;
+constexpr int64_t kStep16 = 512, kStepFp8 = 1024;     // least reduction of a piece
 
 static int64_t tiles(int64_t n, int64_t t) { return (n + t - 1) / t; }
 
@@ -603,16 +604,28 @@ MmPlan mm_plan(int kind, int R, int N, int K, int G) {
     }
   }
   const int64_t units = count(p.cg, p.bn);
-  // Too few tiles: pieces of at least 512 (FP8: 1024) of the reduction, partial
+  // Too few tiles: pieces of at least kStep16 (kStepFp8) of the reduction, partial
   // sums within the workspace's bound (bf16 64 x 2880 x 2880 14.8 us, 20.7 in
   // one piece).
-  const int64_t red = wg ? tiles(R, G) : K, step = kind == kMmFp8 ? 1024 : 512;
+  const int64_t red = wg ? tiles(R, G) : K, step = kind == kMmFp8 ? kStepFp8 : kStep16;
   const int64_t outs = wg ? (int64_t)G * N * K : (int64_t)R * N;
   if (p.cg == 1 && units > 0 && units < kPlanSms && outs > 0)
     p.S = (int)std::max<int64_t>(1, std::min({kPlanSms / units, red / step, kPartBytes / (outs * 4), (int64_t)32}));
   return p;
 }
 int mm_splits(int kind, int R, int N, int K, int G) { return mm_plan(kind, R, N, K, G).S; }
+int64_t mm_part_bytes(int kind, int R, int N, int K, int G) {
+  if (kind == kMmWgrad) {       // the pieces only grow in number with the rows
+    const int S = mm_splits(kind, R, N, K, G);
+    return S > 1 ? (int64_t)G * N * K * 4 * S : 0;
+  }
+  // Few rows are cut into more pieces than many, so the need of R rows says
+  // nothing about fewer. Any of them: at most this many pieces, and together at
+  // most kPlanSms tiles of 128 x 256 outputs.
+  const int64_t most = std::min({(int64_t)32, K / (kind == kMmFp8 ? kStepFp8 : kStep16),
+                                 kPlanSms / tiles(N, kind == kMmFp8 ? 256 : kGM)});
+  return most > 1 ? std::min<int64_t>((int64_t)R * N * 4 * most, (int64_t)kPlanSms * kGM * 256 * 4) : 0;
+}
 
 // ---- host -------------------------------------------------------------------------
 typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,

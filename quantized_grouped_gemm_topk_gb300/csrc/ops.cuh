@@ -323,6 +323,8 @@ struct MmPlan {
 };
 MmPlan mm_plan(int kind, int R, int N, int K, int G);
 int mm_splits(int kind, int R, int N, int K, int G);
+// Bytes of partial sums that suffice for any product of at most R rows.
+int64_t mm_part_bytes(int kind, int R, int N, int K, int G);
 // Adds the partial sums of a split product into out.
 cudaError_t launch_mm_join(const MmArgs& a, bool wgrad, cudaStream_t st);
 // Tensor map of rank dimensions (innermost first; strides in elements, from

@@ -194,3 +194,23 @@ def test_rows_too_long(lib, n):
     assert _call(lib.moe_fp8_quant_rows, QR, C=n, ldx=n, ldq=n, lds=n) == INVALID
     assert _call(lib.moe_fp8_quant_weights, QW, K=n, ldw=n, ldq=n, wg=64 * n, qg=64 * n, qtg=64 * n) == INVALID
     assert _call(lib.moe_fp8_quant_weights, QW, N=n, ldqt=n, wg=64 * n, qg=64 * n, qtg=64 * n) == INVALID
+
+
+@pytest.mark.parametrize("G", [1, 8, 64])
+@pytest.mark.parametrize("N,K", [(64, 8192), (128, 4096), (2880, 2880), (7168, 2048), (4096, 7168), (129, 1024)])
+def test_a_workspace_for_the_largest_batch_serves_every_batch(lib, N, K, G):
+    """Sized for many rows, used with few (which are cut into more pieces): never MOE_ERR_WORKSPACE. Each call stops at
+    another argument behind the workspace's check, so nothing is enqueued."""
+    from quantized_grouped_gemm_topk_gb300 import binding as m
+    small = [*range(1, 130), 200, 255, 256, 257, 500, 1000, 2047, 2048, 4097, 9000, 20000, 65536]
+    for kind, fn, base, kw in (
+            (m.MOE_MM_ROWS, lib.moe_grouped_mm, MM, dict(ldx=K, wg=N * K, ldw=K, ldo=N, dtype=9)),
+            (m.MOE_MM_WGRAD, lib.moe_grouped_mm_wgrad, WGRAD, dict(lddy=N, ldx=K, dwg=N * K, lddw=K, dtype=9)),
+            (m.MOE_MM_FP8, lib.moe_fp8_mm, FP8, dict(ldx=K, ldw=K, ldxs=64, ldo=N, wg=N * K, out_dtype=9))):
+        sizes = [m.moe_mm_workspace_size(kind, R, N, K, G) for R in small]
+        assert sizes == sorted(sizes)
+        for most in (20000, 65536):
+            have = m.moe_mm_workspace_size(kind, most, N, K, G)
+            for R in small:
+                if R <= most:
+                    assert _call(fn, base, R=R, N=N, K=K, G=G, ws_bytes=have, **kw) == INVALID, (kind, R)
