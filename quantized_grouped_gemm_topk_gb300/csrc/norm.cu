@@ -364,7 +364,8 @@ constexpr int kRingBytes = 200 * 1024;    // of an SM's shared memory, for all i
 constexpr int kRingHead = 128;            // barriers, in front of the stages
 
 // The bounded wait for a row. A copy from this GPU's memory always lands;
-// should the wait run out all the same, the row's results become NaN.
+// should the wait run out all the same, the row's results become NaN, and the
+// thread's columns of the weight's gradient with them.
 __device__ __forceinline__ bool ring_wait(uint64_t* bar, uint32_t parity) {
   volatile int give_up = 0;
   return tc::mbar_wait(bar, parity, &give_up);
@@ -541,7 +542,13 @@ __global__ void __launch_bounds__(kNormBwdThreads) k_norm_ring(NormArgs a, int s
 #pragma unroll
       for (int k = 0; k < RW; ++k) {
         const f32x2 nmu = pack2(-mu[k], -mu[k]), rr = pack2(r[k], r[k]);
-        f32x2 p1 = pack2(bad[k], 0.f), p2 = 0;
+        f32x2 p1 = pack2(PART ? 0.f : bad[k], 0.f), p2 = 0;
+        if (PART && bad[k] != 0.f) {      // a NaN dy reaches the row's sums and the columns'
+#pragma unroll
+          for (int i = 0; i < NV; ++i)
+#pragma unroll
+            for (int j = 0; j < V; ++j) pd[k][i].v[j] = E::from(bad[k]);
+        }
 #pragma unroll
         for (int i = 0; i < NV; ++i)
           if ((k == 0 || two) && (i * tpr + t) * V < a.H) {
