@@ -30,14 +30,10 @@
 // are prepacked so a 192-column tile holds 96 gate features and the same 96
 // up features.
 //
-// With clusters (kMxCl > 1), the CTAs of a cluster take consecutive
-// 128-row tiles of the same group and the same 192-column B tile; each CTA
-// copies its part of the B tile and multicasts it into all of them, and a
-// stage slot is refilled only after the MMAs of every CTA released it.
 // Roles (one CTA per SM, persistent over the work units):
 //   warp 0       TMA producer: per stage one 2-D tensor copy of the A tile
-//                and one of the B tile (or its cluster part, multicast),
-//                128-byte swizzle, into a 5-stage ring.
+//                and one of the B tile, 128-byte swizzle, into a 5-stage
+//                ring.
 //   warp 1       MMA issuer: per stage 4 block-scaled MMAs (fewer at a K
 //                tail); commits free the stage and the scale slot; a tile's
 //                last commit hands its accumulator to the epilogue. Also
@@ -66,12 +62,6 @@ constexpr int kMxBM = 128;
 constexpr int kMxBN = 192;
 constexpr int kMxBK = 128;
 constexpr int kMxStages = 5;
-// CTAs per cluster. With 2, a pair takes two m-tiles sharing one B tile and
-// multicasts it (28 KB per CTA-stage from L2 instead of 40 KB); measured on
-// the training shapes it ran 5-10% slower than 1 (the mainloop is not
-// bound by L2 read bandwidth), so 1 is the default.
-constexpr int kMxCl = 1;
-constexpr int kMxBHalf = kMxBN / kMxCl;           // B rows each CTA of the pair loads (multicast to both)
 constexpr int kMxSfSlots = 8;
 constexpr int kMxThreads = 512;
 constexpr int kMxWProd = 0, kMxWMma = 1, kMxWSf = 4, kMxWEpi = 8;
@@ -102,10 +92,9 @@ struct MxUnit {
   int cnt, pad;           // the group's rows and their padded count (token side)
 };
 
-// Unit u of the cluster -> (group, m-tile pair, n-tile) through the
-// per-group prefix sums of m-tile pairs uoff (shared memory); the CTA of
-// cluster rank `rank` takes m-tile 2 * pair + rank.
-__device__ __forceinline__ void mx_unit(const MxArgs& g, const int32_t* uoff, int u, int rank, MxUnit& w) {
+// Unit u -> (group, m-tile, n-tile) through the per-group prefix sums of
+// m-tiles uoff (shared memory).
+__device__ __forceinline__ void mx_unit(const MxArgs& g, const int32_t* uoff, int u, MxUnit& w) {
   const int ui = u / g.n_tiles;
   w.ni = u - ui * g.n_tiles;
   int lo = 0, hi = g.G - 1;   // last e with uoff[e] <= ui
@@ -114,7 +103,7 @@ __device__ __forceinline__ void mx_unit(const MxArgs& g, const int32_t* uoff, in
     if (uoff[mid] <= ui) lo = mid; else hi = mid - 1;
   }
   w.e = lo;
-  w.mi = kMxCl * (ui - uoff[lo]) + rank;
+  w.mi = ui - uoff[lo];
   if (g.mode == kMxWgrad) {
     w.a_row0 = w.mi * kMxBM;
     w.a_valid = min(kMxBM, g.M - w.a_row0);
@@ -494,11 +483,10 @@ __device__ __forceinline__ void mx_epilogue(const MxArgs& g, const MxUnit& w, ui
   }
 }
 
-// m-tile pairs of group e (the cluster's unit height).
+// m-tiles of group e.
 template <int MODE>
-__device__ __forceinline__ int mx_pairs(const MxArgs& g, int e) {
-  const int mt = MODE == kMxWgrad ? g.m_tiles : (g.offsets[e + 1] - g.offsets[e] + kMxBM - 1) / kMxBM;
-  return (mt + kMxCl - 1) / kMxCl;
+__device__ __forceinline__ int mx_tiles(const MxArgs& g, int e) {
+  return MODE == kMxWgrad ? g.m_tiles : (g.offsets[e + 1] - g.offsets[e] + kMxBM - 1) / kMxBM;
 }
 
 template <int MODE>
@@ -530,7 +518,7 @@ __global__ void __launch_bounds__(kMxThreads, 1) k_gemm_mx(const __grid_constant
   }
   __syncthreads();
   if (bad_pack) return;   // the blob is not the packing this GEMM reads: write nothing
-  // per-group prefix sums of m-tile pairs (a block-wide scan)
+  // per-group prefix sums of m-tiles (a block-wide scan)
   {
     __shared__ int32_t wsum[kMxThreads / 32];
     const int G = g.G;
@@ -538,7 +526,7 @@ __global__ void __launch_bounds__(kMxThreads, 1) k_gemm_mx(const __grid_constant
     const int lo = threadIdx.x * per, hi = min(G, lo + per);
     int s = 0;
     for (int e = lo; e < hi; ++e)
-      s += mx_pairs<MODE>(g, e);
+      s += mx_tiles<MODE>(g, e);
     int incl = s;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -552,14 +540,14 @@ __global__ void __launch_bounds__(kMxThreads, 1) k_gemm_mx(const __grid_constant
     int run = base + incl - s;
     for (int e = lo; e < hi; ++e) {
       uoff[e] = run;
-      run += mx_pairs<MODE>(g, e);
+      run += mx_tiles<MODE>(g, e);
     }
     if (threadIdx.x == kMxThreads - 1) uoff[G] = base + incl;
   }
   if (threadIdx.x == 0) {
     for (int i = 0; i < kMxStages; ++i) {
       tc::mbar_init(&full[i], 1);
-      tc::mbar_init(&empty[i], kMxCl);   // released by the MMAs of both CTAs of the pair
+      tc::mbar_init(&empty[i], 1);
     }
     for (int i = 0; i < kMxSfSlots; ++i) {
       tc::mbar_init(&sffull[i], 4);    // one elected arrive per scale-loader warp
@@ -576,13 +564,9 @@ __global__ void __launch_bounds__(kMxThreads, 1) k_gemm_mx(const __grid_constant
   if (warp == kMxWMma) tc::tmem_alloc(tmem_slot, kMxTmemCols);
   tc::fence_before_sync();
   __syncthreads();
-  // the peers' barriers are initialised before any copy or commit reaches them
-  if constexpr (kMxCl > 1) tc::cluster_sync();
   tc::fence_after_sync();
   const uint32_t tmem = *tmem_slot;
   const int U = uoff[g.G] * g.n_tiles;
-  const int rank = kMxCl > 1 ? (int)tc::cluster_rank() : 0;
-  const int cid = blockIdx.x / kMxCl, ncl = gridDim.x / kMxCl;
 
   if (warp == kMxWProd) {
     // ---------------- TMA producer ----------------
@@ -598,9 +582,9 @@ __global__ void __launch_bounds__(kMxThreads, 1) k_gemm_mx(const __grid_constant
       const uint32_t b_tx = g.b_fp4 ? kMxBStage / 2 : kMxBStage;
       uint32_t it = 0;
       bool ok = true;
-      for (int u = cid; ok && u < U; u += ncl) {
+      for (int u = blockIdx.x; ok && u < U; u += gridDim.x) {
         MxUnit w;
-        mx_unit(g, uoff, u, rank, w);
+        mx_unit(g, uoff, u, w);
         const int nk = mx_stages(w.klen);
         for (int s = 0; s < nk; ++s, ++it) {
           const int slot = it % kMxStages;
@@ -610,13 +594,7 @@ __global__ void __launch_bounds__(kMxThreads, 1) k_gemm_mx(const __grid_constant
           const int kx = w.k0 + s * kMxBK;
           tc::tma_load_2d_plain(sfb + slot * kMxSfbBytes, &maps.sfb, w.b_row0, kx / kMxBK, &full[slot]);
           tc::tma_load_2d_plain(sa + slot * kMxAStage, &maps.a[ai], kx, w.a_row0, &full[slot]);
-          if constexpr (kMxCl > 1) {
-            // this CTA's part of the shared B tile, into every CTA of the cluster
-            tc::tma_load_2d_mc(sb + slot * kMxBStage + rank * (kMxBHalf * kMxBK), &maps.b, kx,
-                               w.b_row0 + rank * kMxBHalf, &full[slot], (uint16_t)((1u << kMxCl) - 1));
-          } else {
-            tc::tma_load_2d_plain(sb + slot * kMxBStage, &maps.b, kx, w.b_row0, &full[slot]);
-          }
+          tc::tma_load_2d_plain(sb + slot * kMxBStage, &maps.b, kx, w.b_row0, &full[slot]);
         }
       }
       if (!ok || *abort) {
@@ -636,9 +614,9 @@ __global__ void __launch_bounds__(kMxThreads, 1) k_gemm_mx(const __grid_constant
       uint32_t it = 0, tcount = 0;
       bool ok = true;
       const uint32_t btype = g.b_fp4 ? tc::kMxE2M1 : tc::kMxE4M3;
-      for (int u = cid; ok && u < U; u += ncl, ++tcount) {
+      for (int u = blockIdx.x; ok && u < U; u += gridDim.x, ++tcount) {
         MxUnit w;
-        mx_unit(g, uoff, u, rank, w);
+        mx_unit(g, uoff, u, w);
         const int nk = mx_stages(w.klen);
         const int d = tcount & 1;
         if (!tc::mbar_wait(&accempty[d], ((tcount >> 1) & 1) ^ 1, abort)) { ok = false; break; }
@@ -657,8 +635,7 @@ __global__ void __launch_bounds__(kMxThreads, 1) k_gemm_mx(const __grid_constant
           for (int j = 0; j < kv; ++j)
             tc::mma_mx_ss(dt, ad + 2 * j, bd + 2 * j, tc::idesc_mx(kMxBM, kMxBN, j, j, btype), sfa, sfb,
                           (s | j) != 0 ? 1u : 0u);
-          if constexpr (kMxCl > 1) tc::mma_commit_mc(&empty[slot], (uint16_t)((1u << kMxCl) - 1));
-          else tc::mma_commit(&empty[slot]);
+          tc::mma_commit(&empty[slot]);
           tc::mma_commit(&sfempty[fs]);
         }
         if (!ok) break;
@@ -680,9 +657,9 @@ __global__ void __launch_bounds__(kMxThreads, 1) k_gemm_mx(const __grid_constant
     static_assert(kNB1 == 2, "B's second group holds rows 128-191");
     uint32_t it = 0;
     bool ok = true;
-    for (int u = cid; ok && u < U; u += ncl) {
+    for (int u = blockIdx.x; ok && u < U; u += gridDim.x) {
       MxUnit w;
-      mx_unit(g, uoff, u, rank, w);
+      mx_unit(g, uoff, u, w);
       const int nk = mx_stages(w.klen);
       // each A row's SF4 column (nullptr: no such row); B's words come with
       // the stage into shared memory (sfb)
@@ -746,10 +723,10 @@ __global__ void __launch_bounds__(kMxThreads, 1) k_gemm_mx(const __grid_constant
     const int q = warp & 3;
     const uint32_t acc = tmem + ((uint32_t)(q * 32) << 16) + wg * kMxBN;
     uint32_t tcount = 0, mine = 0;
-    for (int u = cid; u < U; u += ncl, ++tcount) {
+    for (int u = blockIdx.x; u < U; u += gridDim.x, ++tcount) {
       if ((int)(tcount & 1) != wg) continue;
       MxUnit w;
-      mx_unit(g, uoff, u, rank, w);
+      mx_unit(g, uoff, u, w);
       const bool got = tc::mbar_wait(&accfull[wg], mine & 1, abort);
       if (!__all_sync(kFull, got)) break;
       tc::fence_after_sync();
@@ -763,17 +740,6 @@ __global__ void __launch_bounds__(kMxThreads, 1) k_gemm_mx(const __grid_constant
 
   tc::fence_before_sync();
   __syncthreads();
-  if constexpr (kMxCl > 1) {
-    if (*abort) {
-      // a CTA that gave up may have copies into its peers still in flight:
-      // give them time to land (bounded) before the cluster can leave
-      const long long t0 = clock64();
-      while (clock64() - t0 < 100000) {
-      }
-    }
-    // no CTA leaves while a peer may still multicast into it or arrive on it
-    tc::cluster_sync();
-  }
   if (threadIdx.x == 0 && *abort) set_status(g.status, MOE_DEV_TIMEOUT);
   if (warp == kMxWMma) {
     tc::fence_after_sync();
@@ -839,38 +805,11 @@ bool make_tmaps_mx_a(MxMaps* maps, const void* base, int64_t rows, int64_t cols)
 template <int MODE>
 static cudaError_t launch_mx_t(const MxArgs& g, const MxMaps& maps, int grid_cap, cudaStream_t st) {
   static std::atomic<bool> done[kMaxDevices] = {};
-  static std::atomic<int> max_clusters[kMaxDevices] = {};
-  cudaError_t e = set_smem_once((const void*)k_gemm_mx<MODE>, kMxSmemBytes, done);
+  const cudaError_t e = set_smem_once((const void*)k_gemm_mx<MODE>, kMxSmemBytes, done);
   if (e != cudaSuccess) return e;
-  int dev = 0;
-  if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg = {};
-  cfg.blockDim = dim3(kMxThreads);
-  cfg.dynamicSmemBytes = kMxSmemBytes;
-  cfg.stream = st;
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = kMxCl;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[1].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  // clusters that fit on the device at once (pairs of SMs of one GPC),
-  // queried once per device
-  const bool slot = dev >= 0 && dev < kMaxDevices;
-  int nc = slot ? max_clusters[dev].load() : 0;
-  if (nc <= 0) {
-    cfg.gridDim = dim3(kMxCl * 64);
-    cfg.numAttrs = 1;
-    if (cudaOccupancyMaxActiveClusters(&nc, k_gemm_mx<MODE>, &cfg) != cudaSuccess || nc <= 0)
-      nc = std::max(1, device_sms() / kMxCl);
-    if (slot) max_clusters[dev].store(nc);
-  }
-  const int ncl = std::max(1, std::min(nc, grid_cap / kMxCl));
-  cfg.gridDim = dim3(ncl * kMxCl);
-  cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, k_gemm_mx<MODE>, g, maps);
+  // a CTA fills an SM's shared memory
+  const int grid = std::max(1, std::min(device_sms(), grid_cap));
+  return launch_pdl(k_gemm_mx<MODE>, dim3(grid), dim3(kMxThreads), kMxSmemBytes, st, g, maps);
 }
 
 cudaError_t launch_gemm_mx(const MxArgs& g, const MxMaps& maps, int grid, cudaStream_t st) {
@@ -889,7 +828,7 @@ cudaError_t launch_gemm_mx(const MxArgs& g, const MxMaps& maps, int grid, cudaSt
 }
 
 int mx_tile_n() { return kMxBN; }
-int mx_b_box_rows() { return kMxBHalf; }
+int mx_b_box_rows() { return kMxBN; }
 int mx_tile_m() { return kMxBM; }
 
 // ---------------------------------------------------------------------------

@@ -254,7 +254,7 @@ bool make_tmaps_mx_a(MxMaps* maps, const void* base, int64_t rows, int64_t cols)
 // boxes of one word x 192 rows; ld must be a multiple of 4.
 bool make_tmap_mx_sf(CUtensorMap* map, const void* sf, int64_t rows, int64_t words, int64_t ld);
 int mx_tile_n();
-int mx_b_box_rows();          // rows of B per tensor copy (each CTA of a pair copies this many)
+int mx_b_box_rows();          // rows of B per tensor copy
 int mx_tile_m();
 cudaError_t launch_gemm_mx(const MxArgs& g, const MxMaps& maps, int grid, cudaStream_t st);
 // dst rows r < min(R, offsets[G]) = MXFP8 rows src[row_map[r] / row_div];
