@@ -105,10 +105,6 @@ inline bool units_fit(const MmArgs& m, int64_t row_tiles, int64_t n_tiles) {
   return (row_tiles + m.G) * n_tiles * m.S < (1ll << 31) - 4096;
 }
 
-// A copy of a K-major tile covers 16 << i rows, the fewest that hold its real
-// ones; the MMA's other rows are an earlier stage's bytes and are not stored.
-__device__ __forceinline__ int g_a_box(int rows) { return rows <= 16 ? 0 : rows <= 32 ? 1 : rows <= 64 ? 2 : 3; }
-
 // C columns (a multiple of 8) of a row from fp32 bits: n valid ones at p, as
 // out_dtype; vec: 16-byte stores are aligned.
 template <int C>
