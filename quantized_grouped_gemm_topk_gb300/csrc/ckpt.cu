@@ -27,9 +27,10 @@ constexpr int kCkptThreads = 256;
 constexpr int kCkptQuarters = kCkptThreads / 8;
 
 // 1 / (1 + 2^(-v log2 e)): the exponential and the reciprocal on the
-// special-function unit (relative error about 2^-22 each, far below the 16
-// bits that leave here); past the exponent's range 2^x is 0 or infinity and
-// the quotient 1 or 0. NaN stays NaN.
+// special-function unit, relative error about 2^-22 each; the rounding of the
+// exponent adds |v| 2^-24, 2^-17 at most where 2^x is finite. Together below
+// the half step of the 16 bits that leave here (2^-9, 2^-12). Past the
+// exponent's range 2^x is 0 or infinity and the quotient 1 or 0. NaN stays NaN.
 __device__ __forceinline__ float fast_sigmoid(float v) {
   float e, r;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(v * -1.4426950408889634f));
