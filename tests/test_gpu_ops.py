@@ -583,8 +583,8 @@ def test_fp8_mm_dense(R, N, K, out):
     assert m.moe_mm_read_status(ws) == 0
 
 
-# enough rows and columns that pairs of SMs share the tiles: the last rows of a group in either CTA's half of a tile,
-# columns that end in either's, an empty group
+# enough rows and columns for the wider tiles (128 columns; 256 in two halves): groups and columns that end inside a
+# tile, columns that end in either half, an empty group
 @pytest.mark.parametrize("sizes", [(2500,), (1290, 0, 2310), (4097,), (1025, 3001)], ids=lambda s: "-".join(map(str, s)))
 @pytest.mark.parametrize("N,K", [(2100, 700), (2432, 384), (4160, 1000)])
 @pytest.mark.parametrize("out", [F32, BF16])
@@ -756,7 +756,8 @@ def test_elements_past_32_bits():
     assert torch.equal(xq[-L:].view(torch.uint8), xq2.view(torch.uint8)) and torch.equal(xs[-L:], xs2)
 
 
-@pytest.mark.parametrize("R,N,K", [(70, 200, 700), (600, 1100, 640), (2500, 2100, 700)])
+# tiles of 64, 128 and 256 columns, and a reduction in pieces
+@pytest.mark.parametrize("R,N,K", [(70, 200, 700), (600, 1100, 640), (2500, 2100, 700), (4100, 2100, 300), (16, 300, 4200)])
 @pytest.mark.parametrize("swap", [False, True])
 def test_fp8_mm_scales_whose_product_leaves_fp32(R, N, K, swap):
     """Two scales whose product overflows, over a block of zeros, and two whose product is subnormal, over a block whose
