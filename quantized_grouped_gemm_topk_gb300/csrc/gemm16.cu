@@ -36,10 +36,12 @@
 // gradient: those behind a group's last rows, in shared memory).
 // Every wait is bounded; a CTA whose wait runs out sets MOE_DEV_TIMEOUT, waits
 // for its copies and MMAs in flight, frees tensor memory and returns.
-// Measured, bf16: 8192^3 NT 615 us (1.79 PFLOP/s), NN 634, weight gradient 646;
-// 65536 rows in 128 groups x 5760 x 2880 1.45 to 1.53 ms (1.42 to 1.50 PFLOP/s;
-// tensor pipe 68 % busy); 30011 rows in 64 groups, 2880 x 2880 weight gradients
-// 0.43 ms; 8 rows of 8 experts x 4096 x 7168 76 us (6.2 TB/s of weights).
+// Measured, bf16, in a burst and sustained (at the power limit, where the clock
+// falls): 8192^3 NT 621 us (1.77 PFLOP/s) and 702, NN 634 and 708, weight gradient
+// 632 and 706; 65536 rows in 128 groups x 5760 x 2880 1.47 ms (1.47 PFLOP/s, tensor
+// pipe 68 % busy) and 1.67 (1.30); 30011 rows in 64 groups, 2880 x 2880 weight
+// gradients 432 us and 465; 8 rows of 8 experts x 4096 x 7168 76 us (6.2 TB/s of
+// weights).
 #include "groups.cuh"
 #include "tc.cuh"
 
@@ -414,8 +416,8 @@ __global__ void __launch_bounds__(kGThreads, 1) k_gemm16(const GArgs g, const __
         told ^= 1;
         tails ^= 1u << at;
         // eight lanes a line, four lines at a time: the MMAs wait for this (with
-        // a division for each store 64 groups of 385 rows took 500 us, now 416, and
-        // of 470 rows 510, now 476)
+        // a division for each store 64 groups of 385 rows x 2880 x 2880 took 499 us,
+        // now 410, and of 470 rows 492, now 434)
         const int bad = 16 - (left & 15), at0 = (left % kGH + (lane >> 3)) * 128 + (lane & 7) * 16;
         auto clear = [&](uint8_t* p, int chunks) {
           for (int c = 0; c < chunks; ++c, p += kGChunk)

@@ -14,8 +14,9 @@
 // Bound: the tensor pipe at training sizes (a 128 x 256 x 128 block is 512
 // cycles of MMA, its additions 256 issue slots a scheduler at most), the
 // weights' bytes at decode sizes.
-// Measured: 8192^3 511 us (2.15 PFLOP/s), 8192 x 7168 x 4096 236 us, 12289 rows in
-// 32 groups x 4096 x 7168 395 us, 3 x 7168 x 2048 10.6 us.
+// Measured: 8192^3 511 us (2.15 PFLOP/s; sustained, at the power limit, 546), 8192 x
+// 7168 x 4096 237 us, 12289 rows in 32 equal groups x 4096 x 7168 358 us, in ragged
+// ones 395, 3 x 7168 x 2048 10.7 us.
 // At 8192^3 a block takes 1000 cycles; without the additions 816, without them
 // and three of the four MMAs 670 (the copies: 48 KB at what an SM takes in).
 // Of a block's way the issue of its MMAs is 600 cycles, the last commit's until

@@ -17,7 +17,7 @@
 // same bits every run. Where that leaves too few bytes in flight a ring of rows
 // in shared memory runs ahead (k_norm_ring).
 // Measured, bf16: forward 16384 x 2880 47 us (4.0 TB/s), x 7168 87 (5.4 TB/s),
-// 1 x 7168 3.3 us; backward with both weight gradients 16384 x 2880 65 us
+// 1 x 7168 3.5 us; backward with both weight gradients 16384 x 2880 65 us
 // (4.3 TB/s), x 7168 143 (4.9 TB/s). At odd alignments 16384 x 2881 76 and 101
 // us. What is left: a row's reductions are two rounds (backward one) of shuffles
 // and a barrier, and the few rows an SM has in flight wait for them.

@@ -12,8 +12,8 @@
 // quarter-warp (fp32: a half-warp) holds a row's block in registers; a CTA a
 // 128 x 128 block, whose codes cross shared memory once for the transposed
 // copy.
-// Measured, bf16: rows 12289 x 7168 46 us (5.7 TB/s), 8192 x 4096 17 us (5.9),
-// at odd alignments 8192 x 4099 31 us (3.3); weights 7168 x 4096 with the
+// Measured, bf16: rows 12289 x 7168 46 us (5.7 TB/s), 8192 x 4096 19 us (5.3; 17 where
+// L2 holds them), at odd alignments 8192 x 4099 30 us (3.3); weights 7168 x 4096 with the
 // transposed copy 22 us (5.4), 32 x 4096 x 1024 84 us (6.4).
 #include "blocks.cuh"
 
