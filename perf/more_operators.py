@@ -26,7 +26,7 @@ def _layer(name, T, H, I, E, k, shared, act, dtype, bias, scale, pad):
 
 
 def _linear(name, d, R, N, K, act, dtype, wdtype, bias, residual, save, pad):
-    """N: output columns; a gated activation's weights have 2 N rows. wdtype: of the bias and the weights' gradients."""
+    """N: output columns; a gated activation's weights have 2 N rows. wdtype: of the bias and its gradient."""
     return {"name": name, "op": "linear", "dir": d, "R": R, "N": N, "K": K, "act": act, "dtype": dtype, "wdtype": wdtype,
             "bias": bias, "residual": residual, "save": save, "pad": pad}
 
@@ -148,7 +148,7 @@ def prepare(case, seed):
     st["dout"] = _randn(gen, R, N, dtype=dt)
     st["z"] = _randn(gen, R, rows, dtype=dt, std=1.5) if act != "none" else None
     st["dz"] = _out(R, rows, dtype=dt) if act != "none" else None
-    st["dx"], st["dw"] = _out(R, K, dtype=dt), _out(rows, K, dtype=wdt)
+    st["dx"], st["dw"] = _out(R, K, dtype=dt), _out(rows, K, dtype=dt)
     st["db"] = torch.zeros(rows, dtype=wdt, device="cuda")
     return st
 
@@ -256,8 +256,7 @@ def _run_plain(st):
     dz = st["dout"].float()
     if act != "none":
         dz = torch.cat([dz * g for g in _activation(st["z"].float(), act, True)[1]], 1)
-    wdt = st["dw"].dtype
-    return {"dx": (dz @ w).to(dt), "dw": (dz.t() @ x).to(wdt), "db": dz.sum(0).to(wdt)}
+    return {"dx": (dz @ w).to(dt), "dw": (dz.t() @ x).to(dt), "db": dz.sum(0).to(st["db"].dtype)}
 
 
 def run(state):
@@ -280,7 +279,7 @@ def work(case):
     if case["dir"] == "forward":
         return {"bytes": 2 * R * K + 2 * rows * K + (we * rows if case["bias"] else 0) + 2 * R * N * (2 if case["residual"] else 1)
                 + (saved if case["save"] else 0), "flops": 2 * R * rows * K}
-    return {"bytes": 2 * R * N + saved + 4 * R * K + (2 + we) * rows * K + we * rows, "flops": 4 * R * rows * K}
+    return {"bytes": 2 * R * N + saved + 4 * R * K + 4 * rows * K + we * rows, "flops": 4 * R * rows * K}
 
 
 # ---- the definition in 64 bits ---------------------------------------------------
