@@ -91,6 +91,9 @@ typedef enum moe_status {
 #define MOE_DEV_BAD_OFFSETS 0x10  /* a product's group offsets descend or leave [0, R] */
 
 enum { MOE_ACT_SWIGLU = 0, MOE_ACT_SWIGLU_CLAMP = 1, MOE_ACT_GEGLU = 2, MOE_ACT_SRELU = 3 };
+/* further activations of the dense products (moe_linear_*), none of them gated:
+ * none, GELU(v) = v Phi(v) in its erf form, SiLU(v) = v sigmoid(v) */
+enum { MOE_ACT_NONE = 4, MOE_ACT_GELU = 5, MOE_ACT_SILU = 6 };
 enum { MOE_WFMT_NVFP4 = 0, MOE_WFMT_MXFP8 = 1, MOE_WFMT_MXFP4 = 2 };
 enum { MOE_PACK_FORWARD = 0, MOE_PACK_DGRAD = 1 };
 
@@ -518,6 +521,72 @@ moe_status_t moe_fp8_quant_weights(const void* w, int64_t w_group, int64_t ldw, 
 moe_status_t moe_fp8_mm(const uint8_t* xq, int64_t ldx, const float* xs, int64_t ldxs, const uint8_t* wq,
                         int64_t w_group, int64_t ldw, const float* wscale, const int32_t* offsets, int R, int N, int K,
                         int G, void* out, int64_t ldo, int out_dtype, void* ws, size_t ws_bytes, void* stream);
+
+/* Dense product with bias, activation and residual in its epilogue:
+ *   z = x w^T + bias, out = act(z) + residual
+ * x [R, K], w [rows, K], out and residual [R, N] of dtype (bf16 or f16); rows =
+ * 2 N for a gated act (MOE_ACT_SWIGLU, _SWIGLU_CLAMP, _GEGLU: gate rows, then up
+ * rows; z [R, 2 N]), else N (_SRELU, _NONE, _GELU, _SILU). bias [rows] of wdtype
+ * (fp32 or dtype), residual and z nullable. z [R, rows] receives the
+ * pre-activation, rounded, for the backward; out is computed from the fp32 z.
+ * residual may be out itself (same address and stride). x, w and ws start on 16
+ * bytes, ldx and ldw are multiples of 8 elements. ws:
+ * moe_linear_workspace_size bytes, starting with the status word
+ * (moe_mm_read_status); zero it once. */
+moe_status_t moe_linear_forward(const void* x, int64_t ldx, const void* w, int64_t ldw, const void* bias,
+                                const void* residual, int64_t ldr, int R, int N, int K, int act, float alpha,
+                                float limit, int dtype, int wdtype, void* z, int64_t ldz, void* out, int64_t ldo,
+                                void* ws, size_t ws_bytes, void* stream);
+
+/* Its backward from the saved z: dz = dout act'(z) [R, rows], rounded to dtype
+ * (the operand of both products), dx [R, K] = dz w, dw [rows, K] = dz^T x (of
+ * dtype), db [rows] (wdtype) = the column sums of dz before its rounding; the
+ * residual's gradient is dout. dx, dw and db are each nullable (x is read for
+ * dw, w for dx). With MOE_ACT_NONE dz is dout: z and dz are not read or written.
+ * dz (with MOE_ACT_NONE: dout), x, w and ws start on 16 bytes, their strides are
+ * multiples of 8 elements. R = 0 writes zero dw and db. */
+moe_status_t moe_linear_backward(const void* dout, int64_t lddout, const void* x, int64_t ldx, const void* w,
+                                 int64_t ldw, const void* z, int64_t ldz, int R, int N, int K, int act, float alpha,
+                                 float limit, int dtype, int wdtype, void* dz, int64_t lddz, void* dx, int64_t lddx,
+                                 void* dw, int64_t lddw, void* db, void* ws, size_t ws_bytes, void* stream);
+
+/* Host only. Workspace of moe_linear_forward (backward = 0) or
+ * moe_linear_backward (1) with weights [rows, K]; R rows or any fewer. */
+moe_status_t moe_linear_workspace_size(int R, int rows, int K, int backward, size_t* bytes);
+
+/* ---- serving 16-bit experts --------------------------------------------------
+ *
+ * The whole routed layer for a few tokens (T <= MOE_LAYER16_MAX_T) with experts
+ * kept in 16 bits, as moe_grouped_mm takes them: per token t and routed slot
+ *   y = w act(x[t] W1_e^T + b1_e), out[t] = sum over the slots of y W2_e^T
+ * x, out [T, H] and w1 [G, 2I, H] (gate rows, then up rows; MOE_ACT_SRELU:
+ * [G, I, H]), w2 [G, H, I] of dtype (bf16 or f16); b1 [G, 2I] fp32, nullable
+ * (NULL with MOE_ACT_SRELU). G = E + n_shared; experts E.. are shared: every token, weight 1.
+ * Activations as in moe_config_t. y is rounded once to dtype (the second
+ * product's operand); the sums are fp32 and out is rounded once.
+ *
+ * Routing: W_r [H, E] fp32 gives the logits x . W_r, or logits [T, E] fp32 are
+ * given; then topk_ids [T, k] and topk_w [T, k] (fp32) are outputs: the k largest
+ * logits (ties to the lower id; a NaN ranks as -inf and sets
+ * MOE_DEV_NAN_LOGIT), their softmax times routed_scale. A logit of -inf masks its
+ * expert: weight 0, and a token without a finite logit gets weights 0. With both
+ * NULL, topk_ids and topk_w are inputs (an id may repeat; one outside [0, E) is skipped and sets
+ * MOE_DEV_BAD_EXPERT_ID). Slots of weight 0 are left out: their expert's weights are not read for them.
+ *
+ * k <= 32 - n_shared, G <= 2048, n_shared 0 or 1, any H and I up to 2^20. x, w1, w2 and ws
+ * start on 16 bytes, ldx, ldw1, ldw2 and the group strides are multiples of 8
+ * elements. T > MOE_LAYER16_MAX_T: MOE_ERR_UNSUPPORTED (the grouped products are
+ * for those). ws: moe_layer16_workspace_size bytes for T tokens (a larger T's
+ * suffices), starting with the status word (moe_mm_read_status); zero it once. */
+#define MOE_LAYER16_MAX_T 64
+moe_status_t moe_layer16_forward(const void* x, int64_t ldx, const float* W_r, const float* logits, const void* w1,
+                                 int64_t w1_group, int64_t ldw1, const float* b1, const void* w2, int64_t w2_group,
+                                 int64_t ldw2, int T, int H, int I, int E, int k, int n_shared, int act, float alpha,
+                                 float limit, float routed_scale, int dtype, void* out, int64_t ldo, int32_t* topk_ids,
+                                 float* topk_w, void* ws, size_t ws_bytes, void* stream);
+
+/* Host only. */
+moe_status_t moe_layer16_workspace_size(int T, int H, int I, int E, int k, int n_shared, size_t* bytes);
 
 /* Synchronises `stream`, copies the status word of a products' workspace to
  * *out (host) and clears it, as moe_read_status does for the layer's. */

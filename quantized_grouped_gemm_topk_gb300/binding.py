@@ -27,12 +27,16 @@ MOE_DEV_BAD_OFFSETS = 0x10
 MOE_ACT_SWIGLU, MOE_ACT_SWIGLU_CLAMP, MOE_ACT_GEGLU, MOE_ACT_SRELU = 0, 1, 2, 3
 ACTS = {"swiglu": MOE_ACT_SWIGLU, "swiglu_clamp": MOE_ACT_SWIGLU_CLAMP, "geglu": MOE_ACT_GEGLU,
         "srelu": MOE_ACT_SRELU}
+# further activations of the dense products
+MOE_ACT_NONE, MOE_ACT_GELU, MOE_ACT_SILU = 4, 5, 6
+LINEAR_ACTS = {**ACTS, "none": MOE_ACT_NONE, "gelu": MOE_ACT_GELU, "silu": MOE_ACT_SILU}
 MOE_WFMT_NVFP4, MOE_WFMT_MXFP8, MOE_WFMT_MXFP4 = 0, 1, 2
 WFMTS = {"nvfp4": MOE_WFMT_NVFP4, "mxfp8": MOE_WFMT_MXFP8, "mxfp4": MOE_WFMT_MXFP4}
 MOE_PACK_FORWARD, MOE_PACK_DGRAD = 0, 1
 MOE_DT_BF16, MOE_DT_F16, MOE_DT_F32 = 0, 1, 2
 DTYPES = {torch.bfloat16: MOE_DT_BF16, torch.float16: MOE_DT_F16, torch.float32: MOE_DT_F32}
 MOE_MM_ROWS, MOE_MM_WGRAD, MOE_MM_FP8 = 0, 1, 2
+MOE_LAYER16_MAX_T = 64
 FP8_BLOCK = 128     # elements that share a scale in the FP8 products and the activation checkpoints
 
 # every exported symbol the header declares
@@ -46,6 +50,8 @@ EXPORTS = (
     "moe_layer_norm_forward", "moe_layer_norm_backward", "moe_layer_norm_workspace_size",
     "moe_act_ckpt_forward", "moe_act_ckpt_backward", "moe_mm_workspace_size", "moe_grouped_mm",
     "moe_grouped_mm_wgrad", "moe_fp8_quant_rows", "moe_fp8_quant_weights", "moe_fp8_mm", "moe_mm_read_status",
+    "moe_linear_forward", "moe_linear_backward", "moe_linear_workspace_size", "moe_layer16_forward",
+    "moe_layer16_workspace_size",
 )
 MOE_N_PHASE_EVENTS = 6
 
@@ -140,6 +146,11 @@ def load(path: str | None = None) -> ctypes.CDLL:
         "moe_fp8_quant_weights": [P, L, L, N, N, N, N, P, L, L, P, P, L, L, P, P],
         "moe_fp8_mm": [P, L, P, L, P, L, L, P, P, N, N, N, N, P, L, N, P, Z, P],
         "moe_mm_read_status": [P, ctypes.POINTER(ctypes.c_int32), P],
+        "moe_linear_forward": [P, L, P, L, P, P, L, N, N, N, N, F, F, N, N, P, L, P, L, P, Z, P],
+        "moe_linear_backward": [P, L, P, L, P, L, P, L, N, N, N, N, F, F, N, N, P, L, P, L, P, L, P, P, Z, P],
+        "moe_linear_workspace_size": [N, N, N, N, ctypes.POINTER(Z)],
+        "moe_layer16_forward": [P, L, P, P, P, L, L, P, P, L, L, N, N, N, N, N, N, N, F, F, F, N, P, L, P, P, P, Z, P],
+        "moe_layer16_workspace_size": [N, N, N, N, N, N, ctypes.POINTER(Z)],
     }
     for name, args in sig.items():
         f = getattr(lib, name)
@@ -630,6 +641,94 @@ def moe_fp8_mm(xq, xs, wq, wscale, out, ws, offsets=None, stream=None):
         _flat(offsets, "offsets", _I32, (G + 1,), dev), R, N, K, G, _arg(out, "out", _FLOATS, (R, N), dev),
         _ld(out, "out"),
         DTYPES[out.dtype], wp, wn, _stream(stream)))
+
+
+def moe_linear_workspace_size(R, rows, K, backward=False) -> int:
+    """Bytes of workspace for moe_linear_forward or _backward with weights [rows, K] and R rows or fewer."""
+    n = ctypes.c_size_t()
+    _check("moe_linear_workspace_size", load().moe_linear_workspace_size(R, rows, K, int(backward), ctypes.byref(n)))
+    return n.value
+
+
+def _opt(t, name, dtypes, shape, dev):
+    """(address, row stride) of an optional matrix."""
+    return (None, 0) if t is None else (_arg(t, name, dtypes, shape, dev), _ld(t, name))
+
+
+def moe_linear_forward(x, w, out, ws, bias=None, residual=None, z=None, act="none", alpha=1.0, limit=0.0, stream=None):
+    """out [R, N] = act(x w^T + bias) + residual: x [R, K], w [N, K] (gated acts: [2 N, K], gate rows then up rows), bias
+    [rows of w] in x's type or fp32, residual [R, N] (may be out itself), z [R, rows of w]: receives the pre-activation;
+    the last three each None to skip. bf16 or f16. act: "none", "gelu", "silu", "srelu", "swiglu", "swiglu_clamp",
+    "geglu". ws: moe_linear_workspace_size(R, rows of w, K) bytes, zeroed once."""
+    dev = _device()
+    R, K = _dims(x, "x", 2)
+    N = _dims(out, "out", 2)[1]
+    a = LINEAR_ACTS[act]
+    rows = 2 * N if a < MOE_ACT_SRELU else N
+    own = (x.dtype,)
+    wt = torch.float32 if bias is None else bias.dtype
+    rp, rl = _opt(residual, "residual", own, (R, N), dev)
+    zp, zl = _opt(z, "z", own, (R, rows), dev)
+    wp, wn = _ws(ws, dev)
+    _check("moe_linear_forward", load().moe_linear_forward(
+        _arg(x, "x", _16BIT, (R, K), dev), _ld(x, "x", 8), _arg(w, "w", own, (rows, K), dev), _ld(w, "w", 8),
+        _flat(bias, "bias", (x.dtype, torch.float32), (rows,), dev), rp, rl, R, N, K, a, alpha, limit, DTYPES[x.dtype],
+        DTYPES[wt], zp, zl, _arg(out, "out", own, (R, N), dev), _ld(out, "out"), wp, wn, _stream(stream)))
+
+
+def moe_linear_backward(dout, x, w, z, dz, dx, dw, db, ws, act="none", alpha=1.0, limit=0.0, stream=None):
+    """Gradients of moe_linear_forward from its z [R, rows of w]: dz (z's shape, written), dx [R, K], dw (w's shape), db
+    [rows of w] in x's type or fp32; dx, dw, db each None to skip. act "none": z and dz are None (dz is dout). ws:
+    moe_linear_workspace_size(R, rows of w, K, backward=True) bytes, zeroed once."""
+    dev = _device()
+    R, K = _dims(x, "x", 2)
+    N = _dims(dout, "dout", 2)[1]
+    a = LINEAR_ACTS[act]
+    rows = 2 * N if a < MOE_ACT_SRELU else N
+    own = (x.dtype,)
+    wt = torch.float32 if db is None else db.dtype
+    if a == MOE_ACT_NONE and (z is not None or dz is not None):
+        raise ValueError("act \"none\" takes no z and no dz")
+    zp, zl = _opt(z, "z", own, (R, rows), dev)
+    gp = None if dz is None else _arg(dz, "dz", own, (R, rows), dev)
+    xp, xl = _opt(dx, "dx", own, (R, K), dev)
+    dp, dl = _opt(dw, "dw", own, (rows, K), dev)
+    wp, wn = _ws(ws, dev)
+    _check("moe_linear_backward", load().moe_linear_backward(
+        _arg(dout, "dout", own, (R, N), dev), _ld(dout, "dout", 8 if a == MOE_ACT_NONE else 1),
+        _arg(x, "x", _16BIT, (R, K), dev), _ld(x, "x", 8), _arg(w, "w", own, (rows, K), dev), _ld(w, "w", 8), zp, zl, R, N,
+        K, a, alpha, limit, DTYPES[x.dtype], DTYPES[wt], gp, 0 if dz is None else _ld(dz, "dz", 8), xp, xl, dp, dl,
+        _flat(db, "db", (x.dtype, torch.float32), (rows,), dev), wp, wn, _stream(stream)))
+
+
+def moe_layer16_workspace_size(T, H, I, E, k, n_shared=0) -> int:
+    """Bytes of workspace for moe_layer16_forward of T tokens or fewer."""
+    n = ctypes.c_size_t()
+    _check("moe_layer16_workspace_size", load().moe_layer16_workspace_size(T, H, I, E, k, n_shared, ctypes.byref(n)))
+    return n.value
+
+
+def moe_layer16_forward(x, W_r, logits, w1, w2, out, topk_ids, topk_w, ws, b1=None, n_shared=0, act="swiglu", alpha=1.0,
+                        limit=0.0, routed_scale=1.0, stream=None):
+    """The whole layer with 16-bit experts for up to MOE_LAYER16_MAX_T tokens: x, out [T, H], w1 [G, 2 I, H] (gate rows
+    then up rows; sReLU [G, I, H]), w2 [G, H, I] in bf16 or f16, G = E + n_shared, b1 [G, 2 I] fp32 or None. The router's
+    weights W_r [H, E] or the logits [T, E] (fp32): topk_ids [T, k] int32 and topk_w [T, k] fp32 are written; both None:
+    they are read. ws: moe_layer16_workspace_size(T, H, I, E, k, n_shared) bytes, zeroed once."""
+    dev = _device()
+    T, H = _dims(x, "x", 2)
+    G, _, I = _dims(w2, "w2", 3)
+    k = _dims(topk_ids, "topk_ids", 2)[1]
+    E = G - n_shared
+    rows = I if act == "srelu" else 2 * I
+    own = (x.dtype,)
+    wp, wn = _ws(ws, dev)
+    _check("moe_layer16_forward", load().moe_layer16_forward(
+        _arg(x, "x", _16BIT, (T, H), dev), _ld(x, "x", 8), _flat(W_r, "W_r", _F32, (H, E), dev),
+        _flat(logits, "logits", _F32, (T, E), dev), _arg(w1, "w1", own, (G, rows, H), dev), _group(w1), _ld(w1, "w1", 8),
+        _flat(b1, "b1", _F32, (G, 2 * I), dev), _arg(w2, "w2", own, (G, H, I), dev), _group(w2), _ld(w2, "w2", 8), T, H, I,
+        E, k, n_shared, ACTS[act], alpha, limit, routed_scale, DTYPES[x.dtype], _arg(out, "out", own, (T, H), dev),
+        _ld(out, "out"), _flat(topk_ids, "topk_ids", _I32, (T, k), dev), _flat(topk_w, "topk_w", _F32, (T, k), dev), wp,
+        wn, _stream(stream)))
 
 
 def moe_mm_read_status(ws, stream=None) -> int:

@@ -50,6 +50,23 @@ void mm_workspace(MmArgs& a, int kind, void* ws) {
   a.part = a.S > 1 ? reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(ws) + kStatusBytes) : nullptr;
 }
 
+// The dense products' activations, and sizes (a gated one has 2 N weight rows).
+bool linear_act_ok(int act, float limit) {
+  return act_ok(act, limit) || act == MOE_ACT_NONE || act == MOE_ACT_GELU || act == MOE_ACT_SILU;
+}
+bool linear_sizes_ok(int R, int N, int K, int act) {
+  return R >= 0 && R <= kMost && N >= 1 && N <= (act_gated(act) ? kMost / 2 : kMost) && width_ok(K);
+}
+void linear_workspace(LinearArgs& a, void* ws) {
+  a.status = reinterpret_cast<int32_t*>(ws);
+  a.part = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(ws) + kStatusBytes);
+}
+bool layer16_sizes_ok(int T, int H, int I, int E, int k, int S) {
+  constexpr int kWide = 1 << 20;
+  return T >= 0 && H >= 1 && H <= kWide && I >= 1 && I <= kWide && (S == 0 || S == 1) && E >= 1 && E <= 2048 - S &&
+         k >= 1 && k <= E && k + S <= 32;
+}
+
 }  // namespace
 
 extern "C" {
@@ -227,6 +244,110 @@ moe_status_t moe_fp8_mm(const uint8_t* xq, int64_t ldx, const float* xs, int64_t
   a.out = out; a.ldo = ldo; a.out_dtype = out_dtype;
   mm_workspace(a, MOE_MM_FP8, ws);
   return done(launch_mm_fp8(a, (cudaStream_t)stream));
+}
+
+moe_status_t moe_linear_workspace_size(int R, int rows, int K, int backward, size_t* bytes) {
+  if (!bytes || R < 0 || R > kMost || !width_ok(rows) || !width_ok(K) || (backward != 0 && backward != 1))
+    return MOE_ERR_INVALID_ARG;
+  *bytes = kStatusBytes + (size_t)linear_part_bytes(R, rows, K, backward != 0);
+  return MOE_OK;
+}
+
+moe_status_t moe_linear_forward(const void* x, int64_t ldx, const void* w, int64_t ldw, const void* bias,
+                                const void* residual, int64_t ldr, int R, int N, int K, int act, float alpha,
+                                float limit, int dtype, int wdtype, void* z, int64_t ldz, void* out, int64_t ldo,
+                                void* ws, size_t ws_bytes, void* stream) {
+  if (!linear_act_ok(act, limit) || !linear_sizes_ok(R, N, K, act)) return MOE_ERR_INVALID_ARG;
+  const int rows = act_gated(act) ? 2 * N : N;
+  if (!is16(dtype) || (wdtype != MOE_DT_F32 && wdtype != dtype)) return MOE_ERR_INVALID_ARG;
+  if (ldx < K || ldw < K || ldx % 8 || ldw % 8 || ldo < N) return MOE_ERR_INVALID_ARG;
+  if ((residual && ldr < N) || (z && ldz < rows) || (residual == out && residual && ldr != ldo)) return MOE_ERR_INVALID_ARG;
+  if (!have(w, 16) || !maybe(bias, size_of(wdtype)) || !maybe(residual, 2) || !maybe(z, 2)) return MOE_ERR_INVALID_ARG;
+  if (!have(ws, 16)) return MOE_ERR_INVALID_ARG;
+  size_t need = 0;
+  const moe_status_t s = moe_linear_workspace_size(R, rows, K, 0, &need);
+  if (s != MOE_OK) return s;
+  if (ws_bytes < need) return MOE_ERR_WORKSPACE;
+  reset_launch_count();
+  if (R == 0) return MOE_OK;
+  if (!have(x, 16) || !have(out, 2)) return MOE_ERR_INVALID_ARG;
+  LinearArgs a = {};
+  a.R = R; a.N = N; a.K = K; a.act = ActParams{act, alpha, limit}; a.dtype = dtype; a.wdtype = wdtype;
+  a.x = x; a.ldx = ldx; a.w = w; a.ldw = ldw; a.bias = bias; a.res = residual; a.ldr = ldr; a.z = z; a.ldz = ldz;
+  a.out = out; a.ldo = ldo;
+  linear_workspace(a, ws);
+  return done(launch_linear_fwd(a, (cudaStream_t)stream));
+}
+
+moe_status_t moe_linear_backward(const void* dout, int64_t lddout, const void* x, int64_t ldx, const void* w,
+                                 int64_t ldw, const void* z, int64_t ldz, int R, int N, int K, int act, float alpha,
+                                 float limit, int dtype, int wdtype, void* dz, int64_t lddz, void* dx, int64_t lddx,
+                                 void* dw, int64_t lddw, void* db, void* ws, size_t ws_bytes, void* stream) {
+  if (!linear_act_ok(act, limit) || !linear_sizes_ok(R, N, K, act)) return MOE_ERR_INVALID_ARG;
+  const int rows = act_gated(act) ? 2 * N : N;
+  const bool plain = act == MOE_ACT_NONE;
+  if (!is16(dtype) || (wdtype != MOE_DT_F32 && wdtype != dtype)) return MOE_ERR_INVALID_ARG;
+  if (lddout < N || ldx < K || ldw < K || ldx % 8 || ldw % 8 || (dx && lddx < K) || (dw && lddw < K))
+    return MOE_ERR_INVALID_ARG;
+  if (plain ? lddout % 8 != 0 : (ldz < rows || lddz < rows || lddz % 8)) return MOE_ERR_INVALID_ARG;
+  if (!maybe(dx, 2) || !maybe(dw, 2) || !maybe(db, size_of(wdtype)) || !maybe(x, 16) || !maybe(w, 16))
+    return MOE_ERR_INVALID_ARG;
+  if (!have(ws, 16)) return MOE_ERR_INVALID_ARG;
+  size_t need = 0;
+  const moe_status_t s = moe_linear_workspace_size(R, rows, K, 1, &need);
+  if (s != MOE_OK) return s;
+  if (ws_bytes < need) return MOE_ERR_WORKSPACE;
+  cudaStream_t st = (cudaStream_t)stream;
+  reset_launch_count();
+  if (R == 0) {     // the sums over no rows
+    const size_t width = (size_t)K * 2;
+    if (dw && cudaMemset2DAsync(dw, (size_t)lddw * 2, 0, width, rows, st) != cudaSuccess) return MOE_ERR_CUDA;
+    if (db && cudaMemsetAsync(db, 0, rows * size_of(wdtype), st) != cudaSuccess) return MOE_ERR_CUDA;
+    return MOE_OK;
+  }
+  if (!have(dout, plain ? 16 : 2) || (!plain && (!have(z, 2) || !have(dz, 16)))) return MOE_ERR_INVALID_ARG;
+  if ((dx && !w) || (dw && !x)) return MOE_ERR_INVALID_ARG;
+  LinearArgs a = {};
+  a.R = R; a.N = N; a.K = K; a.act = ActParams{act, alpha, limit}; a.dtype = dtype; a.wdtype = wdtype;
+  a.x = x; a.ldx = ldx; a.w = w; a.ldw = ldw; a.z = const_cast<void*>(z); a.ldz = ldz; a.dout = dout; a.lddout = lddout;
+  a.dz = dz; a.lddz = lddz; a.dx = dx; a.lddx = lddx; a.dw = dw; a.lddw = lddw; a.db = db;
+  linear_workspace(a, ws);
+  return done(launch_linear_bwd(a, st));
+}
+
+moe_status_t moe_layer16_workspace_size(int T, int H, int I, int E, int k, int n_shared, size_t* bytes) {
+  if (!bytes || !layer16_sizes_ok(T, H, I, E, k, n_shared)) return MOE_ERR_INVALID_ARG;
+  if (T > MOE_LAYER16_MAX_T) return MOE_ERR_UNSUPPORTED;
+  *bytes = kStatusBytes + (size_t)layer16_ws_bytes(T, H, I, E, k, n_shared);
+  return MOE_OK;
+}
+
+moe_status_t moe_layer16_forward(const void* x, int64_t ldx, const float* W_r, const float* logits, const void* w1,
+                                 int64_t w1_group, int64_t ldw1, const float* b1, const void* w2, int64_t w2_group,
+                                 int64_t ldw2, int T, int H, int I, int E, int k, int n_shared, int act, float alpha,
+                                 float limit, float routed_scale, int dtype, void* out, int64_t ldo, int32_t* topk_ids,
+                                 float* topk_w, void* ws, size_t ws_bytes, void* stream) {
+  if (!act_ok(act, limit) || !is16(dtype) || !(routed_scale > 0.f)) return MOE_ERR_INVALID_ARG;
+  size_t need = 0;
+  const moe_status_t s = moe_layer16_workspace_size(T, H, I, E, k, n_shared, &need);
+  if (s != MOE_OK) return s;
+  const int rows = act == MOE_ACT_SRELU ? I : 2 * I, G = E + n_shared;
+  if ((W_r && logits) || !maybe(W_r, 4) || !maybe(logits, 4) || (b1 && act == MOE_ACT_SRELU) || !maybe(b1, 4))
+    return MOE_ERR_INVALID_ARG;
+  if (ldx < H || ldw1 < H || ldw2 < I || ldo < H || ldx % 8 || ldw1 % 8 || ldw2 % 8) return MOE_ERR_INVALID_ARG;
+  if (G > 1 && (w1_group < span(rows, H, ldw1) || w2_group < span(H, I, ldw2) || w1_group % 8 || w2_group % 8))
+    return MOE_ERR_INVALID_ARG;
+  if (!have(w1, 16) || !have(w2, 16) || !have(ws, 16)) return MOE_ERR_INVALID_ARG;
+  if (ws_bytes < need) return MOE_ERR_WORKSPACE;
+  reset_launch_count();
+  if (T == 0) return MOE_OK;
+  if (!have(x, 16) || !have(out, 2) || !have(topk_ids, 4) || !have(topk_w, 4)) return MOE_ERR_INVALID_ARG;
+  Layer16Args a = {};
+  a.T = T; a.H = H; a.I = I; a.E = E; a.k = k; a.S = n_shared; a.act = ActParams{act, alpha, limit}; a.rs = routed_scale;
+  a.dtype = dtype; a.x = x; a.ldx = ldx; a.W_r = W_r; a.logits = logits; a.w1 = w1; a.g1 = w1_group; a.ld1 = ldw1;
+  a.b1 = b1; a.w2 = w2; a.g2 = w2_group; a.ld2 = ldw2; a.out = out; a.ldo = ldo; a.ids = topk_ids; a.w = topk_w;
+  a.status = reinterpret_cast<int32_t*>(ws); a.ws = reinterpret_cast<uint8_t*>(ws) + kStatusBytes;
+  return done(launch_layer16(a, (cudaStream_t)stream));
 }
 
 moe_status_t moe_mm_read_status(void* ws, int32_t* out, void* stream) {

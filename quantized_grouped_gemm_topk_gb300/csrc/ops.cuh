@@ -334,4 +334,91 @@ bool make_tmap(CUtensorMap* map, const void* base, int esize, int rank, const in
 cudaError_t launch_mm16(const MmArgs& a, bool wgrad, cudaStream_t st);
 cudaError_t launch_mm_fp8(const MmArgs& a, cudaStream_t st);
 
+// ---- dense products with an epilogue (linear.cu) --------------------------------
+// Whether an activation takes a gate and an up column.
+__host__ __device__ __forceinline__ bool act_gated(int act) { return act < MOE_ACT_SRELU; }
+// Phi(v) by erfc: 1 + erf(v / sqrt 2) cancels for negative v, where v Phi(v) is
+// small but not rounded away.
+__device__ __forceinline__ float cdf_(float v) { return 0.5f * erfcf(v * -0.70710678118654752f); }
+// Clamp that lets a NaN through.
+__device__ __forceinline__ float clamp_(float v, float lim) { return v > lim ? lim : (v < -lim ? -lim : v); }
+__device__ __forceinline__ float act_one(float z, int act) {
+  if (act == MOE_ACT_SRELU) return z <= 0.f ? 0.f : z * z;
+  if (act == MOE_ACT_GELU) return z * cdf_(z);
+  if (act == MOE_ACT_SILU) return z * sigmoidf_(z);
+  return z;
+}
+__device__ __forceinline__ float act_two(float g, float u, const ActParams& p) {
+  if (p.act == MOE_ACT_SWIGLU) return g * sigmoidf_(g) * u;
+  if (p.act == MOE_ACT_GEGLU) return g * cdf_(g) * u;
+  const float gc = clamp_(g, p.limit);
+  return gc * sigmoidf_(p.alpha * gc) * clamp_(u, p.limit);
+}
+// d act'(z), and d times the derivatives by gate and up.
+__device__ __forceinline__ float act_one_grad(float z, float d, int act) {
+  if (act == MOE_ACT_SRELU) return z <= 0.f ? 0.f : d * (2.f * z);
+  if (act == MOE_ACT_GELU) return d * (cdf_(z) + z * normal_pdf(z));
+  if (act == MOE_ACT_SILU) {
+    const float s = sigmoidf_(z);
+    return d * (s + z * s * (1.f - s));
+  }
+  return d;
+}
+__device__ __forceinline__ float2 act_two_grad(float g, float u, float d, const ActParams& p) {
+  if (p.act == MOE_ACT_SWIGLU) {
+    const float s = sigmoidf_(g);
+    return make_float2(d * ((s + g * s * (1.f - s)) * u), d * (g * s));
+  }
+  if (p.act == MOE_ACT_GEGLU) {
+    const float c = cdf_(g);
+    return make_float2(d * ((c + g * normal_pdf(g)) * u), d * (g * c));
+  }
+  const float gc = clamp_(g, p.limit), uc = clamp_(u, p.limit), s = sigmoidf_(p.alpha * gc), gs = gc * s;
+  // inclusive, as the layer's; a NaN counts as inside
+  const bool gin = !(fabsf(g) > p.limit), uin = !(fabsf(u) > p.limit);
+  return make_float2(gin ? d * ((s + p.alpha * gs * (1.f - s)) * uc) : 0.f, uin ? d * gs : 0.f);
+}
+
+struct LinearArgs {
+  int R, N, K;                  // N: output columns; weight rows: N, gated 2 N
+  ActParams act;
+  int dtype, wdtype;            // wdtype: of bias and db
+  const void* x; int64_t ldx;
+  const void* w; int64_t ldw;
+  const void* bias;             // nullable
+  const void* res; int64_t ldr; // nullable; may be out
+  void* z; int64_t ldz;         // forward: nullable output; backward: input
+  void* out; int64_t ldo;
+  const void* dout; int64_t lddout;
+  void* dz; int64_t lddz;
+  void* dx; int64_t lddx;
+  void* dw; int64_t lddw;
+  void* db;
+  int32_t* status;
+  float* part;
+};
+int64_t linear_part_bytes(int R, int rows, int K, bool backward);
+cudaError_t launch_linear_fwd(const LinearArgs& a, cudaStream_t st);
+cudaError_t launch_linear_bwd(const LinearArgs& a, cudaStream_t st);
+
+// ---- the layer for a few tokens (layer16.cu) -------------------------------------
+struct Layer16Args {
+  int T, H, I, E, k, S;         // S: shared experts
+  ActParams act;
+  float rs;
+  int dtype;
+  const void* x; int64_t ldx;
+  const float* W_r;             // router weights, or
+  const float* logits;          // logits, or neither: ids and w are inputs
+  const void* w1; int64_t g1, ld1;
+  const float* b1;              // nullable
+  const void* w2; int64_t g2, ld2;
+  void* out; int64_t ldo;
+  int32_t* ids; float* w;
+  uint8_t* ws;                  // past the status word
+  int32_t* status;
+};
+int64_t layer16_ws_bytes(int T, int H, int I, int E, int k, int S);
+cudaError_t launch_layer16(const Layer16Args& a, cudaStream_t st);
+
 }  // namespace moe

@@ -1,0 +1,282 @@
+"""The layer for a few tokens with 16-bit experts on the GPU, against its 64-bit form."""
+import math
+
+import pytest
+import torch
+
+import dense_ref as D
+import ops_ref as P
+import quantized_grouped_gemm_topk_gb300 as m
+
+from util import cuda_device
+
+pytestmark = pytest.mark.gpu
+
+BF16, F16, F32, I32 = torch.bfloat16, torch.float16, torch.float32, torch.int32
+NAN, INF = float("nan"), math.inf
+ALPHA, LIMIT = 1.702, 2.0
+
+
+def _gen(seed=0):
+    return torch.Generator(device="cuda").manual_seed(seed)
+
+
+def _randn(g, *shape, dtype=F32, std=1.0):
+    return (torch.randn(*shape, generator=g, device="cuda") * std).to(dtype)
+
+
+def _inputs(T, H, I, E, k, S, act, dtype, bias, pad, seed=0):
+    g = _gen(seed + T * 11 + H * 3 + I + E)
+    G = E + S
+    c = dict(x=P.strided(_randn(g, T, H, dtype=dtype), pad, whole=8)[0],
+             W_r=_randn(g, H, E, std=H ** -0.5),
+             w1=P.strided(_randn(g, G, D.halves(act) * I, H, dtype=dtype, std=1.5 * H ** -0.5), pad, whole=8)[0],
+             w2=P.strided(_randn(g, G, H, I, dtype=dtype, std=I ** -0.5), pad, whole=8)[0],
+             b1=_randn(g, G, 2 * I, std=0.3) if bias else None,
+             ids=torch.zeros(T, k, dtype=I32, device="cuda"), wts=torch.zeros(T, k, device="cuda"),
+             ws=torch.zeros(m.moe_layer16_workspace_size(T, H, I, E, k, S), dtype=torch.uint8, device="cuda"))
+    c["out"], c["obuf"] = P.strided(torch.zeros(T, H, dtype=dtype, device="cuda"), pad and 3)
+    return c
+
+
+def _run(c, act, S=0, W_r=None, logits=None, scale=1.0, out=None):
+    m.moe_layer16_forward(c["x"], W_r, logits, c["w1"], c["w2"], c["out"] if out is None else out, c["ids"], c["wts"], c["ws"],
+                          b1=c["b1"], n_shared=S, act=act, alpha=ALPHA, limit=LIMIT, routed_scale=scale)
+
+
+def _check_out(c, act, S):
+    ref, bound = D.layer(c["x"], c["w1"], c["w2"], c["b1"], c["ids"].long(), c["wts"], S, act, ALPHA, LIMIT)
+    P.assert_within(c["out"], ref, bound, "out")
+
+
+def _layer(T, H, I, E, k, S=0, act="swiglu", dtype=BF16, bias=False, pad=0, scale=1.0):
+    cuda_device()
+    c = _inputs(T, H, I, E, k, S, act, dtype, bias, pad)
+    _run(c, act, S, W_r=c["W_r"], scale=scale)
+    x, r = c["x"].double(), c["W_r"].double()
+    logits, b = x @ r, (H + 8) * P.EPS32 * (x.abs() @ r.abs()).amax(1, keepdim=True)
+    want, _ = D.routing(logits, k, scale)
+    ids = c["ids"].long()
+    assert bool((ids >= 0).all()) and bool((ids < E).all())
+    assert all(len(set(row)) == k for row in ids.tolist())
+    # ids may differ only where two logits are nearer than their sums' error
+    assert bool(((logits.gather(1, ids) - logits.gather(1, want)).abs() <= 2 * b).all())
+    p = torch.exp(logits.gather(1, ids) - logits.gather(1, ids).amax(1, keepdim=True))
+    w = p / p.sum(1, keepdim=True) * scale
+    # exp of a difference of two logits, twice (CUDA's expf: 2 units); k additions, a division and two products
+    P.assert_within(c["wts"], w, w * (4 * b + (k + 12) * P.EPS32), "weights")
+    _check_out(c, act, S)
+    if pad:
+        assert bool(torch.isnan(c["obuf"][:, H:].float()).all())
+    assert m.moe_mm_read_status(c["ws"]) == 0
+    return c
+
+
+@pytest.mark.parametrize("T,H,I,E,k,S", [
+    (1, 256, 128, 8, 2, 0), (1, 8, 8, 1, 1, 0), (2, 1, 1, 3, 2, 1), (3, 72, 40, 5, 5, 0), (5, 1999, 1001, 24, 3, 1), (8, 520, 264, 16, 4, 0),
+    (16, 640, 384, 160, 8, 1), (17, 300, 65, 7, 3, 0), (31, 129, 200, 40, 6, 0), (32, 1024, 512, 16, 4, 1), (33, 200, 129, 12, 2, 0),
+    (48, 264, 320, 3, 1, 0), (64, 576, 448, 64, 8, 0), (64, 128, 64, 2048, 32, 0), (64, 2880, 360, 32, 4, 0), (63, 64, 1031, 2, 2, 1),
+    (1, 7168, 256, 64, 8, 0), (4, 100, 3001, 2, 1, 0), (1, 17, 4096, 300, 31, 1)])
+@pytest.mark.parametrize("act,dtype,bias,pad", [("swiglu", BF16, False, 0), ("swiglu_clamp", F16, True, 8), ("geglu", BF16, True, 8),
+                                                ("srelu", F16, False, 0)])
+def test_layer16(T, H, I, E, k, S, act, dtype, bias, pad):
+    _layer(T, H, I, E, k, S, act, dtype, bias, pad, scale=2.5 if S else 1.0)
+
+
+@pytest.mark.parametrize("T", [1, 2, 16, 64])
+@pytest.mark.parametrize("H,I,E,k,S", [(2880, 2880, 16, 4, 0), (6144, 1536, 12, 8, 1), (7168, 2048, 9, 8, 0)])
+def test_layer16_of_model_widths(T, H, I, E, k, S):
+    _layer(T, H, I, E, k, S)
+
+
+@pytest.mark.parametrize("T,E,k", [(1, 8, 3), (9, 100, 8), (64, 33, 32), (5, 2047, 6)])
+def test_layer16_from_logits_ties_masks_and_nan(T, E, k):
+    """Ready logits: ties go to the lower id; -inf masks an expert, NaN ranks as -inf and is flagged; a token without a
+    finite logit has weights 0; a masked expert's weights may hold anything."""
+    cuda_device()
+    g = _gen(T + E)
+    c = _inputs(T, 72, 40, E, k, 0, "swiglu", BF16, False, 0)
+    logits = torch.randint(-2, 3, (T, E), generator=g, device="cuda").float()
+    logits[0] = torch.where(logits[0] == 0, torch.tensor(-0.0, device="cuda"), logits[0])
+    _run(c, "swiglu", logits=logits)
+    ids, w = D.routing(logits.double(), k, 1.0)
+    assert torch.equal(c["ids"].long(), ids)
+    P.assert_within(c["wts"], w, w * (k + 12) * P.EPS32, "weights")
+    _check_out(c, "swiglu", 0)
+    assert m.moe_mm_read_status(c["ws"]) == 0
+
+    logits[:, 1:] = torch.where(torch.rand(T, E - 1, generator=g, device="cuda") < 0.7, torch.tensor(-INF, device="cuda"), logits[:, 1:])
+    logits[:, E - 1] = -INF           # nobody's
+    logits[T - 1] = -INF
+    c["w1"][E - 1], c["w2"][E - 1] = NAN, INF
+    c["out"].fill_(NAN)
+    _run(c, "swiglu", logits=logits)
+    ids, w = D.routing(logits.double(), k, 1.0)
+    assert torch.equal(c["ids"].long(), ids)
+    assert torch.equal(c["wts"] == 0, w == 0) and not bool(c["wts"][T - 1].any())
+    assert not bool(c["out"][T - 1].any())
+    safe = {**c, "w1": c["w1"].clone(), "w2": c["w2"].clone()}
+    safe["w1"][E - 1], safe["w2"][E - 1] = 0, 0
+    _check_out(safe, "swiglu", 0)
+
+    logits[0, 0] = NAN
+    _run(c, "swiglu", logits=logits)
+    ids, w = D.routing(logits.double(), k, 1.0)
+    assert torch.equal(c["ids"].long(), ids)
+    assert m.moe_mm_read_status(c["ws"]) == m.MOE_DEV_NAN_LOGIT
+    assert m.moe_mm_read_status(c["ws"]) == 0
+
+
+def test_layer16_from_given_ids():
+    """Ids and weights of the caller: an id may repeat, its weights add up; one out of range is skipped and flagged; weights
+    are taken as they are (negative ones too)."""
+    cuda_device()
+    g = _gen(4)
+    T, E, k, S = 21, 6, 5, 1
+    c = _inputs(T, 200, 136, E, k, S, "geglu", F16, True, 8)
+    c["ids"].copy_(torch.randint(0, E, (T, k), generator=g, device="cuda"))
+    c["wts"].copy_(_randn(g, T, k))
+    c["wts"][3] = 0
+    before = c["ids"].clone(), c["wts"].clone()
+    _run(c, "geglu", S)
+    _check_out(c, "geglu", S)
+    assert torch.equal(c["ids"], before[0]) and torch.equal(c["wts"], before[1])
+    assert m.moe_mm_read_status(c["ws"]) == 0
+    c["ids"][2, 1], c["ids"][20, 4] = -1, E
+    _run(c, "geglu", S)
+    _check_out(c, "geglu", S)
+    assert m.moe_mm_read_status(c["ws"]) == m.MOE_DEV_BAD_EXPERT_ID
+
+
+def test_layer16_tokens_do_not_reach_each_other():
+    """A NaN or infinity in one token, or in an expert that only it chose, leaves the others' bits alone."""
+    cuda_device()
+    T, H, I, E, k = 19, 328, 200, 8, 2
+    c = _inputs(T, H, I, E, k, 0, "swiglu", BF16, False, 0)
+    g = _gen(2)
+    c["ids"].copy_(torch.stack([torch.randperm(E - 1, generator=g, device="cuda")[:k] for _ in range(T)]))
+    c["wts"].copy_(torch.rand(T, k, generator=g, device="cuda") + 0.1)
+    c["ids"][5, 1] = E - 1
+    _run(c, "swiglu")
+    want = c["out"].clone()
+    others = [t for t in range(T) if t != 5]
+    c["w1"][E - 1, 3, 7] = INF
+    c["w2"][E - 1] = NAN
+    _run(c, "swiglu")
+    assert torch.equal(c["out"][others], want[others]) and bool(torch.isnan(c["out"][5].float()).all())
+    c["w1"][E - 1], c["w2"][E - 1] = 0, 0
+    c["x"][5, H - 1] = NAN
+    _run(c, "swiglu")
+    assert torch.equal(c["out"][others], want[others]) and bool(torch.isnan(c["out"][5].float()).all())
+
+
+def test_layer16_repeats_streams_graphs_and_a_shared_workspace():
+    cuda_device()
+    big = _inputs(64, 640, 384, 24, 4, 1, "swiglu", BF16, False, 0)
+    sets = [(big, 1)]
+    small = _inputs(3, 640, 384, 24, 4, 1, "swiglu", BF16, False, 0, seed=9)
+    small["ws"] = big["ws"]           # one for the largest batch serves a smaller one
+    sets.append((small, 1))
+    wants = []
+    for c, S in sets:
+        _run(c, "swiglu", S, W_r=c["W_r"])
+        wants.append(c["out"].clone())
+    for _ in range(4):
+        for (c, S), want in zip(sets, wants):
+            c["out"].fill_(NAN)
+            _run(c, "swiglu", S, W_r=c["W_r"])
+            assert torch.equal(c["out"], want)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        for c, S in sets:
+            c["out"].fill_(NAN)
+            _run(c, "swiglu", S, W_r=c["W_r"])
+    side.synchronize()
+    graphs = []
+    for (c, S), want in zip(sets, wants):
+        assert torch.equal(c["out"], want)
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            _run(c, "swiglu", S, W_r=c["W_r"])
+        graphs.append(graph)
+    for _ in range(3):
+        for graph, (c, S), want in zip(graphs, sets, wants):
+            c["out"].fill_(NAN)
+            graph.replay()
+            torch.cuda.synchronize()
+            assert torch.equal(c["out"], want)
+    assert m.moe_mm_read_status(big["ws"]) == 0
+
+
+def test_layer16_of_two_streams_at_once():
+    """Two calls that may run at the same time, each with its own workspace."""
+    cuda_device()
+    cs = [_inputs(40, 1024, 512, 16, 4, 0, "swiglu", BF16, False, 0, seed=s) for s in (1, 2)]
+    wants = []
+    for c in cs:
+        _run(c, "swiglu", W_r=c["W_r"])
+        wants.append(c["out"].clone())
+        c["out"].fill_(NAN)
+    streams = [torch.cuda.Stream() for _ in cs]
+    for s in streams:
+        s.wait_stream(torch.cuda.current_stream())
+    for _ in range(20):
+        for c, s in zip(cs, streams):
+            with torch.cuda.stream(s):
+                _run(c, "swiglu", W_r=c["W_r"])
+    torch.cuda.synchronize()
+    for c, want in zip(cs, wants):
+        assert torch.equal(c["out"], want)
+        assert m.moe_mm_read_status(c["ws"]) == 0
+
+
+def test_layer16_weights_past_32_bits():
+    """Experts whose matrices lie beyond 2^31 elements."""
+    cuda_device()
+    if torch.cuda.get_device_properties(0).total_memory < 60 << 30:
+        pytest.skip("needs 60 GB")
+    T, H, I, E, k = 3, 4096, 2048, 140, 2
+    w1 = torch.zeros(E, 2 * I, H, dtype=BF16, device="cuda")
+    w2 = torch.zeros(E, H, I, dtype=BF16, device="cuda")
+    assert w1.numel() > 2 ** 31
+    c = _inputs(T, H, I, 2, k, 0, "swiglu", BF16, False, 0)
+    w1[0], w1[E - 1], w2[0], w2[E - 1] = c["w1"][0], c["w1"][1], c["w2"][0], c["w2"][1]
+    ids = torch.tensor([[0, E - 1]] * T, dtype=I32, device="cuda")
+    c["wts"].fill_(0.5)
+    out = torch.empty(T, H, dtype=BF16, device="cuda")
+    ws = torch.zeros(m.moe_layer16_workspace_size(T, H, I, E, k), dtype=torch.uint8, device="cuda")
+    m.moe_layer16_forward(c["x"], None, None, w1, w2, out, ids, c["wts"], ws)
+    ref, bound = D.layer(c["x"], c["w1"], c["w2"], None, torch.tensor([[0, 1]] * T, device="cuda"), c["wts"], 0, "swiglu", 1.0, 0.0)
+    P.assert_within(out, ref, bound, "out")
+
+
+def test_layer16_no_tokens():
+    cuda_device()
+    c = _inputs(1, 64, 64, 4, 2, 0, "swiglu", BF16, False, 0)
+    m.moe_layer16_forward(c["x"][:0], c["W_r"], None, c["w1"], c["w2"], c["out"][:0], c["ids"][:0], c["wts"][:0], c["ws"])
+    assert m.moe_last_launch_count() == 0
+
+
+def test_decode_block_of_the_operators():
+    """A decode step as it is used: norm, the routed layer beside a dense shared part that adds to it, and the residual."""
+    cuda_device()
+    T, H, I, E, k = 6, 512, 256, 16, 4
+    c = _inputs(T, H, I, E, k, 0, "swiglu", BF16, False, 0)
+    g = _gen(77)
+    h = _randn(g, T, H, dtype=BF16)
+    gamma = _randn(g, H) * 0.1 + 1
+    m.moe_layer_norm_forward(h, gamma, None, 1e-5, c["x"])
+    P.assert_within(c["x"], P.norm_fwd(h, gamma, None, 1e-5)[0], torch.full((T, H), 1e-4, dtype=torch.float64, device="cuda"), "norm")
+    _run(c, "swiglu", W_r=c["W_r"])
+    _check_out(c, "swiglu", 0)
+    u, d = _randn(g, 2 * I, H, dtype=BF16, std=H ** -0.5), _randn(g, H, I, dtype=BF16, std=I ** -0.5)
+    a = torch.empty(T, I, dtype=BF16, device="cuda")
+    ws = torch.zeros(max(m.moe_linear_workspace_size(T, 2 * I, H), m.moe_linear_workspace_size(T, H, I)), dtype=torch.uint8, device="cuda")
+    m.moe_linear_forward(c["x"], u, a, ws, act="swiglu")
+    ra, ba, _, _ = D.linear(c["x"], u, None, None, "swiglu", 1.0, 0.0)
+    P.assert_within(a, ra, ba, "shared part")
+    routed = c["out"].clone()
+    m.moe_linear_forward(a, d, c["out"], ws, residual=c["out"])
+    ro, bo, _, _ = D.linear(a, d, None, routed, "none", 1.0, 0.0)
+    P.assert_within(c["out"], ro, bo, "out")

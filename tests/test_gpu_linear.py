@@ -1,0 +1,298 @@
+"""The dense product with bias, activation and residual on the GPU, forward and
+backward, against its 64-bit form."""
+import math
+
+import pytest
+import torch
+
+import dense_ref as D
+import ops_ref as P
+import quantized_grouped_gemm_topk_gb300 as m
+
+from util import cuda_device
+
+pytestmark = pytest.mark.gpu
+
+BF16, F16, F32 = torch.bfloat16, torch.float16, torch.float32
+NAN = float("nan")
+ALPHA, LIMIT = 1.702, 2.0
+
+
+def _gen(seed=0):
+    return torch.Generator(device="cuda").manual_seed(seed)
+
+
+def _randn(g, *shape, dtype=F32, std=1.0):
+    return (torch.randn(*shape, generator=g, device="cuda") * std).to(dtype)
+
+
+def _rows(g, r, c, dtype, std=1.0, pad=0):
+    """Rows that tensor copies take: a stride of a multiple of 8 elements, NaN behind each row."""
+    return P.strided(_randn(g, r, c, dtype=dtype, std=std), pad, whole=8)[0]
+
+
+def _ws(R, rows, K, backward=False):
+    return torch.zeros(m.moe_linear_workspace_size(R, rows, K, backward), dtype=torch.uint8, device="cuda")
+
+
+def _canary(buf, cols, what):
+    assert bool(torch.isnan(buf[..., cols:].float()).all()), f"{what}: wrote past its rows"
+
+
+def _forward(R, N, K, act, dtype, wdtype=F32, bias=True, residual=True, save=True, pad=0, seed=0):
+    cuda_device()
+    g = _gen(seed + R * 7 + N * 3 + K)
+    rows = D.halves(act) * N
+    x, w = _rows(g, R, K, dtype, pad=8 if pad else 0), _rows(g, rows, K, dtype, std=1.5 * K ** -0.5)
+    b = _randn(g, rows, dtype=wdtype, std=0.3) if bias else None
+    res = P.strided(_randn(g, R, N, dtype=dtype), pad)[0] if residual else None
+    out, obuf = P.strided(torch.zeros(R, N, dtype=dtype, device="cuda"), pad)
+    z, zbuf = P.strided(torch.zeros(R, rows, dtype=dtype, device="cuda"), pad) if save else (None, None)
+    ws = _ws(R, rows, K)
+    m.moe_linear_forward(x, w, out, ws, bias=b, residual=res, z=z, act=act, alpha=ALPHA, limit=LIMIT)
+    ro, bo, rz, bz = D.linear(x, w, b, res, act, ALPHA, LIMIT)
+    P.assert_within(out, ro, bo, "out")
+    if save:
+        P.assert_within(z, rz, bz, "z")
+        if pad:
+            _canary(zbuf, rows, "z")
+    if pad:
+        _canary(obuf, N, "out")
+    assert m.moe_mm_read_status(ws) == 0
+    return x, w, b, res, out, z, ws
+
+
+SIZES = [(1, 1, 1), (1, 7168, 72), (3, 40, 129), (16, 130, 2048), (17, 64, 64), (64, 264, 200), (65, 257, 1000), (128, 72, 640),
+         (130, 520, 96), (200, 1031, 333), (257, 256, 2049), (700, 100, 65), (1100, 640, 128)]
+
+
+@pytest.mark.parametrize("R,N,K", SIZES)
+@pytest.mark.parametrize("act", D.ACTS)
+def test_linear_forward(R, N, K, act):
+    _forward(R, N, K, act, BF16)
+
+
+@pytest.mark.parametrize("R,N,K", SIZES)
+@pytest.mark.parametrize("act", ["none", "gelu", "swiglu", "geglu"])
+@pytest.mark.parametrize("kw", [dict(dtype=F16, wdtype=F16, pad=3), dict(dtype=F16, bias=False, residual=False, save=False, pad=8),
+                                dict(dtype=BF16, wdtype=BF16, residual=False, pad=1), dict(dtype=BF16, bias=False, save=False)],
+                         ids=["f16-all", "f16-bare", "bf16-bias-z", "bf16-residual"])
+def test_linear_forward_options(R, N, K, act, kw):
+    _forward(R, N, K, act, **kw)
+
+
+@pytest.mark.parametrize("R,N,K", [(1, 4096, 7168), (8, 7168, 2048), (33, 2880, 2880), (64, 2048, 4096), (300, 2880, 1000),
+                                   (4096, 512, 96), (2500, 2880, 200), (5001, 1100, 520), (1, 40000, 64)])
+@pytest.mark.parametrize("act", ["none", "swiglu_clamp", "silu"])
+def test_linear_forward_of_many_tiles(R, N, K, act):
+    _forward(R, N, K, act, BF16, residual=act == "none", save=act != "none")
+
+
+def test_linear_residual_in_place_and_repeatable():
+    cuda_device()
+    for R in (5, 90, 700):
+        x, w, b, res, out, _, ws = _forward(R, 328, 520, "none", BF16, save=False)
+        again = torch.empty_like(out)
+        m.moe_linear_forward(x, w, again, ws, bias=b, residual=res)
+        assert torch.equal(again, out)
+        m.moe_linear_forward(x, w, res, ws, bias=b, residual=res)
+        assert torch.equal(res, out)
+
+
+def test_linear_nan_and_infinity_stay_in_their_row():
+    cuda_device()
+    g = _gen(3)
+    for R, N, K, act in ((9, 96, 200, "swiglu"), (9, 96, 200, "swiglu_clamp"), (9, 96, 200, "srelu"), (300, 200, 136, "gelu"),
+                         (300, 200, 136, "swiglu_clamp"), (300, 200, 136, "none")):
+        x, w = _rows(g, R, K, BF16), _rows(g, D.halves(act) * N, K, BF16, std=K ** -0.5)
+        ws = _ws(R, D.halves(act) * N, K)
+        want, out = (torch.empty(R, N, dtype=BF16, device="cuda") for _ in range(2))
+        m.moe_linear_forward(x, w, want, ws, act=act, alpha=ALPHA, limit=LIMIT)
+        bad = x.clone()
+        bad[4, K - 1] = NAN
+        bad[7, 0] = math.inf
+        m.moe_linear_forward(torch.nn.functional.pad(bad, (0, 8 - K % 8 if K % 8 else 0))[:, :K], w, out, ws, act=act, alpha=ALPHA,
+                             limit=LIMIT)
+        keep = [r for r in range(R) if r not in (4, 7)]
+        assert torch.equal(out[keep], want[keep])
+        assert bool(torch.isnan(out[4].float()).all())
+
+
+def _backward(R, N, K, act, dtype, wdtype=F32, pad=0):
+    cuda_device()
+    g = _gen(R * 5 + N + K * 3)
+    rows = D.halves(act) * N
+    x, w = _rows(g, R, K, dtype), _rows(g, rows, K, dtype, std=K ** -0.5)
+    plain = act == "none"
+    dout = _rows(g, R, N, dtype) if plain else P.strided(_randn(g, R, N, dtype=dtype), pad)[0]
+    z = None if plain else P.strided(_randn(g, R, rows, dtype=dtype, std=1.5), pad)[0]
+    dz, zbuf = (None, None) if plain else P.strided(torch.zeros(R, rows, dtype=dtype, device="cuda"), pad and 8, whole=8)
+    dx, xbuf = P.strided(torch.zeros(R, K, dtype=dtype, device="cuda"), pad)
+    dw, wbuf = P.strided(torch.zeros(rows, K, dtype=dtype, device="cuda"), pad)
+    db = torch.full((rows,), NAN, dtype=wdtype, device="cuda")
+    ws = _ws(R, rows, K, True)
+    m.moe_linear_backward(dout, x, w, z, dz, dx, dw, db, ws, act=act, alpha=ALPHA, limit=LIMIT)
+    rz, bz = D.linear_dz(dout, z, act, ALPHA, LIMIT)
+    if not plain:
+        P.assert_within(dz, rz, bz, "dz")
+        if pad:
+            _canary(zbuf, rows, "dz")
+    P.assert_within(db, rz.sum(0), bz.sum(0) + (R + 8) * P.EPS32 * (rz.abs() + bz).sum(0), "db")
+    # the products, of dz as it was rounded
+    d = dout.double() if plain else dz.double()
+    P.assert_within(dx, d @ w.double(), (rows + 8) * P.EPS32 * (d.abs() @ w.double().abs()), "dx")
+    P.assert_within(dw, d.t() @ x.double(), (R + 8) * P.EPS32 * (d.abs().t() @ x.double().abs()), "dw")
+    if pad:
+        _canary(xbuf, K, "dx")
+        _canary(wbuf, K, "dw")
+    assert m.moe_mm_read_status(ws) == 0
+    return x, w, dout, z, dz, dx, dw, db, ws
+
+
+BACK = [(1, 1, 1), (1, 264, 72), (3, 40, 129), (64, 264, 200), (130, 257, 1000), (257, 256, 640), (700, 100, 65), (1100, 640, 128)]
+
+
+@pytest.mark.parametrize("R,N,K", BACK)
+@pytest.mark.parametrize("act", D.ACTS)
+@pytest.mark.parametrize("dtype,wdtype,pad", [(BF16, F32, 0), (F16, F16, 3)])
+def test_linear_backward(R, N, K, act, dtype, wdtype, pad):
+    _backward(R, N, K, act, dtype, wdtype, pad)
+
+
+@pytest.mark.parametrize("R,N,K", [(16384, 128, 96), (4096, 1440, 720), (2051, 2881, 264)])
+@pytest.mark.parametrize("act", ["none", "swiglu", "gelu"])
+def test_linear_backward_of_many_rows(R, N, K, act):
+    _backward(R, N, K, act, BF16)
+
+
+def test_linear_backward_parts_and_repeatable():
+    """Each gradient alone has the same bits as all together, and as again."""
+    x, w, dout, z, dz, dx, dw, db, ws = _backward(333, 200, 264, "swiglu", BF16)
+    kw = dict(act="swiglu", alpha=ALPHA, limit=LIMIT)
+    for i in range(3):
+        got = [torch.full_like(t, NAN) for t in (dx, dw, db)]
+        m.moe_linear_backward(dout, x, w, z, torch.empty_like(dz), *[t if i == j else None for j, t in enumerate(got)], ws, **kw)
+        assert torch.equal(got[i], (dx, dw, db)[i])
+        assert all(bool(torch.isnan(got[j].float()).all()) for j in range(3) if j != i)
+
+
+def test_linear_no_rows():
+    cuda_device()
+    w = torch.randn(48, 64, device="cuda").to(BF16)
+    x = torch.empty(0, 64, dtype=BF16, device="cuda")
+    ws = _ws(0, 48, 64)
+    m.moe_linear_forward(x, w, torch.empty(0, 24, dtype=BF16, device="cuda"), ws, act="swiglu")
+    dw, db = torch.full((48, 64), NAN, dtype=BF16, device="cuda"), torch.full((48,), NAN, device="cuda")
+    z = torch.empty(0, 48, dtype=BF16, device="cuda")
+    m.moe_linear_backward(z[:, :24], x, w, z, z.clone(), x.clone(), dw, db, _ws(0, 48, 64, True), act="swiglu")
+    assert not dw.any() and not db.any()
+
+
+@pytest.mark.parametrize("act", D.ACTS)
+def test_linear_gradient_by_differences(act):
+    """dx, dw and db of L = sum(c out) against central differences of the 64-bit forward."""
+    cuda_device()
+    g = _gen(11)
+    R, N, K = 5, 24, 40
+    rows = D.halves(act) * N
+    x, w, b = _rows(g, R, K, F16), _rows(g, rows, K, F16, std=K ** -0.5), _randn(g, rows, std=0.2)
+    c = _randn(g, R, N, dtype=F16)
+    out, z = torch.empty(R, N, dtype=F16, device="cuda"), torch.empty(R, rows, dtype=F16, device="cuda")
+    m.moe_linear_forward(x, w, out, _ws(R, rows, K), bias=b, z=z, act=act, alpha=ALPHA, limit=LIMIT)
+    dx, dw, db = torch.empty_like(x), torch.empty_like(w), torch.empty_like(b)
+    plain = act == "none"
+    m.moe_linear_backward(c, x, w, None if plain else z, None if plain else torch.empty_like(z), dx, dw, db, _ws(R, rows, K, True),
+                          act=act, alpha=ALPHA, limit=LIMIT)
+
+    def loss(x_, w_, b_):
+        return (c.double() * D.linear(x_, w_, b_, None, act, ALPHA, LIMIT)[0]).sum()
+
+    args = [x.double(), w.double(), b.double()]
+    if act in ("swiglu_clamp", "srelu"):       # away from the corners, where the difference means nothing
+        zz = D.product(*args)[0]
+        edge = zz.abs() if act == "srelu" else (zz.abs() - LIMIT).abs()
+        assert float(edge.min()) > 1e-5
+    h = 1e-6
+    # z in 16 bits shifts the derivative by |act''| 2^-11 |z|, dz's rounding by 2^-11: of |c| (1 + |z|^2) at most, summed
+    zz = D.product(*args)[0].abs()
+    wide = (c.double().abs().repeat(1, D.halves(act)) * (2 + zz) ** 2 * 4 * 2.0 ** -11) * (1 + zz.max())
+    bounds = [wide @ w.double().abs(), wide.t() @ x.double().abs(), wide.sum(0)]
+    for i, got in enumerate((dx, dw, db)):
+        flat = args[i].flatten()
+        for at in range(0, flat.numel(), max(1, flat.numel() // 40)):
+            lo, hi = args[i].clone().flatten(), args[i].clone().flatten()
+            lo[at] -= h
+            hi[at] += h
+            diff = [loss(*[v.view_as(args[i]) if j == i else args[j] for j in range(3)]) for v in (lo, hi)]
+            want = float(diff[1] - diff[0]) / (2 * h)
+            lim = float(bounds[i].flatten()[at]) + 1e-4 + 2.0 ** -11 * abs(want)
+            assert abs(float(got.flatten()[at]) - want) <= lim, (act, i, at)
+
+
+def test_linear_on_another_stream_and_in_graphs_that_share_a_workspace():
+    cuda_device()
+    g = _gen(5)
+    N, K = 328, 640
+    ws = _ws(400, 2 * N, K)
+    sets = []
+    for R in (7, 400):
+        x, w = _rows(g, R, K, BF16), _rows(g, 2 * N, K, BF16, std=K ** -0.5)
+        want, out = torch.empty(R, N, dtype=BF16, device="cuda"), torch.zeros(R, N, dtype=BF16, device="cuda")
+        m.moe_linear_forward(x, w, want, ws, act="swiglu")
+        sets.append((x, w, want, out))
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        for x, w, want, out in sets:
+            m.moe_linear_forward(x, w, out, ws, act="swiglu")
+    side.synchronize()
+    graphs = []
+    for x, w, want, out in sets:
+        assert torch.equal(out, want)
+        out.zero_()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            m.moe_linear_forward(x, w, out, ws, act="swiglu")
+        graphs.append(graph)
+    for _ in range(3):
+        for graph, (x, w, want, out) in zip(graphs, sets):
+            out.zero_()
+            graph.replay()
+            torch.cuda.synchronize()
+            assert torch.equal(out, want)
+
+
+def _needs_gb(n):
+    if torch.cuda.get_device_properties(0).total_memory < n << 30:
+        pytest.skip(f"needs {n} GB")
+
+
+@pytest.mark.parametrize("R", [33, 600])
+def test_linear_elements_past_32_bits(R):
+    """Rows so far apart that the last one's offset passes 2^31 elements, of x, residual, z and out."""
+    cuda_device()
+    _needs_gb(60)
+    g = _gen(8)
+    N, K = 48, 64
+    ld = (2 ** 31 // (R - 1) + 64) // 8 * 8
+    buf = torch.zeros(R, ld, dtype=BF16, device="cuda")
+    obuf, zbuf = torch.zeros_like(buf), torch.zeros_like(buf)
+    x = buf[:, :K]
+    x.copy_(_randn(g, R, K))
+    res = buf[:, K:K + N]
+    res.copy_(_randn(g, R, N))
+    w = _rows(g, 2 * N, K, BF16, std=K ** -0.5)
+    m.moe_linear_forward(x, w, obuf[:, :N], _ws(R, 2 * N, K), residual=res, z=zbuf[:, :2 * N], act="swiglu")
+    ro, bo, rz, bz = D.linear(x, w, None, res, "swiglu", ALPHA, LIMIT)
+    P.assert_within(obuf[:, :N], ro, bo, "out")
+    P.assert_within(zbuf[:, :2 * N], rz, bz, "z")
+    obuf[:, N:N + 96].zero_()
+    dz = obuf[:, N:N + 2 * N]
+    dx = zbuf[:, 128:128 + K]
+    dw, db = torch.empty_like(w), torch.empty(2 * N, device="cuda")
+    if N % 8 == 0:
+        m.moe_linear_backward(res, x, w, zbuf[:, :2 * N], dz, dx, dw, db, _ws(R, 2 * N, K, True), act="swiglu")
+        d = dz.double()
+        rdz, bdz = D.linear_dz(res, zbuf[:, :2 * N], "swiglu", ALPHA, LIMIT)
+        P.assert_within(dz, rdz, bdz, "dz")
+        P.assert_within(dx, d @ w.double(), (2 * N + 8) * P.EPS32 * (d.abs() @ w.double().abs()), "dx")
