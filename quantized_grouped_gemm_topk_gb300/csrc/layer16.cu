@@ -1,21 +1,39 @@
 // The routed layer for a few tokens with experts in 16 bits: router, top-k, both
 // products with the activation between them, combine.
-#include "ops.cuh"
+#include "few16.cuh"
 
 namespace moe {
 
 static int64_t al256(int64_t v) { return (v + 255) / 256 * 256; }
 
-// Workspace: y [T (k + S)][I] 16-bit rows, by token and slot.
-int64_t layer16_ws_bytes(int T, int H, int I, int E, int k, int S) {
-  return al256((int64_t)T * (k + S) * I * 2);
+// Workspace: the counters, y [T (k + S)][I] 16-bit and z [T (k + S)][H] fp32 rows
+// by group, partial sums.
+struct Layer16Ws {
+  int64_t ldy, ldz, counters, y, z, part, bytes;
+};
+static Layer16Ws layer16_ws(int T, int H, int I, int E, int k, int S) {
+  Layer16Ws w;
+  const int64_t rows = (int64_t)T * (k + S);
+  w.ldy = (I + 7) / 8 * 8;
+  w.ldz = (H + 127) / 128 * 128;
+  w.counters = 16 + kFewShares + w.ldz / 128;
+  w.y = al256(w.counters * 4);
+  w.z = w.y + al256(rows * w.ldy * 2);
+  w.part = w.z + al256(rows * w.ldz * 4);
+  w.bytes = w.part + few_part_bytes(T);
+  return w;
 }
+int64_t layer16_ws_bytes(int T, int H, int I, int E, int k, int S) { return layer16_ws(T, H, I, E, k, S).bytes; }
 
 // One CTA routes one token.
 template <typename E>
-__global__ void __launch_bounds__(256) k_l16_route(const Layer16Args a) {
+__global__ void __launch_bounds__(256) k_l16_route(const Layer16Args a, int64_t counters) {
   __shared__ float lg[2048];
   pdl_enter();
+  // the products' counters, which the kernel behind this one starts from
+  if (blockIdx.x == 0)
+    for (int64_t i = threadIdx.x; i < counters; i += 256) reinterpret_cast<int32_t*>(a.ws)[i] = 0;
+  if (!a.W_r && !a.logits) return;
   const int t = blockIdx.x, lane = threadIdx.x & 31;
   const uint16_t* x = reinterpret_cast<const uint16_t*>(a.x) + t * a.ldx;
   for (int e = threadIdx.x; e < a.E; e += 256) {
@@ -56,75 +74,24 @@ __global__ void __launch_bounds__(256) k_l16_route(const Layer16Args a) {
   }
 }
 
-// The expert and weight of slot j of token t; false: nothing to add.
-__device__ __forceinline__ bool slot_of(const Layer16Args& a, int t, int j, int& e, float& w) {
-  if (j >= a.k) { e = a.E + j - a.k; w = 1.f; return true; }
-  e = a.ids[t * a.k + j];
-  w = a.w[t * a.k + j];
-  if (e < 0 || e >= a.E) { set_status(a.status, MOE_DEV_BAD_EXPERT_ID); return false; }
-  return w != 0.f;
-}
-template <typename E>
-__device__ __forceinline__ float dot(const uint16_t* a, const uint16_t* b, int n, int lane) {
-  float s = 0.f;
-  for (int i = lane; i < n; i += 32) s = fmaf(E::to(a[i]), E::to(b[i]), s);
-  return warp_sum(s);
-}
-
-// y[t, j, i] of one token and slot: a warp a feature.
-template <typename E>
-__global__ void __launch_bounds__(256) k_l16_w1(const Layer16Args a) {
-  pdl_enter();
-  const int kp = a.k + a.S, t = blockIdx.y / kp, j = blockIdx.y % kp, lane = threadIdx.x & 31;
-  const int i = blockIdx.x * 8 + (threadIdx.x >> 5);
-  int e;
-  float w;
-  if (i >= a.I || !slot_of(a, t, j, e, w)) return;
-  const uint16_t* x = reinterpret_cast<const uint16_t*>(a.x) + t * a.ldx;
-  const uint16_t* w1 = reinterpret_cast<const uint16_t*>(a.w1) + e * a.g1;
-  float g = dot<E>(x, w1 + i * a.ld1, a.H, lane), y;
-  if (act_gated(a.act.act)) {
-    float u = dot<E>(x, w1 + (int64_t)(a.I + i) * a.ld1, a.H, lane);
-    if (a.b1) { g += a.b1[(int64_t)e * 2 * a.I + i]; u += a.b1[(int64_t)e * 2 * a.I + a.I + i]; }
-    y = act_two(g, u, a.act);
-  } else {
-    y = act_one(g, a.act.act);
-  }
-  if (lane == 0) reinterpret_cast<uint16_t*>(a.ws)[(int64_t)blockIdx.y * a.I + i] = E::from(w * y);
-}
-
-// out[t, h] over the token's slots, in slot order: a warp a column.
-template <typename E>
-__global__ void __launch_bounds__(256) k_l16_w2(const Layer16Args a) {
-  pdl_enter();
-  const int kp = a.k + a.S, t = blockIdx.y, lane = threadIdx.x & 31, h = blockIdx.x * 8 + (threadIdx.x >> 5);
-  if (h >= a.H) return;
-  float s = 0.f;
-  for (int j = 0; j < kp; ++j) {
-    int e;
-    float w;
-    if (!slot_of(a, t, j, e, w)) continue;
-    s += dot<E>(reinterpret_cast<const uint16_t*>(a.ws) + (int64_t)(t * kp + j) * a.I,
-                reinterpret_cast<const uint16_t*>(a.w2) + e * a.g2 + h * a.ld2, a.I, lane);
-  }
-  if (lane == 0) reinterpret_cast<uint16_t*>(a.out)[t * a.ldo + h] = E::from(s);
-}
-
-template <typename E>
-static cudaError_t launch_typed(const Layer16Args& a, cudaStream_t st) {
-  cudaError_t e = cudaSuccess;
-  if (a.W_r || a.logits) {
-    note_launch();
-    if ((e = launch_pdl(k_l16_route<E>, dim3(a.T), dim3(256), 0, st, a)) != cudaSuccess) return e;
-  }
-  note_launch();
-  if ((e = launch_pdl(k_l16_w1<E>, dim3((a.I + 7) / 8, a.T * (a.k + a.S)), dim3(256), 0, st, a)) != cudaSuccess) return e;
-  note_launch();
-  return launch_pdl(k_l16_w2<E>, dim3((a.H + 7) / 8, a.T), dim3(256), 0, st, a);
-}
-
 cudaError_t launch_layer16(const Layer16Args& a, cudaStream_t st) {
-  return a.dtype == MOE_DT_BF16 ? launch_typed<Bf16>(a, st) : launch_typed<F16>(a, st);
+  const Layer16Ws w = layer16_ws(a.T, a.H, a.I, a.E, a.k, a.S);
+  note_launch();
+  cudaError_t e = launch_pdl(a.dtype == MOE_DT_BF16 ? k_l16_route<Bf16> : k_l16_route<F16>, dim3(a.T), dim3(256), 0, st, a,
+                             w.counters);
+  if (e != cudaSuccess) return e;
+  FewArgs f = {};
+  f.R = a.T; f.K1 = a.H; f.F1 = a.I; f.K2 = a.I; f.F2 = a.H; f.act = a.act; f.dtype = a.dtype; f.status = a.status;
+  f.E = a.E; f.k = a.k; f.S = a.S; f.ids = a.ids; f.wts = a.w; f.b1 = a.b1;
+  f.y = reinterpret_cast<uint16_t*>(a.ws + w.y); f.ldy = w.ldy;
+  f.zrow = reinterpret_cast<float*>(a.ws + w.z); f.ldz32 = w.ldz;
+  f.part = reinterpret_cast<float*>(a.ws + w.part);
+  f.ticket = reinterpret_cast<int32_t*>(a.ws);
+  f.done = f.ticket + 8;
+  f.split = f.ticket + 16;
+  f.split2 = f.split + kFewShares;
+  f.out = a.out; f.ldo = a.ldo;
+  return launch_few_layer(f, a.x, a.ldx, a.w1, a.g1, a.ld1, a.w2, a.g2, a.ld2, st);
 }
 
 }  // namespace moe

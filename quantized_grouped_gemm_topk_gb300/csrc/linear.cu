@@ -4,9 +4,12 @@
 //
 // and their backward from the saved z: dz = dout act'(z), dx = dz w, dw = dz^T x,
 // db = the column sums of dz.
-#include "ops.cuh"
+#include "few16.cuh"
 
 namespace moe {
+
+constexpr int kFewCounters = 256;      // words in front of the partial sums of few rows
+static_assert(kFewCounters >= kFewShares, "a counter for each share");
 
 // ---- forward ----------------------------------------------------------------------
 // A thread owns 4 rows x 4 columns of a 64 x 64 tile (gated: of gate and up),
@@ -67,6 +70,14 @@ __global__ void __launch_bounds__(256) k_linear_plain(const LinearArgs a) {
 }
 
 cudaError_t launch_linear_fwd(const LinearArgs& a, cudaStream_t st) {
+  if (a.R <= kFewRows) {
+    FewArgs f = {};
+    f.R = a.R; f.K1 = a.K; f.F1 = a.N; f.act = a.act; f.dtype = a.dtype; f.wdtype = a.wdtype; f.status = a.status;
+    f.bias = a.bias; f.res = a.res; f.ldr = a.ldr; f.z = a.z; f.ldz = a.ldz; f.out = a.out; f.ldo = a.ldo;
+    f.split = reinterpret_cast<int32_t*>(a.part);
+    f.part = a.part + kFewCounters;
+    return launch_few_linear(f, a.x, a.ldx, a.w, a.ldw, st);
+  }
   const dim3 grid((a.N + kLT - 1) / kLT, std::min((a.R + kLT - 1) / kLT, 65535));
   const bool bf = a.dtype == MOE_DT_BF16;
   note_launch();
@@ -175,10 +186,10 @@ __global__ void __launch_bounds__(256) k_linear_db(const float* __restrict__ par
 
 static int dz_blocks(int R) { return std::max(1, std::min((R + 4 * kDzWarps - 1) / (4 * kDzWarps), kDzMaxBlocks)); }
 
-// The workspace: the column sums' partial sums, then those of the products (one
-// after the other).
+// The workspace. Forward: the counters and partial sums of few rows. Backward: the
+// column sums' partial sums, then those of the products (one after the other).
 int64_t linear_part_bytes(int R, int rows, int K, bool backward) {
-  if (!backward) return 0;
+  if (!backward) return kFewCounters * 4 + few_part_bytes(std::min(R, kFewRows));
   const int64_t db = (int64_t)dz_blocks(R) * rows * 4;
   return (db + 15) / 16 * 16 + std::max(mm_part_bytes(kMmRows, R, K, rows, 1), mm_part_bytes(kMmWgrad, R, rows, K, 1));
 }
