@@ -1,15 +1,56 @@
-// The routed layer for a few tokens with experts in 16 bits: router, top-k, both
-// products with the activation between them, combine.
+// The routed layer for a few tokens with experts in 16 bits, in two launches:
+// the router (logits, top-k, weights) here, everything behind it in few16.cu.
+//
+// The router's product x . W_r streams W_r [H, E] fp32 once for every eight
+// tokens: the reduction is cut into slices, a CTA each, whose partial sums the last
+// CTA to arrive (of those eight tokens') adds in order and routes. 1 x 7168 x 256:
+// latency, not the 7.3 MB; so all of a thread's rows are asked for at once.
 #include "few16.cuh"
 
 namespace moe {
 
 static int64_t al256(int64_t v) { return (v + 255) / 256 * 256; }
 
+constexpr int kRThreads = 512;
+constexpr int kRTokens = 8;           // most tokens of a CTA
+constexpr int kRChunk = 512;          // rows of x in shared memory at a time
+constexpr int kRRows = 8;             // rows of W_r that a thread asks for at once
+constexpr int kRArrive = 8;           // first arrival counter: zero between calls
+static_assert(MOE_LAYER16_MAX_T <= kRTokens * 8, "an arrival counter for every kRTokens tokens");
+
+struct RoutePlan {
+  int tt;               // tokens a CTA
+  int quads;            // of experts a CTA: a power of two up to 64
+  int et, z, ks;        // expert tiles, groups of tt tokens, slices of H
+  int ep;               // experts, rounded up to 4
+  int64_t floats() const { return (int64_t)z * ks * tt * ep; }
+};
+static RoutePlan route_plan(int T, int H, int E) {
+  RoutePlan p;
+  p.tt = T == 1 ? 1 : T == 2 ? 2 : T <= 4 ? 4 : kRTokens;
+  p.z = (T + p.tt - 1) / p.tt;
+  p.ep = (E + 3) / 4 * 4;
+  p.quads = 1;
+  while (p.quads < 64 && p.quads * 4 < E) p.quads *= 2;
+  p.et = (E + p.quads * 4 - 1) / (p.quads * 4);
+  // a CTA for every SM, at least 16 rows of H each, and no more partial sums than
+  // the last CTA reads in about 40 loads a thread
+  const int items = p.tt * (p.ep / 4);
+  p.ks = std::max(1, std::min({kFewShares / (p.z * p.et), H / 16, 40 * kRThreads / items}));
+  return p;
+}
+// Floats of partial sums that suffice for T tokens and any fewer.
+static int64_t route_floats(int T, int H, int E) {
+  int64_t most = 0;
+  for (int t = 1, before = 0; before < T; before = t, t += std::min(t, kRTokens))      // a plan holds for a range of T
+    most = std::max(most, route_plan(std::min(t, T), H, E).floats());
+  return most;
+}
+
 // Workspace: the counters, y [T (k + S)][I] 16-bit and z [T (k + S)][H] fp32 rows
-// by group, partial sums.
+// by group, the products' and the router's partial sums.
 struct Layer16Ws {
-  int64_t ldy, ldz, counters, y, z, part, bytes;
+  int64_t ldy, ldz, counters, y, z, part, router, bytes;
 };
 static Layer16Ws layer16_ws(int T, int H, int I, int E, int k, int S) {
   Layer16Ws w;
@@ -20,65 +61,219 @@ static Layer16Ws layer16_ws(int T, int H, int I, int E, int k, int S) {
   w.y = al256(w.counters * 4);
   w.z = w.y + al256(rows * w.ldy * 2);
   w.part = w.z + al256(rows * w.ldz * 4);
-  w.bytes = w.part + few_part_bytes(T);
+  w.router = w.part + few_part_bytes(T);
+  w.bytes = w.router + al256(route_floats(T, H, E) * 4);
   return w;
 }
 int64_t layer16_ws_bytes(int T, int H, int I, int E, int k, int S) { return layer16_ws(T, H, I, E, k, S).bytes; }
 
-// One CTA routes one token.
-template <typename E>
-__global__ void __launch_bounds__(256) k_l16_route(const Layer16Args a, int64_t counters) {
-  __shared__ float lg[2048];
+struct RouteArgs16 {
+  Layer16Args a;
+  RoutePlan p;
+  int64_t counters;
+  float* part;          // [z][ks][tt][ep]
+};
+
+// Sums of a float4 over `n` partial sums, `step` floats apart, eight at a time.
+__device__ __forceinline__ float4 sum_parts(const float* p, int n, int64_t step) {
+  float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int i = 0; i < n; i += 8) {
+    float4 v[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      v[j] = i + j < n ? __ldcg(reinterpret_cast<const float4*>(p + (i + j) * step)) : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) { s.x += v[j].x; s.y += v[j].y; s.z += v[j].z; s.w += v[j].w; }
+  }
+  return s;
+}
+
+template <typename E, int TT>
+__global__ void __launch_bounds__(kRThreads) k_l16_route(const RouteArgs16 r) {
+  extern __shared__ __align__(16) uint8_t rsm[];
+  __shared__ float xs[kRChunk * TT];
+  __shared__ int last;
+  const Layer16Args& a = r.a;
+  const RoutePlan& p = r.p;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   pdl_enter();
   // the products' counters, which the kernel behind this one starts from
-  if (blockIdx.x == 0)
-    for (int64_t i = threadIdx.x; i < counters; i += 256) reinterpret_cast<int32_t*>(a.ws)[i] = 0;
+  int32_t* counters = reinterpret_cast<int32_t*>(a.ws);
+  if (blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0)
+    for (int64_t i = tid; i < r.counters; i += kRThreads)
+      if (i < kRArrive || i >= kRArrive + 8) counters[i] = 0;
   if (!a.W_r && !a.logits) return;
-  const int t = blockIdx.x, lane = threadIdx.x & 31;
-  const uint16_t* x = reinterpret_cast<const uint16_t*>(a.x) + t * a.ldx;
-  for (int e = threadIdx.x; e < a.E; e += 256) {
-    float v = 0.f;
-    if (a.W_r) for (int h = 0; h < a.H; ++h) v = fmaf(E::to(x[h]), a.W_r[(int64_t)h * a.E + e], v);
-    else v = a.logits[(int64_t)t * a.E + e];
-    if (v != v) set_status(a.status, MOE_DEV_NAN_LOGIT);
-    lg[e] = v != v ? -INFINITY : v;
-  }
-  __syncthreads();
-  if (threadIdx.x >= 32) return;
-  float sel = 0.f;
-  int id = 0;
-  for (int j = 0; j < a.k; ++j) {
-    float best = 0.f;
-    int at = 0x7fffffff;
-    for (int e = lane; e < a.E; e += 32) {
-      const float v = lg[e];
-      if (v == v && (at == 0x7fffffff || v > best)) { best = v; at = e; }     // a taken one is NaN
-    }
+  const int t0 = blockIdx.z * TT, nt = min(TT, a.T - t0);
+  const int64_t set = (int64_t)TT * p.ep;
+  float* part = r.part + blockIdx.z * p.ks * set;
+
+  if (a.W_r) {
+    // ---- a slice of the product ----
+    const int tq = tid & (p.quads - 1), rows = kRThreads / p.quads, tr = tid / p.quads;
+    const int e0 = (blockIdx.y * p.quads + tq) * 4;
+    const int h0 = (int)((int64_t)a.H * blockIdx.x / p.ks), h1 = (int)((int64_t)a.H * (blockIdx.x + 1) / p.ks);
+    const bool vec = a.E % 4 == 0 && ((uintptr_t)a.W_r & 15) == 0;
+    float acc[TT][4] = {};
+    for (int hb = h0; hb < h1; hb += kRChunk) {
+      const int n = min(kRChunk, h1 - hb);
+      __syncthreads();
+      for (int i = tid; i < n * TT; i += kRThreads) {
+        const int t = i / n, h = i - t * n;
+        xs[h * TT + t] = t < nt ? E::to(reinterpret_cast<const uint16_t*>(a.x)[(t0 + t) * a.ldx + hb + h]) : 0.f;
+      }
+      __syncthreads();
+      for (int h = tr; h < n; h += rows * kRRows) {
+        float w[kRRows][4];
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      const float v = __shfl_xor_sync(kFull, best, o);
-      const int i = __shfl_xor_sync(kFull, at, o);
-      if (i != 0x7fffffff && (at == 0x7fffffff || v > best || (v == best && i < at))) { best = v; at = i; }
+        for (int i = 0; i < kRRows; ++i) {
+          const int hh = h + i * rows;
+          const float* src = a.W_r + (int64_t)(hb + hh) * a.E + e0;
+          if (vec) {
+            const float4 v = hh < n && e0 < a.E ? __ldg(reinterpret_cast<const float4*>(src)) : make_float4(0.f, 0.f, 0.f, 0.f);
+            w[i][0] = v.x; w[i][1] = v.y; w[i][2] = v.z; w[i][3] = v.w;
+          } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) w[i][j] = hh < n && e0 + j < a.E ? __ldg(src + j) : 0.f;
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < kRRows; ++i) {
+          const int hh = h + i * rows;
+          if (hh >= n) break;
+#pragma unroll
+          for (int t = 0; t < TT; ++t) {
+            const float xv = xs[hh * TT + t];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) acc[t][j] = fmaf(xv, w[i][j], acc[t][j]);
+          }
+        }
+      }
     }
-    if (lane == 0) lg[at] = __int_as_float(0x7fffffff);
-    __syncwarp();
-    if (lane == j) { sel = best; id = at; }
+    // row lanes of a warp, then the rest through shared memory
+    for (int o = p.quads; o < 32; o <<= 1)
+#pragma unroll
+      for (int t = 0; t < TT; ++t)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) acc[t][j] += __shfl_xor_sync(kFull, acc[t][j], o);
+    float* red = reinterpret_cast<float*>(rsm);               // [lanes][TT][4 quads]
+    const int width = 4 * p.quads, lanes = p.quads == 64 ? 8 : 16, my = p.quads == 64 ? tr : warp;
+    if (p.quads >= 32 || lane < p.quads)
+#pragma unroll
+      for (int t = 0; t < TT; ++t)
+        *reinterpret_cast<float4*>(red + (my * TT + t) * width + 4 * tq) = make_float4(acc[t][0], acc[t][1], acc[t][2], acc[t][3]);
+    __syncthreads();
+    for (int o = tid; o < TT * width; o += kRThreads) {
+      const int t = o / width, e = blockIdx.y * width + o - t * width;
+      float v = red[o];
+      for (int l = 1; l < lanes; ++l) v += red[l * TT * width + o];
+      if (e < p.ep) part[blockIdx.x * set + (int64_t)t * p.ep + e] = v;
+    }
+    __threadfence();
+    __syncthreads();
+    if (tid == 0) {
+      const int old = atom_add_acq_rel_gpu(&counters[kRArrive + blockIdx.z], 1);
+      last = old == p.ks * p.et - 1;
+      if (last) counters[kRArrive + blockIdx.z] = 0;
+    }
+    __syncthreads();
+    if (!last) return;
+    __threadfence();
   }
-  const float m = __shfl_sync(kFull, sel, 0);
-  const float p = lane < a.k && m != -INFINITY ? expf(sel - m) : 0.f;
-  float sum = 0.f;
-  for (int j = 0; j < a.k; ++j) sum += __shfl_sync(kFull, p, j);
-  if (lane < a.k) {
-    a.ids[t * a.k + lane] = id;
-    a.w[t * a.k + lane] = m != -INFINITY ? p / sum * a.rs : 0.f;
+
+  // ---- the last CTA: keys [nt][ep] of the logits, then a warp a token ----
+  uint32_t* keys = reinterpret_cast<uint32_t*>(rsm);
+  const int q4 = p.ep / 4;
+  bool nan_seen = false;
+  auto key = [&](float v) {
+    nan_seen |= v != v;
+    return logit_key(v != v ? -INFINITY : v);
+  };
+  if (a.W_r) {
+    const int items = nt * q4;
+    int split = 1;                                            // threads an item
+    while (2 * split * items <= kRThreads && 2 * split <= p.ks) split *= 2;
+    float4* red = reinterpret_cast<float4*>(rsm + (int64_t)TT * p.ep * 4);
+    for (int i = tid; i < items * split; i += kRThreads) {
+      const int it = i % items, g = i / items, k0 = p.ks * g / split, k1 = p.ks * (g + 1) / split;
+      red[i] = sum_parts(part + k0 * set + 4 * (int64_t)it, k1 - k0, set);
+    }
+    __syncthreads();
+    for (int it = tid; it < items; it += kRThreads) {
+      float4 v = red[it];
+      for (int g = 1; g < split; ++g) {
+        const float4 u = red[g * items + it];
+        v.x += u.x; v.y += u.y; v.z += u.z; v.w += u.w;
+      }
+      const int e = it % q4 * 4;
+      const float f[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) keys[4 * it + j] = e + j < a.E ? key(f[j]) : 0u;
+    }
+  } else {
+    for (int i = tid; i < nt * p.ep; i += kRThreads) {
+      const int t = i / p.ep, e = i - t * p.ep;
+      keys[i] = e < a.E ? key(a.logits[(int64_t)(t0 + t) * a.E + e]) : 0u;
+    }
+  }
+  if (nan_seen) set_status(a.status, MOE_DEV_NAN_LOGIT);
+  __syncthreads();
+  for (int t = warp; t < nt; t += kRThreads / 32) {
+    uint32_t* row = keys + t * p.ep;
+    float sel = 0.f;
+    int id = 0;
+    for (int j = 0; j < a.k; ++j) {
+      // a lane's ids grow, so among equal keys it keeps the lowest; 0 is a taken one
+      uint32_t best = 0;
+      int at = 0x7fffffff;
+      for (int e = lane; e < a.E; e += 32) {
+        const uint32_t v = row[e];
+        if (v > best) { best = v; at = e; }
+      }
+      const uint32_t top = __reduce_max_sync(kFull, best);
+      const int win = (int)__reduce_min_sync(kFull, best == top ? (uint32_t)at : 0xffffffffu);
+      if ((win & 31) == lane) row[win] = 0;
+      __syncwarp();
+      if (lane == j) { sel = key_logit(top); id = win; }
+    }
+    // softmax over the selected logits, the first of them the largest
+    const float m = __shfl_sync(kFull, sel, 0);
+    const float w = lane < a.k && m != -INFINITY ? expf(sel - m) : 0.f;
+    float sum = 0.f;
+    for (int j = 0; j < a.k; ++j) sum += __shfl_sync(kFull, w, j);
+    if (lane < a.k) {
+      a.ids[(t0 + t) * a.k + lane] = id;
+      a.w[(t0 + t) * a.k + lane] = m != -INFINITY ? w / sum * a.rs : 0.f;
+    }
+  }
+}
+
+template <typename E, int TT>
+static cudaError_t launch_route16(const RouteArgs16& r, cudaStream_t st) {
+  // the row lanes' sums; later the keys and the items' sums
+  const int red = 16 * TT * 4 * 64 * 4, fin = TT * r.p.ep * 4 + std::max(kRThreads, TT * r.p.ep / 4) * 16;
+  const int smem = std::max(r.a.W_r ? red : 0, fin);
+  static std::atomic<bool> done[kMaxDevices] = {};
+  const cudaError_t e = set_smem_once((const void*)k_l16_route<E, TT>, 160 * 1024, done);
+  if (e != cudaSuccess) return e;
+  const bool routes = r.a.W_r || r.a.logits;
+  const dim3 grid(r.a.W_r ? r.p.ks : 1, r.a.W_r ? r.p.et : 1, routes ? r.p.z : 1);
+  note_launch();
+  return launch_pdl(k_l16_route<E, TT>, grid, dim3(kRThreads), smem, st, r);
+}
+template <typename E>
+static cudaError_t launch_route16(const RouteArgs16& r, cudaStream_t st) {
+  switch (r.p.tt) {
+    case 1: return launch_route16<E, 1>(r, st);
+    case 2: return launch_route16<E, 2>(r, st);
+    case 4: return launch_route16<E, 4>(r, st);
+    default: return launch_route16<E, 8>(r, st);
   }
 }
 
 cudaError_t launch_layer16(const Layer16Args& a, cudaStream_t st) {
   const Layer16Ws w = layer16_ws(a.T, a.H, a.I, a.E, a.k, a.S);
-  note_launch();
-  cudaError_t e = launch_pdl(a.dtype == MOE_DT_BF16 ? k_l16_route<Bf16> : k_l16_route<F16>, dim3(a.T), dim3(256), 0, st, a,
-                             w.counters);
+  RouteArgs16 r = {a, route_plan(a.T, a.H, a.E), w.counters, reinterpret_cast<float*>(a.ws + w.router)};
+  const cudaError_t e = a.dtype == MOE_DT_BF16 ? launch_route16<Bf16>(r, st) : launch_route16<F16>(r, st);
   if (e != cudaSuccess) return e;
   FewArgs f = {};
   f.R = a.T; f.K1 = a.H; f.F1 = a.I; f.K2 = a.I; f.F2 = a.H; f.act = a.act; f.dtype = a.dtype; f.status = a.status;
@@ -87,7 +282,7 @@ cudaError_t launch_layer16(const Layer16Args& a, cudaStream_t st) {
   f.zrow = reinterpret_cast<float*>(a.ws + w.z); f.ldz32 = w.ldz;
   f.part = reinterpret_cast<float*>(a.ws + w.part);
   f.ticket = reinterpret_cast<int32_t*>(a.ws);
-  f.done = f.ticket + 8;
+  f.done = f.ticket + 1;
   f.split = f.ticket + 16;
   f.split2 = f.split + kFewShares;
   f.out = a.out; f.ldo = a.ldo;

@@ -8,9 +8,6 @@
 
 namespace moe {
 
-constexpr int kFewCounters = 256;      // words in front of the partial sums of few rows
-static_assert(kFewCounters >= kFewShares, "a counter for each share");
-
 // ---- forward ----------------------------------------------------------------------
 // A thread owns 4 rows x 4 columns of a 64 x 64 tile (gated: of gate and up),
 // summed over K in steps of 16 through shared memory.
@@ -74,8 +71,6 @@ cudaError_t launch_linear_fwd(const LinearArgs& a, cudaStream_t st) {
     FewArgs f = {};
     f.R = a.R; f.K1 = a.K; f.F1 = a.N; f.act = a.act; f.dtype = a.dtype; f.wdtype = a.wdtype; f.status = a.status;
     f.bias = a.bias; f.res = a.res; f.ldr = a.ldr; f.z = a.z; f.ldz = a.ldz; f.out = a.out; f.ldo = a.ldo;
-    f.split = reinterpret_cast<int32_t*>(a.part);
-    f.part = a.part + kFewCounters;
     return launch_few_linear(f, a.x, a.ldx, a.w, a.ldw, st);
   }
   const dim3 grid((a.N + kLT - 1) / kLT, std::min((a.R + kLT - 1) / kLT, 65535));
@@ -186,10 +181,10 @@ __global__ void __launch_bounds__(256) k_linear_db(const float* __restrict__ par
 
 static int dz_blocks(int R) { return std::max(1, std::min((R + 4 * kDzWarps - 1) / (4 * kDzWarps), kDzMaxBlocks)); }
 
-// The workspace. Forward: the counters and partial sums of few rows. Backward: the
-// column sums' partial sums, then those of the products (one after the other).
+// The workspace's partial sums. Backward: of the column sums, then those of the
+// products (one after the other).
 int64_t linear_part_bytes(int R, int rows, int K, bool backward) {
-  if (!backward) return kFewCounters * 4 + few_part_bytes(std::min(R, kFewRows));
+  if (!backward) return 0;
   const int64_t db = (int64_t)dz_blocks(R) * rows * 4;
   return (db + 15) / 16 * 16 + std::max(mm_part_bytes(kMmRows, R, K, rows, 1), mm_part_bytes(kMmWgrad, R, rows, K, 1));
 }

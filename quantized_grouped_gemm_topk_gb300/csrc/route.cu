@@ -445,14 +445,6 @@ __global__ void __launch_bounds__(256) k_router_mid(const uint16_t* __restrict__
 // the lowest id holding it from one redux.sync min, so a round costs two
 // warp reductions instead of five shuffle-and-compare steps.
 // ---------------------------------------------------------------------------
-__device__ __forceinline__ uint32_t logit_key(float v) {
-  const uint32_t u = __float_as_uint(v == 0.f ? 0.f : v);
-  return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
-}
-__device__ __forceinline__ float key_logit(uint32_t k) {
-  return __uint_as_float((k & 0x80000000u) ? (k & 0x7fffffffu) : ~k);
-}
-
 // Sum over ks of part[ks * n + i], in ks order, 16 loads in flight at a
 // time (the tail's loads predicated, not serialised).
 __device__ __forceinline__ float sum_partials(const float* __restrict__ part, int KS, int64_t n, int64_t i) {
