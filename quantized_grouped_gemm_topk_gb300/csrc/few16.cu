@@ -1,90 +1,76 @@
-// Products of 16-bit weights with a few rows, on the 5th-generation tensor
-// cores, in one launch: the routed layer's both products with the activation and
-// the combine between and behind them, or one dense product with its epilogue.
+// Products of 16-bit weights with a few rows, on the 5th-generation tensor cores,
+// in one launch: the routed layer's both products with the activation and the
+// combine, or one dense product with its epilogue.
 //
-// Bound: the weights' bytes. Everything else is arranged around their stream.
+// Bound: the weights' bytes; at small sizes latency. Everything else is arranged
+// around the weights' stream.
 //
-// - Weights are the MMA's M side (128 features; gated: 64 gate and the matching
-//   64 up features, which one tensor copy brings), the rows its N (16 to 256).
-//   The first product multiplies every expert's weights with all the tokens:
-//   up to 64 columns cost the tensor core no more than 16, and no gather is
-//   needed. The epilogue reads the columns of the expert's own tokens; what the
-//   others hold never leaves tensor memory, so a NaN stays with its token.
-// - The work of a product is cut into equal shares of its stages, one to a CTA,
-//   wherever the tiles end (few tiles over 152 SMs would leave up to half of
-//   them idle in the last round). A tile that spans shares leaves fp32 partial
-//   sums; the last CTA to finish one of its pieces adds them in order. No sum
-//   depends on which CTA does what.
-// - The second product's weights do not depend on the first one: their copies
-//   run ahead into the ring while the CTA's B copies wait for all of the first
-//   product's tiles, so the barrier between the products costs no stream time
-//   as long as it is shorter than the ring (200 KB, 4.5 us).
-// - CTAs claim their shares from a counter, all of the first product's before
-//   any of the second's: a CTA that waits only waits for shares that running
-//   CTAs hold, however many of the grid are resident.
+// - Weights are the MMA's M side, the rows its N (16 to 256). The layer's first
+//   product multiplies every expert's weights with all the tokens: up to 64
+//   columns cost the tensor core little more than 16, and no gather is needed. The
+//   epilogue reads the columns of the expert's own tokens; what the others hold
+//   never leaves tensor memory, so a NaN stays with its token.
+// - Each CTA takes an equal range of features over the whole reduction, wherever
+//   it begins: of the first product a range of all touched experts' features, of
+//   the second one of H, for which it runs through all touched experts (or, where
+//   the range would be narrow, half or a quarter of them) and adds their columns to
+//   the tokens' fp32 sums in shared memory. So no reduction is cut
+//   (with tiles of 128 features cut along the reduction into equal shares, whose
+//   partial sums the last CTA added, one token through 7168 x 2048 x 8 experts
+//   took 127 us behind the router, 2880 x 2880 x 4 51, 256 x 128 x 2 20). A
+//   tile's copies may cover a few rows of its neighbour, which the L2 serves.
+// - The second product's weights do not depend on the first one: their copies run
+//   ahead into the ring while the CTA's copies of the rows wait for all of the
+//   first product, so the barrier between them costs no stream time as long as it
+//   is shorter than the ring.
+// - CTAs claim their ranges from a counter, all of the first product's before any
+//   of the second's: a CTA that waits only waits for ranges that running CTAs
+//   hold, however many of the grid are resident.
 //
-// Roles: warp 0 claims and copies weights, warp 2 copies rows, warp 1 issues the
-// MMAs, warps 4-7 are the epilogue (two accumulators, so that it overlaps the
-// next tile's MMAs). Every wait is bounded; a CTA whose wait runs out sets
-// MOE_DEV_TIMEOUT, waits for its copies and MMAs in flight, frees tensor memory
-// and returns.
+// Roles: warp 0 claims and copies weights, warp 2 copies rows, warp 1 (in the layer
+// also 3, 8 and 9) issues the MMAs, warps 4 and up are the epilogue (two
+// accumulators, so that it overlaps the next tile's MMAs). An MMA costs the thread
+// that issues it 65 cycles, however few its rows: with one issuer a half stage
+// of 24 rows took 350 cycles, of which its copies need 130. So each of four
+// issues one step (K = 16) in four, into an accumulator of its own, and the
+// epilogue adds the four. Every wait is bounded; a CTA whose wait runs out sets
+// MOE_DEV_TIMEOUT, waits for its copies and MMAs in flight, frees tensor memory and
+// returns.
+#include <cmath>
+
 #include "few16.cuh"
 #include "tc.cuh"
 
 namespace moe {
 
-constexpr int kFM = 128;              // features a tile (MMA M)
+constexpr int kFM = 128;              // most features a tile (MMA M)
 constexpr int kFH = 64;               // reduction of a half stage: one 128-byte swizzle row
 constexpr int kFK = 2 * kFH;
-constexpr int kFThreads = 256;
-constexpr int kFA = kFM * kFH * 2;    // bytes of A's half
+constexpr int kFThreads = 320;
+constexpr int kFA = kFM * kFH * 2;    // bytes of 128 rows' half
 constexpr int kFMaxStages = 8;
 constexpr int kFBars = 512;           // barriers and scratch, in front of the tables
 constexpr int kFSmem = 227 * 1024;
-constexpr int kFCols = 8;             // columns the epilogue stages at a time
-constexpr int kFQueue = 4;            // claimed shares in flight
+constexpr int kFCols = 8;             // columns the layer's epilogue takes at a time
+constexpr int kFQueue = 4;            // claimed ranges in flight
+constexpr int kFIssuers = 4;          // warps that issue the layer's MMAs
+constexpr int kFLeast = 8;            // features a range, at least
 
 struct FewMaps {
-  CUtensorMap a[2];                   // weights: [G][halves][rows][K], box 64 x rows x halves
-  CUtensorMap x;                      // rows of the (first) product, box 64 x N
-  CUtensorMap y[4];                   // layer: rows of the second, boxes of 16, 32, 48, 64
+  CUtensorMap a[8];                   // weights of the (first) product: boxes of 8 (i + 1) features (not gated: 16 (i + 1)),
+                                      // dense: a[0], the tile's
+  CUtensorMap a2;                     // layer: of the second
+  CUtensorMap x;                      // rows of the (first) product
+  CUtensorMap y[4];                   // layer: rows of the second, boxes of 8 << i
 };
-
-// A product cut into shares.
-struct Cut {
-  int mt, nk, ng;                     // feature tiles, stages of the reduction, groups
-  int P;                              // shares
-  int64_t total;                      // stages
-  __device__ __forceinline__ int64_t begin(int s) const { return total * s / P; }
-  __device__ __forceinline__ int share_of(int64_t step) const { return (int)(((step + 1) * P - 1) / total); }
-};
-// A piece of a tile: stages [k0, k1) of tile (gi, j).
-struct Piece {
-  int gi, j, k0, k1;
-  int64_t t0;                         // the tile's first stage
-};
-template <bool SECOND>
-__device__ __forceinline__ void piece_at(const Cut& c, int64_t at, int64_t end, Piece& p) {
-  const int64_t tile = at / c.nk;
-  p.t0 = tile * c.nk;
-  p.k0 = (int)(at - p.t0);
-  p.k1 = (int)min((int64_t)c.nk, end - p.t0);
-  if (SECOND) {                       // groups innermost: a share holds one feature tile's, by and large
-    p.j = (int)(tile / c.ng);
-    p.gi = (int)(tile - (int64_t)p.j * c.ng);
-  } else {
-    p.gi = (int)(tile / c.mt);
-    p.j = (int)(tile - (int64_t)p.gi * c.mt);
-  }
-}
 
 __device__ __forceinline__ void tmem_ld1(uint32_t taddr, uint32_t& v) {
   asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(v) : "r"(taddr) : "memory");
 }
-// A stage of weights: features f0 .. of group e (both halves of a gated tile),
-// 64 of the reduction after 64. Where the reduction is a whole number of those
-// the map has an axis of them and one copy brings the stage (a copy costs its
-// thread some hundred cycles); else there is one for each 64 that exist.
+// A stage of weights: features f0 .. of group e (both halves of a gated tile), n
+// times 64 of the reduction. Where the reduction is a whole number of those the map
+// has an axis of them and one copy brings the stage (a copy costs its thread some
+// hundred cycles); else there is one for each 64.
 __device__ __forceinline__ void copy_weights(uint32_t dst, int half_bytes, const CUtensorMap* map, bool chunks, int k, int n,
                                              int f0, int e, uint32_t bar, uint64_t policy) {
   for (int h = 0; h < (chunks ? 1 : n); ++h)
@@ -111,17 +97,21 @@ __device__ __forceinline__ void wind_down(uint64_t* full, uint32_t issued, int s
     tc::mbar_wait(&full[i % stages], (i / stages) & 1, &never, 100000000ll);
   }
 }
-// The epilogue's warps only.
+__device__ __forceinline__ float add4(const uint32_t (&v)[4]) {
+  return (__uint_as_float(v[0]) + __uint_as_float(v[1])) + (__uint_as_float(v[2]) + __uint_as_float(v[3]));
+}
+// The layer's epilogue warps only.
 __device__ __forceinline__ void epi_sync() { __syncwarp(); asm volatile("bar.sync 1, 128;" ::: "memory"); }
-
-// Whether `ok` holds for all of them: what one of them gives up, all do.
+// Whether `ok` holds for all threads of `count` (barrier id): what one of them
+// gives up, all do.
+template <int ID, int COUNT>
 __device__ __forceinline__ bool epi_all(bool ok) {
   uint32_t r;
   __syncwarp();
   asm volatile(
-      "{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n bar.red.and.pred q, 1, 128, p;\n selp.u32 %0, 1, 0, q;\n}"
+      "{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n bar.red.and.pred q, %2, %3, p;\n selp.u32 %0, 1, 0, q;\n}"
       : "=r"(r)
-      : "r"((uint32_t)ok)
+      : "r"((uint32_t)ok), "n"(ID), "n"(COUNT)
       : "memory");
   return r != 0;
 }
@@ -132,49 +122,22 @@ __device__ __forceinline__ int next_bit(unsigned long long& m) {
   m &= m - 1;
   return b;
 }
+// Copies cover 8 << i rows, the fewest that hold n.
+__device__ __forceinline__ int box_of(int n) { return n <= 8 ? 0 : n <= 16 ? 1 : n <= 32 ? 2 : 3; }
 
-// out[t][128 j ..] = the rows of the token's slots, in slot order; a row's own
-// pieces (a tile that spans shares) in order too. A warp a token, a lane four
-// columns; the rows of four slots are asked for at once.
-template <typename E>
-__device__ __forceinline__ void join_tokens(const FewArgs& g, const Cut& c, int j, const int2* slot_of, int kp, int q, int lane) {
-  const int h = j * kFM + 4 * lane;
-  const int64_t j0 = (int64_t)j * c.ng * c.nk;
-  const float* z = g.zrow + h;
-  const bool vec = ((uintptr_t)g.out & 7) == 0 && g.ldo % 4 == 0 && h + 4 <= g.F2;
-  for (int t = q; t < g.R; t += 4) {
-    float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
-    auto add = [&](float4 v) { sum.x += v.x; sum.y += v.y; sum.z += v.z; sum.w += v.w; };
-    for (int s = 0; s < kp; s += 8) {
-      float4 v[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int row = s + i < kp ? slot_of[t * kp + s + i].x : -1;
-        v[i] = row < 0 ? make_float4(0.f, 0.f, 0.f, 0.f) : __ldcg(reinterpret_cast<const float4*>(z + (int64_t)row * g.ldz32));
-      }
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        if (s + i >= kp) break;
-        const int2 sl = slot_of[t * kp + s + i];
-        if (sl.x < 0) continue;
-        add(v[i]);
-        const int64_t t0 = j0 + (int64_t)(sl.y & 0xffff) * c.nk;
-        const int w1 = c.share_of(t0 + c.nk - 1);
-        for (int w = c.share_of(t0) + 1; w <= w1; ++w)
-          add(__ldcg(reinterpret_cast<const float4*>(g.part + ((int64_t)w * g.N + (sl.y >> 16)) * kFM) + lane));
-      }
-    }
-    uint16_t* o = reinterpret_cast<uint16_t*>(g.out) + t * g.ldo + h;
-    if (vec) {
-      *reinterpret_cast<uint2*>(o) = make_uint2(E::from2(sum.x, sum.y), E::from2(sum.z, sum.w));
-    } else {
-      if (h < g.F2) o[0] = E::from(sum.x);
-      if (h + 1 < g.F2) o[1] = E::from(sum.y);
-      if (h + 2 < g.F2) o[2] = E::from(sum.z);
-      if (h + 3 < g.F2) o[3] = E::from(sum.w);
-    }
-  }
-}
+// ---- the routed layer ---------------------------------------------------------------
+// A tile: `len` features from f0 of group e, copied in boxes of `box` (gated: of
+// each half). rows: of the operand B that are copied; N: the MMA's.
+struct FewTile {
+  int e, f0, len, box, rows, N;
+};
+// Runs through the tiles of a range. First product: features at .. end of all
+// groups' one after the other, up to 64 (gated) or 128 a tile. Second: features of
+// H, up to 128 (the map's box) a tile, all groups, or one of g.S2 parts of them, for each.
+struct FewRange {
+  int64_t at, end;
+  int g, g0, g1;        // second: groups [g0, g1), the next one
+};
 
 template <typename E>
 __global__ void __launch_bounds__(kFThreads, 1) k_few_layer(const FewArgs g, const __grid_constant__ FewMaps maps) {
@@ -187,64 +150,69 @@ __global__ void __launch_bounds__(kFThreads, 1) k_few_layer(const FewArgs g, con
   uint64_t* qfull = accempty + 2;
   uint64_t* qempty = qfull + kFQueue;
   uint64_t* drain = qempty + kFQueue;
-  int* queue = reinterpret_cast<int*>(drain + 1);
+  int* queue = reinterpret_cast<int*>(drain + kFIssuers);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(queue + kFQueue);
   volatile int* abort = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  int* tmp = reinterpret_cast<int*>(tmem_slot + 2);       // 2 + 2 * 8
-  float* stage = reinterpret_cast<float*>(base + kFBars); // [kFCols][128]
-  // layer's tables
-  const int G = g.E + g.S, kp = g.k + g.S;
-  unsigned long long* mask = reinterpret_cast<unsigned long long*>(base + kFBars + kFCols * kFM * 4);   // [G] tokens
-  int* rowof = reinterpret_cast<int*>(mask + G);        // [G] first row of the group
-  int* glist = rowof + G;                               // [ng] groups with tokens
-  int2* slot_of = reinterpret_cast<int2*>((reinterpret_cast<uintptr_t>(glist + min(G, g.R * kp)) + 7) & ~(uintptr_t)7);
-  // slot_of [T kp]: row of a token's slot (-1: none); its group's place in glist and, from bit 16 on, its row in the group
-  float* wrow = reinterpret_cast<float*>(slot_of + g.R * kp);   // [rows] routing weight
-  int* gplace = reinterpret_cast<int*>(wrow + g.R * kp);        // [G] the group's place in glist
-  uint8_t* sa = base + g.head;
-  uint8_t* sb = sa + g.stages * 2 * kFA;
-  const int b_half = g.N * 128;                                    // bytes of B's half
+  int* tmp = reinterpret_cast<int*>(tmem_slot + 2);                 // 1 + 2 * 10
+  float* stage = reinterpret_cast<float*>(base + kFBars);           // [kFCols][128]
+  const int G = g.E + g.S, A = g.R * g.k;
+  const bool gated = act_gated(g.act.act);
+  // the tokens' sums [T][g.box2]; then the tables
+  float* sums = stage + kFCols * kFM;
+  unsigned long long* mask = reinterpret_cast<unsigned long long*>(sums + ((g.R * g.box2 + 1) & ~1));   // [G] tokens
+  int* rowof = reinterpret_cast<int*>(mask + G);                    // [G] first row of the group
+  int* glist = rowof + G;                                           // groups with tokens
+  float* wrow = reinterpret_cast<float*>(glist + min(G, A + g.S));  // [rows] routing weight
+  int* sid = reinterpret_cast<int*>(wrow + A + g.S * g.R);          // [A] the ids, -1: left out
+  float* swt = reinterpret_cast<float*>(sid + A);                   // [A] their weights
+  uint8_t* ring = base + g.head;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
   if (tid == 0) {
     for (int i = 0; i < g.stages; ++i) {
       tc::mbar_init(&full[i], 2);
-      tc::mbar_init(&empty[i], 1);
+      tc::mbar_init(&empty[i], kFIssuers);
     }
     for (int i = 0; i < 2; ++i) {
-      tc::mbar_init(&accfull[i], 1);
+      tc::mbar_init(&accfull[i], kFIssuers);
       tc::mbar_init(&accempty[i], 4);
     }
     for (int i = 0; i < kFQueue; ++i) {
       tc::mbar_init(&qfull[i], 1);
-      tc::mbar_init(&qempty[i], 3);       // rows' copies, MMAs, epilogue
+      tc::mbar_init(&qempty[i], 2 + kFIssuers);     // rows' copies, epilogue, MMAs
     }
-    tc::mbar_init(drain, 1);
+    for (int i = 0; i < kFIssuers; ++i) tc::mbar_init(&drain[i], 1);
     *abort = 0;
     tc::fence_mbar_init();
-    tc::prefetch_tmap(&maps.a[0]);
+    tc::prefetch_tmap(&maps.a[7]);
     tc::prefetch_tmap(&maps.x);
+    tc::prefetch_tmap(&maps.a2);
   }
-  const uint32_t ncol = g.N <= 32 ? 32 : g.N <= 64 ? 64 : g.N <= 128 ? 128 : 256;     // of an accumulator
-  if (warp == 1) tc::tmem_alloc(tmem_slot, 2 * ncol);
+  const uint32_t ncol = g.N <= 16 ? 16 : g.N <= 32 ? 32 : 64;      // of an accumulator; four a tile, two tiles
+  if (warp == 1) tc::tmem_alloc(tmem_slot, 8 * ncol);
   for (int i = tid; i < G; i += kFThreads) mask[i] = i >= g.E ? (g.R == 64 ? ~0ull : (1ull << g.R) - 1) : 0ull;
   pdl_enter();
+  // the first claim's answer passes behind the tables
+  int claim = 0;
+  if (tid == 0) claim = atomicAdd(g.ticket, 1);
   __syncthreads();
 
-  Cut c1 = {g.mt1, g.nk1, 1, 1, 0}, c2 = {g.mt2, g.nk2, 0, 1, 0};
-  {
-    // the tokens of every expert; an assignment of weight 0 is left out
-    const int A = g.R * g.k;
-    for (int a = tid; a < A; a += kFThreads) {
-      const int e = g.ids[a];
-      if (e < 0 || e >= g.E) {
-        if (blockIdx.x == 0) set_status(g.status, MOE_DEV_BAD_EXPERT_ID);
-      } else if (g.wts[a] != 0.f) {
-        atomicOr(&mask[e], 1ull << (a / g.k));
-      }
+  // the tokens of every expert; an assignment of weight 0 is left out
+  for (int a = tid; a < A; a += kFThreads) {
+    int e = g.ids[a];
+    const float w = g.wts[a];
+    if (e < 0 || e >= g.E) {
+      if (blockIdx.x == 0) set_status(g.status, MOE_DEV_BAD_EXPERT_ID);
+      e = -1;
+    } else if (w != 0.f) {
+      atomicOr(&mask[e], 1ull << (a / g.k));
     }
-    __syncthreads();
-    // groups with tokens, and every group's first row: prefix sums over the groups
+    sid[a] = e;
+    swt[a] = w;
+  }
+  __syncthreads();
+  // groups with tokens, and every group's first row: prefix sums over the groups
+  {
     const int per = (G + kFThreads - 1) / kFThreads, e0 = tid * per, e1 = min(G, e0 + per);
     int live = 0, rows = 0;
     for (int e = e0; e < e1; ++e) {
@@ -257,65 +225,84 @@ __global__ void __launch_bounds__(kFThreads, 1) k_few_layer(const FewArgs g, con
       const int a = __shfl_up_sync(kFull, il, o), b = __shfl_up_sync(kFull, ir, o);
       if (lane >= o) { il += a; ir += b; }
     }
-    if (lane == 31) { tmp[2 + warp] = il; tmp[10 + warp] = ir; }
+    if (lane == 31) { tmp[1 + warp] = il; tmp[11 + warp] = ir; }
     __syncthreads();
     il -= live;
     ir -= rows;
-    for (int w = 0; w < warp; ++w) { il += tmp[2 + w]; ir += tmp[10 + w]; }
+    for (int w = 0; w < warp; ++w) { il += tmp[1 + w]; ir += tmp[11 + w]; }
     for (int e = e0; e < e1; ++e) {
       rowof[e] = ir;
-      gplace[e] = il;
       if (mask[e]) glist[il++] = e;
-      ir += __popcll(mask[e]);
+      const int m = __popcll(mask[e]);
+      if (e >= g.E)
+        for (int i = 0; i < m; ++i) wrow[ir + i] = 1.f;
+      ir += m;
     }
     if (tid == kFThreads - 1) tmp[0] = il;
-    __syncthreads();
-    c1.ng = c2.ng = tmp[0];
-    // rows and weights of the slots: a repeated id's weights add up, in slot order, at its first slot
-    for (int a = tid; a < g.R * kp; a += kFThreads) {
-      const int t = a / kp, j = a - t * kp;
-      int row = -1;
-      float w = 1.f;
-      int e = g.E + j - g.k;
-      bool first = true;
-      if (j < g.k) {
-        e = g.ids[t * g.k + j];
-        first = e >= 0 && e < g.E && (mask[e] >> t & 1);
-        if (first) {
-          w = 0.f;
-          for (int i = 0; i < g.k; ++i)
-            if (g.ids[t * g.k + i] == e) {
-              if (i < j) first = false;
-              w += g.wts[t * g.k + i];
-            }
-        }
-      }
-      if (first) {
-        row = rowof[e] + __popcll(mask[e] & ((1ull << t) - 1));
-        wrow[row] = w;
-      }
-      slot_of[a] = make_int2(row, first ? gplace[e] | (row - rowof[e]) << 16 : 0);
-    }
   }
-  c1.total = (int64_t)c1.ng * c1.mt * c1.nk;
-  c1.P = (int)max((int64_t)1, min((int64_t)gridDim.x, c1.total / g.least));
-  c2.total = (int64_t)c2.ng * c2.mt * c2.nk;
-  c2.P = (int)max((int64_t)1, min((int64_t)gridDim.x, c2.total / g.least));
-  if (c1.total == 0) c1.P = c2.P = 0;       // no token has an expert: nothing to claim
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
+  // a row's weight, by and for the epilogue's warps: a repeated id's weights add up, in slot order
+  for (int a = tid - 128; warp >= 4 && warp < 8 && a < A; a += 128) {
+    const int t = a / g.k, e = sid[a];
+    if (e < 0 || !(mask[e] >> t & 1)) continue;
+    bool first = true;
+    float w = 0.f;
+    for (int i = t * g.k; i < (t + 1) * g.k; ++i)
+      if (sid[i] == e) {
+        if (i < a) first = false;
+        w += swt[i];
+      }
+    if (first) wrow[rowof[e] + __popcll(mask[e] & ((1ull << t) - 1))] = w;
+  }
+  const int ng = tmp[0];
   const uint32_t tmem = *tmem_slot;
-  const uint32_t full_u = tc::smem_u32(full), empty_u = tc::smem_u32(empty);
-  const uint32_t sa_u = tc::smem_u32(sa), sb_u = tc::smem_u32(sb);
-  const int shares = c1.P + c2.P;
+  const uint32_t full_u = tc::smem_u32(full), empty_u = tc::smem_u32(empty), ring_u = tc::smem_u32(ring);
+  const int64_t total1 = (int64_t)ng * g.F1;
+  // ranges of both products; without a token that has an expert only the second's, of zeros
+  const int P1 = (int)min((int64_t)gridDim.x, (total1 + kFLeast - 1) / kFLeast);
+  const int P2 = g.Pf * g.S2;
 
-  // The n-th claimed share, by every role but the claiming one: -1 at the end or
+  // The n-th claimed range, by every role but the claiming one: -1 at the end or
   // where a wait ran out.
   auto take = [&](uint32_t n) -> int {
     if (!tc::mbar_wait(&qfull[n % kFQueue], (n / kFQueue) & 1, abort)) return -1;
-    const int s = *reinterpret_cast<volatile int*>(&queue[n % kFQueue]);
-    return s;
+    return *reinterpret_cast<volatile int*>(&queue[n % kFQueue]);
+  };
+  auto range_of = [&](int s) -> FewRange {
+    if (s < P1) return {total1 * s / P1, total1 * (s + 1) / P1, 0, 0, 0};
+    const int j = (s - P1) / g.S2, part = (s - P1) % g.S2, g0 = ng * part / g.S2;
+    return {(int64_t)g.F2 * j / g.Pf, (int64_t)g.F2 * (j + 1) / g.Pf, g0, g0, ng * (part + 1) / g.S2};
+  };
+  auto next_tile = [&](bool second, FewRange& r, FewTile& t) -> bool {
+    if (r.at >= r.end) return false;
+    if (!second) {
+      const int gi = (int)(r.at / g.F1);
+      t.e = glist[gi];
+      t.f0 = (int)(r.at - (int64_t)gi * g.F1);
+      // of the range in this group; the last two tiles alike, so that neither is narrow
+      const int left = (int)min((int64_t)(g.F1 - t.f0), r.end - r.at), step = g.rows1 / 8;
+      t.len = left >= 2 * g.rows1 ? g.rows1 : left > g.rows1 ? (left / 2 + step - 1) / step * step : left;
+      t.box = (t.len + step - 1) / step * step;
+      r.at += t.len;
+      t.rows = g.xrows;
+      t.N = g.N;
+    } else {
+      if (r.g0 == r.g1) return false;
+      t.e = glist[r.g];
+      t.f0 = (int)r.at;
+      t.len = (int)min((int64_t)g.box2, r.end - r.at);
+      t.box = g.box2;
+      if (++r.g == r.g1) {
+        r.g = r.g0;
+        r.at += t.len;
+      }
+      const int m = __popcll(mask[t.e]);
+      t.rows = 8 << box_of(m);
+      t.N = (m + 15) & ~15;
+    }
+    return true;
   };
 
   if (warp == 0) {
@@ -326,30 +313,24 @@ __global__ void __launch_bounds__(kFThreads, 1) k_few_layer(const FewArgs g, con
       uint32_t phase = 1, issued = 0;
       bool ok = true;
       for (uint32_t n = 0; ok; ++n) {
-        int s = atomicAdd(g.ticket, 1);
-        if (s >= shares) s = -1;
+        const int c = n == 0 ? claim : atomicAdd(g.ticket, 1), s = c < P1 + P2 ? c : -1;
         if (!tc::mbar_wait(&qempty[n % kFQueue], ((n / kFQueue) & 1) ^ 1, abort)) { ok = false; break; }
         queue[n % kFQueue] = s;
         tc::mbar_arrive(&qfull[n % kFQueue]);
         if (s < 0) break;
-        const bool second = s >= c1.P;
-        const Cut& c = second ? c2 : c1;
-        if (second) s -= c1.P;
-        const int K = second ? g.K2 : g.K1, rows = second ? kFM : g.rows1;
-        const CUtensorMap* map = &maps.a[second];
+        const bool second = s >= P1;
+        const int K = second ? g.K2 : g.K1, hs = second ? g.hs2 : 2, nh = (K + kFH - 1) / kFH;
         const bool chunks = K % kFH == 0;
-        const int64_t end = c.begin(s + 1);
-        for (int64_t at = c.begin(s); ok && at < end;) {
-          Piece p;
-          if (second) piece_at<true>(c, at, end, p);
-          else piece_at<false>(c, at, end, p);
-          at = p.t0 + p.k1;
-          const int e = glist[p.gi], f0 = p.j * rows;
-          for (int kb = p.k0; kb < p.k1; ++kb) {
+        FewRange r = range_of(s);
+        FewTile t;
+        while (ok && next_tile(second, r, t)) {
+          const int half = t.box * 128 * (!second && gated ? 2 : 1);
+          const CUtensorMap* map = second ? &maps.a2 : &maps.a[t.box / (g.rows1 / 8) - 1];
+          for (int h = 0; h < nh; h += hs) {
             if (!tc::bar_wait(empty_u + 8 * slot, phase, abort)) { ok = false; break; }
-            const int k = kb * kFK, n = chunks || K - k > kFH ? 2 : 1;
-            tc::bar_arrive_expect_tx(full_u + 8 * slot, n * kFA);
-            copy_weights(sa_u + 2 * slot * kFA, kFA, map, chunks, k, n, f0, e, full_u + 8 * slot, policy);
+            const int n_h = chunks ? hs : min(hs, nh - h);
+            tc::bar_arrive_expect_tx(full_u + 8 * slot, n_h * half);
+            copy_weights(ring_u + slot * g.slot, half, map, chunks, h * kFH, n_h, t.f0, t.e, full_u + 8 * slot, policy);
             ++issued;
             if (++slot == g.stages) {
               slot = 0;
@@ -358,9 +339,7 @@ __global__ void __launch_bounds__(kFThreads, 1) k_few_layer(const FewArgs g, con
           }
         }
       }
-      if (!ok || *abort) {
-        wind_down(full, issued, g.stages);
-      }
+      if (!ok || *abort) wind_down(full, issued, g.stages);
     }
   } else if (warp == 2) {
     // ---------------- the rows' copies ----------------
@@ -369,16 +348,13 @@ __global__ void __launch_bounds__(kFThreads, 1) k_few_layer(const FewArgs g, con
       uint32_t phase = 1, issued = 0;
       bool ok = true, ready = false;
       for (uint32_t n = 0; ok; ++n) {
-        int s = take(n);
+        const int s = take(n);
         if (s < 0) break;
-        const bool second = s >= c1.P;
-        const Cut& c = second ? c2 : c1;
-        if (second) s -= c1.P;
+        const bool second = s >= P1;
         if (second && !ready) {
-          // every tile of the first product has written its rows
-          const int want = c1.ng * c1.mt;
+          // every range of the first product has written its rows
           const long long t0 = clock64();
-          for (uint32_t it = 1; ld_acquire_gpu(g.done) < want; ++it) {
+          for (uint32_t it = 1; ld_acquire_gpu(g.done) < P1; ++it) {
             if ((it & 15) == 0 && (*abort || clock64() - t0 > 4000000000ll)) {
               *abort = 1;
               ok = false;
@@ -389,27 +365,20 @@ __global__ void __launch_bounds__(kFThreads, 1) k_few_layer(const FewArgs g, con
           fence_proxy_async_global();
           ready = true;
         }
-        const int K = second ? g.K2 : g.K1;
+        const int K = second ? g.K2 : g.K1, hs = second ? g.hs2 : 2, nh = (K + kFH - 1) / kFH;
         const bool chunks = K % kFH == 0;
-        const int64_t end = c.begin(s + 1);
-        for (int64_t at = c.begin(s); ok && at < end;) {
-          Piece p;
-          if (second) piece_at<true>(c, at, end, p);
-          else piece_at<false>(c, at, end, p);
-          at = p.t0 + p.k1;
-          int r0 = 0, wide = g.N;
-          const CUtensorMap* map = &maps.x;
-          if (second) {
-            const int e = glist[p.gi], m = __popcll(mask[e]);
-            wide = (m + 15) & ~15;
-            map = &maps.y[wide / 16 - 1];
-            r0 = rowof[e];
-          }
-          for (int kb = p.k0; kb < p.k1; ++kb) {
+        FewRange r = range_of(s);
+        FewTile t;
+        while (ok && next_tile(second, r, t)) {
+          // behind the stage's weights
+          const int a_bytes = hs * t.box * 128 * (!second && gated ? 2 : 1), half = t.rows * 128;
+          const CUtensorMap* map = second ? &maps.y[box_of(t.rows)] : &maps.x;
+          const int r0 = second ? rowof[t.e] : 0;
+          for (int h = 0; h < nh; h += hs) {
             if (!tc::bar_wait(empty_u + 8 * slot, phase, abort)) { ok = false; break; }
-            const int k = kb * kFK, n = chunks || K - k > kFH ? 2 : 1;
-            tc::bar_arrive_expect_tx(full_u + 8 * slot, n * wide * 128);
-            copy_rows(sb_u + 2 * slot * b_half, wide * 128, map, chunks, k, n, r0, full_u + 8 * slot);
+            const int n_h = chunks ? hs : min(hs, nh - h);
+            tc::bar_arrive_expect_tx(full_u + 8 * slot, n_h * half);
+            copy_rows(ring_u + slot * g.slot + a_bytes, half, map, chunks, h * kFH, n_h, r0, full_u + 8 * slot);
             ++issued;
             if (++slot == g.stages) {
               slot = 0;
@@ -419,42 +388,37 @@ __global__ void __launch_bounds__(kFThreads, 1) k_few_layer(const FewArgs g, con
         }
         tc::mbar_arrive(&qempty[n % kFQueue]);
       }
-      if (!ok || *abort) {
-        wind_down(full, issued, g.stages);
-      }
+      if (!ok || *abort) wind_down(full, issued, g.stages);
     }
-  } else if (warp == 1) {
+  } else if (warp < 4 || warp >= 8) {
     // ---------------- MMAs ----------------
     if (lane == 0) {
-      const uint64_t ad0 = tc::smem_desc_sw128(sa_u), bd0 = tc::smem_desc_sw128(sb_u);
-      const uint32_t hi = (uint32_t)(ad0 >> 32), a_step = kFA / 16;
+      const int step = warp == 1 ? 0 : warp == 3 ? 1 : warp - 6;       // of every 64 of the reduction
+      const uint64_t d0 = tc::smem_desc_sw128(ring_u);
+      const uint32_t lo = (uint32_t)d0 + 2 * step, hi = (uint32_t)(d0 >> 32);
       int slot = 0;
       uint32_t phase = 0, tiles = 0;
       bool ok = true;
       for (uint32_t n = 0; ok; ++n) {
-        int s = take(n);
+        const int s = take(n);
         if (s < 0) break;
-        const bool second = s >= c1.P;
-        const Cut& c = second ? c2 : c1;
-        if (second) s -= c1.P;
-        const int K = second ? g.K2 : g.K1;
-        const int64_t end = c.begin(s + 1);
-        for (int64_t at = c.begin(s); ok && at < end; ++tiles) {
-          Piece p;
-          if (second) piece_at<true>(c, at, end, p);
-          else piece_at<false>(c, at, end, p);
-          at = p.t0 + p.k1;
+        const bool second = s >= P1;
+        const int K = second ? g.K2 : g.K1, hs = second ? g.hs2 : 2, nh = (K + kFH - 1) / kFH;
+        FewRange r = range_of(s);
+        FewTile t;
+        while (ok && next_tile(second, r, t)) {
           const int d = tiles & 1;
           if (!tc::mbar_wait(&accempty[d], ((tiles >> 1) & 1) ^ 1, abort)) { ok = false; break; }
           tc::fence_after_sync();
-          const int wide = second ? (__popcll(mask[glist[p.gi]]) + 15) & ~15 : g.N;
-          const uint32_t idesc = tc::idesc_16bit(kFM, wide, g.dtype == MOE_DT_BF16, 0, 0), dt = tmem + d * ncol, b_step = wide * 8;
-          for (int kb = p.k0; kb < p.k1; ++kb) {
+          const int rows = t.box * (!second && gated ? 2 : 1);
+          const uint32_t idesc = tc::idesc_16bit(rows <= 64 ? 64 : kFM, t.N, g.dtype == MOE_DT_BF16, 0, 0), dt = tmem + (4 * d + step) * ncol;
+          for (int h = 0; h < nh; h += hs) {
             if (!tc::bar_wait(full_u + 8 * slot, phase, abort)) { ok = false; break; }
             tc::fence_after_sync();
-            const uint32_t a0 = (uint32_t)ad0 + 2 * slot * a_step, b0 = (uint32_t)bd0 + slot * (b_half / 8);
-            tc::mma_f16_x4<1>(dt, a0, hi, 2, b0, hi, 2, idesc, kb > p.k0);
-            if (K - kb * kFK > kFH) tc::mma_f16_x4<1>(dt, a0 + a_step, hi, 2, b0 + b_step, hi, 2, idesc, 1u);
+            const uint32_t a0 = lo + slot * (g.slot / 16), b0 = a0 + hs * rows * 8;
+            const int n_h = min(hs, nh - h);
+            for (int i = 0; i < n_h; ++i)
+              tc::mma_f16_ss(dt, ((uint64_t)hi << 32) | (a0 + i * rows * 8), ((uint64_t)hi << 32) | (b0 + i * t.rows * 8), idesc, h + i > 0);
             tc::bar_commit(empty_u + 8 * slot);
             if (++slot == g.stages) {
               slot = 0;
@@ -463,158 +427,138 @@ __global__ void __launch_bounds__(kFThreads, 1) k_few_layer(const FewArgs g, con
           }
           if (!ok) break;
           tc::mma_commit(&accfull[d]);
+          ++tiles;
         }
         tc::mbar_arrive(&qempty[n % kFQueue]);
       }
       // every MMA of this thread has completed once `drain` fires
-      tc::mma_commit(drain);
+      tc::mma_commit(&drain[step]);
       volatile int never = 0;
-      tc::mbar_wait(drain, 0, &never, 400000000ll);
+      tc::mbar_wait(&drain[step], 0, &never, 400000000ll);
     }
     __syncwarp();
-  } else if (warp >= 4) {
+  } else {
     // ---------------- epilogue ----------------
-    const int et = tid - 128, q = warp & 3;               // et: the tile's lane
+    const int et = tid - 128, q = warp & 3;
     const uint32_t lanes = tmem + ((uint32_t)(q * 32) << 16);
-    const bool gated = act_gated(g.act.act);
     uint32_t tiles = 0;
     bool ok = true;
     for (uint32_t n = 0; ok; ++n) {
-      int s = take(n);
-      if (!epi_all(s >= 0)) break;
-      const bool second = s >= c1.P;
-      const Cut& c = second ? c2 : c1;
-      if (second) s -= c1.P;
-      const int64_t end = c.begin(s + 1);
-      for (int64_t at = c.begin(s); at < end; ++tiles) {
-        Piece p;
-        if (second) piece_at<true>(c, at, end, p);
-        else piece_at<false>(c, at, end, p);
-        at = p.t0 + p.k1;
+      const int s = take(n);
+      if (!epi_all<1, 128>(s >= 0)) break;
+      const bool second = s >= P1;
+      FewRange r = range_of(s);
+      FewTile t;
+      const int h0 = (int)r.at, nf = (int)(r.end - r.at);      // second: the range
+      if (second && r.g0 == r.g1) {
+        // no group, nothing to add
+        if (g.S2 == 1) {
+          for (int h = et; h < nf; h += 128)
+            for (int i = 0; i < g.R; ++i) reinterpret_cast<uint16_t*>(g.out)[i * g.ldo + h0 + h] = 0;
+        } else if (et < nf) {
+          for (int i = 0; i < g.R; ++i) g.part[((int64_t)(s - P1) * g.R + i) * g.box2 + et] = 0.f;
+        }
+      }
+      while (next_tile(second, r, t)) {
         const int d = tiles & 1;
         const bool got = tc::mbar_wait(&accfull[d], (tiles >> 1) & 1, abort);
-        if (!epi_all(got)) { ok = false; break; }
+        ++tiles;
+        if (!epi_all<1, 128>(got)) { ok = false; break; }
         tc::fence_after_sync();
-        const uint32_t acc = lanes + d * ncol;
+        const uint32_t acc = lanes + d * 4 * ncol;
         auto release = [&] {
           tc::fence_before_sync();
           __syncwarp();
           if (lane == 0) tc::mbar_arrive(&accempty[d]);
         };
-        const int e = glist[p.gi];
-        const unsigned long long toks = mask[e];
-        const int m = __popcll(toks);
-        const bool head = p.k0 == 0, whole = head && p.k1 == c.nk;
+        unsigned long long rem = mask[t.e];
+        const int m = __popcll(rem);
+        // the thread's row of the tile: an MMA of 64 rows leaves sixteen to each warp's lanes
+        const int arows = t.box * (!second && gated ? 2 : 1);
+        const int row = arows > 64 ? et : lane < 16 ? q * 16 + lane : kFM;
         if (!second) {
-          // columns of the group's tokens, kFCols at a time, each as 128 lanes' fp32
-          auto columns = [&](unsigned long long& rem, int i0, int nc, uint32_t (&v)[kFCols]) {
+          const int r0 = rowof[t.e];
+          for (int i0 = 0; i0 < m; i0 += kFCols) {
+            const int nc = min(kFCols, m - i0);
+            uint32_t v[kFCols][4];
 #pragma unroll
             for (int i = 0; i < kFCols; ++i)
-              if (i < nc) tmem_ld1(acc + (next_bit(rem)), v[i]);
+              if (i < nc) {
+                const uint32_t c = acc + next_bit(rem);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) tmem_ld1(c + j * ncol, v[i][j]);
+              }
             tc::tmem_wait_ld();
-          };
-          bool mine = whole;
-          int s0 = s, s1 = s;
-          if (!whole) {
-            s0 = c.share_of(p.t0);
-            s1 = c.share_of(p.t0 + c.nk - 1);
-            float* to = g.part + (int64_t)(2 * s + head) * g.N * kFM;
-            unsigned long long rem = toks;
-            for (int i0 = 0; i0 < m; i0 += kFCols) {
-              uint32_t v[kFCols];
-              const int nc = min(kFCols, m - i0);
-              columns(rem, i0, nc, v);
+            if (row < kFM)
 #pragma unroll
               for (int i = 0; i < kFCols; ++i)
-                if (i < nc) to[(i0 + i) * kFM + et] = __uint_as_float(v[i]);
-            }
-            release();
-            __threadfence();
+                if (i < nc) stage[i * kFM + row] = add4(v[i]);
+            if (i0 + kFCols >= m) release();
             epi_sync();
-            if (et == 0) {
-              const int old = atom_add_acq_rel_gpu(&g.split[s0], 1);
-              tmp[1] = old == s1 - s0;
-            }
-            epi_sync();
-            mine = *reinterpret_cast<volatile int*>(&tmp[1]);
-            __threadfence();
-          }
-          if (mine) {
-            unsigned long long rem = toks;
-            for (int i0 = 0; i0 < m; i0 += kFCols) {
-              const int nc = min(kFCols, m - i0);
-              float f[kFCols];
-              if (whole) {
-                uint32_t v[kFCols];
-                columns(rem, i0, nc, v);
-#pragma unroll
-                for (int i = 0; i < kFCols; ++i) f[i] = __uint_as_float(v[i]);
-              } else {
-#pragma unroll
-                for (int i = 0; i < kFCols; ++i) f[i] = 0.f;
-                for (int w = s0; w <= s1; ++w) {
-                  const float* from = g.part + (int64_t)(2 * w + (w == s0)) * g.N * kFM;
-#pragma unroll
-                  for (int i = 0; i < kFCols; ++i)
-                    if (i < nc) f[i] += __ldcg(from + (i0 + i) * kFM + et);
-                }
+            for (int o = et; o < nc * g.rows1; o += 128) {
+              const int i = o / g.rows1, l = o % g.rows1;
+              if (l >= t.len) continue;
+              const int f = t.f0 + l;
+              float a = stage[i * kFM + l], u = gated ? stage[i * kFM + t.box + l] : 0.f;
+              if (g.b1) {
+                a += g.b1[(int64_t)t.e * 2 * g.F1 + f];
+                u += g.b1[(int64_t)t.e * 2 * g.F1 + g.F1 + f];
               }
-#pragma unroll
-              for (int i = 0; i < kFCols; ++i)
-                if (i < nc) stage[i * kFM + et] = f[i];
-              if (whole && i0 + kFCols >= m) release();
-              epi_sync();
-              const int F = gated ? 64 : 128;             // features of the tile
-              for (int o = et; o < nc * F; o += 128) {
-                const int i = o / F, l = o % F, f1 = p.j * F + l;
-                if (f1 >= g.F1) continue;
-                float a = stage[i * kFM + l], u = gated ? stage[i * kFM + 64 + l] : 0.f;
-                if (g.b1) {
-                  a += g.b1[(int64_t)e * 2 * g.F1 + f1];
-                  u += g.b1[(int64_t)e * 2 * g.F1 + g.F1 + f1];
-                }
-                const int row = rowof[e] + i0 + i;
-                const float y = gated ? act_two(a, u, g.act) : act_one(a, g.act.act);
-                reinterpret_cast<uint16_t*>(g.y)[(int64_t)row * g.ldy + f1] = E::from(wrow[row] * y);
-              }
-              epi_sync();
+              const float y = gated ? act_two(a, u, g.act) : act_one(a, g.act.act);
+              reinterpret_cast<uint16_t*>(g.y)[(int64_t)(r0 + i0 + i) * g.ldy + f] = E::from(wrow[r0 + i0 + i] * y);
             }
-            // the rows of this tile are in memory, for the tensor copies of any CTA
-            __threadfence();
-            fence_proxy_async_global();
             epi_sync();
-            if (et == 0) atom_add_acq_rel_gpu(g.done, 1);
           }
         } else {
-          const int h = p.j * kFM + et;
-          float* to = head ? g.zrow + (int64_t)rowof[e] * g.ldz32 + h : g.part + (int64_t)s * g.N * kFM + et;
-          const int64_t step = head ? g.ldz32 : kFM;
+          // a thread's feature is its own throughout: its sums need no barrier
+          const bool mine = row < t.len;
+          if (mine && t.e == glist[r.g0])
+            for (int i = 0; i < g.R; ++i) sums[i * g.box2 + row] = 0.f;
           for (int i0 = 0; i0 < m; i0 += kFCols) {
-            uint32_t v[kFCols];
+            uint32_t v[kFCols][4];
 #pragma unroll
             for (int i = 0; i < kFCols; ++i)
-              if (i0 + i < m) tmem_ld1(acc + i0 + i, v[i]);
+              if (i0 + i < m)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) tmem_ld1(acc + i0 + i + j * ncol, v[i][j]);
             tc::tmem_wait_ld();
 #pragma unroll
             for (int i = 0; i < kFCols; ++i)
-              if (i0 + i < m) to[(i0 + i) * step] = __uint_as_float(v[i]);
+              if (i0 + i < m) {
+                const int tok = next_bit(rem);
+                if (mine) sums[tok * g.box2 + row] += add4(v[i]);
+              }
           }
           release();
-          // the share's last piece of this feature tile: whoever finishes it joins
-          // the tokens' rows
-          if (at < end && at / c.nk / c.ng == p.j) continue;
-          const int64_t j0 = (int64_t)p.j * c.ng * c.nk;
-          const int n_shares = c.share_of(j0 + (int64_t)c.ng * c.nk - 1) - c.share_of(j0) + 1;
+          if (mine && t.e == glist[r.g1 - 1])
+            for (int i = 0; i < g.R; ++i) {
+              const float v = sums[i * g.box2 + row];
+              if (g.S2 == 1) reinterpret_cast<uint16_t*>(g.out)[i * g.ldo + t.f0 + row] = E::from(v);
+              else g.part[((int64_t)(s - P1) * g.R + i) * g.box2 + row] = v;
+            }
+        }
+      }
+      if (ok && !second) {
+        // the range's rows are in memory, for the tensor copies of any CTA
+        __threadfence();
+        fence_proxy_async_global();
+        epi_sync();
+        if (et == 0) atom_add_acq_rel_gpu(g.done, 1);
+      }
+      if (ok && second && g.S2 > 1) {
+        // whoever is the last of the features' parts adds them, in order
+        const int j = (s - P1) / g.S2;
+        __threadfence();
+        epi_sync();
+        if (et == 0) tmp[0] = atom_add_acq_rel_gpu(&g.joined[j], 1) == g.S2 - 1;
+        epi_sync();
+        if (*reinterpret_cast<volatile int*>(&tmp[0])) {
           __threadfence();
-          epi_sync();
-          if (et == 0) {
-            const int old = atom_add_acq_rel_gpu(&g.split2[p.j], 1);
-            tmp[1] = old == n_shares - 1;
-          }
-          epi_sync();
-          if (*reinterpret_cast<volatile int*>(&tmp[1])) {
-            __threadfence();
-            join_tokens<E>(g, c, p.j, slot_of, kp, q, lane);
+          for (int i = et; i < g.R * nf; i += 128) {
+            const int t = i / nf, h = i - t * nf;
+            float v = 0.f;
+            for (int w = 0; w < g.S2; ++w) v += __ldcg(g.part + ((int64_t)(j * g.S2 + w) * g.R + t) * g.box2 + h);
+            reinterpret_cast<uint16_t*>(g.out)[t * g.ldo + h0 + h] = E::from(v);
           }
         }
       }
@@ -623,15 +567,12 @@ __global__ void __launch_bounds__(kFThreads, 1) k_few_layer(const FewArgs g, con
     }
   }
 
-  if (shares == 0 && blockIdx.x == 0)      // no token has an expert
-    for (int64_t i = tid; i < (int64_t)g.R * g.F2; i += kFThreads)
-      reinterpret_cast<uint16_t*>(g.out)[i / g.F2 * g.ldo + i % g.F2] = 0;
   tc::fence_before_sync();
   __syncthreads();
   if (tid == 0 && *abort) set_status(g.status, MOE_DEV_TIMEOUT);
   if (warp == 1) {
     tc::fence_after_sync();
-    tc::tmem_dealloc(tmem, 2 * ncol);
+    tc::tmem_dealloc(tmem, 8 * ncol);
   }
 }
 
@@ -788,14 +729,7 @@ __global__ void __launch_bounds__(kLThreads, 1) k_few_linear(const FewArgs g, co
         }
       }
       const bool got = tc::mbar_wait(&accfull[d], (done >> 1) & 1, abort);
-      // what one of the eight warps gives up, all do: they meet at barriers below
-      uint32_t all;
-      __syncwarp();
-      asm volatile("{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n bar.red.and.pred q, 3, 256, p;\n selp.u32 %0, 1, 0, q;\n}"
-                   : "=r"(all)
-                   : "r"((uint32_t)got)
-                   : "memory");
-      if (!all) break;
+      if (!epi_all<3, 256>(got)) break;
       tc::fence_after_sync();
       for (int c = grp * kLChunk; c < nr; c += 2 * kLChunk) {
         const int n = min(kLChunk, nr - c);
@@ -854,53 +788,66 @@ __global__ void __launch_bounds__(kLThreads, 1) k_few_linear(const FewArgs g, co
 // ---- host -------------------------------------------------------------------------
 static int64_t up(int64_t n, int64_t t) { return (n + t - 1) / t; }
 
-// Weights [G][halves][rows][K]: boxes of 64 x box rows x halves, twice along K
-// where K is a whole number of 64 (see copy_weights).
+// Weights [G][halves][rows][K]: boxes of 64 x box rows x halves, `depth` of them
+// along K where K is a whole number of 64 (see copy_weights).
 static bool map_weights(CUtensorMap* map, const void* w, int64_t K, int64_t rows, int halves, int64_t ld, int64_t G,
-                        int64_t group, int box_rows) {
+                        int64_t group, int box_rows, int depth) {
   const bool chunks = K % kFH == 0;
   const int64_t dims[5] = {chunks ? kFH : K, rows, halves, chunks ? K / kFH : 1, G};
   const int64_t strides[4] = {ld, halves > 1 ? rows * ld : ld, chunks ? kFH : ld, G > 1 ? group : ld};
-  const int box[5] = {kFH, box_rows, halves, chunks ? 2 : 1, 1};
+  const int box[5] = {kFH, box_rows, halves, chunks ? depth : 1, 1};
   return make_tmap(map, w, 2, 5, dims, strides, box);
 }
-static bool map_rows(CUtensorMap* map, const void* x, int64_t K, int64_t rows, int64_t ld, int box_rows) {
+static bool map_rows(CUtensorMap* map, const void* x, int64_t K, int64_t rows, int64_t ld, int box_rows, int depth) {
   const bool chunks = K % kFH == 0;
   const int64_t dims[3] = {chunks ? kFH : K, rows, chunks ? K / kFH : 1}, strides[2] = {ld, chunks ? kFH : ld};
-  const int box[3] = {kFH, box_rows, chunks ? 2 : 1};
+  const int box[3] = {kFH, box_rows, chunks ? depth : 1};
   return make_tmap(map, x, 2, 3, dims, strides, box);
-}
-
-template <typename E>
-static cudaError_t launch_layer(FewArgs& g, const FewMaps& maps, cudaStream_t st) {
-  const int G = g.E + g.S, kp = g.k + g.S;
-  const int head = kFBars + kFCols * kFM * 4 + 16 * G + 4 * std::min(G, g.R * kp) + 12 * g.R * kp + 64;
-  g.head = (head + 1023) / 1024 * 1024;
-  const int stage = 2 * (kFA + g.N * 128);
-  g.stages = std::min(kFMaxStages, (kFSmem - 1024 - g.head) / stage);
-  const int smem = 1024 + g.head + g.stages * stage;
-  static std::atomic<bool> done[kMaxDevices] = {};
-  const cudaError_t e = set_smem_once((const void*)k_few_layer<E>, kFSmem, done);
-  if (e != cudaSuccess) return e;
-  note_launch();
-  return launch_pdl(k_few_layer<E>, dim3(std::min(device_sms(), kFewShares)), dim3(kFThreads), smem, st, g, maps);
 }
 
 cudaError_t launch_few_layer(FewArgs g, const void* x, int64_t ldx, const void* w1, int64_t g1, int64_t ld1, const void* w2,
                              int64_t g2, int64_t ld2, cudaStream_t st) {
-  const int G = g.E + g.S, halves = act_gated(g.act.act) ? 2 : 1;
+  const int G = g.E + g.S, A = g.R * g.k, halves = act_gated(g.act.act) ? 2 : 1;
+  const int grid = std::min(device_sms(), kFewSms);
   g.N = (g.R + 15) & ~15;
+  g.xrows = (g.R + 7) & ~7;
   g.rows1 = kFM / halves;
-  g.mt1 = (int)up(g.F1, g.rows1); g.nk1 = (int)up(g.K1, kFK);
-  g.mt2 = (int)up(g.F2, kFM); g.nk2 = (int)up(g.K2, kFK);
-  g.least = 4;
+  // The second product's ranges, with all groups or 1 / S2 of them: the time of the
+  // halves (130 cycles of MMA issue and barriers, or the copies of their rows) and
+  // of the join. Groups that some token chooses, when each chooses k at random.
+  const double touched = g.E * (1 - std::pow(1 - (double)g.k / g.E, g.R)) + g.S;
+  double least = 1e300;
+  for (int S2 = 1; S2 <= 4; S2 *= 2) {
+    const int Pf = (int)std::min<int64_t>(grid / S2, up(g.F2, kFLeast)), f = (int)up(g.F2, Pf);
+    if (S2 > 1 && f > kFM) break;
+    const double cost = touched / S2 * up(g.K2, kFH) * std::max(150.0, 128.0 * f / 23.5) * up(f, kFM) + (S2 > 1 ? 5000 : 0);
+    if (cost < least) {
+      least = cost;
+      g.S2 = S2; g.Pf = Pf;
+      g.box2 = std::min(kFM, (f + 7) & ~7);
+    }
+  }
+  int box_t = 8;                                    // rows of the second product's widest copy
+  while (box_t < g.R) box_t *= 2;
+  g.slot = 2 * 128 * (kFM + g.xrows);
+  g.hs2 = std::max(1, g.slot / (128 * (g.box2 + box_t)));
+  const int head = kFBars + kFCols * kFM * 4 + 4 * (g.R * g.box2 + 2) + 12 * G + 4 * std::min(G, A + g.S) + 4 * (A + g.S * g.R) + 8 * A;
+  g.head = (head + 1023) / 1024 * 1024;
+  g.stages = std::min(kFMaxStages, (kFSmem - 1024 - g.head - kFA) / g.slot);
+  const int smem = 1024 + g.head + g.stages * g.slot + kFA;       // behind the ring 16 KB that MMAs may read
   FewMaps maps;
-  if (!map_weights(&maps.a[0], w1, g.K1, g.F1, halves, ld1, G, g1, g.rows1) ||
-      !map_weights(&maps.a[1], w2, g.K2, g.F2, 1, ld2, G, g2, kFM) || !map_rows(&maps.x, x, g.K1, g.R, ldx, g.N))
-    return cudaErrorInvalidValue;
+  for (int i = 0; i < 8; ++i)
+    if (!map_weights(&maps.a[i], w1, g.K1, g.F1, halves, ld1, G, g1, g.rows1 / 8 * (i + 1), 2)) return cudaErrorInvalidValue;
   for (int i = 0; i < 4; ++i)
-    if (!map_rows(&maps.y[i], g.y, g.K2, (int64_t)g.R * (g.k + g.S), g.ldy, 16 * (i + 1))) return cudaErrorInvalidValue;
-  return g.dtype == MOE_DT_BF16 ? launch_layer<Bf16>(g, maps, st) : launch_layer<F16>(g, maps, st);
+    if (!map_rows(&maps.y[i], g.y, g.K2, (int64_t)g.R * (g.k + g.S), g.ldy, 8 << i, g.hs2)) return cudaErrorInvalidValue;
+  if (!map_weights(&maps.a2, w2, g.K2, g.F2, 1, ld2, G, g2, g.box2, g.hs2) || !map_rows(&maps.x, x, g.K1, g.R, ldx, g.xrows, 2))
+    return cudaErrorInvalidValue;
+  const auto kernel = g.dtype == MOE_DT_BF16 ? k_few_layer<Bf16> : k_few_layer<F16>;
+  static std::atomic<bool> done[2][kMaxDevices] = {};
+  const cudaError_t e = set_smem_once((const void*)kernel, kFSmem, done[g.dtype == MOE_DT_BF16]);
+  if (e != cudaSuccess) return e;
+  note_launch();
+  return launch_pdl(kernel, dim3(grid), dim3(kFThreads), smem, st, g, maps);
 }
 
 template <typename E, bool GATED>
@@ -935,7 +882,7 @@ cudaError_t launch_few_linear(FewArgs g, const void* x, int64_t ldx, const void*
   }
   g.mt1 = (int)up(g.F1, g.rows1); g.nk1 = (int)up(g.K1, kFK);
   FewMaps maps = {};
-  if (!map_weights(&maps.a[0], w, g.K1, g.F1, halves, ldw, 1, 0, g.rows1) || !map_rows(&maps.x, x, g.K1, g.R, ldx, g.N))
+  if (!map_weights(&maps.a[0], w, g.K1, g.F1, halves, ldw, 1, 0, g.rows1, 2) || !map_rows(&maps.x, x, g.K1, g.R, ldx, g.N, 2))
     return cudaErrorInvalidValue;
   const int grid = (int)std::min<int64_t>((int64_t)g.mt1 * g.nt, sms);
   if (gated)

@@ -5,9 +5,9 @@
 
 namespace moe {
 
-// Most rows of the dense product, and most shares (CTAs) the layer's products are cut into.
+// Most rows of the dense product, and most CTAs of the layer.
 constexpr int kFewRows = 256;
-constexpr int kFewShares = 152;
+constexpr int kFewSms = 152;
 
 struct FewArgs {
   int R;                      // rows; layer: tokens (at most 64)
@@ -21,22 +21,24 @@ struct FewArgs {
   const int32_t* ids; const float* wts;   // [R][k]
   const float* b1;            // nullable, [E + S][2 F1]
   uint16_t* y; int64_t ldy;   // rows of the second product, by group
-  float* zrow; int64_t ldz32; // its results, fp32, by row
-  int32_t* ticket;            // zero on entry: shares claimed,
-  int32_t* done;              // tiles of the first product,
-  int32_t* split2;            // [mt2] shares done with a feature tile
-  float* part;                // partial sums: 2 kFewShares slots of N x 128 fp32
-  int32_t* split;             // [kFewShares] pieces done of the tiles that span shares; zero on entry
+  int32_t* ticket;            // zero on entry: ranges claimed,
+  int32_t* done;              // ranges of the first product done,
+  int32_t* joined;            // [kFewSms] parts of a range of the second done
+  float* part;                // [kFewSms][R][128] their sums
   // dense
   const void* bias; const void* res; int64_t ldr; void* z; int64_t ldz;
   void* out; int64_t ldo;     // both
   // set by the launch
-  int N, nt, rows1, mt1, nk1, mt2, nk2, least, head, stages;    // nt: dense, tiles of N rows
+  int N;                      // of the MMA; dense: rows a tile
+  int rows1;                  // most features a tile
+  int head, stages;           // bytes in front of the ring, its stages
+  int nt, mt1, nk1;           // dense: tiles of rows and of features, stages of the reduction
+  int Pf, S2;                 // layer: ranges of the second product's features, parts of the groups for each
+  int xrows, box2, hs2, slot; // layer: rows of x a copy takes, features of the second product's tiles, its 64s of the
+                              // reduction a stage, bytes of a stage
 };
 cudaError_t launch_few_layer(FewArgs g, const void* x, int64_t ldx, const void* w1, int64_t g1, int64_t ld1, const void* w2,
                              int64_t g2, int64_t ld2, cudaStream_t st);
 cudaError_t launch_few_linear(FewArgs g, const void* x, int64_t ldx, const void* w, int64_t ldw, cudaStream_t st);
-// Bytes of the layer's partial sums for R tokens.
-inline int64_t few_part_bytes(int R) { return (int64_t)2 * kFewShares * ((R + 15) & ~15) * 128 * 4; }
 
 }  // namespace moe

@@ -36,7 +36,7 @@ static RoutePlan route_plan(int T, int H, int E) {
   // a CTA for every SM, at least 16 rows of H each, and no more partial sums than
   // the last CTA reads in about 40 loads a thread
   const int items = p.tt * (p.ep / 4);
-  p.ks = std::max(1, std::min({kFewShares / (p.z * p.et), H / 16, 40 * kRThreads / items}));
+  p.ks = std::max(1, std::min({kFewSms / (p.z * p.et), H / 16, 40 * kRThreads / items}));
   return p;
 }
 // Floats of partial sums that suffice for T tokens and any fewer.
@@ -47,21 +47,19 @@ static int64_t route_floats(int T, int H, int E) {
   return most;
 }
 
-// Workspace: the counters, y [T (k + S)][I] 16-bit and z [T (k + S)][H] fp32 rows
-// by group, the products' and the router's partial sums.
+// Workspace: the counters, y [T (k + S)][I] 16-bit rows by group, the sums of parts
+// of the groups, the router's partial sums.
+constexpr int kCounters = 16 + kFewSms;
 struct Layer16Ws {
-  int64_t ldy, ldz, counters, y, z, part, router, bytes;
+  int64_t ldy, y, part, router, bytes;
 };
 static Layer16Ws layer16_ws(int T, int H, int I, int E, int k, int S) {
   Layer16Ws w;
   const int64_t rows = (int64_t)T * (k + S);
   w.ldy = (I + 7) / 8 * 8;
-  w.ldz = (H + 127) / 128 * 128;
-  w.counters = 16 + kFewShares + w.ldz / 128;
-  w.y = al256(w.counters * 4);
-  w.z = w.y + al256(rows * w.ldy * 2);
-  w.part = w.z + al256(rows * w.ldz * 4);
-  w.router = w.part + few_part_bytes(T);
+  w.y = al256(kCounters * 4);
+  w.part = w.y + al256(rows * w.ldy * 2);
+  w.router = w.part + (int64_t)kFewSms * T * 128 * 4;
   w.bytes = w.router + al256(route_floats(T, H, E) * 4);
   return w;
 }
@@ -70,7 +68,6 @@ int64_t layer16_ws_bytes(int T, int H, int I, int E, int k, int S) { return laye
 struct RouteArgs16 {
   Layer16Args a;
   RoutePlan p;
-  int64_t counters;
   float* part;          // [z][ks][tt][ep]
 };
 
@@ -100,8 +97,7 @@ __global__ void __launch_bounds__(kRThreads) k_l16_route(const RouteArgs16 r) {
   // the products' counters, which the kernel behind this one starts from
   int32_t* counters = reinterpret_cast<int32_t*>(a.ws);
   if (blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0)
-    for (int64_t i = tid; i < r.counters; i += kRThreads)
-      if (i < kRArrive || i >= kRArrive + 8) counters[i] = 0;
+    if (tid < kRArrive || (tid >= kRArrive + 8 && tid < kCounters)) counters[tid] = 0;
   if (!a.W_r && !a.logits) return;
   const int t0 = blockIdx.z * TT, nt = min(TT, a.T - t0);
   const int64_t set = (int64_t)TT * p.ep;
@@ -272,19 +268,17 @@ static cudaError_t launch_route16(const RouteArgs16& r, cudaStream_t st) {
 
 cudaError_t launch_layer16(const Layer16Args& a, cudaStream_t st) {
   const Layer16Ws w = layer16_ws(a.T, a.H, a.I, a.E, a.k, a.S);
-  RouteArgs16 r = {a, route_plan(a.T, a.H, a.E), w.counters, reinterpret_cast<float*>(a.ws + w.router)};
+  RouteArgs16 r = {a, route_plan(a.T, a.H, a.E), reinterpret_cast<float*>(a.ws + w.router)};
   const cudaError_t e = a.dtype == MOE_DT_BF16 ? launch_route16<Bf16>(r, st) : launch_route16<F16>(r, st);
   if (e != cudaSuccess) return e;
   FewArgs f = {};
   f.R = a.T; f.K1 = a.H; f.F1 = a.I; f.K2 = a.I; f.F2 = a.H; f.act = a.act; f.dtype = a.dtype; f.status = a.status;
   f.E = a.E; f.k = a.k; f.S = a.S; f.ids = a.ids; f.wts = a.w; f.b1 = a.b1;
   f.y = reinterpret_cast<uint16_t*>(a.ws + w.y); f.ldy = w.ldy;
-  f.zrow = reinterpret_cast<float*>(a.ws + w.z); f.ldz32 = w.ldz;
-  f.part = reinterpret_cast<float*>(a.ws + w.part);
   f.ticket = reinterpret_cast<int32_t*>(a.ws);
   f.done = f.ticket + 1;
-  f.split = f.ticket + 16;
-  f.split2 = f.split + kFewShares;
+  f.joined = f.ticket + 16;
+  f.part = reinterpret_cast<float*>(a.ws + w.part);
   f.out = a.out; f.ldo = a.ldo;
   return launch_few_layer(f, a.x, a.ldx, a.w1, a.g1, a.ld1, a.w2, a.g2, a.ld2, st);
 }
