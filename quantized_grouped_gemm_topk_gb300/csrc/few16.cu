@@ -69,22 +69,22 @@ __device__ __forceinline__ void tmem_ld1(uint32_t taddr, uint32_t& v) {
 }
 // A stage of weights: features f0 .. of group e (both halves of a gated tile), n
 // times 64 of the reduction. Where the reduction is a whole number of those the map
-// has an axis of them and one copy brings the stage (a copy costs its thread some
-// hundred cycles); else there is one for each 64.
+// has an axis of them and a copy brings two (a copy costs its thread some hundred
+// cycles); else there is one for each 64.
 __device__ __forceinline__ void copy_weights(uint32_t dst, int half_bytes, const CUtensorMap* map, bool chunks, int k, int n,
                                              int f0, int e, uint32_t bar, uint64_t policy) {
-  for (int h = 0; h < (chunks ? 1 : n); ++h)
+  for (int h = 0; h < n; h += chunks ? 2 : 1)
     asm volatile(
         "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint"
         " [%0], [%1, {%2, %3, %4, %5, %6}], [%7], %8;" ::"r"(dst + h * half_bytes),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(chunks ? 0 : k + h * kFH), "r"(f0), "r"(0), "r"(chunks ? k / kFH : 0), "r"(e),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(chunks ? 0 : k + h * kFH), "r"(f0), "r"(0), "r"(chunks ? k / kFH + h : 0), "r"(e),
         "r"(bar), "l"(policy)
         : "memory");
 }
 __device__ __forceinline__ void copy_rows(uint32_t dst, int half_bytes, const CUtensorMap* map, bool chunks, int k, int n, int r0,
                                           uint32_t bar) {
-  for (int h = 0; h < (chunks ? 1 : n); ++h)
-    tc::tma_load_3d_at(dst + h * half_bytes, map, chunks ? 0 : k + h * kFH, r0, chunks ? k / kFH : 0, bar);
+  for (int h = 0; h < n; h += chunks ? 2 : 1)
+    tc::tma_load_3d_at(dst + h * half_bytes, map, chunks ? 0 : k + h * kFH, r0, chunks ? k / kFH + h : 0, bar);
 }
 // Waits (bounded, whatever the abort flag says) for the copies that a thread still
 // has in flight. A slot's barrier completes only when the other copying warp
@@ -127,9 +127,10 @@ __device__ __forceinline__ int box_of(int n) { return n <= 8 ? 0 : n <= 16 ? 1 :
 
 // ---- the routed layer ---------------------------------------------------------------
 // A tile: `len` features from f0 of group e, copied in boxes of `box` (gated: of
-// each half). rows: of the operand B that are copied; N: the MMA's.
+// each half): arows rows of the MMA's operand A. rows: of B that are copied; N: the
+// MMA's. hs: 64s of the reduction a stage, an even number.
 struct FewTile {
-  int e, f0, len, box, rows, N;
+  int e, f0, len, box, arows, rows, N, hs;
 };
 // Runs through the tiles of a range. First product: features at .. end of all
 // groups' one after the other, up to 64 (gated) or 128 a tile. Second: features of
@@ -184,10 +185,8 @@ __global__ void __launch_bounds__(kFThreads, 1) k_few_layer(const FewArgs g, con
     for (int i = 0; i < kFIssuers; ++i) tc::mbar_init(&drain[i], 1);
     *abort = 0;
     tc::fence_mbar_init();
-    tc::prefetch_tmap(&maps.a[7]);
-    tc::prefetch_tmap(&maps.x);
-    tc::prefetch_tmap(&maps.a2);
   }
+  if (warp == 3 && lane < (int)(sizeof(FewMaps) / sizeof(CUtensorMap))) tc::prefetch_tmap(&maps.a[0] + lane);
   const uint32_t ncol = g.N <= 16 ? 16 : g.N <= 32 ? 32 : 64;      // of an accumulator; four a tile, two tiles
   if (warp == 1) tc::tmem_alloc(tmem_slot, 8 * ncol);
   for (int i = tid; i < G; i += kFThreads) mask[i] = i >= g.E ? (g.R == 64 ? ~0ull : (1ull << g.R) - 1) : 0ull;
@@ -286,6 +285,7 @@ __global__ void __launch_bounds__(kFThreads, 1) k_few_layer(const FewArgs g, con
       t.len = left >= 2 * g.rows1 ? g.rows1 : left > g.rows1 ? (left / 2 + step - 1) / step * step : left;
       t.box = (t.len + step - 1) / step * step;
       r.at += t.len;
+      t.arows = gated ? 2 * t.box : t.box;
       t.rows = g.xrows;
       t.N = g.N;
     } else {
@@ -293,7 +293,7 @@ __global__ void __launch_bounds__(kFThreads, 1) k_few_layer(const FewArgs g, con
       t.e = glist[r.g];
       t.f0 = (int)r.at;
       t.len = (int)min((int64_t)g.box2, r.end - r.at);
-      t.box = g.box2;
+      t.box = t.arows = g.box2;
       if (++r.g == r.g1) {
         r.g = r.g0;
         r.at += t.len;
@@ -302,6 +302,7 @@ __global__ void __launch_bounds__(kFThreads, 1) k_few_layer(const FewArgs g, con
       t.rows = 8 << box_of(m);
       t.N = (m + 15) & ~15;
     }
+    t.hs = g.slot / (256 * (t.arows + t.rows)) * 2;
     return true;
   };
 
@@ -319,16 +320,16 @@ __global__ void __launch_bounds__(kFThreads, 1) k_few_layer(const FewArgs g, con
         tc::mbar_arrive(&qfull[n % kFQueue]);
         if (s < 0) break;
         const bool second = s >= P1;
-        const int K = second ? g.K2 : g.K1, hs = second ? g.hs2 : 2, nh = (K + kFH - 1) / kFH;
+        const int K = second ? g.K2 : g.K1, nh = (K + kFH - 1) / kFH;
         const bool chunks = K % kFH == 0;
         FewRange r = range_of(s);
         FewTile t;
         while (ok && next_tile(second, r, t)) {
-          const int half = t.box * 128 * (!second && gated ? 2 : 1);
+          const int half = t.arows * 128, hs = t.hs;
           const CUtensorMap* map = second ? &maps.a2 : &maps.a[t.box / (g.rows1 / 8) - 1];
           for (int h = 0; h < nh; h += hs) {
             if (!tc::bar_wait(empty_u + 8 * slot, phase, abort)) { ok = false; break; }
-            const int n_h = chunks ? hs : min(hs, nh - h);
+            const int left = min(hs, nh - h), n_h = chunks ? (left + 1) & ~1 : left;
             tc::bar_arrive_expect_tx(full_u + 8 * slot, n_h * half);
             copy_weights(ring_u + slot * g.slot, half, map, chunks, h * kFH, n_h, t.f0, t.e, full_u + 8 * slot, policy);
             ++issued;
@@ -365,18 +366,18 @@ __global__ void __launch_bounds__(kFThreads, 1) k_few_layer(const FewArgs g, con
           fence_proxy_async_global();
           ready = true;
         }
-        const int K = second ? g.K2 : g.K1, hs = second ? g.hs2 : 2, nh = (K + kFH - 1) / kFH;
+        const int K = second ? g.K2 : g.K1, nh = (K + kFH - 1) / kFH;
         const bool chunks = K % kFH == 0;
         FewRange r = range_of(s);
         FewTile t;
         while (ok && next_tile(second, r, t)) {
           // behind the stage's weights
-          const int a_bytes = hs * t.box * 128 * (!second && gated ? 2 : 1), half = t.rows * 128;
+          const int hs = t.hs, a_bytes = hs * t.arows * 128, half = t.rows * 128;
           const CUtensorMap* map = second ? &maps.y[box_of(t.rows)] : &maps.x;
           const int r0 = second ? rowof[t.e] : 0;
           for (int h = 0; h < nh; h += hs) {
             if (!tc::bar_wait(empty_u + 8 * slot, phase, abort)) { ok = false; break; }
-            const int n_h = chunks ? hs : min(hs, nh - h);
+            const int left = min(hs, nh - h), n_h = chunks ? (left + 1) & ~1 : left;
             tc::bar_arrive_expect_tx(full_u + 8 * slot, n_h * half);
             copy_rows(ring_u + slot * g.slot + a_bytes, half, map, chunks, h * kFH, n_h, r0, full_u + 8 * slot);
             ++issued;
@@ -403,14 +404,14 @@ __global__ void __launch_bounds__(kFThreads, 1) k_few_layer(const FewArgs g, con
         const int s = take(n);
         if (s < 0) break;
         const bool second = s >= P1;
-        const int K = second ? g.K2 : g.K1, hs = second ? g.hs2 : 2, nh = (K + kFH - 1) / kFH;
+        const int nh = ((second ? g.K2 : g.K1) + kFH - 1) / kFH;
         FewRange r = range_of(s);
         FewTile t;
         while (ok && next_tile(second, r, t)) {
           const int d = tiles & 1;
           if (!tc::mbar_wait(&accempty[d], ((tiles >> 1) & 1) ^ 1, abort)) { ok = false; break; }
           tc::fence_after_sync();
-          const int rows = t.box * (!second && gated ? 2 : 1);
+          const int rows = t.arows, hs = t.hs;
           const uint32_t idesc = tc::idesc_16bit(rows <= 64 ? 64 : kFM, t.N, g.dtype == MOE_DT_BF16, 0, 0), dt = tmem + (4 * d + step) * ncol;
           for (int h = 0; h < nh; h += hs) {
             if (!tc::bar_wait(full_u + 8 * slot, phase, abort)) { ok = false; break; }
@@ -474,8 +475,7 @@ __global__ void __launch_bounds__(kFThreads, 1) k_few_layer(const FewArgs g, con
         unsigned long long rem = mask[t.e];
         const int m = __popcll(rem);
         // the thread's row of the tile: an MMA of 64 rows leaves sixteen to each warp's lanes
-        const int arows = t.box * (!second && gated ? 2 : 1);
-        const int row = arows > 64 ? et : lane < 16 ? q * 16 + lane : kFM;
+        const int row = t.arows > 64 ? et : lane < 16 ? q * 16 + lane : kFM;
         if (!second) {
           const int r0 = rowof[t.e];
           for (int i0 = 0; i0 < m; i0 += kFCols) {
@@ -829,18 +829,20 @@ cudaError_t launch_few_layer(FewArgs g, const void* x, int64_t ldx, const void* 
   }
   int box_t = 8;                                    // rows of the second product's widest copy
   while (box_t < g.R) box_t *= 2;
-  g.slot = 2 * 128 * (kFM + g.xrows);
-  g.hs2 = std::max(1, g.slot / (128 * (g.box2 + box_t)));
+  g.slot = 2 * 128 * std::max(kFM + g.xrows, g.box2 + box_t);
   const int head = kFBars + kFCols * kFM * 4 + 4 * (g.R * g.box2 + 2) + 12 * G + 4 * std::min(G, A + g.S) + 4 * (A + g.S * g.R) + 8 * A;
   g.head = (head + 1023) / 1024 * 1024;
-  g.stages = std::min(kFMaxStages, (kFSmem - 1024 - g.head - kFA) / g.slot);
-  const int smem = 1024 + g.head + g.stages * g.slot + kFA;       // behind the ring 16 KB that MMAs may read
+  // An MMA of 64 or 128 rows reads past the rows that were copied, of A and of B (16
+  // where 8 were): within the stage but for its last halves, where the tile is narrow.
+  const int pad = 128 * 64;
+  g.stages = std::min(kFMaxStages, (kFSmem - 1024 - g.head - pad) / g.slot);
+  const int smem = 1024 + g.head + g.stages * g.slot + pad;
   FewMaps maps;
   for (int i = 0; i < 8; ++i)
     if (!map_weights(&maps.a[i], w1, g.K1, g.F1, halves, ld1, G, g1, g.rows1 / 8 * (i + 1), 2)) return cudaErrorInvalidValue;
   for (int i = 0; i < 4; ++i)
-    if (!map_rows(&maps.y[i], g.y, g.K2, (int64_t)g.R * (g.k + g.S), g.ldy, 8 << i, g.hs2)) return cudaErrorInvalidValue;
-  if (!map_weights(&maps.a2, w2, g.K2, g.F2, 1, ld2, G, g2, g.box2, g.hs2) || !map_rows(&maps.x, x, g.K1, g.R, ldx, g.xrows, 2))
+    if (!map_rows(&maps.y[i], g.y, g.K2, (int64_t)g.R * (g.k + g.S), g.ldy, 8 << i, 2)) return cudaErrorInvalidValue;
+  if (!map_weights(&maps.a2, w2, g.K2, g.F2, 1, ld2, G, g2, g.box2, 2) || !map_rows(&maps.x, x, g.K1, g.R, ldx, g.xrows, 2))
     return cudaErrorInvalidValue;
   const auto kernel = g.dtype == MOE_DT_BF16 ? k_few_layer<Bf16> : k_few_layer<F16>;
   static std::atomic<bool> done[2][kMaxDevices] = {};

@@ -34,8 +34,7 @@ struct FewArgs {
   int head, stages;           // bytes in front of the ring, its stages
   int nt, mt1, nk1;           // dense: tiles of rows and of features, stages of the reduction
   int Pf, S2;                 // layer: ranges of the second product's features, parts of the groups for each
-  int xrows, box2, hs2, slot; // layer: rows of x a copy takes, features of the second product's tiles, its 64s of the
-                              // reduction a stage, bytes of a stage
+  int xrows, box2, slot;      // layer: rows of x a copy takes, features of the second product's tiles, bytes of a stage
 };
 cudaError_t launch_few_layer(FewArgs g, const void* x, int64_t ldx, const void* w1, int64_t g1, int64_t ld1, const void* w2,
                              int64_t g2, int64_t ld2, cudaStream_t st);
