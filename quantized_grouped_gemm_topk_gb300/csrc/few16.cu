@@ -27,11 +27,11 @@
 //   of the second's: a CTA that waits only waits for ranges that running CTAs
 //   hold, however many of the grid are resident.
 //
-// Roles: warp 0 claims and copies weights, warp 2 copies rows, warp 1 (in the layer
-// also 3, 8 and 9) issues the MMAs, warps 4 and up are the epilogue (two
-// accumulators, so that it overlaps the next tile's MMAs). An MMA costs the thread
-// that issues it 65 cycles, however few its rows: with one issuer a half stage
-// of 24 rows took 350 cycles, of which its copies need 130. So each of four
+// Roles: warp 0 claims and copies weights, warp 2 copies rows, warps 1 and 3 and the
+// last two issue the MMAs, those between are the epilogue (two accumulators, so
+// that it overlaps the next tile's MMAs). An MMA takes its issuer
+// 52 cycles and more, however few its rows: with one issuer a half stage of 24 rows
+// took 350 cycles, of which its copies need 130. So each of four
 // issues one step (K = 16) in four, into an accumulator of its own, and the
 // epilogue adds the four. Every wait is bounded; a CTA whose wait runs out sets
 // MOE_DEV_TIMEOUT, waits for its copies and MMAs in flight, frees tensor memory and
@@ -45,9 +45,7 @@ namespace moe {
 
 constexpr int kFM = 128;              // most features a tile (MMA M)
 constexpr int kFH = 64;               // reduction of a half stage: one 128-byte swizzle row
-constexpr int kFK = 2 * kFH;
 constexpr int kFThreads = 320;
-constexpr int kFA = kFM * kFH * 2;    // bytes of 128 rows' half
 constexpr int kFMaxStages = 8;
 constexpr int kFBars = 512;           // barriers and scratch, in front of the tables
 constexpr int kFSmem = 227 * 1024;
@@ -86,6 +84,11 @@ __device__ __forceinline__ void copy_rows(uint32_t dst, int half_bytes, const CU
   for (int h = 0; h < n; h += chunks ? 2 : 1)
     tc::tma_load_3d_at(dst + h * half_bytes, map, chunks ? 0 : k + h * kFH, r0, chunks ? k / kFH + h : 0, bar);
 }
+// Where the way along the reduction, of ns stages, begins for range (tile) s: not at
+// the same columns for all, whose rows lie a fixed distance apart (64 tokens, 2880 x
+// 2880 x 128 experts 804 -> 789 us). Not by CTA: which one takes a range varies, and
+// sums must not.
+__device__ __forceinline__ int first_stage(int s, int ns) { return (int)((uint32_t)s * 5u % (uint32_t)ns); }
 // Waits (bounded, whatever the abort flag says) for the copies that a thread still
 // has in flight. A slot's barrier completes only when the other copying warp
 // arrived too; where that one stopped earlier the limit ends the wait.
@@ -115,6 +118,27 @@ __device__ __forceinline__ bool epi_all(bool ok) {
       : "memory");
   return r != 0;
 }
+
+// An MMA (and a commit, see tc::bar_commit) by one thread of a warp that runs as a
+// whole: the compiler then keeps addresses and descriptors in uniform registers, where
+// the instruction wants them (a thread of its own takes 67 cycles to issue one, this 52,
+// and its loop's own work on top of that).
+__device__ __forceinline__ void mma_one(uint32_t d, uint32_t a, uint32_t b, uint32_t hi, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n .reg .pred p, q;\n .reg .b64 a, b;\n elect.sync _|q, 0xffffffff;\n setp.ne.b32 p, %5, 0;\n"
+      " mov.b64 a, {%1, %3};\n mov.b64 b, {%2, %3};\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, p;\n}" ::"r"(d),
+      "r"(a), "r"(b), "r"(hi), "r"(idesc), "r"(acc)
+      : "memory");
+}
+__device__ __forceinline__ void commit_one(uint32_t bar) {
+  asm volatile(
+      "{\n .reg .pred q;\n elect.sync _|q, 0xffffffff;\n"
+      " @q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}" ::"r"(bar)
+      : "memory");
+}
+// A value that all lanes hold, in a uniform register.
+__device__ __forceinline__ uint32_t uni(uint32_t v) { return __shfl_sync(kFull, v, 0); }
 
 // Position of the lowest set bit, which is cleared.
 __device__ __forceinline__ int next_bit(unsigned long long& m) {
@@ -327,7 +351,8 @@ __global__ void __launch_bounds__(kFThreads, 1) k_few_layer(const FewArgs g, con
         while (ok && next_tile(second, r, t)) {
           const int half = t.arows * 128, hs = t.hs;
           const CUtensorMap* map = second ? &maps.a2 : &maps.a[t.box / (g.rows1 / 8) - 1];
-          for (int h = 0; h < nh; h += hs) {
+          const int ns = (nh + hs - 1) / hs;
+          for (int i = 0, h = first_stage(s, ns) * hs; i < ns; ++i, h = h + hs < nh ? h + hs : 0) {
             if (!tc::bar_wait(empty_u + 8 * slot, phase, abort)) { ok = false; break; }
             const int left = min(hs, nh - h), n_h = chunks ? (left + 1) & ~1 : left;
             tc::bar_arrive_expect_tx(full_u + 8 * slot, n_h * half);
@@ -375,7 +400,8 @@ __global__ void __launch_bounds__(kFThreads, 1) k_few_layer(const FewArgs g, con
           const int hs = t.hs, a_bytes = hs * t.arows * 128, half = t.rows * 128;
           const CUtensorMap* map = second ? &maps.y[box_of(t.rows)] : &maps.x;
           const int r0 = second ? rowof[t.e] : 0;
-          for (int h = 0; h < nh; h += hs) {
+          const int ns = (nh + hs - 1) / hs;
+          for (int i = 0, h = first_stage(s, ns) * hs; i < ns; ++i, h = h + hs < nh ? h + hs : 0) {
             if (!tc::bar_wait(empty_u + 8 * slot, phase, abort)) { ok = false; break; }
             const int left = min(hs, nh - h), n_h = chunks ? (left + 1) & ~1 : left;
             tc::bar_arrive_expect_tx(full_u + 8 * slot, n_h * half);
@@ -393,50 +419,58 @@ __global__ void __launch_bounds__(kFThreads, 1) k_few_layer(const FewArgs g, con
     }
   } else if (warp < 4 || warp >= 8) {
     // ---------------- MMAs ----------------
-    if (lane == 0) {
-      const int step = warp == 1 ? 0 : warp == 3 ? 1 : warp - 6;       // of every 64 of the reduction
-      const uint64_t d0 = tc::smem_desc_sw128(ring_u);
-      const uint32_t lo = (uint32_t)d0 + 2 * step, hi = (uint32_t)(d0 >> 32);
-      int slot = 0;
-      uint32_t phase = 0, tiles = 0;
-      bool ok = true;
-      for (uint32_t n = 0; ok; ++n) {
-        const int s = take(n);
-        if (s < 0) break;
-        const bool second = s >= P1;
-        const int nh = ((second ? g.K2 : g.K1) + kFH - 1) / kFH;
-        FewRange r = range_of(s);
-        FewTile t;
-        while (ok && next_tile(second, r, t)) {
-          const int d = tiles & 1;
-          if (!tc::mbar_wait(&accempty[d], ((tiles >> 1) & 1) ^ 1, abort)) { ok = false; break; }
+    const uint32_t wi = uni(warp), step = wi == 1 ? 0 : wi == 3 ? 1 : wi - 6;       // of every 64 of the reduction
+    const uint64_t d0 = tc::smem_desc_sw128(ring_u);
+    const uint32_t lo = uni((uint32_t)d0 + 2 * step), hi = uni((uint32_t)(d0 >> 32));
+    const uint32_t tm = uni(tmem) + step * ncol, bars = uni(full_u), accs = uni(tc::smem_u32(accfull));
+    const uint32_t slot_step = (uint32_t)g.slot / 16;
+    uint32_t slot = 0, at = lo, phase = 0, tiles = 0;
+    bool ok = true;
+    for (uint32_t n = 0; ok; ++n) {
+      const int s = (int)uni((uint32_t)take(n));      // one lane's answer, should a wait run out
+      if (s < 0) break;
+      const bool second = s >= P1;
+      const int nh = ((second ? g.K2 : g.K1) + kFH - 1) / kFH;
+      FewRange r = range_of(s);
+      FewTile t;
+      while (ok && next_tile(second, r, t)) {
+        const uint32_t d = tiles & 1;
+        if (!__all_sync(kFull, tc::mbar_wait(&accempty[d], ((tiles >> 1) & 1) ^ 1, abort))) { ok = false; break; }
+        tc::fence_after_sync();
+        const uint32_t a_step = uni(t.arows * 8), b_step = uni(t.rows * 8), hs = uni(t.hs), wide = uni(t.N);
+        const uint32_t idesc = tc::idesc_16bit(a_step <= 64 * 8 ? 64 : kFM, wide, g.dtype == MOE_DT_BF16, 0, 0), dt = tm + d * 4 * ncol;
+        const uint32_t b_off = hs * a_step, ns = ((uint32_t)nh + hs - 1) / hs;
+        uint32_t acc = 0;
+        for (uint32_t i = 0, h = uni(first_stage(s, ns)) * hs; i < ns; ++i) {
+          if (!__all_sync(kFull, tc::bar_wait(bars + 8 * slot, phase, abort))) { ok = false; break; }
           tc::fence_after_sync();
-          const int rows = t.arows, hs = t.hs;
-          const uint32_t idesc = tc::idesc_16bit(rows <= 64 ? 64 : kFM, t.N, g.dtype == MOE_DT_BF16, 0, 0), dt = tmem + (4 * d + step) * ncol;
-          for (int h = 0; h < nh; h += hs) {
-            if (!tc::bar_wait(full_u + 8 * slot, phase, abort)) { ok = false; break; }
-            tc::fence_after_sync();
-            const uint32_t a0 = lo + slot * (g.slot / 16), b0 = a0 + hs * rows * 8;
-            const int n_h = min(hs, nh - h);
-            for (int i = 0; i < n_h; ++i)
-              tc::mma_f16_ss(dt, ((uint64_t)hi << 32) | (a0 + i * rows * 8), ((uint64_t)hi << 32) | (b0 + i * t.rows * 8), idesc, h + i > 0);
-            tc::bar_commit(empty_u + 8 * slot);
-            if (++slot == g.stages) {
-              slot = 0;
-              phase ^= 1;
-            }
+          const uint32_t n_h = min(hs, (uint32_t)nh - h);
+          uint32_t a = at, b = at + b_off;
+#pragma unroll 2
+          for (uint32_t c = 0; c < n_h; ++c, a += a_step, b += b_step) {
+            mma_one(dt, a, b, hi, idesc, acc);
+            acc = 1;
           }
-          if (!ok) break;
-          tc::mma_commit(&accfull[d]);
-          ++tiles;
+          commit_one(bars + 8 * (kFMaxStages + slot));      // its `empty`
+          h = h + hs < (uint32_t)nh ? h + hs : 0;
+          at += slot_step;
+          if (++slot == (uint32_t)g.stages) {
+            slot = 0;
+            at = lo;
+            phase ^= 1;
+          }
         }
-        tc::mbar_arrive(&qempty[n % kFQueue]);
+        if (!ok) break;
+        commit_one(accs + 8 * d);
+        ++tiles;
       }
-      // every MMA of this thread has completed once `drain` fires
-      tc::mma_commit(&drain[step]);
-      volatile int never = 0;
-      tc::mbar_wait(&drain[step], 0, &never, 400000000ll);
+      if (lane == 0) tc::mbar_arrive(&qempty[n % kFQueue]);
     }
+    // every MMA of this warp has completed once its `drain` fires
+    __syncwarp();
+    commit_one(uni(tc::smem_u32(&drain[step])));
+    volatile int never = 0;
+    tc::mbar_wait(&drain[step], 0, &never, 400000000ll);
     __syncwarp();
   } else {
     // ---------------- epilogue ----------------
@@ -577,82 +611,82 @@ __global__ void __launch_bounds__(kFThreads, 1) k_few_layer(const FewArgs g, con
 }
 
 // ---- one dense product ------------------------------------------------------------
-// Tiles of f features (a multiple of 8, gated: of each half) x N rows over the
-// whole reduction, sized so that their rounds over the SMs come out even: with
-// weights on the M side a tile of 48 features costs 48 rows of copies, and what
-// the MMA computes for the other lanes is not read. (Cutting fixed tiles along
+// Tiles of an equal range of features x N rows over the whole reduction, in even
+// rounds over the SMs. A tile copies its features rounded up to 8 (a few rows of its
+// neighbour, which the L2 serves); with weights on the M side one of 48 features
+// costs 48 rows of copies, and what the MMA computes for the other lanes is not read. (Cutting fixed tiles along
 // the reduction instead costs the partial sums' way through memory: 1 x 7168 x
 // 2048 13.9 us, 64 rows 86 us.)
-constexpr int kLStages = 32;
-constexpr int kLThreads = 384;
-constexpr int kLChunk = 16;           // columns the epilogue takes at a time
-constexpr int kLHead = 1024;          // barriers
-constexpr int kLBias = 2 * kLChunk * kFM;     // gated: where a tile's biases lie in the epilogue's memory, two tiles'
+constexpr int kDStages = 16;
+constexpr int kDThreads = 448;
+constexpr int kDCols = 16;            // columns an epilogue group takes at a time
+constexpr int kDHead = 1024;          // barriers
+constexpr int kDBias = 2 * kDCols * kFM;      // where a tile's biases lie in the epilogue's memory, two tiles'
+constexpr int kDPad = 128 * 64;       // behind the ring, see launch_few_layer
 
 template <typename E, bool GATED>
-__global__ void __launch_bounds__(kLThreads, 1) k_few_linear(const FewArgs g, const __grid_constant__ FewMaps maps) {
+__global__ void __launch_bounds__(kDThreads, 1) k_few_linear(const FewArgs g, const __grid_constant__ FewMaps maps) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* base = reinterpret_cast<uint8_t*>(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
   uint64_t* full = reinterpret_cast<uint64_t*>(base);
-  uint64_t* empty = full + kLStages;
-  uint64_t* accfull = empty + kLStages;
+  uint64_t* empty = full + kDStages;
+  uint64_t* accfull = empty + kDStages;
   uint64_t* accempty = accfull + 2;
   uint64_t* drain = accempty + 2;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + kFIssuers);
   volatile int* abort = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  float* stage = reinterpret_cast<float*>(base + kLHead);           // gated: [2][kLChunk][128], biases [2][128]
-  const int a_half = (GATED ? 2 : 1) * g.rows1 * 128, b_half = g.N * 128;
-  uint8_t* sb = base + g.head;
-  uint8_t* sa = sb + g.stages * 2 * b_half;                         // behind it 16 KB that MMAs may read
+  float* stage = reinterpret_cast<float*>(base + kDHead);           // [2][kDCols][128], biases [2][128]
+  const int arows = (GATED ? 2 : 1) * g.rows1, a_half = arows * 128, b_half = g.N * 128;
+  uint8_t* ring = base + g.head;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < g.stages; ++i) {
       tc::mbar_init(&full[i], 2);
-      tc::mbar_init(&empty[i], 1);
+      tc::mbar_init(&empty[i], g.issuers);
     }
     for (int i = 0; i < 2; ++i) {
-      tc::mbar_init(&accfull[i], 1);
+      tc::mbar_init(&accfull[i], g.issuers);
       tc::mbar_init(&accempty[i], 8);
     }
-    tc::mbar_init(drain, 1);
+    for (int i = 0; i < kFIssuers; ++i) tc::mbar_init(&drain[i], 1);
     *abort = 0;
     tc::fence_mbar_init();
     tc::prefetch_tmap(&maps.a[0]);
     tc::prefetch_tmap(&maps.x);
   }
-  const uint32_t ncol = g.N <= 32 ? 32 : g.N <= 64 ? 64 : g.N <= 128 ? 128 : 256;
-  if (warp == 1) tc::tmem_alloc(tmem_slot, 2 * ncol);
+  const uint32_t ncol = g.N <= 16 ? 16 : g.N <= 32 ? 32 : g.N <= 64 ? 64 : g.N <= 128 ? 128 : 256;
+  const uint32_t cols = 2 * g.issuers * ncol < 32 ? 32 : 2 * g.issuers * ncol;
+  if (warp == 1) tc::tmem_alloc(tmem_slot, cols);
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
   pdl_enter();
   const uint32_t tmem = *tmem_slot;
-  const uint32_t full_u = tc::smem_u32(full), empty_u = tc::smem_u32(empty);
-  const uint32_t sa_u = tc::smem_u32(sa), sb_u = tc::smem_u32(sb);
-  const int tiles = g.mt1 * g.nt;
-  const bool chunks = g.K1 % kFH == 0;
+  const uint32_t full_u = tc::smem_u32(full), empty_u = tc::smem_u32(empty), ring_u = tc::smem_u32(ring);
+  const int tiles = g.mt1 * g.nt, hs = g.hs, nh = (g.K1 + kFH - 1) / kFH, ns = (nh + hs - 1) / hs;
 
   if (warp == 0 || warp == 2) {
     // ---------------- copies: warp 0 weights, warp 2 rows ----------------
     if (lane == 0) {
       // weights that several row tiles read are worth keeping
       const uint64_t policy = g.nt > 1 ? tc::policy_evict_last() : tc::policy_evict_first();
+      const bool chunks = g.K1 % kFH == 0;
       int slot = 0;
       uint32_t phase = 1, issued = 0;
       bool ok = true;
       for (int t = blockIdx.x; ok && t < tiles; t += gridDim.x) {
-        const int f0 = t / g.nt * g.rows1, r0 = t % g.nt * g.N;
-        for (int kb = 0; kb < g.nk1; ++kb) {
+        const int f0 = (int)((int64_t)g.F1 * (t / g.nt) / g.mt1), r0 = t % g.nt * g.N;
+        for (int i = 0, h = first_stage(t, ns) * hs; i < ns; ++i, h = h + hs < nh ? h + hs : 0) {
           if (!tc::bar_wait(empty_u + 8 * slot, phase, abort)) { ok = false; break; }
-          const int k = kb * kFK, n = chunks || g.K1 - k > kFH ? 2 : 1;
-          const uint32_t bar = full_u + 8 * slot;
+          const int left = min(hs, nh - h), n = chunks ? (left + 1) & ~1 : left;
+          const uint32_t bar = full_u + 8 * slot, dst = ring_u + slot * g.slot;
           if (warp == 0) {
             tc::bar_arrive_expect_tx(bar, n * a_half);
-            copy_weights(sa_u + 2 * slot * a_half, a_half, &maps.a[0], chunks, k, n, f0, 0, bar, policy);
+            copy_weights(dst, a_half, &maps.a[0], chunks, h * kFH, n, f0, 0, bar, policy);
           } else {
             tc::bar_arrive_expect_tx(bar, n * b_half);
-            copy_rows(sb_u + 2 * slot * b_half, b_half, &maps.x, chunks, k, n, r0, bar);
+            copy_rows(dst + hs * a_half, b_half, &maps.x, chunks, h * kFH, n, r0, bar);
           }
           ++issued;
           if (++slot == g.stages) {
@@ -663,48 +697,66 @@ __global__ void __launch_bounds__(kLThreads, 1) k_few_linear(const FewArgs g, co
       }
       if (!ok || *abort) wind_down(full, issued, g.stages);
     }
-  } else if (warp == 1) {
+  } else if (warp < 4 || warp >= 12) {
     // ---------------- MMAs ----------------
-    if (lane == 0) {
-      const uint64_t ad0 = tc::smem_desc_sw128(sa_u), bd0 = tc::smem_desc_sw128(sb_u);
-      const uint32_t hi = (uint32_t)(ad0 >> 32), a_step = a_half / 16, b_step = b_half / 16;
-      const uint32_t idesc = tc::idesc_16bit(kFM, g.N, g.dtype == MOE_DT_BF16, 0, 0);
-      int slot = 0;
-      uint32_t phase = 0, done = 0;
+    const uint32_t wi = uni(warp), who = wi < 4 ? wi >> 1 : wi - 10, many = (uint32_t)g.issuers;
+    if (who < many) {
+      const uint64_t d0 = tc::smem_desc_sw128(ring_u);
+      const uint32_t lo = uni((uint32_t)d0 + 2 * who), hi = uni((uint32_t)(d0 >> 32));
+      const uint32_t tm = uni(tmem) + who * ncol, bars = uni(full_u), accs = uni(tc::smem_u32(accfull));
+      const uint32_t idesc = tc::idesc_16bit(arows <= 64 ? 64 : kFM, g.N, g.dtype == MOE_DT_BF16, 0, 0);
+      const uint32_t a_step = arows * 8, b_step = g.N * 8, b_off = hs * a_step, slot_step = (uint32_t)g.slot / 16;
+      uint32_t slot = 0, at = lo, phase = 0, done = 0;
       bool ok = true;
       for (int t = blockIdx.x; ok && t < tiles; t += gridDim.x, ++done) {
-        const int d = done & 1;
-        if (!tc::mbar_wait(&accempty[d], ((done >> 1) & 1) ^ 1, abort)) break;
+        const uint32_t d = done & 1;
+        if (!__all_sync(kFull, tc::mbar_wait(&accempty[d], ((done >> 1) & 1) ^ 1, abort))) break;
         tc::fence_after_sync();
-        const uint32_t dt = tmem + d * ncol;
-        for (int kb = 0; kb < g.nk1; ++kb) {
-          if (!tc::bar_wait(full_u + 8 * slot, phase, abort)) { ok = false; break; }
+        const uint32_t dt = tm + d * many * ncol;
+        uint32_t acc = 0;
+        for (int i = 0, h = first_stage(t, ns) * hs; i < ns; ++i) {
+          if (!__all_sync(kFull, tc::bar_wait(bars + 8 * slot, phase, abort))) { ok = false; break; }
           tc::fence_after_sync();
-          const uint32_t a0 = (uint32_t)ad0 + 2 * slot * a_step, b0 = (uint32_t)bd0 + 2 * slot * b_step;
-          tc::mma_f16_x4<1>(dt, a0, hi, 2, b0, hi, 2, idesc, kb > 0);
-          if (g.K1 - kb * kFK > kFH) tc::mma_f16_x4<1>(dt, a0 + a_step, hi, 2, b0 + b_step, hi, 2, idesc, 1u);
-          tc::bar_commit(empty_u + 8 * slot);
-          if (++slot == g.stages) {
+          const int n_h = min(hs, nh - h);
+          uint32_t a = at, b = at + b_off;
+          // the steps (K = 16) of every 64: one in four, in two, or all
+          for (int c = 0; c < n_h; ++c, a += a_step, b += b_step) {
+            mma_one(dt, a, b, hi, idesc, acc);
+            acc = 1;
+            if (many == 2) mma_one(dt, a + 4, b + 4, hi, idesc, 1);
+            if (many == 1) {
+              mma_one(dt, a + 2, b + 2, hi, idesc, 1);
+              mma_one(dt, a + 4, b + 4, hi, idesc, 1);
+              mma_one(dt, a + 6, b + 6, hi, idesc, 1);
+            }
+          }
+          commit_one(bars + 8 * (kDStages + slot));         // its `empty`
+          h = h + hs < nh ? h + hs : 0;
+          at += slot_step;
+          if (++slot == (uint32_t)g.stages) {
             slot = 0;
+            at = lo;
             phase ^= 1;
           }
         }
-        if (ok) tc::mma_commit(&accfull[d]);
+        if (ok) commit_one(accs + 8 * d);
       }
-      // every MMA of this thread has completed once `drain` fires
-      tc::mma_commit(drain);
+      // every MMA of this warp has completed once its `drain` fires
+      __syncwarp();
+      commit_one(uni(tc::smem_u32(&drain[who])));
       volatile int never = 0;
-      tc::mbar_wait(drain, 0, &never, 400000000ll);
+      tc::mbar_wait(&drain[who], 0, &never, 400000000ll);
+      __syncwarp();
     }
-    __syncwarp();
-  } else if (warp >= 4) {
+  } else {
     // ---------------- epilogue ----------------
-    // Two groups of four warps share a tile's columns, kLChunk by kLChunk. A
-    // lane holds a feature; the gate and up of a gated tile lie in different
-    // lanes and meet in shared memory.
+    // Two groups of four warps share a tile's columns, kDCols by kDCols. A lane
+    // holds a feature; they go through shared memory, where the gate and up of a
+    // gated tile meet, and from there in rows of features.
     const int grp = (warp - 4) >> 2, q = warp & 3, et = (threadIdx.x - 128) & 127;
     const uint32_t lanes = tmem + ((uint32_t)(q * 32) << 16);
-    float* st = stage + grp * kLChunk * kFM;
+    const int row = arows > 64 ? et : lane < 16 ? q * 16 + lane : kFM;       // the lane's row of the tile
+    float *st = stage + grp * kDCols * kFM, *bs = stage + kDBias;
     const uint16_t* res = reinterpret_cast<const uint16_t*>(g.res);
     uint16_t *z = reinterpret_cast<uint16_t*>(g.z), *out = reinterpret_cast<uint16_t*>(g.out);
     auto bias = [&](int64_t f) {
@@ -713,62 +765,67 @@ __global__ void __launch_bounds__(kLThreads, 1) k_few_linear(const FewArgs g, co
     };
     auto group_sync = [&] {
       __syncwarp();
-      asm volatile("bar.sync %0, 128;" ::"r"(1 + grp) : "memory");
+      if (grp) asm volatile("bar.sync 2, 128;" ::: "memory");
+      else asm volatile("bar.sync 1, 128;" ::: "memory");
     };
     uint32_t done = 0;
     for (int t = blockIdx.x; t < tiles; t += gridDim.x, ++done) {
-      const int d = done & 1, f0 = t / g.nt * g.rows1, r0 = t % g.nt * g.N, nr = min(g.N, g.R - r0);
-      const int nf = min(g.rows1, g.F1 - f0);                       // features of the tile
-      const uint32_t acc = lanes + d * ncol;
-      float b0 = 0.f;
-      if (et < nf) {
-        b0 = bias(f0 + et);
-        if (GATED && grp == 0) {
-          stage[kLBias + d * kFM + et] = b0;
-          stage[kLBias + d * kFM + 64 + et] = bias((int64_t)g.F1 + f0 + et);
-        }
+      const int d = done & 1, j = t / g.nt, r0 = t % g.nt * g.N, nr = min(g.N, g.R - r0);
+      const int f0 = (int)((int64_t)g.F1 * j / g.mt1), nf = (int)((int64_t)g.F1 * (j + 1) / g.mt1) - f0;
+      const uint32_t acc = lanes + d * g.issuers * ncol;
+      if (grp == 0 && et < nf) {
+        bs[d * kFM + et] = bias(f0 + et);
+        if (GATED) bs[d * kFM + 64 + et] = bias((int64_t)g.F1 + f0 + et);
       }
       const bool got = tc::mbar_wait(&accfull[d], (done >> 1) & 1, abort);
       if (!epi_all<3, 256>(got)) break;
       tc::fence_after_sync();
-      for (int c = grp * kLChunk; c < nr; c += 2 * kLChunk) {
-        const int n = min(kLChunk, nr - c);
-        uint32_t v[kLChunk];
+      // thread: feature l of every `step`-th column
+      const int step = 128 / g.lanes, l = et % g.lanes, i0 = et / g.lanes;
+      const int64_t f = f0 + l;
+      const float b0 = bs[d * kFM + l], b1 = GATED ? bs[d * kFM + 64 + l] : 0.f;
+      for (int c = grp * kDCols; c < nr; c += 2 * kDCols) {
+        const int n = min(kDCols, nr - c);
+        uint16_t rv[kDCols];              // the residual, asked for ahead
+#pragma unroll
+        for (int k = 0; k < kDCols; ++k) {
+          const int i = i0 + k * step;
+          rv[k] = res && i < n && l < nf ? res[(r0 + c + i) * g.ldr + f] : (uint16_t)0;
+        }
+        uint32_t v[kDCols];
         tc::tmem_ld16(acc + c, v);
         tc::tmem_wait_ld();
-        if constexpr (!GATED) {
-          if (et < nf) {
-            const int64_t f = f0 + et, r = r0 + c;
-            float rv[kLChunk];
+        for (int w = 1; w < g.issuers; ++w) {
+          uint32_t u[kDCols];
+          tc::tmem_ld16(acc + w * ncol + c, u);
+          tc::tmem_wait_ld();
 #pragma unroll
-            for (int i = 0; i < kLChunk; ++i) rv[i] = res && i < n ? E::to(res[(r + i) * g.ldr + f]) : 0.f;
-#pragma unroll
-            for (int i = 0; i < kLChunk; ++i) {
-              if (i >= n) break;
-              const float a = __uint_as_float(v[i]) + b0;
-              if (z) z[(r + i) * g.ldz + f] = E::from(a);
-              out[(r + i) * g.ldo + f] = E::from(act_one(a, g.act.act) + rv[i]);
-            }
-          }
-        } else {
-#pragma unroll
-          for (int i = 0; i < kLChunk; ++i) st[i * kFM + et] = __uint_as_float(v[i]);
-          group_sync();
-          const float* bs = stage + kLBias + d * kFM;
-          for (int o = et; o < n * 64; o += 128) {
-            const int i = o >> 6, l = o & 63;
-            if (l >= nf) continue;
-            const int64_t f = f0 + l, r = r0 + c + i;
-            const float a = st[i * kFM + l] + bs[l], u = st[i * kFM + g.rows1 + l] + bs[64 + l];
-            if (z) {
-              z[r * g.ldz + f] = E::from(a);
-              z[r * g.ldz + g.F1 + f] = E::from(u);
-            }
-            const float y = act_two(a, u, g.act);
-            out[r * g.ldo + f] = E::from(res ? y + E::to(res[r * g.ldr + f]) : y);
-          }
-          group_sync();
+          for (int i = 0; i < kDCols; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) + __uint_as_float(u[i]));
         }
+        if (row < kFM)
+#pragma unroll
+          for (int i = 0; i < kDCols; ++i) st[i * kFM + row] = __uint_as_float(v[i]);
+        group_sync();
+        if (l < nf) {
+#pragma unroll
+          for (int k = 0; k < kDCols; ++k) {
+            const int i = i0 + k * step;
+            if (i >= n) break;
+            const int64_t r = r0 + c + i;
+            const float p = st[i * kFM + l] + b0;
+            float y;
+            if (z) z[r * g.ldz + f] = E::from(p);
+            if constexpr (GATED) {
+              const float u = st[i * kFM + g.rows1 + l] + b1;
+              if (z) z[r * g.ldz + g.F1 + f] = E::from(u);
+              y = act_two(p, u, g.act);
+            } else {
+              y = act_one(p, g.act.act);
+            }
+            out[r * g.ldo + f] = E::from(res ? y + E::to(rv[k]) : y);
+          }
+        }
+        group_sync();
       }
       tc::fence_before_sync();
       __syncwarp();
@@ -781,7 +838,7 @@ __global__ void __launch_bounds__(kLThreads, 1) k_few_linear(const FewArgs g, co
   if (threadIdx.x == 0 && *abort) set_status(g.status, MOE_DEV_TIMEOUT);
   if (warp == 1) {
     tc::fence_after_sync();
-    tc::tmem_dealloc(tmem, 2 * ncol);
+    tc::tmem_dealloc(tmem, cols);
   }
 }
 
@@ -857,32 +914,42 @@ static cudaError_t launch_linear(FewArgs& g, const FewMaps& maps, int grid, cuda
   static std::atomic<bool> done[kMaxDevices] = {};
   const cudaError_t e = set_smem_once((const void*)k_few_linear<E, GATED>, kFSmem, done);
   if (e != cudaSuccess) return e;
-  const int stage = 2 * 128 * ((GATED ? 2 : 1) * g.rows1 + g.N);
-  g.head = (kLHead + (GATED ? (kLBias + 2 * kFM) * 4 : 0) + 1023) / 1024 * 1024;
-  g.stages = std::min(kLStages, (kFSmem - 1024 - g.head - kFA) / stage);
+  const int half = 128 * ((GATED ? 2 : 1) * g.rows1 + g.N);
+  g.hs = std::max(1, 32768 / (2 * half)) * 2;
+  g.slot = g.hs * half;
+  g.head = (kDHead + (kDBias + 2 * kFM) * 4 + 1023) / 1024 * 1024;
+  g.stages = std::min(kDStages, (kFSmem - 1024 - g.head - kDPad) / g.slot);
+  // as many issuers as tensor memory has room for accumulators; wide MMAs need fewer
+  g.issuers = g.N <= 64 ? 4 : g.N <= 128 ? 2 : 1;
+  g.lanes = g.rows1 <= 16 ? 16 : g.rows1 <= 32 ? 32 : g.rows1 <= 64 ? 64 : 128;
   note_launch();
-  return launch_pdl(k_few_linear<E, GATED>, dim3(grid), dim3(kLThreads), 1024 + g.head + g.stages * stage + kFA, st, g, maps);
+  return launch_pdl(k_few_linear<E, GATED>, dim3(grid), dim3(kDThreads), 1024 + g.head + g.stages * g.slot + kDPad, st, g, maps);
 }
 
 cudaError_t launch_few_linear(FewArgs g, const void* x, int64_t ldx, const void* w, int64_t ldw, cudaStream_t st) {
   const bool gated = act_gated(g.act.act);
   const int halves = gated ? 2 : 1, sms = device_sms();
-  // the tile with the least to copy: rounds over the SMs times its rows of both
+  // the tiles with the least to copy: rounds over the SMs times their rows of both
   // operands, and a fixed cost of a round
   int64_t least = INT64_MAX;
   for (int nt = (int)up(g.R, 256); nt <= up(g.R, 16); ++nt) {
     const int n = (int)(up(up(g.R, nt), 16) * 16);
-    if (up(g.R, n) != nt) continue;
-    for (int f = kFM / halves; f >= 8; f -= 8) {
-      if (f * halves + n > 256) continue;       // three stages at least
-      const int64_t cost = up(up(g.F1, f) * nt, sms) * (f * halves + n + 16);
-      if (cost < least) {
-        least = cost;
-        g.rows1 = f; g.N = n; g.nt = nt;
+    if (up(g.R, n) != nt || n > 240) continue;
+    const int64_t most = up(g.F1, 8);             // ranges
+    for (int64_t rounds = std::max<int64_t>(1, up(up(g.F1, kFM / halves) * nt, sms));; ++rounds) {
+      const int64_t mt = std::min(most, std::max<int64_t>(1, rounds * sms / nt)), box = up(up(g.F1, mt), 8) * 8;
+      // three stages at least
+      if (box * halves <= kFM && box * halves + n <= 256) {
+        const int64_t cost = up(mt * nt, sms) * (box * halves + n + 16);
+        if (cost < least) {
+          least = cost;
+          g.rows1 = (int)box; g.N = n; g.nt = nt; g.mt1 = (int)mt;
+        }
+        if (box * halves + n <= 96) break;        // smaller tiles only add rounds
       }
+      if (mt == most) break;
     }
   }
-  g.mt1 = (int)up(g.F1, g.rows1); g.nk1 = (int)up(g.K1, kFK);
   FewMaps maps = {};
   if (!map_weights(&maps.a[0], w, g.K1, g.F1, halves, ldw, 1, 0, g.rows1, 2) || !map_rows(&maps.x, x, g.K1, g.R, ldx, g.N, 2))
     return cudaErrorInvalidValue;

@@ -32,9 +32,11 @@ struct FewArgs {
   int N;                      // of the MMA; dense: rows a tile
   int rows1;                  // most features a tile
   int head, stages;           // bytes in front of the ring, its stages
-  int nt, mt1, nk1;           // dense: tiles of rows and of features, stages of the reduction
+  int nt, mt1;                // dense: tiles of rows and of features
+  int hs, issuers, lanes;     // dense: 64s of the reduction a stage, warps that issue MMAs, features side by side in the epilogue
   int Pf, S2;                 // layer: ranges of the second product's features, parts of the groups for each
-  int xrows, box2, slot;      // layer: rows of x a copy takes, features of the second product's tiles, bytes of a stage
+  int xrows, box2;            // layer: rows of x a copy takes, features of the second product's tiles
+  int slot;                   // bytes of a stage
 };
 cudaError_t launch_few_layer(FewArgs g, const void* x, int64_t ldx, const void* w1, int64_t g1, int64_t ld1, const void* w2,
                              int64_t g2, int64_t ld2, cudaStream_t st);

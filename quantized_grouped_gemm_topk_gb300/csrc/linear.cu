@@ -49,19 +49,20 @@ __device__ __forceinline__ void lin_tile(const LinArgs& g, int u, int& m, int& n
 // A warp's block of nr x nc <= 32 x 32 elements at p (row stride ld), by way of its
 // staging memory, between rows of the block held by lanes and whole segments of
 // memory; vec: rows start on 16 bytes.
-template <typename E>
-__device__ __forceinline__ void block_in(uint8_t* st, const uint16_t* p, int64_t ld, int nr, int nc, bool vec, int lane, float (&r)[32]) {
-  if (vec && nc >= 32) {
+__device__ __forceinline__ void block_in(uint8_t* st, const uint16_t* p, int64_t ld, int nr, int nc, int lane) {
+  // at any alignment, an element a lane; many rows in flight
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int row = (lane >> 2) + 8 * i, part = lane & 3;
-      if (row < nr) *reinterpret_cast<uint4*>(st + row * kLRow + 16 * part) = *reinterpret_cast<const uint4*>(p + row * ld + 8 * part);
-    }
-  } else {
-#pragma unroll 8
-    for (int row = 0; row < 32; ++row)
-      if (row < nr && lane < nc) *reinterpret_cast<uint16_t*>(st + row * kLRow + 2 * lane) = p[row * ld + lane];
+  for (int r = 0; r < 32; r += 16) {
+    uint16_t v[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v[i] = r + i < nr && lane < nc ? p[(r + i) * ld + lane] : (uint16_t)0;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) *reinterpret_cast<uint16_t*>(st + (r + i) * kLRow + 2 * lane) = v[i];
   }
+}
+// y += the lane's row of the block in staging memory.
+template <typename E>
+__device__ __forceinline__ void add_row(uint8_t* st, int lane, float (&y)[32]) {
   __syncwarp();
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -69,8 +70,8 @@ __device__ __forceinline__ void block_in(uint8_t* st, const uint16_t* p, int64_t
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      r[8 * i + 2 * j] = E::to((uint16_t)(w[j] & 0xffffu));
-      r[8 * i + 2 * j + 1] = E::to((uint16_t)(w[j] >> 16));
+      y[8 * i + 2 * j] += E::to((uint16_t)(w[j] & 0xffffu));
+      y[8 * i + 2 * j + 1] += E::to((uint16_t)(w[j] >> 16));
     }
   }
   __syncwarp();
@@ -125,7 +126,7 @@ __global__ void __launch_bounds__(kLThreads, 1) k_linear(const LinArgs g, const 
     }
     for (int i = 0; i < 2; ++i) {
       tc::mbar_init(&accfull[i], 1);
-      tc::mbar_init(&accempty[i], 8);           // the tile's four epilogue warps of both CTAs
+      tc::mbar_init(&accempty[i], 16);          // the epilogue warps of both CTAs
     }
     tc::mbar_init(drain, 1);
     *abort = 0;
@@ -226,8 +227,10 @@ __global__ void __launch_bounds__(kLThreads, 1) k_linear(const LinArgs g, const 
     __syncwarp();
   } else if (warp >= 4) {
     // ---------------- epilogue ----------------
+    // All eight warps take each tile, 32 columns by 32 columns: four of them a lane
+    // of tensor memory each, the other four the next 32. What a block reads from
+    // memory (biases, the residual) is asked for ahead.
     const int wg = (warp - 4) >> 2, q = warp & 3;
-    const uint32_t acc = tmem + ((uint32_t)(q * 32) << 16) + wg * 256;
     uint8_t* st = staging + (warp - 4) * kLWarp;
     const uint16_t* res = reinterpret_cast<const uint16_t*>(a.res);
     uint16_t *z = reinterpret_cast<uint16_t*>(a.z), *out = reinterpret_cast<uint16_t*>(a.out);
@@ -235,31 +238,51 @@ __global__ void __launch_bounds__(kLThreads, 1) k_linear(const LinArgs g, const 
     auto bias = [&](int64_t f) {
       return a.wdtype == MOE_DT_F32 ? reinterpret_cast<const float*>(a.bias)[f] : E::to(reinterpret_cast<const uint16_t*>(a.bias)[f]);
     };
-    uint32_t count = 0, mine = 0;
+    constexpr int kBlocks = GATED ? 2 : 4;      // of 32 columns, that a warp takes of a tile at most
+    uint32_t count = 0;
     for (int u = first; u < U; u += stride, ++count) {
-      if ((int)(count & 1) != wg) continue;
       int tm, tn;
       lin_tile(g, u, tm, tn);
-      const bool got = tc::mbar_wait(&accfull[wg], mine & 1, abort);
-      if (!__all_sync(kFull, got)) break;
-      tc::fence_after_sync();
+      const int d = count & 1;
+      const uint32_t acc = tmem + ((uint32_t)(q * 32) << 16) + d * 256;
       const int64_t r0 = (int64_t)tm * 2 * kLM + rank * kLM + q * 32;
       const int nr = (int)max((int64_t)0, min((int64_t)32, a.R - r0));
       const int cols = min(fn, a.N - tn * fn);
-      for (int c = 0; c < cols; c += 32) {
-        const int nc = min(32, cols - c);
+      float bl[kBlocks], bu[kBlocks];
+#pragma unroll
+      for (int i = 0; i < kBlocks; ++i) {
+        const int c = 32 * (wg + 2 * i) + lane;
+        bl[i] = a.bias && c < cols ? bias((int64_t)tn * fn + c) : 0.f;
+        bu[i] = GATED && a.bias && c < cols ? bias((int64_t)a.N + (int64_t)tn * fn + c) : 0.f;
+      }
+      uint4 ahead[4];       // the next block's residual, as block_in holds it
+      const uint16_t* rp = res ? res + r0 * a.ldr + (int64_t)tn * fn : nullptr;
+      auto fetch = [&](int c) {
+        if (!res || !vr || c + 32 > cols) return;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int row = (lane >> 2) + 8 * i;
+          if (row < nr) ahead[i] = *reinterpret_cast<const uint4*>(rp + row * a.ldr + c + 8 * (lane & 3));
+        }
+      };
+      fetch(32 * wg);
+      const bool got = tc::mbar_wait(&accfull[d], (count >> 1) & 1, abort);
+      if (!__all_sync(kFull, got)) break;
+      tc::fence_after_sync();
+#pragma unroll
+      for (int blk = 0; blk < kBlocks; ++blk) {
+        const int c = 32 * (wg + 2 * blk), nc = min(32, cols - c);
+        if (nc <= 0) break;
         const int64_t n0 = (int64_t)tn * fn + c;
         uint32_t v[32], w[GATED ? 32 : 1];
         tc::tmem_ld32(acc + c, v);
         if constexpr (GATED) tc::tmem_ld32(acc + fn + c, w);
-        const float bl = a.bias && lane < nc ? bias(n0 + lane) : 0.f;
-        const float bu = GATED && a.bias && lane < nc ? bias(a.N + n0 + lane) : 0.f;
         tc::tmem_wait_ld();
         float y[32];
 #pragma unroll
         for (int i = 0; i < 32; ++i) {
-          y[i] = __uint_as_float(v[i]) + __shfl_sync(kFull, bl, i);
-          if constexpr (GATED) w[i] = __float_as_uint(__uint_as_float(w[i]) + __shfl_sync(kFull, bu, i));
+          y[i] = __uint_as_float(v[i]) + __shfl_sync(kFull, bl[blk], i);
+          if constexpr (GATED) w[i] = __float_as_uint(__uint_as_float(w[i]) + __shfl_sync(kFull, bu[blk], i));
         }
         if (z) {
           block_out<E>(st, z + r0 * a.ldz + n0, a.ldz, nr, nc, vz, lane, y);
@@ -271,20 +294,24 @@ __global__ void __launch_bounds__(kLThreads, 1) k_linear(const LinArgs g, const 
           else y[i] = act_one(y[i], a.act.act);
         }
         if (res) {
-          float r[32];
-          block_in<E>(st, res + r0 * a.ldr + n0, a.ldr, nr, nc, vr, lane, r);
+          if (vr && nc == 32) {
 #pragma unroll
-          for (int i = 0; i < 32; ++i) y[i] += r[i];
+            for (int i = 0; i < 4; ++i)
+              *reinterpret_cast<uint4*>(st + ((lane >> 2) + 8 * i) * kLRow + 16 * (lane & 3)) = ahead[i];
+            fetch(c + 64);
+          } else {
+            block_in(st, res + r0 * a.ldr + n0, a.ldr, nr, nc, lane);
+          }
+          add_row<E>(st, lane, y);
         }
         block_out<E>(st, out + r0 * a.ldo + n0, a.ldo, nr, nc, vo, lane, y);
       }
       tc::fence_before_sync();
       __syncwarp();
       if (lane == 0) {
-        if (rank != 0) tc::mbar_arrive_peer(tc::peer_smem(&accempty[wg], 0));
-        else tc::mbar_arrive(&accempty[wg]);
+        if (rank != 0) tc::mbar_arrive_peer(tc::peer_smem(&accempty[d], 0));
+        else tc::mbar_arrive(&accempty[d]);
       }
-      ++mine;
     }
   }
 
@@ -357,7 +384,8 @@ static cudaError_t launch_pairs(LinArgs& g, cudaStream_t st) {
 }
 
 cudaError_t launch_linear_fwd(const LinearArgs& a, cudaStream_t st) {
-  if (a.R <= kFewRows) {
+  // Few rows, or too few columns for the pairs: 128 rows x 7168 x 2048 TODO
+  if (a.R <= 128 || (a.R <= kFewRows && (int64_t)a.N * (act_gated(a.act.act) ? 2 : 1) < 40 * 64)) {
     FewArgs f = {};
     f.R = a.R; f.K1 = a.K; f.F1 = a.N; f.act = a.act; f.dtype = a.dtype; f.wdtype = a.wdtype; f.status = a.status;
     f.bias = a.bias; f.res = a.res; f.ldr = a.ldr; f.z = a.z; f.ldz = a.ldz; f.out = a.out; f.ldo = a.ldo;
