@@ -28,14 +28,17 @@
 //   hold, however many of the grid are resident.
 //
 // Roles: warp 0 claims and copies weights, warp 2 copies rows, warps 1 and 3 and the
-// last two issue the MMAs, those between are the epilogue (two accumulators, so
-// that it overlaps the next tile's MMAs). An MMA takes its issuer
-// 52 cycles and more, however few its rows: with one issuer a half stage of 24 rows
-// took 350 cycles, of which its copies need 130. So each of four
-// issues one step (K = 16) in four, into an accumulator of its own, and the
-// epilogue adds the four. Every wait is bounded; a CTA whose wait runs out sets
-// MOE_DEV_TIMEOUT, waits for its copies and MMAs in flight, frees tensor memory and
-// returns.
+// last two issue the MMAs, those between are the epilogue (two accumulators, so that it
+// overlaps the next tile's MMAs). An MMA takes its issuer some 60 cycles, however few its rows,
+// and each stage a wait, a commit and the latency between them, 600 cycles together:
+// with one issuer a half stage of 24 rows took 350 cycles, of which its copies
+// need 130. So up to four warps take the stages in turn, into an accumulator of their
+// own each, and the epilogue adds those, in the order of the tile's stages. The ring has a
+// multiple of as many stages, so that a slot is always the same warp's: one that waits
+// for a use of a slot has itself seen the use before it (a barrier tells neighbouring
+// uses apart only). Every wait is bounded; a CTA whose wait runs
+// out sets MOE_DEV_TIMEOUT, waits for its copies and MMAs in flight, frees tensor
+// memory and returns.
 #include <cmath>
 
 #include "few16.cuh"
@@ -100,8 +103,14 @@ __device__ __forceinline__ void wind_down(uint64_t* full, uint32_t issued, int s
     tc::mbar_wait(&full[i % stages], (i / stages) & 1, &never, 100000000ll);
   }
 }
-__device__ __forceinline__ float add4(const uint32_t (&v)[4]) {
-  return (__uint_as_float(v[0]) + __uint_as_float(v[1])) + (__uint_as_float(v[2]) + __uint_as_float(v[3]));
+// The sum of the first n accumulators (a tile of fewer stages than issuers leaves
+// the others' as they were).
+__device__ __forceinline__ float add4(const uint32_t (&v)[4], int n) {
+  float s = __uint_as_float(v[0]);
+#pragma unroll
+  for (int j = 1; j < 4; ++j)
+    if (j < n) s += __uint_as_float(v[j]);
+  return s;
 }
 // The layer's epilogue warps only.
 __device__ __forceinline__ void epi_sync() { __syncwarp(); asm volatile("bar.sync 1, 128;" ::: "memory"); }
@@ -119,16 +128,23 @@ __device__ __forceinline__ bool epi_all(bool ok) {
   return r != 0;
 }
 
-// An MMA (and a commit, see tc::bar_commit) by one thread of a warp that runs as a
-// whole: the compiler then keeps addresses and descriptors in uniform registers, where
-// the instruction wants them (a thread of its own takes 67 cycles to issue one, this 52,
-// and its loop's own work on top of that).
-__device__ __forceinline__ void mma_one(uint32_t d, uint32_t a, uint32_t b, uint32_t hi, uint32_t idesc, uint32_t acc) {
+// Four MMAs (the steps of 64 of the reduction; and a commit, see tc::bar_commit) by
+// one thread of a warp that runs as a whole: the compiler then keeps addresses and
+// descriptors in uniform registers, where the instructions want them (a thread of its
+// own takes 67 cycles for each, this 52 to 64, and its loop's own work on top of that).
+__device__ __forceinline__ void mma_four(uint32_t d, uint32_t a, uint32_t b, uint32_t hi, uint32_t idesc, uint32_t acc) {
   asm volatile(
-      "{\n .reg .pred p, q;\n .reg .b64 a, b;\n elect.sync _|q, 0xffffffff;\n setp.ne.b32 p, %5, 0;\n"
-      " mov.b64 a, {%1, %3};\n mov.b64 b, {%2, %3};\n"
-      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, p;\n}" ::"r"(d),
-      "r"(a), "r"(b), "r"(hi), "r"(idesc), "r"(acc)
+      "{\n .reg .pred p, q, t;\n .reg .b64 a0, a1, a2, a3, b0, b1, b2, b3;\n elect.sync _|q, 0xffffffff;\n"
+      " setp.ne.b32 p, %11, 0;\n setp.eq.u32 t, 0, 0;\n"
+      " mov.b64 a0, {%1, %9};\n mov.b64 b0, {%5, %9};\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], a0, b0, %10, p;\n"
+      " mov.b64 a1, {%2, %9};\n mov.b64 b1, {%6, %9};\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], a1, b1, %10, t;\n"
+      " mov.b64 a2, {%3, %9};\n mov.b64 b2, {%7, %9};\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], a2, b2, %10, t;\n"
+      " mov.b64 a3, {%4, %9};\n mov.b64 b3, {%8, %9};\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], a3, b3, %10, t;\n}" ::"r"(d),
+      "r"(a), "r"(a + 2), "r"(a + 4), "r"(a + 6), "r"(b), "r"(b + 2), "r"(b + 4), "r"(b + 6), "r"(hi), "r"(idesc), "r"(acc)
       : "memory");
 }
 __device__ __forceinline__ void commit_one(uint32_t bar) {
@@ -196,15 +212,15 @@ __global__ void __launch_bounds__(kFThreads, 1) k_few_layer(const FewArgs g, con
   if (tid == 0) {
     for (int i = 0; i < g.stages; ++i) {
       tc::mbar_init(&full[i], 2);
-      tc::mbar_init(&empty[i], kFIssuers);
+      tc::mbar_init(&empty[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
-      tc::mbar_init(&accfull[i], kFIssuers);
+      tc::mbar_init(&accfull[i], g.issuers);
       tc::mbar_init(&accempty[i], 4);
     }
     for (int i = 0; i < kFQueue; ++i) {
       tc::mbar_init(&qfull[i], 1);
-      tc::mbar_init(&qempty[i], 2 + kFIssuers);     // rows' copies, epilogue, MMAs
+      tc::mbar_init(&qempty[i], 2 + g.issuers);     // rows' copies, epilogue, MMAs
     }
     for (int i = 0; i < kFIssuers; ++i) tc::mbar_init(&drain[i], 1);
     *abort = 0;
@@ -419,13 +435,14 @@ __global__ void __launch_bounds__(kFThreads, 1) k_few_layer(const FewArgs g, con
     }
   } else if (warp < 4 || warp >= 8) {
     // ---------------- MMAs ----------------
-    const uint32_t wi = uni(warp), step = wi == 1 ? 0 : wi == 3 ? 1 : wi - 6;       // of every 64 of the reduction
+    const uint32_t wi = uni(warp), who = wi == 1 ? 0 : wi == 3 ? 1 : wi - 6;
     const uint64_t d0 = tc::smem_desc_sw128(ring_u);
-    const uint32_t lo = uni((uint32_t)d0 + 2 * step), hi = uni((uint32_t)(d0 >> 32));
-    const uint32_t tm = uni(tmem) + step * ncol, bars = uni(full_u), accs = uni(tc::smem_u32(accfull));
+    const uint32_t lo = uni((uint32_t)d0), hi = uni((uint32_t)(d0 >> 32));
+    const uint32_t tm = uni(tmem) + who * ncol, bars = uni(full_u), accs = uni(tc::smem_u32(accfull));
     const uint32_t slot_step = (uint32_t)g.slot / 16;
-    uint32_t slot = 0, at = lo, phase = 0, tiles = 0;
-    bool ok = true;
+    const uint32_t many = (uint32_t)g.issuers;
+    uint32_t slot = 0, at = lo, phase = 0, tiles = 0, turn = 0;      // turn: whose the next stage is
+    bool ok = who < many;
     for (uint32_t n = 0; ok; ++n) {
       const int s = (int)uni((uint32_t)take(n));      // one lane's answer, should a wait run out
       if (s < 0) break;
@@ -442,16 +459,17 @@ __global__ void __launch_bounds__(kFThreads, 1) k_few_layer(const FewArgs g, con
         const uint32_t b_off = hs * a_step, ns = ((uint32_t)nh + hs - 1) / hs;
         uint32_t acc = 0;
         for (uint32_t i = 0, h = uni(first_stage(s, ns)) * hs; i < ns; ++i) {
-          if (!__all_sync(kFull, tc::bar_wait(bars + 8 * slot, phase, abort))) { ok = false; break; }
-          tc::fence_after_sync();
-          const uint32_t n_h = min(hs, (uint32_t)nh - h);
-          uint32_t a = at, b = at + b_off;
-#pragma unroll 2
-          for (uint32_t c = 0; c < n_h; ++c, a += a_step, b += b_step) {
-            mma_one(dt, a, b, hi, idesc, acc);
-            acc = 1;
+          if (turn == who) {
+            if (!__all_sync(kFull, tc::bar_wait(bars + 8 * slot, phase, abort))) { ok = false; break; }
+            tc::fence_after_sync();
+            uint32_t a = at, b = at + b_off;
+            for (uint32_t c = min(hs, (uint32_t)nh - h); c > 0; --c, a += a_step, b += b_step) {
+              mma_four(dt, a, b, hi, idesc, acc);
+              acc = 1;
+            }
+            commit_one(bars + 8 * (kFMaxStages + slot));    // its `empty`
           }
-          commit_one(bars + 8 * (kFMaxStages + slot));      // its `empty`
+          turn = turn + 1 == many ? 0 : turn + 1;
           h = h + hs < (uint32_t)nh ? h + hs : 0;
           at += slot_step;
           if (++slot == (uint32_t)g.stages) {
@@ -468,15 +486,15 @@ __global__ void __launch_bounds__(kFThreads, 1) k_few_layer(const FewArgs g, con
     }
     // every MMA of this warp has completed once its `drain` fires
     __syncwarp();
-    commit_one(uni(tc::smem_u32(&drain[step])));
+    commit_one(uni(tc::smem_u32(&drain[who])));
     volatile int never = 0;
-    tc::mbar_wait(&drain[step], 0, &never, 400000000ll);
+    tc::mbar_wait(&drain[who], 0, &never, 400000000ll);
     __syncwarp();
   } else {
     // ---------------- epilogue ----------------
     const int et = tid - 128, q = warp & 3;
     const uint32_t lanes = tmem + ((uint32_t)(q * 32) << 16);
-    uint32_t tiles = 0;
+    uint32_t tiles = 0, turn = 0;
     bool ok = true;
     for (uint32_t n = 0; ok; ++n) {
       const int s = take(n);
@@ -508,6 +526,12 @@ __global__ void __launch_bounds__(kFThreads, 1) k_few_layer(const FewArgs g, con
         };
         unsigned long long rem = mask[t.e];
         const int m = __popcll(rem);
+        // the accumulators, from that of the tile's first stage on
+        const int ns = (((second ? g.K2 : g.K1) + kFH - 1) / kFH + t.hs - 1) / t.hs, n_acc = min(ns, g.issuers);
+        uint32_t part[4];
+#pragma unroll
+        for (uint32_t j = 0; j < 4; ++j) part[j] = (turn + j) % (uint32_t)g.issuers * ncol;
+        turn = (turn + (uint32_t)ns) % (uint32_t)g.issuers;
         // the thread's row of the tile: an MMA of 64 rows leaves sixteen to each warp's lanes
         const int row = t.arows > 64 ? et : lane < 16 ? q * 16 + lane : kFM;
         if (!second) {
@@ -520,13 +544,14 @@ __global__ void __launch_bounds__(kFThreads, 1) k_few_layer(const FewArgs g, con
               if (i < nc) {
                 const uint32_t c = acc + next_bit(rem);
 #pragma unroll
-                for (int j = 0; j < 4; ++j) tmem_ld1(c + j * ncol, v[i][j]);
+                for (int j = 0; j < 4; ++j)
+                  if (j < n_acc) tmem_ld1(c + part[j], v[i][j]);
               }
             tc::tmem_wait_ld();
             if (row < kFM)
 #pragma unroll
               for (int i = 0; i < kFCols; ++i)
-                if (i < nc) stage[i * kFM + row] = add4(v[i]);
+                if (i < nc) stage[i * kFM + row] = add4(v[i], n_acc);
             if (i0 + kFCols >= m) release();
             epi_sync();
             for (int o = et; o < nc * g.rows1; o += 128) {
@@ -554,13 +579,14 @@ __global__ void __launch_bounds__(kFThreads, 1) k_few_layer(const FewArgs g, con
             for (int i = 0; i < kFCols; ++i)
               if (i0 + i < m)
 #pragma unroll
-                for (int j = 0; j < 4; ++j) tmem_ld1(acc + i0 + i + j * ncol, v[i][j]);
+                for (int j = 0; j < 4; ++j)
+                  if (j < n_acc) tmem_ld1(acc + i0 + i + part[j], v[i][j]);
             tc::tmem_wait_ld();
 #pragma unroll
             for (int i = 0; i < kFCols; ++i)
               if (i0 + i < m) {
                 const int tok = next_bit(rem);
-                if (mine) sums[tok * g.box2 + row] += add4(v[i]);
+                if (mine) sums[tok * g.box2 + row] += add4(v[i], n_acc);
               }
           }
           release();
@@ -643,7 +669,7 @@ __global__ void __launch_bounds__(kDThreads, 1) k_few_linear(const FewArgs g, co
   if (threadIdx.x == 0) {
     for (int i = 0; i < g.stages; ++i) {
       tc::mbar_init(&full[i], 2);
-      tc::mbar_init(&empty[i], g.issuers);
+      tc::mbar_init(&empty[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
       tc::mbar_init(&accfull[i], g.issuers);
@@ -656,7 +682,8 @@ __global__ void __launch_bounds__(kDThreads, 1) k_few_linear(const FewArgs g, co
     tc::prefetch_tmap(&maps.x);
   }
   const uint32_t ncol = g.N <= 16 ? 16 : g.N <= 32 ? 32 : g.N <= 64 ? 64 : g.N <= 128 ? 128 : 256;
-  const uint32_t cols = 2 * g.issuers * ncol < 32 ? 32 : 2 * g.issuers * ncol;
+  uint32_t cols = 32;
+  while (cols < 2 * g.issuers * ncol) cols *= 2;
   if (warp == 1) tc::tmem_alloc(tmem_slot, cols);
   tc::fence_before_sync();
   __syncthreads();
@@ -702,11 +729,11 @@ __global__ void __launch_bounds__(kDThreads, 1) k_few_linear(const FewArgs g, co
     const uint32_t wi = uni(warp), who = wi < 4 ? wi >> 1 : wi - 10, many = (uint32_t)g.issuers;
     if (who < many) {
       const uint64_t d0 = tc::smem_desc_sw128(ring_u);
-      const uint32_t lo = uni((uint32_t)d0 + 2 * who), hi = uni((uint32_t)(d0 >> 32));
+      const uint32_t lo = uni((uint32_t)d0), hi = uni((uint32_t)(d0 >> 32));
       const uint32_t tm = uni(tmem) + who * ncol, bars = uni(full_u), accs = uni(tc::smem_u32(accfull));
       const uint32_t idesc = tc::idesc_16bit(arows <= 64 ? 64 : kFM, g.N, g.dtype == MOE_DT_BF16, 0, 0);
       const uint32_t a_step = arows * 8, b_step = g.N * 8, b_off = hs * a_step, slot_step = (uint32_t)g.slot / 16;
-      uint32_t slot = 0, at = lo, phase = 0, done = 0;
+      uint32_t slot = 0, at = lo, phase = 0, done = 0, turn = 0;      // turn: whose the next stage is
       bool ok = true;
       for (int t = blockIdx.x; ok && t < tiles; t += gridDim.x, ++done) {
         const uint32_t d = done & 1;
@@ -715,22 +742,17 @@ __global__ void __launch_bounds__(kDThreads, 1) k_few_linear(const FewArgs g, co
         const uint32_t dt = tm + d * many * ncol;
         uint32_t acc = 0;
         for (int i = 0, h = first_stage(t, ns) * hs; i < ns; ++i) {
-          if (!__all_sync(kFull, tc::bar_wait(bars + 8 * slot, phase, abort))) { ok = false; break; }
-          tc::fence_after_sync();
-          const int n_h = min(hs, nh - h);
-          uint32_t a = at, b = at + b_off;
-          // the steps (K = 16) of every 64: one in four, in two, or all
-          for (int c = 0; c < n_h; ++c, a += a_step, b += b_step) {
-            mma_one(dt, a, b, hi, idesc, acc);
-            acc = 1;
-            if (many == 2) mma_one(dt, a + 4, b + 4, hi, idesc, 1);
-            if (many == 1) {
-              mma_one(dt, a + 2, b + 2, hi, idesc, 1);
-              mma_one(dt, a + 4, b + 4, hi, idesc, 1);
-              mma_one(dt, a + 6, b + 6, hi, idesc, 1);
+          if (turn == who) {
+            if (!__all_sync(kFull, tc::bar_wait(bars + 8 * slot, phase, abort))) { ok = false; break; }
+            tc::fence_after_sync();
+            uint32_t a = at, b = at + b_off;
+            for (int c = min(hs, nh - h); c > 0; --c, a += a_step, b += b_step) {
+              mma_four(dt, a, b, hi, idesc, acc);
+              acc = 1;
             }
+            commit_one(bars + 8 * (kDStages + slot));       // its `empty`
           }
-          commit_one(bars + 8 * (kDStages + slot));         // its `empty`
+          turn = turn + 1 == many ? 0 : turn + 1;
           h = h + hs < nh ? h + hs : 0;
           at += slot_step;
           if (++slot == (uint32_t)g.stages) {
@@ -792,12 +814,14 @@ __global__ void __launch_bounds__(kDThreads, 1) k_few_linear(const FewArgs g, co
           const int i = i0 + k * step;
           rv[k] = res && i < n && l < nf ? res[(r0 + c + i) * g.ldr + f] : (uint16_t)0;
         }
-        uint32_t v[kDCols];
-        tc::tmem_ld16(acc + c, v);
+        // the accumulators, from that of the tile's first stage on
+        uint32_t v[kDCols], turn = done * (uint32_t)ns % (uint32_t)g.issuers;
+        tc::tmem_ld16(acc + turn * ncol + c, v);
         tc::tmem_wait_ld();
-        for (int w = 1; w < g.issuers; ++w) {
+        for (int w = 1; w < min(g.issuers, ns); ++w) {
           uint32_t u[kDCols];
-          tc::tmem_ld16(acc + w * ncol + c, u);
+          turn = turn + 1 == (uint32_t)g.issuers ? 0 : turn + 1;
+          tc::tmem_ld16(acc + turn * ncol + c, u);
           tc::tmem_wait_ld();
 #pragma unroll
           for (int i = 0; i < kDCols; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) + __uint_as_float(u[i]));
@@ -844,6 +868,13 @@ __global__ void __launch_bounds__(kDThreads, 1) k_few_linear(const FewArgs g, co
 
 // ---- host -------------------------------------------------------------------------
 static int64_t up(int64_t n, int64_t t) { return (n + t - 1) / t; }
+
+// A ring of at most `most` stages, a multiple of its issuers: as many of those as can be.
+static void ring(FewArgs& g, int most, int issuers) {
+  while (issuers > 1 && (most < issuers || most % issuers > 1)) --issuers;      // one stage may go unused
+  g.issuers = issuers;
+  g.stages = most / issuers * issuers;
+}
 
 // Weights [G][halves][rows][K]: boxes of 64 x box rows x halves, `depth` of them
 // along K where K is a whole number of 64 (see copy_weights).
@@ -892,7 +923,7 @@ cudaError_t launch_few_layer(FewArgs g, const void* x, int64_t ldx, const void* 
   // An MMA of 64 or 128 rows reads past the rows that were copied, of A and of B (16
   // where 8 were): within the stage but for its last halves, where the tile is narrow.
   const int pad = 128 * 64;
-  g.stages = std::min(kFMaxStages, (kFSmem - 1024 - g.head - pad) / g.slot);
+  ring(g, std::min(kFMaxStages, (kFSmem - 1024 - g.head - pad) / g.slot), kFIssuers);
   const int smem = 1024 + g.head + g.stages * g.slot + pad;
   FewMaps maps;
   for (int i = 0; i < 8; ++i)
@@ -918,9 +949,8 @@ static cudaError_t launch_linear(FewArgs& g, const FewMaps& maps, int grid, cuda
   g.hs = std::max(1, 32768 / (2 * half)) * 2;
   g.slot = g.hs * half;
   g.head = (kDHead + (kDBias + 2 * kFM) * 4 + 1023) / 1024 * 1024;
-  g.stages = std::min(kDStages, (kFSmem - 1024 - g.head - kDPad) / g.slot);
-  // as many issuers as tensor memory has room for accumulators; wide MMAs need fewer
-  g.issuers = g.N <= 64 ? 4 : g.N <= 128 ? 2 : 1;
+  // no more issuers than tensor memory has room for accumulators; wide MMAs need fewer
+  ring(g, std::min(kDStages, (kFSmem - 1024 - g.head - kDPad) / g.slot), g.N <= 64 ? kFIssuers : g.N <= 128 ? 2 : 1);
   g.lanes = g.rows1 <= 16 ? 16 : g.rows1 <= 32 ? 32 : g.rows1 <= 64 ? 64 : 128;
   note_launch();
   return launch_pdl(k_few_linear<E, GATED>, dim3(grid), dim3(kDThreads), 1024 + g.head + g.stages * g.slot + kDPad, st, g, maps);

@@ -33,7 +33,8 @@ struct FewArgs {
   int rows1;                  // most features a tile
   int head, stages;           // bytes in front of the ring, its stages
   int nt, mt1;                // dense: tiles of rows and of features
-  int hs, issuers, lanes;     // dense: 64s of the reduction a stage, warps that issue MMAs, features side by side in the epilogue
+  int hs, lanes;              // dense: 64s of the reduction a stage, features side by side in the epilogue
+  int issuers;                // warps that issue MMAs; `stages` is a multiple of them
   int Pf, S2;                 // layer: ranges of the second product's features, parts of the groups for each
   int xrows, box2;            // layer: rows of x a copy takes, features of the second product's tiles
   int slot;                   // bytes of a stage
