@@ -29,16 +29,16 @@
 //
 // Roles: warp 0 claims and copies weights, warp 2 copies rows, warps 1 and 3 and the
 // last two issue the MMAs, those between are the epilogue (two accumulators, so that it
-// overlaps the next tile's MMAs). An MMA takes its issuer some 60 cycles, however few its rows,
-// and each stage a wait, a commit and the latency between them, 600 cycles together:
-// with one issuer a half stage of 24 rows took 350 cycles, of which its copies
-// need 130. So up to four warps take the stages in turn, into an accumulator of their
-// own each, and the epilogue adds those, in the order of the tile's stages. The ring has a
-// multiple of as many stages, so that a slot is always the same warp's: one that waits
-// for a use of a slot has itself seen the use before it (a barrier tells neighbouring
-// uses apart only). Every wait is bounded; a CTA whose wait runs
-// out sets MOE_DEV_TIMEOUT, waits for its copies and MMAs in flight, frees tensor
-// memory and returns.
+// overlaps the next tile's MMAs). An MMA takes its issuer some 60 cycles, however few
+// its rows, and each stage a wait, a commit and the latency between them: with one
+// issuer a half stage of 24 rows took 350 cycles, of which its copies need 130. So four
+// warps issue, into an accumulator of their own each, and the epilogue adds the four.
+// In the layer each takes one step (K = 16) in four of every stage, which is done
+// the sooner; a dense product, whose calls are shorter, is the faster with whole
+// stages in turn (16 x 2 x 2048 x 7168 13.5 us against 18.0; the layer 16 tokens, 2880 x 2880
+// 394 against 379). Every wait is bounded; a CTA whose wait runs out sets
+// MOE_DEV_TIMEOUT, waits for its copies and MMAs in flight, frees tensor memory and
+// returns.
 #include <cmath>
 
 #include "few16.cuh"
@@ -52,7 +52,7 @@ constexpr int kFThreads = 320;
 constexpr int kFMaxStages = 8;
 constexpr int kFBars = 512;           // barriers and scratch, in front of the tables
 constexpr int kFSmem = 227 * 1024;
-constexpr int kFCols = 8;             // columns the layer's epilogue takes at a time
+constexpr int kFCols = 8;             // columns the layer's epilogue takes at a time (16 where there are no more)
 constexpr int kFQueue = 4;            // claimed ranges in flight
 constexpr int kFIssuers = 4;          // warps that issue the layer's MMAs
 constexpr int kFLeast = 8;            // features a range, at least
@@ -65,6 +65,12 @@ struct FewMaps {
   CUtensorMap y[4];                   // layer: rows of the second, boxes of 8 << i
 };
 
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&v)[8]) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7])
+               : "r"(taddr)
+               : "memory");
+}
 __device__ __forceinline__ void tmem_ld1(uint32_t taddr, uint32_t& v) {
   asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(v) : "r"(taddr) : "memory");
 }
@@ -92,6 +98,9 @@ __device__ __forceinline__ void copy_rows(uint32_t dst, int half_bytes, const CU
 // 2880 x 128 experts 804 -> 789 us). Not by CTA: which one takes a range varies, and
 // sums must not.
 __device__ __forceinline__ int first_stage(int s, int ns) { return (int)((uint32_t)s * 5u % (uint32_t)ns); }
+// Most 64s of a reduction of K that a stage should hold (an even number): an eighth,
+// so that a short reduction is shared among the issuers too.
+__host__ __device__ __forceinline__ int stage_halves(int K) { return 2 * (1 + K / (16 * kFH)); }
 // Waits (bounded, whatever the abort flag says) for the copies that a thread still
 // has in flight. A slot's barrier completes only when the other copying warp
 // arrived too; where that one stopped earlier the limit ends the wait.
@@ -103,14 +112,24 @@ __device__ __forceinline__ void wind_down(uint64_t* full, uint32_t issued, int s
     tc::mbar_wait(&full[i % stages], (i / stages) & 1, &never, 100000000ll);
   }
 }
-// The sum of the first n accumulators (a tile of fewer stages than issuers leaves
-// the others' as they were).
-__device__ __forceinline__ float add4(const uint32_t (&v)[4], int n) {
-  float s = __uint_as_float(v[0]);
+__device__ __forceinline__ float add4(const uint32_t (&v)[4]) {
+  return (__uint_as_float(v[0]) + __uint_as_float(v[1])) + (__uint_as_float(v[2]) + __uint_as_float(v[3]));
+}
+// C columns of the four accumulators, `ncol` columns apart, added.
+template <int C>
+__device__ __forceinline__ void add_columns(uint32_t (&v)[C], uint32_t acc, uint32_t ncol) {
+  uint32_t u[4][C];
 #pragma unroll
-  for (int j = 1; j < 4; ++j)
-    if (j < n) s += __uint_as_float(v[j]);
-  return s;
+  for (int j = 0; j < 4; ++j) {
+    if constexpr (C == 16) tc::tmem_ld16(acc + j * ncol, u[j]);
+    else tmem_ld8(acc + j * ncol, u[j]);
+  }
+  tc::tmem_wait_ld();
+#pragma unroll
+  for (int i = 0; i < C; ++i) {
+    const uint32_t w[4] = {u[0][i], u[1][i], u[2][i], u[3][i]};
+    v[i] = __float_as_uint(add4(w));
+  }
 }
 // The layer's epilogue warps only.
 __device__ __forceinline__ void epi_sync() { __syncwarp(); asm volatile("bar.sync 1, 128;" ::: "memory"); }
@@ -128,10 +147,18 @@ __device__ __forceinline__ bool epi_all(bool ok) {
   return r != 0;
 }
 
-// Four MMAs (the steps of 64 of the reduction; and a commit, see tc::bar_commit) by
+// An MMA, four (the steps of 64 of the reduction) and a commit (see tc::bar_commit) by
 // one thread of a warp that runs as a whole: the compiler then keeps addresses and
 // descriptors in uniform registers, where the instructions want them (a thread of its
-// own takes 67 cycles for each, this 52 to 64, and its loop's own work on top of that).
+// own takes 67 cycles for an MMA, this 52 to 64, and its loop's own work on top of that).
+__device__ __forceinline__ void mma_one(uint32_t d, uint32_t a, uint32_t b, uint32_t hi, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n .reg .pred p, q;\n .reg .b64 a, b;\n elect.sync _|q, 0xffffffff;\n setp.ne.b32 p, %5, 0;\n"
+      " mov.b64 a, {%1, %3};\n mov.b64 b, {%2, %3};\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, p;\n}" ::"r"(d),
+      "r"(a), "r"(b), "r"(hi), "r"(idesc), "r"(acc)
+      : "memory");
+}
 __device__ __forceinline__ void mma_four(uint32_t d, uint32_t a, uint32_t b, uint32_t hi, uint32_t idesc, uint32_t acc) {
   asm volatile(
       "{\n .reg .pred p, q, t;\n .reg .b64 a0, a1, a2, a3, b0, b1, b2, b3;\n elect.sync _|q, 0xffffffff;\n"
@@ -195,11 +222,11 @@ __global__ void __launch_bounds__(kFThreads, 1) k_few_layer(const FewArgs g, con
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(queue + kFQueue);
   volatile int* abort = reinterpret_cast<volatile int*>(tmem_slot + 1);
   int* tmp = reinterpret_cast<int*>(tmem_slot + 2);                 // 1 + 2 * 10
-  float* stage = reinterpret_cast<float*>(base + kFBars);           // [kFCols][128]
+  float* stage = reinterpret_cast<float*>(base + kFBars);           // [16][128]
   const int G = g.E + g.S, A = g.R * g.k;
   const bool gated = act_gated(g.act.act);
   // the tokens' sums [T][g.box2]; then the tables
-  float* sums = stage + kFCols * kFM;
+  float* sums = stage + 16 * kFM;
   unsigned long long* mask = reinterpret_cast<unsigned long long*>(sums + ((g.R * g.box2 + 1) & ~1));   // [G] tokens
   int* rowof = reinterpret_cast<int*>(mask + G);                    // [G] first row of the group
   int* glist = rowof + G;                                           // groups with tokens
@@ -212,15 +239,15 @@ __global__ void __launch_bounds__(kFThreads, 1) k_few_layer(const FewArgs g, con
   if (tid == 0) {
     for (int i = 0; i < g.stages; ++i) {
       tc::mbar_init(&full[i], 2);
-      tc::mbar_init(&empty[i], 1);
+      tc::mbar_init(&empty[i], kFIssuers);
     }
     for (int i = 0; i < 2; ++i) {
-      tc::mbar_init(&accfull[i], g.issuers);
+      tc::mbar_init(&accfull[i], kFIssuers);
       tc::mbar_init(&accempty[i], 4);
     }
     for (int i = 0; i < kFQueue; ++i) {
       tc::mbar_init(&qfull[i], 1);
-      tc::mbar_init(&qempty[i], 2 + g.issuers);     // rows' copies, epilogue, MMAs
+      tc::mbar_init(&qempty[i], 2 + kFIssuers);     // rows' copies, epilogue, MMAs
     }
     for (int i = 0; i < kFIssuers; ++i) tc::mbar_init(&drain[i], 1);
     *abort = 0;
@@ -435,14 +462,13 @@ __global__ void __launch_bounds__(kFThreads, 1) k_few_layer(const FewArgs g, con
     }
   } else if (warp < 4 || warp >= 8) {
     // ---------------- MMAs ----------------
-    const uint32_t wi = uni(warp), who = wi == 1 ? 0 : wi == 3 ? 1 : wi - 6;
+    const uint32_t wi = uni(warp), step = wi == 1 ? 0 : wi == 3 ? 1 : wi - 6;       // of every 64 of the reduction
     const uint64_t d0 = tc::smem_desc_sw128(ring_u);
-    const uint32_t lo = uni((uint32_t)d0), hi = uni((uint32_t)(d0 >> 32));
-    const uint32_t tm = uni(tmem) + who * ncol, bars = uni(full_u), accs = uni(tc::smem_u32(accfull));
+    const uint32_t lo = uni((uint32_t)d0 + 2 * step), hi = uni((uint32_t)(d0 >> 32));
+    const uint32_t tm = uni(tmem) + step * ncol, bars = uni(full_u), accs = uni(tc::smem_u32(accfull));
     const uint32_t slot_step = (uint32_t)g.slot / 16;
-    const uint32_t many = (uint32_t)g.issuers;
-    uint32_t slot = 0, at = lo, phase = 0, tiles = 0, turn = 0;      // turn: whose the next stage is
-    bool ok = who < many;
+    uint32_t slot = 0, at = lo, phase = 0, tiles = 0;
+    bool ok = true;
     for (uint32_t n = 0; ok; ++n) {
       const int s = (int)uni((uint32_t)take(n));      // one lane's answer, should a wait run out
       if (s < 0) break;
@@ -459,17 +485,16 @@ __global__ void __launch_bounds__(kFThreads, 1) k_few_layer(const FewArgs g, con
         const uint32_t b_off = hs * a_step, ns = ((uint32_t)nh + hs - 1) / hs;
         uint32_t acc = 0;
         for (uint32_t i = 0, h = uni(first_stage(s, ns)) * hs; i < ns; ++i) {
-          if (turn == who) {
-            if (!__all_sync(kFull, tc::bar_wait(bars + 8 * slot, phase, abort))) { ok = false; break; }
-            tc::fence_after_sync();
-            uint32_t a = at, b = at + b_off;
-            for (uint32_t c = min(hs, (uint32_t)nh - h); c > 0; --c, a += a_step, b += b_step) {
-              mma_four(dt, a, b, hi, idesc, acc);
-              acc = 1;
-            }
-            commit_one(bars + 8 * (kFMaxStages + slot));    // its `empty`
+          if (!__all_sync(kFull, tc::bar_wait(bars + 8 * slot, phase, abort))) { ok = false; break; }
+          tc::fence_after_sync();
+          const uint32_t n_h = min(hs, (uint32_t)nh - h);
+          uint32_t a = at, b = at + b_off;
+#pragma unroll 2
+          for (uint32_t c = 0; c < n_h; ++c, a += a_step, b += b_step) {
+            mma_one(dt, a, b, hi, idesc, acc);
+            acc = 1;
           }
-          turn = turn + 1 == many ? 0 : turn + 1;
+          commit_one(bars + 8 * (kFMaxStages + slot));      // its `empty`
           h = h + hs < (uint32_t)nh ? h + hs : 0;
           at += slot_step;
           if (++slot == (uint32_t)g.stages) {
@@ -486,15 +511,15 @@ __global__ void __launch_bounds__(kFThreads, 1) k_few_layer(const FewArgs g, con
     }
     // every MMA of this warp has completed once its `drain` fires
     __syncwarp();
-    commit_one(uni(tc::smem_u32(&drain[who])));
+    commit_one(uni(tc::smem_u32(&drain[step])));
     volatile int never = 0;
-    tc::mbar_wait(&drain[who], 0, &never, 400000000ll);
+    tc::mbar_wait(&drain[step], 0, &never, 400000000ll);
     __syncwarp();
   } else {
     // ---------------- epilogue ----------------
     const int et = tid - 128, q = warp & 3;
     const uint32_t lanes = tmem + ((uint32_t)(q * 32) << 16);
-    uint32_t tiles = 0, turn = 0;
+    uint32_t tiles = 0;
     bool ok = true;
     for (uint32_t n = 0; ok; ++n) {
       const int s = take(n);
@@ -526,39 +551,46 @@ __global__ void __launch_bounds__(kFThreads, 1) k_few_layer(const FewArgs g, con
         };
         unsigned long long rem = mask[t.e];
         const int m = __popcll(rem);
-        // the accumulators, from that of the tile's first stage on
-        const int ns = (((second ? g.K2 : g.K1) + kFH - 1) / kFH + t.hs - 1) / t.hs, n_acc = min(ns, g.issuers);
-        uint32_t part[4];
-#pragma unroll
-        for (uint32_t j = 0; j < 4; ++j) part[j] = (turn + j) % (uint32_t)g.issuers * ncol;
-        turn = (turn + (uint32_t)ns) % (uint32_t)g.issuers;
         // the thread's row of the tile: an MMA of 64 rows leaves sixteen to each warp's lanes
         const int row = t.arows > 64 ? et : lane < 16 ? q * 16 + lane : kFM;
         if (!second) {
           const int r0 = rowof[t.e];
-          for (int i0 = 0; i0 < m; i0 += kFCols) {
-            const int nc = min(kFCols, m - i0);
-            uint32_t v[kFCols][4];
+          const bool all = g.N == 16;         // up to 16 tokens: all their columns at once, the group's own picked below
+          const int step = all ? 16 : kFCols;
+          for (int i0 = 0; i0 < m; i0 += step) {
+            const int nc = min(step, m - i0);
+            if (all) {
+              uint32_t v[16];
+              add_columns<16>(v, acc, ncol);
+              if (row < kFM)
 #pragma unroll
-            for (int i = 0; i < kFCols; ++i)
-              if (i < nc) {
-                const uint32_t c = acc + next_bit(rem);
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                  if (j < n_acc) tmem_ld1(c + part[j], v[i][j]);
-              }
-            tc::tmem_wait_ld();
-            if (row < kFM)
+                for (int i = 0; i < 16; ++i) stage[i * kFM + row] = __uint_as_float(v[i]);
+            } else {
+              uint32_t v[kFCols][4];
 #pragma unroll
               for (int i = 0; i < kFCols; ++i)
-                if (i < nc) stage[i * kFM + row] = add4(v[i], n_acc);
-            if (i0 + kFCols >= m) release();
+                if (i < nc) {
+                  const uint32_t c = acc + next_bit(rem);
+#pragma unroll
+                  for (int j = 0; j < 4; ++j) tmem_ld1(c + j * ncol, v[i][j]);
+                }
+              tc::tmem_wait_ld();
+              if (row < kFM)
+#pragma unroll
+                for (int i = 0; i < kFCols; ++i)
+                  if (i < nc) stage[i * kFM + row] = add4(v[i]);
+            }
+            if (i0 + step >= m) release();
             epi_sync();
-            for (int o = et; o < nc * g.rows1; o += 128) {
-              const int i = o / g.rows1, l = o % g.rows1;
+            // a thread's feature l of the tile, of every `skip`-th token
+            const int l = et & (g.rows1 - 1), skip = 128 / g.rows1;
+            unsigned long long cols = rem;                // all: the columns of the group's tokens
+            if (et >= g.rows1) cols &= cols - 1;
+            for (int i = et / g.rows1; i < nc; i += skip) {
+              const int c = all ? __ffsll((long long)cols) - 1 : i, f = t.f0 + l;
+              for (int j = 0; j < skip; ++j) cols &= cols - 1;
               if (l >= t.len) continue;
-              const int f = t.f0 + l;
-              float a = stage[i * kFM + l], u = gated ? stage[i * kFM + t.box + l] : 0.f;
+              float a = stage[c * kFM + l], u = gated ? stage[c * kFM + t.box + l] : 0.f;
               if (g.b1) {
                 a += g.b1[(int64_t)t.e * 2 * g.F1 + f];
                 u += g.b1[(int64_t)t.e * 2 * g.F1 + g.F1 + f];
@@ -574,19 +606,13 @@ __global__ void __launch_bounds__(kFThreads, 1) k_few_layer(const FewArgs g, con
           if (mine && t.e == glist[r.g0])
             for (int i = 0; i < g.R; ++i) sums[i * g.box2 + row] = 0.f;
           for (int i0 = 0; i0 < m; i0 += kFCols) {
-            uint32_t v[kFCols][4];
-#pragma unroll
-            for (int i = 0; i < kFCols; ++i)
-              if (i0 + i < m)
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                  if (j < n_acc) tmem_ld1(acc + i0 + i + part[j], v[i][j]);
-            tc::tmem_wait_ld();
+            uint32_t v[kFCols];
+            add_columns<kFCols>(v, acc + i0, ncol);
 #pragma unroll
             for (int i = 0; i < kFCols; ++i)
               if (i0 + i < m) {
                 const int tok = next_bit(rem);
-                if (mine) sums[tok * g.box2 + row] += add4(v[i], n_acc);
+                if (mine) sums[tok * g.box2 + row] += __uint_as_float(v[i]);
               }
           }
           release();
@@ -869,7 +895,9 @@ __global__ void __launch_bounds__(kDThreads, 1) k_few_linear(const FewArgs g, co
 // ---- host -------------------------------------------------------------------------
 static int64_t up(int64_t n, int64_t t) { return (n + t - 1) / t; }
 
-// A ring of at most `most` stages, a multiple of its issuers: as many of those as can be.
+// A ring of at most `most` stages, a multiple of its issuers, as many of those as can be:
+// a slot is then always the same warp's, and one that waits for a use of a slot has
+// itself seen the use before it (a barrier tells neighbouring uses apart only).
 static void ring(FewArgs& g, int most, int issuers) {
   while (issuers > 1 && (most < issuers || most % issuers > 1)) --issuers;      // one stage may go unused
   g.issuers = issuers;
@@ -918,12 +946,12 @@ cudaError_t launch_few_layer(FewArgs g, const void* x, int64_t ldx, const void* 
   int box_t = 8;                                    // rows of the second product's widest copy
   while (box_t < g.R) box_t *= 2;
   g.slot = 2 * 128 * std::max(kFM + g.xrows, g.box2 + box_t);
-  const int head = kFBars + kFCols * kFM * 4 + 4 * (g.R * g.box2 + 2) + 12 * G + 4 * std::min(G, A + g.S) + 4 * (A + g.S * g.R) + 8 * A;
+  const int head = kFBars + 16 * kFM * 4 + 4 * (g.R * g.box2 + 2) + 12 * G + 4 * std::min(G, A + g.S) + 4 * (A + g.S * g.R) + 8 * A;
   g.head = (head + 1023) / 1024 * 1024;
   // An MMA of 64 or 128 rows reads past the rows that were copied, of A and of B (16
   // where 8 were): within the stage but for its last halves, where the tile is narrow.
   const int pad = 128 * 64;
-  ring(g, std::min(kFMaxStages, (kFSmem - 1024 - g.head - pad) / g.slot), kFIssuers);
+  g.stages = std::min(kFMaxStages, (kFSmem - 1024 - g.head - pad) / g.slot);
   const int smem = 1024 + g.head + g.stages * g.slot + pad;
   FewMaps maps;
   for (int i = 0; i < 8; ++i)
@@ -946,7 +974,7 @@ static cudaError_t launch_linear(FewArgs& g, const FewMaps& maps, int grid, cuda
   const cudaError_t e = set_smem_once((const void*)k_few_linear<E, GATED>, kFSmem, done);
   if (e != cudaSuccess) return e;
   const int half = 128 * ((GATED ? 2 : 1) * g.rows1 + g.N);
-  g.hs = std::max(1, 32768 / (2 * half)) * 2;
+  g.hs = std::min(std::max(1, 32768 / (2 * half)) * 2, stage_halves(g.K1));
   g.slot = g.hs * half;
   g.head = (kDHead + (kDBias + 2 * kFM) * 4 + 1023) / 1024 * 1024;
   // no more issuers than tensor memory has room for accumulators; wide MMAs need fewer
