@@ -336,12 +336,16 @@ cudaError_t launch_mm_fp8(const MmArgs& a, cudaStream_t st);
 
 // ---- dense products with an epilogue (linear.cu) --------------------------------
 // Whether an activation takes a gate and an up column.
-__host__ __device__ __forceinline__ bool act_gated(int act) { return act < MOE_ACT_SRELU; }
+__host__ __device__ constexpr bool act_gated(int act) { return act < MOE_ACT_SRELU; }
 // Phi(v) by erfc: 1 + erf(v / sqrt 2) cancels for negative v, where v Phi(v) is
 // small but not rounded away.
 __device__ __forceinline__ float cdf_(float v) { return 0.5f * erfcf(v * -0.70710678118654752f); }
-// Clamp that lets a NaN through.
-__device__ __forceinline__ float clamp_(float v, float lim) { return v > lim ? lim : (v < -lim ? -lim : v); }
+// Clamp to [-lim, lim] that lets a NaN through.
+__device__ __forceinline__ float clamp_(float v, float lim) {
+  asm("min.NaN.f32 %0, %0, %1;" : "+f"(v) : "f"(lim));
+  asm("max.NaN.f32 %0, %0, %1;" : "+f"(v) : "f"(-lim));
+  return v;
+}
 __device__ __forceinline__ float act_one(float z, int act) {
   if (act == MOE_ACT_SRELU) return z <= 0.f ? 0.f : z * z;
   if (act == MOE_ACT_GELU) return z * cdf_(z);
