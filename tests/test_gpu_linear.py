@@ -88,6 +88,33 @@ def test_linear_forward_of_many_tiles(R, N, K, act):
     _forward(R, N, K, act, BF16, residual=act == "none", save=act != "none")
 
 
+@pytest.mark.parametrize("act", ["gelu", "silu", "geglu"])
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("R", [1, 300])
+def test_linear_activation_over_its_range(act, dtype, R):
+    """z = w (x and K are one): every value of the type from -14 to 14 in steps, and the smallest, through the activation and
+    its derivative; relative to the result, which is tiny on the left."""
+    cuda_device()
+    v = torch.cat([torch.linspace(-14, 14, 5000), torch.logspace(-4, 1, 300), -torch.logspace(-4, 1, 300)]).to("cuda", dtype)
+    n = v.numel()
+    rows = D.halves(act) * n
+    w = torch.zeros(rows, 8, dtype=dtype, device="cuda")[:, :1]
+    w[:n, 0] = v
+    if rows > n:
+        w[n:, 0] = 1
+    x = torch.ones(R, 8, dtype=dtype, device="cuda")[:, :1]
+    out, z = torch.empty(R, n, dtype=dtype, device="cuda"), torch.empty(R, rows, dtype=dtype, device="cuda")
+    m.moe_linear_forward(x, w, out, _ws(R, rows, 1), z=z, act=act)
+    ro, bo, rz, _ = D.linear(x, w, None, None, act, 1.0, 0.0)
+    assert torch.equal(z.double(), rz)
+    val, err, _, _, _ = D.act(rz.chunk(D.halves(act), 1), act)       # z is exact: the activation's error alone
+    P.assert_within(out, val, err, "out")
+    dz = torch.empty_like(z)
+    m.moe_linear_backward(torch.ones_like(out), x, w, z, dz, None, None, None, _ws(R, rows, 1, True), act=act)
+    rdz, bdz = D.linear_dz(torch.ones_like(out), z, act, 1.0, 0.0)
+    P.assert_within(dz, rdz, bdz, "dz")
+
+
 def test_linear_residual_in_place_and_repeatable():
     cuda_device()
     for R in (5, 90, 700):
