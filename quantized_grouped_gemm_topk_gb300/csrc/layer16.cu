@@ -71,16 +71,17 @@ struct RouteArgs16 {
   float* part;          // [z][ks][tt][ep]
 };
 
-// Sums of a float4 over `n` partial sums, `step` floats apart, eight at a time.
+// Sums of a float4 over `n` partial sums, `step` floats apart, kRAhead at a time.
+constexpr int kRAhead = 20;
 __device__ __forceinline__ float4 sum_parts(const float* p, int n, int64_t step) {
   float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int i = 0; i < n; i += 8) {
-    float4 v[8];
+  for (int i = 0; i < n; i += kRAhead) {
+    float4 v[kRAhead];
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
+    for (int j = 0; j < kRAhead; ++j)
       v[j] = i + j < n ? __ldcg(reinterpret_cast<const float4*>(p + (i + j) * step)) : make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) { s.x += v[j].x; s.y += v[j].y; s.z += v[j].z; s.w += v[j].w; }
+    for (int j = 0; j < kRAhead; ++j) { s.x += v[j].x; s.y += v[j].y; s.z += v[j].z; s.w += v[j].w; }
   }
   return s;
 }
