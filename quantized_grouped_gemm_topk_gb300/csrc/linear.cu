@@ -12,18 +12,20 @@
 namespace moe {
 
 // ---- forward ----------------------------------------------------------------------
-// Whether a result of M x N (gated: of N columns a half) has tiles for about half of the pairs.
-static bool for_pairs(int64_t M, int64_t N) { return up(M, 256) * up(N, 64) >= 40; }
-
 static cudaError_t launch_pairs(LinArgs& g, int mode, bool gated, cudaStream_t st) {
   return g.a.dtype == MOE_DT_BF16 ? launch_pairs_bf16(g, mode, gated, st) : launch_pairs_f16(g, mode, gated, st);
 }
 
 cudaError_t launch_linear_fwd(const LinearArgs& a, cudaStream_t st) {
   const bool gated = act_gated(a.act.act);
-  // Few rows, or too few columns for the pairs. 128 rows x 7168 x 2048 18 us here, 15 with
-  // pairs, 96 rows x 2 x 2048 x 7168 21 and 31, 256 rows x 640 x 704 7 and 9.
-  if (a.R <= 128 || (a.R <= kFewRows && !for_pairs(a.R, (int64_t)a.N * (gated ? 2 : 1)))) {
+  // Few rows: there a tile's weights are shared out over all SMs, and the time grows with
+  // the rows; on pairs, one tile of 256 rows however many there are, with the
+  // reduction (4 us and 3.8 for each 1000 of it). In us, here and on pairs: 64 rows x
+  // 7168 x 2048 11.0, 13.4; 128 rows 15.1, 13.6, x 2 x 2880 x 2880 17.3, 17.4, x 2880 x
+  // 7168 20.4, 30.7; 256 rows x 7168 x 2048 23.8, 13.9, x 1440 x 2880 12.8, 15.9, x 2 x
+  // 1024 x 512 6.8, 6.2.
+  const int64_t rows = (int64_t)a.N * (gated ? 2 : 1);
+  if (a.R <= 64 || (a.R <= kFewRows && a.R * rows < 256ll * a.K)) {
     FewArgs f = {};
     f.R = a.R; f.K1 = a.K; f.F1 = a.N; f.act = a.act; f.dtype = a.dtype; f.wdtype = a.wdtype; f.status = a.status;
     f.bias = a.bias; f.res = a.res; f.ldr = a.ldr; f.z = a.z; f.ldz = a.ldz; f.out = a.out; f.ldo = a.ldo;
@@ -210,8 +212,12 @@ cudaError_t launch_linear_bwd(const LinearArgs& a, cudaStream_t st) {
   cudaError_t e = cudaSuccess;
   if (!plain || a.db) e = a.dtype == MOE_DT_BF16 ? launch_dz<Bf16>(a, st) : launch_dz<F16>(a, st);
   if (e != cudaSuccess) return e;
-  // The products: pairs of SMs where there are tiles for them, else the grouped
-  // products' kernel with one group (narrow tiles, the reduction split).
+  // The products run on pairs of SMs. A long reduction of few tiles takes them long (as
+  // the forward's few rows), and goes to the grouped products' kernel with one group, which
+  // splits it. In us, there and on pairs: dx of 16 x 2880 x 2880 9.7, 13.5, of 200 x 4096
+  // x 1024 13.7, 18.1, of 512 x 2880 x 2880 17.3, 14.6; dw of 4096 x 300 x 200 11.1, 17.6, of
+  // 8192 x 128 x 4096 30, 36, of 1003 x 1441 x 1999 15.8, 10.3.
+  auto split = [](int64_t M, int64_t N, int64_t red) { return red >= 2048 && up(M, 256) * up(N, 128) < 40; };
   LinArgs g = {};
   g.a = a;
   if (plain) {
@@ -224,7 +230,7 @@ cudaError_t launch_linear_bwd(const LinearArgs& a, cudaStream_t st) {
   m.lda = plain ? a.lddout : a.lddz;
   m.part = a.part + (dz_part_floats(a.R, rows) + 3) / 4 * 4;
   if (a.dx) {
-    if (a.R > 128 && for_pairs(a.R, a.K)) {
+    if (!split(a.R, a.K, rows)) {
       g.M = a.R; g.N = a.K; g.K = rows; g.out = reinterpret_cast<uint16_t*>(a.dx); g.ldo = a.lddx;
       e = launch_pairs(g, kLinDx, false, st);
     } else {
@@ -235,7 +241,7 @@ cudaError_t launch_linear_bwd(const LinearArgs& a, cudaStream_t st) {
     if (e != cudaSuccess) return e;
   }
   if (a.dw) {
-    if (a.R > 128 && for_pairs(rows, a.K)) {
+    if (!split(rows, a.K, a.R)) {
       g.M = rows; g.N = a.K; g.K = a.R; g.out = reinterpret_cast<uint16_t*>(a.dw); g.ldo = a.lddw;
       return launch_pairs(g, kLinDw, false, st);
     }
