@@ -650,9 +650,19 @@ def moe_linear_workspace_size(R, rows, K, backward=False) -> int:
     return n.value
 
 
-def _opt(t, name, dtypes, shape, dev):
-    """(address, row stride) of an optional matrix."""
-    return (None, 0) if t is None else (_arg(t, name, dtypes, shape, dev), _ld(t, name))
+def _mat(t, name, dtypes, shape, dev, whole=1):
+    """(address, row stride) of a matrix, checked as by _arg and _ld in one go: a short call's time is these checks'."""
+    st = t.stride()
+    if t.shape != shape or t.dtype not in dtypes or t.get_device() != dev or st[-1] != 1:
+        return _arg(t, name, dtypes, shape, dev), _ld(t, name, whole)
+    if shape[-2] > 1 and st[-2] >= shape[-1]:
+        return t.data_ptr(), st[-2]
+    return t.data_ptr(), _ld(t, name, whole)
+
+
+def _opt(t, name, dtypes, shape, dev, whole=1):
+    """_mat of an optional matrix."""
+    return (None, 0) if t is None else _mat(t, name, dtypes, shape, dev, whole)
 
 
 def moe_linear_forward(x, w, out, ws, bias=None, residual=None, z=None, act="none", alpha=1.0, limit=0.0, stream=None):
@@ -667,13 +677,15 @@ def moe_linear_forward(x, w, out, ws, bias=None, residual=None, z=None, act="non
     rows = 2 * N if a < MOE_ACT_SRELU else N
     own = (x.dtype,)
     wt = torch.float32 if bias is None else bias.dtype
+    xp, xl = _mat(x, "x", _16BIT, (R, K), dev, 8)
+    kp, kl = _mat(w, "w", own, (rows, K), dev, 8)
     rp, rl = _opt(residual, "residual", own, (R, N), dev)
     zp, zl = _opt(z, "z", own, (R, rows), dev)
+    op, ol = _mat(out, "out", own, (R, N), dev)
     wp, wn = _ws(ws, dev)
     _check("moe_linear_forward", load().moe_linear_forward(
-        _arg(x, "x", _16BIT, (R, K), dev), _ld(x, "x", 8), _arg(w, "w", own, (rows, K), dev), _ld(w, "w", 8),
-        _flat(bias, "bias", (x.dtype, torch.float32), (rows,), dev), rp, rl, R, N, K, a, alpha, limit, DTYPES[x.dtype],
-        DTYPES[wt], zp, zl, _arg(out, "out", own, (R, N), dev), _ld(out, "out"), wp, wn, _stream(stream)))
+        xp, xl, kp, kl, _flat(bias, "bias", (x.dtype, torch.float32), (rows,), dev), rp, rl, R, N, K, a, alpha, limit,
+        DTYPES[x.dtype], DTYPES[wt], zp, zl, op, ol, wp, wn, _stream(stream)))
 
 
 def moe_linear_backward(dout, x, w, z, dz, dx, dw, db, ws, act="none", alpha=1.0, limit=0.0, stream=None):
@@ -689,15 +701,16 @@ def moe_linear_backward(dout, x, w, z, dz, dx, dw, db, ws, act="none", alpha=1.0
     wt = torch.float32 if db is None else db.dtype
     if a == MOE_ACT_NONE and (z is not None or dz is not None):
         raise ValueError("act \"none\" takes no z and no dz")
+    op, ol = _mat(dout, "dout", own, (R, N), dev, 8 if a == MOE_ACT_NONE else 1)
+    xp, xl = _mat(x, "x", _16BIT, (R, K), dev, 8)
+    kp, kl = _mat(w, "w", own, (rows, K), dev, 8)
     zp, zl = _opt(z, "z", own, (R, rows), dev)
-    gp = None if dz is None else _arg(dz, "dz", own, (R, rows), dev)
-    xp, xl = _opt(dx, "dx", own, (R, K), dev)
-    dp, dl = _opt(dw, "dw", own, (rows, K), dev)
+    gp, gl = _opt(dz, "dz", own, (R, rows), dev, 8)
+    dxp, dxl = _opt(dx, "dx", own, (R, K), dev)
+    dwp, dwl = _opt(dw, "dw", own, (rows, K), dev)
     wp, wn = _ws(ws, dev)
     _check("moe_linear_backward", load().moe_linear_backward(
-        _arg(dout, "dout", own, (R, N), dev), _ld(dout, "dout", 8 if a == MOE_ACT_NONE else 1),
-        _arg(x, "x", _16BIT, (R, K), dev), _ld(x, "x", 8), _arg(w, "w", own, (rows, K), dev), _ld(w, "w", 8), zp, zl, R, N,
-        K, a, alpha, limit, DTYPES[x.dtype], DTYPES[wt], gp, 0 if dz is None else _ld(dz, "dz", 8), xp, xl, dp, dl,
+        op, ol, xp, xl, kp, kl, zp, zl, R, N, K, a, alpha, limit, DTYPES[x.dtype], DTYPES[wt], gp, gl, dxp, dxl, dwp, dwl,
         _flat(db, "db", (x.dtype, torch.float32), (rows,), dev), wp, wn, _stream(stream)))
 
 
@@ -721,14 +734,16 @@ def moe_layer16_forward(x, W_r, logits, w1, w2, out, topk_ids, topk_w, ws, b1=No
     E = G - n_shared
     rows = I if act == "srelu" else 2 * I
     own = (x.dtype,)
+    xp, xl = _mat(x, "x", _16BIT, (T, H), dev, 8)
+    w1p, l1 = _mat(w1, "w1", own, (G, rows, H), dev, 8)
+    w2p, l2 = _mat(w2, "w2", own, (G, H, I), dev, 8)
+    op, ol = _mat(out, "out", own, (T, H), dev)
     wp, wn = _ws(ws, dev)
     _check("moe_layer16_forward", load().moe_layer16_forward(
-        _arg(x, "x", _16BIT, (T, H), dev), _ld(x, "x", 8), _flat(W_r, "W_r", _F32, (H, E), dev),
-        _flat(logits, "logits", _F32, (T, E), dev), _arg(w1, "w1", own, (G, rows, H), dev), _group(w1), _ld(w1, "w1", 8),
-        _flat(b1, "b1", _F32, (G, 2 * I), dev), _arg(w2, "w2", own, (G, H, I), dev), _group(w2), _ld(w2, "w2", 8), T, H, I,
-        E, k, n_shared, ACTS[act], alpha, limit, routed_scale, DTYPES[x.dtype], _arg(out, "out", own, (T, H), dev),
-        _ld(out, "out"), _flat(topk_ids, "topk_ids", _I32, (T, k), dev), _flat(topk_w, "topk_w", _F32, (T, k), dev), wp,
-        wn, _stream(stream)))
+        xp, xl, _flat(W_r, "W_r", _F32, (H, E), dev), _flat(logits, "logits", _F32, (T, E), dev), w1p, _group(w1), l1,
+        _flat(b1, "b1", _F32, (G, 2 * I), dev), w2p, _group(w2), l2, T, H, I, E, k, n_shared, ACTS[act], alpha, limit,
+        routed_scale, DTYPES[x.dtype], op, ol, _flat(topk_ids, "topk_ids", _I32, (T, k), dev),
+        _flat(topk_w, "topk_w", _F32, (T, k), dev), wp, wn, _stream(stream)))
 
 
 def moe_mm_read_status(ws, stream=None) -> int:

@@ -251,6 +251,69 @@ def test_layer16_weights_past_32_bits():
     P.assert_within(out, ref, bound, "out")
 
 
+@pytest.mark.parametrize("T,H,I,E,k,S", [(3, 40008, 72, 3, 2, 0), (64, 20001, 40, 5, 3, 1), (2, 72, 30001, 2, 2, 0), (20, 16, 9000, 40, 2, 0)])
+def test_layer16_wide(T, H, I, E, k, S):
+    """Wider than a tile for every SM, in the second product and in the first."""
+    _layer(T, H, I, E, k, S, "swiglu_clamp", BF16, True)
+
+
+def test_layer16_first_call_in_a_graph_on_another_stream():
+    """Captured without a call before it, in the same process or not: nothing is allocated or waited for."""
+    cuda_device()
+    c = _inputs(7, 320, 192, 9, 3, 0, "geglu", F16, False, 0)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        _run(c, "geglu", W_r=c["W_r"])
+    for _ in range(2):
+        c["out"].fill_(NAN)
+        graph.replay()
+        torch.cuda.synchronize()
+        _check_out(c, "geglu", 0)
+
+
+def test_layer16_of_a_trained_block():
+    """The experts that the example's grouped products train, served: the same layer, token by token and in a batch."""
+    cuda_device()
+    T, H, I, E, k = 24, 256, 128, 8, 2
+    c = _inputs(T, H, I, E, k, 0, "swiglu", BF16, False, 0)
+    _run(c, "swiglu", W_r=c["W_r"])
+    whole, ids, wts = c["out"].clone(), c["ids"].clone(), c["wts"].clone()
+    # the same tokens by the grouped products, sorted by expert
+    order = torch.argsort(ids.flatten().long(), stable=True)
+    off = torch.zeros(E + 1, dtype=I32, device="cuda")
+    off[1:] = torch.bincount(ids.flatten().long(), minlength=E).cumsum(0)
+    rows = T * k
+    xg = c["x"][order // k].contiguous()
+    h, y, z = (torch.empty(rows, n, dtype=BF16, device="cuda") for n in (2 * I, I, H))
+    ws = torch.zeros(max(m.moe_mm_workspace_size(m.MOE_MM_ROWS, rows, n, q, E) for n, q in ((2 * I, H), (H, I))), dtype=torch.uint8,
+                     device="cuda")
+    m.moe_grouped_mm(xg, c["w1"].contiguous(), off, h, ws)
+    q, s = torch.empty(rows, 2 * I, dtype=torch.uint8, device="cuda"), torch.empty(rows, 2 * -(-I // 128), device="cuda")
+    m.moe_act_ckpt_forward(h, wts.flatten()[order].contiguous(), y, q, s)
+    m.moe_grouped_mm(y, c["w2"].contiguous(), off, z, ws)
+    other = torch.zeros(T, H, dtype=torch.float64, device="cuda").index_add_(0, order // k, z.double())
+    # h and z of the grouped way are rounded to bf16 too: h's half step moves act by 2^-8 (|g| act'_g + |u| act'_u) <= 2^-8 * 3
+    # |act| and a little, z's is 2^-8 |z| a slot
+    ref, bound = D.layer(c["x"], c["w1"], c["w2"], None, ids.long(), wts, 0, "swiglu", 1.0, 0.0)
+    mag = z.double().abs()
+    slack = torch.zeros_like(other).index_add_(0, order // k, 2.0 ** -8 * mag)
+    a = torch.cat([v.double() for v in (h,)], 1)
+    g, u = a[:, :I], a[:, I:]
+    dact = 2.0 ** -8 * (g.abs() * (1.2 * u.abs()) + u.abs() * g.abs()) * wts.flatten()[order].double()[:, None]
+    for e in range(E):
+        sl = slice(int(off[e]), int(off[e + 1]))
+        slack.index_add_(0, order[sl] // k, dact[sl] @ c["w2"][e].double().abs().t())
+    assert bool(((other - ref).abs() <= bound + slack + 1e-6).all())
+    P.assert_within(whole, ref, bound, "out")
+    # one token at a time: its own weights, whose logits may be summed in another order, and the same bound
+    for t in (0, 11, 23):
+        out = torch.empty(1, H, dtype=BF16, device="cuda")
+        m.moe_layer16_forward(c["x"][t:t + 1], c["W_r"], None, c["w1"], c["w2"], out, c["ids"][:1], c["wts"][:1], c["ws"])
+        assert torch.equal(c["ids"][0], ids[t])
+        one = D.layer(c["x"][t:t + 1], c["w1"], c["w2"], None, c["ids"][:1].long(), c["wts"][:1], 0, "swiglu", 1.0, 0.0)
+        P.assert_within(out, *one, "one token")
+
+
 def test_layer16_no_tokens():
     cuda_device()
     c = _inputs(1, 64, 64, 4, 2, 0, "swiglu", BF16, False, 0)

@@ -115,6 +115,22 @@ def test_linear_activation_over_its_range(act, dtype, R):
     P.assert_within(dz, rdz, bdz, "dz")
 
 
+# both sides of the rules that pick a kernel: rows times weight rows against 256 times the reduction (65 to 256 rows); backward:
+# a reduction from 2048 on with fewer than 40 tiles of 256 x 128
+@pytest.mark.parametrize("R,N,K", [(64, 520, 64), (65, 520, 128), (65, 520, 136), (256, 256, 256), (256, 248, 256), (255, 1000, 1000),
+                                   (250, 130, 2500), (130, 40, 70000), (2, 8, 70000), (256, 2056, 2048)])
+@pytest.mark.parametrize("act", ["none", "swiglu"])
+def test_linear_forward_on_both_sides_of_the_rule(R, N, K, act):
+    _forward(R, N, K, act, BF16)
+
+
+@pytest.mark.parametrize("R,N,K", [(2047, 264, 136), (2048, 264, 136), (40, 2048, 264), (40, 2040, 264), (2304, 600, 1280), (2300, 1300, 1300),
+                                   (600, 2100, 1300)])
+@pytest.mark.parametrize("act", ["none", "silu", "geglu"])
+def test_linear_backward_on_both_sides_of_the_rule(R, N, K, act):
+    _backward(R, N, K, act, BF16)
+
+
 def test_linear_residual_in_place_and_repeatable():
     cuda_device()
     for R in (5, 90, 700):
