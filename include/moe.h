@@ -577,7 +577,9 @@ moe_status_t moe_linear_workspace_size(int R, int rows, int K, int backward, siz
  * start on 16 bytes, ldx, ldw1, ldw2 and the group strides are multiples of 8
  * elements. T > MOE_LAYER16_MAX_T: MOE_ERR_UNSUPPORTED (the grouped products are
  * for those). ws: moe_layer16_workspace_size bytes for T tokens (a larger T's
- * suffices), starting with the status word (moe_mm_read_status); zero it once. */
+ * suffices), starting with the status word (moe_mm_read_status); zero it once.
+ * Calls that follow one another may share a workspace, those of the products too:
+ * only its first 256 bytes carry anything from call to call. */
 #define MOE_LAYER16_MAX_T 64
 moe_status_t moe_layer16_forward(const void* x, int64_t ldx, const float* W_r, const float* logits, const void* w1,
                                  int64_t w1_group, int64_t ldw1, const float* b1, const void* w2, int64_t w2_group,

@@ -7,7 +7,8 @@ using namespace moe;
 
 namespace {
 
-constexpr size_t kStatusBytes = 256;   // the status word's place in a products' workspace
+constexpr size_t kStatusBytes = 256;   // the status word's block in a products' workspace; all behind it is scratch
+constexpr size_t kArriveAt = 128;      // in it, the few tokens' layer's counters
 
 bool is16(int dt) { return dt == MOE_DT_BF16 || dt == MOE_DT_F16; }
 bool is_float(int dt) { return is16(dt) || dt == MOE_DT_F32; }
@@ -347,6 +348,7 @@ moe_status_t moe_layer16_forward(const void* x, int64_t ldx, const float* W_r, c
   a.dtype = dtype; a.x = x; a.ldx = ldx; a.W_r = W_r; a.logits = logits; a.w1 = w1; a.g1 = w1_group; a.ld1 = ldw1;
   a.b1 = b1; a.w2 = w2; a.g2 = w2_group; a.ld2 = ldw2; a.out = out; a.ldo = ldo; a.ids = topk_ids; a.w = topk_w;
   a.status = reinterpret_cast<int32_t*>(ws); a.ws = reinterpret_cast<uint8_t*>(ws) + kStatusBytes;
+  a.arrive = reinterpret_cast<int32_t*>(reinterpret_cast<uint8_t*>(ws) + kArriveAt);
   return done(launch_layer16(a, (cudaStream_t)stream));
 }
 

@@ -15,8 +15,7 @@ constexpr int kRThreads = 512;
 constexpr int kRTokens = 8;           // most tokens of a CTA
 constexpr int kRChunk = 512;          // rows of x in shared memory at a time
 constexpr int kRRows = 8;             // rows of W_r that a thread asks for at once
-constexpr int kRArrive = 8;           // first arrival counter: zero between calls
-static_assert(MOE_LAYER16_MAX_T <= kRTokens * 8, "an arrival counter for every kRTokens tokens");
+static_assert(MOE_LAYER16_MAX_T <= kRTokens * kL16Arrive, "an arrival counter for every kRTokens tokens");
 
 struct RoutePlan {
   int tt;               // tokens a CTA
@@ -98,7 +97,7 @@ __global__ void __launch_bounds__(kRThreads) k_l16_route(const RouteArgs16 r) {
   // the products' counters, which the kernel behind this one starts from
   int32_t* counters = reinterpret_cast<int32_t*>(a.ws);
   if (blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0)
-    if (tid < kRArrive || (tid >= kRArrive + 8 && tid < kCounters)) counters[tid] = 0;
+    if (tid < kCounters) counters[tid] = 0;
   if (!a.W_r && !a.logits) return;
   const int t0 = blockIdx.z * TT, nt = min(TT, a.T - t0);
   const int64_t set = (int64_t)TT * p.ep;
@@ -168,9 +167,9 @@ __global__ void __launch_bounds__(kRThreads) k_l16_route(const RouteArgs16 r) {
     __threadfence();
     __syncthreads();
     if (tid == 0) {
-      const int old = atom_add_acq_rel_gpu(&counters[kRArrive + blockIdx.z], 1);
+      const int old = atom_add_acq_rel_gpu(&a.arrive[blockIdx.z], 1);
       last = old == p.ks * p.et - 1;
-      if (last) counters[kRArrive + blockIdx.z] = 0;
+      if (last) a.arrive[blockIdx.z] = 0;
     }
     __syncthreads();
     if (!last) return;

@@ -442,9 +442,12 @@ struct Layer16Args {
   const void* w2; int64_t g2, ld2;
   void* out; int64_t ldo;
   int32_t* ids; float* w;
-  uint8_t* ws;                  // past the status word
+  uint8_t* ws;                  // past the status word's block; scratch
   int32_t* status;
+  int32_t* arrive;              // [kL16Arrive] zero between calls: next to the status word, where no operator
+                                // that shares the workspace writes
 };
+constexpr int kL16Arrive = 8;
 int64_t layer16_ws_bytes(int T, int H, int I, int E, int k, int S);
 cudaError_t launch_layer16(const Layer16Args& a, cudaStream_t st);
 

@@ -314,6 +314,21 @@ def test_layer16_of_a_trained_block():
         P.assert_within(out, *one, "one token")
 
 
+@pytest.mark.parametrize("T", [1, 3, 20, 64])
+def test_layer16_shares_its_workspace(T):
+    """Behind the status word's block the workspace holds nothing between calls: what another product left there does no harm."""
+    cuda_device()
+    c = _inputs(T, 264, 136, 12, 3, 1, "swiglu", BF16, False, 0)
+    _run(c, "swiglu", 1, W_r=c["W_r"])
+    first = c["out"].clone()
+    for v in (0x7f, 0xff, 1):
+        c["ws"][256:] = v
+        c["out"].fill_(NAN)
+        _run(c, "swiglu", 1, W_r=c["W_r"])
+        assert torch.equal(c["out"], first)
+        assert m.moe_mm_read_status(c["ws"]) == 0
+
+
 def test_layer16_no_tokens():
     cuda_device()
     c = _inputs(1, 64, 64, 4, 2, 0, "swiglu", BF16, False, 0)
