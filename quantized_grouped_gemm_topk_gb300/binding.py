@@ -460,13 +460,13 @@ def _flat(t, name, dtypes, shape, dev):
         return None
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
+    if t.shape == shape and t.dtype in dtypes and t.get_device() == dev:
+        return t.data_ptr()
     return _arg(t, name, dtypes, shape, dev)
 
 
-def _ld(t, name, whole=1):
-    """Stride between the rows of t (axis -2), in elements. A single row has none: its length, rounded up to `whole`."""
-    rows, cols = t.shape[-2:]
-    ld = t.stride(-2)
+def _apart(name, rows, cols, ld, whole):
+    """ld, the stride between rows, in elements. A single row has none: its length, rounded up to `whole`."""
     if rows <= 1:
         return -(-max(cols, ld) // whole) * whole
     if ld < cols:
@@ -474,9 +474,14 @@ def _ld(t, name, whole=1):
     return ld
 
 
+def _ld(t, name, whole=1):
+    """_apart of the rows of t (axis -2)."""
+    return _apart(name, *t.shape[-2:], t.stride(-2), whole)
+
+
 def _group(t):
     """Stride between the matrices of t [G, rows, cols]; ignored by the library for one group."""
-    return t.stride(0) if t.shape[0] > 1 else 0
+    return t.stride()[0] if t.shape[0] > 1 else 0
 
 
 def _dims(t, name, n):
@@ -490,7 +495,7 @@ def _ws(ws, dev):
         return None, 0
     if ws.get_device() != dev or not ws.is_contiguous():
         raise ValueError("ws must be a contiguous buffer on the current CUDA device")
-    return ws.data_ptr(), ws.numel() * ws.element_size()
+    return ws.data_ptr(), ws.nbytes
 
 
 def moe_layer_norm_workspace_size(T, H) -> int:
@@ -655,9 +660,7 @@ def _mat(t, name, dtypes, shape, dev, whole=1):
     st = t.stride()
     if t.shape != shape or t.dtype not in dtypes or t.get_device() != dev or st[-1] != 1:
         return _arg(t, name, dtypes, shape, dev), _ld(t, name, whole)
-    if shape[-2] > 1 and st[-2] >= shape[-1]:
-        return t.data_ptr(), st[-2]
-    return t.data_ptr(), _ld(t, name, whole)
+    return t.data_ptr(), _apart(name, shape[-2], shape[-1], st[-2], whole)
 
 
 def _opt(t, name, dtypes, shape, dev, whole=1):

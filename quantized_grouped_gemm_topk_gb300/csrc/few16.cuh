@@ -5,7 +5,8 @@
 
 namespace moe {
 
-// Most rows of the dense product, and most CTAs of the layer.
+// Most rows of the dense product here, and most CTAs of the layer (for which the
+// workspace has places).
 constexpr int kFewRows = 256;
 constexpr int kFewSms = 152;
 

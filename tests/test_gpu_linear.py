@@ -305,6 +305,48 @@ def test_linear_on_another_stream_and_in_graphs_that_share_a_workspace():
             assert torch.equal(out, want)
 
 
+def test_linear_backward_on_another_stream_and_in_graphs_that_share_a_workspace():
+    """Sizes whose products take different kernels, their partial sums in the same places."""
+    cuda_device()
+    sizes = ((20, 2048, 264, "silu"), (2100, 300, 136, "swiglu"), (700, 520, 640, "none"))
+    ws = torch.zeros(max(m.moe_linear_workspace_size(R, D.halves(act) * N, K, True) for R, N, K, act in sizes), dtype=torch.uint8,
+                     device="cuda")
+    sets, graphs = [], []
+    for R, N, K, act in sizes:
+        x, w, dout, z, dz, *want, _ = _backward(R, N, K, act, BF16)
+        sets.append(((dout, x, w, z, dz), want, [torch.zeros_like(t) for t in want], act))
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+
+    def each(i):
+        args, want, got, act = sets[i]
+        for t in got:
+            t.fill_(NAN)
+        yield
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+    def call(i):
+        args, _, got, act = sets[i]
+        m.moe_linear_backward(*args, *got, ws, act=act, alpha=ALPHA, limit=LIMIT)
+
+    for i in range(len(sets)):
+        for _ in each(i):
+            torch.cuda.synchronize()
+            with torch.cuda.stream(side):
+                call(i)
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            call(i)
+        graphs.append(graph)
+    for _ in range(2):
+        for i, graph in enumerate(graphs):
+            for _ in each(i):
+                graph.replay()
+            for _ in each(i):
+                call(i)
+
+
 def _needs_gb(n):
     if torch.cuda.get_device_properties(0).total_memory < n << 30:
         pytest.skip(f"needs {n} GB")
