@@ -4,7 +4,9 @@
 // The router's product x . W_r streams W_r [H, E] fp32 once for every eight
 // tokens: the reduction is cut into slices, a CTA each, whose partial sums the last
 // CTA to arrive (of those eight tokens') adds in order and routes. 1 x 7168 x 256:
-// latency, not the 7.3 MB; so all of a thread's rows are asked for at once.
+// latency, not the 7.3 MB; so all of a thread's rows are asked for at once, and a small
+// product is one CTA's, without a join. Launch to launch the router takes 2.4 us of a
+// layer where one CTA does it, 5 to 7 else.
 #include "few16.cuh"
 
 namespace moe {
@@ -13,7 +15,7 @@ static int64_t al256(int64_t v) { return (v + 255) / 256 * 256; }
 
 constexpr int kRThreads = 512;
 constexpr int kRTokens = 8;           // most tokens of a CTA
-constexpr int kRChunk = 512;          // rows of x in shared memory at a time
+constexpr int kRChunk = 4096;         // values of x in shared memory at a time
 constexpr int kRRows = 8;             // rows of W_r that a thread asks for at once
 static_assert(MOE_LAYER16_MAX_T <= kRTokens * kL16Arrive, "an arrival counter for every kRTokens tokens");
 
@@ -36,6 +38,10 @@ static RoutePlan route_plan(int T, int H, int E) {
   // the last CTA reads in about 40 loads a thread
   const int items = p.tt * (p.ep / 4);
   p.ks = std::max(1, std::min({kFewSms / (p.z * p.et), H / 16, 40 * kRThreads / items}));
+  // One CTA alone where it asks for all rows at once and needs no join: the layer of 1
+  // token, 256 x 128 x 8, 15.4 us against 18.3; 1 x 2048 x 8 21.1, 24.0; 8 x 256 x 64 40.1, 41.4. Where
+  // it needs more rounds, it is the slower: 8 x 1024 x 8 30.9, 28.8; 1 x 1024 x 64 no gain.
+  if (p.et == 1 && H <= kRRows * (kRThreads / p.quads) && H * p.tt <= kRChunk) p.ks = 1;
   return p;
 }
 // Floats of partial sums that suffice for T tokens and any fewer.
@@ -88,7 +94,8 @@ __device__ __forceinline__ float4 sum_parts(const float* p, int n, int64_t step)
 template <typename E, int TT>
 __global__ void __launch_bounds__(kRThreads) k_l16_route(const RouteArgs16 r) {
   extern __shared__ __align__(16) uint8_t rsm[];
-  __shared__ float xs[kRChunk * TT];
+  __shared__ float xs[kRChunk];
+  constexpr int kRows = kRChunk / TT;
   __shared__ int last;
   const Layer16Args& a = r.a;
   const RoutePlan& p = r.p;
@@ -102,6 +109,14 @@ __global__ void __launch_bounds__(kRThreads) k_l16_route(const RouteArgs16 r) {
   const int t0 = blockIdx.z * TT, nt = min(TT, a.T - t0);
   const int64_t set = (int64_t)TT * p.ep;
   float* part = r.part + blockIdx.z * p.ks * set;
+  const bool alone = a.W_r && p.ks * p.et == 1;
+  uint32_t* keys = reinterpret_cast<uint32_t*>(rsm);          // [nt][ep] of the logits
+  const int q4 = p.ep / 4;
+  bool nan_seen = false;
+  auto key = [&](float v) {
+    nan_seen |= v != v;
+    return logit_key(v != v ? -INFINITY : v);
+  };
 
   if (a.W_r) {
     // ---- a slice of the product ----
@@ -110,8 +125,8 @@ __global__ void __launch_bounds__(kRThreads) k_l16_route(const RouteArgs16 r) {
     const int h0 = (int)((int64_t)a.H * blockIdx.x / p.ks), h1 = (int)((int64_t)a.H * (blockIdx.x + 1) / p.ks);
     const bool vec = a.E % 4 == 0 && ((uintptr_t)a.W_r & 15) == 0;
     float acc[TT][4] = {};
-    for (int hb = h0; hb < h1; hb += kRChunk) {
-      const int n = min(kRChunk, h1 - hb);
+    for (int hb = h0; hb < h1; hb += kRows) {
+      const int n = min(kRows, h1 - hb);
       __syncthreads();
       for (int i = tid; i < n * TT; i += kRThreads) {
         const int t = i / n, h = i - t * n;
@@ -158,33 +173,44 @@ __global__ void __launch_bounds__(kRThreads) k_l16_route(const RouteArgs16 r) {
       for (int t = 0; t < TT; ++t)
         *reinterpret_cast<float4*>(red + (my * TT + t) * width + 4 * tq) = make_float4(acc[t][0], acc[t][1], acc[t][2], acc[t][3]);
     __syncthreads();
-    for (int o = tid; o < TT * width; o += kRThreads) {
+    constexpr int kOwn = (TT * 256 + kRThreads - 1) / kRThreads;
+    float own[kOwn];                                          // a thread's sums
+#pragma unroll
+    for (int i = 0; i < kOwn; ++i) {
+      const int o = tid + i * kRThreads;
+      own[i] = 0.f;
+      if (o >= TT * width) break;
       const int t = o / width, e = blockIdx.y * width + o - t * width;
       float v = red[o];
       for (int l = 1; l < lanes; ++l) v += red[l * TT * width + o];
-      if (e < p.ep) part[blockIdx.x * set + (int64_t)t * p.ep + e] = v;
+      own[i] = v;
+      if (!alone && e < p.ep) part[blockIdx.x * set + (int64_t)t * p.ep + e] = v;
     }
-    __threadfence();
-    __syncthreads();
-    if (tid == 0) {
-      const int old = atom_add_acq_rel_gpu(&a.arrive[blockIdx.z], 1);
-      last = old == p.ks * p.et - 1;
-      if (last) a.arrive[blockIdx.z] = 0;
+    if (alone) {
+      __syncthreads();                                        // the keys lie where the sums' parts did
+#pragma unroll
+      for (int i = 0; i < kOwn; ++i) {
+        const int o = tid + i * kRThreads;
+        if (o >= TT * width) break;
+        const int t = o / width, e = o - t * width;
+        if (t < nt && e < p.ep) keys[t * p.ep + e] = e < a.E ? key(own[i]) : 0u;
+      }
+    } else {
+      __threadfence();
+      __syncthreads();
+      if (tid == 0) {
+        const int old = atom_add_acq_rel_gpu(&a.arrive[blockIdx.z], 1);
+        last = old == p.ks * p.et - 1;
+        if (last) a.arrive[blockIdx.z] = 0;
+      }
+      __syncthreads();
+      if (!last) return;
+      __threadfence();
     }
-    __syncthreads();
-    if (!last) return;
-    __threadfence();
   }
 
-  // ---- the last CTA: keys [nt][ep] of the logits, then a warp a token ----
-  uint32_t* keys = reinterpret_cast<uint32_t*>(rsm);
-  const int q4 = p.ep / 4;
-  bool nan_seen = false;
-  auto key = [&](float v) {
-    nan_seen |= v != v;
-    return logit_key(v != v ? -INFINITY : v);
-  };
-  if (a.W_r) {
+  // ---- the only or last CTA: keys of the logits, then a warp a token ----
+  if (a.W_r && !alone) {
     const int items = nt * q4;
     int split = 1;                                            // threads an item
     while (2 * split * items <= kRThreads && 2 * split <= p.ks) split *= 2;
@@ -205,7 +231,7 @@ __global__ void __launch_bounds__(kRThreads) k_l16_route(const RouteArgs16 r) {
 #pragma unroll
       for (int j = 0; j < 4; ++j) keys[4 * it + j] = e + j < a.E ? key(f[j]) : 0u;
     }
-  } else {
+  } else if (!a.W_r) {
     for (int i = tid; i < nt * p.ep; i += kRThreads) {
       const int t = i / p.ep, e = i - t * p.ep;
       keys[i] = e < a.E ? key(a.logits[(int64_t)(t0 + t) * a.E + e]) : 0u;

@@ -314,6 +314,14 @@ def test_layer16_of_a_trained_block():
         P.assert_within(out, *one, "one token")
 
 
+# the router in one CTA and in slices: eight rows a thread, 4096 values of x
+@pytest.mark.parametrize("T,H,E,k", [(1, 2048, 8, 2), (1, 2049, 8, 2), (1, 4096, 3, 3), (2, 2048, 4, 1), (2, 2056, 4, 1), (3, 1024, 13, 5),
+                                     (4, 1025, 13, 5), (8, 512, 30, 4), (9, 513, 30, 4), (33, 64, 256, 8), (64, 65, 256, 8), (64, 64, 257, 8),
+                                     (5, 8, 100, 32), (64, 1, 1, 1)])
+def test_layer16_routers(T, H, E, k):
+    _layer(T, H, 24, E, k, 0, "swiglu", BF16, False)
+
+
 @pytest.mark.parametrize("T", [1, 3, 20, 64])
 def test_layer16_shares_its_workspace(T):
     """Behind the status word's block the workspace holds nothing between calls: what another product left there does no harm."""
