@@ -105,7 +105,9 @@ __device__ __forceinline__ void copy_rows(uint32_t dst, int half_bytes, const CU
 // the same columns for all, whose rows lie a fixed distance apart (64 tokens, 2880 x
 // 2880 x 128 experts 804 -> 789 us). Not by CTA: which one takes a range varies, and
 // sums must not.
-__device__ __forceinline__ int first_stage(int s, int ns) { return (int)((uint32_t)s * 5u % (uint32_t)ns); }
+__device__ __forceinline__ int first_stage(int s, int ns) {
+  return (int)(((uint32_t)s * 40503u & 0xffffu) * (uint32_t)ns >> 16);      // the fraction of s times the golden ratio
+}
 // Most 64s of a reduction of K that a stage should hold (an even number): an eighth,
 // so that a short reduction is shared among the issuers too.
 __host__ __device__ __forceinline__ int stage_halves(int K) { return 2 * (1 + K / (16 * kFH)); }
@@ -203,17 +205,21 @@ __device__ __forceinline__ int box_of(int n) { return n <= 8 ? 0 : n <= 16 ? 1 :
 // ---- the routed layer ---------------------------------------------------------------
 // A tile: `len` features from f0 of group e, copied in boxes of `box` (gated: of
 // each half): arows rows of the MMA's operand A. rows: of B that are copied; N: the
-// MMA's. hs: 64s of the reduction a stage, an even number.
+// MMA's. hs: 64s of the reduction a stage, an even number; ns: stages. Every role finds
+// its tiles by itself, so no division is among the steps to the next one.
 struct FewTile {
-  int e, f0, len, box, arows, rows, N, hs;
+  int e, f0, len, bi, box, arows, rows, N, hs, ns;
 };
-// Runs through the tiles of a range. First product: features at .. end of all
-// groups' one after the other, up to 64 (gated) or 128 a tile. Second: features of
-// H, up to 128 (the map's box) a tile, all groups, or one of g.S2 parts of them, for each.
+// Runs through the tiles of a range, of `left` features from f0 of the g-th group. First
+// product: over all groups' features one after the other, up to 64 (gated) or 128 a tile. Second: over
+// features of H, up to 128 (the map's box) a tile, for each all groups [g0, g1), or one of g.S2 parts of them.
 struct FewRange {
-  int64_t at, end;
-  int g, g0, g1;        // second: groups [g0, g1), the next one
+  int f0, left, g, g0, g1;
 };
+// a / b of a < 2^39 or so, mostly of 32 bits.
+__device__ __forceinline__ int64_t div_short(int64_t a, int b) {
+  return a < (1ll << 32) ? (int64_t)((uint32_t)a / (uint32_t)b) : a / b;
+}
 
 template <typename E>
 __global__ void __launch_bounds__(kFThreads, 1) k_few_layer(const FewArgs g, const __grid_constant__ FewMaps maps) {
@@ -345,39 +351,52 @@ __global__ void __launch_bounds__(kFThreads, 1) k_few_layer(const FewArgs g, con
     return *reinterpret_cast<volatile int*>(&queue[n % kFQueue]);
   };
   auto range_of = [&](int s) -> FewRange {
-    if (s < P1) return {total1 * s / P1, total1 * (s + 1) / P1, 0, 0, 0};
-    const int j = (s - P1) / g.S2, part = (s - P1) % g.S2, g0 = ng * part / g.S2;
-    return {(int64_t)g.F2 * j / g.Pf, (int64_t)g.F2 * (j + 1) / g.Pf, g0, g0, ng * (part + 1) / g.S2};
+    if (s < P1) {
+      const int64_t at = div_short(total1 * s, P1), gi = div_short(at, g.F1);
+      return {(int)(at - gi * g.F1), (int)(div_short(total1 * (s + 1), P1) - at), (int)gi, 0, 0};
+    }
+    // F2 <= 2^20, at most kFewSms ranges
+    const int j = (s - P1) / g.S2, part = (s - P1) % g.S2, g0 = ng * part / g.S2, f0 = g.F2 * j / g.Pf;
+    return {f0, g.F2 * (j + 1) / g.Pf - f0, g0, g0, ng * (part + 1) / g.S2};
   };
   auto next_tile = [&](bool second, FewRange& r, FewTile& t) -> bool {
-    if (r.at >= r.end) return false;
+    if (r.left <= 0) return false;
+    t.f0 = r.f0;
     if (!second) {
-      const int gi = (int)(r.at / g.F1);
-      t.e = glist[gi];
-      t.f0 = (int)(r.at - (int64_t)gi * g.F1);
+      t.e = glist[r.g];
       // of the range in this group; the last two tiles alike, so that neither is narrow
-      const int left = (int)min((int64_t)(g.F1 - t.f0), r.end - r.at), step = g.rows1 / 8;
-      t.len = left >= 2 * g.rows1 ? g.rows1 : left > g.rows1 ? (left / 2 + step - 1) / step * step : left;
-      t.box = (t.len + step - 1) / step * step;
-      r.at += t.len;
+      const int sh = gated ? 3 : 4, left = min(g.F1 - r.f0, r.left), step = 1 << sh;
+      t.len = left >= 2 * g.rows1 ? g.rows1 : left > g.rows1 ? ((left >> 1) + step - 1) >> sh << sh : left;
+      t.bi = (t.len - 1) >> sh;
+      t.box = (t.bi + 1) << sh;
+      r.left -= t.len;
+      r.f0 += t.len;
+      if (r.f0 == g.F1) {
+        r.f0 = 0;
+        ++r.g;
+      }
       t.arows = gated ? 2 * t.box : t.box;
       t.rows = g.xrows;
       t.N = g.N;
+      t.hs = g.hs1[t.bi];
+      t.ns = g.ns1[t.bi];
     } else {
       if (r.g0 == r.g1) return false;
       t.e = glist[r.g];
-      t.f0 = (int)r.at;
-      t.len = (int)min((int64_t)g.box2, r.end - r.at);
+      t.len = min(g.box2, r.left);
       t.box = t.arows = g.box2;
       if (++r.g == r.g1) {
         r.g = r.g0;
-        r.at += t.len;
+        r.f0 += t.len;
+        r.left -= t.len;
       }
       const int m = __popcll(mask[t.e]);
-      t.rows = 8 << box_of(m);
+      t.bi = box_of(m);
+      t.rows = 8 << t.bi;
       t.N = (m + 15) & ~15;
+      t.hs = g.hs2[t.bi];
+      t.ns = g.ns2[t.bi];
     }
-    t.hs = g.slot / (256 * (t.arows + t.rows)) * 2;
     return true;
   };
 
@@ -401,8 +420,8 @@ __global__ void __launch_bounds__(kFThreads, 1) k_few_layer(const FewArgs g, con
         FewTile t;
         while (ok && next_tile(second, r, t)) {
           const int half = t.arows * 128, hs = t.hs;
-          const CUtensorMap* map = second ? &maps.a2 : &maps.a[t.box / (g.rows1 / 8) - 1];
-          const int ns = (nh + hs - 1) / hs;
+          const CUtensorMap* map = second ? &maps.a2 : &maps.a[t.bi];
+          const int ns = t.ns;
           for (int i = 0, h = first_stage(s, ns) * hs; i < ns; ++i, h = h + hs < nh ? h + hs : 0) {
             if (!tc::bar_wait(empty_u + 8 * slot, phase, abort)) { ok = false; break; }
             const int left = min(hs, nh - h), n_h = chunks ? (left + 1) & ~1 : left;
@@ -449,9 +468,9 @@ __global__ void __launch_bounds__(kFThreads, 1) k_few_layer(const FewArgs g, con
         while (ok && next_tile(second, r, t)) {
           // behind the stage's weights
           const int hs = t.hs, a_bytes = hs * t.arows * 128, half = t.rows * 128;
-          const CUtensorMap* map = second ? &maps.y[box_of(t.rows)] : &maps.x;
+          const CUtensorMap* map = second ? &maps.y[t.bi] : &maps.x;
           const int r0 = second ? rowof[t.e] : 0;
-          const int ns = (nh + hs - 1) / hs;
+          const int ns = t.ns;
           for (int i = 0, h = first_stage(s, ns) * hs; i < ns; ++i, h = h + hs < nh ? h + hs : 0) {
             if (!tc::bar_wait(empty_u + 8 * slot, phase, abort)) { ok = false; break; }
             const int left = min(hs, nh - h), n_h = chunks ? (left + 1) & ~1 : left;
@@ -490,7 +509,7 @@ __global__ void __launch_bounds__(kFThreads, 1) k_few_layer(const FewArgs g, con
         tc::fence_after_sync();
         const uint32_t a_step = uni(t.arows * 8), b_step = uni(t.rows * 8), hs = uni(t.hs), wide = uni(t.N);
         const uint32_t idesc = tc::idesc_16bit(a_step <= 64 * 8 ? 64 : kFM, wide, g.dtype == MOE_DT_BF16, 0, 0), dt = tm + d * 4 * ncol;
-        const uint32_t b_off = hs * a_step, ns = ((uint32_t)nh + hs - 1) / hs;
+        const uint32_t b_off = hs * a_step, ns = uni(t.ns);
         uint32_t acc = 0;
         for (uint32_t i = 0, h = uni(first_stage(s, ns)) * hs; i < ns; ++i) {
           if (!__all_sync(kFull, tc::bar_wait(bars + 8 * slot, phase, abort))) { ok = false; break; }
@@ -535,7 +554,7 @@ __global__ void __launch_bounds__(kFThreads, 1) k_few_layer(const FewArgs g, con
       const bool second = s >= P1;
       FewRange r = range_of(s);
       FewTile t;
-      const int h0 = (int)r.at, nf = (int)(r.end - r.at);      // second: the range
+      const int h0 = r.f0, nf = r.left;         // second: the range
       if (second && r.g0 == r.g1) {
         // no group, nothing to add
         if (g.S2 == 1) {
@@ -549,7 +568,8 @@ __global__ void __launch_bounds__(kFThreads, 1) k_few_layer(const FewArgs g, con
         const int d = tiles & 1;
         const bool got = tc::mbar_wait(&accfull[d], (tiles >> 1) & 1, abort);
         ++tiles;
-        if (!epi_all<1, 128>(got)) { ok = false; break; }
+        // the second product's warps meet at the end of the range only
+        if (!(second ? __all_sync(kFull, got) != 0 : epi_all<1, 128>(got))) { ok = false; break; }
         tc::fence_after_sync();
         const uint32_t acc = lanes + d * 4 * ncol;
         auto release = [&] {
@@ -632,6 +652,7 @@ __global__ void __launch_bounds__(kFThreads, 1) k_few_layer(const FewArgs g, con
             }
         }
       }
+      if (second) ok = epi_all<1, 128>(ok);
       if (ok && !second) {
         // the range's rows are in memory, for the tensor copies of any CTA
         __threadfence();
@@ -964,6 +985,12 @@ cudaError_t launch_few_layer(FewArgs g, const void* x, int64_t ldx, const void* 
   int box_t = 8;                                    // rows of the second product's widest copy
   while (box_t < g.R) box_t *= 2;
   g.slot = 2 * 128 * std::max(kFM + g.xrows, g.box2 + box_t);
+  auto stages = [&](int rows, int64_t K, int& hs, int& ns) {
+    hs = g.slot / (256 * rows) * 2;
+    ns = (int)up(up(K, kFH), hs);
+  };
+  for (int i = 0; i < 8; ++i) stages(16 * (i + 1) + g.xrows, g.K1, g.hs1[i], g.ns1[i]);      // halves * step * (i + 1) rows
+  for (int i = 0; i < 4; ++i) stages(g.box2 + std::min(8 << i, box_t), g.K2, g.hs2[i], g.ns2[i]);
   const int head = kFBars + 16 * kFM * 4 + 4 * (g.R * g.box2 + 2) + 12 * G + 4 * std::min(G, A + g.S) + 4 * (A + g.S * g.R) + 8 * A;
   g.head = (head + 1023) / 1024 * 1024;
   // An MMA of 64 or 128 rows reads past the rows that were copied, of A and of B (16

@@ -39,6 +39,7 @@ struct FewArgs {
   int Pf, S2;                 // layer: ranges of the second product's features, parts of the groups for each
   int xrows, box2;            // layer: rows of x a copy takes, features of the second product's tiles
   int slot;                   // bytes of a stage
+  int hs1[8], ns1[8], hs2[4], ns2[4];   // layer: 64s of the reduction a stage and stages, by the tile's copies
 };
 cudaError_t launch_few_layer(FewArgs g, const void* x, int64_t ldx, const void* w1, int64_t g1, int64_t ld1, const void* w2,
                              int64_t g2, int64_t ld2, cudaStream_t st);
