@@ -41,10 +41,11 @@
 // returns.
 //
 // Measured, in us, behind the router (bf16, SwiGLU; in brackets the bytes that the
-// tokens' experts need, at 6775 GB/s): 1 token x 7168 x 2048, 8 of 256 experts 114
-// (105); 8 tokens 699 (748 for that many at random, fewer were drawn); 16 tokens x
-// 2880 x 2880, 4 of 128, 370 (375); 64 tokens x 7168 x 2048, 8 of 64, 881 (832); 1 token x
-// 2880 x 2880, 4 of 128, 45 (29); 1 token x 256 x 128, 2 of 8, 12.8 (latency). With
+// tokens' experts need, at 6775 GB/s): 1 token x 7168 x 2048, 8 of 256 experts 113
+// (105); 8 tokens 692 (748 for that many at random, fewer were drawn); 16 tokens x
+// 2880 x 2880, 4 of 128, 365 (375); x 4096 x 512, 8 of 256, 199 (190); 64 tokens x 7168 x 2048, 8 of
+// 64, 832 (832); x 2048 x 768, 8 of 128, 193 (176); 1 token x 2880 x 2880, 4 of 128, 44 (29); 1 token x
+// 256 x 128, 2 of 8, 11.7 (latency). With
 // 16 tokens and 24 experts the memory reads 1.015 times the weights' bytes, at 74 %
 // of its time, the tensor pipe is 7 % busy.
 #include <cmath>
@@ -247,6 +248,7 @@ __global__ void __launch_bounds__(kFThreads, 1) k_few_layer(const FewArgs g, con
   float* wrow = reinterpret_cast<float*>(glist + min(G, A + g.S));  // [rows] routing weight
   int* sid = reinterpret_cast<int*>(wrow + A + g.S * g.R);          // [A] the ids, -1: left out
   float* swt = reinterpret_cast<float*>(sid + A);                   // [A] their weights
+  uint8_t* tokof = reinterpret_cast<uint8_t*>(swt + A);             // [rows] token
   uint8_t* ring = base + g.head;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
@@ -315,7 +317,10 @@ __global__ void __launch_bounds__(kFThreads, 1) k_few_layer(const FewArgs g, con
       if (mask[e]) glist[il++] = e;
       const int m = __popcll(mask[e]);
       if (e >= g.E)
-        for (int i = 0; i < m; ++i) wrow[ir + i] = 1.f;
+        for (int i = 0; i < m; ++i) {
+          wrow[ir + i] = 1.f;
+          tokof[ir + i] = (uint8_t)i;
+        }
       ir += m;
     }
     if (tid == kFThreads - 1) tmp[0] = il;
@@ -334,7 +339,11 @@ __global__ void __launch_bounds__(kFThreads, 1) k_few_layer(const FewArgs g, con
         if (i < a) first = false;
         w += swt[i];
       }
-    if (first) wrow[rowof[e] + __popcll(mask[e] & ((1ull << t) - 1))] = w;
+    if (first) {
+      const int r = rowof[e] + __popcll(mask[e] & ((1ull << t) - 1));
+      wrow[r] = w;
+      tokof[r] = (uint8_t)t;
+    }
   }
   const int ng = tmp[0];
   const uint32_t tmem = *tmem_slot;
@@ -632,19 +641,27 @@ __global__ void __launch_bounds__(kFThreads, 1) k_few_layer(const FewArgs g, con
           // a thread's feature is its own throughout: its sums need no barrier
           const bool mine = row < t.len;
           if (mine && t.e == glist[r.g0])
+#pragma unroll 8
             for (int i = 0; i < g.R; ++i) sums[i * g.box2 + row] = 0.f;
+          const uint8_t* tok = tokof + rowof[t.e];
           for (int i0 = 0; i0 < m; i0 += kFCols) {
+            // the sums (of tokens that differ) are asked for together, and in front of the accumulators
+            float* at[kFCols];
+            float u[kFCols];
+#pragma unroll
+            for (int i = 0; i < kFCols; ++i) {
+              at[i] = sums + tok[min(i0 + i, m - 1)] * g.box2 + (mine ? row : 0);
+              u[i] = *at[i];
+            }
             uint32_t v[kFCols];
             add_columns<kFCols>(v, acc + i0, ncol);
+            if (i0 + kFCols >= m) release();
 #pragma unroll
             for (int i = 0; i < kFCols; ++i)
-              if (i0 + i < m) {
-                const int tok = next_bit(rem);
-                if (mine) sums[tok * g.box2 + row] += __uint_as_float(v[i]);
-              }
+              if (mine && i0 + i < m) *at[i] = u[i] + __uint_as_float(v[i]);
           }
-          release();
           if (mine && t.e == glist[r.g1 - 1])
+#pragma unroll 8
             for (int i = 0; i < g.R; ++i) {
               const float v = sums[i * g.box2 + row];
               if (g.S2 == 1) reinterpret_cast<uint16_t*>(g.out)[i * g.ldo + t.f0 + row] = E::from(v);
@@ -669,11 +686,28 @@ __global__ void __launch_bounds__(kFThreads, 1) k_few_layer(const FewArgs g, con
         epi_sync();
         if (*reinterpret_cast<volatile int*>(&tmp[0])) {
           __threadfence();
-          for (int i = et; i < g.R * nf; i += 128) {
-            const int t = i / nf, h = i - t * nf;
-            float v = 0.f;
-            for (int w = 0; w < g.S2; ++w) v += __ldcg(g.part + ((int64_t)(j * g.S2 + w) * g.R + t) * g.box2 + h);
-            reinterpret_cast<uint16_t*>(g.out)[t * g.ldo + h0 + h] = E::from(v);
+          // eight at a time, whose loads are all asked for before the first sum
+          const float* set = g.part + (int64_t)j * g.S2 * g.R * g.box2;
+          for (int i0 = et; i0 < g.R * nf; i0 += 8 * 128) {
+            float v[8];
+            int t[8], h[8];
+#pragma unroll
+            for (int u = 0; u < 8; ++u) {
+              const int i = min(i0 + u * 128, g.R * nf - 1);
+              t[u] = i / nf;
+              h[u] = i - t[u] * nf;
+              v[u] = __ldcg(set + t[u] * g.box2 + h[u]);
+            }
+            for (int w = 1; w < g.S2; ++w) {
+              float p[8];
+#pragma unroll
+              for (int u = 0; u < 8; ++u) p[u] = __ldcg(set + (w * g.R + t[u]) * g.box2 + h[u]);
+#pragma unroll
+              for (int u = 0; u < 8; ++u) v[u] += p[u];
+            }
+#pragma unroll
+            for (int u = 0; u < 8; ++u)
+              if (i0 + u * 128 < g.R * nf) reinterpret_cast<uint16_t*>(g.out)[t[u] * g.ldo + h0 + h[u]] = E::from(v[u]);
           }
         }
       }
@@ -967,36 +1001,53 @@ cudaError_t launch_few_layer(FewArgs g, const void* x, int64_t ldx, const void* 
   g.N = (g.R + 15) & ~15;
   g.xrows = (g.R + 7) & ~7;
   g.rows1 = kFM / halves;
-  // The second product's ranges, with all groups or 1 / S2 of them: the time of the
-  // halves (130 cycles of MMA issue and barriers, or the copies of their rows) and
-  // of the join. Groups that some token chooses, when each chooses k at random.
-  const double touched = g.E * (1 - std::pow(1 - (double)g.k / g.E, g.R)) + g.S;
-  double least = 1e300;
-  for (int S2 = 1; S2 <= 4; S2 *= 2) {
-    const int Pf = (int)std::min<int64_t>(grid / S2, up(g.F2, kFLeast)), f = (int)up(g.F2, Pf);
-    if (S2 > 1 && f > kFM) break;
-    const double cost = touched / S2 * up(g.K2, kFH) * std::max(150.0, 128.0 * f / 23.5) * up(f, kFM) + (S2 > 1 ? 5000 : 0);
-    if (cost < least) {
-      least = cost;
-      g.S2 = S2; g.Pf = Pf;
-      g.box2 = std::min(kFM, (f + 7) & ~7);
-    }
-  }
   int box_t = 8;                                    // rows of the second product's widest copy
   while (box_t < g.R) box_t *= 2;
-  g.slot = 2 * 128 * std::max(kFM + g.xrows, g.box2 + box_t);
+  // Bytes of a stage, of what stands in front of the ring, and its stages, by the
+  // features of the second product's tiles. An MMA of 64 or 128 rows reads past the rows that were
+  // copied, of A and of B (16 where 8 were): within the stage but for its last halves, where the tile is narrow.
+  const int pad = 128 * 64;
+  auto layout = [&](int box2) {
+    const int head = kFBars + 16 * kFM * 4 + 4 * (g.R * box2 + 2) + 12 * G + 4 * std::min(G, A + g.S) + 5 * (A + g.S * g.R) + 8 * A;
+    g.box2 = box2;
+    g.slot = 2 * 128 * std::max(kFM + g.xrows, box2 + box_t);
+    g.head = (head + 1023) / 1024 * 1024;
+    g.stages = std::min(kFMaxStages, (kFSmem - 1024 - g.head - pad) / g.slot);
+  };
   auto stages = [&](int rows, int64_t K, int& hs, int& ns) {
     hs = g.slot / (256 * rows) * 2;
     ns = (int)up(up(K, kFH), hs);
   };
+  // The second product's ranges, with all groups or 1 / S2 of them, in cycles: a tile takes
+  // its weights' bytes, the issue of its MMAs and stages, or that of its copies (two 64s of the reduction each where
+  // those are whole), whichever is longest; a split costs the join; a ring of three stages instead of four a tenth.
+  // Groups that some token chooses, when each chooses k at random. Measured, S2 = 1, 2 and 4, in us
+  // behind the router: 16 tokens x 4096 x 512, 8 of 256 experts 239, 202, 204; 64 x 2048 x 1408, 6 of 64 221,
+  // 180, 188; 16 x 2880 x 2880, 4 of 128 403, 373, 380; 64 x 7168 x 2048, 8 of 64 853, 869, -; 64 x 1024 x 256, 8 of
+  // 64 76, 55, 45; 1 x 256 x 128, 2 of 8 11.7, 14.2, 15.0.
+  const double touched = g.E * (1 - std::pow(1 - (double)g.k / g.E, g.R)) + g.S;
+  const double nh = (double)up(g.K2, kFH), copies = g.K2 % kFH ? nh : nh / 2;
+  int rows = 8;                                     // of a tile's copies
+  while (rows < box_t && rows * touched < (double)A + g.S * g.R) rows *= 2;
+  double least = 1e300;
+  int most = 1;
+  for (int S2 = 1; S2 <= 4; S2 *= 2) {
+    const int Pf = (int)std::min<int64_t>(grid / S2, up(g.F2, kFLeast)), f = (int)up(g.F2, Pf);
+    if (S2 > 1 && f > kFM) break;
+    layout(std::min(kFM, (f + 7) & ~7));
+    int hs, ns;
+    stages(g.box2 + rows, g.K2, hs, ns);
+    const double tile = std::max({nh * 128 * std::min((double)g.F2 / Pf, (double)kFM) / 23.5, 600 + 90 * nh + 300 * ns, 150 * copies + 200 * ns});
+    const double cost = touched / S2 * tile * up(f, kFM) * (g.stages < 4 ? 1.1 : 1.) + (S2 > 1 ? 3000 + 1000 * S2 + 6. * g.R * f : 0);
+    if (cost < least) {
+      least = cost;
+      g.S2 = S2; g.Pf = Pf;
+      most = g.box2;
+    }
+  }
+  layout(most);
   for (int i = 0; i < 8; ++i) stages(16 * (i + 1) + g.xrows, g.K1, g.hs1[i], g.ns1[i]);      // halves * step * (i + 1) rows
   for (int i = 0; i < 4; ++i) stages(g.box2 + std::min(8 << i, box_t), g.K2, g.hs2[i], g.ns2[i]);
-  const int head = kFBars + 16 * kFM * 4 + 4 * (g.R * g.box2 + 2) + 12 * G + 4 * std::min(G, A + g.S) + 4 * (A + g.S * g.R) + 8 * A;
-  g.head = (head + 1023) / 1024 * 1024;
-  // An MMA of 64 or 128 rows reads past the rows that were copied, of A and of B (16
-  // where 8 were): within the stage but for its last halves, where the tile is narrow.
-  const int pad = 128 * 64;
-  g.stages = std::min(kFMaxStages, (kFSmem - 1024 - g.head - pad) / g.slot);
   const int smem = 1024 + g.head + g.stages * g.slot + pad;
   FewMaps maps;
   for (int i = 0; i < 8; ++i)
