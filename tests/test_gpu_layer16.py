@@ -314,6 +314,14 @@ def test_layer16_of_a_trained_block():
         P.assert_within(out, *one, "one token")
 
 
+# the second product's groups whole, in halves and in quarters, with one to all tokens a group
+@pytest.mark.parametrize("T,H,I,E,k,S", [(16, 4096, 512, 24, 8, 0), (64, 1024, 256, 16, 8, 1), (64, 4096, 64, 4, 2, 0), (64, 7168, 264, 6, 4, 0),
+                                         (3, 2048, 768, 40, 8, 1), (40, 2880, 520, 9, 3, 0), (64, 300, 72, 2, 2, 1), (17, 512, 2056, 60, 6, 0)])
+@pytest.mark.parametrize("act,dtype", [("swiglu", BF16), ("srelu", F16)])
+def test_layer16_narrow_experts(T, H, I, E, k, S, act, dtype):
+    _layer(T, H, I, E, k, S, act, dtype, False, 8)
+
+
 # the router in one CTA and in slices: eight rows a thread, 4096 values of x
 @pytest.mark.parametrize("T,H,E,k", [(1, 2048, 8, 2), (1, 2049, 8, 2), (1, 4096, 3, 3), (2, 2048, 4, 1), (2, 2056, 4, 1), (3, 1024, 13, 5),
                                      (4, 1025, 13, 5), (8, 512, 30, 4), (9, 513, 30, 4), (33, 64, 256, 8), (64, 65, 256, 8), (64, 64, 257, 8),
