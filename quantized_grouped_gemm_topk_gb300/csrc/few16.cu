@@ -71,7 +71,7 @@ struct FewMaps {
                                       // dense: a[0], the tile's
   CUtensorMap a2;                     // layer: of the second
   CUtensorMap x;                      // rows of the (first) product
-  CUtensorMap y[4];                   // layer: rows of the second, boxes of 8 << i
+  CUtensorMap y[4];                   // layer: rows of the second, boxes of 8 << i, of each part
 };
 
 __device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&v)[8]) {
@@ -101,6 +101,12 @@ __device__ __forceinline__ void copy_rows(uint32_t dst, int half_bytes, const CU
                                           uint32_t bar) {
   for (int h = 0; h < n; h += chunks ? 2 : 1)
     tc::tma_load_3d_at(dst + h * half_bytes, map, chunks ? 0 : k + h * kFH, r0, chunks ? k / kFH + h : 0, bar);
+}
+// Rows of the layer's second product, of both parts.
+__device__ __forceinline__ void copy_y(uint32_t dst, int half_bytes, const CUtensorMap* map, bool chunks, int k, int n, int r0,
+                                       uint32_t bar) {
+  for (int h = 0; h < n; h += chunks ? 2 : 1)
+    tc::tma_load_4d_at(dst + h * half_bytes, map, chunks ? 0 : k + h * kFH, r0, 0, chunks ? k / kFH + h : 0, bar);
 }
 // Where the way along the reduction, of ns stages, begins for range (tile) s: not at
 // the same columns for all, whose rows lie a fixed distance apart (64 tokens, 2880 x
@@ -271,7 +277,7 @@ __global__ void __launch_bounds__(kFThreads, 1) k_few_layer(const FewArgs g, con
     tc::fence_mbar_init();
   }
   if (warp == 3 && lane < (int)(sizeof(FewMaps) / sizeof(CUtensorMap))) tc::prefetch_tmap(&maps.a[0] + lane);
-  const uint32_t ncol = g.N <= 16 ? 16 : g.N <= 32 ? 32 : 64;      // of an accumulator; four a tile, two tiles
+  const uint32_t ncol = g.ncol;         // four accumulators a tile, two tiles
   if (warp == 1) tc::tmem_alloc(tmem_slot, 8 * ncol);
   for (int i = tid; i < G; i += kFThreads) mask[i] = i >= g.E ? (g.R == 64 ? ~0ull : (1ull << g.R) - 1) : 0ull;
   pdl_enter();
@@ -402,8 +408,8 @@ __global__ void __launch_bounds__(kFThreads, 1) k_few_layer(const FewArgs g, con
       }
       const int m = __popcll(mask[t.e]);
       t.bi = box_of(m);
-      t.rows = 8 << t.bi;
-      t.N = (m + 15) & ~15;
+      t.rows = g.parts * 8 << t.bi;
+      t.N = g.parts > 1 ? t.rows : (m + 15) & ~15;
       t.hs = g.hs2[t.bi];
       t.ns = g.ns2[t.bi];
     }
@@ -485,7 +491,8 @@ __global__ void __launch_bounds__(kFThreads, 1) k_few_layer(const FewArgs g, con
             if (!tc::bar_wait(empty_u + 8 * slot, phase, abort)) { ok = false; break; }
             const int left = min(hs, nh - h), n_h = chunks ? (left + 1) & ~1 : left;
             tc::bar_arrive_expect_tx(full_u + 8 * slot, n_h * half);
-            copy_rows(ring_u + slot * g.slot + a_bytes, half, map, chunks, h * kFH, n_h, r0, full_u + 8 * slot);
+            if (second) copy_y(ring_u + slot * g.slot + a_bytes, half, map, chunks, h * kFH, n_h, r0, full_u + 8 * slot);
+            else copy_rows(ring_u + slot * g.slot + a_bytes, half, map, chunks, h * kFH, n_h, r0, full_u + 8 * slot);
             ++issued;
             if (++slot == g.stages) {
               slot = 0;
@@ -633,8 +640,12 @@ __global__ void __launch_bounds__(kFThreads, 1) k_few_layer(const FewArgs g, con
                 a += g.b1[(int64_t)t.e * 2 * g.F1 + f];
                 u += g.b1[(int64_t)t.e * 2 * g.F1 + g.F1 + f];
               }
-              const float y = gated ? act_two(a, u, g.act) : act_one(a, g.act.act);
-              reinterpret_cast<uint16_t*>(g.y)[(int64_t)(r0 + i0 + i) * g.ldy + f] = E::from(wrow[r0 + i0 + i] * y);
+              const float y = wrow[r0 + i0 + i] * (gated ? act_two(a, u, g.act) : act_one(a, g.act.act));
+              uint16_t* to = g.y + (int64_t)(r0 + i0 + i) * g.ldy + f;
+              const uint16_t hi = E::from(y);
+              *to = hi;
+              // what the first part's rounding left (of an infinity nothing)
+              if (g.parts > 1) to[(int64_t)(A + g.S * g.R) * g.ldy] = E::from(isinf(E::to(hi)) ? 0.f : y - E::to(hi));
             }
             epi_sync();
           }
@@ -656,6 +667,12 @@ __global__ void __launch_bounds__(kFThreads, 1) k_few_layer(const FewArgs g, con
             }
             uint32_t v[kFCols];
             add_columns<kFCols>(v, acc + i0, ncol);
+            if (g.parts > 1) {
+              uint32_t w[kFCols];
+              add_columns<kFCols>(w, acc + (8 << t.bi) + i0, ncol);
+#pragma unroll
+              for (int i = 0; i < kFCols; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) + __uint_as_float(w[i]));
+            }
             if (i0 + kFCols >= m) release();
 #pragma unroll
             for (int i = 0; i < kFCols; ++i)
@@ -995,6 +1012,13 @@ static bool map_rows(CUtensorMap* map, const void* x, int64_t K, int64_t rows, i
   return make_tmap(map, x, 2, 3, dims, strides, box);
 }
 
+static bool map_y(CUtensorMap* map, const void* y, int64_t K, int64_t rows, int64_t ld, int box_rows, int parts) {
+  const bool chunks = K % kFH == 0;
+  const int64_t dims[4] = {chunks ? kFH : K, rows, parts, chunks ? K / kFH : 1}, strides[3] = {ld, rows * ld, chunks ? kFH : ld};
+  const int box[4] = {kFH, box_rows, parts, chunks ? 2 : 1};
+  return make_tmap(map, y, 2, 4, dims, strides, box);
+}
+
 cudaError_t launch_few_layer(FewArgs g, const void* x, int64_t ldx, const void* w1, int64_t g1, int64_t ld1, const void* w2,
                              int64_t g2, int64_t ld2, cudaStream_t st) {
   const int G = g.E + g.S, A = g.R * g.k, halves = act_gated(g.act.act) ? 2 : 1;
@@ -1002,8 +1026,14 @@ cudaError_t launch_few_layer(FewArgs g, const void* x, int64_t ldx, const void* 
   g.N = (g.R + 15) & ~15;
   g.xrows = (g.R + 7) & ~7;
   g.rows1 = kFM / halves;
-  int box_t = 8;                                    // rows of the second product's widest copy
+  int box_t = 8;                                    // rows of the second product's widest copy, of a part
   while (box_t < g.R) box_t *= 2;
+  // y as a sum of two 16-bit numbers where tensor memory has room for both parts' columns (its weights
+  // are read once all the same): rounded to one, it leaves out 1.4 times as far off as out's own rounding, and where
+  // few values are summed more (256 x 128, 1 token: 1.53); as two, 1.0. More tokens are rounded to one.
+  g.parts = g.R <= 32 ? 2 : 1;
+  g.ncol = 16;
+  while (g.ncol < g.N || (g.parts > 1 && g.ncol < 2 * box_t)) g.ncol *= 2;
   // Bytes of a stage, of what stands in front of the ring, and its stages, by the
   // features of the second product's tiles. An MMA of 64 or 128 rows reads past the rows that were
   // copied, of A and of B (16 where 8 were): within the stage but for its last halves, where the tile is narrow.
@@ -1011,7 +1041,7 @@ cudaError_t launch_few_layer(FewArgs g, const void* x, int64_t ldx, const void* 
   auto layout = [&](int box2) {
     const int head = kFBars + 16 * kFM * 4 + 4 * (g.R * box2 + 2) + 12 * G + 4 * std::min(G, A + g.S) + 5 * (A + g.S * g.R) + 8 * A;
     g.box2 = box2;
-    g.slot = 2 * 128 * std::max(kFM + g.xrows, box2 + box_t);
+    g.slot = 2 * 128 * std::max(kFM + g.xrows, box2 + g.parts * box_t);
     g.head = (head + 1023) / 1024 * 1024;
     g.stages = std::min(kFMaxStages, (kFSmem - 1024 - g.head - pad) / g.slot);
   };
@@ -1037,7 +1067,7 @@ cudaError_t launch_few_layer(FewArgs g, const void* x, int64_t ldx, const void* 
     if (S2 > 1 && f > kFM) break;
     layout(std::min(kFM, (f + 7) & ~7));
     int hs, ns;
-    stages(g.box2 + rows, g.K2, hs, ns);
+    stages(g.box2 + g.parts * rows, g.K2, hs, ns);
     const double tile = std::max({nh * 128 * std::min((double)g.F2 / Pf, (double)kFM) / 23.5, 600 + 90 * nh + 300 * ns, 150 * copies + 200 * ns});
     const double cost = touched / S2 * tile * up(f, kFM) * (g.stages < 4 ? 1.1 : 1.) + (S2 > 1 ? 3000 + 1000 * S2 + 6. * g.R * f : 0);
     if (cost < least) {
@@ -1048,13 +1078,13 @@ cudaError_t launch_few_layer(FewArgs g, const void* x, int64_t ldx, const void* 
   }
   layout(most);
   for (int i = 0; i < 8; ++i) stages(16 * (i + 1) + g.xrows, g.K1, g.hs1[i], g.ns1[i]);      // halves * step * (i + 1) rows
-  for (int i = 0; i < 4; ++i) stages(g.box2 + std::min(8 << i, box_t), g.K2, g.hs2[i], g.ns2[i]);
+  for (int i = 0; i < 4; ++i) stages(g.box2 + g.parts * std::min(8 << i, box_t), g.K2, g.hs2[i], g.ns2[i]);
   const int smem = 1024 + g.head + g.stages * g.slot + pad;
   FewMaps maps;
   for (int i = 0; i < 8; ++i)
     if (!map_weights(&maps.a[i], w1, g.K1, g.F1, halves, ld1, G, g1, g.rows1 / 8 * (i + 1), 2)) return cudaErrorInvalidValue;
   for (int i = 0; i < 4; ++i)
-    if (!map_rows(&maps.y[i], g.y, g.K2, (int64_t)g.R * (g.k + g.S), g.ldy, 8 << i, 2)) return cudaErrorInvalidValue;
+    if (!map_y(&maps.y[i], g.y, g.K2, (int64_t)g.R * (g.k + g.S), g.ldy, 8 << i, g.parts)) return cudaErrorInvalidValue;
   if (!map_weights(&maps.a2, w2, g.K2, g.F2, 1, ld2, G, g2, g.box2, 2) || !map_rows(&maps.x, x, g.K1, g.R, ldx, g.xrows, 2))
     return cudaErrorInvalidValue;
   const auto kernel = g.dtype == MOE_DT_BF16 ? k_few_layer<Bf16> : k_few_layer<F16>;
