@@ -121,7 +121,7 @@ def routing(logits, k, scale):
 
 def layer(x, w1, w2, b1, ids, wts, n_shared, name, alpha, limit):
     """out [T, H] and its bound from given ids and weights (a slot whose id is out of range or whose weight is 0 is left
-    out). y is rounded once to x's type."""
+    out). y is a sum of two numbers of x's type, for more than 32 tokens rounded to one."""
     T, H = x.shape
     E, I = w1.shape[0] - n_shared, w2.shape[2]
     out = torch.zeros(T, H, dtype=torch.float64, device=x.device)
@@ -136,7 +136,11 @@ def layer(x, w1, w2, b1, ids, wts, n_shared, name, alpha, limit):
             continue
         y, b, _, _ = linear(x[t], w1[e], None if b1 is None else b1[e], None, name, alpha, limit)
         y, b = y * w[t, None], (b + 4 * EPS32 * y.abs()) * w[t, None].abs()
-        b = rounded(b, y, x.dtype)
+        if T > 32:
+            b = rounded(b, y, x.dtype)
+        else:       # half a step of what half a step left, or of the smallest numbers
+            f = torch.finfo(x.dtype)
+            b = b + (f.eps / 2) ** 2 * (y.abs() + b) + f.smallest_normal * f.eps / 2
         m = w2[e].double()
         out[t] += y @ m.t()
         err[t] += b @ m.abs().t()
