@@ -244,6 +244,9 @@ __global__ void __launch_bounds__(kFThreads, 1) k_few_layer(const FewArgs g, con
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(queue + kFQueue);
   volatile int* abort = reinterpret_cast<volatile int*>(tmem_slot + 1);
   int* tmp = reinterpret_cast<int*>(tmem_slot + 2);                 // 1 + 2 * 10
+  // the epilogue's answer to whether a part of a range was the last to be done. A word of its own: a warp without
+  // a tile may read tmp[0], the groups, after the epilogue's first range
+  volatile int* last = tmp + 21;
   float* stage = reinterpret_cast<float*>(base + kFBars);           // [16][128]
   const int G = g.E + g.S, A = g.R * g.k;
   const bool gated = act_gated(g.act.act);
@@ -700,9 +703,9 @@ __global__ void __launch_bounds__(kFThreads, 1) k_few_layer(const FewArgs g, con
         const int j = (s - P1) / g.S2;
         __threadfence();
         epi_sync();
-        if (et == 0) tmp[0] = atom_add_acq_rel_gpu(&g.joined[j], 1) == g.S2 - 1;
+        if (et == 0) *last = atom_add_acq_rel_gpu(&g.joined[j], 1) == g.S2 - 1;
         epi_sync();
-        if (*reinterpret_cast<volatile int*>(&tmp[0])) {
+        if (*last) {
           __threadfence();
           // eight at a time, whose loads are all asked for before the first sum
           const float* set = g.part + (int64_t)j * g.S2 * g.R * g.box2;

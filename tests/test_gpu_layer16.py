@@ -374,3 +374,26 @@ def test_decode_block_of_the_operators():
     m.moe_linear_forward(a, d, c["out"], ws, residual=c["out"])
     ro, bo, _, _ = D.linear(a, d, None, routed, "none", 1.0, 0.0)
     P.assert_within(c["out"], ro, bo, "out")
+
+
+# sizes whose second product splits its groups in halves and in quarters
+@pytest.mark.parametrize("T,H,I,E,k", [(16, 4096, 512, 24, 8), (64, 1024, 256, 64, 8), (3, 2048, 768, 40, 8), (17, 512, 264, 60, 6)])
+def test_layer16_fewer_groups_than_parts(T, H, I, E, k):
+    """No token with an expert, or all of them with the same few: parts without a group have nothing to compute and are
+    joined all the same."""
+    cuda_device()
+    c = _inputs(T, H, I, E, k, 0, "swiglu", BF16, False, 0)
+    for live in (0, 1, 2, 3, 5):
+        c["ids"].copy_(torch.arange(k, device="cuda").expand(T, k) * 3 % E)
+        c["wts"].copy_((torch.arange(k, device="cuda") < live).float() * 0.25)
+        want = None
+        for _ in range(20 if live < 2 else 3):
+            c["out"].fill_(NAN)
+            _run(c, "swiglu")
+            if want is None:
+                want = c["out"].clone()
+                _check_out(c, "swiglu", 0)
+            assert torch.equal(c["out"], want)
+        if not live:
+            assert not bool(want.any())
+        assert m.moe_mm_read_status(c["ws"]) == 0
