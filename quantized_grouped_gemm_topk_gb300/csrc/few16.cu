@@ -65,6 +65,7 @@ constexpr int kFCols = 8;             // columns the layer's epilogue takes at a
 constexpr int kFQueue = 4;            // claimed ranges in flight
 constexpr int kFIssuers = 4;          // warps that issue the layer's MMAs
 constexpr int kFLeast = 8;            // features a range, at least
+constexpr int kFWide = 128;           // columns of an accumulator of the second product with more than 32 tokens
 
 struct FewMaps {
   CUtensorMap a[8];                   // weights of the (first) product: boxes of 8 (i + 1) features (not gated: 16 (i + 1)),
@@ -133,14 +134,14 @@ __device__ __forceinline__ void wind_down(uint64_t* full, uint32_t issued, int s
 __device__ __forceinline__ float add4(const uint32_t (&v)[4]) {
   return (__uint_as_float(v[0]) + __uint_as_float(v[1])) + (__uint_as_float(v[2]) + __uint_as_float(v[3]));
 }
-// C columns of the four accumulators, `ncol` columns apart, added.
+// C columns of the four accumulators, `apart` columns apart, added.
 template <int C>
-__device__ __forceinline__ void add_columns(uint32_t (&v)[C], uint32_t acc, uint32_t ncol) {
+__device__ __forceinline__ void add_columns(uint32_t (&v)[C], uint32_t acc, uint32_t apart) {
   uint32_t u[4][C];
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
-    if constexpr (C == 16) tc::tmem_ld16(acc + j * ncol, u[j]);
-    else tmem_ld8(acc + j * ncol, u[j]);
+    if constexpr (C == 16) tc::tmem_ld16(acc + j * apart, u[j]);
+    else tmem_ld8(acc + j * apart, u[j]);
   }
   tc::tmem_wait_ld();
 #pragma unroll
@@ -411,8 +412,7 @@ __global__ void __launch_bounds__(kFThreads, 1) k_few_layer(const FewArgs g, con
       }
       const int m = __popcll(mask[t.e]);
       t.bi = box_of(m);
-      t.rows = g.parts * 8 << t.bi;
-      t.N = g.parts > 1 ? t.rows : (m + 15) & ~15;
+      t.rows = t.N = 16 << t.bi;      // both parts of y
       t.hs = g.hs2[t.bi];
       t.ns = g.ns2[t.bi];
     }
@@ -512,7 +512,7 @@ __global__ void __launch_bounds__(kFThreads, 1) k_few_layer(const FewArgs g, con
     const uint32_t wi = uni(warp), step = wi == 1 ? 0 : wi == 3 ? 1 : wi - 6;       // of every 64 of the reduction
     const uint64_t d0 = tc::smem_desc_sw128(ring_u);
     const uint32_t lo = uni((uint32_t)d0 + 2 * step), hi = uni((uint32_t)(d0 >> 32));
-    const uint32_t tm = uni(tmem) + step * ncol, bars = uni(full_u), accs = uni(tc::smem_u32(accfull));
+    const uint32_t tm = uni(tmem) + step * ncol, tmw = uni(tmem) + step * kFWide, bars = uni(full_u), accs = uni(tc::smem_u32(accfull));
     const uint32_t slot_step = (uint32_t)g.slot / 16;
     uint32_t slot = 0, at = lo, phase = 0, tiles = 0;
     bool ok = true;
@@ -528,7 +528,10 @@ __global__ void __launch_bounds__(kFThreads, 1) k_few_layer(const FewArgs g, con
         if (!__all_sync(kFull, tc::mbar_wait(&accempty[d], ((tiles >> 1) & 1) ^ 1, abort))) { ok = false; break; }
         tc::fence_after_sync();
         const uint32_t a_step = uni(t.arows * 8), b_step = uni(t.rows * 8), hs = uni(t.hs), wide = uni(t.N);
-        const uint32_t idesc = tc::idesc_16bit(a_step <= 64 * 8 ? 64 : kFM, wide, g.dtype == MOE_DT_BF16, 0, 0), dt = tm + d * 4 * ncol;
+        const uint32_t idesc = tc::idesc_16bit(a_step <= 64 * 8 ? 64 : kFM, wide, g.dtype == MOE_DT_BF16, 0, 0);
+        // 128 columns: room for two accumulators a tile, so two of the warps issue, two steps each
+        const bool narrow = wide < kFWide;
+        const uint32_t dt = (narrow ? tm : tmw) + d * 4 * ncol;
         const uint32_t b_off = hs * a_step, ns = uni(t.ns);
         uint32_t acc = 0;
         for (uint32_t i = 0, h = uni(first_stage(s, ns)) * hs; i < ns; ++i) {
@@ -536,10 +539,20 @@ __global__ void __launch_bounds__(kFThreads, 1) k_few_layer(const FewArgs g, con
           tc::fence_after_sync();
           const uint32_t n_h = min(hs, (uint32_t)nh - h);
           uint32_t a = at, b = at + b_off;
+          if (narrow) {
 #pragma unroll 2
-          for (uint32_t c = 0; c < n_h; ++c, a += a_step, b += b_step) {
-            mma_one(dt, a, b, hi, idesc, acc);
-            acc = 1;
+            for (uint32_t c = 0; c < n_h; ++c, a += a_step, b += b_step) {
+              mma_one(dt, a, b, hi, idesc, acc);
+              acc = 1;
+            }
+          } else if (step < 2) {
+            a += 2 * step;              // steps 0 and 1, 2 and 3
+            b += 2 * step;
+            for (uint32_t c = 0; c < n_h; ++c, a += a_step, b += b_step) {
+              mma_one(dt, a, b, hi, idesc, acc);
+              mma_one(dt, a + 2, b + 2, hi, idesc, 1u);
+              acc = 1;
+            }
           }
           commit_one(bars + 8 * (kFMaxStages + slot));      // its `empty`
           h = h + hs < (uint32_t)nh ? h + hs : 0;
@@ -648,7 +661,7 @@ __global__ void __launch_bounds__(kFThreads, 1) k_few_layer(const FewArgs g, con
               const uint16_t hi = E::from(y);
               *to = hi;
               // what the first part's rounding left (of an infinity nothing)
-              if (g.parts > 1) to[(int64_t)(A + g.S * g.R) * g.ldy] = E::from(isinf(E::to(hi)) ? 0.f : y - E::to(hi));
+              to[(int64_t)(A + g.S * g.R) * g.ldy] = E::from(isinf(E::to(hi)) ? 0.f : y - E::to(hi));
             }
             epi_sync();
           }
@@ -668,9 +681,10 @@ __global__ void __launch_bounds__(kFThreads, 1) k_few_layer(const FewArgs g, con
               at[i] = sums + tok[min(i0 + i, m - 1)] * g.box2 + (mine ? row : 0);
               u[i] = *at[i];
             }
+            // y's parts are 8 << bi columns apart; two wide accumulators have theirs where four narrow ones begin
             uint32_t v[kFCols];
             add_columns<kFCols>(v, acc + i0, ncol);
-            if (g.parts > 1) {
+            if (t.bi < 3) {
               uint32_t w[kFCols];
               add_columns<kFCols>(w, acc + (8 << t.bi) + i0, ncol);
 #pragma unroll
@@ -1015,10 +1029,10 @@ static bool map_rows(CUtensorMap* map, const void* x, int64_t K, int64_t rows, i
   return make_tmap(map, x, 2, 3, dims, strides, box);
 }
 
-static bool map_y(CUtensorMap* map, const void* y, int64_t K, int64_t rows, int64_t ld, int box_rows, int parts) {
+static bool map_y(CUtensorMap* map, const void* y, int64_t K, int64_t rows, int64_t ld, int box_rows) {
   const bool chunks = K % kFH == 0;
-  const int64_t dims[4] = {chunks ? kFH : K, rows, parts, chunks ? K / kFH : 1}, strides[3] = {ld, rows * ld, chunks ? kFH : ld};
-  const int box[4] = {kFH, box_rows, parts, chunks ? 2 : 1};
+  const int64_t dims[4] = {chunks ? kFH : K, rows, 2, chunks ? K / kFH : 1}, strides[3] = {ld, rows * ld, chunks ? kFH : ld};
+  const int box[4] = {kFH, box_rows, 2, chunks ? 2 : 1};
   return make_tmap(map, y, 2, 4, dims, strides, box);
 }
 
@@ -1031,12 +1045,14 @@ cudaError_t launch_few_layer(FewArgs g, const void* x, int64_t ldx, const void* 
   g.rows1 = kFM / halves;
   int box_t = 8;                                    // rows of the second product's widest copy, of a part
   while (box_t < g.R) box_t *= 2;
-  // y as a sum of two 16-bit numbers where tensor memory has room for both parts' columns (its weights
+  // y is a sum of two 16-bit numbers, side by side in the MMA's columns (its weights
   // are read once all the same): rounded to one, it leaves out 1.4 times as far off as out's own rounding, and where
-  // few values are summed more (256 x 128, 1 token: 1.53); as two, 1.0. More tokens are rounded to one.
-  g.parts = g.R <= 32 ? 2 : 1;
+  // few values are summed more (256 x 128, 1 token: 1.53); as two, 1.0. Four accumulators of up to 64 columns (groups of 32
+  // tokens) fill tensor memory, two of 128 as well. In us, as one and as two, 64 tokens: x 2880 x 2880, 4 of 128 769, 775;
+  // x 7168 x 2048, 8 of 64 849, 859; x 4096 x 512, 8 of 256 453, 450; with large groups, x 4096 x 14336, 2 of 8 426, 447; all
+  // tokens on both of 2, 4096 x 2048 56.0, 61.4.
   g.ncol = 16;
-  while (g.ncol < g.N || (g.parts > 1 && g.ncol < 2 * box_t)) g.ncol *= 2;
+  while (g.ncol < std::max(g.N, std::min(64, 2 * box_t))) g.ncol *= 2;
   // Bytes of a stage, of what stands in front of the ring, and its stages, by the
   // features of the second product's tiles. An MMA of 64 or 128 rows reads past the rows that were
   // copied, of A and of B (16 where 8 were): within the stage but for its last halves, where the tile is narrow.
@@ -1044,7 +1060,7 @@ cudaError_t launch_few_layer(FewArgs g, const void* x, int64_t ldx, const void* 
   auto layout = [&](int box2) {
     const int head = kFBars + 16 * kFM * 4 + 4 * (g.R * box2 + 2) + 12 * G + 4 * std::min(G, A + g.S) + 5 * (A + g.S * g.R) + 8 * A;
     g.box2 = box2;
-    g.slot = 2 * 128 * std::max(kFM + g.xrows, box2 + g.parts * box_t);
+    g.slot = 2 * 128 * std::max(kFM + g.xrows, box2 + 2 * box_t);
     g.head = (head + 1023) / 1024 * 1024;
     g.stages = std::min(kFMaxStages, (kFSmem - 1024 - g.head - pad) / g.slot);
   };
@@ -1070,7 +1086,7 @@ cudaError_t launch_few_layer(FewArgs g, const void* x, int64_t ldx, const void* 
     if (S2 > 1 && f > kFM) break;
     layout(std::min(kFM, (f + 7) & ~7));
     int hs, ns;
-    stages(g.box2 + g.parts * rows, g.K2, hs, ns);
+    stages(g.box2 + 2 * rows, g.K2, hs, ns);
     const double tile = std::max({nh * 128 * std::min((double)g.F2 / Pf, (double)kFM) / 23.5, 600 + 90 * nh + 300 * ns, 150 * copies + 200 * ns});
     const double cost = touched / S2 * tile * up(f, kFM) * (g.stages < 4 ? 1.1 : 1.) + (S2 > 1 ? 3000 + 1000 * S2 + 6. * g.R * f : 0);
     if (cost < least) {
@@ -1081,13 +1097,13 @@ cudaError_t launch_few_layer(FewArgs g, const void* x, int64_t ldx, const void* 
   }
   layout(most);
   for (int i = 0; i < 8; ++i) stages(16 * (i + 1) + g.xrows, g.K1, g.hs1[i], g.ns1[i]);      // halves * step * (i + 1) rows
-  for (int i = 0; i < 4; ++i) stages(g.box2 + g.parts * std::min(8 << i, box_t), g.K2, g.hs2[i], g.ns2[i]);
+  for (int i = 0; i < 4; ++i) stages(g.box2 + 2 * std::min(8 << i, box_t), g.K2, g.hs2[i], g.ns2[i]);
   const int smem = 1024 + g.head + g.stages * g.slot + pad;
   FewMaps maps;
   for (int i = 0; i < 8; ++i)
     if (!map_weights(&maps.a[i], w1, g.K1, g.F1, halves, ld1, G, g1, g.rows1 / 8 * (i + 1), 2)) return cudaErrorInvalidValue;
   for (int i = 0; i < 4; ++i)
-    if (!map_y(&maps.y[i], g.y, g.K2, (int64_t)g.R * (g.k + g.S), g.ldy, 8 << i, g.parts)) return cudaErrorInvalidValue;
+    if (!map_y(&maps.y[i], g.y, g.K2, (int64_t)g.R * (g.k + g.S), g.ldy, 8 << i)) return cudaErrorInvalidValue;
   if (!map_weights(&maps.a2, w2, g.K2, g.F2, 1, ld2, G, g2, g.box2, 2) || !map_rows(&maps.x, x, g.K1, g.R, ldx, g.xrows, 2))
     return cudaErrorInvalidValue;
   const auto kernel = g.dtype == MOE_DT_BF16 ? k_few_layer<Bf16> : k_few_layer<F16>;

@@ -21,7 +21,7 @@ struct FewArgs {
   int E, k, S;
   const int32_t* ids; const float* wts;   // [R][k]
   const float* b1;            // nullable, [E + S][2 F1]
-  uint16_t* y; int64_t ldy;   // rows of the second product, by group; of a second part the same behind all of them
+  uint16_t* y; int64_t ldy;   // rows of the second product, by group; of their second part the same behind all of them
   int32_t* ticket;            // zero on entry: ranges claimed,
   int32_t* done;              // ranges of the first product done,
   int32_t* joined;            // [kFewSms] parts of a range of the second done
@@ -36,7 +36,6 @@ struct FewArgs {
   int nt, mt1;                // dense: tiles of rows and of features
   int hs, lanes;              // dense: 64s of the reduction a stage, features side by side in the epilogue
   int issuers;                // warps that issue MMAs; `stages` is a multiple of them
-  int parts;                  // layer: 16-bit numbers that hold a value of y
   int ncol;                   // layer: columns of an accumulator
   int Pf, S2;                 // layer: ranges of the second product's features, parts of the groups for each
   int xrows, box2;            // layer: rows of x a copy takes, features of the second product's tiles

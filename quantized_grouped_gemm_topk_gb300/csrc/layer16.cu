@@ -52,7 +52,7 @@ static int64_t route_floats(int T, int H, int E) {
   return most;
 }
 
-// Workspace: the counters, y [parts][T (k + S)][I] 16-bit rows by group, the sums of parts
+// Workspace: the counters, y [2 parts][T (k + S)][I] 16-bit rows by group, the sums of parts
 // of the groups, the router's partial sums.
 constexpr int kCounters = 16 + kFewSms;
 struct Layer16Ws {
@@ -62,7 +62,7 @@ static Layer16Ws layer16_ws(int T, int H, int I, int E, int k, int S) {
   Layer16Ws w;
   w.ldy = (I + 7) / 8 * 8;
   w.y = al256(kCounters * 4);
-  w.part = w.y + al256(std::min<int64_t>(2 * T, MOE_LAYER16_MAX_T) * (k + S) * w.ldy * 2);      // two parts of up to 32 tokens
+  w.part = w.y + al256(2 * (int64_t)T * (k + S) * w.ldy * 2);
   w.router = w.part + (int64_t)kFewSms * T * 128 * 4;
   w.bytes = w.router + al256(route_floats(T, H, E) * 4);
   return w;

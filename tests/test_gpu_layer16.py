@@ -397,3 +397,24 @@ def test_layer16_fewer_groups_than_parts(T, H, I, E, k):
         if not live:
             assert not bool(want.any())
         assert m.moe_mm_read_status(c["ws"]) == 0
+
+
+def _check_out_in_parts(c, act, S):
+    """The bound of y in two parts, which dense_ref.layer knows for up to 32 tokens, at any number of them."""
+    parts = [D.layer(c["x"][t:t + 32], c["w1"], c["w2"], c["b1"], c["ids"][t:t + 32].long(), c["wts"][t:t + 32], S, act, ALPHA, LIMIT)
+             for t in range(0, c["x"].shape[0], 32)]
+    P.assert_within(c["out"], torch.cat([p[0] for p in parts]), torch.cat([p[1] for p in parts]), "out")
+
+
+# few values to sum, so that a rounding of y is seen; groups of a few tokens, of up to 32, and of more
+@pytest.mark.parametrize("T,H,I,E,k,S", [(32, 264, 40, 4, 2, 0), (33, 264, 40, 40, 2, 0), (33, 520, 72, 4, 2, 1), (48, 1024, 64, 2, 1, 0),
+                                         (64, 300, 24, 3, 2, 1), (64, 2048, 128, 24, 4, 0), (64, 7168, 72, 2, 2, 0), (64, 1024, 136, 64, 8, 1),
+                                         (50, 20001, 40, 3, 3, 0), (64, 128, 1, 5, 2, 0)])
+@pytest.mark.parametrize("act,dtype,bias", [("swiglu", BF16, False), ("geglu", F16, True), ("srelu", BF16, False)])
+def test_layer16_is_as_exact_for_many_tokens(T, H, I, E, k, S, act, dtype, bias):
+    """A token's result is as exact in a batch of 64 as in one of 32: y is in two parts at any number of tokens."""
+    cuda_device()
+    c = _inputs(T, H, I, E, k, S, act, dtype, bias, 8)
+    _run(c, act, S, W_r=c["W_r"])
+    _check_out_in_parts(c, act, S)
+    assert m.moe_mm_read_status(c["ws"]) == 0
