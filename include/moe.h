@@ -563,7 +563,8 @@ moe_status_t moe_linear_workspace_size(int R, int rows, int K, int backward, siz
  * [G, I, H]), w2 [G, H, I] of dtype (bf16 or f16); b1 [G, 2I] fp32, nullable
  * (NULL with MOE_ACT_SRELU). G = E + n_shared; experts E.. are shared: every token, weight 1.
  * Activations as in moe_config_t. y, the second product's operand, is a sum of
- * two numbers of dtype; the sums are fp32 and out is rounded once.
+ * two numbers of dtype (with f16 from about 2^28 on an infinity); the sums are
+ * fp32 and out is rounded once.
  *
  * Routing: W_r [H, E] fp32 gives the logits x . W_r, or logits [T, E] fp32 are
  * given; then topk_ids [T, k] and topk_w [T, k] (fp32) are outputs: the k largest

@@ -134,21 +134,32 @@ __device__ __forceinline__ void wind_down(uint64_t* full, uint32_t issued, int s
 __device__ __forceinline__ float add4(const uint32_t (&v)[4]) {
   return (__uint_as_float(v[0]) + __uint_as_float(v[1])) + (__uint_as_float(v[2]) + __uint_as_float(v[3]));
 }
-// C columns of the four accumulators, `apart` columns apart, added.
-template <int C>
+// C columns of the J accumulators (two or four), `apart` columns apart, added.
+template <int C, int J = 4>
 __device__ __forceinline__ void add_columns(uint32_t (&v)[C], uint32_t acc, uint32_t apart) {
-  uint32_t u[4][C];
+  uint32_t u[J][C];
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
+  for (int j = 0; j < J; ++j) {
     if constexpr (C == 16) tc::tmem_ld16(acc + j * apart, u[j]);
     else tmem_ld8(acc + j * apart, u[j]);
   }
   tc::tmem_wait_ld();
 #pragma unroll
   for (int i = 0; i < C; ++i) {
-    const uint32_t w[4] = {u[0][i], u[1][i], u[2][i], u[3][i]};
-    v[i] = __float_as_uint(add4(w));
+    if constexpr (J == 4) {
+      const uint32_t w[4] = {u[0][i], u[1][i], u[2][i], u[3][i]};
+      v[i] = __float_as_uint(add4(w));
+    } else {
+      v[i] = __float_as_uint(__uint_as_float(u[0][i]) + __uint_as_float(u[1][i]));
+    }
   }
+}
+// What the first part of y is a multiple of. An f16 number ends at 65504, which squared ReLU passes at 256; in
+// steps of 4096 the first part reaches 2^28, and what its rounding leaves, at most 2^-11 of it or 2^-13, the
+// second holds to the 2^-25 that it would be off by in any case.
+template <typename E>
+__device__ constexpr float y_unit() {
+  return E::kInf == F16::kInf ? 4096.f : 1.f;
 }
 // The layer's epilogue warps only.
 __device__ __forceinline__ void epi_sync() { __syncwarp(); asm volatile("bar.sync 1, 128;" ::: "memory"); }
@@ -658,10 +669,10 @@ __global__ void __launch_bounds__(kFThreads, 1) k_few_layer(const FewArgs g, con
               }
               const float y = wrow[r0 + i0 + i] * (gated ? act_two(a, u, g.act) : act_one(a, g.act.act));
               uint16_t* to = g.y + (int64_t)(r0 + i0 + i) * g.ldy + f;
-              const uint16_t hi = E::from(y);
+              const uint16_t hi = E::from(y * (1.f / y_unit<E>()));
               *to = hi;
               // what the first part's rounding left (of an infinity nothing)
-              to[(int64_t)(A + g.S * g.R) * g.ldy] = E::from(isinf(E::to(hi)) ? 0.f : y - E::to(hi));
+              to[(int64_t)(A + g.S * g.R) * g.ldy] = E::from(isinf(E::to(hi)) ? 0.f : y - E::to(hi) * y_unit<E>());
             }
             epi_sync();
           }
@@ -681,19 +692,18 @@ __global__ void __launch_bounds__(kFThreads, 1) k_few_layer(const FewArgs g, con
               at[i] = sums + tok[min(i0 + i, m - 1)] * g.box2 + (mine ? row : 0);
               u[i] = *at[i];
             }
-            // y's parts are 8 << bi columns apart; two wide accumulators have theirs where four narrow ones begin
-            uint32_t v[kFCols];
-            add_columns<kFCols>(v, acc + i0, ncol);
+            uint32_t v[kFCols], w[kFCols];          // of both parts of y
             if (t.bi < 3) {
-              uint32_t w[kFCols];
+              add_columns<kFCols>(v, acc + i0, ncol);
               add_columns<kFCols>(w, acc + (8 << t.bi) + i0, ncol);
-#pragma unroll
-              for (int i = 0; i < kFCols; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) + __uint_as_float(w[i]));
+            } else {
+              add_columns<kFCols, 2>(v, acc + i0, kFWide);
+              add_columns<kFCols, 2>(w, acc + kFWide / 2 + i0, kFWide);
             }
             if (i0 + kFCols >= m) release();
 #pragma unroll
             for (int i = 0; i < kFCols; ++i)
-              if (mine && i0 + i < m) *at[i] = u[i] + __uint_as_float(v[i]);
+              if (mine && i0 + i < m) *at[i] = u[i] + fmaf(__uint_as_float(v[i]), y_unit<E>(), __uint_as_float(w[i]));
           }
           if (mine && t.e == glist[r.g1 - 1])
 #pragma unroll 8

@@ -418,3 +418,31 @@ def test_layer16_is_as_exact_for_many_tokens(T, H, I, E, k, S, act, dtype, bias)
     _run(c, act, S, W_r=c["W_r"])
     _check_out_in_parts(c, act, S)
     assert m.moe_mm_read_status(c["ws"]) == 0
+
+
+@pytest.mark.parametrize("T,H,I,E,k,S", [(1, 264, 136, 4, 2, 0), (16, 264, 136, 40, 2, 0), (30, 1024, 256, 4, 2, 1), (64, 520, 72, 3, 2, 1),
+                                         (64, 1024, 256, 64, 4, 0)])
+@pytest.mark.parametrize("act", ["srelu", "swiglu"])
+def test_layer16_f16_activations_past_its_range(T, H, I, E, k, S, act):
+    """Activations that an f16 number cannot hold, of results that it can; and, past what y holds, an infinity of one token."""
+    cuda_device()
+    c = _inputs(T, H, I, E, k, S, act, F16, False, 8)
+    c["w1"] *= 160
+    c["w2"] *= 2.0 ** -8
+    _run(c, act, S, W_r=c["W_r"])
+    largest = 0.0
+    for e in range(E):
+        w = (c["wts"].double() * (c["ids"] == e)).sum(1)
+        y = D.linear(c["x"], c["w1"][e], None, None, act, ALPHA, LIMIT)[0] * w[:, None]
+        largest = max(largest, float(y.abs().max()))
+    assert largest > 65520
+    assert bool(torch.isfinite(c["out"].float()).all())
+    _check_out_in_parts(c, act, S)
+    if T == 1 or S:
+        return
+    want = c["out"].clone()
+    c["x"][T // 2] *= 500
+    _run(c, act, S)             # with the ids and weights of before
+    keep = [t for t in range(T) if t != T // 2]
+    assert torch.equal(c["out"][keep], want[keep]) and not bool(torch.isfinite(c["out"][T // 2].float()).all())
+    assert m.moe_mm_read_status(c["ws"]) == 0
