@@ -381,3 +381,39 @@ def test_linear_elements_past_32_bits(R):
         rdz, bdz = D.linear_dz(res, zbuf[:, :2 * N], "swiglu", ALPHA, LIMIT)
         P.assert_within(dz, rdz, bdz, "dz")
         P.assert_within(dx, d @ w.double(), (2 * N + 8) * P.EPS32 * (d.abs() @ w.double().abs()), "dx")
+
+
+@pytest.mark.parametrize("act", [a for a in D.ACTS if a != "none"])
+@pytest.mark.parametrize("dtype", [BF16, F16])
+def test_linear_derivative_by_differences(act, dtype):
+    """dz against central differences of the activation alone, in 64 bits at the very z that the kernel reads: only dz's
+    own rounding and the kernel's error are between the two. A derivative that lacks a term is outside."""
+    cuda_device()
+    g = _gen(12)
+    R, N = 37, 200
+    hv = D.halves(act)
+    z, d = _randn(g, R, hv * N, dtype=dtype, std=1.5), _randn(g, R, N, dtype=dtype)
+    x, w = _rows(g, R, 8, dtype), _rows(g, hv * N, 8, dtype)
+    dz = torch.empty_like(z)
+    m.moe_linear_backward(d, x, w, z, dz, None, None, None, _ws(R, hv * N, 8, True), act=act, alpha=ALPHA, limit=LIMIT)
+    h = 1e-4
+    zs = list(z.double().chunk(hv, 1))
+    bound = D.linear_dz(d, z, act, ALPHA, LIMIT)[1].chunk(hv, 1)
+    for i, got in enumerate(dz.chunk(hv, 1)):
+        f = [D.act([v + s * h if j == i else v for j, v in enumerate(zs)], act, ALPHA, LIMIT)[0] for s in (1, -1)]
+        want = d.double() * (f[0] - f[1]) / (2 * h)
+        # the difference's own error: h^2 / 6 of a third derivative below 4 (1 + |other half|), at srelu's corner h
+        other = 1 + (zs[1 - i].abs() if hv == 2 else 0)
+        lim = bound[i] + d.double().abs() * other * (4 * h * h + (h if act == "srelu" else 0))
+        lim = lim + P.HALF_STEP[dtype] * (want.abs() + lim) + P.TINY[dtype]
+        smooth = torch.ones_like(want, dtype=torch.bool)
+        if act == "swiglu_clamp":         # a corner has no difference
+            smooth = (zs[i].abs() - LIMIT).abs() > 2 * h
+        assert float(smooth.double().mean()) > 0.95
+        assert bool(((got.double() - want).abs() <= lim)[smooth].all()), (act, i)
+        # without f's own slope in v s(v), or without the derivative at all
+        live = smooth & (want != 0)
+        value = D.act(zs, act, ALPHA, LIMIT)[0]
+        less = want / 2 if act == "srelu" else d.double() * value / zs[0] if i == 0 else d.double() * value / zs[1] * 0.5
+        for wrong in (less, want * 0):
+            assert float(((wrong - want).abs() > lim)[live].double().mean()) > 0.9, (act, i)
