@@ -446,3 +446,47 @@ def test_layer16_f16_activations_past_its_range(T, H, I, E, k, S, act):
     keep = [t for t in range(T) if t != T // 2]
     assert torch.equal(c["out"][keep], want[keep]) and not bool(torch.isfinite(c["out"][T // 2].float()).all())
     assert m.moe_mm_read_status(c["ws"]) == 0
+
+
+@pytest.mark.parametrize("T,k", [(2, 2), (16, 3), (17, 2), (40, 2), (64, 5)])
+@pytest.mark.parametrize("dtype", [BF16, F16])
+def test_layer16_tokens_do_not_reach_each_other_at_any_number(T, k, dtype):
+    """As above with each way through the epilogues (up to 16 tokens, up to 32, more) and with groups of many tokens: a NaN
+    or an infinity of a token, of its weight, or of an expert that only it chose."""
+    cuda_device()
+    H, I, E = 328, 200, 6
+    c = _inputs(T, H, I, E, k, 0, "swiglu", dtype, False, 0)
+    g = _gen(3)
+    c["ids"].copy_(torch.stack([torch.randperm(E - 1, generator=g, device="cuda")[:k] for _ in range(T)]))
+    c["wts"].copy_(torch.rand(T, k, generator=g, device="cuda") + 0.1)
+    t = T // 2
+    c["ids"][t, 1] = E - 1
+    _run(c, "swiglu")
+    want = c["out"].clone()
+    others = [i for i in range(T) if i != t]
+
+    def check(alone=NAN):
+        c["out"].fill_(7)
+        _run(c, "swiglu")
+        assert torch.equal(c["out"][others], want[others])
+        mine = c["out"][t].float()
+        assert bool((torch.isnan(mine) if alone != alone else ~torch.isfinite(mine)).all())
+
+    w1, w2, x = c["w1"][E - 1].clone(), c["w2"][E - 1].clone(), c["x"][t].clone()
+    c["w1"][E - 1, 3, 7] = INF
+    c["w2"][E - 1] = NAN
+    check()
+    c["w1"][E - 1], c["w2"][E - 1] = w1, w2
+    for v in (NAN, INF, -INF):
+        c["x"][t, H - 1] = v
+        check()
+    c["x"][t] = x
+    c["wts"][t, 0] = NAN
+    check()
+    c["wts"][t, 0] = INF
+    check(INF)
+    c["wts"][t, 0] = 0.5
+    c["out"].fill_(7)
+    _run(c, "swiglu")
+    assert torch.equal(c["out"][others], want[others]) and bool(torch.isfinite(c["out"][t].float()).all())
+    assert m.moe_mm_read_status(c["ws"]) == 0

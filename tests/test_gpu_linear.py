@@ -417,3 +417,29 @@ def test_linear_derivative_by_differences(act, dtype):
         less = want / 2 if act == "srelu" else d.double() * value / zs[0] if i == 0 else d.double() * value / zs[1] * 0.5
         for wrong in (less, want * 0):
             assert float(((wrong - want).abs() > lim)[live].double().mean()) > 0.9, (act, i)
+
+
+@pytest.mark.parametrize("R,N,K,act", [(300, 200, 136, "silu"), (300, 200, 136, "swiglu"), (300, 200, 136, "swiglu_clamp"), (40, 2048, 264, "gelu"),
+                                       (2304, 40, 136, "geglu"), (300, 200, 136, "none")])
+def test_linear_backward_nan_stays_in_its_row(R, N, K, act):
+    """A NaN in a row of dout or of z leaves the other rows of dz and dx alone, in either kind of product kernel; dw and db
+    hold it where dz's column does."""
+    x, w, dout, z, dz, dx, dw, db, ws = _backward(R, N, K, act, BF16)
+    dout[4, N - 1] = NAN
+    if z is not None:
+        z[7, 3] = NAN
+    got_z = None if dz is None else torch.zeros_like(dz)
+    got_x, got_w, got_b = torch.zeros_like(dx), torch.zeros_like(dw), torch.zeros_like(db)
+    m.moe_linear_backward(dout, x, w, z, got_z, got_x, got_w, got_b, ws, act=act, alpha=ALPHA, limit=LIMIT)
+    keep = torch.ones(R, dtype=torch.bool, device="cuda")
+    keep[4], keep[7] = False, act == "none"
+    assert torch.equal(got_x[keep], dx[keep])
+    assert bool(torch.isnan(got_x[~keep].float()).all())
+    d = dout if dz is None else got_z
+    if dz is not None:
+        assert torch.equal(got_z[keep], dz[keep])
+    bad = torch.isnan(d.float()).any(0)
+    assert bool(bad.any()) and not bool(bad.all())
+    assert torch.equal(torch.isnan(got_b.float()), bad) and torch.equal(got_b[~bad], db[~bad])
+    assert torch.equal(torch.isnan(got_w.float()), bad[:, None].expand_as(got_w)) and torch.equal(got_w[~bad], dw[~bad])
+    assert m.moe_mm_read_status(ws) == 0
