@@ -443,3 +443,38 @@ def test_linear_backward_nan_stays_in_its_row(R, N, K, act):
     assert torch.equal(torch.isnan(got_b.float()), bad) and torch.equal(got_b[~bad], db[~bad])
     assert torch.equal(torch.isnan(got_w.float()), bad[:, None].expand_as(got_w)) and torch.equal(got_w[~bad], dw[~bad])
     assert m.moe_mm_read_status(ws) == 0
+
+
+@pytest.mark.parametrize("R,N,K,act", [(33, 48, 64, "swiglu"), (600, 48, 64, "swiglu"), (2200, 40, 72, "silu"), (600, 48, 64, "none")])
+def test_linear_backward_elements_past_32_bits(R, N, K, act):
+    """Rows so far apart that the last one's offset passes 2^31 elements, of every matrix of the backward; few and many
+    rows, and a split reduction of dw."""
+    cuda_device()
+    _needs_gb(80)
+    g = _gen(9)
+    rows = D.halves(act) * N
+
+    def far(n, cols):
+        ld = (2 ** 31 // (n - 1) + 64) // 8 * 8
+        return torch.zeros(n, ld, dtype=BF16, device="cuda")[:, :cols]
+
+    x, dout, dx, dw, w = far(R, K), far(R, N), far(R, K), far(rows, K), far(rows, K)
+    x.copy_(_randn(g, R, K))
+    dout.copy_(_randn(g, R, N))
+    w.copy_(_randn(g, rows, K, std=K ** -0.5))
+    z = dz = None
+    if act != "none":
+        z, dz = far(R, rows), far(R, rows)
+        z.copy_(_randn(g, R, rows, std=1.5))
+    db = torch.full((rows,), NAN, device="cuda")
+    ws = _ws(R, rows, K, True)
+    m.moe_linear_backward(dout, x, w, z, dz, dx, dw, db, ws, act=act, alpha=ALPHA, limit=LIMIT)
+    rz, bz = D.linear_dz(dout, z, act, ALPHA, LIMIT)
+    d = dout.double()
+    if z is not None:
+        P.assert_within(dz, rz, bz, "dz")
+        d = dz.double()
+    P.assert_within(db, rz.sum(0), bz.sum(0) + (R + 8) * P.EPS32 * (rz.abs() + bz).sum(0), "db")
+    P.assert_within(dx, d @ w.double(), (rows + 8) * P.EPS32 * (d.abs() @ w.double().abs()), "dx")
+    P.assert_within(dw, d.t() @ x.double(), (R + 8) * P.EPS32 * (d.abs().t() @ x.double().abs()), "dw")
+    assert m.moe_mm_read_status(ws) == 0
