@@ -478,3 +478,66 @@ def test_linear_backward_elements_past_32_bits(R, N, K, act):
     P.assert_within(dx, d @ w.double(), (rows + 8) * P.EPS32 * (d.abs() @ w.double().abs()), "dx")
     P.assert_within(dw, d.t() @ x.double(), (R + 8) * P.EPS32 * (d.abs().t() @ x.double().abs()), "dw")
     assert m.moe_mm_read_status(ws) == 0
+
+
+FIRST_CALL = '''
+import torch
+import quantized_grouped_gemm_topk_gb300 as m
+
+torch.manual_seed(0)
+bf = torch.bfloat16
+dev = dict(device="cuda")
+
+
+def randn(*shape):
+    return torch.randn(*shape, **dev).to(bf) * 0.2
+
+
+def zeros(n):
+    return torch.zeros(n, dtype=torch.uint8, **dev)
+
+
+T, H, I, E, k = 7, 320, 192, 9, 3
+layer = [randn(T, H), torch.randn(H, E, **dev), None, randn(E, 2 * I, H), randn(E, H, I), torch.zeros(T, H, dtype=bf, **dev),
+         torch.zeros(T, k, dtype=torch.int32, **dev), torch.zeros(T, k, **dev), zeros(m.moe_layer16_workspace_size(T, H, I, E, k))]
+outs = [layer[5]]
+calls = [lambda: m.moe_layer16_forward(*layer)]
+for R, N, K in ((5, 200, 264), (400, 200, 264), (40, 2048, 264)):
+    x, w, d = randn(R, K), randn(2 * N, K), randn(R, N)
+    out, z, dz, dx, dw = (torch.zeros(*s, dtype=bf, **dev) for s in ((R, N), (R, 2 * N), (R, 2 * N), (R, K), (2 * N, K)))
+    db = torch.zeros(2 * N, **dev)
+    fws, bws = (zeros(m.moe_linear_workspace_size(R, 2 * N, K, b)) for b in (False, True))
+    calls.append(lambda x=x, w=w, out=out, ws=fws, z=z: m.moe_linear_forward(x, w, out, ws, z=z, act="swiglu"))
+    calls.append(lambda d=d, x=x, w=w, z=z, dz=dz, dx=dx, dw=dw, db=db, ws=bws: m.moe_linear_backward(d, x, w, z, dz, dx, dw, db, ws, act="swiglu"))
+    outs += [out, z, dz, dx, dw, db]
+torch.cuda.synchronize()
+stream, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph, stream=stream):
+    for call in calls:
+        call()
+torch.cuda.synchronize()
+assert not any(bool(o.any()) for o in outs)             # captured, not run
+graph.replay()
+torch.cuda.synchronize()
+got = [o.clone() for o in outs]
+assert all(bool(o.any()) for o in outs)
+for o in outs:
+    o.zero_()
+for call in calls:
+    call()
+torch.cuda.synchronize()
+assert all(torch.equal(a, b) for a, b in zip(got, outs))
+print("same")
+'''
+
+
+def test_first_calls_of_a_process_in_a_graph():
+    """The layer's and the dense products' first calls in a process are captured, on a stream of their own: what the library
+    asks the driver once (attributes, residency) may be asked during a capture."""
+    import os
+    import subprocess
+    import sys
+    cuda_device()
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", FIRST_CALL], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and r.stdout.split() == ["same"], r.stdout + r.stderr
