@@ -544,7 +544,8 @@ moe_status_t moe_linear_forward(const void* x, int64_t ldx, const void* w, int64
  * residual's gradient is dout. dx, dw and db are each nullable (x is read for
  * dw, w for dx). With MOE_ACT_NONE dz is dout: z and dz are not read or written.
  * dz (with MOE_ACT_NONE: dout), x, w and ws start on 16 bytes, their strides are
- * multiples of 8 elements. R = 0 writes zero dw and db. */
+ * multiples of 8 elements. R = 0 writes zero dw and db. A dw in fp32 (to add up
+ * over batches) is moe_grouped_mm_wgrad's, of dz (dout) and x with one group. */
 moe_status_t moe_linear_backward(const void* dout, int64_t lddout, const void* x, int64_t ldx, const void* w,
                                  int64_t ldw, const void* z, int64_t ldz, int R, int N, int K, int act, float alpha,
                                  float limit, int dtype, int wdtype, void* dz, int64_t lddz, void* dx, int64_t lddx,

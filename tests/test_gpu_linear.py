@@ -541,3 +541,20 @@ def test_first_calls_of_a_process_in_a_graph():
     root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
     r = subprocess.run([sys.executable, "-c", FIRST_CALL], cwd=root, capture_output=True, text=True, timeout=300)
     assert r.returncode == 0 and r.stdout.split() == ["same"], r.stdout + r.stderr
+
+
+@pytest.mark.parametrize("act", ["none", "swiglu"])
+def test_linear_fp32_weight_gradient_of_the_grouped_products(act):
+    """dw in fp32: the grouped products' weight gradient of dz, with one group of all rows."""
+    R, N, K = 700, 200, 264
+    x, w, dout, z, dz, _, dw, _, _ = _backward(R, N, K, act, BF16)
+    d = dout if dz is None else dz
+    rows = d.shape[1]
+    off = torch.tensor([0, R], dtype=torch.int32, device="cuda")
+    got = torch.full((1, rows, K), NAN, device="cuda")
+    ws = torch.zeros(m.moe_mm_workspace_size(m.MOE_MM_WGRAD, R, rows, K, 1), dtype=torch.uint8, device="cuda")
+    m.moe_grouped_mm_wgrad(d, x, off, got, ws)
+    ref, mag = d.double().t() @ x.double(), d.double().abs().t() @ x.double().abs()
+    P.assert_within(got[0], ref, (R + 8) * P.EPS32 * mag, "dw")
+    # one rounding less than the 16-bit one
+    assert float((got[0].double() - ref).norm()) < 0.01 * float((dw.double() - ref).norm())
