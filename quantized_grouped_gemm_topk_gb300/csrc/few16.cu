@@ -49,6 +49,7 @@
 // 16 tokens and 24 experts the memory reads 1.015 times the weights' bytes, at 77 %
 // of its time, the tensor pipe is 7 % busy.
 #include <cmath>
+#include <type_traits>
 
 #include "few16.cuh"
 #include "tc.cuh"
@@ -109,11 +110,12 @@ __device__ __forceinline__ void copy_y(uint32_t dst, int half_bytes, const CUten
   for (int h = 0; h < n; h += chunks ? 2 : 1)
     tc::tma_load_4d_at(dst + h * half_bytes, map, chunks ? 0 : k + h * kFH, r0, 0, chunks ? k / kFH + h : 0, bar);
 }
-// Where the way along the reduction, of ns stages, begins for range (tile) s: not at
-// the same columns for all, whose rows lie a fixed distance apart (64 tokens, 2880 x
-// 2880 x 128 experts 804 -> 789 us), but a small part of the way further for each (16 x 2 x 2048 x
-// 7168 13.4 us; the golden ratio's part 14.0). Not by CTA: which one takes a range varies, and
-// sums must not.
+// Where the way along the reduction, of ns stages, begins for range (tile) s: a small part of the way further for
+// each, not at the same columns for all, whose rows lie a fixed distance apart. Not by CTA: which one takes a range
+// varies, and sums must not. It is worth little, and not always that. In us, from the first column on, an
+// eleventh further, and the golden ratio's part: dense 1 x 4096 x 4096 9.9, 9.5, 9.9; 16 x 2 x 2048 x 7168 13.4, 13.5, 13.8; 4 x
+// 4096 x 14336 22.5, 22.7, 23.4; layer, 1 token x 7168 x 2048 122.6, 122.0, 122.0; x 4096 x 512 38.2, 38.7, 39.9; 16 x 2880 x 2880
+// 379, 381, 381; 64 tokens 794, 796, 795.
 __device__ __forceinline__ int first_stage(int s, int ns) {
   return (int)(((uint32_t)s * 5851u & 0xffffu) * (uint32_t)ns >> 16);      // an eleventh
 }
@@ -159,7 +161,7 @@ __device__ __forceinline__ void add_columns(uint32_t (&v)[C], uint32_t acc, uint
 // second holds to the 2^-25 that it would be off by in any case.
 template <typename E>
 __device__ constexpr float y_unit() {
-  return E::kInf == F16::kInf ? 4096.f : 1.f;
+  return std::is_same_v<E, F16> ? 4096.f : 1.f;
 }
 // The layer's epilogue warps only.
 __device__ __forceinline__ void epi_sync() { __syncwarp(); asm volatile("bar.sync 1, 128;" ::: "memory"); }
@@ -1011,8 +1013,6 @@ __global__ void __launch_bounds__(kDThreads, 1) k_few_linear(const FewArgs g, co
 }
 
 // ---- host -------------------------------------------------------------------------
-static int64_t up(int64_t n, int64_t t) { return (n + t - 1) / t; }
-
 // A ring of at most `most` stages, a multiple of its issuers, as many of those as can be:
 // a slot is then always the same warp's, and one that waits for a use of a slot has
 // itself seen the use before it (a barrier tells neighbouring uses apart only).

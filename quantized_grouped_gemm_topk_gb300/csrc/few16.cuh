@@ -10,6 +10,8 @@ namespace moe {
 constexpr int kFewRows = 256;
 constexpr int kFewSms = 152;
 
+inline int64_t up(int64_t n, int64_t t) { return (n + t - 1) / t; }      // n / t, rounded up
+
 struct FewArgs {
   int R;                      // rows; layer: tokens (at most 64)
   int K1, F1;                 // first product: reduction, features (gated: of a half)

@@ -18,7 +18,6 @@ struct LinArgs {
 };
 
 __host__ __device__ __forceinline__ bool rows16(const void* p, int64_t ld) { return ((uintptr_t)p & 15) == 0 && ld % 8 == 0; }
-inline int64_t up(int64_t n, int64_t t) { return (n + t - 1) / t; }
 
 // The product of g on pairs of SMs.
 cudaError_t launch_pairs_bf16(LinArgs& g, int mode, bool gated, cudaStream_t st);
