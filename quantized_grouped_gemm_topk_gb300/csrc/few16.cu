@@ -1095,6 +1095,10 @@ cudaError_t launch_few_layer(FewArgs g, const void* x, int64_t ldx, const void* 
     const int Pf = (int)std::min<int64_t>(grid / S2, up(g.F2, kFLeast)), f = (int)up(g.F2, Pf);
     if (S2 > 1 && f > kFM) break;
     layout(std::min(kFM, (f + 7) & ~7));
+    if (g.stages < 2) {           // beside the tables of 2000 experts; narrower tiles for a split range there are not
+      if (S2 > 1) break;
+      layout(64);
+    }
     int hs, ns;
     stages(g.box2 + 2 * rows, g.K2, hs, ns);
     const double tile = std::max({nh * 128 * std::min((double)g.F2 / Pf, (double)kFM) / 23.5, 600 + 90 * nh + 300 * ns, 150 * copies + 200 * ns});

@@ -490,3 +490,29 @@ def test_layer16_tokens_do_not_reach_each_other_at_any_number(T, k, dtype):
     _run(c, "swiglu")
     assert torch.equal(c["out"][others], want[others]) and bool(torch.isfinite(c["out"][t].float()).all())
     assert m.moe_mm_read_status(c["ws"]) == 0
+
+
+def test_layer16_of_many_wide_experts():
+    """As many experts and slots as there can be, whose tables take most of what the ring of weights has, and ranges of H of
+    more than 64 features: only the experts that a token chose hold anything else than NaN."""
+    cuda_device()
+    if torch.cuda.get_device_properties(0).total_memory < 60 << 30:
+        pytest.skip("needs 60 GB")
+    T, I, E, S, dtype = 64, 72, 2047, 1, BF16
+    for H, k in ((20008, 31), (8200, 8)):
+        g = _gen(H)
+        few = 40
+        live = torch.randperm(E, generator=g, device="cuda")[:few]
+        kept = torch.cat([live, torch.tensor([E], device="cuda")])
+        w1 = torch.full((E + S, 2 * I, H), NAN, dtype=dtype, device="cuda")
+        w2 = torch.full((E + S, H, I), NAN, dtype=dtype, device="cuda")
+        w1[kept] = _randn(g, few + 1, 2 * I, H, dtype=dtype, std=H ** -0.5)
+        w2[kept] = _randn(g, few + 1, H, I, dtype=dtype, std=I ** -0.5)
+        at = torch.stack([torch.randperm(few, generator=g, device="cuda")[:k] for _ in range(T)])
+        c = dict(x=_randn(g, T, H, dtype=dtype), w1=w1, w2=w2, b1=None, ids=live[at].int().contiguous(),
+                 wts=torch.rand(T, k, generator=g, device="cuda"), out=torch.empty(T, H, dtype=dtype, device="cuda"),
+                 ws=torch.zeros(m.moe_layer16_workspace_size(T, H, I, E, k, S), dtype=torch.uint8, device="cuda"))
+        _run(c, "swiglu", S)
+        small = {**c, "w1": w1[kept], "w2": w2[kept], "ids": at}
+        _check_out_in_parts(small, "swiglu", S)
+        assert m.moe_mm_read_status(c["ws"]) == 0
