@@ -40,13 +40,13 @@
 // MOE_DEV_TIMEOUT, waits for its copies and MMAs in flight, frees tensor memory and
 // returns.
 //
-// Measured, in us, behind the router (bf16, SwiGLU; in brackets the bytes that the
-// tokens' experts need, at 6775 GB/s): 1 token x 7168 x 2048, 8 of 256 experts 113
-// (105); 8 tokens 692 (748 for that many at random, fewer were drawn); 16 tokens x
-// 2880 x 2880, 4 of 128, 373 (375); x 4096 x 512, 8 of 256, 199 (190); 64 tokens x 7168 x 2048, 8 of
-// 64, 832 (832); x 2048 x 768, 8 of 128, 193 (176); 1 token x 2880 x 2880, 4 of 128, 44 (29); 1 token x
-// 256 x 128, 2 of 8, 12.0 (latency). With
-// 16 tokens and 24 experts the memory reads 1.015 times the weights' bytes, at 77 %
+// Measured, in us, with ready ids (bf16, SwiGLU; in brackets the bytes that the
+// tokens' experts need, at 6775 GB/s): 1 token x 7168 x 2048, 8 of 256 experts 114
+// (105); 8 tokens 742 (748 for that many at random); 16 tokens x
+// 2880 x 2880, 4 of 128, 370 (375); x 4096 x 512, 8 of 256, 203 (190); 64 tokens x 7168 x 2048, 8 of
+// 64, 868 (832); x 2048 x 768, 8 of 128, 198 (176); 1 token x 2880 x 2880, 4 of 128, 45 (29); 1 token x
+// 256 x 128, 2 of 8, 13.0 (latency); GPUs of one kind differ by 3 %, this is one of the slower. With
+// 16 tokens and 24 experts the memory reads 1.015 times the weights' bytes, at 75 %
 // of its time, the tensor pipe is 7 % busy.
 #include <cmath>
 #include <type_traits>

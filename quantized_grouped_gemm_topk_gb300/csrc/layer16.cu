@@ -5,8 +5,10 @@
 // tokens: the reduction is cut into slices, a CTA each, whose partial sums the last
 // CTA to arrive (of those eight tokens') adds in order and routes. 1 x 7168 x 256:
 // latency, not the 7.3 MB; so all of a thread's rows are asked for at once, and a small
-// product is one CTA's, without a join. Launch to launch the router takes 2.4 us of a
-// layer where one CTA does it, 5 to 7 else.
+// product is one CTA's, without a join. What the router adds to a layer with ready ids, in us,
+// tokens x H x experts: one CTA's 1 x 256 x 8 2.2, 1 x 2048 x 8 3.5; joined 1 x 2880 x 128 6.3, 1 x
+// 7168 x 256 8.0 to 8.7, 5 x 1999 x 24 7.6, 16 x 2880 x 24 7.5, x 128 10, 16 x 7168 x 256 14; 64 x 2880 x 128 9.8, 64
+// x 7168 x 256 18.
 #include "few16.cuh"
 
 namespace moe {
